@@ -396,6 +396,193 @@ emb_status emb_sparse_adagrad_noalloc(const int64_t* rows, int64_t n, const floa
 emb_status emb_noalloc_get_device_status(void* stream);
 
 /* ------------------------------------------------------------------------ */
+/* Dense operators behind the lookups (no counterpart on the pages): a gated */
+/* recurrence over padded sequences, tokens sorted by expert and back, AdamW  */
+/* ------------------------------------------------------------------------ */
+/* Element types are EMB_DT_F32, EMB_DT_BF16 and EMB_DT_F16 of
+ * emb_table_dtype (called dtype below).  All arithmetic is fp32; a result
+ * of 16 bits is rounded once, when it is stored.  Pointers need the alignment
+ * of their element; rows whose pointers, strides and sizes are multiples of
+ * 16 bytes move in 16-byte accesses.  Outputs must not overlap inputs or
+ * each other. */
+
+typedef struct emb_scan_s* emb_scan;
+
+/* A [batch, time, dim] array of `dtype`: element (b, t, d) is
+ * data[b * batch_stride + t * time_stride + d] (strides in elements, >= 0).
+ * Outputs must not map two elements to one place. */
+typedef struct {
+    void* data;
+    int64_t batch_stride;
+    int64_t time_stride;
+} scan_view;
+
+/* scan_create -- workspace of a gated linear recurrence over sequences:
+ *   a_t = sigmoid(gate_t);  h_t = a_t * h_{t-1} + (1 - a_t) * x_t
+ * per batch entry and channel, over dim channels (1 .. 65536), at most
+ * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^31-1) positions.
+ * Calls on one handle must be ordered (one stream, or streams joined by
+ * events).  *out is NULL on error. */
+emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_len, emb_scan* out);
+
+/* scan_forward -- h_t for every position.
+ *  x, gate   (host structs) inputs of `dtype`
+ *  offsets   NULL, or [batch + 1] int32: entry b has offsets[b+1] - offsets[b]
+ *            live positions, cut to [0, len] -- a padded column's slice of
+ *            emb_forward's id_offsets.  Positions past the end read nothing;
+ *            their y is 0.
+ *  state_in  [batch, dim] fp32 h before the first position; NULL = 0
+ *  y         (host struct) h_t in `dtype`
+ *  state_out NULL, or [batch, dim] fp32: h after the last live position
+ * The state between positions is fp32 throughout. */
+emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
+                        const scan_view* gate, const int32_t* offsets, const float* state_in, const scan_view* y,
+                        float* state_out, void* stream);
+
+/* scan_backward -- gradients of scan_forward's x, gate and state_in, from
+ * the same inputs, its y and the gradients of y and state_out:
+ *   G_t = grad_y_t + a_{t+1} G_{t+1} (grad_state_out past the last position)
+ *   grad_x_t = (1 - a_t) G_t;  grad_gate_t = a_t (1 - a_t) (h_{t-1} - x_t) G_t
+ * Positions past an entry's end read nothing and get gradient 0.
+ * y is read at a few positions only; the states between them are computed
+ * again in fp32.  grad_state_out (NULL = 0) and grad_state_in (NULL = not
+ * wanted) are [batch, dim] fp32. */
+emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
+                         const scan_view* gate, const int32_t* offsets, const float* state_in, const scan_view* y,
+                         const scan_view* grad_y, const float* grad_state_out, const scan_view* grad_x,
+                         const scan_view* grad_gate, float* grad_state_in, void* stream);
+
+/* scan_step -- one position for each of n sessions whose states are rows of a
+ * pool (serving): row = rows[i]; states[row] = h of (x_i, gate_i) on
+ * states[row]; y_i = that h.  A row outside [0, num_rows) (-1: no row yet) is
+ * dropped: y_i = 0.  Rows of one call must be distinct.
+ *  x, gate, y  [n, dim] of `dtype`, rows x_stride, gate_stride, y_stride apart
+ *  states      [num_rows, dim] fp32 */
+emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride, const void* gate,
+                     int64_t gate_stride, const int64_t* rows, float* states, int64_t num_rows, void* y,
+                     int64_t y_stride, void* stream);
+
+/* Synchronizes `stream`, returns and clears the latched device status
+ * (EMB_ERR_TIMEOUT: a wait between parts of a sequence ran out, the outputs of
+ * that call are incomplete; EMB_ERR_BAD_INDEX: decreasing offsets, read as
+ * length 0). */
+emb_status scan_get_device_status(emb_scan h, void* stream);
+emb_status scan_destroy(emb_scan h);
+
+typedef struct emb_moe_s* emb_moe;
+
+/* moe_create -- workspace for tokens that each go to top_k of n_experts
+ * experts.  1 <= n_experts <= 2048, 1 <= top_k <= 64, 1 <= align <= 65536,
+ * max_tokens * top_k + n_experts * align < 2^31.  Each expert's rows start at
+ * a multiple of align; the expert-ordered arrays have
+ *   R(n) = n * top_k + n_experts * (align - 1), rounded up to align
+ * rows for n tokens.  Calls on one handle must be ordered.  *out is NULL on
+ * error. */
+emb_status moe_create(int32_t n_experts, int32_t top_k, int64_t max_tokens, int32_t align, emb_moe* out);
+
+/* moe_route -- the order of the choices by expert (a stable counting sort).
+ *  experts  [n, top_k] int32; a choice outside [0, n_experts) is dropped
+ *  offsets  [n_experts + 1] int32: first row of each expert's segment; the last
+ *           entry is the end of the last segment, rounded up to align
+ *  counts   [n_experts] int32: live rows of each segment
+ *  pos      [n, top_k] int32: row of each choice, -1 where dropped.  Rows of
+ *           one expert are in the order of their flat index token * top_k + k.
+ *  src      [R(n)] int32: flat index of each row's choice, -1 for padding */
+emb_status moe_route(emb_moe h, int64_t n, const int32_t* experts, int32_t* offsets, int32_t* counts, int32_t* pos,
+                     int32_t* src, void* stream);
+
+/* moe_dispatch -- xs[pos[t, k], :] = x[t, :]; padding rows (src -1) are 0.
+ *  x [n, dim] of `dtype`, rows x_stride elements apart; xs [R(n), dim] dense. */
+emb_status moe_dispatch(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
+                        const int32_t* pos, const int32_t* src, void* xs, void* stream);
+
+/* moe_combine -- y[t, :] = sum over k with pos[t, k] >= 0 of weights[t, k] *
+ * ys[pos[t, k], :], in the order of k (a token with no live choice gets 0).
+ * weights [n, top_k] fp32, NULL = 1: that is the gradient of moe_dispatch,
+ * with ys the gradient of xs and y the gradient of x.
+ *  ys [R(n), dim] dense; y [n, dim], rows y_stride elements apart. */
+emb_status moe_combine(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const void* ys, const float* weights,
+                       const int32_t* pos, void* y, int64_t y_stride, void* stream);
+
+/* moe_combine_backward -- gradients of moe_combine:
+ *   grad_ys[pos[t, k], :] = weights[t, k] * grad_y[t, :]; padding rows 0
+ *   grad_weights[t, k] = <grad_y[t, :], ys[pos[t, k], :]>, 0 where dropped
+ * grad_weights NULL = not wanted (ys is then not read). */
+emb_status moe_combine_backward(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const void* grad_y,
+                                int64_t grad_y_stride, const void* ys, const float* weights, const int32_t* pos,
+                                const int32_t* src, void* grad_ys, float* grad_weights, void* stream);
+emb_status moe_destroy(emb_moe h);
+
+typedef struct emb_adamw_s* emb_adamw;
+
+/* One parameter tensor of an AdamW handle.  Everything is caller-owned and
+ * must outlive the handle. */
+typedef struct {
+    void* param;          /* [numel] of dtype                                      */
+    const void* grad;     /* [numel] of dtype, or fp32 (grad_dtype)                */
+    float* master;        /* NULL, or [numel] fp32: the weights that are updated,
+                             param then receives them rounded (16-bit dtypes only) */
+    void* m;              /* [numel] fp32, or uint8 codes                          */
+    void* v;              /* [numel] fp32, or uint8 codes                          */
+    int16_t* m_top;       /* 8-bit states: [ceil(numel / 256)] (see below)         */
+    int16_t* v_top;
+    int64_t numel;        /* >= 0                                                  */
+    float weight_decay;   /* >= 0                                                  */
+    int32_t dtype;        /* emb_table_dtype of param                              */
+    int32_t grad_dtype;   /* dtype or EMB_DT_F32                                   */
+    int32_t reserved;     /* 0                                                     */
+} adamw_tensor;
+
+/* Flags of adamw_create. */
+#define ADAMW_STATES_8BIT 1u
+
+/* adamw_create -- one optimizer step over n tensors in one call (the dense
+ * weights beside the tables' sparse Adagrad).
+ *
+ * 8-bit states.  A value's place is its fp32 pattern without the sign, shifted
+ * right by 20 (exponent and three bits of the fraction).  Each block of 256
+ * elements of a tensor holds `top`, the place of its largest magnitude rounded
+ * up.  m: bit 7 is the sign, the low 7 bits the place counted from
+ * max(top - 127, 0) (15.9 octaves below the top); v: 8 bits counted from
+ * max(top - 255, 0) (31.9 octaves: the square of m's range); code 0 is zero.
+ * Places are rounded up or down at random with the exact value as their mean
+ * (to 2^-16 of a place), so that a second moment moves although one step
+ * changes it by less than a place; the 16 random bits of an element are a
+ * function of seed, step and the element's number alone (one SplitMix64
+ * output per four elements), so runs repeat bit for bit.  An element whose new
+ * state is not finite is left out of its block's top and its state restarts
+ * at 0 (its parameter shows the fault, as with 32-bit states).
+ *  tensors (host) [n], copied; 1 <= n < 2^24, fewer than 2^40 elements */
+emb_status adamw_create(const adamw_tensor* tensors, int32_t n, uint32_t flags, emb_adamw* out);
+
+/* adamw_bind_grads -- from the next step on the gradients are read from
+ * grads[0..n) (host array of device pointers; same element types as before).
+ * Stream-ordered; the host array may be reused when the call returns. */
+emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream);
+
+/* adamw_step -- step number `step` >= 1 on every tensor:
+ *   g = grad * (grad_scale ? *grad_scale : 1)
+ *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g g
+ *   w = w - lr weight_decay w
+ *         - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ * in fp32, from the new m and v before they are rounded to 8 bits.  The new
+ * states are the same bits as the formulas' operations rounded one by one;
+ * the weights use the hardware's approximate square root and division (a few
+ * ulp of the step).  grad_scale: device fp32 or NULL.
+ * Needs lr, eps >= 0 and 0 <= beta < 1, all finite. */
+emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,
+                      const float* grad_scale, uint32_t seed, void* stream);
+
+/* adamw_export_states -- what 8-bit states stand for, exactly (every value has
+ * three bits of fraction), as bf16: m_out, v_out [adamw_export_size] with
+ * tensor after tensor, each starting at the next multiple of 256 elements,
+ * zeros between them.  16-byte aligned.  EMB_ERR_UNSUPPORTED for 32-bit
+ * states (they are the caller's fp32 arrays). */
+emb_status adamw_export_states(emb_adamw h, void* m_out, void* v_out, void* stream);
+emb_status adamw_export_size(emb_adamw h, int64_t* elements);
+emb_status adamw_destroy(emb_adamw h);
+
+/* ------------------------------------------------------------------------ */
 /* Self tests and fault injection (no counterpart on the pages)              */
 /* ------------------------------------------------------------------------ */
 

@@ -9,13 +9,14 @@ been built, every call raises.
 Raw entry points keep their C names (emb_plan_create, emb_forward,
 emb_backward_update, hash_lookup_or_insert, hash_evict_expired, ...); the
 ``Plan`` and ``HashTable`` classes wrap them for callers that hold PyTorch
-tensors.
+tensors, and so do ``GatedScan``, ``ExpertRouter`` and ``AdamW`` (dense.py) for
+the operators of the dense layers behind the lookups.
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int32, c_int64, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_double, c_float, c_int32, c_int64, c_uint32, c_uint64, c_void_p
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libsparse_lookup.so")
@@ -92,6 +93,30 @@ _SIGS = {
     "hash_destroy": (c_int32, [c_void_p]),
     "emb_sparse_adagrad_noalloc": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_int64, c_int32,
                                              c_float, c_float, c_void_p]),
+    "scan_create": (c_int32, [c_int32, c_int32, c_int32, POINTER(c_void_p)]),
+    "scan_forward": (c_int32, [c_void_p, c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p,
+                               c_void_p, c_void_p]),
+    "scan_backward": (c_int32, [c_void_p, c_int32, c_int32, c_int32] + [c_void_p] * 11),
+    "scan_step": (c_int32, [c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
+                            c_int64, c_void_p, c_int64, c_void_p]),
+    "scan_get_device_status": (c_int32, [c_void_p, c_void_p]),
+    "scan_destroy": (c_int32, [c_void_p]),
+    "moe_create": (c_int32, [c_int32, c_int32, c_int64, c_int32, POINTER(c_void_p)]),
+    "moe_route": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_dispatch": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p, c_void_p,
+                               c_void_p]),
+    "moe_combine": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p, c_int64,
+                              c_void_p]),
+    "moe_combine_backward": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
+                                       c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_destroy": (c_int32, [c_void_p]),
+    "adamw_create": (c_int32, [c_void_p, c_int32, c_uint32, POINTER(c_void_p)]),
+    "adamw_bind_grads": (c_int32, [c_void_p, c_void_p, c_void_p]),
+    "adamw_step": (c_int32, [c_void_p, c_int64, c_double, c_double, c_double, c_double, c_void_p, c_uint32,
+                             c_void_p]),
+    "adamw_export_states": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p]),
+    "adamw_export_size": (c_int32, [c_void_p, POINTER(c_int64)]),
+    "adamw_destroy": (c_int32, [c_void_p]),
     "emb_calibrate_gather": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_void_p]),
     "emb_selftest_hash_mod": (c_int32, [c_void_p, c_int64, c_int64, c_void_p]),
     "emb_noalloc_get_device_status": (c_int32, [c_void_p]),
@@ -481,3 +506,9 @@ def _device_view(ptr_value, shape):
     h.__cuda_array_interface__ = {"shape": tuple(shape), "typestr": "<f4", "data": (ptr_value, False),
                                   "version": 2, "strides": None}
     return torch.as_tensor(h, device="cuda")
+
+
+from .dense import (AdamW, AdamwTensor, ExpertRouter, GatedScan, Routing, ScanView, adamw_bind_grads,  # noqa: E402,F401
+                    adamw_create, adamw_destroy, adamw_export_size, adamw_export_states, adamw_step, moe_combine,
+                    moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_route, scan_backward,
+                    scan_create, scan_destroy, scan_forward, scan_get_device_status, scan_step)

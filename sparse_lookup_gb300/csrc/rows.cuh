@@ -1,0 +1,62 @@
+// rows.cuh -- element types and vector accesses the dense operators share
+// (library-internal).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "plan.cuh"
+
+namespace emb {
+
+template <class T>
+__device__ __forceinline__ float to_f32(T x);
+template <>
+__device__ __forceinline__ float to_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ float to_f32<__nv_bfloat16>(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <>
+__device__ __forceinline__ float to_f32<__half>(__half x) { return __half2float(x); }
+
+template <class T>
+__device__ __forceinline__ T from_f32(float x);
+template <>
+__device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+template <>
+__device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+
+// V consecutive elements, moved in one access (V * sizeof(T) = 2, 4, 8 or 16).
+template <class T, int V>
+struct alignas(V * sizeof(T)) Vec {
+  T e[V];
+};
+
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> load_vec(const T* p) {
+  return *reinterpret_cast<const Vec<T, V>*>(p);
+}
+
+template <class T, int V>
+__device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
+  *reinterpret_cast<Vec<T, V>*>(p) = v;
+}
+
+inline int dtype_size(int32_t dtype) {
+  return dtype == EMB_DT_F32 ? 4 : dtype == EMB_DT_BF16 || dtype == EMB_DT_F16 ? 2 : 0;
+}
+
+inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// Calls f with a null pointer of the element type `dtype` names.
+template <class F>
+inline auto with_element(int32_t dtype, F f) {
+  switch (dtype) {
+    case EMB_DT_BF16: return f((__nv_bfloat16*)nullptr);
+    case EMB_DT_F16: return f((__half*)nullptr);
+    default: return f((float*)nullptr);
+  }
+}
+
+}  // namespace emb
