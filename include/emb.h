@@ -420,7 +420,7 @@ typedef struct {
 /* scan_create -- workspace of a gated linear recurrence over sequences:
  *   a_t = sigmoid(gate_t);  h_t = a_t * h_{t-1} + (1 - a_t) * x_t
  * per batch entry and channel, over dim channels (1 .. 65536), at most
- * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^31-1) positions.
+ * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^30) positions.
  * Calls on one handle must be ordered (one stream, or streams joined by
  * events).  *out is NULL on error. */
 emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_len, emb_scan* out);
@@ -444,8 +444,7 @@ emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, c
  *   G_t = grad_y_t + a_{t+1} G_{t+1} (grad_state_out past the last position)
  *   grad_x_t = (1 - a_t) G_t;  grad_gate_t = a_t (1 - a_t) (h_{t-1} - x_t) G_t
  * Positions past an entry's end read nothing and get gradient 0.
- * y is read at a few positions only; the states between them are computed
- * again in fp32.  grad_state_out (NULL = 0) and grad_state_in (NULL = not
+ * h_{t-1} is taken from y (16-bit types: as y was rounded).  grad_state_out (NULL = 0) and grad_state_in (NULL = not
  * wanted) are [batch, dim] fp32. */
 emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
                          const scan_view* gate, const int32_t* offsets, const float* state_in, const scan_view* y,

@@ -4,13 +4,35 @@
 
 #include "rows.cuh"
 
+namespace emb {
+
+// Words the tiles of one call share.  The last CTA of a call leaves ticket,
+// done and fail at zero and counts the epoch up, so a call needs no clearing.
+struct ScanShared {
+  uint32_t ticket;   // next tile
+  uint32_t done;     // CTAs that found no more tiles
+  uint32_t epoch;    // calls so far: the tag of this call's records
+  uint32_t fail;     // a wait ran out: the others stop waiting
+};
+
+}  // namespace emb
+
 struct emb_scan_s {
   int32_t dim = 0, max_batch = 0, max_len = 0;
   int sm_count = 0;
+  int64_t max_records = 0;
   uint32_t* status_d = nullptr;
+  emb::ScanShared* shared_d = nullptr;
+  ulonglong2* records_d = nullptr;   // [tiles][channels] what a tile does to a state (below)
 };
 
 namespace emb {
+
+constexpr int kScanThreads = 256;
+constexpr unsigned kScanSpins = 1u << 21;   // rounds a wait takes at most (about a second)
+constexpr int kGroup = 32;                  // tiles of a chain's group
+constexpr int kAhead = 4;                   // records of a group that one lane reads
+constexpr int kCtasPerSm = 2;
 
 // sigmoid(g) and sigmoid(-g), each from its own quotient: 1 - a would lose
 // every digit of the smaller one where the gate saturates.
@@ -19,20 +41,52 @@ __device__ __forceinline__ void gates(float g, float& a, float& na) {
   const float hi = __fdividef(1.f, 1.f + e), lo = e * hi;
   a = g >= 0.f ? hi : lo;
   na = g >= 0.f ? lo : hi;
-  if (g != g) a = na = g;
 }
 
+// `wide`: every column vector of the view can be moved in one access.  The
+// others are moved element by element by the same threads, so results do not
+// depend on strides and alignment.
 template <class T>
 struct View {
   T* p;
   int64_t bs, ts;
+  bool wide;
   __device__ T* at(int64_t b, int64_t t, int64_t d) const { return p + b * bs + t * ts + d; }
 };
 
+template <int V, class T>
+__device__ __forceinline__ auto get(const View<const T>& w, int64_t b, int64_t t, int64_t d) {
+  const T* p = w.at(b, t, d);
+  if (w.wide) return load_vec<T, V>(p);
+  Vec<T, V> r;
+#pragma unroll
+  for (int v = 0; v < V; ++v) r.e[v] = p[v];
+  return r;
+}
+
+template <int V, class T>
+__device__ __forceinline__ void put(const View<T>& w, int64_t b, int64_t t, int64_t d, const Vec<T, V>& r) {
+  T* p = w.at(b, t, d);
+  if (w.wide) {
+    store_vec(p, r);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v) p[v] = r.e[v];
+  }
+}
+
+// A call's shape.  A tile is TT = (256 / cx) * R positions of cx column vectors
+// of V channels; a column vector is V neighbouring channels of one batch entry.
 struct ScanArgs {
   int32_t batch, len, dim;
+  int32_t cx_log;        // column vectors of a tile, log2
+  int32_t tiles;         // along time
+  int64_t vecs;          // column vectors in all: batch * dim / V
+  int64_t groups;        // tiles across: ceil(vecs / cx)
   const int32_t* offsets;
   uint32_t* status;
+  ScanShared* shared;
+  ulonglong2* records;
 };
 
 __device__ __forceinline__ int live_len(const ScanArgs& s, int b) {
@@ -42,45 +96,436 @@ __device__ __forceinline__ int live_len(const ScanArgs& s, int b) {
   return n < 0 ? 0 : n > s.len ? s.len : (int)n;
 }
 
-template <class T>
-__global__ void __launch_bounds__(128) k_scan_fwd(ScanArgs s, View<const T> x, View<const T> g, View<T> y,
-                                                  const float* state_in, float* state_out) {
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  if (i >= (int64_t)s.batch * s.dim) return;
-  const int b = (int)(i / s.dim), d = (int)(i % s.dim);
-  const int n = live_len(s, b);
-  float h = state_in ? state_in[i] : 0.f;
-  for (int t = 0; t < n; ++t) {
-    float a, na;
-    gates(to_f32(*g.at(b, t, d)), a, na);
-    h = a * h + na * to_f32(*x.at(b, t, d));
-    *y.at(b, t, d) = from_f32<T>(h);
-  }
-  for (int t = n; t < s.len; ++t) *y.at(b, t, d) = from_f32<T>(0.f);
-  if (state_out) state_out[i] = h;
+// What a stretch of positions does to the state before it: h -> a h + b.
+struct Affine {
+  float a, b;
+};
+__device__ __forceinline__ Affine after(const Affine& later, const Affine& earlier) {
+  return {later.a * earlier.a, fmaf(later.a, earlier.b, later.b)};
 }
 
-template <class T>
-__global__ void __launch_bounds__(128) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g, View<const T> y,
-                                                  View<const T> gy, const float* state_in, const float* grad_out,
-                                                  View<T> gx, View<T> gg, float* grad_in) {
-  const int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x;
-  if (i >= (int64_t)s.batch * s.dim) return;
-  const int b = (int)(i / s.dim), d = (int)(i % s.dim);
-  const int n = live_len(s, b);
-  for (int t = n; t < s.len; ++t) *gx.at(b, t, d) = *gg.at(b, t, d) = from_f32<T>(0.f);
-  float c = grad_out ? grad_out[i] : 0.f;   // what the next position passes back
-  for (int t = n - 1; t >= 0; --t) {
-    float a, na;
-    gates(to_f32(*g.at(b, t, d)), a, na);
-    const float xv = to_f32(*x.at(b, t, d));
-    const float before = t ? to_f32(*y.at(b, t - 1, d)) : state_in ? state_in[i] : 0.f;
-    const float G = to_f32(*gy.at(b, t, d)) + c;
-    *gx.at(b, t, d) = from_f32<T>(na * G);
-    *gg.at(b, t, d) = from_f32<T>(a * na * (before - xv) * G);
-    c = a * G;
+// Records of the chain.  Each 64-bit half carries the tag, so a reader that
+// sees the wanted tag in both has both values of one write: no fence is needed.
+__device__ __forceinline__ void put_record(ulonglong2* p, Affine f, uint32_t tag) {
+  const uint64_t x = (uint64_t)tag << 32 | __float_as_uint(f.a), y = (uint64_t)tag << 32 | __float_as_uint(f.b);
+  asm volatile("st.relaxed.gpu.global.v2.b64 [%0], {%1, %2};" ::"l"(p), "l"(x), "l"(y) : "memory");
+}
+__device__ __forceinline__ uint32_t get_record(const ulonglong2* p, Affine& f) {
+  uint64_t x, y;
+  asm volatile("ld.relaxed.gpu.global.v2.b64 {%0, %1}, [%2];" : "=l"(x), "=l"(y) : "l"(p) : "memory");
+  f = {__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)y)};
+  const uint32_t tx = (uint32_t)(x >> 32), ty = (uint32_t)(y >> 32);
+  return tx == ty ? tx : 0u;
+}
+// The state before tile `i` of one channel's chain.  The chain is cut into
+// groups of kGroup tiles.  A tile writes its own effect for the later tiles of
+// its group, and a group's last tile the state after the group; a tile joins
+// the effects ahead of it in its group, read at once by the channel's J =
+// kGroup / kAhead lanes, behind the state before the group.  Along a sequence
+// only the groups wait for one another in turn (one write and read in L2 per
+// kGroup tiles), and the order of every join is fixed: results repeat bit for
+// bit.  `all`: what this tile does; `next`: a later tile needs to know; state0:
+// the state before tile 0.  All lanes of the warp call; the arguments are
+// uniform over a channel's lanes.
+__device__ __forceinline__ float chain_state(const ScanArgs& s, int64_t col, int i, bool want, bool next, Affine all,
+                                             float state0, uint32_t epoch) {
+  constexpr int J = kGroup / kAhead;
+  const int64_t pitch = (int64_t)s.batch * s.dim;
+  ulonglong2 *own = s.records + col, *states = s.records + s.tiles * pitch + col;
+  const int j = threadIdx.x & (J - 1), m = i / kGroup, at = i % kGroup;
+  if (want && next && j == 0 && at != kGroup - 1) put_record(own + i * pitch, all, epoch);
+  Affine f[kAhead], st{0.f, state0};
+  bool have[kAhead], have_state = !want || m == 0 || j != 0;
+#pragma unroll
+  for (int u = 0; u < kAhead; ++u) {
+    f[u] = {1.f, 0.f};
+    have[u] = !want || j * kAhead + u >= at;
   }
-  if (grad_in) grad_in[i] = c;
+  for (unsigned spins = 0;; ++spins) {
+    bool all_here = true;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u)
+      if (!have[u]) have[u] = get_record(own + (m * kGroup + j * kAhead + u) * pitch, f[u]) == epoch;
+    if (!have_state) have_state = get_record(states + m * pitch, st) == epoch;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) all_here = all_here && have[u];
+    if (__all_sync(kFull, all_here && have_state)) break;
+    if (spins >= kScanSpins) {
+      latch(s.status, EMB_ERR_TIMEOUT);
+      *(volatile uint32_t*)&s.shared->fail = 1u;
+      break;
+    }
+    if ((spins & 255u) == 255u && __any_sync(kFull, *(volatile uint32_t*)&s.shared->fail != 0u)) break;
+  }
+  Affine sum = f[0];
+#pragma unroll
+  for (int u = 1; u < kAhead; ++u) sum = after(f[u], sum);
+#pragma unroll
+  for (int o = 1; o < J; o <<= 1) {
+    const Affine e{__shfl_down_sync(kFull, sum.a, o, J), __shfl_down_sync(kFull, sum.b, o, J)};
+    sum = after(e, sum);   // the upper lanes' sums are not used
+  }
+  const float h = __shfl_sync(kFull, fmaf(sum.a, st.b, sum.b), 0, J);
+  if (want && next && j == 0 && at == kGroup - 1)
+    put_record(states + (m + 1) * pitch, {0.f, fmaf(all.a, h, all.b)}, epoch);
+  return h;
+}
+
+// A CTA's place: its threads as column vectors by stretches of R positions,
+// and again as channels by J lanes, for joining the stretches.
+template <int V, int R>
+struct Place {
+  int cx, ty, TT;            // column vector in the tile, stretch, positions of a tile
+  int ch, j, j_log, pitch;   // channel in the tile, lane of it
+  __device__ explicit Place(const ScanArgs& s) {
+    const int tid = threadIdx.x;
+    cx = tid & ((1 << s.cx_log) - 1);
+    ty = tid >> s.cx_log;
+    TT = (kScanThreads >> s.cx_log) * R;
+    j_log = max(31 - __clz(kScanThreads / V) - s.cx_log, 0);
+    j = tid & ((1 << j_log) - 1);
+    ch = tid >> j_log;
+    pitch = (V << s.cx_log) + 1;   // the lanes of a channel then read different banks
+  }
+};
+
+// Joins the stretches of a tile for one channel: lane j takes stretches j V ..
+// j V + V - 1 of (a, b) in shared memory, `back` in descending order.
+// ex: what the stretches before this lane's do; all: what the whole tile does.
+template <int V, class P>
+__device__ __forceinline__ void join_stretches(const P& p, const float* sa, const float* sb, bool back, Affine (&f)[V],
+                                               Affine& ex, Affine& all) {
+  const int J = 1 << p.j_log;
+  Affine m{1.f, 0.f};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int y = p.j * V + i, at = (back ? J * V - 1 - y : y) * p.pitch + p.ch;
+    f[i] = {sa[at], sb[at]};
+    m = after(f[i], m);
+  }
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    if (o < J) {
+      const Affine e{__shfl_up_sync(kFull, m.a, o, J), __shfl_up_sync(kFull, m.b, o, J)};
+      if (p.j >= o) m = after(m, e);
+    }
+  }
+  ex = {__shfl_up_sync(kFull, m.a, 1, J), __shfl_up_sync(kFull, m.b, 1, J)};
+  if (p.j == 0) ex = {1.f, 0.f};
+  all = {__shfl_sync(kFull, m.a, J - 1, J), __shfl_sync(kFull, m.b, J - 1, J)};
+}
+
+// The next tile of a chained call, in an order in which a tile comes after
+// the one it waits for.  Returns false when there are none.
+__device__ __forceinline__ bool take_tile(const ScanArgs& s, uint32_t* slot, uint32_t& tile) {
+  if (threadIdx.x == 0) *slot = atomicAdd(&s.shared->ticket, 1u);
+  __syncthreads();
+  tile = *slot;
+  if (tile < (uint32_t)(s.tiles * s.groups)) return true;
+  if (threadIdx.x == 0 && atomicAdd(&s.shared->done, 1u) == gridDim.x - 1) {
+    s.shared->ticket = 0;
+    s.shared->done = 0;
+    s.shared->fail = 0;
+    s.shared->epoch = s.shared->epoch == 0xffffffffu ? 1u : s.shared->epoch + 1;
+  }
+  return false;
+}
+
+// Channels of a tile as one lane group sees them.
+struct Channel {
+  bool ok;
+  int b, d, n;
+  int64_t col;   // b * dim + d
+};
+template <int V>
+__device__ __forceinline__ Channel channel_of(const ScanArgs& s, int64_t vec, int v) {
+  Channel c;
+  c.ok = vec < s.vecs;
+  const int per = s.dim / V;
+  c.b = c.ok ? (int)(vec / per) : 0;
+  c.d = c.ok ? (int)(vec % per) * V + v : 0;
+  c.n = c.ok ? live_len(s, c.b) : 0;
+  c.col = (int64_t)c.b * s.dim + c.d;
+  return c;
+}
+
+// Forward.  A thread keeps R positions of V channels as (a, (1 - a) x) in
+// registers, so x and gate are read once.  Its stretch's effect goes to shared
+// memory, the channels' lanes join the stretches behind the state before the
+// tile, and each thread then runs its positions from its own first state.
+// CHAIN: a CTA takes tiles by ticket and finds the state before its tile in the
+// records of the tiles ahead; otherwise it walks along time with the state in
+// hand.  cx = 256: a thread is a whole stretch of its own, nothing is joined.
+template <class T, int V, int R, bool CHAIN>
+__global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs s, View<const T> x, View<const T> g, View<T> y,
+                                                           const float* __restrict__ state_in,
+                                                           float* __restrict__ state_out) {
+  extern __shared__ float sm[];
+  __shared__ uint32_t slot;
+  const Place<V, R> p(s);
+  const bool whole = s.cx_log == 8;
+  float* sa = sm;
+  float* sb = sm + (kScanThreads >> s.cx_log) * p.pitch;
+  const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
+  uint32_t ticket = 0;
+  int64_t gi = blockIdx.x;
+  int k = 0;
+  float held = 0.f;          // walking: the channel's state
+  float own[V];              // whole: the thread's states
+  while (true) {
+    if constexpr (CHAIN) {
+      if (!take_tile(s, &slot, ticket)) break;
+      k = (int)(ticket / (uint32_t)s.groups);
+      gi = ticket % (uint32_t)s.groups;
+    }
+    const int t0 = k * p.TT + p.ty * R;
+    const Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
+    float a[R][V], b[R][V];
+    Vec<T, V> xr[R], gr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (t0 + r < c.n) {
+        xr[r] = get<V>(x, c.b, t0 + r, c.d);
+        gr[r] = get<V>(g, c.b, t0 + r, c.d);
+      }
+    }
+    float fa[V], fb[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool on = t0 + r < c.n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        float na;
+        gates(to_f32(gr[r].e[v]), a[r][v], na);
+        b[r][v] = na * to_f32(xr[r].e[v]);
+        if (!on) a[r][v] = 1.f, b[r][v] = 0.f;
+        fa[v] *= a[r][v];
+        fb[v] = fmaf(a[r][v], fb[v], b[r][v]);
+      }
+    }
+    float h[V];
+    if (whole) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (k == 0) own[v] = state_in && c.ok ? state_in[c.col + v] : 0.f;
+        h[v] = own[v];
+        own[v] = fmaf(fa[v], own[v], fb[v]);
+        if (state_out && c.ok && k == s.tiles - 1) state_out[c.col + v] = own[v];
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        sa[p.ty * p.pitch + p.cx * V + v] = fa[v];
+        sb[p.ty * p.pitch + p.cx * V + v] = fb[v];
+      }
+      __syncthreads();
+      const Channel q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
+      Affine f[V], ex, all;
+      join_stretches<V>(p, sa, sb, false, f, ex, all);
+      const int end = (k + 1) * p.TT;
+      const bool live = q.ok && (k * p.TT < q.n || k == 0);
+      if constexpr (CHAIN) {
+        const float state0 = live && k < kGroup && state_in ? state_in[q.col] : 0.f;
+        held = chain_state(s, q.col, k, live, end < q.n, all, state0, epoch);
+      } else if (k == 0) {
+        held = state_in && q.ok ? state_in[q.col] : 0.f;
+      }
+      float st = fmaf(ex.a, held, ex.b);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sb[(p.j * V + i) * p.pitch + p.ch] = st;
+        st = fmaf(f[i].a, st, f[i].b);
+      }
+      held = fmaf(all.a, held, all.b);
+      if (state_out && live && p.j == 0 && end >= q.n) state_out[q.col] = held;
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) h[v] = sb[p.ty * p.pitch + p.cx * V + v];
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int t = t0 + r;
+      Vec<T, V> o;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        h[v] = fmaf(a[r][v], h[v], b[r][v]);
+        o.e[v] = from_f32<T>(t < c.n ? h[v] : 0.f);
+      }
+      if (c.ok && t < s.len) put<V>(y, c.b, t, c.d, o);
+    }
+    if constexpr (!CHAIN) {
+      if (++k == s.tiles) break;
+    }
+    if (!CHAIN && !whole) __syncthreads();   // the shared stretches are read before the next tile's are written
+  }
+}
+
+// Backward, from the last position to the first: C_t = a_t (grad_y_t + C_{t+1})
+// is what position t passes back.  The gate's gradient needs the state before
+// each position.  fp32: a tile runs forward from y just before it, which costs
+// one row of y instead of all of them; both joins use the same products of
+// gates.  16 bits: y is read at every position (RERUN false) -- a rerun would
+// carry the rounding of the one row it starts from into states that are
+// smaller than that row, where y itself is off by half a unit of its own.
+template <class T, int V, int R, bool CHAIN>
+__global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
+                                                           View<const T> y, View<const T> gy,
+                                                           const float* __restrict__ state_in,
+                                                           const float* __restrict__ grad_out, View<T> gx, View<T> gg,
+                                                           float* __restrict__ grad_in) {
+  extern __shared__ float sm[];
+  __shared__ uint32_t slot;
+  const Place<V, R> p(s);
+  constexpr bool RERUN = sizeof(T) == 4;
+  const bool whole = s.cx_log == 8;
+  const int area = (kScanThreads >> s.cx_log) * p.pitch;
+  float *sa = sm, *sb = sm + area, *sc = sm + 2 * area;
+  const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
+  uint32_t ticket = 0;
+  int64_t gi = blockIdx.x;
+  int k = s.tiles - 1;
+  float held = 0.f;
+  float own[V];
+  while (true) {
+    if constexpr (CHAIN) {
+      if (!take_tile(s, &slot, ticket)) break;
+      k = s.tiles - 1 - (int)(ticket / (uint32_t)s.groups);
+      gi = ticket % (uint32_t)s.groups;
+    }
+    const int t0 = k * p.TT + p.ty * R;
+    const Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
+    Vec<T, V> xr[R], gr[R], dr[R], yr[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (t0 + r < c.n) {
+        xr[r] = get<V>(x, c.b, t0 + r, c.d);
+        gr[r] = get<V>(g, c.b, t0 + r, c.d);
+        dr[r] = get<V>(gy, c.b, t0 + r, c.d);
+        if (!RERUN && t0 + r > 0) yr[r] = get<V>(y, c.b, t0 + r - 1, c.d);
+      }
+    }
+    float a[R][V], na[R][V], xv[R][V], dy[R][V];
+    float fa[V], fb[V], fc[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f, fc[v] = 0.f;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool on = t0 + r < c.n;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        gates(to_f32(gr[r].e[v]), a[r][v], na[r][v]);
+        xv[r][v] = to_f32(xr[r].e[v]);
+        dy[r][v] = to_f32(dr[r].e[v]);
+        if (!on) a[r][v] = 1.f, na[r][v] = 0.f, xv[r][v] = 0.f, dy[r][v] = 0.f;
+        if (!RERUN) {
+          const float before = t0 + r > 0 ? to_f32(yr[r].e[v]) : state_in && on ? state_in[c.col + v] : 0.f;
+          xv[r][v] = on ? a[r][v] * na[r][v] * (before - xv[r][v]) : 0.f;   // the gate's factor of G
+        }
+        fa[v] *= a[r][v];
+        if (RERUN) fb[v] = fmaf(a[r][v], fb[v], na[r][v] * xv[r][v]);
+      }
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r)
+#pragma unroll
+      for (int v = 0; v < V; ++v) fc[v] = a[r][v] * (dy[r][v] + fc[v]);
+    float h[V], C[V];
+    if (whole) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (k == s.tiles - 1) own[v] = grad_out && c.ok ? grad_out[c.col + v] : 0.f;
+        C[v] = own[v];
+        own[v] = fmaf(fa[v], own[v], fc[v]);
+        if (grad_in && c.ok && k == 0) grad_in[c.col + v] = own[v];
+        h[v] = 0.f;
+        if (!RERUN) continue;
+        if (c.ok && t0 == 0) h[v] = state_in ? state_in[c.col + v] : 0.f;
+        else if (t0 < c.n) h[v] = to_f32(*y.at(c.b, t0 - 1, c.d + v));
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        sa[p.ty * p.pitch + p.cx * V + v] = fa[v];
+        if (RERUN) sb[p.ty * p.pitch + p.cx * V + v] = fb[v];
+        sc[p.ty * p.pitch + p.cx * V + v] = fc[v];
+      }
+      const Channel q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
+      const int start = k * p.TT;
+      const bool live = q.ok && (start < q.n || k == 0);
+      float first = 0.f;
+      if (RERUN && live) first = k == 0 ? (state_in ? state_in[q.col] : 0.f) : to_f32(*y.at(q.b, start - 1, q.d));
+      __syncthreads();
+      Affine f[V], ex, all;
+      float st;
+      if (RERUN) {
+        join_stretches<V>(p, sa, sb, false, f, ex, all);
+        st = fmaf(ex.a, first, ex.b);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          sb[(p.j * V + i) * p.pitch + p.ch] = st;
+          st = fmaf(f[i].a, st, f[i].b);
+        }
+      }
+      join_stretches<V>(p, sa, sc, true, f, ex, all);
+      // the chain of a channel begins at the tile of its last position
+      const int last = q.n > 0 ? (q.n - 1) / p.TT : 0;
+      if constexpr (CHAIN) {
+        const int i = live ? last - k : 0;
+        const float state0 = live && i < kGroup && grad_out ? grad_out[q.col] : 0.f;
+        held = chain_state(s, q.col, i, live, k > 0, all, state0, epoch);
+      } else if (k == last) {
+        held = grad_out && q.ok ? grad_out[q.col] : 0.f;
+      }
+      st = fmaf(ex.a, held, ex.b);
+      const int J = 1 << p.j_log;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        sc[(J * V - 1 - (p.j * V + i)) * p.pitch + p.ch] = st;
+        st = fmaf(f[i].a, st, f[i].b);
+      }
+      if (live) held = fmaf(all.a, held, all.b);
+      if (grad_in && live && p.j == 0 && k == 0) grad_in[q.col] = held;
+      __syncthreads();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if (RERUN) h[v] = sb[p.ty * p.pitch + p.cx * V + v];
+        C[v] = sc[p.ty * p.pitch + p.cx * V + v];
+      }
+    }
+    if (RERUN) {
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float before = h[v];
+          h[v] = fmaf(a[r][v], before, na[r][v] * xv[r][v]);
+          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);   // the gate's factor of G
+        }
+    }
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const int t = t0 + r;
+      Vec<T, V> ox, og;
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float G = dy[r][v] + C[v];
+        const bool on = t < c.n;
+        ox.e[v] = from_f32<T>(on ? na[r][v] * G : 0.f);
+        og.e[v] = from_f32<T>(on ? xv[r][v] * G : 0.f);
+        C[v] = a[r][v] * G;
+      }
+      if (c.ok && t < s.len) {
+        put<V>(gx, c.b, t, c.d, ox);
+        put<V>(gg, c.b, t, c.d, og);
+      }
+    }
+    if constexpr (!CHAIN) {
+      if (--k < 0) break;
+    }
+    if (!CHAIN && !whole) __syncthreads();
+  }
 }
 
 template <class T>
@@ -117,13 +562,58 @@ bool view_ok(const scan_view* v, int32_t dtype, int64_t batch, int64_t len, int6
          v->time_stride >= (batch - 1) * v->batch_stride + dim;
 }
 
-template <class T>
+
+template <class T, int V>
 View<T> as_view(const scan_view* v) {
-  return View<T>{(T*)v->data, v->batch_stride, v->time_stride};
+  return View<T>{(T*)v->data, v->batch_stride, v->time_stride,
+                 aligned_to(v->data, V * sizeof(T)) && v->batch_stride % V == 0 && v->time_stride % V == 0};
 }
 
 bool call_ok(emb_scan h, int32_t batch, int32_t len, int32_t dtype) {
   return h && batch >= 0 && batch <= h->max_batch && len >= 0 && len <= h->max_len && dtype_size(dtype) != 0;
+}
+
+// How a call is cut.  R: positions of a thread.
+struct Cut {
+  ScanArgs args;
+  bool chain;
+  unsigned grid;
+  size_t smem;
+};
+
+constexpr int kWideV = 4, kFwdR = 8, kBwdR = 4;   // V = 1: twice the positions, for as many bytes in flight
+constexpr int kChainCx = 3, kWalkCx = 5;          // log2 of the column vectors of a tile
+int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R, int sms) {
+  const int64_t cols = batch * dim;
+  (void)sms;
+  const int TT = (kScanThreads >> (V == 1 ? 5 : kChainCx)) * R;
+  const int64_t tiles = (len + TT - 1) / TT;
+  return (tiles + tiles / kGroup + 1) * cols;
+}
+
+Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int V, int R, int areas) {
+  Cut c{};
+  ScanArgs& a = c.args;
+  a.batch = batch;
+  a.len = len;
+  a.dim = h->dim;
+  a.vecs = (int64_t)batch * h->dim / V;
+  a.offsets = offsets;
+  a.status = h->status_d;
+  a.shared = h->shared_d;
+  a.records = h->records_d;
+  const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
+  c.chain = (a.vecs >> kWalkCx) < slots;
+  a.cx_log = c.chain ? (V == 1 ? 5 : kChainCx) : kWalkCx;
+  const int TT = (kScanThreads >> a.cx_log) * R;
+  a.tiles = (len + TT - 1) / TT;
+  if (a.tiles < 1) a.tiles = 1;
+  a.groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
+  if (a.tiles == 1) c.chain = false;
+  const int64_t all = a.groups * a.tiles;
+  c.grid = (unsigned)(c.chain ? (all < slots ? all : slots) : a.groups);
+  c.smem = (size_t)areas * (kScanThreads >> a.cx_log) * ((V << a.cx_log) + 1) * sizeof(float);
+  return c;
 }
 
 }  // namespace emb
@@ -134,7 +624,7 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   if (!out) return EMB_ERR_INVALID_ARG;
   *out = nullptr;
   if (dim < 1 || max_batch < 1 || max_len < 1) return EMB_ERR_INVALID_ARG;
-  if (dim > 65536) return EMB_ERR_UNSUPPORTED;
+  if (dim > 65536 || max_len > (1 << 30)) return EMB_ERR_UNSUPPORTED;
   emb_scan_s* h = new (std::nothrow) emb_scan_s();
   if (!h) return EMB_ERR_OOM;
   h->dim = dim;
@@ -143,10 +633,27 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
-  if (e == cudaSuccess) e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
+  if (e == cudaSuccess) {
+    const int64_t cols = (int64_t)h->sm_count * kCtasPerSm * (kWideV << kWalkCx) + dim;   // a call with more walks
+    const int64_t batch = (int64_t)max_batch * dim < cols ? max_batch : cols / dim + 1;
+    for (int V : {1, kWideV})
+      for (int R : {kFwdR, kBwdR}) {
+        const int64_t n = chain_records(dim, batch, max_len, V, V == 1 ? 2 * R : R, h->sm_count);
+        if (n > h->max_records) h->max_records = n;
+      }
+    e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
+  }
+  if (e == cudaSuccess) e = dev_alloc((void**)&h->shared_d, sizeof(ScanShared));
+  if (e == cudaSuccess) e = dev_alloc((void**)&h->records_d, sizeof(ulonglong2) * h->max_records);
   if (e == cudaSuccess) e = cudaMemset(h->status_d, 0, sizeof(uint32_t));
+  const ScanShared first{0, 0, 1, 0};   // epoch 0 is what cleared records hold
+  if (e == cudaSuccess) e = cudaMemcpy(h->shared_d, &first, sizeof(first), cudaMemcpyHostToDevice);
+  if (e == cudaSuccess) e = cudaMemset(h->records_d, 0, sizeof(ulonglong2) * h->max_records);
+  if (e == cudaSuccess) e = cudaDeviceSynchronize();
   if (e != cudaSuccess) {
     dev_free(h->status_d);
+    dev_free(h->shared_d);
+    dev_free(h->records_d);
     delete h;
     return cuda_status(e);
   }
@@ -158,6 +665,8 @@ extern "C" emb_status scan_destroy(emb_scan h) {
   if (!h) return EMB_ERR_INVALID_ARG;
   const cudaError_t e = cudaDeviceSynchronize();
   dev_free(h->status_d);
+  dev_free(h->shared_d);
+  dev_free(h->records_d);
   delete h;
   return cuda_status(e);
 }
@@ -171,6 +680,29 @@ extern "C" emb_status scan_get_device_status(emb_scan h, void* stream) {
   return (emb_status)st;
 }
 
+template <class T, int V, int R>
+static void launch_fwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
+                       const int32_t* offsets, const float* state_in, const scan_view* y, float* state_out,
+                       cudaStream_t stream) {
+  const Cut c = cut_call(h, batch, len, offsets, V, R, 2);
+  auto kernel = c.chain ? k_scan_fwd<T, V, R, true> : k_scan_fwd<T, V, R, false>;
+  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y),
+                                                  state_in, state_out);
+}
+
+template <class T, int V, int R>
+static void launch_bwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
+                       const int32_t* offsets, const float* state_in, const scan_view* y, const scan_view* grad_y,
+                       const float* grad_state_out, const scan_view* grad_x, const scan_view* grad_gate,
+                       float* grad_state_in, cudaStream_t stream) {
+  const Cut c = cut_call(h, batch, len, offsets, V, R, 3);
+  auto kernel = c.chain ? k_scan_bwd<T, V, R, true> : k_scan_bwd<T, V, R, false>;
+  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
+                                                  as_view<const T, V>(y), as_view<const T, V>(grad_y), state_in,
+                                                  grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate),
+                                                  grad_state_in);
+}
+
 extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
                                    const scan_view* gate, const int32_t* offsets, const float* state_in,
                                    const scan_view* y, float* state_out, void* stream) {
@@ -178,13 +710,11 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
       !view_ok(gate, dtype, batch, len, h->dim, false) || !view_ok(y, dtype, batch, len, h->dim, true))
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
-  const ScanArgs s{batch, len, h->dim, offsets, h->status_d};
-  const int64_t n = (int64_t)batch * h->dim, grid = (n + 127) / 128;
-  if (grid >= (int64_t(1) << 31)) return EMB_ERR_UNSUPPORTED;
+  const bool vec = h->dim % kWideV == 0;
   with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_scan_fwd<T><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(s, as_view<const T>(x), as_view<const T>(gate),
-                                                                   as_view<T>(y), state_in, state_out);
+    auto launch = vec ? launch_fwd<T, kWideV, kFwdR> : launch_fwd<T, 1, 2 * kFwdR>;
+    launch(h, batch, len, x, gate, offsets, state_in, y, state_out, (cudaStream_t)stream);
   });
   return cuda_status(cudaGetLastError());
 }
@@ -200,14 +730,12 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
       !view_ok(grad_gate, dtype, batch, len, h->dim, true))
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
-  const ScanArgs s{batch, len, h->dim, offsets, h->status_d};
-  const int64_t n = (int64_t)batch * h->dim, grid = (n + 127) / 128;
-  if (grid >= (int64_t(1) << 31)) return EMB_ERR_UNSUPPORTED;
+  const bool vec = h->dim % kWideV == 0;
   with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_scan_bwd<T><<<(unsigned)grid, 128, 0, (cudaStream_t)stream>>>(
-        s, as_view<const T>(x), as_view<const T>(gate), as_view<const T>(y), as_view<const T>(grad_y), state_in,
-        grad_state_out, as_view<T>(grad_x), as_view<T>(grad_gate), grad_state_in);
+    auto launch = vec ? launch_bwd<T, kWideV, kBwdR> : launch_bwd<T, 1, 2 * kBwdR>;
+    launch(h, batch, len, x, gate, offsets, state_in, y, grad_y, grad_state_out, grad_x, grad_gate, grad_state_in,
+           (cudaStream_t)stream);
   });
   return cuda_status(cudaGetLastError());
 }
