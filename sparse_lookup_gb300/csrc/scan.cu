@@ -34,13 +34,16 @@ constexpr int kGroup = 32;                  // tiles of a chain's group
 constexpr int kAhead = 4;                   // records of a group that one lane reads
 constexpr int kCtasPerSm = 2;
 
-// sigmoid(g) and sigmoid(-g), each from its own quotient: 1 - a would lose
-// every digit of the smaller one where the gate saturates.
+// sigmoid(g) and sigmoid(-g) from one exponential: with e = exp(-g), a = 1 /
+// (1 + e) and 1 - a = e a keeps every digit where the gate saturates.  e stops
+// at 2^126 (gates below -87 then leave 2^-126 of the state); NaN goes through.
+// A gate of +infinity gives exactly (1, 0): positions that are not there.
 __device__ __forceinline__ void gates(float g, float& a, float& na) {
-  const float e = __expf(-fabsf(g));
-  const float hi = __fdividef(1.f, 1.f + e), lo = e * hi;
-  a = g >= 0.f ? hi : lo;
-  na = g >= 0.f ? lo : hi;
+  float e;
+  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e) : "f"(g * -1.44269504f));
+  asm("ex2.approx.f32 %0, %0;" : "+f"(e));
+  asm("rcp.approx.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
+  na = e * a;
 }
 
 // `wide`: every column vector of the view can be moved in one access.  The
@@ -55,9 +58,8 @@ struct View {
 };
 
 template <int V, class T>
-__device__ __forceinline__ auto get(const View<const T>& w, int64_t b, int64_t t, int64_t d) {
-  const T* p = w.at(b, t, d);
-  if (w.wide) return load_vec<T, V>(p);
+__device__ __forceinline__ Vec<T, V> get(const T* p, bool wide) {
+  if (wide) return load_vec<T, V>(p);
   Vec<T, V> r;
 #pragma unroll
   for (int v = 0; v < V; ++v) r.e[v] = p[v];
@@ -65,9 +67,8 @@ __device__ __forceinline__ auto get(const View<const T>& w, int64_t b, int64_t t
 }
 
 template <int V, class T>
-__device__ __forceinline__ void put(const View<T>& w, int64_t b, int64_t t, int64_t d, const Vec<T, V>& r) {
-  T* p = w.at(b, t, d);
-  if (w.wide) {
+__device__ __forceinline__ void put(T* p, bool wide, const Vec<T, V>& r) {
+  if (wide) {
     store_vec(p, r);
   } else {
 #pragma unroll
@@ -81,8 +82,10 @@ struct ScanArgs {
   int32_t batch, len, dim;
   int32_t cx_log;        // column vectors of a tile, log2
   int32_t tiles;         // along time
+  uint32_t total;        // tiles in all (chained calls)
   int64_t vecs;          // column vectors in all: batch * dim / V
-  int64_t groups;        // tiles across: ceil(vecs / cx)
+  DivMagic per;          // by dim / V: a column vector's batch entry
+  DivMagic32 groups;     // by the tiles across (chained calls)
   const int32_t* offsets;
   uint32_t* status;
   ScanShared* shared;
@@ -215,23 +218,20 @@ __device__ __forceinline__ void join_stretches(const P& p, const float* sa, cons
   all = {__shfl_sync(kFull, m.a, J - 1, J), __shfl_sync(kFull, m.b, J - 1, J)};
 }
 
-// The next tile of a chained call, in an order in which a tile comes after
-// the one it waits for.  Returns false when there are none.
-__device__ __forceinline__ bool take_tile(const ScanArgs& s, uint32_t* slot, uint32_t& tile) {
-  if (threadIdx.x == 0) *slot = atomicAdd(&s.shared->ticket, 1u);
-  __syncthreads();
-  tile = *slot;
-  if (tile < (uint32_t)(s.tiles * s.groups)) return true;
-  if (threadIdx.x == 0 && atomicAdd(&s.shared->done, 1u) == gridDim.x - 1) {
-    s.shared->ticket = 0;
-    s.shared->done = 0;
-    s.shared->fail = 0;
-    s.shared->epoch = s.shared->epoch == 0xffffffffu ? 1u : s.shared->epoch + 1;
-  }
-  return false;
+// The next tile of a chained call: tickets go to the tiles of one stretch of
+// time, then of the next, so a tile comes after the one it waits for.
+__device__ __forceinline__ uint32_t take_ticket(const ScanArgs& s) { return atomicAdd(&s.shared->ticket, 1u); }
+
+// Called by one thread of a CTA that found no more tiles.
+__device__ __forceinline__ void leave(const ScanArgs& s) {
+  if (atomicAdd(&s.shared->done, 1u) != gridDim.x - 1) return;
+  s.shared->ticket = 0;
+  s.shared->done = 0;
+  s.shared->fail = 0;
+  s.shared->epoch = s.shared->epoch == 0xffffffffu ? 1u : s.shared->epoch + 1;
 }
 
-// Channels of a tile as one lane group sees them.
+// Channel v of a column vector.
 struct Channel {
   bool ok;
   int b, d, n;
@@ -241,72 +241,140 @@ template <int V>
 __device__ __forceinline__ Channel channel_of(const ScanArgs& s, int64_t vec, int v) {
   Channel c;
   c.ok = vec < s.vecs;
-  const int per = s.dim / V;
-  c.b = c.ok ? (int)(vec / per) : 0;
-  c.d = c.ok ? (int)(vec % per) * V + v : 0;
+  if (!c.ok) vec = 0;
+  c.b = (int)div_magic((uint64_t)vec, s.per);
+  c.d = (int)(vec - (int64_t)c.b * (int64_t)s.per.d) * V + v;
   c.n = c.ok ? live_len(s, c.b) : 0;
-  c.col = (int64_t)c.b * s.dim + c.d;
+  c.col = vec * V + v;
   return c;
 }
+
+// A thread's R column vectors of one input, staged in shared memory: only the
+// thread itself reads what it copied, so no barrier is needed.  Copies are
+// asynchronous where the view allows it; otherwise the vectors are loaded
+// when they are due (`now`).  Positions at or past n hold `dead`.
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <class T, int V, int R>
+struct Staged {
+  static constexpr int kBytes = V * (int)sizeof(T);
+  Vec<T, V>* at;   // + r * kScanThreads
+  __device__ bool async(const View<const T>& w) const { return kBytes >= 4 && w.wide; }
+  __device__ void fill(const View<const T>& w, const T* p, int t0, int first, int n, float dead, bool now) const {
+    if (async(w) == now) return;
+    Vec<T, V> z;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z.e[v] = from_f32<T>(dead);
+    if constexpr (kBytes >= 4) {
+      if (!now) {
+#pragma unroll
+        for (int r = 0; r < R; ++r, p += w.ts) {
+          Vec<T, V>* to = at + r * kScanThreads;
+          if (t0 + r >= first && t0 + r < n) {
+            const unsigned d = (unsigned)__cvta_generic_to_shared(to);
+            if constexpr (kBytes == 16)
+              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+            else
+              asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(p), "n"(kBytes) : "memory");
+          } else {
+            *to = z;
+          }
+        }
+        return;
+      }
+    }
+    Vec<T, V> got[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r, p += w.ts) {
+      got[r] = z;
+      if (t0 + r >= first && t0 + r < n) got[r] = get<V>(p, w.wide);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) at[r * kScanThreads] = got[r];
+  }
+};
+
+#define SCAN_DEAD_GATE __int_as_float(0x7f800000)
 
 // Forward.  A thread keeps R positions of V channels as (a, (1 - a) x) in
 // registers, so x and gate are read once.  Its stretch's effect goes to shared
 // memory, the channels' lanes join the stretches behind the state before the
-// tile, and each thread then runs its positions from its own first state.
+// tile, and each thread then runs its positions from its own first state.  The
+// next tile's inputs are copied meanwhile.
 // CHAIN: a CTA takes tiles by ticket and finds the state before its tile in the
 // records of the tiles ahead; otherwise it walks along time with the state in
 // hand.  cx = 256: a thread is a whole stretch of its own, nothing is joined.
 template <class T, int V, int R, bool CHAIN>
-__global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs s, View<const T> x, View<const T> g, View<T> y,
-                                                           const float* __restrict__ state_in,
-                                                           float* __restrict__ state_out) {
-  extern __shared__ float sm[];
+__global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs s, View<const T> x, View<const T> g,
+                                                                       View<T> y, const float* __restrict__ state_in,
+                                                                       float* __restrict__ state_out) {
+  extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t slot;
   const Place<V, R> p(s);
   const bool whole = s.cx_log == 8;
-  float* sa = sm;
-  float* sb = sm + (kScanThreads >> s.cx_log) * p.pitch;
+  const Staged<T, V, R> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads};
+  float* sa = (float*)(raw + 2 * R * kScanThreads * sizeof(Vec<T, V>));
+  float* sb = sa + (kScanThreads >> s.cx_log) * p.pitch;
   const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
-  uint32_t ticket = 0;
-  int64_t gi = blockIdx.x;
-  int k = 0;
+  uint32_t tile = 0, next = 0;
+  if constexpr (CHAIN) {
+    if (threadIdx.x == 0) slot = take_ticket(s);
+    __syncthreads();
+    tile = slot;
+  }
+  int k = CHAIN ? (int)div_magic32(tile, s.groups) : 0;
+  int64_t gi = CHAIN ? tile - (uint32_t)k * s.groups.d : blockIdx.x;
+  Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
+  auto fill = [&](const Channel& c, int k, bool now) {
+    const int t0 = k * p.TT + p.ty * R;
+    sx.fill(x, x.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
+    sg.fill(g, g.at(c.b, t0, c.d), t0, 0, c.n, SCAN_DEAD_GATE, now);
+  };
+  if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;          // walking: the channel's state
   float own[V];              // whole: the thread's states
-  while (true) {
-    if constexpr (CHAIN) {
-      if (!take_tile(s, &slot, ticket)) break;
-      k = (int)(ticket / (uint32_t)s.groups);
-      gi = ticket % (uint32_t)s.groups;
-    }
+  while (CHAIN ? tile < s.total : k < s.tiles) {
     const int t0 = k * p.TT + p.ty * R;
-    const Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
-    float a[R][V], b[R][V];
-    Vec<T, V> xr[R], gr[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (t0 + r < c.n) {
-        xr[r] = get<V>(x, c.b, t0 + r, c.d);
-        gr[r] = get<V>(g, c.b, t0 + r, c.d);
-      }
-    }
-    float fa[V], fb[V];
+    fill(c, k, true);
+    copies_done();
+    uint32_t ticket = 0;
+    if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
+    float a[R][V], b[R][V], fa[V], fb[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool on = t0 + r < c.n;
+      const Vec<T, V> xr = sx.at[r * kScanThreads], gr = sg.at[r * kScanThreads];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         float na;
-        gates(to_f32(gr[r].e[v]), a[r][v], na);
-        b[r][v] = na * to_f32(xr[r].e[v]);
-        if (!on) a[r][v] = 1.f, b[r][v] = 0.f;
+        gates(to_f32(gr.e[v]), a[r][v], na);
+        b[r][v] = na * to_f32(xr.e[v]);
         fa[v] *= a[r][v];
         fb[v] = fmaf(a[r][v], fb[v], b[r][v]);
       }
     }
+    // the staged inputs are in registers: copy the next tile's.  Its ticket was
+    // drawn when this tile's inputs had come, not before: a CTA that drew two
+    // neighbours would publish the second only after the first's own wait.
+    int k1 = k + 1;
+    int64_t gi1 = gi;
+    Channel c1 = c;
+    auto ahead = [&] {
+      if constexpr (CHAIN) {
+        next = slot;
+        k1 = (int)div_magic32(next, s.groups);
+        gi1 = next - (uint32_t)k1 * s.groups.d;
+        if (next >= s.total) return;
+        c1 = channel_of<V>(s, (gi1 << s.cx_log) + p.cx, 0);
+      } else if (k1 >= s.tiles) {
+        return;
+      }
+      fill(c1, k1, false);
+    };
     float h[V];
     if (whole) {
+      ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (k == 0) own[v] = state_in && c.ok ? state_in[c.col + v] : 0.f;
@@ -320,7 +388,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
         sa[p.ty * p.pitch + p.cx * V + v] = fa[v];
         sb[p.ty * p.pitch + p.cx * V + v] = fb[v];
       }
+      if (CHAIN && threadIdx.x == 0) slot = ticket;
       __syncthreads();
+      ahead();
       const Channel q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
       Affine f[V], ex, all;
       join_stretches<V>(p, sa, sb, false, f, ex, all);
@@ -344,8 +414,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
 #pragma unroll
       for (int v = 0; v < V; ++v) h[v] = sb[p.ty * p.pitch + p.cx * V + v];
     }
+    T* to = y.at(c.b, t0, c.d);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
+    for (int r = 0; r < R; ++r, to += y.ts) {
       const int t = t0 + r;
       Vec<T, V> o;
 #pragma unroll
@@ -353,13 +424,12 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
         h[v] = fmaf(a[r][v], h[v], b[r][v]);
         o.e[v] = from_f32<T>(t < c.n ? h[v] : 0.f);
       }
-      if (c.ok && t < s.len) put<V>(y, c.b, t, c.d, o);
+      if (c.ok && t < s.len) put<V>(to, y.wide, o);
     }
-    if constexpr (!CHAIN) {
-      if (++k == s.tiles) break;
-    }
-    if (!CHAIN && !whole) __syncthreads();   // the shared stretches are read before the next tile's are written
+    c = c1, k = k1, gi = gi1;
+    tile = next;
   }
+  if (CHAIN && threadIdx.x == 0) leave(s);
 }
 
 // Backward, from the last position to the first: C_t = a_t (grad_y_t + C_{t+1})
@@ -371,57 +441,64 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
 // smaller than that row, where y itself is off by half a unit of its own.
 template <class T, int V, int R, bool CHAIN>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
-                                                           View<const T> y, View<const T> gy,
-                                                           const float* __restrict__ state_in,
-                                                           const float* __restrict__ grad_out, View<T> gx, View<T> gg,
-                                                           float* __restrict__ grad_in) {
-  extern __shared__ float sm[];
+                                                                       View<const T> y, View<const T> gy,
+                                                                       const float* __restrict__ state_in,
+                                                                       const float* __restrict__ grad_out, View<T> gx,
+                                                                       View<T> gg, float* __restrict__ grad_in) {
+  constexpr bool RERUN = sizeof(T) == 4;
+  extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t slot;
   const Place<V, R> p(s);
-  constexpr bool RERUN = sizeof(T) == 4;
   const bool whole = s.cx_log == 8;
   const int area = (kScanThreads >> s.cx_log) * p.pitch;
-  float *sa = sm, *sb = sm + area, *sc = sm + 2 * area;
+  const Staged<T, V, R> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads},
+      sd{sg.at + R * kScanThreads}, sy{sd.at + R * kScanThreads};
+  float* sa = (float*)(raw + (RERUN ? 3 : 4) * R * kScanThreads * sizeof(Vec<T, V>));
+  float *sb = sa + area, *sc = sb + area;
   const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
-  uint32_t ticket = 0;
-  int64_t gi = blockIdx.x;
-  int k = s.tiles - 1;
+  uint32_t tile = 0, next = 0;
+  if constexpr (CHAIN) {
+    if (threadIdx.x == 0) slot = take_ticket(s);
+    __syncthreads();
+    tile = slot;
+  }
+  int k = s.tiles - 1 - (CHAIN ? (int)div_magic32(tile, s.groups) : 0);
+  int64_t gi = CHAIN ? tile - (uint32_t)(s.tiles - 1 - k) * s.groups.d : blockIdx.x;
+  Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
+  auto fill = [&](const Channel& c, int k, bool now) {
+    const int t0 = k * p.TT + p.ty * R;
+    sx.fill(x, x.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
+    sg.fill(g, g.at(c.b, t0, c.d), t0, 0, c.n, SCAN_DEAD_GATE, now);
+    sd.fill(gy, gy.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
+    if (!RERUN) sy.fill(y, y.at(c.b, (int64_t)t0 - 1, c.d), t0, 1, c.n, 0.f, now);
+  };
+  if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;
   float own[V];
-  while (true) {
-    if constexpr (CHAIN) {
-      if (!take_tile(s, &slot, ticket)) break;
-      k = s.tiles - 1 - (int)(ticket / (uint32_t)s.groups);
-      gi = ticket % (uint32_t)s.groups;
-    }
+  while (CHAIN ? tile < s.total : k >= 0) {
     const int t0 = k * p.TT + p.ty * R;
-    const Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
-    Vec<T, V> xr[R], gr[R], dr[R], yr[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      if (t0 + r < c.n) {
-        xr[r] = get<V>(x, c.b, t0 + r, c.d);
-        gr[r] = get<V>(g, c.b, t0 + r, c.d);
-        dr[r] = get<V>(gy, c.b, t0 + r, c.d);
-        if (!RERUN && t0 + r > 0) yr[r] = get<V>(y, c.b, t0 + r - 1, c.d);
-      }
-    }
-    float a[R][V], na[R][V], xv[R][V], dy[R][V];
+    fill(c, k, true);
+    copies_done();
+    uint32_t ticket = 0;
+    if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
+    float a[R][V], na[R][V], xv[R][V], dy[R][V];   // xv: x, then the gate's factor of G
     float fa[V], fb[V], fc[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f, fc[v] = 0.f;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const bool on = t0 + r < c.n;
+      const Vec<T, V> xr = sx.at[r * kScanThreads], gr = sg.at[r * kScanThreads], dr = sd.at[r * kScanThreads];
+      Vec<T, V> yr;
+      if (!RERUN) yr = sy.at[r * kScanThreads];
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        gates(to_f32(gr[r].e[v]), a[r][v], na[r][v]);
-        xv[r][v] = to_f32(xr[r].e[v]);
-        dy[r][v] = to_f32(dr[r].e[v]);
-        if (!on) a[r][v] = 1.f, na[r][v] = 0.f, xv[r][v] = 0.f, dy[r][v] = 0.f;
+        gates(to_f32(gr.e[v]), a[r][v], na[r][v]);
+        xv[r][v] = to_f32(xr.e[v]);
+        dy[r][v] = to_f32(dr.e[v]);
         if (!RERUN) {
-          const float before = t0 + r > 0 ? to_f32(yr[r].e[v]) : state_in && on ? state_in[c.col + v] : 0.f;
-          xv[r][v] = on ? a[r][v] * na[r][v] * (before - xv[r][v]) : 0.f;   // the gate's factor of G
+          float before = to_f32(yr.e[v]);
+          if (r == 0 && t0 == 0) before = state_in && c.ok ? state_in[c.col + v] : 0.f;
+          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);
         }
         fa[v] *= a[r][v];
         if (RERUN) fb[v] = fmaf(a[r][v], fb[v], na[r][v] * xv[r][v]);
@@ -431,8 +508,26 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
     for (int r = R - 1; r >= 0; --r)
 #pragma unroll
       for (int v = 0; v < V; ++v) fc[v] = a[r][v] * (dy[r][v] + fc[v]);
+    // the next tile's inputs (as in the forward)
+    int k1 = k - 1;
+    int64_t gi1 = gi;
+    Channel c1 = c;
+    auto ahead = [&] {
+      if constexpr (CHAIN) {
+        next = slot;
+        const int back = (int)div_magic32(next, s.groups);
+        k1 = s.tiles - 1 - back;
+        gi1 = next - (uint32_t)back * s.groups.d;
+        if (next >= s.total) return;
+        c1 = channel_of<V>(s, (gi1 << s.cx_log) + p.cx, 0);
+      } else if (k1 < 0) {
+        return;
+      }
+      fill(c1, k1, false);
+    };
     float h[V], C[V];
     if (whole) {
+      ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (k == s.tiles - 1) own[v] = grad_out && c.ok ? grad_out[c.col + v] : 0.f;
@@ -456,7 +551,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       const bool live = q.ok && (start < q.n || k == 0);
       float first = 0.f;
       if (RERUN && live) first = k == 0 ? (state_in ? state_in[q.col] : 0.f) : to_f32(*y.at(q.b, start - 1, q.d));
+      if (CHAIN && threadIdx.x == 0) slot = ticket;
       __syncthreads();
+      ahead();
       Affine f[V], ex, all;
       float st;
       if (RERUN) {
@@ -501,11 +598,12 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
         for (int v = 0; v < V; ++v) {
           const float before = h[v];
           h[v] = fmaf(a[r][v], before, na[r][v] * xv[r][v]);
-          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);   // the gate's factor of G
+          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);
         }
     }
+    T *tx = gx.at(c.b, (int64_t)t0 + R - 1, c.d), *tg = gg.at(c.b, (int64_t)t0 + R - 1, c.d);
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) {
+    for (int r = R - 1; r >= 0; --r, tx -= gx.ts, tg -= gg.ts) {
       const int t = t0 + r;
       Vec<T, V> ox, og;
 #pragma unroll
@@ -517,15 +615,14 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
         C[v] = a[r][v] * G;
       }
       if (c.ok && t < s.len) {
-        put<V>(gx, c.b, t, c.d, ox);
-        put<V>(gg, c.b, t, c.d, og);
+        put<V>(tx, gx.wide, ox);
+        put<V>(tg, gg.wide, og);
       }
     }
-    if constexpr (!CHAIN) {
-      if (--k < 0) break;
-    }
-    if (!CHAIN && !whole) __syncthreads();
+    c = c1, k = k1, gi = gi1;
+    tile = next;
   }
+  if (CHAIN && threadIdx.x == 0) leave(s);
 }
 
 template <class T>
@@ -591,7 +688,8 @@ int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R, int
   return (tiles + tiles / kGroup + 1) * cols;
 }
 
-Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int V, int R, int areas) {
+Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int V, int R, int areas,
+             size_t staged) {
   Cut c{};
   ScanArgs& a = c.args;
   a.batch = batch;
@@ -608,11 +706,16 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   const int TT = (kScanThreads >> a.cx_log) * R;
   a.tiles = (len + TT - 1) / TT;
   if (a.tiles < 1) a.tiles = 1;
-  a.groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
+  const int64_t groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
   if (a.tiles == 1) c.chain = false;
-  const int64_t all = a.groups * a.tiles;
-  c.grid = (unsigned)(c.chain ? (all < slots ? all : slots) : a.groups);
-  c.smem = (size_t)areas * (kScanThreads >> a.cx_log) * ((V << a.cx_log) + 1) * sizeof(float);
+  a.per = make_div_magic((uint64_t)(h->dim / V));
+  if (c.chain) {
+    a.groups = make_div_magic32((uint32_t)groups);
+    a.total = (uint32_t)(groups * a.tiles);
+  }
+  const int64_t all = groups * a.tiles;
+  c.grid = (unsigned)(c.chain ? (all < slots ? all : slots) : groups);
+  c.smem = staged + (size_t)areas * (kScanThreads >> a.cx_log) * ((V << a.cx_log) + 1) * sizeof(float);
   return c;
 }
 
@@ -680,27 +783,38 @@ extern "C" emb_status scan_get_device_status(emb_scan h, void* stream) {
   return (emb_status)st;
 }
 
-template <class T, int V, int R>
-static void launch_fwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
-                       const int32_t* offsets, const float* state_in, const scan_view* y, float* state_out,
-                       cudaStream_t stream) {
-  const Cut c = cut_call(h, batch, len, offsets, V, R, 2);
-  auto kernel = c.chain ? k_scan_fwd<T, V, R, true> : k_scan_fwd<T, V, R, false>;
-  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y),
-                                                  state_in, state_out);
+template <class K>
+static cudaError_t allow_shared(K kernel) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 << 10);
 }
 
 template <class T, int V, int R>
-static void launch_bwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
+static cudaError_t launch_fwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
+                       const int32_t* offsets, const float* state_in, const scan_view* y, float* state_out,
+                       cudaStream_t stream) {
+  const Cut c = cut_call(h, batch, len, offsets, V, R, 2, 2 * R * kScanThreads * V * sizeof(T));
+  auto kernel = c.chain ? k_scan_fwd<T, V, R, true> : k_scan_fwd<T, V, R, false>;
+  static const cudaError_t room[2] = {allow_shared(k_scan_fwd<T, V, R, false>), allow_shared(k_scan_fwd<T, V, R, true>)};
+  if (room[c.chain] != cudaSuccess) return room[c.chain];
+  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y),
+                                                  state_in, state_out);
+  return cudaGetLastError();
+}
+
+template <class T, int V, int R>
+static cudaError_t launch_bwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
                        const int32_t* offsets, const float* state_in, const scan_view* y, const scan_view* grad_y,
                        const float* grad_state_out, const scan_view* grad_x, const scan_view* grad_gate,
                        float* grad_state_in, cudaStream_t stream) {
-  const Cut c = cut_call(h, batch, len, offsets, V, R, 3);
+  const Cut c = cut_call(h, batch, len, offsets, V, R, 3, (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T));
   auto kernel = c.chain ? k_scan_bwd<T, V, R, true> : k_scan_bwd<T, V, R, false>;
+  static const cudaError_t room[2] = {allow_shared(k_scan_bwd<T, V, R, false>), allow_shared(k_scan_bwd<T, V, R, true>)};
+  if (room[c.chain] != cudaSuccess) return room[c.chain];
   kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
                                                   as_view<const T, V>(y), as_view<const T, V>(grad_y), state_in,
                                                   grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate),
                                                   grad_state_in);
+  return cudaGetLastError();
 }
 
 extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
@@ -711,12 +825,11 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
   const bool vec = h->dim % kWideV == 0;
-  with_element(dtype, [&](auto* t) {
+  return cuda_status(with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     auto launch = vec ? launch_fwd<T, kWideV, kFwdR> : launch_fwd<T, 1, 2 * kFwdR>;
-    launch(h, batch, len, x, gate, offsets, state_in, y, state_out, (cudaStream_t)stream);
-  });
-  return cuda_status(cudaGetLastError());
+    return launch(h, batch, len, x, gate, offsets, state_in, y, state_out, (cudaStream_t)stream);
+  }));
 }
 
 extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
@@ -731,13 +844,12 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
   const bool vec = h->dim % kWideV == 0;
-  with_element(dtype, [&](auto* t) {
+  return cuda_status(with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
     auto launch = vec ? launch_bwd<T, kWideV, kBwdR> : launch_bwd<T, 1, 2 * kBwdR>;
-    launch(h, batch, len, x, gate, offsets, state_in, y, grad_y, grad_state_out, grad_x, grad_gate, grad_state_in,
-           (cudaStream_t)stream);
-  });
-  return cuda_status(cudaGetLastError());
+    return launch(h, batch, len, x, gate, offsets, state_in, y, grad_y, grad_state_out, grad_x, grad_gate,
+                  grad_state_in, (cudaStream_t)stream);
+  }));
 }
 
 extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
