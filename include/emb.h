@@ -420,7 +420,8 @@ typedef struct {
 /* scan_create -- workspace of a gated linear recurrence over sequences:
  *   a_t = sigmoid(gate_t);  h_t = a_t * h_{t-1} + (1 - a_t) * x_t
  * per batch entry and channel, over dim channels (1 .. 65536), at most
- * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^30) positions.
+ * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^30) positions,
+ * batch * dim < 2^32 in a call.
  * Calls on one handle must be ordered (one stream, or streams joined by
  * events).  *out is NULL on error. */
 emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_len, emb_scan* out);

@@ -30,20 +30,125 @@ namespace emb {
 
 constexpr int kScanThreads = 256;
 constexpr unsigned kScanSpins = 1u << 21;   // rounds a wait takes at most (about a second)
-constexpr int kGroup = 32;                  // tiles of a chain's group
-constexpr int kAhead = 4;                   // records of a group that one lane reads
+constexpr int kGroup = 16;                  // tiles of a chain's group
+constexpr int kAhead = 2;                   // records of a group that one lane reads
 constexpr int kCtasPerSm = 2;
 
+// V channels of a thread.  Pairs go through the packed fp32 instructions: the
+// recurrence is bound by instruction issue where elements are 16 bits.
+template <int V>
+struct Lanes {
+  float v[V];
+};
+template <int V>
+__device__ __forceinline__ Lanes<V> all_of(float x) {
+  Lanes<V> o;
+#pragma unroll
+  for (int i = 0; i < V; ++i) o.v[i] = x;
+  return o;
+}
+#define LANES_OP(name, args, one, two)                          \
+  template <int V>                                              \
+  __device__ __forceinline__ Lanes<V> name args {               \
+    Lanes<V> o;                                                 \
+    if constexpr (V == 1) {                                     \
+      o.v[0] = one;                                             \
+    } else {                                                    \
+      _Pragma("unroll") for (int i = 0; i < V; i += 2) {        \
+        const float2 r = two;                                   \
+        o.v[i] = r.x, o.v[i + 1] = r.y;                         \
+      }                                                         \
+    }                                                           \
+    return o;                                                   \
+  }
+#define PAIR(x) make_float2((x).v[i], (x).v[i + 1])
+LANES_OP(add, (const Lanes<V>& a, const Lanes<V>& b), __fadd_rn(a.v[0], b.v[0]), __fadd2_rn(PAIR(a), PAIR(b)))
+LANES_OP(sub, (const Lanes<V>& a, const Lanes<V>& b), __fsub_rn(a.v[0], b.v[0]),
+         __ffma2_rn(PAIR(b), make_float2(-1.f, -1.f), PAIR(a)))
+LANES_OP(mul, (const Lanes<V>& a, const Lanes<V>& b), __fmul_rn(a.v[0], b.v[0]), __fmul2_rn(PAIR(a), PAIR(b)))
+LANES_OP(mad, (const Lanes<V>& a, const Lanes<V>& b, const Lanes<V>& c), __fmaf_rn(a.v[0], b.v[0], c.v[0]),
+         __ffma2_rn(PAIR(a), PAIR(b), PAIR(c)))
+#undef PAIR
+#undef LANES_OP
+
+template <class T, int V>
+__device__ __forceinline__ Lanes<V> widen(const Vec<T, V>& x) {
+  Lanes<V> o;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      float2 r;
+      if constexpr (std::is_same_v<T, __half>) {
+        r = __half22float2(*reinterpret_cast<const __half2*>(&x.e[i]));
+      } else {
+        const uint32_t u = *reinterpret_cast<const uint32_t*>(&x.e[i]);
+        r = make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+      }
+      o.v[i] = r.x, o.v[i + 1] = r.y;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.v[i] = to_f32(x.e[i]);
+  }
+  return o;
+}
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> narrow(const Lanes<V>& x) {
+  Vec<T, V> o;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if constexpr (std::is_same_v<T, __half>)
+        *reinterpret_cast<__half2*>(&o.e[i]) = __floats2half2_rn(x.v[i], x.v[i + 1]);
+      else
+        *reinterpret_cast<__nv_bfloat162*>(&o.e[i]) = __floats2bfloat162_rn(x.v[i], x.v[i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(x.v[i]);
+  }
+  return o;
+}
+
 // sigmoid(g) and sigmoid(-g) from one exponential: with e = exp(-g), a = 1 /
-// (1 + e) and 1 - a = e a keeps every digit where the gate saturates.  e stops
-// at 2^126 (gates below -87 then leave 2^-126 of the state); NaN goes through.
-// A gate of +infinity gives exactly (1, 0): positions that are not there.
+// (1 + e) and 1 - a = e a keeps every digit where the gate saturates.  Gates
+// stop at -87 (they would leave less than 2^-125 of the state), so e is
+// finite; NaN goes through.  A gate of +infinity gives exactly (1, 0):
+// positions that are not there.
 __device__ __forceinline__ void gates(float g, float& a, float& na) {
   float e;
-  asm("min.NaN.f32 %0, %1, 0f42FC0000;" : "=f"(e) : "f"(g * -1.44269504f));
-  asm("ex2.approx.f32 %0, %0;" : "+f"(e));
+  asm("max.NaN.f32 %0, %1, 0fC2AE0000;" : "=f"(e) : "f"(g));
+  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(e * -1.44269504f));
   asm("rcp.approx.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
   na = e * a;
+}
+template <class T, int V>
+__device__ __forceinline__ void gates(const Vec<T, V>& g, Lanes<V>& a, Lanes<V>& na) {
+  Lanes<V> x;
+  if constexpr (sizeof(T) == 2 && V > 1) {
+    Vec<T, V> c;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      if constexpr (std::is_same_v<T, __half>)
+        *reinterpret_cast<__half2*>(&c.e[i]) =
+            __hmax2_nan(*reinterpret_cast<const __half2*>(&g.e[i]), __float2half2_rn(-87.f));
+      else
+        *reinterpret_cast<__nv_bfloat162*>(&c.e[i]) =
+            __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&g.e[i]), __float2bfloat162_rn(-87.f));
+    }
+    x = widen(c);
+  } else {
+    x = widen(g);
+#pragma unroll
+    for (int i = 0; i < V; ++i) asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(x.v[i]));
+  }
+  Lanes<V> e = mul(x, all_of<V>(-1.44269504f));
+#pragma unroll
+  for (int i = 0; i < V; ++i) asm("ex2.approx.f32 %0, %0;" : "+f"(e.v[i]));
+  a = add(e, all_of<V>(1.f));
+#pragma unroll
+  for (int i = 0; i < V; ++i) asm("rcp.approx.f32 %0, %0;" : "+f"(a.v[i]));
+  na = mul(e, a);
 }
 
 // `wide`: every column vector of the view can be moved in one access.  The
@@ -54,7 +159,7 @@ struct View {
   T* p;
   int64_t bs, ts;
   bool wide;
-  __device__ T* at(int64_t b, int64_t t, int64_t d) const { return p + b * bs + t * ts + d; }
+  __device__ T* at(int64_t b, int64_t t, int64_t d) const { return p + (b * bs + t * ts + d); }
 };
 
 template <int V, class T>
@@ -76,6 +181,28 @@ __device__ __forceinline__ void put(T* p, bool wide, const Vec<T, V>& r) {
   }
 }
 
+// Writes one thread's R column vectors; positions past n are 0, past `len` not
+// there.
+template <bool WIDE, int V, int R, class T>
+__device__ __forceinline__ void put_stretch(const View<T>& w, T* p, const Vec<T, V> (&o)[R], int t0, int n, int len) {
+  if (t0 + R <= n) {
+#pragma unroll
+    for (int r = 0; r < R; ++r, p += w.ts) put<V>(p, WIDE || w.wide, o[r]);
+  } else {
+    Vec<T, V> z;
+#pragma unroll
+    for (int v = 0; v < V; ++v) z.e[v] = from_f32<T>(0.f);
+    for (int r = 0; r < R; ++r, p += w.ts)
+      if (t0 + r < len) {
+        Vec<T, V> x = z;
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+          if (i == r && t0 + r < n) x = o[i];
+        put<V>(p, WIDE || w.wide, x);
+      }
+  }
+}
+
 // A call's shape.  A tile is TT = (256 / cx) * R positions of cx column vectors
 // of V channels; a column vector is V neighbouring channels of one batch entry.
 struct ScanArgs {
@@ -84,7 +211,7 @@ struct ScanArgs {
   int32_t tiles;         // along time
   uint32_t total;        // tiles in all (chained calls)
   int64_t vecs;          // column vectors in all: batch * dim / V
-  DivMagic per;          // by dim / V: a column vector's batch entry
+  DivMagic32 per;        // by dim / V: a column vector's batch entry
   DivMagic32 groups;     // by the tiles across (chained calls)
   const int32_t* offsets;
   uint32_t* status;
@@ -241,11 +368,11 @@ template <int V>
 __device__ __forceinline__ Channel channel_of(const ScanArgs& s, int64_t vec, int v) {
   Channel c;
   c.ok = vec < s.vecs;
-  if (!c.ok) vec = 0;
-  c.b = (int)div_magic((uint64_t)vec, s.per);
-  c.d = (int)(vec - (int64_t)c.b * (int64_t)s.per.d) * V + v;
+  const uint32_t i = c.ok ? (uint32_t)vec : 0u;
+  c.b = (int)div_magic32(i, s.per);
+  c.d = (int)(i - (uint32_t)c.b * s.per.d) * V + v;
   c.n = c.ok ? live_len(s, c.b) : 0;
-  c.col = vec * V + v;
+  c.col = (int64_t)i * V + v;
   return c;
 }
 
@@ -255,42 +382,44 @@ __device__ __forceinline__ Channel channel_of(const ScanArgs& s, int64_t vec, in
 // when they are due (`now`).  Positions at or past n hold `dead`.
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-template <class T, int V, int R>
+template <class T, int V, int R, bool WIDE>
 struct Staged {
   static constexpr int kBytes = V * (int)sizeof(T);
+  static constexpr bool kAlways = WIDE && kBytes >= 4;
   Vec<T, V>* at;   // + r * kScanThreads
-  __device__ bool async(const View<const T>& w) const { return kBytes >= 4 && w.wide; }
+  __device__ bool async(const View<const T>& w) const { return kAlways || (kBytes >= 4 && w.wide); }
+  __device__ static void copy(Vec<T, V>* to, const T* p) {
+    const unsigned d = (unsigned)__cvta_generic_to_shared(to);
+    if constexpr (kBytes == 16)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
+    else if constexpr (kBytes >= 4)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(p), "n"(kBytes) : "memory");
+  }
   __device__ void fill(const View<const T>& w, const T* p, int t0, int first, int n, float dead, bool now) const {
-    if (async(w) == now) return;
+    if (kAlways ? now : async(w) == now) return;
     Vec<T, V> z;
 #pragma unroll
     for (int v = 0; v < V; ++v) z.e[v] = from_f32<T>(dead);
-    if constexpr (kBytes >= 4) {
-      if (!now) {
+    if (kAlways || !now) {
+      if (t0 >= first && t0 + R <= n) {
 #pragma unroll
+        for (int r = 0; r < R; ++r, p += w.ts) copy(at + r * kScanThreads, p);
+      } else {
         for (int r = 0; r < R; ++r, p += w.ts) {
-          Vec<T, V>* to = at + r * kScanThreads;
-          if (t0 + r >= first && t0 + r < n) {
-            const unsigned d = (unsigned)__cvta_generic_to_shared(to);
-            if constexpr (kBytes == 16)
-              asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(d), "l"(p) : "memory");
-            else
-              asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(p), "n"(kBytes) : "memory");
-          } else {
-            *to = z;
-          }
+          if (t0 + r >= first && t0 + r < n) copy(at + r * kScanThreads, p);
+          else at[r * kScanThreads] = z;
         }
-        return;
       }
-    }
-    Vec<T, V> got[R];
+    } else if constexpr (!kAlways) {
+      Vec<T, V> got[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r, p += w.ts) {
-      got[r] = z;
-      if (t0 + r >= first && t0 + r < n) got[r] = get<V>(p, w.wide);
-    }
+      for (int r = 0; r < R; ++r, p += w.ts) {
+        got[r] = z;
+        if (t0 + r >= first && t0 + r < n) got[r] = get<V>(p, WIDE || w.wide);
+      }
 #pragma unroll
-    for (int r = 0; r < R; ++r) at[r * kScanThreads] = got[r];
+      for (int r = 0; r < R; ++r) at[r * kScanThreads] = got[r];
+    }
   }
 };
 
@@ -304,7 +433,7 @@ struct Staged {
 // CHAIN: a CTA takes tiles by ticket and finds the state before its tile in the
 // records of the tiles ahead; otherwise it walks along time with the state in
 // hand.  cx = 256: a thread is a whole stretch of its own, nothing is joined.
-template <class T, int V, int R, bool CHAIN>
+template <class T, int V, int R, bool CHAIN, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs s, View<const T> x, View<const T> g,
                                                                        View<T> y, const float* __restrict__ state_in,
                                                                        float* __restrict__ state_out) {
@@ -312,7 +441,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
   __shared__ uint32_t slot;
   const Place<V, R> p(s);
   const bool whole = s.cx_log == 8;
-  const Staged<T, V, R> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads};
+  const Staged<T, V, R, WIDE> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads};
   float* sa = (float*)(raw + 2 * R * kScanThreads * sizeof(Vec<T, V>));
   float* sb = sa + (kScanThreads >> s.cx_log) * p.pitch;
   const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
@@ -332,27 +461,21 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
   };
   if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;          // walking: the channel's state
-  float own[V];              // whole: the thread's states
+  Lanes<V> own;              // whole: the thread's states
   while (CHAIN ? tile < s.total : k < s.tiles) {
     const int t0 = k * p.TT + p.ty * R;
     fill(c, k, true);
     copies_done();
     uint32_t ticket = 0;
     if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
-    float a[R][V], b[R][V], fa[V], fb[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f;
+    Lanes<V> a[R], b[R], fa = all_of<V>(1.f), fb = all_of<V>(0.f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const Vec<T, V> xr = sx.at[r * kScanThreads], gr = sg.at[r * kScanThreads];
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float na;
-        gates(to_f32(gr.e[v]), a[r][v], na);
-        b[r][v] = na * to_f32(xr.e[v]);
-        fa[v] *= a[r][v];
-        fb[v] = fmaf(a[r][v], fb[v], b[r][v]);
-      }
+      Lanes<V> na;
+      gates(sg.at[r * kScanThreads], a[r], na);
+      b[r] = mul(na, widen(sx.at[r * kScanThreads]));
+      fa = mul(fa, a[r]);
+      fb = mad(a[r], fb, b[r]);
     }
     // the staged inputs are in registers: copy the next tile's.  Its ticket was
     // drawn when this tile's inputs had come, not before: a CTA that drew two
@@ -372,21 +495,21 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       }
       fill(c1, k1, false);
     };
-    float h[V];
+    Lanes<V> h;
     if (whole) {
       ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (k == 0) own[v] = state_in && c.ok ? state_in[c.col + v] : 0.f;
-        h[v] = own[v];
-        own[v] = fmaf(fa[v], own[v], fb[v]);
-        if (state_out && c.ok && k == s.tiles - 1) state_out[c.col + v] = own[v];
+        if (k == 0) own.v[v] = state_in && c.ok ? state_in[c.col + v] : 0.f;
+        h.v[v] = own.v[v];
+        own.v[v] = fmaf(fa.v[v], own.v[v], fb.v[v]);
+        if (state_out && c.ok && k == s.tiles - 1) state_out[c.col + v] = own.v[v];
       }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        sa[p.ty * p.pitch + p.cx * V + v] = fa[v];
-        sb[p.ty * p.pitch + p.cx * V + v] = fb[v];
+        sa[p.ty * p.pitch + p.cx * V + v] = fa.v[v];
+        sb[p.ty * p.pitch + p.cx * V + v] = fb.v[v];
       }
       if (CHAIN && threadIdx.x == 0) slot = ticket;
       __syncthreads();
@@ -412,20 +535,15 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       if (state_out && live && p.j == 0 && end >= q.n) state_out[q.col] = held;
       __syncthreads();
 #pragma unroll
-      for (int v = 0; v < V; ++v) h[v] = sb[p.ty * p.pitch + p.cx * V + v];
+      for (int v = 0; v < V; ++v) h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
     }
-    T* to = y.at(c.b, t0, c.d);
+    Vec<T, V> o[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r, to += y.ts) {
-      const int t = t0 + r;
-      Vec<T, V> o;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        h[v] = fmaf(a[r][v], h[v], b[r][v]);
-        o.e[v] = from_f32<T>(t < c.n ? h[v] : 0.f);
-      }
-      if (c.ok && t < s.len) put<V>(to, y.wide, o);
+    for (int r = 0; r < R; ++r) {
+      h = mad(a[r], h, b[r]);
+      o[r] = narrow<T>(h);
     }
+    put_stretch<WIDE, V, R>(y, y.at(c.b, t0, c.d), o, t0, c.n, c.ok ? s.len : 0);
     c = c1, k = k1, gi = gi1;
     tile = next;
   }
@@ -439,7 +557,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
 // gates.  16 bits: y is read at every position (RERUN false) -- a rerun would
 // carry the rounding of the one row it starts from into states that are
 // smaller than that row, where y itself is off by half a unit of its own.
-template <class T, int V, int R, bool CHAIN>
+template <class T, int V, int R, bool CHAIN, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
                                                                        View<const T> y, View<const T> gy,
                                                                        const float* __restrict__ state_in,
@@ -451,7 +569,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
   const Place<V, R> p(s);
   const bool whole = s.cx_log == 8;
   const int area = (kScanThreads >> s.cx_log) * p.pitch;
-  const Staged<T, V, R> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads},
+  const Staged<T, V, R, WIDE> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads},
       sd{sg.at + R * kScanThreads}, sy{sd.at + R * kScanThreads};
   float* sa = (float*)(raw + (RERUN ? 3 : 4) * R * kScanThreads * sizeof(Vec<T, V>));
   float *sb = sa + area, *sc = sb + area;
@@ -474,40 +592,34 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
   };
   if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;
-  float own[V];
+  Lanes<V> own;
   while (CHAIN ? tile < s.total : k >= 0) {
     const int t0 = k * p.TT + p.ty * R;
     fill(c, k, true);
     copies_done();
     uint32_t ticket = 0;
     if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
-    float a[R][V], na[R][V], xv[R][V], dy[R][V];   // xv: x, then the gate's factor of G
-    float fa[V], fb[V], fc[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) fa[v] = 1.f, fb[v] = 0.f, fc[v] = 0.f;
+    Lanes<V> a[R], na[R], xv[R], dy[R];   // xv: x, then the gate's factor of G
+    Lanes<V> fa = all_of<V>(1.f), fb = all_of<V>(0.f), fc = all_of<V>(0.f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      const Vec<T, V> xr = sx.at[r * kScanThreads], gr = sg.at[r * kScanThreads], dr = sd.at[r * kScanThreads];
-      Vec<T, V> yr;
-      if (!RERUN) yr = sy.at[r * kScanThreads];
+      gates(sg.at[r * kScanThreads], a[r], na[r]);
+      xv[r] = widen(sx.at[r * kScanThreads]);
+      dy[r] = widen(sd.at[r * kScanThreads]);
+      fa = mul(fa, a[r]);
+      if constexpr (RERUN) {
+        fb = mad(a[r], fb, mul(na[r], xv[r]));
+      } else {
+        Lanes<V> before = widen(sy.at[r * kScanThreads]);
+        if (r == 0 && t0 == 0 && state_in && c.ok) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        gates(to_f32(gr.e[v]), a[r][v], na[r][v]);
-        xv[r][v] = to_f32(xr.e[v]);
-        dy[r][v] = to_f32(dr.e[v]);
-        if (!RERUN) {
-          float before = to_f32(yr.e[v]);
-          if (r == 0 && t0 == 0) before = state_in && c.ok ? state_in[c.col + v] : 0.f;
-          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);
+          for (int v = 0; v < V; ++v) before.v[v] = state_in[c.col + v];
         }
-        fa[v] *= a[r][v];
-        if (RERUN) fb[v] = fmaf(a[r][v], fb[v], na[r][v] * xv[r][v]);
+        xv[r] = mul(mul(a[r], na[r]), sub(before, xv[r]));
       }
     }
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r)
-#pragma unroll
-      for (int v = 0; v < V; ++v) fc[v] = a[r][v] * (dy[r][v] + fc[v]);
+    for (int r = R - 1; r >= 0; --r) fc = mul(a[r], add(dy[r], fc));
     // the next tile's inputs (as in the forward)
     int k1 = k - 1;
     int64_t gi1 = gi;
@@ -525,26 +637,26 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       }
       fill(c1, k1, false);
     };
-    float h[V], C[V];
+    Lanes<V> h, C;
     if (whole) {
       ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (k == s.tiles - 1) own[v] = grad_out && c.ok ? grad_out[c.col + v] : 0.f;
-        C[v] = own[v];
-        own[v] = fmaf(fa[v], own[v], fc[v]);
-        if (grad_in && c.ok && k == 0) grad_in[c.col + v] = own[v];
-        h[v] = 0.f;
+        if (k == s.tiles - 1) own.v[v] = grad_out && c.ok ? grad_out[c.col + v] : 0.f;
+        C.v[v] = own.v[v];
+        own.v[v] = fmaf(fa.v[v], own.v[v], fc.v[v]);
+        if (grad_in && c.ok && k == 0) grad_in[c.col + v] = own.v[v];
+        h.v[v] = 0.f;
         if (!RERUN) continue;
-        if (c.ok && t0 == 0) h[v] = state_in ? state_in[c.col + v] : 0.f;
-        else if (t0 < c.n) h[v] = to_f32(*y.at(c.b, t0 - 1, c.d + v));
+        if (c.ok && t0 == 0) h.v[v] = state_in ? state_in[c.col + v] : 0.f;
+        else if (t0 < c.n) h.v[v] = to_f32(*y.at(c.b, t0 - 1, c.d + v));
       }
     } else {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        sa[p.ty * p.pitch + p.cx * V + v] = fa[v];
-        if (RERUN) sb[p.ty * p.pitch + p.cx * V + v] = fb[v];
-        sc[p.ty * p.pitch + p.cx * V + v] = fc[v];
+        sa[p.ty * p.pitch + p.cx * V + v] = fa.v[v];
+        if (RERUN) sb[p.ty * p.pitch + p.cx * V + v] = fb.v[v];
+        sc[p.ty * p.pitch + p.cx * V + v] = fc.v[v];
       }
       const Channel q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
       const int start = k * p.TT;
@@ -587,38 +699,28 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       __syncthreads();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (RERUN) h[v] = sb[p.ty * p.pitch + p.cx * V + v];
-        C[v] = sc[p.ty * p.pitch + p.cx * V + v];
+        if (RERUN) h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
+        C.v[v] = sc[p.ty * p.pitch + p.cx * V + v];
       }
     }
     if (RERUN) {
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float before = h[v];
-          h[v] = fmaf(a[r][v], before, na[r][v] * xv[r][v]);
-          xv[r][v] = a[r][v] * na[r][v] * (before - xv[r][v]);
-        }
-    }
-    T *tx = gx.at(c.b, (int64_t)t0 + R - 1, c.d), *tg = gg.at(c.b, (int64_t)t0 + R - 1, c.d);
-#pragma unroll
-    for (int r = R - 1; r >= 0; --r, tx -= gx.ts, tg -= gg.ts) {
-      const int t = t0 + r;
-      Vec<T, V> ox, og;
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const float G = dy[r][v] + C[v];
-        const bool on = t < c.n;
-        ox.e[v] = from_f32<T>(on ? na[r][v] * G : 0.f);
-        og.e[v] = from_f32<T>(on ? xv[r][v] * G : 0.f);
-        C[v] = a[r][v] * G;
-      }
-      if (c.ok && t < s.len) {
-        put<V>(tx, gx.wide, ox);
-        put<V>(tg, gg.wide, og);
+      for (int r = 0; r < R; ++r) {
+        const Lanes<V> before = h;
+        h = mad(a[r], h, mul(na[r], xv[r]));
+        xv[r] = mul(mul(a[r], na[r]), sub(before, xv[r]));
       }
     }
+    Vec<T, V> ox[R], og[R];
+#pragma unroll
+    for (int r = R - 1; r >= 0; --r) {
+      const Lanes<V> G = add(dy[r], C);
+      ox[r] = narrow<T>(mul(na[r], G));
+      og[r] = narrow<T>(mul(xv[r], G));
+      C = mul(a[r], G);
+    }
+    put_stretch<WIDE, V, R>(gx, gx.at(c.b, t0, c.d), ox, t0, c.n, c.ok ? s.len : 0);
+    put_stretch<WIDE, V, R>(gg, gg.at(c.b, t0, c.d), og, t0, c.n, c.ok ? s.len : 0);
     c = c1, k = k1, gi = gi1;
     tile = next;
   }
@@ -679,11 +781,12 @@ struct Cut {
 };
 
 constexpr int kWideV = 4, kFwdR = 8, kBwdR = 4;   // V = 1: twice the positions, for as many bytes in flight
-constexpr int kChainCx = 3, kWalkCx = 5;          // log2 of the column vectors of a tile
+// log2 of the column vectors of a tile, for V = 4 and V = 1
+constexpr int kCx = 3, kCxOne = 5;
 int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R, int sms) {
   const int64_t cols = batch * dim;
   (void)sms;
-  const int TT = (kScanThreads >> (V == 1 ? 5 : kChainCx)) * R;
+  const int TT = (kScanThreads >> (V == 1 ? kCxOne : kCx)) * R;
   const int64_t tiles = (len + TT - 1) / TT;
   return (tiles + tiles / kGroup + 1) * cols;
 }
@@ -701,14 +804,20 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   a.shared = h->shared_d;
   a.records = h->records_d;
   const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
-  c.chain = (a.vecs >> kWalkCx) < slots;
-  a.cx_log = c.chain ? (V == 1 ? 5 : kChainCx) : kWalkCx;
+  const int least = V == 1 ? kCxOne : kCx;
+  // stretches that a sequence fills, rounded up to a power of two
+  int ty_log = 0;
+  while (ty_log < 8 && (R << ty_log) < len) ++ty_log;
+  a.cx_log = 8 - ty_log < least ? least : 8 - ty_log;
+  // fewer than four stretches, or four that would fill the GPU side by side: a thread walks alone
+  if (V == 4 && (a.cx_log > 6 || (a.cx_log == 6 && (a.vecs >> 8) >= h->sm_count))) a.cx_log = 8;
+  if (a.cx_log == least && R == 8 && ((a.vecs + (2 << least) - 1) >> (least + 1)) >= slots) ++a.cx_log;
+  const int64_t groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
   const int TT = (kScanThreads >> a.cx_log) * R;
   a.tiles = (len + TT - 1) / TT;
   if (a.tiles < 1) a.tiles = 1;
-  const int64_t groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
-  if (a.tiles == 1) c.chain = false;
-  a.per = make_div_magic((uint64_t)(h->dim / V));
+  c.chain = a.tiles > 1 && a.cx_log == least && groups < slots;
+  a.per = make_div_magic32((uint32_t)(h->dim / V));
   if (c.chain) {
     a.groups = make_div_magic32((uint32_t)groups);
     a.total = (uint32_t)(groups * a.tiles);
@@ -737,7 +846,7 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) {
-    const int64_t cols = (int64_t)h->sm_count * kCtasPerSm * (kWideV << kWalkCx) + dim;   // a call with more walks
+    const int64_t cols = (int64_t)h->sm_count * kCtasPerSm * (kWideV << (kCx + 1)) + dim;   // a call with more walks
     const int64_t batch = (int64_t)max_batch * dim < cols ? max_batch : cols / dim + 1;
     for (int V : {1, kWideV})
       for (int R : {kFwdR, kBwdR}) {
@@ -788,33 +897,25 @@ static cudaError_t allow_shared(K kernel) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 << 10);
 }
 
-template <class T, int V, int R>
-static cudaError_t launch_fwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
-                       const int32_t* offsets, const float* state_in, const scan_view* y, float* state_out,
-                       cudaStream_t stream) {
-  const Cut c = cut_call(h, batch, len, offsets, V, R, 2, 2 * R * kScanThreads * V * sizeof(T));
-  auto kernel = c.chain ? k_scan_fwd<T, V, R, true> : k_scan_fwd<T, V, R, false>;
-  static const cudaError_t room[2] = {allow_shared(k_scan_fwd<T, V, R, false>), allow_shared(k_scan_fwd<T, V, R, true>)};
-  if (room[c.chain] != cudaSuccess) return room[c.chain];
-  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y),
-                                                  state_in, state_out);
+// All views wide: the kernels of this variant have no other path.
+template <int V, class... W>
+static bool all_wide(int size, const W*... w) {
+  return ((aligned_to(w->data, V * size) && w->batch_stride % V == 0 && w->time_stride % V == 0) && ...);
+}
+
+template <class K, class... A>
+static cudaError_t launch(K kernel, const Cut& c, cudaStream_t stream, A... a) {
+  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, a...);
   return cudaGetLastError();
 }
 
-template <class T, int V, int R>
-static cudaError_t launch_bwd(const emb_scan_s* h, int32_t batch, int32_t len, const scan_view* x, const scan_view* gate,
-                       const int32_t* offsets, const float* state_in, const scan_view* y, const scan_view* grad_y,
-                       const float* grad_state_out, const scan_view* grad_x, const scan_view* grad_gate,
-                       float* grad_state_in, cudaStream_t stream) {
-  const Cut c = cut_call(h, batch, len, offsets, V, R, 3, (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T));
-  auto kernel = c.chain ? k_scan_bwd<T, V, R, true> : k_scan_bwd<T, V, R, false>;
-  static const cudaError_t room[2] = {allow_shared(k_scan_bwd<T, V, R, false>), allow_shared(k_scan_bwd<T, V, R, true>)};
-  if (room[c.chain] != cudaSuccess) return room[c.chain];
-  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
-                                                  as_view<const T, V>(y), as_view<const T, V>(grad_y), state_in,
-                                                  grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate),
-                                                  grad_state_in);
-  return cudaGetLastError();
+// Calls f with the kernel's variant as constants: V, WIDE.
+template <class T, class F, class... W>
+static cudaError_t with_variant(int32_t dim, F f, const W*... w) {
+  using std::integral_constant;
+  if (dim % kWideV) return f(integral_constant<int, 1>(), std::true_type());
+  if (all_wide<kWideV>(sizeof(T), w...)) return f(integral_constant<int, kWideV>(), std::true_type());
+  return f(integral_constant<int, kWideV>(), std::false_type());
 }
 
 extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
@@ -824,11 +925,19 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
       !view_ok(gate, dtype, batch, len, h->dim, false) || !view_ok(y, dtype, batch, len, h->dim, true))
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
-  const bool vec = h->dim % kWideV == 0;
-  return cuda_status(with_element(dtype, [&](auto* t) {
-    using T = std::remove_pointer_t<decltype(t)>;
-    auto launch = vec ? launch_fwd<T, kWideV, kFwdR> : launch_fwd<T, 1, 2 * kFwdR>;
-    return launch(h, batch, len, x, gate, offsets, state_in, y, state_out, (cudaStream_t)stream);
+  if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
+  return cuda_status(with_element(dtype, [&](auto* e) {
+    using T = std::remove_pointer_t<decltype(e)>;
+    return with_variant<T>(h->dim, [&](auto v, auto wide) {
+      constexpr int V = decltype(v)::value, R = V == 1 ? 2 * kFwdR : kFwdR;
+      constexpr bool W = decltype(wide)::value;
+      static const cudaError_t room[2] = {allow_shared(k_scan_fwd<T, V, R, false, W>),
+                                          allow_shared(k_scan_fwd<T, V, R, true, W>)};
+      const Cut c = cut_call(h, batch, len, offsets, V, R, 2, 2 * R * kScanThreads * V * sizeof(T));
+      if (room[c.chain] != cudaSuccess) return room[c.chain];
+      return launch(c.chain ? k_scan_fwd<T, V, R, true, W> : k_scan_fwd<T, V, R, false, W>, c, (cudaStream_t)stream,
+                    as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
+    }, x, gate, y);
   }));
 }
 
@@ -843,12 +952,22 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
       !view_ok(grad_gate, dtype, batch, len, h->dim, true))
     return EMB_ERR_INVALID_ARG;
   if (batch == 0) return EMB_OK;
-  const bool vec = h->dim % kWideV == 0;
-  return cuda_status(with_element(dtype, [&](auto* t) {
-    using T = std::remove_pointer_t<decltype(t)>;
-    auto launch = vec ? launch_bwd<T, kWideV, kBwdR> : launch_bwd<T, 1, 2 * kBwdR>;
-    return launch(h, batch, len, x, gate, offsets, state_in, y, grad_y, grad_state_out, grad_x, grad_gate,
-                  grad_state_in, (cudaStream_t)stream);
+  if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
+  return cuda_status(with_element(dtype, [&](auto* e) {
+    using T = std::remove_pointer_t<decltype(e)>;
+    return with_variant<T>(h->dim, [&](auto v, auto wide) {
+      constexpr int V = decltype(v)::value, R = V == 1 ? 2 * kBwdR : kBwdR;
+      constexpr bool W = decltype(wide)::value;
+      static const cudaError_t room[2] = {allow_shared(k_scan_bwd<T, V, R, false, W>),
+                                          allow_shared(k_scan_bwd<T, V, R, true, W>)};
+      const Cut c = cut_call(h, batch, len, offsets, V, R, 3,
+                             (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T));
+      if (room[c.chain] != cudaSuccess) return room[c.chain];
+      return launch(c.chain ? k_scan_bwd<T, V, R, true, W> : k_scan_bwd<T, V, R, false, W>, c, (cudaStream_t)stream,
+                    as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y),
+                    as_view<const T, V>(grad_y), state_in, grad_state_out, as_view<T, V>(grad_x),
+                    as_view<T, V>(grad_gate), grad_state_in);
+    }, x, gate, y, grad_y, grad_x, grad_gate);
   }));
 }
 

@@ -14,7 +14,7 @@ import ctypes
 from ctypes import c_float, c_int32, c_int64, c_void_p
 from typing import NamedTuple
 
-from . import TABLE_DTYPE, _check, _stream, lib, ptr
+from . import TABLE_DTYPE, EmbError, _check, lib, ptr
 
 STATES_8BIT = 1
 BLOCK = 256          # elements that share a top in an 8-bit state
@@ -35,6 +35,15 @@ class AdamwTensor(ctypes.Structure):
 # ---------------------------------------------------------------------------
 # raw C names
 # ---------------------------------------------------------------------------
+
+def _stream(stream):
+    """The raw handle of a stream; None: the current stream of the current
+    device (the short way to it: a call may be a few microseconds of work)."""
+    if stream is None:
+        import torch
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
+
 
 def _ref(view):
     return None if view is None else ctypes.byref(view)
