@@ -9,8 +9,12 @@
 namespace emb {
 
 constexpr int kBlock = 256;        // elements that share a top: one warp, eight elements per lane
-constexpr int kAdamThreads = 256;
-constexpr int kChunk = 2048;       // elements of a CTA's pass: one block per warp
+constexpr int kAdamThreads = 128;
+// CTAs on an SM: as many as hold a block's values without spilling.  Measured
+// with 8-bit states (128 M elements): bf16 weights 304 us with 10, 324 with
+// 8; fp32 weights (100 M) 290 with 10, 261 with 8.
+template <class W>
+constexpr int adam_ctas() { return sizeof(W) == 4 ? 8 : 10; }
 
 struct AdamTensor {
   void* param;
@@ -25,50 +29,119 @@ struct AdamTensor {
   int32_t aligned;       // every pointer allows 16-byte accesses of eight elements
 };
 
-struct AdamChunk {
+// A warp's work: one block of one tensor.
+struct AdamUnit {
   int32_t tensor;
-  int32_t chunk;         // first element / kChunk
+  int32_t block;
 };
 
 // A step's scalars, each computed in 64 bits and rounded once.
 struct AdamScalars {
-  float lr, b1, nb1, b2, nb2, c1, c2, eps;
+  float lr, lr_c1, b1, nb1, b2, nb2, c2, eps, one;
   uint64_t key;          // SplitMix64 output for seed and step
 };
 
-// The place of each magnitude on the 8-bit grid, and back (emb.h).
+// Places on the 8-bit grid, and back (emb.h).  Codes of eight elements are
+// handled as two words of four bytes.
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return __byte_perm(w, 0, 0x4440 + i); }
+__device__ __forceinline__ uint32_t pack4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+}
+__device__ __forceinline__ uint32_t top4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+template <int LEVELS>
+__device__ __forceinline__ void decode8(uint2 codes, int base, float (&x)[8]) {
+  const uint32_t base20 = (uint32_t)base << 20;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t w = h ? codes.y : codes.x;
+    const uint32_t mags = LEVELS == 127 ? w & 0x7f7f7f7fu : w, signs = w & 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t c = byte_of(mags, i);
+      uint32_t u = c ? (c << 20) + base20 : 0u;
+      if (LEVELS == 127) u |= __byte_perm(signs, 0, 0x0444 | (i << 12));
+      x[4 * h + i] = __uint_as_float(u);
+    }
+  }
+}
+
+// Largest magnitude of three and of eight, NaN if there is one.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float max8(const float (&x)[8]) {
+  return max3(max3(max3(x[0], x[1], x[2]), x[3], x[4]), max3(x[5], x[6], x[7]), 0.f);
+}
 __device__ __forceinline__ uint32_t magnitude(float x) {
   const uint32_t u = __float_as_uint(x) & 0x7fffffffu;
   return u < 0x7f800000u ? u : 0u;
 }
+
+// Rounds a block's eight elements per lane to codes; noise: 16 bits for each,
+// two to a word.  Returns the block's top.  All lanes call.
 template <int LEVELS>
-__device__ __forceinline__ uint32_t encode(float x, uint32_t noise, int base) {
-  const int c = (int)((magnitude(x) + (noise << 4)) >> 20) - base;
-  const uint32_t code = (uint32_t)max(c, 0);
-  return LEVELS == 127 ? code | ((__float_as_uint(x) >> 24) & 0x80u) : code;
-}
-template <int LEVELS>
-__device__ __forceinline__ float decode(uint32_t code, int base) {
-  const uint32_t c = code & LEVELS;
-  const uint32_t mag = c ? (c + (uint32_t)base) << 20 : 0u;
-  return __uint_as_float(LEVELS == 127 ? mag | ((code & 0x80u) << 24) : mag);
+__device__ __forceinline__ int encode8(const float (&x)[8], const uint32_t (&noise)[4], uint2& codes) {
+  uint32_t u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = __float_as_uint(x[i]) & 0x7fffffffu;
+  uint32_t big = __reduce_max_sync(kFull, __float_as_uint(max8(x)));
+  if (big >= 0x7f800000u) {   // some are not finite: they count for nothing and become 0
+    uint32_t most = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = max(most, u[i] = magnitude(x[i]));
+    big = __reduce_max_sync(kFull, most);
+  }
+  const int top = (int)((big + 0xfffffu) >> 20), base = max(top - LEVELS, 0);
+  uint32_t c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t n = __byte_perm(noise[i >> 1], 0, i & 1 ? 0x4432 : 0x4410);
+    // the code ends up in the top byte: shifts as products, which are not bound by the integer pipe
+    c[i] = (uint32_t)__viaddmax_s32((int)(u[i] + 16u * n), -(base << 20), 0) * 16u;
+  }
+  codes = make_uint2(top4(c[0], c[1], c[2], c[3]), top4(c[4], c[5], c[6], c[7]));
+  if (LEVELS == 127) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float* f = x + 4 * h;
+      (h ? codes.y : codes.x) |= top4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                                      __float_as_uint(f[3])) & 0x80808080u;
+    }
+  }
+  return top;
 }
 
+// Eight consecutive elements, as they are stored.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, float (&r)[8], int n, bool vec) {
+struct Eight {
+  T e[8];
+};
+template <class T>
+__device__ __forceinline__ void load8(const T* p, Eight<T>& r, int n, bool vec) {
+  constexpr int V = 16 / sizeof(T);
   if (vec) {
-    if constexpr (sizeof(T) == 4) {
-      const auto a = load_vec<T, 4>(p), b = load_vec<T, 4>(p + 4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) r[i] = to_f32(a.e[i]), r[4 + i] = to_f32(b.e[i]);
-    } else {
-      const auto a = load_vec<T, 8>(p);
+    for (int i = 0; i < 8; i += V) {
+      const auto x = load_vec<T, V>(p + i);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) r[i] = to_f32(a.e[i]);
+      for (int k = 0; k < V; ++k) r.e[i + k] = x.e[k];
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) r[i] = i < n ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < 8; ++i) r.e[i] = i < n ? p[i] : from_f32<T>(0.f);
+  }
+}
+template <class T>
+__device__ __forceinline__ void widen8(const Eight<T>& r, float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 f = widen2(&r.e[i]);
+    x[i] = f.x, x[i + 1] = f.y;
   }
 }
 
@@ -84,7 +157,7 @@ __device__ __forceinline__ void store8(T* p, const float (&r)[8], int n, bool ve
     } else {
       Vec<T, 8> a;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) a.e[i] = from_f32<T>(r[i]);
+      for (int i = 0; i < 8; i += 2) narrow2(&a.e[i], make_float2(r[i], r[i + 1]));
       store_vec(p, a);
     }
   } else {
@@ -94,131 +167,152 @@ __device__ __forceinline__ void store8(T* p, const float (&r)[8], int n, bool ve
   }
 }
 
-__device__ __forceinline__ uint64_t load_codes(const uint8_t* p, int n, bool vec) {
-  if (vec) return *reinterpret_cast<const uint64_t*>(p);
-  uint64_t c = 0;
+__device__ __forceinline__ uint2 load_codes(const uint8_t* p, int n, bool vec) {
+  if (vec) return *reinterpret_cast<const uint2*>(p);
+  uint32_t c[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) c |= (uint64_t)p[i] << (8 * i);
-  return c;
+  for (int i = 0; i < 8; ++i) c[i] = i < n ? p[i] : 0u;
+  return make_uint2(pack4(c[0], c[1], c[2], c[3]), pack4(c[4], c[5], c[6], c[7]));
 }
 
-__device__ __forceinline__ void store_codes(uint8_t* p, uint64_t c, int n, bool vec) {
+__device__ __forceinline__ void store_codes(uint8_t* p, uint2 c, int n, bool vec) {
   if (vec) {
-    *reinterpret_cast<uint64_t*>(p) = c;
+    *reinterpret_cast<uint2*>(p) = c;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) p[i] = (uint8_t)(c >> (8 * i));
+      if (i < n) p[i] = (uint8_t)byte_of(i < 4 ? c.x : c.y, i & 3);
   }
 }
 
-// Writes a block's eight elements per lane as codes and its top.
-template <int LEVELS>
-__device__ __forceinline__ void store_state(uint8_t* codes, int16_t* top_p, const float (&x)[8], uint64_t z0,
-                                            uint64_t z1, int n, bool vec) {
-  uint32_t big = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) big = max(big, i < n ? magnitude(x[i]) : 0u);
-  big = __reduce_max_sync(kFull, big);
-  const int top = (int)((big + 0xfffffu) >> 20), base = max(top - LEVELS, 0);
-  uint64_t c = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t noise = (uint32_t)((i < 4 ? z0 : z1) >> (16 * (i & 3))) & 0xffffu;
-    c |= (uint64_t)encode<LEVELS>(x[i], noise, base) << (8 * i);
-  }
-  if (n > 0) store_codes(codes, c, n, vec);
-  if ((threadIdx.x & 31) == 0) *top_p = (int16_t)top;
-}
-
-template <class P, class G, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads) k_adamw(const AdamTensor* __restrict__ tensors,
-                                                        const void* const* __restrict__ grads,
-                                                        const AdamChunk* __restrict__ chunks, AdamScalars s,
-                                                        const float* __restrict__ grad_scale) {
-  const AdamChunk ch = chunks[blockIdx.x];
-  const AdamTensor t = tensors[ch.tensor];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t block0 = (int64_t)ch.chunk * kChunk + warp * kBlock;
-  if (block0 >= t.numel) return;
-  const int64_t i0 = block0 + lane * 8;
+__device__ __forceinline__ int lane_elements(const AdamTensor& t, int64_t i0) {
   const int64_t left = t.numel - i0;
-  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
-  const bool vec = t.aligned && n == 8;
-  const G* gp = (const G*)grads[ch.tensor];
-  const bool gvec = vec && ((uintptr_t)gp & 15) == 0;
-  float g[8], w[8], m[8], v[8];
-  load8(gp + i0, g, n, gvec);
-  if constexpr (MASTER) load8(t.master + i0, w, n, vec);
-  else load8((const P*)t.param + i0, w, n, vec);
+  return left >= 8 ? 8 : left > 0 ? (int)left : 0;
+}
+
+// One block of one tensor, eight consecutive elements per lane, n of them the
+// tensor's.  VEC: all of the block's are, and every access is wide.
+template <class P, class G, bool MASTER, bool EIGHT, bool VEC>
+__device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int64_t block, const AdamScalars& s,
+                                           const float* grad_scale) {
+  const int64_t i0 = block * kBlock + (threadIdx.x & 31) * 8;
+  const int n = VEC ? 8 : lane_elements(t, i0);
+  Eight<G> gr;
+  Eight<std::conditional_t<MASTER, float, P>> wr;
+  Eight<float> mr, vr;
+  uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
+  int mt, vt;
+  load8(gp + i0, gr, n, VEC);
+  if constexpr (MASTER) load8(t.master + i0, wr, n, VEC);
+  else load8((const P*)t.param + i0, wr, n, VEC);
   if constexpr (EIGHT) {
-    const uint64_t mc = n ? load_codes((const uint8_t*)t.m + i0, n, vec) : 0;
-    const uint64_t vc = n ? load_codes((const uint8_t*)t.v + i0, n, vec) : 0;
-    const int mb = max((int)t.m_top[block0 / kBlock] - 127, 0), vb = max((int)t.v_top[block0 / kBlock] - 255, 0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      m[i] = decode<127>((uint32_t)(mc >> (8 * i)) & 255u, mb);
-      v[i] = decode<255>((uint32_t)(vc >> (8 * i)) & 255u, vb);
-    }
-    __syncwarp();   // every lane has the old tops
+    if (n) mc = load_codes((const uint8_t*)t.m + i0, n, VEC), vc = load_codes((const uint8_t*)t.v + i0, n, VEC);
+    mt = t.m_top[block], vt = t.v_top[block];
   } else {
-    load8((const float*)t.m + i0, m, n, vec);
-    load8((const float*)t.v + i0, v, n, vec);
+    load8((const float*)t.m + i0, mr, n, VEC);
+    load8((const float*)t.v + i0, vr, n, VEC);
   }
-  const float scale = grad_scale ? *grad_scale : 1.f;
+  const float scale = grad_scale ? *grad_scale : 1.f, keep = 1.f - s.lr * t.decay;
+  float g[8], w[8], m[8], v[8];
+  if constexpr (EIGHT) {
+    decode8<127>(mc, max(mt - 127, 0), m);
+    decode8<255>(vc, max(vt - 255, 0), v);
+  } else {
+    widen8(mr, m);
+    widen8(vr, v);
+  }
+  widen8(gr, g);
+  widen8(wr, w);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float gi = __fmul_rn(g[i], scale);
-    // each operation rounded by itself: the codes are then a function of the
-    // formulas alone, whatever the compiler would have contracted
-    m[i] = __fadd_rn(__fmul_rn(m[i], s.b1), __fmul_rn(gi, s.nb1));
-    v[i] = __fadd_rn(__fmul_rn(v[i], s.b2), __fmul_rn(__fmul_rn(gi, gi), s.nb2));
-    float r;
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(v[i] * s.c2));
-    const float u = __fdividef(m[i] * s.c1, r + s.eps);
-    w[i] = w[i] - s.lr * t.decay * w[i] - s.lr * u;
+  for (int i = 0; i < 8; i += 2) {
+    const auto both = [](float x) { return make_float2(x, x); };
+    float2 gi = make_float2(g[i], g[i + 1]), mi = make_float2(m[i], m[i + 1]), vi = make_float2(v[i], v[i + 1]);
+    gi = __fmul2_rn(gi, both(scale));
+    // Each operation rounded by itself, so that the codes are a function of the
+    // formulas alone.  A packed product and sum would be joined to one
+    // multiply-add by the compiler; a sum as a multiply-add by a 1 that it does
+    // not know stays a sum.
+    mi = __ffma2_rn(__fmul2_rn(mi, both(s.b1)), both(s.one), __fmul2_rn(gi, both(s.nb1)));
+    vi = __ffma2_rn(__fmul2_rn(vi, both(s.b2)), both(s.one), __fmul2_rn(__fmul2_rn(gi, gi), both(s.nb2)));
+    m[i] = mi.x, m[i + 1] = mi.y, v[i] = vi.x, v[i + 1] = vi.y;
+    float2 r = __fmul2_rn(vi, both(s.c2));
+    asm("sqrt.approx.f32 %0, %0;" : "+f"(r.x));
+    asm("sqrt.approx.f32 %0, %0;" : "+f"(r.y));
+    r = __fadd2_rn(r, both(s.eps));
+    const float2 q = make_float2(__fdividef(mi.x, r.x), __fdividef(mi.y, r.y));
+    const float2 wi = __ffma2_rn(q, both(-s.lr_c1), __fmul2_rn(make_float2(w[i], w[i + 1]), both(keep)));
+    w[i] = wi.x, w[i + 1] = wi.y;
   }
-  if constexpr (MASTER) store8(t.master + i0, w, n, vec);
-  store8((P*)t.param + i0, w, n, vec);
+  if constexpr (MASTER) store8(t.master + i0, w, n, VEC);
+  store8((P*)t.param + i0, w, n, VEC);
   if constexpr (EIGHT) {
     const uint64_t group = (uint64_t)(t.start + i0) / 4;
     const uint64_t z0 = splitmix64(s.key + group), z1 = splitmix64(s.key + group + 1);
-    store_state<127>((uint8_t*)t.m + i0, t.m_top + block0 / kBlock, m, z0, z1, n, vec);
-    store_state<255>((uint8_t*)t.v + i0, t.v_top + block0 / kBlock, v, z0, z1, n, vec);
+    const uint32_t noise[4] = {(uint32_t)z0, (uint32_t)(z0 >> 32), (uint32_t)z1, (uint32_t)(z1 >> 32)};
+    mt = encode8<127>(m, noise, mc);
+    if (n) store_codes((uint8_t*)t.m + i0, mc, n, VEC);
+    vt = encode8<255>(v, noise, vc);
+    if (n) store_codes((uint8_t*)t.v + i0, vc, n, VEC);
+    if ((threadIdx.x & 31) == 0) t.m_top[block] = (int16_t)mt, t.v_top[block] = (int16_t)vt;
   } else {
-    store8((float*)t.m + i0, m, n, vec);
-    store8((float*)t.v + i0, v, n, vec);
+    store8((float*)t.m + i0, m, n, VEC);
+    store8((float*)t.v + i0, v, n, VEC);
   }
 }
 
+// The blocks at tensors' ends and off the 16-byte boundaries, out of line: they
+// would cost the others registers.
+template <class P, class G, bool MASTER, bool EIGHT>
+__device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64_t block, const AdamScalars* s,
+                                         const float* grad_scale) {
+  adam_block<P, G, MASTER, EIGHT, false>(*t, gp, block, *s, grad_scale);
+}
+
+// All bytes are read once and written once; a warp takes one block, and the
+// other warps of the SM hide its loads.  With 16-bit weights and 8-bit states
+// (10 bytes an element) the kernel is bound by instruction issue and the
+// latency in front of it: arithmetic goes in pairs, codes in words of four.
+// Warps that walked several blocks with the next one's loads ahead held fewer
+// blocks in flight for the registers that took, and were slower.
+template <class P, class G, bool MASTER, bool EIGHT>
+__global__ void __launch_bounds__(kAdamThreads, adam_ctas<P>()) k_adamw(const AdamTensor* __restrict__ tensors,
+                                                                   const void* const* __restrict__ grads,
+                                                                   const AdamUnit* __restrict__ units, int64_t n_units,
+                                                                   const __grid_constant__ AdamScalars s,
+                                                                   const float* __restrict__ grad_scale) {
+  const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
+  if (i >= n_units) return;
+  const AdamUnit u = units[i];
+  const AdamTensor& t = tensors[u.tensor];
+  const G* gp = (const G*)grads[u.tensor];
+  if (t.aligned && ((uintptr_t)gp & 15) == 0 && ((int64_t)u.block + 1) * kBlock <= t.numel)
+    adam_block<P, G, MASTER, EIGHT, true>(t, gp, u.block, s, grad_scale);
+  else
+    adam_ragged<P, G, MASTER, EIGHT>(&t, gp, u.block, &s, grad_scale);
+}
+
 __global__ void __launch_bounds__(kAdamThreads) k_adamw_export(const AdamTensor* __restrict__ tensors,
-                                                               const AdamChunk* __restrict__ chunks,
+                                                               const AdamUnit* __restrict__ units, int64_t n_units,
                                                                __nv_bfloat16* __restrict__ m_out,
                                                                __nv_bfloat16* __restrict__ v_out) {
-  const AdamChunk ch = chunks[blockIdx.x];
-  const AdamTensor t = tensors[ch.tensor];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t block0 = (int64_t)ch.chunk * kChunk + warp * kBlock;
-  if (block0 >= t.numel) return;
-  const int64_t i0 = block0 + lane * 8, left = t.numel - i0;
-  const int n = left >= 8 ? 8 : left > 0 ? (int)left : 0;
+  const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
+  if (i >= n_units) return;
+  const AdamUnit u = units[i];
+  const AdamTensor t = tensors[u.tensor];
+  const int64_t i0 = (int64_t)u.block * kBlock + (threadIdx.x & 31) * 8;
+  const int n = lane_elements(t, i0);
   const bool vec = t.aligned && n == 8;
-  const uint64_t mc = n ? load_codes((const uint8_t*)t.m + i0, n, vec) : 0;
-  const uint64_t vc = n ? load_codes((const uint8_t*)t.v + i0, n, vec) : 0;
-  const int mb = max((int)t.m_top[block0 / kBlock] - 127, 0), vb = max((int)t.v_top[block0 / kBlock] - 255, 0);
+  uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
+  if (n) mc = load_codes((const uint8_t*)t.m + i0, n, vec), vc = load_codes((const uint8_t*)t.v + i0, n, vec);
   float m[8], v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    m[i] = decode<127>((uint32_t)(mc >> (8 * i)) & 255u, mb);
-    v[i] = decode<255>((uint32_t)(vc >> (8 * i)) & 255u, vb);
-  }
+  decode8<127>(mc, max((int)t.m_top[u.block] - 127, 0), m);
+  decode8<255>(vc, max((int)t.v_top[u.block] - 255, 0), v);
   store8(m_out + t.start + i0, m, 8, true);   // a tensor's room is whole blocks: the rest of the last one is zeros
   store8(v_out + t.start + i0, v, 8, true);
 }
 
 // A kind of tensors: element types and master decide the kernel.
-using AdamKernel = void (*)(const AdamTensor*, const void* const*, const AdamChunk*, AdamScalars, const float*);
+using AdamKernel = void (*)(const AdamTensor*, const void* const*, const AdamUnit*, int64_t, AdamScalars, const float*);
 
 template <class P, class G, bool MASTER>
 AdamKernel adam_states(bool eight) {
@@ -237,7 +331,7 @@ AdamKernel adam_kernel(int32_t dtype, int32_t grad_dtype, bool master, bool eigh
 
 struct AdamKind {
   AdamKernel kernel;
-  int64_t first, count;   // its chunks
+  int64_t first, count;   // its units
 };
 
 }  // namespace emb
@@ -246,13 +340,13 @@ struct emb_adamw_s {
   int32_t n = 0;
   bool eight = false;
   int64_t elements = 0;                 // of the padded order
-  int64_t n_chunks = 0;
+  int64_t n_units = 0;
   std::vector<emb::AdamKind> kinds;
   std::vector<int32_t> grad_size;       // alignment of each tensor's gradient
   std::vector<int64_t> numel;
   emb::AdamTensor* tensors_d = nullptr;
   const void** grads_d = nullptr;
-  emb::AdamChunk* chunks_d = nullptr;
+  emb::AdamUnit* units_d = nullptr;
 };
 
 using namespace emb;
@@ -262,9 +356,12 @@ namespace {
 void free_adamw(emb_adamw_s* h) {
   dev_free(h->tensors_d);
   dev_free((void*)h->grads_d);
-  dev_free(h->chunks_d);
+  dev_free(h->units_d);
   delete h;
 }
+
+// One warp per unit.
+unsigned unit_grid(int64_t units) { return (unsigned)((units + kAdamThreads / 32 - 1) / (kAdamThreads / 32)); }
 
 bool tensor_ok(const adamw_tensor& t, bool eight) {
   if (t.numel < 0 || t.reserved != 0 || !(t.weight_decay >= 0.f) || std::isinf(t.weight_decay)) return false;
@@ -307,24 +404,24 @@ emb_status create_adamw(const adamw_tensor* tensors, int32_t n, bool eight, emb_
     }
     of_kind[k].push_back(i);
   }
-  std::vector<AdamChunk> chunks;
+  std::vector<AdamUnit> units;
   for (size_t k = 0; k < of_kind.size(); ++k) {
-    h->kinds[k].first = (int64_t)chunks.size();
+    h->kinds[k].first = (int64_t)units.size();
     for (int32_t i : of_kind[k]) {
-      const int64_t c = (meta[i].numel + kChunk - 1) / kChunk;
-      if ((int64_t)chunks.size() + c >= (int64_t(1) << 31)) return EMB_ERR_UNSUPPORTED;
-      for (int64_t j = 0; j < c; ++j) chunks.push_back(AdamChunk{i, (int32_t)j});
+      const int64_t blocks = (meta[i].numel + kBlock - 1) / kBlock;
+      if ((int64_t)units.size() + blocks >= (int64_t(1) << 31)) return EMB_ERR_UNSUPPORTED;
+      for (int64_t j = 0; j < blocks; ++j) units.push_back(AdamUnit{i, (int32_t)j});
     }
-    h->kinds[k].count = (int64_t)chunks.size() - h->kinds[k].first;
+    h->kinds[k].count = (int64_t)units.size() - h->kinds[k].first;
   }
-  h->n_chunks = (int64_t)chunks.size();
+  h->n_units = (int64_t)units.size();
   EMB_CUDA_TRY(dev_alloc((void**)&h->tensors_d, sizeof(AdamTensor) * n));
   EMB_CUDA_TRY(dev_alloc((void**)&h->grads_d, sizeof(void*) * n));
-  EMB_CUDA_TRY(dev_alloc((void**)&h->chunks_d, sizeof(AdamChunk) * (chunks.empty() ? 1 : chunks.size())));
+  EMB_CUDA_TRY(dev_alloc((void**)&h->units_d, sizeof(AdamUnit) * (units.empty() ? 1 : units.size())));
   EMB_CUDA_TRY(cudaMemcpy(h->tensors_d, meta.data(), sizeof(AdamTensor) * n, cudaMemcpyHostToDevice));
   EMB_CUDA_TRY(cudaMemcpy((void*)h->grads_d, grads.data(), sizeof(void*) * n, cudaMemcpyHostToDevice));
-  if (!chunks.empty())
-    EMB_CUDA_TRY(cudaMemcpy(h->chunks_d, chunks.data(), sizeof(AdamChunk) * chunks.size(), cudaMemcpyHostToDevice));
+  if (!units.empty())
+    EMB_CUDA_TRY(cudaMemcpy(h->units_d, units.data(), sizeof(AdamUnit) * units.size(), cudaMemcpyHostToDevice));
   return EMB_OK;
 }
 
@@ -381,13 +478,14 @@ extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double be
   s.nb1 = (float)(1.0 - beta1);
   s.b2 = (float)beta2;
   s.nb2 = (float)(1.0 - beta2);
-  s.c1 = (float)(1.0 / (1.0 - std::pow(beta1, (double)step)));
+  s.lr_c1 = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
   s.c2 = (float)(1.0 / (1.0 - std::pow(beta2, (double)step)));
   s.eps = (float)eps;
+  s.one = 1.f;
   s.key = splitmix64(((uint64_t)seed << 32) + (uint64_t)step);
   for (const AdamKind& k : h->kinds) {
-    k.kernel<<<(unsigned)k.count, kAdamThreads, 0, (cudaStream_t)stream>>>(h->tensors_d, h->grads_d,
-                                                                          h->chunks_d + k.first, s, grad_scale);
+    k.kernel<<<unit_grid(k.count), kAdamThreads, 0, (cudaStream_t)stream>>>(
+        h->tensors_d, h->grads_d, h->units_d + k.first, k.count, s, grad_scale);
     EMB_CUDA_TRY(cudaGetLastError());
   }
   return EMB_OK;
@@ -402,9 +500,9 @@ extern "C" emb_status adamw_export_size(emb_adamw h, int64_t* elements) {
 extern "C" emb_status adamw_export_states(emb_adamw h, void* m_out, void* v_out, void* stream) {
   if (!h) return EMB_ERR_INVALID_ARG;
   if (!h->eight) return EMB_ERR_UNSUPPORTED;
-  if (h->n_chunks == 0) return EMB_OK;
+  if (h->n_units == 0) return EMB_OK;
   if (!m_out || !v_out || !aligned16(m_out) || !aligned16(v_out)) return EMB_ERR_INVALID_ARG;
-  k_adamw_export<<<(unsigned)h->n_chunks, kAdamThreads, 0, (cudaStream_t)stream>>>(
-      h->tensors_d, h->chunks_d, (__nv_bfloat16*)m_out, (__nv_bfloat16*)v_out);
+  k_adamw_export<<<unit_grid(h->n_units), kAdamThreads, 0, (cudaStream_t)stream>>>(
+      h->tensors_d, h->units_d, h->n_units, (__nv_bfloat16*)m_out, (__nv_bfloat16*)v_out);
   return cuda_status(cudaGetLastError());
 }

@@ -27,6 +27,26 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { retu
 template <>
 __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
+// Two neighbouring elements as fp32, and back, in one or two instructions.
+__device__ __forceinline__ float2 widen2(const float* p) { return make_float2(p[0], p[1]); }
+__device__ __forceinline__ float2 widen2(const __half* p) {
+  return __half22float2(__half2{p[0], p[1]});
+}
+__device__ __forceinline__ float2 widen2(const __nv_bfloat16* p) {
+  const __nv_bfloat162 h{p[0], p[1]};
+  const uint32_t u = *reinterpret_cast<const uint32_t*>(&h);
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+__device__ __forceinline__ void narrow2(float* p, float2 x) { p[0] = x.x, p[1] = x.y; }
+__device__ __forceinline__ void narrow2(__half* p, float2 x) {
+  const __half2 h = __floats2half2_rn(x.x, x.y);
+  p[0] = h.x, p[1] = h.y;
+}
+__device__ __forceinline__ void narrow2(__nv_bfloat16* p, float2 x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(x.x, x.y);
+  p[0] = h.x, p[1] = h.y;
+}
+
 // V consecutive elements, moved in one access (V * sizeof(T) = 2, 4, 8 or 16).
 template <class T, int V>
 struct alignas(V * sizeof(T)) Vec {

@@ -14,7 +14,7 @@ import ctypes
 from ctypes import c_float, c_int32, c_int64, c_void_p
 from typing import NamedTuple
 
-from . import TABLE_DTYPE, EmbError, _check, lib, ptr
+from . import TABLE_DTYPE, _check, lib, ptr
 
 STATES_8BIT = 1
 BLOCK = 256          # elements that share a top in an 8-bit state
@@ -157,31 +157,25 @@ def _element(dtype):
 
 
 def _want(t, name, shape, dtype, dense=True):
-    """Checks one tensor argument: on the GPU, of this shape and type, dense
-    (or only its last axis contiguous)."""
-    if not t.is_cuda or t.shape != shape or t.dtype != dtype:
+    """Checks one tensor argument -- on the GPU, of this shape and type, dense
+    (or only its last axis contiguous) -- and returns its pointer."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
         raise ValueError("%s: %s %s on the GPU expected, got %s %s on %s" % (
             name, tuple(shape), dtype, tuple(t.shape), t.dtype, t.device))
-    if dense:
-        if not t.is_contiguous():
+    if not t.is_contiguous():
+        if dense:
             raise ValueError("%s: a contiguous tensor expected, got strides %s" % (name, t.stride()))
-    elif t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
-        raise ValueError("%s: a contiguous last axis expected, got strides %s" % (name, t.stride()))
-    return t
-
-
-def _empty(shape, dtype, device, stream):
-    """A tensor that belongs to the stream the kernel will run on."""
-    import torch
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
-    with torch.cuda.stream(s):
-        return torch.empty(shape, dtype=dtype, device=device)
+        if t.stride(-1) != 1 and t.shape[-1] > 1 and t.numel():
+            raise ValueError("%s: a contiguous last axis expected, got strides %s" % (name, t.stride()))
+    return t.data_ptr()
 
 
 class _Handle:
     handle = None
+
+    def __init__(self):
+        import torch
+        self._t = torch
 
     def close(self):
         if self.handle:
@@ -193,6 +187,15 @@ class _Handle:
             self.close()
         except Exception:
             pass
+
+    def _empty(self, shape, dtype, device, stream):
+        """A tensor that belongs to the stream the kernel will run on."""
+        torch = self._t
+        if stream is None:
+            return torch.empty(shape, dtype=dtype, device=device)
+        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+        with torch.cuda.stream(s):
+            return torch.empty(shape, dtype=dtype, device=device)
 
 
 class GatedScan(_Handle):
@@ -210,41 +213,45 @@ class GatedScan(_Handle):
     _destroy = staticmethod(scan_destroy)
 
     def __init__(self, dim, max_batch, max_len):
+        super().__init__()
         self.dim = dim
         self.handle = scan_create(dim, max_batch, max_len)
+        self._fwd, self._bwd = lib().scan_forward, lib().scan_backward
+        # the views of a call, rewritten by each call and read before it returns
+        self._views = (c_int64 * 21)()
+        at = ctypes.addressof(self._views)
+        self._view_at = [at + 24 * i for i in range(7)]
 
-    def _view(self, t, name, shape, dtype):
-        _want(t, name, shape, dtype, dense=False)
+    def _view(self, i, t, name, shape, dtype):
+        p = _want(t, name, shape, dtype, False)
         sb, st, _ = t.stride()
-        return ScanView(t.data_ptr(), sb, st)
+        self._views[3 * i:3 * i + 3] = (p, sb, st)
 
     def _common(self, x, gate, offsets, state):
-        import torch
         if x.dim() != 3 or x.shape[2] != self.dim:
             raise ValueError("x: [batch, time, %d] expected, got %s" % (self.dim, tuple(x.shape)))
-        code, shape = _element(x.dtype), x.shape
-        vx = self._view(x, "x", shape, x.dtype)
-        vg = self._view(gate, "gate", shape, x.dtype)
-        if offsets is not None:
-            _want(offsets, "offsets", (shape[0] + 1,), torch.int32)
-        if state is not None:
-            _want(state, "state", (shape[0], self.dim), torch.float32)
-        return code, shape, vx, vg
+        dt, shape = x.dtype, x.shape
+        code = _element(dt)
+        self._view(0, x, "x", shape, dt)
+        self._view(1, gate, "gate", shape, dt)
+        o = None if offsets is None else _want(offsets, "offsets", (shape[0] + 1,), self._t.int32)
+        s = None if state is None else _want(state, "state", (shape[0], self.dim), self._t.float32)
+        return code, dt, shape, x.device, o, s
 
     def forward(self, x, gate, offsets=None, state=None, y=None, last=None, stream=None):
         """(y, last): h_t at every position, and the state [batch, dim]
         float32 after the last live one.  state: the one before the first
         (None = 0).  y and last may be given."""
-        import torch
-        code, shape, vx, vg = self._common(x, gate, offsets, state)
+        code, dt, shape, dev, o, s = self._common(x, gate, offsets, state)
+        f32, ends = self._t.float32, (shape[0], self.dim)
         if y is None:
-            y = _empty(shape, x.dtype, x.device, stream)
+            y = self._empty(shape, dt, dev, stream)
         if last is None:
-            last = _empty((shape[0], self.dim), torch.float32, x.device, stream)
-        else:
-            _want(last, "last", (shape[0], self.dim), torch.float32)
-        scan_forward(self.handle, shape[0], shape[1], code, vx, vg, offsets, state,
-                     self._view(y, "y", shape, x.dtype), last, stream)
+            last = self._empty(ends, f32, dev, stream)
+        self._view(2, y, "y", shape, dt)
+        v = self._view_at
+        _check(self._fwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], _want(last, "last", ends, f32),
+                         _stream(stream)), "scan_forward")
         return y, last
 
     def backward(self, x, gate, y, grad_y, offsets=None, state=None, grad_last=None, grad_x=None, grad_gate=None,
@@ -252,21 +259,23 @@ class GatedScan(_Handle):
         """(grad_x, grad_gate, grad_state) from the gradients of y and (None =
         0) of last; x, gate, offsets and state as in forward, y as it gave
         it.  The results may be given."""
-        import torch
-        code, shape, vx, vg = self._common(x, gate, offsets, state)
-        dt = x.dtype
-        for t, name in ((grad_last, "grad_last"), (grad_state, "grad_state")):
-            if t is not None:
-                _want(t, name, (shape[0], self.dim), torch.float32)
+        code, dt, shape, dev, o, s = self._common(x, gate, offsets, state)
+        f32, ends = self._t.float32, (shape[0], self.dim)
+        gl = None if grad_last is None else _want(grad_last, "grad_last", ends, f32)
         if grad_x is None:
-            grad_x = _empty(shape, dt, x.device, stream)
+            grad_x = self._empty(shape, dt, dev, stream)
         if grad_gate is None:
-            grad_gate = _empty(shape, dt, x.device, stream)
+            grad_gate = self._empty(shape, dt, dev, stream)
         if grad_state is None:
-            grad_state = _empty((shape[0], self.dim), torch.float32, x.device, stream)
-        scan_backward(self.handle, shape[0], shape[1], code, vx, vg, offsets, state, self._view(y, "y", shape, dt),
-                      self._view(grad_y, "grad_y", shape, dt), grad_last, self._view(grad_x, "grad_x", shape, dt),
-                      self._view(grad_gate, "grad_gate", shape, dt), grad_state, stream)
+            grad_state = self._empty(ends, f32, dev, stream)
+        gs = _want(grad_state, "grad_state", ends, f32)
+        self._view(2, y, "y", shape, dt)
+        self._view(3, grad_y, "grad_y", shape, dt)
+        self._view(4, grad_x, "grad_x", shape, dt)
+        self._view(5, grad_gate, "grad_gate", shape, dt)
+        v = self._view_at
+        _check(self._bwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], v[3], gl, v[4], v[5], gs,
+                         _stream(stream)), "scan_backward")
         return grad_x, grad_gate, grad_state
 
     def step(self, x, gate, rows, states, y=None, stream=None):
@@ -274,21 +283,17 @@ class GatedScan(_Handle):
         int64, the session's row of states [num_rows, dim] float32 (outside:
         dropped, y = 0).  Updates states in place, returns y [n, dim].  Rows
         of one call must be distinct."""
-        import torch
         if x.dim() != 2 or x.shape[1] != self.dim or states.dim() != 2:
             raise ValueError("x: [n, %d] and states [num_rows, %d] expected" % (self.dim, self.dim))
         shape, dt = x.shape, x.dtype
-        code = _element(dt)
-        _want(x, "x", shape, dt, dense=False)
-        _want(gate, "gate", shape, dt, dense=False)
-        _want(rows, "rows", shape[:1], torch.int64)
-        _want(states, "states", (states.shape[0], self.dim), torch.float32)
+        n, pool = shape[0], states.shape[0]
         if y is None:
-            y = _empty(shape, dt, x.device, stream)
-        else:
-            _want(y, "y", shape, dt, dense=False)
-        scan_step(shape[0], self.dim, code, x, x.stride(0), gate, gate.stride(0), rows, states, states.shape[0], y,
-                  y.stride(0), stream)
+            y = self._empty(shape, dt, x.device, stream)
+        _check(lib().scan_step(n, self.dim, _element(dt), _want(x, "x", shape, dt, False), x.stride(0),
+                               _want(gate, "gate", shape, dt, False), gate.stride(0),
+                               _want(rows, "rows", (n,), self._t.int64),
+                               _want(states, "states", (pool, self.dim), self._t.float32), pool,
+                               _want(y, "y", shape, dt, False), y.stride(0), _stream(stream)), "scan_step")
         return y
 
     def device_status(self, stream=None):
@@ -311,6 +316,7 @@ class ExpertRouter(_Handle):
     _destroy = staticmethod(moe_destroy)
 
     def __init__(self, n_experts, top_k, max_tokens, align=1):
+        super().__init__()
         self.n_experts, self.top_k, self.align = n_experts, top_k, align
         self.handle = moe_create(n_experts, top_k, max_tokens, align)
 
@@ -322,83 +328,69 @@ class ExpertRouter(_Handle):
     def route(self, experts, stream=None):
         """Routing of experts [tokens, top_k] int32 (a choice outside [0,
         n_experts) is dropped)."""
-        import torch
         if experts.dim() != 2:
             raise ValueError("experts: [tokens, %d] expected, got %s" % (self.top_k, tuple(experts.shape)))
-        n, dev = experts.shape[0], experts.device
-        _want(experts, "experts", (n, self.top_k), torch.int32)
-        E, K, R = self.n_experts, self.top_k, self.rows(n)
-        # one allocation, each part at a multiple of 32 bytes
-        at, end = [], 0
-        for k in (E + 1, E, n * K, R):
-            at.append((end, k))
-            end += (k + 7) // 8 * 8
-        whole = _empty((end,), torch.int32, dev, stream)
-        offsets, counts, pos, src = [whole[a:a + k] for a, k in at]
-        moe_route(self.handle, n, experts, offsets, counts, pos, src, stream)
+        i32 = self._t.int32
+        n, E, K = experts.shape[0], self.n_experts, self.top_k
+        e = _want(experts, "experts", (n, K), i32)
+        R = self.rows(n)
+        whole = self._empty((n * K + R + 2 * E + 1,), i32, experts.device, stream)
+        p = whole.data_ptr()
+        src = p + 4 * n * K
+        off = src + 4 * R
+        _check(lib().moe_route(self.handle, n, e, off, off + 4 * (E + 1), p, src, _stream(stream)), "moe_route")
+        pos, src, offsets, counts = whole.split_with_sizes((n * K, R, E + 1, E))
         return Routing(offsets, counts, pos.view(n, K), src)
 
     def _routed(self, n, r):
-        import torch
-        _want(r.pos, "pos", (n, self.top_k), torch.int32)
-        _want(r.src, "src", (self.rows(n),), torch.int32)
-
-    def _tokens(self, x, name):
-        if x.dim() != 2:
-            raise ValueError("%s: [tokens, dim] expected, got %s" % (name, tuple(x.shape)))
-        _want(x, name, x.shape, x.dtype, dense=False)
-        return x.shape[0], x.shape[1], _element(x.dtype)
+        i32 = self._t.int32
+        return _want(r.pos, "pos", (n, self.top_k), i32), _want(r.src, "src", (self.rows(n),), i32)
 
     def dispatch(self, x, routing, xs=None, stream=None):
         """xs [rows, dim]: the token of each row; padding rows are 0."""
-        n, dim, code = self._tokens(x, "x")
-        self._routed(n, routing)
+        if x.dim() != 2:
+            raise ValueError("x: [tokens, dim] expected, got %s" % (tuple(x.shape),))
+        (n, dim), dt = x.shape, x.dtype
+        pos, src = self._routed(n, routing)
+        shape = (self.rows(n), dim)
         if xs is None:
-            xs = _empty((self.rows(n), dim), x.dtype, x.device, stream)
-        else:
-            _want(xs, "xs", (self.rows(n), dim), x.dtype)
-        moe_dispatch(self.handle, n, dim, code, x, x.stride(0), routing.pos, routing.src, xs, stream)
+            xs = self._empty(shape, dt, x.device, stream)
+        _check(lib().moe_dispatch(self.handle, n, dim, _element(dt), _want(x, "x", x.shape, dt, False), x.stride(0),
+                                  pos, src, _want(xs, "xs", shape, dt), _stream(stream)), "moe_dispatch")
         return xs
 
     def combine(self, ys, weights, routing, y=None, stream=None):
         """y [tokens, dim]: the sum of each token's rows of ys, each times its
         weight ([tokens, top_k] float32; None = 1)."""
-        import torch
-        n, dt = routing.pos.shape[0], ys.dtype
-        self._routed(n, routing)
         if ys.dim() != 2:
             raise ValueError("ys: [rows, dim] expected, got %s" % (tuple(ys.shape),))
-        dim, code = ys.shape[1], _element(dt)
-        _want(ys, "ys", (self.rows(n), dim), dt)
-        if weights is not None:
-            _want(weights, "weights", (n, self.top_k), torch.float32)
+        n, dim, dt = routing.pos.shape[0], ys.shape[1], ys.dtype
+        pos, _ = self._routed(n, routing)
+        w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._t.float32)
         if y is None:
-            y = _empty((n, dim), dt, ys.device, stream)
-        else:
-            _want(y, "y", (n, dim), dt, dense=False)
-        moe_combine(self.handle, n, dim, code, ys, weights, routing.pos, y, y.stride(0), stream)
+            y = self._empty((n, dim), dt, ys.device, stream)
+        _check(lib().moe_combine(self.handle, n, dim, _element(dt), _want(ys, "ys", (self.rows(n), dim), dt), w, pos,
+                                 _want(y, "y", (n, dim), dt, False), y.stride(0), _stream(stream)), "moe_combine")
         return y
 
     def combine_backward(self, grad_y, ys, weights, routing, grad_ys=None, grad_weights=None, stream=None):
         """(grad_ys, grad_weights) of combine; weights None gives grad_weights
         None."""
-        import torch
-        n, dim, code = self._tokens(grad_y, "grad_y")
-        self._routed(n, routing)
-        dt, R = grad_y.dtype, self.rows(n)
-        _want(ys, "ys", (R, dim), dt)
-        if weights is not None:
-            _want(weights, "weights", (n, self.top_k), torch.float32)
-            if grad_weights is None:
-                grad_weights = _empty((n, self.top_k), torch.float32, grad_y.device, stream)
-        if grad_weights is not None:
-            _want(grad_weights, "grad_weights", (n, self.top_k), torch.float32)
+        if grad_y.dim() != 2:
+            raise ValueError("grad_y: [tokens, dim] expected, got %s" % (tuple(grad_y.shape),))
+        (n, dim), dt, f32 = grad_y.shape, grad_y.dtype, self._t.float32
+        pos, src = self._routed(n, routing)
+        shape, each, dev = (self.rows(n), dim), (n, self.top_k), grad_y.device
+        w = None if weights is None else _want(weights, "weights", each, f32)
+        if weights is not None and grad_weights is None:
+            grad_weights = self._empty(each, f32, dev, stream)
+        gw = None if grad_weights is None else _want(grad_weights, "grad_weights", each, f32)
         if grad_ys is None:
-            grad_ys = _empty((R, dim), dt, grad_y.device, stream)
-        else:
-            _want(grad_ys, "grad_ys", (R, dim), dt)
-        moe_combine_backward(self.handle, n, dim, code, grad_y, grad_y.stride(0), ys, weights, routing.pos,
-                             routing.src, grad_ys, grad_weights, stream)
+            grad_ys = self._empty(shape, dt, dev, stream)
+        _check(lib().moe_combine_backward(self.handle, n, dim, _element(dt), _want(grad_y, "grad_y", (n, dim), dt, False),
+                                          grad_y.stride(0), _want(ys, "ys", shape, dt), w, pos, src,
+                                          _want(grad_ys, "grad_ys", shape, dt), gw, _stream(stream)),
+               "moe_combine_backward")
         return grad_ys, grad_weights
 
     def dispatch_backward(self, grad_xs, routing, grad_x=None, stream=None):
@@ -420,7 +412,8 @@ class AdamW(_Handle):
 
     def __init__(self, params, grads, masters=None, weight_decay=0.01, betas=(0.9, 0.999), eps=1e-8, state_bits=32,
                  m=None, v=None, m_top=None, v_top=None, seed=0, step=0):
-        import torch
+        super().__init__()
+        torch = self._t
         self.params, self.betas, self.eps, self.seed, self.step_count = list(params), betas, eps, seed, step
         self.grads = list(grads)
         self.masters = list(masters) if masters is not None else [None] * len(self.params)
@@ -453,7 +446,8 @@ class AdamW(_Handle):
         for i, p in enumerate(self.params):
             code = _element(p.dtype)
             _want(p, "params", p.shape, p.dtype)
-            g = self._grad(i, self.grads[i])
+            g = self.grads[i]
+            self._grad(i, g)
             if self.masters[i] is not None:
                 _want(self.masters[i], "masters", p.shape, torch.float32)
             eight = state_bits == 8
@@ -464,9 +458,8 @@ class AdamW(_Handle):
         self.handle = adamw_create(descs, STATES_8BIT if state_bits == 8 else 0)
 
     def _grad(self, i, g):
-        import torch
         p = self.params[i]
-        return _want(g, "grads", p.shape, p.dtype if g.dtype == p.dtype else torch.float32)
+        return _want(g, "grads", p.shape, p.dtype if g.dtype == p.dtype else self._t.float32)
 
     def bind_grads(self, grads, stream=None):
         """Read other gradient tensors (same shapes and types) from the next
@@ -482,9 +475,8 @@ class AdamW(_Handle):
     def step(self, lr, grad_scale=None, stream=None):
         """One step on every parameter.  grad_scale: a float32 scalar tensor
         on the GPU that every gradient is multiplied by."""
-        import torch
         if grad_scale is not None:
-            if grad_scale.numel() != 1 or not grad_scale.is_cuda or grad_scale.dtype != torch.float32:
+            if grad_scale.numel() != 1 or not grad_scale.is_cuda or grad_scale.dtype != self._t.float32:
                 raise ValueError("grad_scale: one float32 on the GPU")
         adamw_step(self.handle, self.step_count + 1, lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.seed,
                    stream)
@@ -494,11 +486,10 @@ class AdamW(_Handle):
         """What the 8-bit states stand for: (m, v), bfloat16 (exact), tensor
         after tensor, each from the next multiple of 256 elements on, zeros
         between them."""
-        import torch
         n = adamw_export_size(self.handle)
-        dev = self.params[0].device
-        m = _empty((n,), torch.bfloat16, dev, stream)
-        v = _empty((n,), torch.bfloat16, dev, stream)
+        dev, bf16 = self.params[0].device, self._t.bfloat16
+        m = self._empty((n,), bf16, dev, stream)
+        v = self._empty((n,), bf16, dev, stream)
         adamw_export_states(self.handle, m, v, stream)
         return m, v
 
