@@ -8,9 +8,12 @@ namespace emb {
 
 constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
-constexpr int kRouteMinSpan = 4096;   // choices a CTA takes at least
+constexpr int kRouteOne = 8192;       // choices that one CTA places alone
+constexpr int kRouteMinSpan = 2048;   // choices of a CTA at least, where there are more
 constexpr int kMaxExperts = 2048;
-constexpr int kRowThreads = 256;
+constexpr int kRowThreads = 128;
+constexpr int kBwdCtas = 8;           // its CTAs on an SM: at 64 registers a lane none spill
+constexpr int kInFlight = 4;          // accesses of a lane that the combine's backward keeps in flight
 
 struct RouteArgs {
   const int32_t* experts;
@@ -37,8 +40,8 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_count(RouteArgs a) {
     if (e >= 0) atomicAdd(&hist[e], 1u);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads)
-    a.part[(int64_t)blockIdx.x * a.n_experts + e] = hist[e];
+  pdl_trigger();
+  for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) a.part[blockIdx.x * a.n_experts + e] = hist[e];
 }
 
 // Exclusive sum over the CTA of one value per thread; every thread calls.
@@ -59,37 +62,57 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t x, uint32_t* wsum) {
 }
 
 // Places a CTA's span.  Shared: cnt [warps][experts] -- next row of each
-// expert for each warp's part of the span.
+// expert for each warp's part of the span; of the experts' choices, those
+// ahead of the span and all.  One CTA (ONE) counts for itself, without
+// k_route_count.
+template <bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
   extern __shared__ uint32_t cnt[];
   __shared__ uint32_t wsum[kRouteWarps];
   const int E = a.n_experts, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint32_t* mine = cnt + warp * E;
+  uint32_t *mine = cnt + warp * E, *ahead = cnt + kRouteWarps * E, *all = ahead + E;
+  if constexpr (!ONE) pdl_wait();
   const int64_t lo = blockIdx.x * a.span, hi = min(a.n, lo + a.span);
   const int64_t part = (a.span / kRouteWarps + 31) / 32 * 32;
   const int64_t wlo = min(hi, lo + warp * part), whi = min(hi, wlo + part);
-  for (int i = threadIdx.x; i < kRouteWarps * E; i += kRouteThreads) cnt[i] = 0;
+  for (int i = threadIdx.x; i < (kRouteWarps + 2) * E; i += kRouteThreads) cnt[i] = 0;
   __syncthreads();
   for (int64_t i = wlo + lane; i < whi; i += 32) {
     const int e = expert_at(a, i);
     if (e >= 0) atomicAdd(&mine[e], 1u);
+  }
+  if constexpr (!ONE) {
+    // the spans' counts, a row of E for each CTA
+    int e = threadIdx.x % E;
+    const int step = kRouteThreads % E, rows = gridDim.x * E;
+#pragma unroll 8
+    for (int i = threadIdx.x; i < rows; i += kRouteThreads) {
+      const uint32_t k = a.part[i];
+      if (k) {
+        atomicAdd(&all[e], k);
+        if (i < (int)blockIdx.x * E) atomicAdd(&ahead[e], k);
+      }
+      e += step;
+      if (e >= E) e -= E;
+    }
   }
   __syncthreads();
   // starts of the segments, then of each warp's share of them
   uint32_t carry = 0;
   for (int e0 = 0; e0 < E; e0 += kRouteThreads) {
     const int e = e0 + threadIdx.x;
-    uint32_t before = 0, total = 0;
-    if (e < E)
-      for (unsigned c = 0; c < gridDim.x; ++c) {
-        const uint32_t k = a.part[(int64_t)c * E + e];
-        if (c < blockIdx.x) before += k;
-        total += k;
-      }
+    uint32_t total = 0;
+    if (e < E) {
+      if constexpr (ONE)
+        for (int w = 0; w < kRouteWarps; ++w) total += cnt[w * E + e];
+      else
+        total = all[e];
+    }
     const uint32_t room = (total + a.align - 1) / a.align * a.align;
     const uint32_t start = carry + cta_exclusive(room, wsum);
     if (e < E) {
-      uint32_t row = start + before;
+      uint32_t row = start + ahead[e];
+#pragma unroll
       for (int w = 0; w < kRouteWarps; ++w) {
         const uint32_t k = cnt[w * E + e];
         cnt[w * E + e] = row;
@@ -112,9 +135,10 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
        r += (int64_t)gridDim.x * kRouteThreads)
     a.src[r] = -1;
   const unsigned lt = (1u << lane) - 1u;
+  int e = wlo + lane < whi ? expert_at(a, wlo + lane) : -1;
   for (int64_t i0 = wlo; i0 < whi; i0 += 32) {
     const int64_t i = i0 + lane;
-    const int e = i < whi ? expert_at(a, i) : -1;
+    const int next = i + 32 < whi ? expert_at(a, i + 32) : -1;
     const unsigned peers = __match_any_sync(kFull, e);
     uint32_t row = 0;
     if (e >= 0) row = mine[e] + __popc(peers & lt);
@@ -125,6 +149,7 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
       a.pos[i] = e >= 0 ? (int32_t)row : -1;
       if (e >= 0) a.src[row] = (int32_t)i;
     }
+    e = next;
   }
 }
 
@@ -138,98 +163,185 @@ struct RowArgs {
 // -1 is a dropped choice; no position reaches outside the arrays.
 __device__ __forceinline__ bool live_row(const RowArgs& a, int64_t p) { return p >= 0 && p < a.rows; }
 
+// Rows whose src is -1 become 0.  A warp looks at up to 32 neighbouring rows
+// at once, at fewer where there are not enough to go round: padding comes in
+// stretches, which few warps would otherwise fill.
 template <class T, int V>
-__device__ __forceinline__ void zero_padding(const RowArgs& a, T* xs, int glog) {
-  const int sub = threadIdx.x & ((1 << glog) - 1);
-  const int64_t group = (blockIdx.x * (int64_t)kRowThreads + threadIdx.x) >> glog;
-  const int64_t groups = ((int64_t)gridDim.x * kRowThreads) >> glog;
+__device__ __forceinline__ void zero_padding(const RowArgs& a, T* xs) {
+  const int lane = threadIdx.x & 31;
+  const int64_t warp = (blockIdx.x * (int64_t)kRowThreads + threadIdx.x) >> 5;
+  const int64_t warps = ((int64_t)gridDim.x * kRowThreads) >> 5;
+  int look = 1;
+  while (look < 32 && look * warps < a.rows) look <<= 1;
   Vec<T, V> z;
 #pragma unroll
   for (int i = 0; i < V; ++i) z.e[i] = from_f32<T>(0.f);
-  for (int64_t r = group; r < a.rows; r += groups)
-    if (a.src[r] < 0)
-      for (int j = sub; j < a.vecs; j += 1 << glog) store_vec(xs + (r * a.vecs + j) * V, z);
+  for (int64_t r0 = warp * look; r0 < a.rows; r0 += warps * look) {
+    unsigned empty = __ballot_sync(kFull, lane < look && r0 + lane < a.rows && a.src[r0 + lane] < 0);
+    while (empty) {
+      const int64_t r = r0 + __ffs(empty) - 1;
+      empty &= empty - 1;
+      for (int j = lane; j < a.vecs; j += 32) store_vec(xs + (r * a.vecs + j) * V, z);
+    }
+  }
 }
 
-template <class T, int V>
+// A token's rows, KU of them at a time: -1 where there is none.
+template <int KU>
+__device__ __forceinline__ void load_rows(const RowArgs& a, int64_t t, int k0, int32_t (&p)[KU]) {
+#pragma unroll
+  for (int u = 0; u < KU; ++u) {
+    p[u] = k0 + u < a.top_k ? a.pos[t * a.top_k + k0 + u] : -1;
+    if (!live_row(a, p[u])) p[u] = -1;
+  }
+}
+template <int KU>
+__device__ __forceinline__ void load_weights(const RowArgs& a, const float* w, int64_t t, int k0, float (&x)[KU]) {
+#pragma unroll
+  for (int u = 0; u < KU; ++u) x[u] = w && k0 + u < a.top_k ? w[t * a.top_k + k0 + u] : 1.f;
+}
+
+// Each row of x is read once and written to its top_k places.
+template <class T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads) k_dispatch(RowArgs a, const T* __restrict__ x, int64_t stride,
                                                           T* __restrict__ xs, int glog) {
-  const int sub = threadIdx.x & ((1 << glog) - 1);
+  const int L = 1 << glog, sub = threadIdx.x & (L - 1);
   const int64_t group = (blockIdx.x * (int64_t)kRowThreads + threadIdx.x) >> glog;
   const int64_t groups = ((int64_t)gridDim.x * kRowThreads) >> glog;
   for (int64_t t = group; t < a.n; t += groups)
-    for (int j = sub; j < a.vecs; j += 1 << glog) {
-      const Vec<T, V> r = load_vec<T, V>(x + t * stride + (int64_t)j * V);
-      for (int k = 0; k < a.top_k; ++k) {
-        const int64_t p = a.pos[t * a.top_k + k];
-        if (live_row(a, p)) store_vec(xs + (p * a.vecs + j) * V, r);
+    for (int k0 = 0; k0 < a.top_k; k0 += KU) {
+      int32_t p[KU];
+      load_rows<KU>(a, t, k0, p);
+      const T* from = x + t * stride;
+#pragma unroll 4
+      for (int j = sub; j < a.vecs; j += L) {
+        const Vec<T, V> r = load_vec<T, V>(from + (int64_t)j * V);
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+          if (p[u] >= 0) store_last(xs + ((int64_t)p[u] * a.vecs + j) * V, r);
       }
     }
-  zero_padding<T, V>(a, xs, glog);
+  zero_padding<T, V>(a, xs);
 }
 
-template <class T, int V>
+// Each row of ys is read once; a lane sums its columns of a token's rows in
+// registers, in the order of k, with the rows' loads in flight together.
+template <class T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads) k_combine(RowArgs a, const T* __restrict__ ys,
                                                          const float* __restrict__ w, T* __restrict__ y,
                                                          int64_t stride, int glog) {
-  const int sub = threadIdx.x & ((1 << glog) - 1);
+  const int L = 1 << glog, sub = threadIdx.x & (L - 1);
   const int64_t group = (blockIdx.x * (int64_t)kRowThreads + threadIdx.x) >> glog;
   const int64_t groups = ((int64_t)gridDim.x * kRowThreads) >> glog;
-  for (int64_t t = group; t < a.n; t += groups)
-    for (int j = sub; j < a.vecs; j += 1 << glog) {
-      float acc[V];
+  for (int64_t t = group; t < a.n; t += groups) {
+    int32_t p[KU];
+    float wk[KU];
+    load_rows<KU>(a, t, 0, p);
+    load_weights<KU>(a, w, t, 0, wk);
+    for (int j = sub; j < a.vecs; j += L) {
+      Pairs<V> acc;
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] = 0.f;
-      for (int k = 0; k < a.top_k; ++k) {
-        const int64_t p = a.pos[t * a.top_k + k];
-        if (!live_row(a, p)) continue;
-        const float wk = w ? w[t * a.top_k + k] : 1.f;
-        const Vec<T, V> r = load_vec<T, V>(ys + (p * a.vecs + j) * V);
+      for (int i = 0; i < (V + 1) / 2; ++i) acc.p[i] = make_float2(0.f, 0.f);
+      for (int k0 = 0;;) {
+        Vec<T, V> r[KU];
 #pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += wk * to_f32(r.e[i]);
+        for (int u = 0; u < KU; ++u)
+          if (p[u] >= 0) r[u] = load_vec<T, V>(ys + ((int64_t)p[u] * a.vecs + j) * V);
+#pragma unroll
+        for (int u = 0; u < KU; ++u)
+          if (p[u] >= 0) {
+            const Pairs<V> x = pairs_of(r[u]);
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) acc.p[i] = __ffma2_rn(make_float2(wk[u], wk[u]), x.p[i], acc.p[i]);
+          }
+        if (a.top_k <= KU) break;   // more choices than KU: their rows are looked up for every column
+        k0 = k0 + KU < a.top_k ? k0 + KU : 0;
+        load_rows<KU>(a, t, k0, p);
+        load_weights<KU>(a, w, t, k0, wk);
+        if (k0 == 0) break;
       }
-      Vec<T, V> o;
-#pragma unroll
-      for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(acc[i]);
-      store_vec(y + t * stride + (int64_t)j * V, o);
+      store_vec(y + t * stride + (int64_t)j * V, vec_of<T>(acc));
     }
+  }
 }
 
-template <class T, int V>
-__global__ void __launch_bounds__(kRowThreads) k_combine_bwd(RowArgs a, const T* __restrict__ gy, int64_t stride,
+// Each row of ys is read once, each row of grad_ys written once, grad_y's row
+// once where C accesses of a lane hold it (again from the caches for each k
+// where it is wider).  4 / C choices go together, so that four accesses of a
+// lane are in flight whatever the width; the lanes' partial dot products are
+// joined by shuffles.
+template <class T, int V, int C>
+__global__ void __launch_bounds__(kRowThreads, kBwdCtas) k_combine_bwd(RowArgs a, const T* __restrict__ gy, int64_t stride,
                                                              const T* __restrict__ ys, const float* __restrict__ w,
                                                              T* __restrict__ gys, float* __restrict__ gw, int glog) {
-  const int sub = threadIdx.x & ((1 << glog) - 1);
+  constexpr int KB = kInFlight / C;
+  const int L = 1 << glog, sub = threadIdx.x & (L - 1);
   const int64_t group = (blockIdx.x * (int64_t)kRowThreads + threadIdx.x) >> glog;
   const int64_t groups = ((int64_t)gridDim.x * kRowThreads) >> glog;
+  const int in_warp = (int)(group & ((32 >> glog) - 1));
   // every lane of a warp makes the same number of rounds (the sums shuffle)
-  for (int64_t t0 = group - (group & ((32 >> glog) - 1)); t0 < a.n; t0 += groups) {
-    const int64_t t = t0 + (group & ((32 >> glog) - 1));
-    for (int k = 0; k < a.top_k; ++k) {
-      const int64_t p = t < a.n ? a.pos[t * a.top_k + k] : -1;
-      float dot = 0.f;
-      if (live_row(a, p)) {
-        const float wk = w ? w[t * a.top_k + k] : 1.f;
-        for (int j = sub; j < a.vecs; j += 1 << glog) {
-          const Vec<T, V> g = load_vec<T, V>(gy + t * stride + (int64_t)j * V);
-          if (gw) {
-            const Vec<T, V> r = load_vec<T, V>(ys + (p * a.vecs + j) * V);
+  for (int64_t t0 = group - in_warp; t0 < a.n; t0 += groups) {
+    const int64_t t = t0 + in_warp;
+    const bool ok = t < a.n;
+    const T* from = gy + t * stride;
+    Vec<T, V> g[C];
+    const auto load_g = [&](int j0) {
 #pragma unroll
-            for (int i = 0; i < V; ++i) dot += to_f32(g.e[i]) * to_f32(r.e[i]);
-          }
-          Vec<T, V> o;
+      for (int c = 0; c < C; ++c)
+        if (ok && j0 + c * L < a.vecs) g[c] = load_vec<T, V>(from + (int64_t)(j0 + c * L) * V);
+    };
+    load_g(sub);
+    for (int k0 = 0; k0 < a.top_k; k0 += KB) {
+      int32_t p[KB];
+      float wk[KB], dot[KB];
+      float2 part[KB];   // a dot product, even and odd columns
 #pragma unroll
-          for (int i = 0; i < V; ++i) o.e[i] = from_f32<T>(wk * to_f32(g.e[i]));
-          store_vec(gys + (p * a.vecs + j) * V, o);
+      for (int u = 0; u < KB; ++u) {
+        p[u] = ok && k0 + u < a.top_k ? a.pos[t * a.top_k + k0 + u] : -1;
+        if (!live_row(a, p[u])) p[u] = -1;
+        wk[u] = w && p[u] >= 0 ? w[t * a.top_k + k0 + u] : 1.f;
+        part[u] = make_float2(0.f, 0.f);
+      }
+      for (int j0 = sub; j0 < a.vecs; j0 += C * L) {
+        if (C == 4 && a.vecs > C * L) load_g(j0);
+        Vec<T, V> r[KB][C];
+        if (gw) {
+#pragma unroll
+          for (int u = 0; u < KB; ++u)
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+              if (p[u] >= 0 && j0 + c * L < a.vecs)
+                r[u][c] = load_vec<T, V>(ys + ((int64_t)p[u] * a.vecs + j0 + c * L) * V);
         }
+#pragma unroll
+        for (int u = 0; u < KB; ++u)
+#pragma unroll
+          for (int c = 0; c < C; ++c) {
+            if (p[u] < 0 || j0 + c * L >= a.vecs) continue;
+            const Pairs<V> x = pairs_of(g[c]), y = pairs_of(r[u][c]);
+            Pairs<V> o;
+#pragma unroll
+            for (int i = 0; i < (V + 1) / 2; ++i) {
+              if (gw) part[u] = __ffma2_rn(x.p[i], y.p[i], part[u]);
+              o.p[i] = __fmul2_rn(make_float2(wk[u], wk[u]), x.p[i]);
+            }
+            store_last(gys + ((int64_t)p[u] * a.vecs + j0 + c * L) * V, vec_of<T>(o));
+          }
       }
       if (gw) {
-        for (int o = (1 << glog) >> 1; o; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-        if (sub == 0 && t < a.n) gw[t * a.top_k + k] = dot;
+#pragma unroll
+        for (int u = 0; u < KB; ++u) dot[u] = part[u].x + part[u].y;
+        for (int o = L >> 1; o; o >>= 1) {
+#pragma unroll
+          for (int u = 0; u < KB; ++u) dot[u] += __shfl_xor_sync(kFull, dot[u], o);
+        }
+#pragma unroll
+        for (int u = 0; u < KB; ++u)
+          if (sub == 0 && ok && k0 + u < a.top_k) gw[t * a.top_k + k0 + u] = dot[u];
       }
     }
   }
-  zero_padding<T, V>(a, gys, glog);
+  zero_padding<T, V>(a, gys);
 }
 
 }  // namespace emb
@@ -273,7 +385,7 @@ int lanes_log(int vecs) {
 }
 
 unsigned row_grid(const emb_moe_s* h, int64_t groups, int glog) {
-  const int64_t need = ((groups << glog) + kRowThreads - 1) / kRowThreads, most = (int64_t)h->sm_count * 8;
+  const int64_t need = ((groups << glog) + kRowThreads - 1) / kRowThreads, most = (int64_t)h->sm_count * 64;
   return (unsigned)(need < 1 ? 1 : need < most ? need : most);
 }
 
@@ -313,9 +425,10 @@ extern "C" emb_status moe_create(int32_t n_experts, int32_t top_k, int64_t max_t
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) e = dev_alloc((void**)&h->part, sizeof(uint32_t) * h->sm_count * n_experts);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(k_route_place, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kRouteWarps * kMaxExperts * (int)sizeof(uint32_t));
+  for (auto k : {k_route_place<true>, k_route_place<false>})
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               (kRouteWarps + 2) * kMaxExperts * (int)sizeof(uint32_t));
   if (e != cudaSuccess) {
     dev_free(h->part);
     delete h;
@@ -341,14 +454,20 @@ extern "C" emb_status moe_route(emb_moe h, int64_t n, const int32_t* experts, in
   for (const void* p : {(const void*)experts, (const void*)offsets, (const void*)counts, (const void*)pos, (const void*)src})
     if (!aligned_to(p, 4)) return EMB_ERR_INVALID_ARG;
   RouteArgs a{experts, n * h->top_k, h->n_experts, h->align, rows_of(h, n), 0, h->part, offsets, counts, pos, src};
-  int64_t ctas = (a.n + kRouteMinSpan - 1) / kRouteMinSpan;
-  ctas = ctas < 1 ? 1 : ctas > h->sm_count ? h->sm_count : ctas;
-  a.span = ((a.n + ctas - 1) / ctas + kRouteThreads - 1) / kRouteThreads * kRouteThreads;
   cudaStream_t s = (cudaStream_t)stream;
+  const size_t smem = sizeof(uint32_t) * a.n_experts * (kRouteWarps + 2);
+  const auto round = [](int64_t n) { return (n + kRouteThreads - 1) / kRouteThreads * kRouteThreads; };
+  if (a.n <= kRouteOne) {
+    a.span = round(a.n);
+    k_route_place<true><<<1, kRouteThreads, smem, s>>>(a);
+    return cuda_status(cudaGetLastError());
+  }
+  int64_t ctas = (a.n + kRouteMinSpan - 1) / kRouteMinSpan;
+  if (ctas > h->sm_count) ctas = h->sm_count;
+  a.span = round((a.n + ctas - 1) / ctas);
   k_route_count<<<(unsigned)ctas, kRouteThreads, sizeof(uint32_t) * a.n_experts, s>>>(a);
   EMB_CUDA_TRY(cudaGetLastError());
-  k_route_place<<<(unsigned)ctas, kRouteThreads, sizeof(uint32_t) * a.n_experts * kRouteWarps, s>>>(a);
-  return cuda_status(cudaGetLastError());
+  return cuda_status(launch_dependent(k_route_place<false>, (unsigned)ctas, kRouteThreads, smem, s, a));
 }
 
 extern "C" emb_status moe_dispatch(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const void* x, int64_t x_stride,
@@ -365,8 +484,10 @@ extern "C" emb_status moe_dispatch(emb_moe h, int64_t n, int32_t dim, int32_t dt
   const int glog = lanes_log(a.vecs);
   with_access(dtype, v, [&](auto* t, auto*, auto V) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_dispatch<T, decltype(V)::value><<<row_grid(h, R, glog), kRowThreads, 0, (cudaStream_t)stream>>>(
-        a, (const T*)x, x_stride, (T*)xs, glog);
+    constexpr int W = decltype(V)::value;
+    auto k = h->top_k <= 2 ? k_dispatch<T, W, 2> : h->top_k <= 4 ? k_dispatch<T, W, 4> : k_dispatch<T, W, 8>;
+    k<<<row_grid(h, n > R / 32 ? n : R / 32, glog), kRowThreads, 0, (cudaStream_t)stream>>>(a, (const T*)x, x_stride,
+                                                                                          (T*)xs, glog);
   });
   return cuda_status(cudaGetLastError());
 }
@@ -384,8 +505,9 @@ extern "C" emb_status moe_combine(emb_moe h, int64_t n, int32_t dim, int32_t dty
   const int glog = lanes_log(a.vecs);
   with_access(dtype, v, [&](auto* t, auto*, auto V) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_combine<T, decltype(V)::value><<<row_grid(h, n, glog), kRowThreads, 0, (cudaStream_t)stream>>>(
-        a, (const T*)ys, weights, (T*)y, y_stride, glog);
+    constexpr int W = decltype(V)::value;
+    auto k = h->top_k <= 2 ? k_combine<T, W, 2> : h->top_k <= 4 ? k_combine<T, W, 4> : k_combine<T, W, 8>;
+    k<<<row_grid(h, n, glog), kRowThreads, 0, (cudaStream_t)stream>>>(a, (const T*)ys, weights, (T*)y, y_stride, glog);
   });
   return cuda_status(cudaGetLastError());
 }
@@ -407,7 +529,9 @@ extern "C" emb_status moe_combine_backward(emb_moe h, int64_t n, int32_t dim, in
   const int glog = lanes_log(a.vecs);
   with_access(dtype, v, [&](auto* t, auto*, auto V) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_combine_bwd<T, decltype(V)::value><<<row_grid(h, R, glog), kRowThreads, 0, (cudaStream_t)stream>>>(
+    constexpr int W = decltype(V)::value;
+    auto k = a.vecs <= 32 ? k_combine_bwd<T, W, 1> : a.vecs <= 64 ? k_combine_bwd<T, W, 2> : k_combine_bwd<T, W, 4>;
+    k<<<row_grid(h, n > R / 32 ? n : R / 32, glog), kRowThreads, 0, (cudaStream_t)stream>>>(
         a, (const T*)grad_y, grad_y_stride, (const T*)ys, weights, (T*)grad_ys, grad_weights, glog);
   });
   return cuda_status(cudaGetLastError());

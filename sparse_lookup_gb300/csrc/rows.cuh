@@ -63,6 +63,42 @@ __device__ __forceinline__ void store_vec(T* p, const Vec<T, V>& v) {
   *reinterpret_cast<Vec<T, V>*>(p) = v;
 }
 
+// Stored once and not read again soon: leaves the caches first.
+template <class T, int V>
+__device__ __forceinline__ void store_last(T* p, const Vec<T, V>& v) {
+  if constexpr (sizeof(v) == 16) __stcs(reinterpret_cast<float4*>(p), *reinterpret_cast<const float4*>(&v));
+  else if constexpr (sizeof(v) == 8) __stcs(reinterpret_cast<float2*>(p), *reinterpret_cast<const float2*>(&v));
+  else store_vec(p, v);
+}
+
+// V elements as fp32 pairs; V = 1 leaves the second of its pair 0.
+template <int V>
+struct Pairs {
+  float2 p[(V + 1) / 2];
+};
+template <class T, int V>
+__device__ __forceinline__ Pairs<V> pairs_of(const Vec<T, V>& x) {
+  Pairs<V> o;
+  if constexpr (V == 1) {
+    o.p[0] = make_float2(to_f32(x.e[0]), 0.f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) o.p[i / 2] = widen2(&x.e[i]);
+  }
+  return o;
+}
+template <class T, int V>
+__device__ __forceinline__ Vec<T, V> vec_of(const Pairs<V>& x) {
+  Vec<T, V> o;
+  if constexpr (V == 1) {
+    o.e[0] = from_f32<T>(x.p[0].x);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; i += 2) narrow2(&o.e[i], x.p[i / 2]);
+  }
+  return o;
+}
+
 inline int dtype_size(int32_t dtype) {
   return dtype == EMB_DT_F32 ? 4 : dtype == EMB_DT_BF16 || dtype == EMB_DT_F16 ? 2 : 0;
 }

@@ -334,13 +334,10 @@ class ExpertRouter(_Handle):
         n, E, K = experts.shape[0], self.n_experts, self.top_k
         e = _want(experts, "experts", (n, K), i32)
         R = self.rows(n)
-        whole = self._empty((n * K + R + 2 * E + 1,), i32, experts.device, stream)
-        p = whole.data_ptr()
-        src = p + 4 * n * K
-        off = src + 4 * R
-        _check(lib().moe_route(self.handle, n, e, off, off + 4 * (E + 1), p, src, _stream(stream)), "moe_route")
-        pos, src, offsets, counts = whole.split_with_sizes((n * K, R, E + 1, E))
-        return Routing(offsets, counts, pos.view(n, K), src)
+        offsets, counts, pos, src = [self._empty(k, i32, experts.device, stream) for k in ((E + 1,), (E,), (n, K), (R,))]
+        _check(lib().moe_route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), pos.data_ptr(),
+                               src.data_ptr(), _stream(stream)), "moe_route")
+        return Routing(offsets, counts, pos, src)
 
     def _routed(self, n, r):
         i32 = self._t.int32
