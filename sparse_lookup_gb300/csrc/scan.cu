@@ -113,13 +113,21 @@ __device__ __forceinline__ Vec<T, V> narrow(const Lanes<V>& x) {
 // sigmoid(g) and sigmoid(-g) from one exponential: with e = exp(-g), a = 1 /
 // (1 + e) and 1 - a = e a keeps every digit where the gate saturates.  Gates
 // stop at -87 (they would leave less than 2^-125 of the state), so e is
-// finite; NaN goes through.  A gate of +infinity gives exactly (1, 0):
-// positions that are not there.
+// finite; above 87 e counts as 0; NaN goes through.  A gate of +infinity gives
+// exactly (1, 0): positions that are not there.  The flushing forms of the
+// two approximations are single instructions, the others scale around them.
+__device__ __forceinline__ float exp2_flush(float x) {
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
+__device__ __forceinline__ float inverse_flush(float x) {
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(x));
+  return x;
+}
 __device__ __forceinline__ void gates(float g, float& a, float& na) {
-  float e;
-  asm("max.NaN.f32 %0, %1, 0fC2AE0000;" : "=f"(e) : "f"(g));
-  asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(e * -1.44269504f));
-  asm("rcp.approx.f32 %0, %1;" : "=f"(a) : "f"(1.f + e));
+  asm("max.NaN.f32 %0, %0, 0fC2AE0000;" : "+f"(g));
+  const float e = exp2_flush(g * -1.44269504f);
+  a = inverse_flush(1.f + e);
   na = e * a;
 }
 template <class T, int V>
@@ -144,10 +152,10 @@ __device__ __forceinline__ void gates(const Vec<T, V>& g, Lanes<V>& a, Lanes<V>&
   }
   Lanes<V> e = mul(x, all_of<V>(-1.44269504f));
 #pragma unroll
-  for (int i = 0; i < V; ++i) asm("ex2.approx.f32 %0, %0;" : "+f"(e.v[i]));
+  for (int i = 0; i < V; ++i) e.v[i] = exp2_flush(e.v[i]);
   a = add(e, all_of<V>(1.f));
 #pragma unroll
-  for (int i = 0; i < V; ++i) asm("rcp.approx.f32 %0, %0;" : "+f"(a.v[i]));
+  for (int i = 0; i < V; ++i) a.v[i] = inverse_flush(a.v[i]);
   na = mul(e, a);
 }
 
@@ -160,6 +168,22 @@ struct View {
   int64_t bs, ts;
   bool wide;
   __device__ T* at(int64_t b, int64_t t, int64_t d) const { return p + (b * bs + t * ts + d); }
+};
+
+// Where a thread's stretch starts.  In the WIDE variant all views of a call
+// have the same strides: one offset serves them all.
+template <bool WIDE>
+struct Start {
+  int64_t o = 0;
+  int b = 0, d = 0, t = 0;
+  template <class T>
+  __device__ Start(const View<T>& w, int b, int d, int t) : b(b), d(d), t(t) {
+    if (WIDE) o = b * w.bs + t * w.ts + d;
+  }
+  template <class T>
+  __device__ T* of(const View<T>& w, int back = 0) const {
+    return WIDE ? w.p + (back ? o - w.ts : o) : w.at(b, t - back, d);
+  }
 };
 
 template <int V, class T>
@@ -456,8 +480,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
   Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
   auto fill = [&](const Channel& c, int k, bool now) {
     const int t0 = k * p.TT + p.ty * R;
-    sx.fill(x, x.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
-    sg.fill(g, g.at(c.b, t0, c.d), t0, 0, c.n, SCAN_DEAD_GATE, now);
+    const Start<WIDE> at(x, c.b, c.d, t0);
+    sx.fill(x, at.of(x), t0, 0, c.n, 0.f, now);
+    sg.fill(g, at.of(g), t0, 0, c.n, SCAN_DEAD_GATE, now);
   };
   if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;          // walking: the channel's state
@@ -543,7 +568,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       h = mad(a[r], h, b[r]);
       o[r] = narrow<T>(h);
     }
-    put_stretch<WIDE, V, R>(y, y.at(c.b, t0, c.d), o, t0, c.n, c.ok ? s.len : 0);
+    put_stretch<WIDE, V, R>(y, Start<WIDE>(y, c.b, c.d, t0).of(y), o, t0, c.n, c.ok ? s.len : 0);
     c = c1, k = k1, gi = gi1;
     tile = next;
   }
@@ -585,10 +610,11 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
   Channel c = channel_of<V>(s, (gi << s.cx_log) + p.cx, 0);
   auto fill = [&](const Channel& c, int k, bool now) {
     const int t0 = k * p.TT + p.ty * R;
-    sx.fill(x, x.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
-    sg.fill(g, g.at(c.b, t0, c.d), t0, 0, c.n, SCAN_DEAD_GATE, now);
-    sd.fill(gy, gy.at(c.b, t0, c.d), t0, 0, c.n, 0.f, now);
-    if (!RERUN) sy.fill(y, y.at(c.b, (int64_t)t0 - 1, c.d), t0, 1, c.n, 0.f, now);
+    const Start<WIDE> at(x, c.b, c.d, t0);
+    sx.fill(x, at.of(x), t0, 0, c.n, 0.f, now);
+    sg.fill(g, at.of(g), t0, 0, c.n, SCAN_DEAD_GATE, now);
+    sd.fill(gy, at.of(gy), t0, 0, c.n, 0.f, now);
+    if (!RERUN) sy.fill(y, at.of(y, 1), t0, 1, c.n, 0.f, now);
   };
   if (!CHAIN || tile < s.total) fill(c, k, false);
   float held = 0.f;
@@ -719,8 +745,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       og[r] = narrow<T>(mul(xv[r], G));
       C = mul(a[r], G);
     }
-    put_stretch<WIDE, V, R>(gx, gx.at(c.b, t0, c.d), ox, t0, c.n, c.ok ? s.len : 0);
-    put_stretch<WIDE, V, R>(gg, gg.at(c.b, t0, c.d), og, t0, c.n, c.ok ? s.len : 0);
+    const Start<WIDE> to(gx, c.b, c.d, t0);
+    put_stretch<WIDE, V, R>(gx, to.of(gx), ox, t0, c.n, c.ok ? s.len : 0);
+    put_stretch<WIDE, V, R>(gg, to.of(gg), og, t0, c.n, c.ok ? s.len : 0);
     c = c1, k = k1, gi = gi1;
     tile = next;
   }
@@ -897,10 +924,15 @@ static cudaError_t allow_shared(K kernel) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 << 10);
 }
 
-// All views wide: the kernels of this variant have no other path.
+// All views wide, with the first one's strides: the kernels of this variant
+// have no other path.
 template <int V, class... W>
-static bool all_wide(int size, const W*... w) {
-  return ((aligned_to(w->data, V * size) && w->batch_stride % V == 0 && w->time_stride % V == 0) && ...);
+static bool all_wide(int size, const scan_view* first, const W*... w) {
+  const auto same = [&](const scan_view* v) {
+    return aligned_to(v->data, V * size) && v->batch_stride == first->batch_stride &&
+           v->time_stride == first->time_stride;
+  };
+  return first->batch_stride % V == 0 && first->time_stride % V == 0 && same(first) && (same(w) && ...);
 }
 
 template <class K, class... A>
@@ -913,7 +945,10 @@ static cudaError_t launch(K kernel, const Cut& c, cudaStream_t stream, A... a) {
 template <class T, class F, class... W>
 static cudaError_t with_variant(int32_t dim, F f, const W*... w) {
   using std::integral_constant;
-  if (dim % kWideV) return f(integral_constant<int, 1>(), std::true_type());
+  if (dim % kWideV) {
+    if (all_wide<1>(sizeof(T), w...)) return f(integral_constant<int, 1>(), std::true_type());
+    return f(integral_constant<int, 1>(), std::false_type());
+  }
   if (all_wide<kWideV>(sizeof(T), w...)) return f(integral_constant<int, kWideV>(), std::true_type());
   return f(integral_constant<int, kWideV>(), std::false_type());
 }
