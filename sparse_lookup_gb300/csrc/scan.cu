@@ -240,7 +240,9 @@ struct ScanArgs {
   const int32_t* offsets;
   uint32_t* status;
   ScanShared* shared;
-  ulonglong2* records;
+  ulonglong2* records;   // [tiles][pitch] (chained calls)
+  ulonglong2* states;    // [groups of tiles + 1][pitch]
+  uint32_t pitch;        // channels in all: a chained call has few
 };
 
 __device__ __forceinline__ int live_len(const ScanArgs& s, int b) {
@@ -284,10 +286,12 @@ __device__ __forceinline__ uint32_t get_record(const ulonglong2* p, Affine& f) {
 __device__ __forceinline__ float chain_state(const ScanArgs& s, int64_t col, int i, bool want, bool next, Affine all,
                                              float state0, uint32_t epoch) {
   constexpr int J = kGroup / kAhead;
-  const int64_t pitch = (int64_t)s.batch * s.dim;
-  ulonglong2 *own = s.records + col, *states = s.records + s.tiles * pitch + col;
+  const auto row = [&](uint32_t r) { return (uint64_t)r * s.pitch; };
   const int j = threadIdx.x & (J - 1), m = i / kGroup, at = i % kGroup;
-  if (want && next && j == 0 && at != kGroup - 1) put_record(own + i * pitch, all, epoch);
+  ulonglong2* own = s.records + (row(m * kGroup) + col);   // the group's first tile
+  ulonglong2* states = s.states + (row(m) + col);
+  if (want && next && j == 0 && at != kGroup - 1) put_record(own + row(at), all, epoch);
+  own += row(j * kAhead);
   Affine f[kAhead], st{0.f, state0};
   bool have[kAhead], have_state = !want || m == 0 || j != 0;
 #pragma unroll
@@ -299,8 +303,8 @@ __device__ __forceinline__ float chain_state(const ScanArgs& s, int64_t col, int
     bool all_here = true;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u)
-      if (!have[u]) have[u] = get_record(own + (m * kGroup + j * kAhead + u) * pitch, f[u]) == epoch;
-    if (!have_state) have_state = get_record(states + m * pitch, st) == epoch;
+      if (!have[u]) have[u] = get_record(own + row(u), f[u]) == epoch;
+    if (!have_state) have_state = get_record(states, st) == epoch;
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) all_here = all_here && have[u];
     if (__all_sync(kFull, all_here && have_state)) break;
@@ -321,7 +325,7 @@ __device__ __forceinline__ float chain_state(const ScanArgs& s, int64_t col, int
   }
   const float h = __shfl_sync(kFull, fmaf(sum.a, st.b, sum.b), 0, J);
   if (want && next && j == 0 && at == kGroup - 1)
-    put_record(states + (m + 1) * pitch, {0.f, fmaf(all.a, h, all.b)}, epoch);
+    put_record(states + s.pitch, {0.f, fmaf(all.a, h, all.b)}, epoch);
   return h;
 }
 
@@ -491,8 +495,6 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
     const int t0 = k * p.TT + p.ty * R;
     fill(c, k, true);
     copies_done();
-    uint32_t ticket = 0;
-    if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
     Lanes<V> a[R], b[R], fa = all_of<V>(1.f), fb = all_of<V>(0.f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -502,9 +504,10 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       fa = mul(fa, a[r]);
       fb = mad(a[r], fb, b[r]);
     }
-    // the staged inputs are in registers: copy the next tile's.  Its ticket was
-    // drawn when this tile's inputs had come, not before: a CTA that drew two
-    // neighbours would publish the second only after the first's own wait.
+    // The staged inputs are in registers: copy the next tile's.  A chained call
+    // draws its ticket only when this tile has waited for the state before it:
+    // a tile held by a CTA that still waits would make later ones wait for it
+    // (drawn before the join: 131072 x 512 fp32 177 us forward, after: 157).
     int k1 = k + 1;
     int64_t gi1 = gi;
     Channel c1 = c;
@@ -536,9 +539,8 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
         sa[p.ty * p.pitch + p.cx * V + v] = fa.v[v];
         sb[p.ty * p.pitch + p.cx * V + v] = fb.v[v];
       }
-      if (CHAIN && threadIdx.x == 0) slot = ticket;
       __syncthreads();
-      ahead();
+      if (!CHAIN) ahead();
       const Channel q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
       Affine f[V], ex, all;
       join_stretches<V>(p, sa, sb, false, f, ex, all);
@@ -558,7 +560,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       }
       held = fmaf(all.a, held, all.b);
       if (state_out && live && p.j == 0 && end >= q.n) state_out[q.col] = held;
+      if (CHAIN && threadIdx.x == 0) slot = take_ticket(s);
       __syncthreads();
+      if (CHAIN) ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
     }
@@ -623,8 +627,6 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
     const int t0 = k * p.TT + p.ty * R;
     fill(c, k, true);
     copies_done();
-    uint32_t ticket = 0;
-    if (CHAIN && threadIdx.x == 0) ticket = take_ticket(s);
     Lanes<V> a[R], na[R], xv[R], dy[R];   // xv: x, then the gate's factor of G
     Lanes<V> fa = all_of<V>(1.f), fb = all_of<V>(0.f), fc = all_of<V>(0.f);
 #pragma unroll
@@ -689,9 +691,8 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       const bool live = q.ok && (start < q.n || k == 0);
       float first = 0.f;
       if (RERUN && live) first = k == 0 ? (state_in ? state_in[q.col] : 0.f) : to_f32(*y.at(q.b, start - 1, q.d));
-      if (CHAIN && threadIdx.x == 0) slot = ticket;
       __syncthreads();
-      ahead();
+      if (!CHAIN) ahead();
       Affine f[V], ex, all;
       float st;
       if (RERUN) {
@@ -722,7 +723,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       }
       if (live) held = fmaf(all.a, held, all.b);
       if (grad_in && live && p.j == 0 && k == 0) grad_in[q.col] = held;
+      if (CHAIN && threadIdx.x == 0) slot = take_ticket(s);
       __syncthreads();
+      if (CHAIN) ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         if (RERUN) h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
@@ -848,6 +851,8 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   if (c.chain) {
     a.groups = make_div_magic32((uint32_t)groups);
     a.total = (uint32_t)(groups * a.tiles);
+    a.pitch = (uint32_t)(batch * h->dim);
+    a.states = a.records + (int64_t)a.tiles * a.pitch;
   }
   const int64_t all = groups * a.tiles;
   c.grid = (unsigned)(c.chain ? (all < slots ? all : slots) : groups);

@@ -36,12 +36,21 @@ class AdamwTensor(ctypes.Structure):
 # raw C names
 # ---------------------------------------------------------------------------
 
-def _stream(stream):
-    """The raw handle of a stream; None: the current stream of the current
-    device (the short way to it: a call may be a few microseconds of work)."""
+_current_stream = None
+
+
+def _stream(stream, device=None):
+    """The raw handle of a stream; None: the current stream of the device (the
+    short way to it: a call may be a few microseconds of work)."""
+    global _current_stream
     if stream is None:
-        import torch
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        if _current_stream is None:
+            import torch
+            _current_stream = torch._C._cuda_getCurrentRawStream
+        if device is None:
+            import torch
+            device = torch.cuda.current_device()
+        return _current_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -175,7 +184,7 @@ class _Handle:
 
     def __init__(self):
         import torch
-        self._t = torch
+        self._t, self._f32, self._i32, self._new = torch, torch.float32, torch.int32, torch.empty
 
     def close(self):
         if self.handle:
@@ -190,9 +199,9 @@ class _Handle:
 
     def _empty(self, shape, dtype, device, stream):
         """A tensor that belongs to the stream the kernel will run on."""
-        torch = self._t
         if stream is None:
-            return torch.empty(shape, dtype=dtype, device=device)
+            return self._new(shape, dtype=dtype, device=device)
+        torch = self._t
         s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
         with torch.cuda.stream(s):
             return torch.empty(shape, dtype=dtype, device=device)
@@ -216,42 +225,49 @@ class GatedScan(_Handle):
         super().__init__()
         self.dim = dim
         self.handle = scan_create(dim, max_batch, max_len)
-        self._fwd, self._bwd = lib().scan_forward, lib().scan_backward
+        L = lib()
+        self._fwd, self._bwd, self._step = L.scan_forward, L.scan_backward, L.scan_step
         # the views of a call, rewritten by each call and read before it returns
-        self._views = (c_int64 * 21)()
+        self._views = (c_int64 * 18)()
         at = ctypes.addressof(self._views)
-        self._view_at = [at + 24 * i for i in range(7)]
+        self._view_at = [at + 24 * i for i in range(6)]
 
-    def _view(self, i, t, name, shape, dtype):
+    def _view(self, t, name, shape, dtype):
+        """(pointer, batch stride, time stride) of a [batch, time, dim] tensor."""
         p = _want(t, name, shape, dtype, False)
+        if t.is_contiguous():
+            return p, shape[1] * shape[2], shape[2]
         sb, st, _ = t.stride()
-        self._views[3 * i:3 * i + 3] = (p, sb, st)
+        return p, sb, st
 
     def _common(self, x, gate, offsets, state):
-        if x.dim() != 3 or x.shape[2] != self.dim:
-            raise ValueError("x: [batch, time, %d] expected, got %s" % (self.dim, tuple(x.shape)))
-        dt, shape = x.dtype, x.shape
-        code = _element(dt)
-        self._view(0, x, "x", shape, dt)
-        self._view(1, gate, "gate", shape, dt)
-        o = None if offsets is None else _want(offsets, "offsets", (shape[0] + 1,), self._t.int32)
-        s = None if state is None else _want(state, "state", (shape[0], self.dim), self._t.float32)
-        return code, dt, shape, x.device, o, s
+        shape, dt = x.shape, x.dtype
+        if len(shape) != 3 or shape[2] != self.dim:
+            raise ValueError("x: [batch, time, %d] expected, got %s" % (self.dim, tuple(shape)))
+        code = _dtype_codes.get(dt)
+        if code is None:
+            code = _element(dt)
+        B = shape[0]
+        return (code, dt, shape, x.device, None if offsets is None else _want(offsets, "offsets", (B + 1,), self._i32),
+                None if state is None else _want(state, "state", (B, self.dim), self._f32),
+                self._view(x, "x", shape, dt) + self._view(gate, "gate", shape, dt))
 
     def forward(self, x, gate, offsets=None, state=None, y=None, last=None, stream=None):
         """(y, last): h_t at every position, and the state [batch, dim]
         float32 after the last live one.  state: the one before the first
         (None = 0).  y and last may be given."""
-        code, dt, shape, dev, o, s = self._common(x, gate, offsets, state)
-        f32, ends = self._t.float32, (shape[0], self.dim)
+        code, dt, shape, dev, o, s, views = self._common(x, gate, offsets, state)
+        ends = (shape[0], shape[2])
         if y is None:
             y = self._empty(shape, dt, dev, stream)
         if last is None:
-            last = self._empty(ends, f32, dev, stream)
-        self._view(2, y, "y", shape, dt)
+            last = self._empty(ends, self._f32, dev, stream)
+        self._views[0:9] = views + self._view(y, "y", shape, dt)
         v = self._view_at
-        _check(self._fwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], _want(last, "last", ends, f32),
-                         _stream(stream)), "scan_forward")
+        st = self._fwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2],
+                       _want(last, "last", ends, self._f32), _stream(stream, dev.index))
+        if st:
+            _check(st, "scan_forward")
         return y, last
 
     def backward(self, x, gate, y, grad_y, offsets=None, state=None, grad_last=None, grad_x=None, grad_gate=None,
@@ -259,8 +275,8 @@ class GatedScan(_Handle):
         """(grad_x, grad_gate, grad_state) from the gradients of y and (None =
         0) of last; x, gate, offsets and state as in forward, y as it gave
         it.  The results may be given."""
-        code, dt, shape, dev, o, s = self._common(x, gate, offsets, state)
-        f32, ends = self._t.float32, (shape[0], self.dim)
+        code, dt, shape, dev, o, s, views = self._common(x, gate, offsets, state)
+        f32, ends = self._f32, (shape[0], shape[2])
         gl = None if grad_last is None else _want(grad_last, "grad_last", ends, f32)
         if grad_x is None:
             grad_x = self._empty(shape, dt, dev, stream)
@@ -268,14 +284,13 @@ class GatedScan(_Handle):
             grad_gate = self._empty(shape, dt, dev, stream)
         if grad_state is None:
             grad_state = self._empty(ends, f32, dev, stream)
-        gs = _want(grad_state, "grad_state", ends, f32)
-        self._view(2, y, "y", shape, dt)
-        self._view(3, grad_y, "grad_y", shape, dt)
-        self._view(4, grad_x, "grad_x", shape, dt)
-        self._view(5, grad_gate, "grad_gate", shape, dt)
+        self._views[:] = (views + self._view(y, "y", shape, dt) + self._view(grad_y, "grad_y", shape, dt) +
+                          self._view(grad_x, "grad_x", shape, dt) + self._view(grad_gate, "grad_gate", shape, dt))
         v = self._view_at
-        _check(self._bwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], v[3], gl, v[4], v[5], gs,
-                         _stream(stream)), "scan_backward")
+        st = self._bwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], v[3], gl, v[4], v[5],
+                       _want(grad_state, "grad_state", ends, f32), _stream(stream, dev.index))
+        if st:
+            _check(st, "scan_backward")
         return grad_x, grad_gate, grad_state
 
     def step(self, x, gate, rows, states, y=None, stream=None):
@@ -283,17 +298,18 @@ class GatedScan(_Handle):
         int64, the session's row of states [num_rows, dim] float32 (outside:
         dropped, y = 0).  Updates states in place, returns y [n, dim].  Rows
         of one call must be distinct."""
-        if x.dim() != 2 or x.shape[1] != self.dim or states.dim() != 2:
-            raise ValueError("x: [n, %d] and states [num_rows, %d] expected" % (self.dim, self.dim))
-        shape, dt = x.shape, x.dtype
-        n, pool = shape[0], states.shape[0]
+        shape, dt, D = x.shape, x.dtype, self.dim
+        if len(shape) != 2 or shape[1] != D or states.dim() != 2:
+            raise ValueError("x: [n, %d] and states [num_rows, %d] expected" % (D, D))
+        n, pool, dev = shape[0], states.shape[0], x.device
         if y is None:
-            y = self._empty(shape, dt, x.device, stream)
-        _check(lib().scan_step(n, self.dim, _element(dt), _want(x, "x", shape, dt, False), x.stride(0),
-                               _want(gate, "gate", shape, dt, False), gate.stride(0),
-                               _want(rows, "rows", (n,), self._t.int64),
-                               _want(states, "states", (pool, self.dim), self._t.float32), pool,
-                               _want(y, "y", shape, dt, False), y.stride(0), _stream(stream)), "scan_step")
+            y = self._empty(shape, dt, dev, stream)
+        st = self._step(n, D, _element(dt), _want(x, "x", shape, dt, False), x.stride(0),
+                        _want(gate, "gate", shape, dt, False), gate.stride(0),
+                        _want(rows, "rows", (n,), self._t.int64), _want(states, "states", (pool, D), self._f32), pool,
+                        _want(y, "y", shape, dt, False), y.stride(0), _stream(stream, dev.index))
+        if st:
+            _check(st, "scan_step")
         return y
 
     def device_status(self, stream=None):
@@ -319,6 +335,9 @@ class ExpertRouter(_Handle):
         super().__init__()
         self.n_experts, self.top_k, self.align = n_experts, top_k, align
         self.handle = moe_create(n_experts, top_k, max_tokens, align)
+        L = lib()
+        self._route, self._dispatch, self._combine = L.moe_route, L.moe_dispatch, L.moe_combine
+        self._combine_backward = L.moe_combine_backward
 
     def rows(self, n_tokens):
         """Rows of the expert-ordered arrays for n_tokens tokens."""
@@ -328,66 +347,83 @@ class ExpertRouter(_Handle):
     def route(self, experts, stream=None):
         """Routing of experts [tokens, top_k] int32 (a choice outside [0,
         n_experts) is dropped)."""
-        if experts.dim() != 2:
-            raise ValueError("experts: [tokens, %d] expected, got %s" % (self.top_k, tuple(experts.shape)))
-        i32 = self._t.int32
-        n, E, K = experts.shape[0], self.n_experts, self.top_k
-        e = _want(experts, "experts", (n, K), i32)
-        R = self.rows(n)
-        offsets, counts, pos, src = [self._empty(k, i32, experts.device, stream) for k in ((E + 1,), (E,), (n, K), (R,))]
-        _check(lib().moe_route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), pos.data_ptr(),
-                               src.data_ptr(), _stream(stream)), "moe_route")
+        shape, i32, E = experts.shape, self._i32, self.n_experts
+        if len(shape) != 2:
+            raise ValueError("experts: [tokens, %d] expected, got %s" % (self.top_k, tuple(shape)))
+        n, dev = shape[0], experts.device
+        pos = (n, self.top_k)
+        e = _want(experts, "experts", pos, i32)
+        offsets, counts = self._empty((E + 1,), i32, dev, stream), self._empty((E,), i32, dev, stream)
+        pos, src = self._empty(pos, i32, dev, stream), self._empty((self.rows(n),), i32, dev, stream)
+        st = self._route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), pos.data_ptr(), src.data_ptr(),
+                         _stream(stream, dev.index))
+        if st:
+            _check(st, "moe_route")
         return Routing(offsets, counts, pos, src)
 
     def _routed(self, n, r):
-        i32 = self._t.int32
-        return _want(r.pos, "pos", (n, self.top_k), i32), _want(r.src, "src", (self.rows(n),), i32)
+        """(pointer of pos, pointer of src, rows) of a routing of n tokens."""
+        i32, rows = self._i32, self.rows(n)
+        return _want(r.pos, "pos", (n, self.top_k), i32), _want(r.src, "src", (rows,), i32), rows
 
     def dispatch(self, x, routing, xs=None, stream=None):
         """xs [rows, dim]: the token of each row; padding rows are 0."""
-        if x.dim() != 2:
-            raise ValueError("x: [tokens, dim] expected, got %s" % (tuple(x.shape),))
-        (n, dim), dt = x.shape, x.dtype
-        pos, src = self._routed(n, routing)
-        shape = (self.rows(n), dim)
+        shape, dt, dev = x.shape, x.dtype, x.device
+        if len(shape) != 2:
+            raise ValueError("x: [tokens, dim] expected, got %s" % (tuple(shape),))
+        n, dim = shape
+        pos, src, rows = self._routed(n, routing)
         if xs is None:
-            xs = self._empty(shape, dt, x.device, stream)
-        _check(lib().moe_dispatch(self.handle, n, dim, _element(dt), _want(x, "x", x.shape, dt, False), x.stride(0),
-                                  pos, src, _want(xs, "xs", shape, dt), _stream(stream)), "moe_dispatch")
+            xs = self._empty((rows, dim), dt, dev, stream)
+            to = xs.data_ptr()
+        else:
+            to = _want(xs, "xs", (rows, dim), dt)
+        st = self._dispatch(self.handle, n, dim, _element(dt), _want(x, "x", shape, dt, False), x.stride(0), pos, src,
+                            to, _stream(stream, dev.index))
+        if st:
+            _check(st, "moe_dispatch")
         return xs
 
     def combine(self, ys, weights, routing, y=None, stream=None):
         """y [tokens, dim]: the sum of each token's rows of ys, each times its
         weight ([tokens, top_k] float32; None = 1)."""
-        if ys.dim() != 2:
-            raise ValueError("ys: [rows, dim] expected, got %s" % (tuple(ys.shape),))
-        n, dim, dt = routing.pos.shape[0], ys.shape[1], ys.dtype
-        pos, _ = self._routed(n, routing)
-        w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._t.float32)
+        shape, dt, dev = ys.shape, ys.dtype, ys.device
+        if len(shape) != 2:
+            raise ValueError("ys: [rows, dim] expected, got %s" % (tuple(shape),))
+        n, dim = routing.pos.shape[0], shape[1]
+        pos, _, rows = self._routed(n, routing)
+        w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._f32)
         if y is None:
-            y = self._empty((n, dim), dt, ys.device, stream)
-        _check(lib().moe_combine(self.handle, n, dim, _element(dt), _want(ys, "ys", (self.rows(n), dim), dt), w, pos,
-                                 _want(y, "y", (n, dim), dt, False), y.stride(0), _stream(stream)), "moe_combine")
+            y = self._empty((n, dim), dt, dev, stream)
+            to, stride = y.data_ptr(), dim
+        else:
+            to, stride = _want(y, "y", (n, dim), dt, False), y.stride(0)
+        st = self._combine(self.handle, n, dim, _element(dt), _want(ys, "ys", (rows, dim), dt), w, pos, to, stride,
+                           _stream(stream, dev.index))
+        if st:
+            _check(st, "moe_combine")
         return y
 
     def combine_backward(self, grad_y, ys, weights, routing, grad_ys=None, grad_weights=None, stream=None):
         """(grad_ys, grad_weights) of combine; weights None gives grad_weights
         None."""
-        if grad_y.dim() != 2:
-            raise ValueError("grad_y: [tokens, dim] expected, got %s" % (tuple(grad_y.shape),))
-        (n, dim), dt, f32 = grad_y.shape, grad_y.dtype, self._t.float32
-        pos, src = self._routed(n, routing)
-        shape, each, dev = (self.rows(n), dim), (n, self.top_k), grad_y.device
+        shape, dt, dev, f32 = grad_y.shape, grad_y.dtype, grad_y.device, self._f32
+        if len(shape) != 2:
+            raise ValueError("grad_y: [tokens, dim] expected, got %s" % (tuple(shape),))
+        n, dim = shape
+        pos, src, rows = self._routed(n, routing)
+        wide, each = (rows, dim), (n, self.top_k)
         w = None if weights is None else _want(weights, "weights", each, f32)
         if weights is not None and grad_weights is None:
             grad_weights = self._empty(each, f32, dev, stream)
         gw = None if grad_weights is None else _want(grad_weights, "grad_weights", each, f32)
         if grad_ys is None:
-            grad_ys = self._empty(shape, dt, dev, stream)
-        _check(lib().moe_combine_backward(self.handle, n, dim, _element(dt), _want(grad_y, "grad_y", (n, dim), dt, False),
-                                          grad_y.stride(0), _want(ys, "ys", shape, dt), w, pos, src,
-                                          _want(grad_ys, "grad_ys", shape, dt), gw, _stream(stream)),
-               "moe_combine_backward")
+            grad_ys = self._empty(wide, dt, dev, stream)
+        st = self._combine_backward(self.handle, n, dim, _element(dt), _want(grad_y, "grad_y", shape, dt, False),
+                                    grad_y.stride(0), _want(ys, "ys", wide, dt), w, pos, src,
+                                    _want(grad_ys, "grad_ys", wide, dt), gw, _stream(stream, dev.index))
+        if st:
+            _check(st, "moe_combine_backward")
         return grad_ys, grad_weights
 
     def dispatch_backward(self, grad_xs, routing, grad_x=None, stream=None):
