@@ -10,11 +10,12 @@ namespace emb {
 
 constexpr int kBlock = 256;        // elements that share a top: one warp, eight elements per lane
 constexpr int kAdamThreads = 128;
-// CTAs on an SM: as many as hold a block's values without spilling.  Measured
-// with 8-bit states (128 M elements): bf16 weights 304 us with 10, 324 with
-// 8; fp32 weights (100 M) 290 with 10, 261 with 8.
-template <class W>
-constexpr int adam_ctas() { return sizeof(W) == 4 ? 8 : 10; }
+constexpr int kExportUnits = 2;
+// CTAs on an SM: as many as hold a block's values without spilling much.
+// Measured with 8-bit states on 128 M weights: bf16 262 us with 10, 267 with 9;
+// bf16 with fp32 masters 365 and 353; 100 M fp32 283 and 248.
+template <class P, bool MASTER>
+constexpr int adam_ctas() { return sizeof(P) == 4 || MASTER ? 9 : 10; }
 
 struct AdamTensor {
   void* param;
@@ -38,6 +39,7 @@ struct AdamUnit {
 // A step's scalars, each computed in 64 bits and rounded once.
 struct AdamScalars {
   float lr, lr_c1, b1, nb1, b2, nb2, c2, eps, one;
+  bool flush;            // eps is large enough to drop roots below fp32's normal range
   uint64_t key;          // SplitMix64 output for seed and step
 };
 
@@ -158,7 +160,7 @@ __device__ __forceinline__ void store8(T* p, const float (&r)[8], int n, bool ve
       Vec<T, 8> a;
 #pragma unroll
       for (int i = 0; i < 8; i += 2) narrow2(&a.e[i], make_float2(r[i], r[i + 1]));
-      store_vec(p, a);
+      store_last(p, a);
     }
   } else {
 #pragma unroll
@@ -235,11 +237,22 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int
     mi = __ffma2_rn(__fmul2_rn(mi, both(s.b1)), both(s.one), __fmul2_rn(gi, both(s.nb1)));
     vi = __ffma2_rn(__fmul2_rn(vi, both(s.b2)), both(s.one), __fmul2_rn(__fmul2_rn(gi, gi), both(s.nb2)));
     m[i] = mi.x, m[i + 1] = mi.y, v[i] = vi.x, v[i + 1] = vi.y;
-    float2 r = __fmul2_rn(vi, both(s.c2));
-    asm("sqrt.approx.f32 %0, %0;" : "+f"(r.x));
-    asm("sqrt.approx.f32 %0, %0;" : "+f"(r.y));
-    r = __fadd2_rn(r, both(s.eps));
-    const float2 q = make_float2(__fdividef(mi.x, r.x), __fdividef(mi.y, r.y));
+    float2 r = __fmul2_rn(vi, both(s.c2)), q;
+    if (s.flush) {
+      // the flushing forms are single instructions; what they drop (a root
+      // below 1.1e-19) is under 2^-23 of eps
+      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+      asm("sqrt.approx.ftz.f32 %0, %0;" : "+f"(r.y));
+      r = __fadd2_rn(r, both(s.eps));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.x));
+      asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(r.y));
+      q = __fmul2_rn(mi, r);
+    } else {
+      asm("sqrt.approx.f32 %0, %0;" : "+f"(r.x));
+      asm("sqrt.approx.f32 %0, %0;" : "+f"(r.y));
+      r = __fadd2_rn(r, both(s.eps));
+      q = make_float2(__fdividef(mi.x, r.x), __fdividef(mi.y, r.y));
+    }
     const float2 wi = __ffma2_rn(q, both(-s.lr_c1), __fmul2_rn(make_float2(w[i], w[i + 1]), both(keep)));
     w[i] = wi.x, w[i + 1] = wi.y;
   }
@@ -275,7 +288,7 @@ __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64
 // Warps that walked several blocks with the next one's loads ahead held fewer
 // blocks in flight for the registers that took, and were slower.
 template <class P, class G, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads, adam_ctas<P>()) k_adamw(const AdamTensor* __restrict__ tensors,
+__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adamw(const AdamTensor* __restrict__ tensors,
                                                                    const void* const* __restrict__ grads,
                                                                    const AdamUnit* __restrict__ units, int64_t n_units,
                                                                    const __grid_constant__ AdamScalars s,
@@ -295,20 +308,34 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw_export(const AdamTensor*
                                                                const AdamUnit* __restrict__ units, int64_t n_units,
                                                                __nv_bfloat16* __restrict__ m_out,
                                                                __nv_bfloat16* __restrict__ v_out) {
-  const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
-  if (i >= n_units) return;
-  const AdamUnit u = units[i];
-  const AdamTensor t = tensors[u.tensor];
-  const int64_t i0 = (int64_t)u.block * kBlock + (threadIdx.x & 31) * 8;
-  const int n = lane_elements(t, i0);
-  const bool vec = t.aligned && n == 8;
-  uint2 mc = make_uint2(0, 0), vc = make_uint2(0, 0);
-  if (n) mc = load_codes((const uint8_t*)t.m + i0, n, vec), vc = load_codes((const uint8_t*)t.v + i0, n, vec);
-  float m[8], v[8];
-  decode8<127>(mc, max((int)t.m_top[u.block] - 127, 0), m);
-  decode8<255>(vc, max((int)t.v_top[u.block] - 255, 0), v);
-  store8(m_out + t.start + i0, m, 8, true);   // a tensor's room is whole blocks: the rest of the last one is zeros
-  store8(v_out + t.start + i0, v, 8, true);
+  constexpr int K = kExportUnits;   // a warp's units, their loads in flight together
+  const int64_t first = ((blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5) * K;
+  uint2 mc[K], vc[K];
+  int mt[K], vt[K];
+  int64_t at[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    at[k] = -1;
+    if (first + k >= n_units) continue;
+    const AdamUnit u = units[first + k];
+    const AdamTensor& t = tensors[u.tensor];
+    const int64_t i0 = (int64_t)u.block * kBlock + (threadIdx.x & 31) * 8;
+    const int n = lane_elements(t, i0);
+    const bool vec = t.aligned && n == 8;
+    mc[k] = vc[k] = make_uint2(0, 0);
+    if (n) mc[k] = load_codes((const uint8_t*)t.m + i0, n, vec), vc[k] = load_codes((const uint8_t*)t.v + i0, n, vec);
+    mt[k] = t.m_top[u.block], vt[k] = t.v_top[u.block];
+    at[k] = t.start + i0;
+  }
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if (at[k] < 0) continue;
+    float m[8], v[8];
+    decode8<127>(mc[k], max(mt[k] - 127, 0), m);
+    decode8<255>(vc[k], max(vt[k] - 255, 0), v);
+    store8(m_out + at[k], m, 8, true);   // a tensor's room is whole blocks: the rest of the last one is zeros
+    store8(v_out + at[k], v, 8, true);
+  }
 }
 
 // A kind of tensors: element types and master decide the kernel.
@@ -482,6 +509,7 @@ extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double be
   s.c2 = (float)(1.0 / (1.0 - std::pow(beta2, (double)step)));
   s.eps = (float)eps;
   s.one = 1.f;
+  s.flush = eps >= 1e-12;
   s.key = splitmix64(((uint64_t)seed << 32) + (uint64_t)step);
   for (const AdamKind& k : h->kinds) {
     k.kernel<<<unit_grid(k.count), kAdamThreads, 0, (cudaStream_t)stream>>>(
@@ -502,7 +530,7 @@ extern "C" emb_status adamw_export_states(emb_adamw h, void* m_out, void* v_out,
   if (!h->eight) return EMB_ERR_UNSUPPORTED;
   if (h->n_units == 0) return EMB_OK;
   if (!m_out || !v_out || !aligned16(m_out) || !aligned16(v_out)) return EMB_ERR_INVALID_ARG;
-  k_adamw_export<<<unit_grid(h->n_units), kAdamThreads, 0, (cudaStream_t)stream>>>(
+  k_adamw_export<<<unit_grid((h->n_units + kExportUnits - 1) / kExportUnits), kAdamThreads, 0, (cudaStream_t)stream>>>(
       h->tensors_d, h->units_d, h->n_units, (__nv_bfloat16*)m_out, (__nv_bfloat16*)v_out);
   return cuda_status(cudaGetLastError());
 }
