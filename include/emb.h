@@ -601,6 +601,18 @@ emb_status adamw_destroy(emb_adamw h);
 emb_status emb_selftest_sort_timeout(uint32_t* latched, uint32_t* fail_word, int32_t* table_untouched,
                                      float* wait_ms);
 
+/* scan_selftest_timeout -- makes the bounded wait between parts of a sequence
+ * run out on purpose, without faulting or hanging the GPU: a chained
+ * scan_forward over two tiles of which only the second is handed out, so its
+ * wait for the first can never end; after its bound (about a second) it latches
+ * EMB_ERR_TIMEOUT, and the next call on the same handle runs as ever.
+ * Allocates and frees its own buffers and synchronizes the device.  All
+ * pointers are host:
+ *  latched        status after the call that waited (EMB_ERR_TIMEOUT expected)
+ *  latched_after  status after the next call (EMB_OK expected)
+ *  wait_ms        optional: device time of the waiting call */
+emb_status scan_selftest_timeout(uint32_t* latched, uint32_t* latched_after, float* wait_ms);
+
 /* emb_debug_fail_alloc -- host-side fault injection for the create calls:
  * after `after` more device allocations by emb_plan_create / hash_create /
  * the self tests succeed, the next one fails as if the device were out of

@@ -100,6 +100,7 @@ _SIGS = {
     "scan_step": (c_int32, [c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p,
                             c_int64, c_void_p, c_int64, c_void_p]),
     "scan_get_device_status": (c_int32, [c_void_p, c_void_p]),
+    "scan_selftest_timeout": (c_int32, [c_void_p, c_void_p, c_void_p]),
     "scan_destroy": (c_int32, [c_void_p]),
     "moe_create": (c_int32, [c_int32, c_int32, c_int64, c_int32, POINTER(c_void_p)]),
     "moe_route": (c_int32, [c_void_p, c_int64, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -511,4 +512,4 @@ def _device_view(ptr_value, shape):
 from .dense import (AdamW, AdamwTensor, ExpertRouter, GatedScan, Routing, ScanView, adamw_bind_grads,  # noqa: E402,F401
                     adamw_create, adamw_destroy, adamw_export_size, adamw_export_states, adamw_step, moe_combine,
                     moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_route, scan_backward,
-                    scan_create, scan_destroy, scan_forward, scan_get_device_status, scan_step)
+                    scan_create, scan_destroy, scan_forward, scan_get_device_status, scan_selftest_timeout, scan_step)

@@ -757,24 +757,26 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
   if (CHAIN && threadIdx.x == 0) leave(s);
 }
 
-template <class T>
-__global__ void __launch_bounds__(256) k_scan_step(int64_t n, int32_t dim, const T* __restrict__ x, int64_t xs,
+// One position per session: a thread takes V channels of one row.
+template <class T, int V>
+__global__ void __launch_bounds__(128) k_scan_step(int64_t n, DivMagic vecs, const T* __restrict__ x, int64_t xs,
                                                    const T* __restrict__ g, int64_t gs,
                                                    const int64_t* __restrict__ rows, float* __restrict__ states,
                                                    int64_t num_rows, T* __restrict__ y, int64_t ys) {
-  for (int64_t i = blockIdx.x; i < n; i += gridDim.x) {
-    const int64_t row = rows[i];
-    const bool live = row >= 0 && row < num_rows;
-    for (int d = threadIdx.x; d < dim; d += blockDim.x) {
-      float h = 0.f;
-      if (live) {
-        float a, na;
-        gates(to_f32(g[i * gs + d]), a, na);
-        h = a * states[row * dim + d] + na * to_f32(x[i * xs + d]);
-        states[row * dim + d] = h;
-      }
-      y[i * ys + d] = from_f32<T>(h);
+  const int64_t per = (int64_t)vecs.d, dim = per * V;
+  for (int64_t i = blockIdx.x * 128ll + threadIdx.x; i < n * per; i += gridDim.x * 128ll) {
+    const int64_t row = (int64_t)div_magic((uint64_t)i, vecs), d = (i - row * per) * V;
+    const int64_t at = rows[row];
+    Lanes<V> h = all_of<V>(0.f);
+    if (at >= 0 && at < num_rows) {
+      const Vec<T, V> gv = load_vec<T, V>(g + row * gs + d), xv = load_vec<T, V>(x + row * xs + d);
+      Vec<float, V>* s = reinterpret_cast<Vec<float, V>*>(states + at * dim + d);
+      Lanes<V> a, na;
+      gates(gv, a, na);
+      h = mad(a, widen(*s), mul(na, widen(xv)));
+      *s = narrow<float>(h);
     }
+    store_vec(y + row * ys + d, narrow<T>(h));
   }
 }
 
@@ -813,9 +815,8 @@ struct Cut {
 constexpr int kWideV = 4, kFwdR = 8, kBwdR = 4;   // V = 1: twice the positions, for as many bytes in flight
 // log2 of the column vectors of a tile, for V = 4 and V = 1
 constexpr int kCx = 3, kCxOne = 5;
-int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R, int sms) {
+int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R) {
   const int64_t cols = batch * dim;
-  (void)sms;
   const int TT = (kScanThreads >> (V == 1 ? kCxOne : kCx)) * R;
   const int64_t tiles = (len + TT - 1) / TT;
   return (tiles + tiles / kGroup + 1) * cols;
@@ -880,11 +881,11 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   if (e == cudaSuccess) {
     const int64_t cols = (int64_t)h->sm_count * kCtasPerSm * (kWideV << (kCx + 1)) + dim;   // a call with more walks
     const int64_t batch = (int64_t)max_batch * dim < cols ? max_batch : cols / dim + 1;
-    for (int V : {1, kWideV})
-      for (int R : {kFwdR, kBwdR}) {
-        const int64_t n = chain_records(dim, batch, max_len, V, V == 1 ? 2 * R : R, h->sm_count);
-        if (n > h->max_records) h->max_records = n;
-      }
+    const int V = dim % kWideV ? 1 : kWideV;
+    for (int R : {kFwdR, kBwdR}) {
+      const int64_t n = chain_records(dim, batch, max_len, V, V == 1 ? 2 * R : R);
+      if (n > h->max_records) h->max_records = n;
+    }
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
   }
   if (e == cudaSuccess) e = dev_alloc((void**)&h->shared_d, sizeof(ScanShared));
@@ -1022,11 +1023,50 @@ extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const voi
       !aligned_to(y, size) || !aligned_to(states, 4) || !aligned_to(rows, 8) || (n > 1 && y_stride < dim))
     return EMB_ERR_INVALID_ARG;
   if (dim > 65536) return EMB_ERR_UNSUPPORTED;
-  const unsigned grid = (unsigned)(n < (1 << 20) ? n : (1 << 20));
+  const bool wide = dim % kWideV == 0 && x_stride % kWideV == 0 && gate_stride % kWideV == 0 &&
+                    y_stride % kWideV == 0 && aligned_to(x, kWideV * size) && aligned_to(gate, kWideV * size) &&
+                    aligned_to(y, kWideV * size) && aligned_to(states, kWideV * sizeof(float));
+  const int vecs = wide ? dim / kWideV : dim;
+  const int64_t need = (n * vecs + 127) / 128;
+  const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
   with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    k_scan_step<T><<<grid, 256, 0, (cudaStream_t)stream>>>(n, dim, (const T*)x, x_stride, (const T*)gate, gate_stride,
-                                                         rows, states, num_rows, (T*)y, y_stride);
+    auto kernel = wide ? k_scan_step<T, kWideV> : k_scan_step<T, 1>;
+    kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(n, make_div_magic((uint64_t)vecs), (const T*)x, x_stride,
+                                                  (const T*)gate, gate_stride, rows, states, num_rows, (T*)y,
+                                                  y_stride);
   });
   return cuda_status(cudaGetLastError());
+}
+
+// A sequence of two tiles of which only the second is handed out.
+extern "C" emb_status scan_selftest_timeout(uint32_t* latched, uint32_t* latched_after, float* wait_ms) {
+  if (!latched || !latched_after) return EMB_ERR_INVALID_ARG;
+  constexpr int dim = 32, len = 2 * (kScanThreads >> kCx) * kFwdR;
+  emb_scan h = nullptr;
+  emb_status st = scan_create(dim, 1, len, &h);
+  if (st != EMB_OK) return st;
+  float* buf = nullptr;   // x, gate and y
+  cudaEvent_t a = nullptr, b = nullptr;
+  cudaError_t e = dev_alloc((void**)&buf, sizeof(float) * dim * len * 3);
+  if (e == cudaSuccess) e = cudaMemset(buf, 0, sizeof(float) * dim * len * 3);
+  if (e == cudaSuccess) e = cudaEventCreate(&a);
+  if (e == cudaSuccess) e = cudaEventCreate(&b);
+  const uint32_t second = 1;
+  if (e == cudaSuccess) e = cudaMemcpy(&h->shared_d->ticket, &second, sizeof(second), cudaMemcpyHostToDevice);
+  const scan_view x{buf, dim * len, dim}, g{buf + dim * len, dim * len, dim}, y{buf + 2 * dim * len, dim * len, dim};
+  for (uint32_t* out : {latched, latched_after}) {
+    if (e != cudaSuccess) break;
+    e = cudaEventRecord(a, nullptr);
+    if (e == cudaSuccess) st = scan_forward(h, 1, len, EMB_DT_F32, &x, &g, nullptr, nullptr, &y, nullptr, nullptr);
+    if (e == cudaSuccess && st == EMB_OK) e = cudaEventRecord(b, nullptr);
+    if (e == cudaSuccess && st == EMB_OK) *out = (uint32_t)scan_get_device_status(h, nullptr);
+    if (e == cudaSuccess && st == EMB_OK && out == latched && wait_ms) e = cudaEventElapsedTime(wait_ms, a, b);
+    if (st != EMB_OK) break;
+  }
+  if (a) cudaEventDestroy(a);
+  if (b) cudaEventDestroy(b);
+  dev_free(buf);
+  scan_destroy(h);
+  return st != EMB_OK ? st : cuda_status(e);
 }

@@ -85,6 +85,14 @@ def scan_get_device_status(h, stream=None):
     return int(lib().scan_get_device_status(h, _stream(stream)))
 
 
+def scan_selftest_timeout():
+    """Runs the chain's bounded-wait self test; returns dict(status, latched,
+    latched_after, wait_ms)."""
+    latched, after, ms = ctypes.c_uint32(0), ctypes.c_uint32(0), c_float(0.0)
+    st = lib().scan_selftest_timeout(ctypes.byref(latched), ctypes.byref(after), ctypes.byref(ms))
+    return dict(status=int(st), latched=latched.value, latched_after=after.value, wait_ms=ms.value)
+
+
 def scan_destroy(h):
     _check(lib().scan_destroy(h), "scan_destroy")
 

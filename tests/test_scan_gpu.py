@@ -416,3 +416,9 @@ def test_allocation_failure():
         plan.close()
         break
     assert k >= 1 and sl.emb_debug_live_allocations() == base
+
+
+def test_wait_that_runs_out_is_reported():
+    r = sl.scan_selftest_timeout()
+    assert r["status"] == 0 and r["latched"] == 8 and r["latched_after"] == 0, r
+    assert 0.0 < r["wait_ms"] < 60000.0, r
