@@ -237,6 +237,7 @@ struct ScanArgs {
   int64_t vecs;          // column vectors in all: batch * dim / V
   DivMagic32 per;        // by dim / V: a column vector's batch entry
   DivMagic32 groups;     // by the tiles across (chained calls)
+  DivMagic32 tile;       // by the positions of a tile
   const int32_t* offsets;
   uint32_t* status;
   ScanShared* shared;
@@ -627,13 +628,14 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
     const int t0 = k * p.TT + p.ty * R;
     fill(c, k, true);
     copies_done();
-    Lanes<V> a[R], na[R], xv[R], dy[R];   // xv: x, then the gate's factor of G
+    Lanes<V> a[R], na[R], xv[R];   // xv: x, then the gate's factor of G
+    Vec<T, V> dy[R];               // as it is stored: 16 bits take half the registers
     Lanes<V> fa = all_of<V>(1.f), fb = all_of<V>(0.f), fc = all_of<V>(0.f);
 #pragma unroll
     for (int r = 0; r < R; ++r) {
       gates(sg.at[r * kScanThreads], a[r], na[r]);
       xv[r] = widen(sx.at[r * kScanThreads]);
-      dy[r] = widen(sd.at[r * kScanThreads]);
+      dy[r] = sd.at[r * kScanThreads];
       fa = mul(fa, a[r]);
       if constexpr (RERUN) {
         fb = mad(a[r], fb, mul(na[r], xv[r]));
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       }
     }
 #pragma unroll
-    for (int r = R - 1; r >= 0; --r) fc = mul(a[r], add(dy[r], fc));
+    for (int r = R - 1; r >= 0; --r) fc = mul(a[r], add(widen(dy[r]), fc));
     // the next tile's inputs (as in the forward)
     int k1 = k - 1;
     int64_t gi1 = gi;
@@ -706,7 +708,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       }
       join_stretches<V>(p, sa, sc, true, f, ex, all);
       // the chain of a channel begins at the tile of its last position
-      const int last = q.n > 0 ? (q.n - 1) / p.TT : 0;
+      const int last = q.n > 0 ? (int)div_magic32((uint32_t)q.n - 1, s.tile) : 0;
       if constexpr (CHAIN) {
         const int i = live ? last - k : 0;
         const float state0 = live && i < kGroup && grad_out ? grad_out[q.col] : 0.f;
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
     Vec<T, V> ox[R], og[R];
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) {
-      const Lanes<V> G = add(dy[r], C);
+      const Lanes<V> G = add(widen(dy[r]), C);
       ox[r] = narrow<T>(mul(na[r], G));
       og[r] = narrow<T>(mul(xv[r], G));
       C = mul(a[r], G);
@@ -755,6 +757,99 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
     tile = next;
   }
   if (CHAIN && threadIdx.x == 0) leave(s);
+}
+
+// Short sequences, of at most U positions: a thread holds a whole column vector
+// in registers, so the backward runs forward from the first state and needs no
+// y.  The tiles above would leave most of their positions empty (20000 x 2 x
+// 75 fp16: 47 us forward).
+template <class T, int V, int U>
+__global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ ScanArgs s, View<const T> x,
+                                                        View<const T> g, View<T> y,
+                                                        const float* __restrict__ state_in,
+                                                        float* __restrict__ state_out) {
+  const Channel c = channel_of<V>(s, blockIdx.x * 128ll + threadIdx.x, 0);
+  if (!c.ok) return;
+  Vec<T, V> xr[U], gr[U];
+#pragma unroll
+  for (int t = 0; t < U; ++t)
+    if (t < c.n) {
+      xr[t] = get<V>(x.at(c.b, t, c.d), x.wide);
+      gr[t] = get<V>(g.at(c.b, t, c.d), g.wide);
+    }
+  Lanes<V> h = all_of<V>(0.f);
+  if (state_in) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) h.v[v] = state_in[c.col + v];
+  }
+#pragma unroll
+  for (int t = 0; t < U; ++t) {
+    Vec<T, V> o;
+    if (t < c.n) {
+      Lanes<V> a, na;
+      gates(gr[t], a, na);
+      h = mad(a, h, mul(na, widen(xr[t])));
+      o = narrow<T>(h);
+    } else {
+      o = narrow<T>(all_of<V>(0.f));
+    }
+    if (t < s.len) put<V>(y.at(c.b, t, c.d), y.wide, o);
+  }
+  if (state_out) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) state_out[c.col + v] = h.v[v];
+  }
+}
+
+template <class T, int V, int U>
+__global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ ScanArgs s, View<const T> x,
+                                                        View<const T> g, View<const T> gy,
+                                                        const float* __restrict__ state_in,
+                                                        const float* __restrict__ grad_out, View<T> gx, View<T> gg,
+                                                        float* __restrict__ grad_in) {
+  const Channel c = channel_of<V>(s, blockIdx.x * 128ll + threadIdx.x, 0);
+  if (!c.ok) return;
+  Vec<T, V> xr[U], gr[U], dr[U];
+#pragma unroll
+  for (int t = 0; t < U; ++t)
+    if (t < c.n) {
+      xr[t] = get<V>(x.at(c.b, t, c.d), x.wide);
+      gr[t] = get<V>(g.at(c.b, t, c.d), g.wide);
+      dr[t] = get<V>(gy.at(c.b, t, c.d), gy.wide);
+    }
+  Lanes<V> h = all_of<V>(0.f), C = all_of<V>(0.f);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    if (state_in) h.v[v] = state_in[c.col + v];
+    if (grad_out) C.v[v] = grad_out[c.col + v];
+  }
+  Lanes<V> a[U], na[U], w[U];   // w: the gate's factor of G
+#pragma unroll
+  for (int t = 0; t < U; ++t)
+    if (t < c.n) {
+      gates(gr[t], a[t], na[t]);
+      const Lanes<V> xv = widen(xr[t]);
+      w[t] = mul(mul(a[t], na[t]), sub(h, xv));
+      h = mad(a[t], h, mul(na[t], xv));
+    }
+#pragma unroll
+  for (int t = U - 1; t >= 0; --t) {
+    Vec<T, V> ox = narrow<T>(all_of<V>(0.f)), og = ox;
+    if (t < c.n) {
+      const Lanes<V> G = add(widen(dr[t]), C);
+      ox = narrow<T>(mul(na[t], G));
+      og = narrow<T>(mul(w[t], G));
+      C = mul(a[t], G);
+    }
+    if (t < s.len) {
+      put<V>(gx.at(c.b, t, c.d), gx.wide, ox);
+      put<V>(gg.at(c.b, t, c.d), gg.wide, og);
+    }
+  }
+  if (grad_in) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) grad_in[c.col + v] = C.v[v];
+  }
 }
 
 // One position per session: a thread takes V channels of one row.
@@ -809,21 +904,39 @@ struct Cut {
   ScanArgs args;
   bool chain;
   unsigned grid;
-  size_t smem;
 };
 
-constexpr int kWideV = 4, kFwdR = 8, kBwdR = 4;   // V = 1: twice the positions, for as many bytes in flight
-// log2 of the column vectors of a tile, for V = 4 and V = 1
-constexpr int kCx = 3, kCxOne = 5;
-int64_t chain_records(int64_t dim, int64_t batch, int64_t len, int V, int R) {
-  const int64_t cols = batch * dim;
-  const int TT = (kScanThreads >> (V == 1 ? kCxOne : kCx)) * R;
+// Positions of a thread, as many as its registers hold, for V = 4, 2 and 1
+// channels.  Fewer tiles wait for one another where there are more, so a
+// chained backward of 16-bit elements, whose gradients of y take half the
+// registers, has five (131072 x 512 bf16: 205 us, with four 226, with six 211);
+// walking, tiles of 160 positions fit sequences worse (1024 x 512 x 128 bf16:
+// 160 us with four, 169 with five).
+template <int V>
+constexpr int fwd_positions() { return V == 4 ? 8 : V == 2 ? 16 : 24; }
+template <class T, int V, bool CHAIN>
+constexpr int bwd_positions() {
+  if (V == 4) return sizeof(T) == 2 && CHAIN ? 5 : 4;
+  if (V == 2) return 8;
+  return sizeof(T) == 2 ? 16 : 8;
+}
+// log2 of the column vectors of a tile where sequences are long: 32 channels
+template <int V>
+constexpr int long_cx() { return V == 4 ? 3 : V == 2 ? 4 : 5; }
+
+int channels_at_once(int32_t dim) { return dim % 4 == 0 ? 4 : dim % 2 == 0 ? 2 : 1; }
+
+// Records of a chained call, for the smallest tiles that one has.
+int64_t chain_records(int V, int64_t cols, int64_t len) {
+  const int TT = V == 4 ? 32 * 4 : V == 2 ? 16 * 8 : 8 * 8;
   const int64_t tiles = (len + TT - 1) / TT;
   return (tiles + tiles / kGroup + 1) * cols;
 }
 
-Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int V, int R, int areas,
-             size_t staged) {
+// With fewer tiles across than CTAs that the GPU holds a call is chained,
+// otherwise it walks.  chain_r, walk_r: positions of a thread in either case.
+template <int V>
+Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int chain_r, int walk_r) {
   Cut c{};
   ScanArgs& a = c.args;
   a.batch = batch;
@@ -834,21 +947,29 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   a.status = h->status_d;
   a.shared = h->shared_d;
   a.records = h->records_d;
-  const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
-  const int least = V == 1 ? kCxOne : kCx;
-  // stretches that a sequence fills, rounded up to a power of two
-  int ty_log = 0;
-  while (ty_log < 8 && (R << ty_log) < len) ++ty_log;
-  a.cx_log = 8 - ty_log < least ? least : 8 - ty_log;
-  // fewer than four stretches, or four that would fill the GPU side by side: a thread walks alone
-  if (V == 4 && (a.cx_log > 6 || (a.cx_log == 6 && (a.vecs >> 8) >= h->sm_count))) a.cx_log = 8;
-  if (a.cx_log == least && R == 8 && ((a.vecs + (2 << least) - 1) >> (least + 1)) >= slots) ++a.cx_log;
-  const int64_t groups = (a.vecs + (1 << a.cx_log) - 1) >> a.cx_log;
-  const int TT = (kScanThreads >> a.cx_log) * R;
-  a.tiles = (len + TT - 1) / TT;
-  if (a.tiles < 1) a.tiles = 1;
-  c.chain = a.tiles > 1 && a.cx_log == least && groups < slots;
   a.per = make_div_magic32((uint32_t)(h->dim / V));
+  constexpr int kCx = long_cx<V>();
+  const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
+  const auto across = [&](int cx_log) { return (a.vecs + (1 << cx_log) - 1) >> cx_log; };
+  c.chain = across(kCx) < slots && (int64_t)len > (kScanThreads >> kCx) * chain_r;
+  const int R = c.chain ? chain_r : walk_r;
+  if (c.chain) {
+    a.cx_log = kCx;
+  } else {
+    // stretches that a sequence fills, rounded up to a power of two
+    int ty_log = 0;
+    while (ty_log < 8 - kCx && (R << ty_log) < len) ++ty_log;
+    a.cx_log = 8 - ty_log;
+    // fewer than V stretches, or V that would fill the GPU side by side: a thread walks alone
+    constexpr int kAlone = V == 4 ? 6 : V == 2 ? 7 : 8;
+    if (a.cx_log > kAlone || (a.cx_log == kAlone && (a.vecs >> 8) >= h->sm_count)) a.cx_log = 8;
+    // tiles of 128 positions rather than of 256 where both fill the GPU: less of the last one is past the end
+    if (V == 4 && a.cx_log == kCx && R == 8 && across(kCx + 1) >= slots) ++a.cx_log;
+  }
+  const int64_t groups = across(a.cx_log);
+  const int TT = (kScanThreads >> a.cx_log) * R;
+  a.tiles = len > TT ? (len + TT - 1) / TT : 1;
+  a.tile = make_div_magic32((uint32_t)TT);
   if (c.chain) {
     a.groups = make_div_magic32((uint32_t)groups);
     a.total = (uint32_t)(groups * a.tiles);
@@ -856,9 +977,51 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
     a.states = a.records + (int64_t)a.tiles * a.pitch;
   }
   const int64_t all = groups * a.tiles;
-  c.grid = (unsigned)(c.chain ? (all < slots ? all : slots) : groups);
-  c.smem = staged + (size_t)areas * (kScanThreads >> a.cx_log) * ((V << a.cx_log) + 1) * sizeof(float);
+  c.grid = (unsigned)(c.chain && all >= slots ? slots : c.chain ? all : groups);
   return c;
+}
+
+constexpr int kShort = 16;   // elements of a column vector that a thread holds whole
+unsigned short_grid(const Cut& c) { return (unsigned)((c.args.vecs + 127) / 128); }
+
+// `staged`: bytes of the inputs' copies; `areas`: shared arrays of the joins.
+template <int V, class K, class... A>
+cudaError_t launch(K kernel, const Cut& c, size_t staged, int areas, cudaStream_t stream, A... a) {
+  const size_t smem = staged + (size_t)areas * (kScanThreads >> c.args.cx_log) * ((V << c.args.cx_log) + 1) *
+                                   sizeof(float);
+  if (smem > 48 << 10) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  kernel<<<c.grid, kScanThreads, smem, stream>>>(c.args, a...);
+  return cudaGetLastError();
+}
+
+// All views wide, with the first one's strides: the kernels of this variant
+// have no other path.
+template <int V, class... W>
+bool all_wide(int size, const scan_view* first, const W*... w) {
+  const auto same = [&](const scan_view* v) {
+    return aligned_to(v->data, V * size) && v->batch_stride == first->batch_stride &&
+           v->time_stride == first->time_stride;
+  };
+  return first->batch_stride % V == 0 && first->time_stride % V == 0 && same(first) && (same(w) && ...);
+}
+
+// Calls f with the channels that a thread takes as a constant.
+template <class F>
+cudaError_t with_channels(int32_t dim, F f) {
+  switch (channels_at_once(dim)) {
+    case 4: return f(std::integral_constant<int, 4>());
+    case 2: return f(std::integral_constant<int, 2>());
+    default: return f(std::integral_constant<int, 1>());
+  }
+}
+// Calls f with two truth values as constants.
+template <class F>
+cudaError_t with_flags(bool a, bool b, F f) {
+  if (a) return b ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
+  return b ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
 }
 
 }  // namespace emb
@@ -879,13 +1042,9 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) {
-    const int64_t cols = (int64_t)h->sm_count * kCtasPerSm * (kWideV << (kCx + 1)) + dim;   // a call with more walks
-    const int64_t batch = (int64_t)max_batch * dim < cols ? max_batch : cols / dim + 1;
-    const int V = dim % kWideV ? 1 : kWideV;
-    for (int R : {kFwdR, kBwdR}) {
-      const int64_t n = chain_records(dim, batch, max_len, V, V == 1 ? 2 * R : R);
-      if (n > h->max_records) h->max_records = n;
-    }
+    // a call with more channels than this walks
+    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 + dim, all = (int64_t)max_batch * dim;
+    h->max_records = chain_records(channels_at_once(dim), all < most ? all : most, max_len);
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
   }
   if (e == cudaSuccess) e = dev_alloc((void**)&h->shared_d, sizeof(ScanShared));
@@ -925,40 +1084,6 @@ extern "C" emb_status scan_get_device_status(emb_scan h, void* stream) {
   return (emb_status)st;
 }
 
-template <class K>
-static cudaError_t allow_shared(K kernel) {
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 100 << 10);
-}
-
-// All views wide, with the first one's strides: the kernels of this variant
-// have no other path.
-template <int V, class... W>
-static bool all_wide(int size, const scan_view* first, const W*... w) {
-  const auto same = [&](const scan_view* v) {
-    return aligned_to(v->data, V * size) && v->batch_stride == first->batch_stride &&
-           v->time_stride == first->time_stride;
-  };
-  return first->batch_stride % V == 0 && first->time_stride % V == 0 && same(first) && (same(w) && ...);
-}
-
-template <class K, class... A>
-static cudaError_t launch(K kernel, const Cut& c, cudaStream_t stream, A... a) {
-  kernel<<<c.grid, kScanThreads, c.smem, stream>>>(c.args, a...);
-  return cudaGetLastError();
-}
-
-// Calls f with the kernel's variant as constants: V, WIDE.
-template <class T, class F, class... W>
-static cudaError_t with_variant(int32_t dim, F f, const W*... w) {
-  using std::integral_constant;
-  if (dim % kWideV) {
-    if (all_wide<1>(sizeof(T), w...)) return f(integral_constant<int, 1>(), std::true_type());
-    return f(integral_constant<int, 1>(), std::false_type());
-  }
-  if (all_wide<kWideV>(sizeof(T), w...)) return f(integral_constant<int, kWideV>(), std::true_type());
-  return f(integral_constant<int, kWideV>(), std::false_type());
-}
-
 extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
                                    const scan_view* gate, const int32_t* offsets, const float* state_in,
                                    const scan_view* y, float* state_out, void* stream) {
@@ -969,16 +1094,24 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
-    return with_variant<T>(h->dim, [&](auto v, auto wide) {
-      constexpr int V = decltype(v)::value, R = V == 1 ? 2 * kFwdR : kFwdR;
-      constexpr bool W = decltype(wide)::value;
-      static const cudaError_t room[2] = {allow_shared(k_scan_fwd<T, V, R, false, W>),
-                                          allow_shared(k_scan_fwd<T, V, R, true, W>)};
-      const Cut c = cut_call(h, batch, len, offsets, V, R, 2, 2 * R * kScanThreads * V * sizeof(T));
-      if (room[c.chain] != cudaSuccess) return room[c.chain];
-      return launch(c.chain ? k_scan_fwd<T, V, R, true, W> : k_scan_fwd<T, V, R, false, W>, c, (cudaStream_t)stream,
-                    as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
-    }, x, gate, y);
+    return with_channels(h->dim, [&](auto v) {
+      constexpr int V = decltype(v)::value, R = fwd_positions<V>();
+      const Cut c = cut_call<V>(h, batch, len, offsets, R, R);
+      constexpr int kMost = V == 4 ? 8 : kShort / V;   // twice kShort still fits: 30000 x 8 x 64 bf16 29 -> 19 us
+      if (len <= kMost) {
+        auto kernel = len <= 2           ? k_scan_short_fwd<T, V, 2>
+                      : len <= kShort / V ? k_scan_short_fwd<T, V, kShort / V>
+                                          : k_scan_short_fwd<T, V, kMost>;
+        kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
+                                                               as_view<T, V>(y), state_in, state_out);
+        return cudaGetLastError();
+      }
+      return with_flags(c.chain, all_wide<V>(sizeof(T), x, gate, y), [&](auto chain, auto wide) {
+        return launch<V>(k_scan_fwd<T, V, R, decltype(chain)::value, decltype(wide)::value>, c,
+                         2 * R * kScanThreads * V * sizeof(T), 2, (cudaStream_t)stream, as_view<const T, V>(x),
+                         as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
+      });
+    });
   }));
 }
 
@@ -996,19 +1129,26 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
-    return with_variant<T>(h->dim, [&](auto v, auto wide) {
-      constexpr int V = decltype(v)::value, R = V == 1 ? 2 * kBwdR : kBwdR;
-      constexpr bool W = decltype(wide)::value;
-      static const cudaError_t room[2] = {allow_shared(k_scan_bwd<T, V, R, false, W>),
-                                          allow_shared(k_scan_bwd<T, V, R, true, W>)};
-      const Cut c = cut_call(h, batch, len, offsets, V, R, 3,
-                             (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T));
-      if (room[c.chain] != cudaSuccess) return room[c.chain];
-      return launch(c.chain ? k_scan_bwd<T, V, R, true, W> : k_scan_bwd<T, V, R, false, W>, c, (cudaStream_t)stream,
-                    as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y),
-                    as_view<const T, V>(grad_y), state_in, grad_state_out, as_view<T, V>(grad_x),
-                    as_view<T, V>(grad_gate), grad_state_in);
-    }, x, gate, y, grad_y, grad_x, grad_gate);
+    return with_channels(h->dim, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      const Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
+      if (len <= kShort / V) {
+        auto kernel = len <= 2 ? k_scan_short_bwd<T, V, 2> : k_scan_short_bwd<T, V, kShort / V>;
+        kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(
+            c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(grad_y), state_in,
+            grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate), grad_state_in);
+        return cudaGetLastError();
+      }
+      const bool same = all_wide<V>(sizeof(T), x, gate, y, grad_y, grad_x, grad_gate);
+      return with_flags(c.chain, same, [&](auto chain, auto wide) {
+        constexpr int R = bwd_positions<T, V, decltype(chain)::value>();
+        return launch<V>(k_scan_bwd<T, V, R, decltype(chain)::value, decltype(wide)::value>, c,
+                         (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T), 3, (cudaStream_t)stream,
+                         as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y),
+                         as_view<const T, V>(grad_y), state_in, grad_state_out, as_view<T, V>(grad_x),
+                         as_view<T, V>(grad_gate), grad_state_in);
+      });
+    });
   }));
 }
 
@@ -1023,15 +1163,15 @@ extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const voi
       !aligned_to(y, size) || !aligned_to(states, 4) || !aligned_to(rows, 8) || (n > 1 && y_stride < dim))
     return EMB_ERR_INVALID_ARG;
   if (dim > 65536) return EMB_ERR_UNSUPPORTED;
-  const bool wide = dim % kWideV == 0 && x_stride % kWideV == 0 && gate_stride % kWideV == 0 &&
-                    y_stride % kWideV == 0 && aligned_to(x, kWideV * size) && aligned_to(gate, kWideV * size) &&
-                    aligned_to(y, kWideV * size) && aligned_to(states, kWideV * sizeof(float));
-  const int vecs = wide ? dim / kWideV : dim;
+  const bool wide = dim % 4 == 0 && x_stride % 4 == 0 && gate_stride % 4 == 0 &&
+                    y_stride % 4 == 0 && aligned_to(x, 4 * size) && aligned_to(gate, 4 * size) &&
+                    aligned_to(y, 4 * size) && aligned_to(states, 4 * sizeof(float));
+  const int vecs = wide ? dim / 4 : dim;
   const int64_t need = (n * vecs + 127) / 128;
   const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
   with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    auto kernel = wide ? k_scan_step<T, kWideV> : k_scan_step<T, 1>;
+    auto kernel = wide ? k_scan_step<T, 4> : k_scan_step<T, 1>;
     kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(n, make_div_magic((uint64_t)vecs), (const T*)x, x_stride,
                                                   (const T*)gate, gate_stride, rows, states, num_rows, (T*)y,
                                                   y_stride);
@@ -1042,7 +1182,7 @@ extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const voi
 // A sequence of two tiles of which only the second is handed out.
 extern "C" emb_status scan_selftest_timeout(uint32_t* latched, uint32_t* latched_after, float* wait_ms) {
   if (!latched || !latched_after) return EMB_ERR_INVALID_ARG;
-  constexpr int dim = 32, len = 2 * (kScanThreads >> kCx) * kFwdR;
+  constexpr int dim = 32, len = 2 * (kScanThreads >> long_cx<4>()) * fwd_positions<4>();
   emb_scan h = nullptr;
   emb_status st = scan_create(dim, 1, len, &h);
   if (st != EMB_OK) return st;

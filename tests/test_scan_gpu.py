@@ -422,3 +422,18 @@ def test_wait_that_runs_out_is_reported():
     r = sl.scan_selftest_timeout()
     assert r["status"] == 0 and r["latched"] == 8 and r["latched_after"] == 0, r
     assert 0.0 < r["wait_ms"] < 60000.0, r
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("D", [32, 30, 33])
+def test_every_short_length(D, dtype):
+    """Lengths around every change of kernel, widths of each access."""
+    for T in (1, 2, 3, 4, 5, 7, 8, 9, 15, 16, 17, 24, 25, 32, 33):
+        check(7, T, D, dtype, T)
+
+
+def test_even_and_odd_widths_in_long_sequences():
+    check(1, 9000, 34, "float32", 1)
+    check(2, 5000, 18, "float16", 2)
+    check(1, 7001, 35, "bfloat16", 3)
+    check(700, 130, 30, "bfloat16", 4)
