@@ -130,9 +130,11 @@ def moe_destroy(h):
 
 
 def adamw_create(tensors, flags):
-    arr = (AdamwTensor * max(1, len(tensors)))(*tensors)
+    """tensors: AdamwTensor structures, or a numpy array of their type."""
+    arr = tensors if hasattr(tensors, "ctypes") else (AdamwTensor * max(1, len(tensors)))(*tensors)
     h = c_void_p()
-    _check(lib().adamw_create(arr, len(tensors), flags, ctypes.byref(h)), "adamw_create")
+    at = ptr(arr) if hasattr(arr, "ctypes") else arr
+    _check(lib().adamw_create(at, len(tensors), flags, ctypes.byref(h)), "adamw_create")
     return h.value
 
 
@@ -205,14 +207,15 @@ class _Handle:
         except Exception:
             pass
 
-    def _empty(self, shape, dtype, device, stream):
-        """A tensor that belongs to the stream the kernel will run on."""
+    def _empty(self, shape, dtype, like, stream):
+        """A tensor beside `like` that belongs to the stream the kernel will
+        run on."""
         if stream is None:
-            return self._new(shape, dtype=dtype, device=device)
+            return self._new(shape, dtype=dtype, device=like.device)
         torch = self._t
-        s = torch.cuda.ExternalStream(stream, device=device) if isinstance(stream, int) else stream
+        s = torch.cuda.ExternalStream(stream, device=like.device) if isinstance(stream, int) else stream
         with torch.cuda.stream(s):
-            return torch.empty(shape, dtype=dtype, device=device)
+            return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 class GatedScan(_Handle):
@@ -267,9 +270,9 @@ class GatedScan(_Handle):
         code, dt, shape, dev, o, s, views = self._common(x, gate, offsets, state)
         ends = (shape[0], shape[2])
         if y is None:
-            y = self._empty(shape, dt, dev, stream)
+            y = self._empty(shape, dt, x, stream)
         if last is None:
-            last = self._empty(ends, self._f32, dev, stream)
+            last = self._empty(ends, self._f32, x, stream)
         self._views[0:9] = views + self._view(y, "y", shape, dt)
         v = self._view_at
         st = self._fwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2],
@@ -287,11 +290,11 @@ class GatedScan(_Handle):
         f32, ends = self._f32, (shape[0], shape[2])
         gl = None if grad_last is None else _want(grad_last, "grad_last", ends, f32)
         if grad_x is None:
-            grad_x = self._empty(shape, dt, dev, stream)
+            grad_x = self._empty(shape, dt, x, stream)
         if grad_gate is None:
-            grad_gate = self._empty(shape, dt, dev, stream)
+            grad_gate = self._empty(shape, dt, x, stream)
         if grad_state is None:
-            grad_state = self._empty(ends, f32, dev, stream)
+            grad_state = self._empty(ends, f32, x, stream)
         self._views[:] = (views + self._view(y, "y", shape, dt) + self._view(grad_y, "grad_y", shape, dt) +
                           self._view(grad_x, "grad_x", shape, dt) + self._view(grad_gate, "grad_gate", shape, dt))
         v = self._view_at
@@ -311,7 +314,7 @@ class GatedScan(_Handle):
             raise ValueError("x: [n, %d] and states [num_rows, %d] expected" % (D, D))
         n, pool, dev = shape[0], states.shape[0], x.device
         if y is None:
-            y = self._empty(shape, dt, dev, stream)
+            y = self._empty(shape, dt, x, stream)
         st = self._step(n, D, _element(dt), _want(x, "x", shape, dt, False), x.stride(0),
                         _want(gate, "gate", shape, dt, False), gate.stride(0),
                         _want(rows, "rows", (n,), self._t.int64), _want(states, "states", (pool, D), self._f32), pool,
@@ -361,8 +364,8 @@ class ExpertRouter(_Handle):
         n, dev = shape[0], experts.device
         pos = (n, self.top_k)
         e = _want(experts, "experts", pos, i32)
-        offsets, counts = self._empty((E + 1,), i32, dev, stream), self._empty((E,), i32, dev, stream)
-        pos, src = self._empty(pos, i32, dev, stream), self._empty((self.rows(n),), i32, dev, stream)
+        offsets, counts = self._empty((E + 1,), i32, experts, stream), self._empty((E,), i32, experts, stream)
+        pos, src = self._empty(pos, i32, experts, stream), self._empty((self.rows(n),), i32, experts, stream)
         st = self._route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), pos.data_ptr(), src.data_ptr(),
                          _stream(stream, dev.index))
         if st:
@@ -382,7 +385,7 @@ class ExpertRouter(_Handle):
         n, dim = shape
         pos, src, rows = self._routed(n, routing)
         if xs is None:
-            xs = self._empty((rows, dim), dt, dev, stream)
+            xs = self._empty((rows, dim), dt, x, stream)
             to = xs.data_ptr()
         else:
             to = _want(xs, "xs", (rows, dim), dt)
@@ -402,7 +405,7 @@ class ExpertRouter(_Handle):
         pos, _, rows = self._routed(n, routing)
         w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._f32)
         if y is None:
-            y = self._empty((n, dim), dt, dev, stream)
+            y = self._empty((n, dim), dt, ys, stream)
             to, stride = y.data_ptr(), dim
         else:
             to, stride = _want(y, "y", (n, dim), dt, False), y.stride(0)
@@ -423,10 +426,10 @@ class ExpertRouter(_Handle):
         wide, each = (rows, dim), (n, self.top_k)
         w = None if weights is None else _want(weights, "weights", each, f32)
         if weights is not None and grad_weights is None:
-            grad_weights = self._empty(each, f32, dev, stream)
+            grad_weights = self._empty(each, f32, weights, stream)
         gw = None if grad_weights is None else _want(grad_weights, "grad_weights", each, f32)
         if grad_ys is None:
-            grad_ys = self._empty(wide, dt, dev, stream)
+            grad_ys = self._empty(wide, dt, grad_y, stream)
         st = self._combine_backward(self.handle, n, dim, _element(dt), _want(grad_y, "grad_y", shape, dt, False),
                                     grad_y.stride(0), _want(ys, "ys", wide, dt), w, pos, src,
                                     _want(grad_ys, "grad_ys", wide, dt), gw, _stream(stream, dev.index))
@@ -465,42 +468,36 @@ class AdamW(_Handle):
         if len(self.grads) != n or len(self.masters) != n or len(decay) != n:
             raise ValueError("one gradient, master and weight decay per parameter")
         self.state_bits = state_bits
-        state = torch.float32 if state_bits == 32 else torch.uint8
-
-        def states(given, make, name, dtype, shape):
-            out = [make(p) for p in self.params] if given is None else list(given)
-            if len(out) != n:
-                raise ValueError("%s: one per parameter" % name)
-            for t, p in zip(out, self.params):
-                _want(t, name, shape(p), dtype)
-            return out
-        for given, name, dtype, shape in ((m, "m", state, lambda p: p.shape), (v, "v", state, lambda p: p.shape),
-                                          (m_top, "m_top", torch.int16, _blocks), (v_top, "v_top", torch.int16, _blocks)):
-            if name.endswith("_top") and state_bits == 32:
+        eight = state_bits == 8
+        state = torch.uint8 if eight else torch.float32
+        shapes = [p.shape for p in self.params]
+        blocks = [_blocks(p) for p in self.params] if eight else None
+        fields = {"param": [_want(p, "params", k, p.dtype) for p, k in zip(self.params, shapes)],
+                  "grad": [_want(g, "grads", k, p.dtype if g.dtype is p.dtype else torch.float32)
+                           for g, p, k in zip(self.grads, self.params, shapes)],
+                  "master": [0 if w is None else _want(w, "masters", k, torch.float32)
+                             for w, k in zip(self.masters, shapes)]}
+        for given, name, dtype, sizes in ((m, "m", state, shapes), (v, "v", state, shapes),
+                                          (m_top, "m_top", torch.int16, blocks), (v_top, "v_top", torch.int16, blocks)):
+            if sizes is None:
                 if given is not None:
                     raise ValueError("%s: 8-bit states only" % name)
                 setattr(self, name, None)
                 continue
-            setattr(self, name, states(given, lambda p: torch.zeros(shape(p), dtype=dtype, device=p.device), name,
-                                       dtype, shape))
-        descs = []
-        for i, p in enumerate(self.params):
-            code = _element(p.dtype)
-            _want(p, "params", p.shape, p.dtype)
-            g = self.grads[i]
-            self._grad(i, g)
-            if self.masters[i] is not None:
-                _want(self.masters[i], "masters", p.shape, torch.float32)
-            eight = state_bits == 8
-            descs.append(AdamwTensor(ptr(p), ptr(g), ptr(self.masters[i]), ptr(self.m[i]), ptr(self.v[i]),
-                                     ptr(self.m_top[i]) if eight else None, ptr(self.v_top[i]) if eight else None,
-                                     p.numel(), decay[i], code, _element(g.dtype), 0))
+            held = ([torch.zeros(k, dtype=dtype, device=p.device) for p, k in zip(self.params, sizes)]
+                    if given is None else list(given))
+            if len(held) != n:
+                raise ValueError("%s: one per parameter" % name)
+            fields[name] = [_want(t, name, k, dtype) for t, k in zip(held, sizes)]
+            setattr(self, name, held)
+        fields["numel"] = [p.numel() for p in self.params]
+        fields["weight_decay"] = decay
+        fields["dtype"] = [_element(p.dtype) for p in self.params]
+        fields["grad_dtype"] = [_element(g.dtype) for g in self.grads]
         self._grad_dtypes = [g.dtype for g in self.grads]
-        self.handle = adamw_create(descs, STATES_8BIT if state_bits == 8 else 0)
-
-    def _grad(self, i, g):
-        p = self.params[i]
-        return _want(g, "grads", p.shape, p.dtype if g.dtype == p.dtype else self._t.float32)
+        self.handle = adamw_create(_tensors(fields, n), STATES_8BIT if eight else 0)
+        self._device = self.params[0].device.index
+        self._step, self._size = lib().adamw_step, adamw_export_size(self.handle)
 
     def bind_grads(self, grads, stream=None):
         """Read other gradient tensors (same shapes and types) from the next
@@ -519,21 +516,32 @@ class AdamW(_Handle):
         if grad_scale is not None:
             if grad_scale.numel() != 1 or not grad_scale.is_cuda or grad_scale.dtype != self._t.float32:
                 raise ValueError("grad_scale: one float32 on the GPU")
-        adamw_step(self.handle, self.step_count + 1, lr, self.betas[0], self.betas[1], self.eps, grad_scale, self.seed,
-                   stream)
+        st = self._step(self.handle, self.step_count + 1, lr, self.betas[0], self.betas[1], self.eps,
+                        None if grad_scale is None else grad_scale.data_ptr(), self.seed,
+                        _stream(stream, self._device))
+        if st:
+            _check(st, "adamw_step")
         self.step_count += 1
 
     def states(self, stream=None):
         """What the 8-bit states stand for: (m, v), bfloat16 (exact), tensor
         after tensor, each from the next multiple of 256 elements on, zeros
         between them."""
-        n = adamw_export_size(self.handle)
-        dev, bf16 = self.params[0].device, self._t.bfloat16
-        m = self._empty((n,), bf16, dev, stream)
-        v = self._empty((n,), bf16, dev, stream)
-        adamw_export_states(self.handle, m, v, stream)
+        like, bf16 = self.params[0], self._t.bfloat16
+        m, v = self._empty((self._size,), bf16, like, stream), self._empty((self._size,), bf16, like, stream)
+        adamw_export_states(self.handle, m, v, _stream(stream, self._device))
         return m, v
 
 
 def _blocks(p):
     return ((p.numel() + BLOCK - 1) // BLOCK,)
+
+
+def _tensors(fields, n):
+    """adamw_tensor structures from lists of their fields (fast for thousands
+    of tensors)."""
+    import numpy as np
+    out = np.zeros(n, np.dtype(AdamwTensor))
+    for name, values in fields.items():
+        out[name] = values
+    return out
