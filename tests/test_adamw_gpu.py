@@ -5,6 +5,8 @@ bound of their own arithmetic: w' = w - lr d w - lr q, each product and
 difference one rounding (3 u |w| and 2 u lr |q| in all, u = 2^-24), and q, from
 an approximate root and quotient of a few ulp and four roundings, within 12 u;
 16-bit weights add half a unit of their type."""
+import gc
+
 import numpy as np
 import pytest
 
@@ -326,6 +328,7 @@ def test_refusals():
 def test_allocation_failure():
     import torch
     p, g = [torch.zeros(8, device="cuda")], [torch.zeros(8, device="cuda")]
+    gc.collect()   # handles of earlier tests are freed now, not in the middle of the count
     base = sl.emb_debug_live_allocations()
     for k in range(3):
         sl.emb_debug_fail_alloc(k)

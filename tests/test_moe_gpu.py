@@ -2,6 +2,8 @@
 Index results are exact.  Sums of n fp32 terms in any order are within
 n u sum|terms| (u = 2^-24, n counting the products' own roundings); stores of
 16 bits add half a unit."""
+import gc
+
 import numpy as np
 import pytest
 
@@ -277,6 +279,7 @@ def test_refusals():
 
 
 def test_allocation_failure():
+    gc.collect()   # handles of earlier tests are freed now, not in the middle of the count
     base = sl.emb_debug_live_allocations()
     sl.emb_debug_fail_alloc(0)
     with pytest.raises(sl.EmbError) as e:

@@ -11,6 +11,8 @@ scan may join stretches of a sequence in another order, which costs each
 product of gates at most its own errors once more on either side: factor 3.
 Stores of 16 bits add half a unit (2^-8 or 2^-11 of the value, and half the
 smallest fp16), and the backward may read such a stored state."""
+import gc
+
 import numpy as np
 import pytest
 
@@ -404,6 +406,7 @@ def test_refusals():
 
 
 def test_allocation_failure():
+    gc.collect()   # handles of earlier tests are freed now, not in the middle of the count
     base = sl.emb_debug_live_allocations()
     for k in range(20):
         sl.emb_debug_fail_alloc(k)
