@@ -902,7 +902,7 @@ bool call_ok(emb_scan h, int32_t batch, int32_t len, int32_t dtype) {
 // How a call is cut.  R: positions of a thread.
 struct Cut {
   ScanArgs args;
-  bool chain;
+  bool chain, fits;
   unsigned grid;
 };
 
@@ -926,9 +926,16 @@ constexpr int long_cx() { return V == 4 ? 3 : V == 2 ? 4 : 5; }
 
 int channels_at_once(int32_t dim) { return dim % 4 == 0 ? 4 : dim % 2 == 0 ? 2 : 1; }
 
-// Records of a chained call, for the smallest tiles that one has.
-int64_t chain_records(int V, int64_t cols, int64_t len) {
-  const int TT = V == 4 ? 32 * 4 : V == 2 ? 16 * 8 : 8 * 8;
+// Positions of the smallest tile that a chained call has, forward or backward,
+// and the records of one whose tiles have TT positions: one of each tile, one
+// of each group of tiles, for every channel.
+template <int V>
+constexpr int least_tile() {
+  constexpr int f = fwd_positions<V>(), b4 = bwd_positions<float, V, true>(), b2 = bwd_positions<__half, V, true>();
+  constexpr int b = b4 < b2 ? b4 : b2;
+  return (kScanThreads >> long_cx<V>()) * (f < b ? f : b);
+}
+int64_t chain_records(int TT, int64_t cols, int64_t len) {
   const int64_t tiles = (len + TT - 1) / TT;
   return (tiles + tiles / kGroup + 1) * cols;
 }
@@ -976,6 +983,8 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
     a.pitch = (uint32_t)(batch * h->dim);
     a.states = a.records + (int64_t)a.tiles * a.pitch;
   }
+  // the records were sized for this call when the handle was made; a cut that does not fit them is not launched
+  c.fits = !c.chain || chain_records(TT, a.pitch, len) <= h->max_records;
   const int64_t all = groups * a.tiles;
   c.grid = (unsigned)(c.chain && all >= slots ? slots : c.chain ? all : groups);
   return c;
@@ -987,6 +996,7 @@ unsigned short_grid(const Cut& c) { return (unsigned)((c.args.vecs + 127) / 128)
 // `staged`: bytes of the inputs' copies; `areas`: shared arrays of the joins.
 template <int V, class K, class... A>
 cudaError_t launch(K kernel, const Cut& c, size_t staged, int areas, cudaStream_t stream, A... a) {
+  if (!c.fits) return cudaErrorNotSupported;
   const size_t smem = staged + (size_t)areas * (kScanThreads >> c.args.cx_log) * ((V << c.args.cx_log) + 1) *
                                    sizeof(float);
   if (smem > 48 << 10) {
@@ -1044,7 +1054,8 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   if (e == cudaSuccess) {
     // a call with more channels than this walks
     const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 + dim, all = (int64_t)max_batch * dim;
-    h->max_records = chain_records(channels_at_once(dim), all < most ? all : most, max_len);
+    const int V = channels_at_once(dim), TT = V == 4 ? least_tile<4>() : V == 2 ? least_tile<2>() : least_tile<1>();
+    h->max_records = chain_records(TT, all < most ? all : most, max_len);
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
   }
   if (e == cudaSuccess) e = dev_alloc((void**)&h->shared_d, sizeof(ScanShared));

@@ -12,7 +12,6 @@ from __future__ import annotations
 
 import ctypes
 from ctypes import c_float, c_int32, c_int64, c_void_p
-from typing import NamedTuple
 
 from . import TABLE_DTYPE, _check, lib, ptr
 
@@ -327,12 +326,30 @@ class GatedScan(_Handle):
         return scan_get_device_status(self.handle, stream)
 
 
-class Routing(NamedTuple):
-    """The order of a batch's choices by expert (moe_route of emb.h)."""
-    offsets: object      # [experts + 1] int32: first row of each expert's segment
-    counts: object       # [experts] int32: live rows of each segment
-    pos: object          # [tokens, top_k] int32: row of each choice, -1 where dropped
-    src: object          # [rows] int32: flat choice of each row, -1 for padding
+class Routing:
+    """The order of a batch's choices by expert (moe_route of emb.h):
+    offsets  [experts + 1] int32: first row of each expert's segment
+    counts   [experts] int32: live rows of each segment
+    pos      [tokens, top_k] int32: row of each choice, -1 where dropped
+    src      [rows] int32: flat choice of each row, -1 for padding"""
+
+    __slots__ = ("offsets", "counts", "pos", "src", "_at", "_shape")
+
+    def __init__(self, offsets, counts, pos, src):
+        import torch
+        for t, name in ((offsets, "offsets"), (counts, "counts"), (pos, "pos"), (src, "src")):
+            _want(t, name, t.shape, torch.int32)
+        self.offsets, self.counts, self.pos, self.src = offsets, counts, pos, src
+        self._at, self._shape = (pos.data_ptr(), src.data_ptr()), (*pos.shape, src.numel())
+
+    def __iter__(self):
+        return iter((self.offsets, self.counts, self.pos, self.src))
+
+    @classmethod
+    def _made(cls, offsets, counts, pos, src, at, shape):
+        r = cls.__new__(cls)
+        r.offsets, r.counts, r.pos, r.src, r._at, r._shape = offsets, counts, pos, src, at, shape
+        return r
 
 
 class ExpertRouter(_Handle):
@@ -364,18 +381,22 @@ class ExpertRouter(_Handle):
         n, dev = shape[0], experts.device
         pos = (n, self.top_k)
         e = _want(experts, "experts", pos, i32)
+        rows = self.rows(n)
         offsets, counts = self._empty((E + 1,), i32, experts, stream), self._empty((E,), i32, experts, stream)
-        pos, src = self._empty(pos, i32, experts, stream), self._empty((self.rows(n),), i32, experts, stream)
-        st = self._route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), pos.data_ptr(), src.data_ptr(),
+        pos, src = self._empty(pos, i32, experts, stream), self._empty((rows,), i32, experts, stream)
+        at = (pos.data_ptr(), src.data_ptr())
+        st = self._route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), at[0], at[1],
                          _stream(stream, dev.index))
         if st:
             _check(st, "moe_route")
-        return Routing(offsets, counts, pos, src)
+        return Routing._made(offsets, counts, pos, src, at, (n, self.top_k, rows))
 
     def _routed(self, n, r):
         """(pointer of pos, pointer of src, rows) of a routing of n tokens."""
-        i32, rows = self._i32, self.rows(n)
-        return _want(r.pos, "pos", (n, self.top_k), i32), _want(r.src, "src", (rows,), i32), rows
+        m, k, rows = r._shape
+        if m != n or k != self.top_k or rows != self.rows(n):
+            raise ValueError("routing: of %d tokens by %d and %d rows, for %d tokens" % (m, k, rows, n))
+        return r._at[0], r._at[1], rows
 
     def dispatch(self, x, routing, xs=None, stream=None):
         """xs [rows, dim]: the token of each row; padding rows are 0."""
@@ -401,7 +422,7 @@ class ExpertRouter(_Handle):
         shape, dt, dev = ys.shape, ys.dtype, ys.device
         if len(shape) != 2:
             raise ValueError("ys: [rows, dim] expected, got %s" % (tuple(shape),))
-        n, dim = routing.pos.shape[0], shape[1]
+        n, dim = routing._shape[0], shape[1]
         pos, _, rows = self._routed(n, routing)
         w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._f32)
         if y is None:
