@@ -435,7 +435,9 @@ emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_len, emb_scan
  *  state_in  [batch, dim] fp32 h before the first position; NULL = 0
  *  y         (host struct) h_t in `dtype`
  *  state_out NULL, or [batch, dim] fp32: h after the last live position
- * The state between positions is fp32 throughout. */
+ * The state between positions is fp32 throughout.  Positions are joined in
+ * stretches: an infinite input or state makes the later states of its channel
+ * infinite or NaN. */
 emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
                         const scan_view* gate, const int32_t* offsets, const float* state_in, const scan_view* y,
                         float* state_out, void* stream);
@@ -516,7 +518,7 @@ emb_status moe_destroy(emb_moe h);
 typedef struct emb_adamw_s* emb_adamw;
 
 /* One parameter tensor of an AdamW handle.  Everything is caller-owned and
- * must outlive the handle. */
+ * must outlive the handle; no two arrays of a handle may overlap. */
 typedef struct {
     void* param;          /* [numel] of dtype                                      */
     const void* grad;     /* [numel] of dtype, or fp32 (grad_dtype)                */

@@ -994,15 +994,15 @@ constexpr int kShort = 16;   // elements of a column vector that a thread holds 
 unsigned short_grid(const Cut& c) { return (unsigned)((c.args.vecs + 127) / 128); }
 
 // `staged`: bytes of the inputs' copies; `areas`: shared arrays of the joins.
-template <int V, class K, class... A>
-cudaError_t launch(K kernel, const Cut& c, size_t staged, int areas, cudaStream_t stream, A... a) {
-  if (!c.fits) return cudaErrorNotSupported;
+template <int V, auto kernel, class... A>
+cudaError_t launch(const Cut& c, size_t staged, int areas, cudaStream_t stream, A... a) {
+  constexpr int kMostShared = 100 << 10;   // of each of the CTAs that share an SM
+  static const cudaError_t room =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
   const size_t smem = staged + (size_t)areas * (kScanThreads >> c.args.cx_log) * ((V << c.args.cx_log) + 1) *
                                    sizeof(float);
-  if (smem > 48 << 10) {
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-  }
+  if (room != cudaSuccess) return room;
+  if (!c.fits || smem > kMostShared) return cudaErrorNotSupported;
   kernel<<<c.grid, kScanThreads, smem, stream>>>(c.args, a...);
   return cudaGetLastError();
 }
@@ -1118,9 +1118,9 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
         return cudaGetLastError();
       }
       return with_flags(c.chain, all_wide<V>(sizeof(T), x, gate, y), [&](auto chain, auto wide) {
-        return launch<V>(k_scan_fwd<T, V, R, decltype(chain)::value, decltype(wide)::value>, c,
-                         2 * R * kScanThreads * V * sizeof(T), 2, (cudaStream_t)stream, as_view<const T, V>(x),
-                         as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
+        return launch<V, k_scan_fwd<T, V, R, decltype(chain)::value, decltype(wide)::value>>(
+            c, 2 * R * kScanThreads * V * sizeof(T), 2, (cudaStream_t)stream, as_view<const T, V>(x),
+            as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
       });
     });
   }));
@@ -1153,11 +1153,10 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
       const bool same = all_wide<V>(sizeof(T), x, gate, y, grad_y, grad_x, grad_gate);
       return with_flags(c.chain, same, [&](auto chain, auto wide) {
         constexpr int R = bwd_positions<T, V, decltype(chain)::value>();
-        return launch<V>(k_scan_bwd<T, V, R, decltype(chain)::value, decltype(wide)::value>, c,
-                         (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T), 3, (cudaStream_t)stream,
-                         as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y),
-                         as_view<const T, V>(grad_y), state_in, grad_state_out, as_view<T, V>(grad_x),
-                         as_view<T, V>(grad_gate), grad_state_in);
+        return launch<V, k_scan_bwd<T, V, R, decltype(chain)::value, decltype(wide)::value>>(
+            c, (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T), 3, (cudaStream_t)stream,
+            as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y), as_view<const T, V>(grad_y),
+            state_in, grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate), grad_state_in);
       });
     });
   }));
