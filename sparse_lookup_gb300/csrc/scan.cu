@@ -30,8 +30,7 @@ namespace emb {
 
 constexpr int kScanThreads = 256;
 constexpr unsigned kScanSpins = 1u << 21;   // rounds a wait takes at most (about a second)
-constexpr int kGroup = 16;                  // tiles of a chain's group
-constexpr int kAhead = 2;                   // records of a group that one lane reads
+constexpr int kJoin = 8;                    // lanes of a channel in a chained call
 constexpr int kCtasPerSm = 2;
 
 // V channels of a thread.  Pairs go through the packed fp32 instructions: the
@@ -244,6 +243,7 @@ struct ScanArgs {
   ulonglong2* records;   // [tiles][pitch] (chained calls)
   ulonglong2* states;    // [groups of tiles + 1][pitch]
   uint32_t pitch;        // channels in all: a chained call has few
+  int32_t group_log;     // log2 of the tiles of a chain's group
 };
 
 __device__ __forceinline__ int live_len(const ScanArgs& s, int b) {
@@ -275,60 +275,61 @@ __device__ __forceinline__ uint32_t get_record(const ulonglong2* p, Affine& f) {
   return tx == ty ? tx : 0u;
 }
 // The state before tile `i` of one channel's chain.  The chain is cut into
-// groups of kGroup tiles.  A tile writes its own effect for the later tiles of
-// its group, and a group's last tile the state after the group; a tile joins
-// the effects ahead of it in its group, read at once by the channel's J =
-// kGroup / kAhead lanes, behind the state before the group.  Along a sequence
-// only the groups wait for one another in turn (one write and read in L2 per
-// kGroup tiles), and the order of every join is fixed: results repeat bit for
-// bit.  `all`: what this tile does; `next`: a later tile needs to know; state0:
-// the state before tile 0.  All lanes of the warp call; the arguments are
-// uniform over a channel's lanes.
+// groups of tiles.  A tile writes its own effect for the later tiles of its
+// group, and a group's last tile the state after the group; a tile joins the
+// effects ahead of it in its group, which the channel's kJoin lanes read, behind
+// the state before the group.  Along a sequence only the groups wait for one
+// another in turn (one write and read in L2 per group), and the order of every
+// join is fixed: results repeat bit for bit.  `all`: what this tile does;
+// `next`: a later tile needs to know; state0: the state before tile 0.  All
+// lanes of the warp call; the arguments are uniform over a channel's lanes.
 __device__ __forceinline__ float chain_state(const ScanArgs& s, int64_t col, int i, bool want, bool next, Affine all,
                                              float state0, uint32_t epoch) {
-  constexpr int J = kGroup / kAhead;
   const auto row = [&](uint32_t r) { return (uint64_t)r * s.pitch; };
-  const int j = threadIdx.x & (J - 1), m = i / kGroup, at = i % kGroup;
-  ulonglong2* own = s.records + (row(m * kGroup) + col);   // the group's first tile
+  const int each_log = s.group_log - 3, last = (1 << s.group_log) - 1;   // a lane's records
+  const int j = threadIdx.x & (kJoin - 1), m = i >> s.group_log, at = i & last, first = j << each_log;
+  ulonglong2* own = s.records + (row(i - at) + col);   // the group's first tile
   ulonglong2* states = s.states + (row(m) + col);
-  if (want && next && j == 0 && at != kGroup - 1) put_record(own + row(at), all, epoch);
-  own += row(j * kAhead);
-  Affine f[kAhead], st{0.f, state0};
-  bool have[kAhead], have_state = !want || m == 0 || j != 0;
-#pragma unroll
-  for (int u = 0; u < kAhead; ++u) {
-    f[u] = {1.f, 0.f};
-    have[u] = !want || j * kAhead + u >= at;
-  }
-  for (unsigned spins = 0;; ++spins) {
-    bool all_here = true;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u)
-      if (!have[u]) have[u] = get_record(own + row(u), f[u]) == epoch;
-    if (!have_state) have_state = get_record(states, st) == epoch;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) all_here = all_here && have[u];
-    if (__all_sync(kFull, all_here && have_state)) break;
-    if (spins >= kScanSpins) {
-      latch(s.status, EMB_ERR_TIMEOUT);
-      *(volatile uint32_t*)&s.shared->fail = 1u;
-      break;
+  if (want && next && j == 0 && at != last) put_record(own + row(at), all, epoch);
+  own += row(first);
+  Affine sum{1.f, 0.f}, st{0.f, state0};
+  bool have_state = !want || m == 0 || j != 0;
+  unsigned spins = 0;
+  for (int u = 0;; ++u) {
+    bool have = !want || first + u >= at;
+    Affine f{1.f, 0.f};
+    const bool ends = (u + 1) >> each_log != 0;
+    for (;; ++spins) {
+      if (!have) have = get_record(own, f) == epoch;
+      if (!have_state) have_state = get_record(states, st) == epoch;
+      if (__all_sync(kFull, have && (have_state || !ends))) break;
+      if (spins >= kScanSpins) {
+        latch(s.status, EMB_ERR_TIMEOUT);
+        *(volatile uint32_t*)&s.shared->fail = 1u;
+        break;
+      }
+      if ((spins & 255u) == 255u && __any_sync(kFull, *(volatile uint32_t*)&s.shared->fail != 0u)) spins = kScanSpins;
     }
-    if ((spins & 255u) == 255u && __any_sync(kFull, *(volatile uint32_t*)&s.shared->fail != 0u)) break;
+    sum = after(f, sum);
+    own += s.pitch;
+    if (ends) break;
   }
-  Affine sum = f[0];
 #pragma unroll
-  for (int u = 1; u < kAhead; ++u) sum = after(f[u], sum);
-#pragma unroll
-  for (int o = 1; o < J; o <<= 1) {
-    const Affine e{__shfl_down_sync(kFull, sum.a, o, J), __shfl_down_sync(kFull, sum.b, o, J)};
+  for (int o = 1; o < kJoin; o <<= 1) {
+    const Affine e{__shfl_down_sync(kFull, sum.a, o, kJoin), __shfl_down_sync(kFull, sum.b, o, kJoin)};
     sum = after(e, sum);   // the upper lanes' sums are not used
   }
-  const float h = __shfl_sync(kFull, fmaf(sum.a, st.b, sum.b), 0, J);
-  if (want && next && j == 0 && at == kGroup - 1)
-    put_record(states + s.pitch, {0.f, fmaf(all.a, h, all.b)}, epoch);
+  const float h = __shfl_sync(kFull, fmaf(sum.a, st.b, sum.b), 0, kJoin);
+  if (want && next && j == 0 && at == last) put_record(states + s.pitch, {0.f, fmaf(all.a, h, all.b)}, epoch);
   return h;
 }
+// Small groups wait for fewer tiles, large ones for fewer groups in turn; with
+// few channels the turns bound the call.  us forward with groups of 8, 16 and
+// 32: 4 x 32768 x 512 bf16 (64 tiles across) 105, 113, 128; 65536 x 320 bf16
+// (10) 46, 47, 52; 65536 x 128 fp32 (4) 36, 32, 33; 131072 x 16 bf16 (1) 39,
+// 24, 19.
+constexpr int kLeastGroup = 8;
+constexpr int group_log(int64_t across) { return across >= 8 ? 3 : across >= 3 ? 4 : 5; }
 
 // A CTA's place: its threads as column vectors by stretches of R positions,
 // and again as channels by J lanes, for joining the stretches.
@@ -548,7 +549,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
       const int end = (k + 1) * p.TT;
       const bool live = q.ok && (k * p.TT < q.n || k == 0);
       if constexpr (CHAIN) {
-        const float state0 = live && k < kGroup && state_in ? state_in[q.col] : 0.f;
+        const float state0 = live && k >> s.group_log == 0 && state_in ? state_in[q.col] : 0.f;
         held = chain_state(s, q.col, k, live, end < q.n, all, state0, epoch);
       } else if (k == 0) {
         held = state_in && q.ok ? state_in[q.col] : 0.f;
@@ -711,7 +712,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       const int last = q.n > 0 ? (int)div_magic32((uint32_t)q.n - 1, s.tile) : 0;
       if constexpr (CHAIN) {
         const int i = live ? last - k : 0;
-        const float state0 = live && i < kGroup && grad_out ? grad_out[q.col] : 0.f;
+        const float state0 = live && i >> s.group_log == 0 && grad_out ? grad_out[q.col] : 0.f;
         held = chain_state(s, q.col, i, live, k > 0, all, state0, epoch);
       } else if (k == last) {
         held = grad_out && q.ok ? grad_out[q.col] : 0.f;
@@ -921,6 +922,7 @@ constexpr int bwd_positions() {
   return sizeof(T) == 2 ? 16 : 8;
 }
 // log2 of the column vectors of a tile where sequences are long: 32 channels
+// (chained with 16: 131072 x 512 bf16 138 us forward against 122; with 64: 127)
 template <int V>
 constexpr int long_cx() { return V == 4 ? 3 : V == 2 ? 4 : 5; }
 
@@ -937,11 +939,13 @@ constexpr int least_tile() {
 }
 int64_t chain_records(int TT, int64_t cols, int64_t len) {
   const int64_t tiles = (len + TT - 1) / TT;
-  return (tiles + tiles / kGroup + 1) * cols;
+  return (tiles + tiles / kLeastGroup + 1) * cols;
 }
 
-// With fewer tiles across than CTAs that the GPU holds a call is chained,
-// otherwise it walks.  chain_r, walk_r: positions of a thread in either case.
+// A call whose last round of walking CTAs would leave more than a quarter of
+// the GPU idle is chained, else it walks (us forward, walking and chained, on
+// 304 places: 176 tiles across, 11 x 8192 x 512 bf16, 94 and 74; 256 tiles 97
+// and 107; 320 tiles 147 and 127; fp32 backward of 256 tiles 209 and 263).  chain_r, walk_r: positions of a thread in either case.
 template <int V>
 Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int chain_r, int walk_r) {
   Cut c{};
@@ -956,9 +960,11 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   a.records = h->records_d;
   a.per = make_div_magic32((uint32_t)(h->dim / V));
   constexpr int kCx = long_cx<V>();
+  static_assert((kScanThreads / V >> kCx) == kJoin, "the lanes of a channel read its group's records");
   const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
   const auto across = [&](int cx_log) { return (a.vecs + (1 << cx_log) - 1) >> cx_log; };
-  c.chain = across(kCx) < slots && (int64_t)len > (kScanThreads >> kCx) * chain_r;
+  const int64_t rounds = (across(kCx) + slots - 1) / slots;
+  c.chain = across(kCx) * 4 < rounds * slots * 3 && (int64_t)len > (kScanThreads >> kCx) * chain_r;
   const int R = c.chain ? chain_r : walk_r;
   if (c.chain) {
     a.cx_log = kCx;
@@ -981,6 +987,7 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
     a.groups = make_div_magic32((uint32_t)groups);
     a.total = (uint32_t)(groups * a.tiles);
     a.pitch = (uint32_t)(batch * h->dim);
+    a.group_log = group_log(groups);
     a.states = a.records + (int64_t)a.tiles * a.pitch;
   }
   // the records were sized for this call when the handle was made; a cut that does not fit them is not launched
@@ -1053,7 +1060,7 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) {
     // a call with more channels than this walks
-    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 + dim, all = (int64_t)max_batch * dim;
+    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 * 3 + dim, all = (int64_t)max_batch * dim;
     const int V = channels_at_once(dim), TT = V == 4 ? least_tile<4>() : V == 2 ? least_tile<2>() : least_tile<1>();
     h->max_records = chain_records(TT, all < most ? all : most, max_len);
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));

@@ -440,3 +440,28 @@ def test_even_and_odd_widths_in_long_sequences():
     check(2, 5000, 18, "float16", 2)
     check(1, 7001, 35, "bfloat16", 3)
     check(700, 130, 30, "bfloat16", 4)
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("B,T,D", [(1, 30000, 16), (1, 20000, 30), (1, 20000, 15), (1, 12000, 96), (2, 9000, 256),
+                                   (41, 600, 256)])
+def test_chains_of_few_and_of_many_tiles_across(B, T, D, dtype):
+    check(B, T, D, dtype, B + T + D)
+
+
+def test_one_handle_for_chains_of_other_shapes():
+    """The records of one call lie where another call's groups begin."""
+    import torch
+    plan = sl.GatedScan(32, max_batch=12, max_len=12000)
+    for B, T in [(12, 12000), (1, 12000), (4, 5000), (1, 700), (12, 12000), (2, 11999)]:
+        x, g, gy, h0, gl, lens, off = make(B, T, 32, "float32", B + T)
+        y, last = plan.forward(x, g, off, h0)
+        got = (y, last) + plan.backward(x, g, y, gy, off, h0, gl)
+        other = sl.GatedScan(32, max_batch=B, max_len=T)
+        y, last = other.forward(x, g, off, h0)
+        want = (y, last) + other.backward(x, g, y, gy, off, h0, gl)
+        for p, q in zip(got, want):
+            assert torch.equal(p, q)
+        other.close()
+    assert plan.device_status() == 0
+    plan.close()
