@@ -333,22 +333,28 @@ class Routing:
     pos      [tokens, top_k] int32: row of each choice, -1 where dropped
     src      [rows] int32: flat choice of each row, -1 for padding"""
 
-    __slots__ = ("offsets", "counts", "pos", "src", "_at", "_shape")
+    __slots__ = ("_arrays", "_at", "_shape")
 
     def __init__(self, offsets, counts, pos, src):
         import torch
         for t, name in ((offsets, "offsets"), (counts, "counts"), (pos, "pos"), (src, "src")):
             _want(t, name, t.shape, torch.int32)
-        self.offsets, self.counts, self.pos, self.src = offsets, counts, pos, src
+        self._arrays = (offsets, counts, pos, src)
         self._at, self._shape = (pos.data_ptr(), src.data_ptr()), (*pos.shape, src.numel())
 
     def __iter__(self):
-        return iter((self.offsets, self.counts, self.pos, self.src))
+        return iter(self._arrays)
+
+    # not to be replaced: the calls use the addresses found when it was made
+    offsets = property(lambda self: self._arrays[0])
+    counts = property(lambda self: self._arrays[1])
+    pos = property(lambda self: self._arrays[2])
+    src = property(lambda self: self._arrays[3])
 
     @classmethod
     def _made(cls, offsets, counts, pos, src, at, shape):
         r = cls.__new__(cls)
-        r.offsets, r.counts, r.pos, r.src, r._at, r._shape = offsets, counts, pos, src, at, shape
+        r._arrays, r._at, r._shape = (offsets, counts, pos, src), at, shape
         return r
 
 
