@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
 // in registers, so the backward runs forward from the first state and needs no
 // y.  The tiles above would leave most of their positions empty (20000 x 2 x
 // 75 fp16: 47 us forward).
-template <class T, int V, int U>
+template <class T, int V, int U, bool WIDE>
 __global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ ScanArgs s, View<const T> x,
                                                         View<const T> g, View<T> y,
                                                         const float* __restrict__ state_in,
@@ -781,19 +781,22 @@ __global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ 
   const Channel c = channel_of<V>(s, blockIdx.x * 128ll + threadIdx.x, 0);
   if (!c.ok) return;
   Vec<T, V> xr[U], gr[U];
+  const Start<WIDE> at(x, c.b, c.d, 0);
+  const T *px = at.of(x), *pg = at.of(g);
 #pragma unroll
-  for (int t = 0; t < U; ++t)
+  for (int t = 0; t < U; ++t, px += x.ts, pg += g.ts)
     if (t < c.n) {
-      xr[t] = get<V>(x.at(c.b, t, c.d), x.wide);
-      gr[t] = get<V>(g.at(c.b, t, c.d), g.wide);
+      xr[t] = get<V>(px, WIDE || x.wide);
+      gr[t] = get<V>(pg, WIDE || g.wide);
     }
   Lanes<V> h = all_of<V>(0.f);
   if (state_in) {
 #pragma unroll
     for (int v = 0; v < V; ++v) h.v[v] = state_in[c.col + v];
   }
+  T* py = at.of(y);
 #pragma unroll
-  for (int t = 0; t < U; ++t) {
+  for (int t = 0; t < U; ++t, py += y.ts) {
     Vec<T, V> o;
     if (t < c.n) {
       Lanes<V> a, na;
@@ -803,7 +806,7 @@ __global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ 
     } else {
       o = narrow<T>(all_of<V>(0.f));
     }
-    if (t < s.len) put<V>(y.at(c.b, t, c.d), y.wide, o);
+    if (t < s.len) put<V>(py, WIDE || y.wide, o);
   }
   if (state_out) {
 #pragma unroll
@@ -811,7 +814,7 @@ __global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ 
   }
 }
 
-template <class T, int V, int U>
+template <class T, int V, int U, bool WIDE>
 __global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ ScanArgs s, View<const T> x,
                                                         View<const T> g, View<const T> gy,
                                                         const float* __restrict__ state_in,
@@ -820,12 +823,14 @@ __global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ 
   const Channel c = channel_of<V>(s, blockIdx.x * 128ll + threadIdx.x, 0);
   if (!c.ok) return;
   Vec<T, V> xr[U], gr[U], dr[U];
+  const Start<WIDE> at(x, c.b, c.d, 0);
+  const T *px = at.of(x), *pg = at.of(g), *pd = at.of(gy);
 #pragma unroll
-  for (int t = 0; t < U; ++t)
+  for (int t = 0; t < U; ++t, px += x.ts, pg += g.ts, pd += gy.ts)
     if (t < c.n) {
-      xr[t] = get<V>(x.at(c.b, t, c.d), x.wide);
-      gr[t] = get<V>(g.at(c.b, t, c.d), g.wide);
-      dr[t] = get<V>(gy.at(c.b, t, c.d), gy.wide);
+      xr[t] = get<V>(px, WIDE || x.wide);
+      gr[t] = get<V>(pg, WIDE || g.wide);
+      dr[t] = get<V>(pd, WIDE || gy.wide);
     }
   Lanes<V> h = all_of<V>(0.f), C = all_of<V>(0.f);
 #pragma unroll
@@ -842,8 +847,9 @@ __global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ 
       w[t] = mul(mul(a[t], na[t]), sub(h, xv));
       h = mad(a[t], h, mul(na[t], xv));
     }
+  T *pgx = at.of(gx) + (U - 1) * gx.ts, *pgg = at.of(gg) + (U - 1) * gg.ts;
 #pragma unroll
-  for (int t = U - 1; t >= 0; --t) {
+  for (int t = U - 1; t >= 0; --t, pgx -= gx.ts, pgg -= gg.ts) {
     Vec<T, V> ox = narrow<T>(all_of<V>(0.f)), og = ox;
     if (t < c.n) {
       const Lanes<V> G = add(widen(dr[t]), C);
@@ -852,8 +858,8 @@ __global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ 
       C = mul(a[t], G);
     }
     if (t < s.len) {
-      put<V>(gx.at(c.b, t, c.d), gx.wide, ox);
-      put<V>(gg.at(c.b, t, c.d), gg.wide, og);
+      put<V>(pgx, WIDE || gx.wide, ox);
+      put<V>(pgg, WIDE || gg.wide, og);
     }
   }
   if (grad_in) {
@@ -1045,7 +1051,7 @@ cudaError_t with_channels(int32_t dim, F f) {
 }
 // Calls f with two truth values as constants.
 template <class F>
-cudaError_t with_flags(bool a, bool b, F f) {
+auto with_flags(bool a, bool b, F f) {
   if (a) return b ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
   return b ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
 }
@@ -1125,15 +1131,19 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
       constexpr int V = decltype(v)::value, R = fwd_positions<V>();
       const Cut c = cut_call<V>(h, batch, len, offsets, R, R);
       constexpr int kMost = V == 4 ? 8 : kShort / V;   // twice kShort still fits: 30000 x 8 x 64 bf16 29 -> 19 us
+      const bool same = all_wide<V>(sizeof(T), x, gate, y);
       if (len <= kMost) {
-        auto kernel = len <= 2           ? k_scan_short_fwd<T, V, 2>
-                      : len <= kShort / V ? k_scan_short_fwd<T, V, kShort / V>
-                                          : k_scan_short_fwd<T, V, kMost>;
+        const auto kernel = with_flags(same, false, [&](auto wide, auto) {
+          constexpr bool W = decltype(wide)::value;
+          return len <= 2           ? k_scan_short_fwd<T, V, 2, W>
+                 : len <= kShort / V ? k_scan_short_fwd<T, V, kShort / V, W>
+                                     : k_scan_short_fwd<T, V, kMost, W>;
+        });
         kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
                                                                as_view<T, V>(y), state_in, state_out);
         return cudaGetLastError();
       }
-      return with_flags(c.chain, all_wide<V>(sizeof(T), x, gate, y), [&](auto chain, auto wide) {
+      return with_flags(c.chain, same, [&](auto chain, auto wide) {
         return launch<V, k_scan_fwd<T, V, R, decltype(chain)::value, decltype(wide)::value>>(
             c, 2 * R * kScanThreads * V * sizeof(T), 2, (cudaStream_t)stream, as_view<const T, V>(x),
             as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
@@ -1160,7 +1170,11 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
       constexpr int V = decltype(v)::value;
       const Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
       if (len <= kShort / V) {
-        auto kernel = len <= 2 ? k_scan_short_bwd<T, V, 2> : k_scan_short_bwd<T, V, kShort / V>;
+        const auto kernel =
+            with_flags(all_wide<V>(sizeof(T), x, gate, grad_y, grad_x, grad_gate), false, [&](auto wide, auto) {
+              constexpr bool W = decltype(wide)::value;
+              return len <= 2 ? k_scan_short_bwd<T, V, 2, W> : k_scan_short_bwd<T, V, kShort / V, W>;
+            });
         kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(
             c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(grad_y), state_in,
             grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate), grad_state_in);
@@ -1189,15 +1203,16 @@ extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const voi
       !aligned_to(y, size) || !aligned_to(states, 4) || !aligned_to(rows, 8) || (n > 1 && y_stride < dim))
     return EMB_ERR_INVALID_ARG;
   if (dim > 65536) return EMB_ERR_UNSUPPORTED;
-  const bool wide = dim % 4 == 0 && x_stride % 4 == 0 && gate_stride % 4 == 0 &&
-                    y_stride % 4 == 0 && aligned_to(x, 4 * size) && aligned_to(gate, 4 * size) &&
-                    aligned_to(y, 4 * size) && aligned_to(states, 4 * sizeof(float));
-  const int vecs = wide ? dim / 4 : dim;
+  const auto fits = [&](int v) {
+    return dim % v == 0 && x_stride % v == 0 && gate_stride % v == 0 && y_stride % v == 0 && aligned_to(x, v * size) &&
+           aligned_to(gate, v * size) && aligned_to(y, v * size) && aligned_to(states, v * sizeof(float));
+  };
+  const int v = fits(4) ? 4 : fits(2) ? 2 : 1, vecs = dim / v;
   const int64_t need = (n * vecs + 127) / 128;
   const unsigned grid = (unsigned)(need < (1 << 20) ? need : (1 << 20));
   with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    auto kernel = wide ? k_scan_step<T, 4> : k_scan_step<T, 1>;
+    auto kernel = v == 4 ? k_scan_step<T, 4> : v == 2 ? k_scan_step<T, 2> : k_scan_step<T, 1>;
     kernel<<<grid, 128, 0, (cudaStream_t)stream>>>(n, make_div_magic((uint64_t)vecs), (const T*)x, x_stride,
                                                   (const T*)gate, gate_stride, rows, states, num_rows, (T*)y,
                                                   y_stride);
