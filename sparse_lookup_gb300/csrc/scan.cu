@@ -459,7 +459,11 @@ struct Staged {
 // registers, so x and gate are read once.  Its stretch's effect goes to shared
 // memory, the channels' lanes join the stretches behind the state before the
 // tile, and each thread then runs its positions from its own first state.  The
-// next tile's inputs are copied meanwhile.
+// next tile's inputs are copied meanwhile.  fp32 is bound by memory (16 x 8192
+// x 512 walking 129 us, 6.2 TB/s); 16 bits by instruction issue and the latency
+// between a tile's steps (128 x 1024 x 512 bf16 81 us, 5.0 TB/s; 19 instructions
+// an element), chained also by the waits (131072 x 512 bf16 120 us, 10 of them
+// waiting for records).
 // CHAIN: a CTA takes tiles by ticket and finds the state before its tile in the
 // records of the tiles ahead; otherwise it walks along time with the state in
 // hand.  cx = 256: a thread is a whole stretch of its own, nothing is joined.
@@ -592,6 +596,8 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
 // gates.  16 bits: y is read at every position (RERUN false) -- a rerun would
 // carry the rounding of the one row it starts from into states that are
 // smaller than that row, where y itself is off by half a unit of its own.
+// Bound as the forward is: 16 x 8192 x 512 fp32 208 us, 6.4 TB/s; 128 x 1024 x
+// 512 bf16 153 us, 4.4 TB/s; 131072 x 512 bf16 202 us.
 template <class T, int V, int R, bool CHAIN, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
                                                                        View<const T> y, View<const T> gy,
@@ -772,7 +778,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
 // Short sequences, of at most U positions: a thread holds a whole column vector
 // in registers, so the backward runs forward from the first state and needs no
 // y.  The tiles above would leave most of their positions empty (20000 x 2 x
-// 75 fp16: 47 us forward).
+// 75 fp16: 47 us forward, 8 here).  Bound by memory where a vector fills an
+// access (50000 x 4 x 256 fp32 7.0 TB/s in either direction, 100000 x 7 x 50
+// fp16 6.4), by instruction issue for single channels of 16 bits (3.9).
 template <class T, int V, int U, bool WIDE>
 __global__ void __launch_bounds__(128) k_scan_short_fwd(const __grid_constant__ ScanArgs s, View<const T> x,
                                                         View<const T> g, View<T> y,
@@ -868,7 +876,10 @@ __global__ void __launch_bounds__(128) k_scan_short_bwd(const __grid_constant__ 
   }
 }
 
-// One position per session: a thread takes V channels of one row.
+// One position per session: a thread takes V channels of one row, each value is
+// read and written once.  Bound by memory (100000 x 256 bf16 56 us, 6.4 TB/s),
+// few sessions by their launch (192 x 256: 1.6 us); widths that only pairs or
+// single channels divide by instruction issue (100000 x 50 fp16 17 us).
 template <class T, int V>
 __global__ void __launch_bounds__(128) k_scan_step(int64_t n, DivMagic vecs, const T* __restrict__ x, int64_t xs,
                                                    const T* __restrict__ g, int64_t gs,
@@ -960,7 +971,8 @@ int64_t chain_records(int TT, int64_t cols, int64_t len) {
 // A call whose last round of walking CTAs would leave more than a quarter of
 // the GPU idle is chained, else it walks (us forward, walking and chained, on
 // 304 places: 176 tiles across, 11 x 8192 x 512 bf16, 94 and 74; 256 tiles 97
-// and 107; 320 tiles 147 and 127; fp32 backward of 256 tiles 209 and 263).  chain_r, walk_r: positions of a thread in either case.
+// and 107; 320 tiles 147 and 127; fp32 backward of 256 tiles 209 and 263).
+// chain_r, walk_r: positions of a thread in either case.
 template <int V>
 Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int chain_r, int walk_r) {
   Cut c{};
@@ -1012,7 +1024,27 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   return c;
 }
 
-constexpr int kShort = 16;   // elements of a column vector that a thread holds whole
+// Sequences that single threads hold whole (k_scan_short_*): how long they may
+// be, the positions that a thread of V channels has registers for, and the
+// channels of a thread.  Measured, held whole and in tiles: 50000 x 9 x 64 bf16
+// forward 30 and 47 us, with 16 positions 47 and 52; backward of 8 positions 77
+// and 98 us, of 9 72 and 64; fp32 forward of 9 61 and 59; pairs of 50000 x 9 x
+// 50 fp16 backward 59, single channels 75.
+constexpr int kShort = 16;
+template <class T, bool BACKWARD>
+int32_t short_len(int32_t dim) {
+  return channels_at_once(dim) == 4 && (BACKWARD || sizeof(T) == 4) ? 8 : 16;
+}
+template <class T, bool BACKWARD, int V>
+constexpr int short_positions() {
+  return V > 1 && sizeof(T) == 2 && (V == 2 || !BACKWARD) ? 2 * kShort / V : kShort / V;
+}
+template <class T, bool BACKWARD>
+int32_t short_channels(int32_t dim, int32_t len) {
+  const int V = channels_at_once(dim);
+  if (V == 4 && len <= short_positions<T, BACKWARD, 4>()) return 4;
+  return V > 1 && len <= short_positions<T, BACKWARD, 2>() ? 2 : 1;
+}
 unsigned short_grid(const Cut& c) { return (unsigned)((c.args.vecs + 127) / 128); }
 
 // `staged`: bytes of the inputs' copies; `areas`: shared arrays of the joins.
@@ -1049,11 +1081,14 @@ cudaError_t with_channels(int32_t dim, F f) {
     default: return f(std::integral_constant<int, 1>());
   }
 }
-// Calls f with two truth values as constants.
+// Calls f with truth values as constants.
+template <class F>
+auto with_flag(bool a, F f) {
+  return a ? f(std::true_type()) : f(std::false_type());
+}
 template <class F>
 auto with_flags(bool a, bool b, F f) {
-  if (a) return b ? f(std::true_type(), std::true_type()) : f(std::true_type(), std::false_type());
-  return b ? f(std::false_type(), std::true_type()) : f(std::false_type(), std::false_type());
+  return with_flag(a, [&](auto x) { return with_flag(b, [&](auto y) { return f(x, y); }); });
 }
 
 }  // namespace emb
@@ -1127,23 +1162,24 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
+    if (len <= short_len<T, false>(h->dim))
+      return with_channels(short_channels<T, false>(h->dim, len), [&](auto v) {
+        constexpr int V = decltype(v)::value, U = kShort / V, most = short_positions<T, false, V>();
+        const Cut c = cut_call<V>(h, batch, len, offsets, 1, 1);
+        const auto kernel = with_flag(all_wide<V>(sizeof(T), x, gate, y), [&](auto wide) {
+          constexpr bool W = decltype(wide)::value;
+          return len <= 2   ? k_scan_short_fwd<T, V, 2, W>
+                 : len <= U ? k_scan_short_fwd<T, V, U, W>
+                            : k_scan_short_fwd<T, V, most, W>;
+        });
+        kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(
+            c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
+        return cudaGetLastError();
+      });
     return with_channels(h->dim, [&](auto v) {
       constexpr int V = decltype(v)::value, R = fwd_positions<V>();
       const Cut c = cut_call<V>(h, batch, len, offsets, R, R);
-      constexpr int kMost = V == 4 ? 8 : kShort / V;   // twice kShort still fits: 30000 x 8 x 64 bf16 29 -> 19 us
-      const bool same = all_wide<V>(sizeof(T), x, gate, y);
-      if (len <= kMost) {
-        const auto kernel = with_flags(same, false, [&](auto wide, auto) {
-          constexpr bool W = decltype(wide)::value;
-          return len <= 2           ? k_scan_short_fwd<T, V, 2, W>
-                 : len <= kShort / V ? k_scan_short_fwd<T, V, kShort / V, W>
-                                     : k_scan_short_fwd<T, V, kMost, W>;
-        });
-        kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(c.args, as_view<const T, V>(x), as_view<const T, V>(gate),
-                                                               as_view<T, V>(y), state_in, state_out);
-        return cudaGetLastError();
-      }
-      return with_flags(c.chain, same, [&](auto chain, auto wide) {
+      return with_flags(c.chain, all_wide<V>(sizeof(T), x, gate, y), [&](auto chain, auto wide) {
         return launch<V, k_scan_fwd<T, V, R, decltype(chain)::value, decltype(wide)::value>>(
             c, 2 * R * kScanThreads * V * sizeof(T), 2, (cudaStream_t)stream, as_view<const T, V>(x),
             as_view<const T, V>(gate), as_view<T, V>(y), state_in, state_out);
@@ -1166,20 +1202,24 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
-    return with_channels(h->dim, [&](auto v) {
-      constexpr int V = decltype(v)::value;
-      const Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
-      if (len <= kShort / V) {
-        const auto kernel =
-            with_flags(all_wide<V>(sizeof(T), x, gate, grad_y, grad_x, grad_gate), false, [&](auto wide, auto) {
-              constexpr bool W = decltype(wide)::value;
-              return len <= 2 ? k_scan_short_bwd<T, V, 2, W> : k_scan_short_bwd<T, V, kShort / V, W>;
-            });
+    if (len <= short_len<T, true>(h->dim))
+      return with_channels(short_channels<T, true>(h->dim, len), [&](auto v) {
+        constexpr int V = decltype(v)::value, U = kShort / V, most = short_positions<T, true, V>();
+        const Cut c = cut_call<V>(h, batch, len, offsets, 1, 1);
+        const auto kernel = with_flag(all_wide<V>(sizeof(T), x, gate, grad_y, grad_x, grad_gate), [&](auto wide) {
+          constexpr bool W = decltype(wide)::value;
+          return len <= 2   ? k_scan_short_bwd<T, V, 2, W>
+                 : len <= U ? k_scan_short_bwd<T, V, U, W>
+                            : k_scan_short_bwd<T, V, most, W>;
+        });
         kernel<<<short_grid(c), 128, 0, (cudaStream_t)stream>>>(
             c.args, as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(grad_y), state_in,
             grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate), grad_state_in);
         return cudaGetLastError();
-      }
+      });
+    return with_channels(h->dim, [&](auto v) {
+      constexpr int V = decltype(v)::value;
+      const Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
       const bool same = all_wide<V>(sizeof(T), x, gate, y, grad_y, grad_x, grad_gate);
       return with_flags(c.chain, same, [&](auto chain, auto wide) {
         constexpr int R = bwd_positions<T, V, decltype(chain)::value>();
