@@ -465,3 +465,40 @@ def test_one_handle_for_chains_of_other_shapes():
         other.close()
     assert plan.device_status() == 0
     plan.close()
+
+
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("T,D", [(2, 24), (4, 32), (7, 24), (8, 30), (11, 24), (13, 30), (16, 33), (17, 24)])
+def test_short_sequences_in_views_and_with_dead_positions(T, D, dtype):
+    """Sequences held whole: the same bits from halves of one projection,
+    time-major arrays, rows off the access boundaries and broadcast entries,
+    whatever the dead positions hold."""
+    import torch
+    B = 19
+    x, g, gy, h0, gl, lens, off = make(B, T, D, dtype, T * D)
+    plan = sl.GatedScan(D, B, T)
+
+    def run(x, g, gy):
+        y, last = plan.forward(x, g, off, h0)
+        return (y, last) + plan.backward(x, g, y, gy, off, h0, gl)
+
+    def off_boundary(t):
+        u = torch.empty(t.numel() + 1, dtype=t.dtype, device="cuda")[1:].view(t.shape)
+        return u.copy_(t)
+
+    want = run(x, g, gy)
+    both = torch.cat([x, g], 2)
+    for views in ((both[..., :D], both[..., D:], gy), (off_boundary(x), off_boundary(g), off_boundary(gy)),
+                  tuple(t.transpose(0, 1).contiguous().transpose(0, 1) for t in (x, g, gy))):
+        for p, q in zip(run(*views), want):
+            assert torch.equal(p, q)
+    dead = (torch.arange(T)[None, :] >= torch.from_numpy(lens)[:, None]).cuda()[..., None]
+    for fill in (float("nan"), float("inf"), torch.finfo(x.dtype).min):
+        for p, q in zip(run(*(torch.where(dead, fill, t) for t in (x, g, gy))), want):
+            assert torch.equal(p, q)
+    one = run(x[:1].expand(B, T, D), g, gy)
+    for p, q in zip(one, run(x[:1].repeat(B, 1, 1), g, gy)):
+        assert torch.equal(p, q)
+    assert plan.device_status() == 0
+    plan.close()
+    check(B, T, D, dtype, T * D)
