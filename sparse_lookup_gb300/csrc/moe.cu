@@ -68,9 +68,10 @@ __device__ __forceinline__ uint32_t cta_exclusive(uint32_t x, uint32_t* wsum) {
 // ahead of the span and all.  One CTA (ONE) counts for itself, without
 // k_route_count: one launch in place of two pays up to kRouteOne choices.
 // A warp ranks 32 choices at a time by matching lanes, so rows follow the
-// choices' order.  Both kernels take 14 us for 524288 choices of 128 experts and
-// 36 for 1.6 M of 512 (a floor of 1 and 3 us): the ranking's chain of shared
-// memory accesses bounds them; 16 choices of 16 experts take 2.8 us, a launch.
+// choices' order.  Both kernels take 12 us for 524288 choices of 128 experts and
+// 31 for 1.6 M of 512 (a floor of 1 and 3 us): latency bounds them, of the
+// ranking's shared memory and of the spans' counts; more choices loaded ahead
+// changed nothing.  16 choices of 16 experts take 2.8 us, a launch.
 template <bool ONE>
 __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
   extern __shared__ uint32_t cnt[];
@@ -88,18 +89,20 @@ __global__ void __launch_bounds__(kRouteThreads) k_route_place(RouteArgs a) {
     if (e >= 0) atomicAdd(&mine[e], 1u);
   }
   if constexpr (!ONE) {
-    // the spans' counts, a row of E for each CTA
-    int e = threadIdx.x % E;
-    const int step = kRouteThreads % E, rows = gridDim.x * E;
-#pragma unroll 8
-    for (int i = threadIdx.x; i < rows; i += kRouteThreads) {
-      const uint32_t k = a.part[i];
-      if (k) {
-        atomicAdd(&all[e], k);
-        if (i < (int)blockIdx.x * E) atomicAdd(&ahead[e], k);
+    // the spans' counts, a row of E for each CTA: a thread sums its part of one
+    // expert's column in registers, many loads in flight (65536 x 2 choices of
+    // 1500 experts: 20 us in all, with eight in flight 31)
+    const int wide = min(E, kRouteThreads), parts = kRouteThreads / wide, first = threadIdx.x / wide;
+    for (int e = threadIdx.x % wide; first < parts && e < E; e += wide) {
+      uint32_t total = 0, before = 0;
+#pragma unroll 32
+      for (int r = first; r < (int)gridDim.x; r += parts) {
+        const uint32_t k = a.part[r * E + e];
+        total += k;
+        before += r < (int)blockIdx.x ? k : 0u;
       }
-      e += step;
-      if (e >= E) e -= E;
+      if (total) atomicAdd(&all[e], total);
+      if (before) atomicAdd(&ahead[e], before);
     }
   }
   __syncthreads();
