@@ -605,7 +605,7 @@ emb_status emb_selftest_sort_timeout(uint32_t* latched, uint32_t* fail_word, int
 
 /* scan_selftest_timeout -- makes the bounded wait between parts of a sequence
  * run out on purpose, without faulting or hanging the GPU: a chained
- * scan_forward over two tiles of which only the second is handed out, so its
+ * scan_forward over four tiles of which only the last is handed out, so its
  * wait for the first can never end; after its bound (about a second) it latches
  * EMB_ERR_TIMEOUT, and the next call on the same handle runs as ever.
  * Allocates and frees its own buffers and synchronizes the device.  All

@@ -968,10 +968,12 @@ int64_t chain_records(int TT, int64_t cols, int64_t len) {
   return (tiles + tiles / kLeastGroup + 1) * cols;
 }
 
-// A call whose last round of walking CTAs would leave more than a quarter of
-// the GPU idle is chained, else it walks (us forward, walking and chained, on
-// 304 places: 176 tiles across, 11 x 8192 x 512 bf16, 94 and 74; 256 tiles 97
-// and 107; 320 tiles 147 and 127; fp32 backward of 256 tiles 209 and 263).
+// A call whose last round of walking CTAs would leave more than two fifths of
+// the GPU's places idle is chained, if it is long enough for a chain to start:
+// the more CTAs walk side by side, the more.  us forward, walking and chained,
+// on 304 places: 176 tiles across, 11 x 8192 x 512 bf16, 94 and 74; 256 tiles 97
+// and 107; 430 of 2400 positions fp32 69 and 79; 100 of 600, 1200 and 2400
+// positions bf16 8.4 and 10.4, 12.6 and 12.9, 22 and 19; 800 x 512 10.4 and 8.1.
 // chain_r, walk_r: positions of a thread in either case.
 template <int V>
 Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int chain_r, int walk_r) {
@@ -990,8 +992,8 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   static_assert((kScanThreads / V >> kCx) == kJoin, "the lanes of a channel read its group's records");
   const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
   const auto across = [&](int cx_log) { return (a.vecs + (1 << cx_log) - 1) >> cx_log; };
-  const int64_t rounds = (across(kCx) + slots - 1) / slots;
-  c.chain = across(kCx) * 4 < rounds * slots * 3 && (int64_t)len > (kScanThreads >> kCx) * chain_r;
+  const int64_t wide = across(kCx), places = (wide + slots - 1) / slots * slots;
+  c.chain = wide * 5 < places * 3 && len * places > (kScanThreads >> kCx) * chain_r * (2 * places + 10 * wide);
   const int R = c.chain ? chain_r : walk_r;
   if (c.chain) {
     a.cx_log = kCx;
@@ -1110,7 +1112,7 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
   if (e == cudaSuccess) {
     // a call with more channels than this walks
-    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 * 3 + dim, all = (int64_t)max_batch * dim;
+    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 * 2 + dim, all = (int64_t)max_batch * dim;
     const int V = channels_at_once(dim), TT = V == 4 ? least_tile<4>() : V == 2 ? least_tile<2>() : least_tile<1>();
     h->max_records = chain_records(TT, all < most ? all : most, max_len);
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
@@ -1260,10 +1262,10 @@ extern "C" emb_status scan_step(int64_t n, int32_t dim, int32_t dtype, const voi
   return cuda_status(cudaGetLastError());
 }
 
-// A sequence of two tiles of which only the second is handed out.
+// A sequence of four tiles of which only the last is handed out.
 extern "C" emb_status scan_selftest_timeout(uint32_t* latched, uint32_t* latched_after, float* wait_ms) {
   if (!latched || !latched_after) return EMB_ERR_INVALID_ARG;
-  constexpr int dim = 32, len = 2 * (kScanThreads >> long_cx<4>()) * fwd_positions<4>();
+  constexpr int dim = 32, len = 4 * (kScanThreads >> long_cx<4>()) * fwd_positions<4>();
   emb_scan h = nullptr;
   emb_status st = scan_create(dim, 1, len, &h);
   if (st != EMB_OK) return st;
@@ -1273,8 +1275,8 @@ extern "C" emb_status scan_selftest_timeout(uint32_t* latched, uint32_t* latched
   if (e == cudaSuccess) e = cudaMemset(buf, 0, sizeof(float) * dim * len * 3);
   if (e == cudaSuccess) e = cudaEventCreate(&a);
   if (e == cudaSuccess) e = cudaEventCreate(&b);
-  const uint32_t second = 1;
-  if (e == cudaSuccess) e = cudaMemcpy(&h->shared_d->ticket, &second, sizeof(second), cudaMemcpyHostToDevice);
+  const uint32_t last = 3;
+  if (e == cudaSuccess) e = cudaMemcpy(&h->shared_d->ticket, &last, sizeof(last), cudaMemcpyHostToDevice);
   const scan_view x{buf, dim * len, dim}, g{buf + dim * len, dim * len, dim}, y{buf + 2 * dim * len, dim * len, dim};
   for (uint32_t* out : {latched, latched_after}) {
     if (e != cudaSuccess) break;
