@@ -447,8 +447,10 @@ emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, c
  *   G_t = grad_y_t + a_{t+1} G_{t+1} (grad_state_out past the last position)
  *   grad_x_t = (1 - a_t) G_t;  grad_gate_t = a_t (1 - a_t) (h_{t-1} - x_t) G_t
  * Positions past an entry's end read nothing and get gradient 0.
- * h_{t-1} is taken from y (16-bit types: as y was rounded).  grad_state_out (NULL = 0) and grad_state_in (NULL = not
- * wanted) are [batch, dim] fp32. */
+ * h_{t-1} is fp32 for every type: fp32 calls may read it from y, 16-bit calls
+ * find it again from x, gate and state_in and do not read y.  Outputs are used
+ * as scratch until they are written.  grad_state_out (NULL = 0) and
+ * grad_state_in (NULL = not wanted) are [batch, dim] fp32. */
 emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int32_t dtype, const scan_view* x,
                          const scan_view* gate, const int32_t* offsets, const float* state_in, const scan_view* y,
                          const scan_view* grad_y, const float* grad_state_out, const scan_view* grad_x,

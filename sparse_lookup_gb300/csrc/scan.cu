@@ -180,8 +180,8 @@ struct Start {
     if (WIDE) o = b * w.bs + t * w.ts + d;
   }
   template <class T>
-  __device__ T* of(const View<T>& w, int back = 0) const {
-    return WIDE ? w.p + (back ? o - w.ts : o) : w.at(b, t - back, d);
+  __device__ T* of(const View<T>& w) const {
+    return WIDE ? w.p + o : w.at(b, t, d);
   }
 };
 
@@ -425,18 +425,18 @@ struct Staged {
     else if constexpr (kBytes >= 4)
       asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(d), "l"(p), "n"(kBytes) : "memory");
   }
-  __device__ void fill(const View<const T>& w, const T* p, int t0, int first, int n, float dead, bool now) const {
+  __device__ void fill(const View<const T>& w, const T* p, int t0, int n, float dead, bool now) const {
     if (kAlways ? now : async(w) == now) return;
     Vec<T, V> z;
 #pragma unroll
     for (int v = 0; v < V; ++v) z.e[v] = from_f32<T>(dead);
     if (kAlways || !now) {
-      if (t0 >= first && t0 + R <= n) {
+      if (t0 + R <= n) {
 #pragma unroll
         for (int r = 0; r < R; ++r, p += w.ts) copy(at + r * kScanThreads, p);
       } else {
         for (int r = 0; r < R; ++r, p += w.ts) {
-          if (t0 + r >= first && t0 + r < n) copy(at + r * kScanThreads, p);
+          if (t0 + r < n) copy(at + r * kScanThreads, p);
           else at[r * kScanThreads] = z;
         }
       }
@@ -445,7 +445,7 @@ struct Staged {
 #pragma unroll
       for (int r = 0; r < R; ++r, p += w.ts) {
         got[r] = z;
-        if (t0 + r >= first && t0 + r < n) got[r] = get<V>(p, WIDE || w.wide);
+        if (t0 + r < n) got[r] = get<V>(p, WIDE || w.wide);
       }
 #pragma unroll
       for (int r = 0; r < R; ++r) at[r * kScanThreads] = got[r];
@@ -491,8 +491,8 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
   auto fill = [&](const Channel& c, int k, bool now) {
     const int t0 = k * p.TT + p.ty * R;
     const Start<WIDE> at(x, c.b, c.d, t0);
-    sx.fill(x, at.of(x), t0, 0, c.n, 0.f, now);
-    sg.fill(g, at.of(g), t0, 0, c.n, SCAN_DEAD_GATE, now);
+    sx.fill(x, at.of(x), t0, c.n, 0.f, now);
+    sg.fill(g, at.of(g), t0, c.n, SCAN_DEAD_GATE, now);
     return at.o;
   };
   int64_t o = 0, o1 = 0;   // WIDE: this tile's and the next one's start
@@ -589,31 +589,158 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
   if (CHAIN && threadIdx.x == 0) leave(s);
 }
 
+// The backward of 16-bit elements finds the fp32 states before its tiles again.
+// k_scan_effects reduces each tile to what it does to a state, all tiles at
+// once; k_scan_states runs along each channel's tiles.  Both leave their numbers
+// in the first rows of the tile's gradients, the upper half of an fp32 in one
+// and the lower in the other, which that tile's CTA reads and overwrites: no
+// workspace.  Only whole tiles with live positions behind them are looked at.
+// 131072 x 512 bf16: 45 us, the inputs read a second time at 5.9 TB/s, and 32 us,
+// the latency of few channels' strided rows; 128 x 1024 x 512 41 and 8 us.  As
+// a chain of tiles like the forward's they took 139 us and 68.
+template <class T, int V>
+__device__ __forceinline__ void put_halves(const View<T>& up, const View<T>& low, int b, int t, int d,
+                                           const Lanes<V>& x) {
+  Vec<T, V> u, l;
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const uint32_t w = __float_as_uint(x.v[v]);
+    *reinterpret_cast<uint16_t*>(&u.e[v]) = (uint16_t)(w >> 16);
+    *reinterpret_cast<uint16_t*>(&l.e[v]) = (uint16_t)w;
+  }
+  put<V>(up.at(b, t, d), up.wide, u);
+  put<V>(low.at(b, t, d), low.wide, l);
+}
+template <int V, class T>
+__device__ __forceinline__ Lanes<V> get_halves(const View<T>& up, const View<T>& low, int b, int t, int d) {
+  const Vec<T, V> u = get<V>((const T*)up.at(b, t, d), up.wide), l = get<V>((const T*)low.at(b, t, d), low.wide);
+  Lanes<V> x;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    x.v[v] = __uint_as_float((uint32_t) * reinterpret_cast<const uint16_t*>(&u.e[v]) << 16 |
+                             *reinterpret_cast<const uint16_t*>(&l.e[v]));
+  return x;
+}
+
+// A CTA takes 32 column vectors of one tile, its warps a part of the tile's
+// positions each; a call of several tiles has them of 128 or 160 positions.
+constexpr int kEffectWarps = 4, kEffectRows = 8;
+template <class T, int V>
+__global__ void __launch_bounds__(kEffectWarps * 32) k_scan_effects(const __grid_constant__ ScanArgs s,
+                                                                    View<const T> x, View<const T> g, View<T> gx,
+                                                                    View<T> gg) {
+  __shared__ Lanes<V> sa[kEffectWarps][32], sb[kEffectWarps][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, TT = (int)s.tile.d;
+  const uint32_t k = div_magic32(blockIdx.x, s.groups);
+  const Channel c = channel_of<V>(s, (int64_t)(blockIdx.x - k * s.groups.d) * 32 + lane, 0);
+  const int t0 = (int)k * TT, part = TT / kEffectWarps;
+  const bool live = t0 + TT < c.n;
+  Lanes<V> a = all_of<V>(1.f), b = all_of<V>(0.f);
+  if (live) {
+    const T *px = x.at(c.b, t0 + warp * part, c.d), *pg = g.at(c.b, t0 + warp * part, c.d);
+    for (int t = 0; t < part; t += kEffectRows) {
+      Vec<T, V> xv[kEffectRows], gv[kEffectRows];
+#pragma unroll
+      for (int r = 0; r < kEffectRows; ++r, px += x.ts, pg += g.ts)
+        xv[r] = get<V>(px, x.wide), gv[r] = get<V>(pg, g.wide);
+#pragma unroll
+      for (int r = 0; r < kEffectRows; ++r) {
+        Lanes<V> e, ne;
+        gates(gv[r], e, ne);
+        a = mul(a, e);
+        b = mad(e, b, mul(ne, widen(xv[r])));
+      }
+    }
+  }
+  sa[warp][lane] = a, sb[warp][lane] = b;
+  __syncthreads();
+  if (warp != 0 || !live) return;
+#pragma unroll
+  for (int w = 1; w < kEffectWarps; ++w) {
+    b = mad(sa[w][lane], b, sb[w][lane]);
+    a = mul(sa[w][lane], a);
+  }
+  put_halves<T, V>(gx, gg, c.b, t0, c.d, a);
+  put_halves<T, V>(gx, gg, c.b, t0 + 1, c.d, b);
+}
+
+// A CTA takes 32 channels, its warps `each` neighbouring tiles.  A few warps per
+// channel walk the whole sequence, so loads go in batches.
+constexpr int kStateWarps = 32, kStateRows = 8;
+template <class T>
+__global__ void __launch_bounds__(kStateWarps * 32) k_scan_states(const __grid_constant__ ScanArgs s, int each,
+                                                                  View<T> gx, View<T> gg,
+                                                                  const float* __restrict__ state_in) {
+  __shared__ Affine part[kStateWarps][32];
+  pdl_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, TT = (int)s.tile.d;
+  const Channel c = channel_of<1>(s, (int64_t)blockIdx.x * 32 + lane, 0);
+  const int whole = c.n > 0 ? (int)div_magic32((uint32_t)c.n - 1, s.tile) : 0;   // tiles with live positions behind them
+  const int lo = min(warp * each, whole), hi = min(lo + each, whole);
+  Affine f[kStateRows];
+  const auto load = [&](int k0) {
+#pragma unroll
+    for (int i = 0; i < kStateRows; ++i) {
+      f[i] = {1.f, 0.f};
+      if (k0 + i < hi)
+        f[i] = {get_halves<1>(gx, gg, c.b, (k0 + i) * TT, c.d).v[0],
+                get_halves<1>(gx, gg, c.b, (k0 + i) * TT + 1, c.d).v[0]};
+    }
+  };
+  Affine all{1.f, 0.f};
+  for (int k0 = lo; k0 < hi; k0 += kStateRows) {
+    load(k0);
+#pragma unroll
+    for (int i = 0; i < kStateRows; ++i) all = after(f[i], all);
+  }
+  part[warp][lane] = all;
+  __syncthreads();
+  float h = state_in && c.ok ? state_in[c.col] : 0.f;
+  for (int w = 0; w < warp; ++w) h = fmaf(part[w][lane].a, h, part[w][lane].b);
+  for (int k0 = lo; k0 < hi; k0 += kStateRows) {   // effects are read before states take their places
+    load(k0);
+#pragma unroll
+    for (int i = 0; i < kStateRows; ++i) {
+      if (k0 + i < hi && k0 + i > 0) put_halves<T, 1>(gx, gg, c.b, (k0 + i) * TT, c.d, all_of<1>(h));
+      h = fmaf(f[i].a, h, f[i].b);
+    }
+  }
+  if (hi > lo && hi == whole) put_halves<T, 1>(gx, gg, c.b, whole * TT, c.d, all_of<1>(h));
+}
+
+template <class T>
+__device__ __forceinline__ float get_state(const View<T>& up, const View<T>& low, int b, int t, int d) {
+  return get_halves<1>(View<T>{up.p, up.bs, up.ts, true}, View<T>{low.p, low.bs, low.ts, true}, b, t, d).v[0];
+}
+
 // Backward, from the last position to the first: C_t = a_t (grad_y_t + C_{t+1})
 // is what position t passes back.  The gate's gradient needs the state before
-// each position.  fp32: a tile runs forward from y just before it, which costs
-// one row of y instead of all of them; both joins use the same products of
-// gates.  16 bits: y is read at every position (RERUN false) -- a rerun would
-// carry the rounding of the one row it starts from into states that are
-// smaller than that row, where y itself is off by half a unit of its own.
+// each position, in fp32: a tile runs forward from the state before it, and
+// both joins use the same products of gates.  fp32 elements: that state is y just
+// before the tile, one row of y instead of all of them.  16 bits: y is rounded,
+// and h - x may be far smaller than h; so the states are found again from x and
+// gate (k_scan_effects, k_scan_states) and y is not read.
 // Bound as the forward is: 16 x 8192 x 512 fp32 208 us, 6.4 TB/s; 128 x 1024 x
-// 512 bf16 153 us, 4.4 TB/s; 131072 x 512 bf16 202 us.
+// 512 bf16 156 us, 131072 x 512 bf16 206 us, with the states before the tiles
+// 215 and 293 (from y as it is rounded 154 and 202: every position's y read, and
+// the gate's gradient as far off as h's rounding is beside h - x).
 template <class T, int V, int R, bool CHAIN, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
                                                                        View<const T> y, View<const T> gy,
                                                                        const float* __restrict__ state_in,
                                                                        const float* __restrict__ grad_out, View<T> gx,
                                                                        View<T> gg, float* __restrict__ grad_in) {
-  constexpr bool RERUN = sizeof(T) == 4;
+  constexpr bool HALF = sizeof(T) == 2;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ uint32_t slot;
   const Place<V, R> p(s);
-  const bool whole = s.cx_log == 8;
+  const bool whole = !HALF && s.cx_log == 8;   // 16 bits: such lengths are held whole (k_scan_short_bwd)
   const int area = (kScanThreads >> s.cx_log) * p.pitch;
   const Staged<T, V, R, WIDE> sx{(Vec<T, V>*)raw + threadIdx.x}, sg{sx.at + R * kScanThreads},
-      sd{sg.at + R * kScanThreads}, sy{sd.at + R * kScanThreads};
-  float* sa = (float*)(raw + (RERUN ? 3 : 4) * R * kScanThreads * sizeof(Vec<T, V>));
+      sd{sg.at + R * kScanThreads};
+  float* sa = (float*)(raw + 3 * R * kScanThreads * sizeof(Vec<T, V>));
   float *sb = sa + area, *sc = sb + area;
+  if constexpr (HALF) pdl_wait();
   const uint32_t epoch = CHAIN ? *(volatile uint32_t*)&s.shared->epoch : 0;
   uint32_t tile = 0, next = 0;
   if constexpr (CHAIN) {
@@ -627,17 +754,16 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
   auto fill = [&](const Channel& c, int k, bool now) {
     const int t0 = k * p.TT + p.ty * R;
     const Start<WIDE> at(x, c.b, c.d, t0);
-    sx.fill(x, at.of(x), t0, 0, c.n, 0.f, now);
-    sg.fill(g, at.of(g), t0, 0, c.n, SCAN_DEAD_GATE, now);
-    sd.fill(gy, at.of(gy), t0, 0, c.n, 0.f, now);
-    if (!RERUN) sy.fill(y, at.of(y, 1), t0, 1, c.n, 0.f, now);
+    sx.fill(x, at.of(x), t0, c.n, 0.f, now);
+    sg.fill(g, at.of(g), t0, c.n, SCAN_DEAD_GATE, now);
+    sd.fill(gy, at.of(gy), t0, c.n, 0.f, now);
     return at.o;
   };
   int64_t o = 0, o1 = 0;
   if (!CHAIN || tile < s.total) o = fill(c, k, false);
   float held = 0.f;
   // fp32 with four channels has no registers to keep it in
-  constexpr bool kHeld = !CHAIN && !(RERUN && V == 4);
+  constexpr bool kHeld = !CHAIN && !(!HALF && V == 4);
   Channel q{};
   if (kHeld && !whole) q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
   Lanes<V> own;
@@ -654,16 +780,7 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       xv[r] = widen(sx.at[r * kScanThreads]);
       dy[r] = sd.at[r * kScanThreads];
       fa = mul(fa, a[r]);
-      if constexpr (RERUN) {
-        fb = mad(a[r], fb, mul(na[r], xv[r]));
-      } else {
-        Lanes<V> before = widen(sy.at[r * kScanThreads]);
-        if (r == 0 && t0 == 0 && state_in && c.ok) {
-#pragma unroll
-          for (int v = 0; v < V; ++v) before.v[v] = state_in[c.col + v];
-        }
-        xv[r] = mul(mul(a[r], na[r]), sub(before, xv[r]));
-      }
+      fb = mad(a[r], fb, mul(na[r], xv[r]));
     }
 #pragma unroll
     for (int r = R - 1; r >= 0; --r) fc = mul(a[r], add(widen(dy[r]), fc));
@@ -694,7 +811,6 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
         own.v[v] = fmaf(fa.v[v], own.v[v], fc.v[v]);
         if (grad_in && c.ok && k == 0) grad_in[c.col + v] = own.v[v];
         h.v[v] = 0.f;
-        if (!RERUN) continue;
         if (c.ok && t0 == 0) h.v[v] = state_in ? state_in[c.col + v] : 0.f;
         else if (t0 < c.n) h.v[v] = to_f32(*y.at(c.b, t0 - 1, c.d + v));
       }
@@ -702,26 +818,24 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         sa[p.ty * p.pitch + p.cx * V + v] = fa.v[v];
-        if (RERUN) sb[p.ty * p.pitch + p.cx * V + v] = fb.v[v];
+        sb[p.ty * p.pitch + p.cx * V + v] = fb.v[v];
         sc[p.ty * p.pitch + p.cx * V + v] = fc.v[v];
       }
       if constexpr (!kHeld) q = channel_of<V>(s, (gi << s.cx_log) + p.ch / V, p.ch % V);
       const int start = k * p.TT;
       const bool live = q.ok && (start < q.n || k == 0);
       float first = 0.f;
-      if (RERUN && live) first = k == 0 ? (state_in ? state_in[q.col] : 0.f) : to_f32(*y.at(q.b, start - 1, q.d));
+      if (live && k == 0) first = state_in ? state_in[q.col] : 0.f;
+      else if (live) first = HALF ? get_state(gx, gg, q.b, start, q.d) : to_f32(*y.at(q.b, start - 1, q.d));
       __syncthreads();
       if (!CHAIN) ahead();
       Affine f[V], ex, all;
-      float st;
-      if (RERUN) {
-        join_stretches<V>(p, sa, sb, false, f, ex, all);
-        st = fmaf(ex.a, first, ex.b);
+      join_stretches<V>(p, sa, sb, false, f, ex, all);
+      float st = fmaf(ex.a, first, ex.b);
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          sb[(p.j * V + i) * p.pitch + p.ch] = st;
-          st = fmaf(f[i].a, st, f[i].b);
-        }
+      for (int i = 0; i < V; ++i) {
+        sb[(p.j * V + i) * p.pitch + p.ch] = st;
+        st = fmaf(f[i].a, st, f[i].b);
       }
       join_stretches<V>(p, sa, sc, true, f, ex, all);
       // the chain of a channel begins at the tile of its last position
@@ -747,17 +861,15 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs 
       if (CHAIN) ahead();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        if (RERUN) h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
+        h.v[v] = sb[p.ty * p.pitch + p.cx * V + v];
         C.v[v] = sc[p.ty * p.pitch + p.cx * V + v];
       }
     }
-    if (RERUN) {
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const Lanes<V> before = h;
-        h = mad(a[r], h, mul(na[r], xv[r]));
-        xv[r] = mul(mul(a[r], na[r]), sub(before, xv[r]));
-      }
+    for (int r = 0; r < R; ++r) {
+      const Lanes<V> before = h;
+      h = mad(a[r], h, mul(na[r], xv[r]));
+      xv[r] = mul(mul(a[r], na[r]), sub(before, xv[r]));
     }
     Vec<T, V> ox[R], og[R];
 #pragma unroll
@@ -930,13 +1042,14 @@ bool call_ok(emb_scan h, int32_t batch, int32_t len, int32_t dtype) {
 struct Cut {
   ScanArgs args;
   bool chain, fits;
+  bool follows;   // launched as the dependant of the kernel ahead of it
   unsigned grid;
 };
 
 // Positions of a thread, as many as its registers hold, for V = 4, 2 and 1
 // channels.  Fewer tiles wait for one another where there are more, so a
 // chained backward of 16-bit elements, whose gradients of y take half the
-// registers, has five (131072 x 512 bf16: 205 us, with four 226, with six 211);
+// registers, has five (131072 x 512 bf16: 206 us);
 // walking, tiles of 160 positions fit sequences worse (1024 x 512 x 128 bf16:
 // 160 us with four, 169 with five).
 template <int V>
@@ -1030,12 +1143,14 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
 // be, the positions that a thread of V channels has registers for, and the
 // channels of a thread.  Measured, held whole and in tiles: 50000 x 9 x 64 bf16
 // forward 30 and 47 us, with 16 positions 47 and 52; backward of 8 positions 77
-// and 98 us, of 9 72 and 64; fp32 forward of 9 61 and 59; pairs of 50000 x 9 x
-// 50 fp16 backward 59, single channels 75.
+// and 98 us; fp32 forward of 9 61 and 59; pairs of 50000 x 9 x 50 fp16 backward
+// 59, single channels 75.  16-bit backwards of 9 to 16 positions are held whole,
+// in pairs, so that no state before a tile is needed (50000 x 9 x 64 85 us, of 16
+// 106).
 constexpr int kShort = 16;
-template <class T, bool BACKWARD>
+template <class T>
 int32_t short_len(int32_t dim) {
-  return channels_at_once(dim) == 4 && (BACKWARD || sizeof(T) == 4) ? 8 : 16;
+  return channels_at_once(dim) == 4 && sizeof(T) == 4 ? 8 : 16;
 }
 template <class T, bool BACKWARD, int V>
 constexpr int short_positions() {
@@ -1059,8 +1174,29 @@ cudaError_t launch(const Cut& c, size_t staged, int areas, cudaStream_t stream, 
                                    sizeof(float);
   if (room != cudaSuccess) return room;
   if (!c.fits || smem > kMostShared) return cudaErrorNotSupported;
+  if (c.follows) return launch_dependent(kernel, c.grid, kScanThreads, smem, stream, c.args, a...);
   kernel<<<c.grid, kScanThreads, smem, stream>>>(c.args, a...);
   return cudaGetLastError();
+}
+
+// The states before a backward's tiles, where it has several.
+template <class T, int V>
+cudaError_t find_states(const Cut& c, View<const T> x, View<const T> g, View<T> gx, View<T> gg, const float* state_in,
+                        cudaStream_t stream, std::integral_constant<int, V>) {
+  ScanArgs a = c.args;
+  const int64_t groups = (a.vecs + 31) / 32, most = a.tiles - 1;
+  if (!c.fits) return cudaErrorNotSupported;
+  if (most == 0) return cudaSuccess;
+  a.groups = make_div_magic32((uint32_t)groups);
+  k_scan_effects<T, V><<<(unsigned)(groups * most), kEffectWarps * 32, 0, stream>>>(a, x, g, gx, gg);
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  a.vecs = (int64_t)a.batch * a.dim;
+  a.per = make_div_magic32((uint32_t)a.dim);
+  int warps = 1;   // about four tiles each
+  while (warps < kStateWarps && warps * 4 < most) warps *= 2;
+  return launch_dependent(k_scan_states<T>, (unsigned)((a.vecs + 31) / 32), warps * 32, 0, stream, a,
+                          (int)((most + warps - 1) / warps), gx, gg, state_in);
 }
 
 // All views wide, with the first one's strides: the kernels of this variant
@@ -1164,7 +1300,7 @@ extern "C" emb_status scan_forward(emb_scan h, int32_t batch, int32_t len, int32
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
-    if (len <= short_len<T, false>(h->dim))
+    if (len <= short_len<T>(h->dim))
       return with_channels(short_channels<T, false>(h->dim, len), [&](auto v) {
         constexpr int V = decltype(v)::value, U = kShort / V, most = short_positions<T, false, V>();
         const Cut c = cut_call<V>(h, batch, len, offsets, 1, 1);
@@ -1204,7 +1340,7 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
   if ((int64_t)batch * h->dim >= (int64_t(1) << 32)) return EMB_ERR_UNSUPPORTED;
   return cuda_status(with_element(dtype, [&](auto* e) {
     using T = std::remove_pointer_t<decltype(e)>;
-    if (len <= short_len<T, true>(h->dim))
+    if (len <= short_len<T>(h->dim))
       return with_channels(short_channels<T, true>(h->dim, len), [&](auto v) {
         constexpr int V = decltype(v)::value, U = kShort / V, most = short_positions<T, true, V>();
         const Cut c = cut_call<V>(h, batch, len, offsets, 1, 1);
@@ -1221,12 +1357,19 @@ extern "C" emb_status scan_backward(emb_scan h, int32_t batch, int32_t len, int3
       });
     return with_channels(h->dim, [&](auto v) {
       constexpr int V = decltype(v)::value;
-      const Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
-      const bool same = all_wide<V>(sizeof(T), x, gate, y, grad_y, grad_x, grad_gate);
+      Cut c = cut_call<V>(h, batch, len, offsets, bwd_positions<T, V, true>(), bwd_positions<T, V, false>());
+      if constexpr (sizeof(T) == 2) {
+        const cudaError_t e = find_states(c, as_view<const T, V>(x), as_view<const T, V>(gate),
+                                          as_view<T, V>(grad_x), as_view<T, V>(grad_gate), state_in,
+                                          (cudaStream_t)stream, std::integral_constant<int, V>());
+        if (e != cudaSuccess) return e;
+        c.follows = c.args.tiles > 1;
+      }
+      const bool same = all_wide<V>(sizeof(T), x, gate, grad_y, grad_x, grad_gate);   // of y: single elements
       return with_flags(c.chain, same, [&](auto chain, auto wide) {
         constexpr int R = bwd_positions<T, V, decltype(chain)::value>();
         return launch<V, k_scan_bwd<T, V, R, decltype(chain)::value, decltype(wide)::value>>(
-            c, (sizeof(T) == 4 ? 3 : 4) * R * kScanThreads * V * sizeof(T), 3, (cudaStream_t)stream,
+            c, 3 * R * kScanThreads * V * sizeof(T), 3, (cudaStream_t)stream,
             as_view<const T, V>(x), as_view<const T, V>(gate), as_view<const T, V>(y), as_view<const T, V>(grad_y),
             state_in, grad_state_out, as_view<T, V>(grad_x), as_view<T, V>(grad_gate), grad_state_in);
       });
