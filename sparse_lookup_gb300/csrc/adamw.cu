@@ -453,7 +453,9 @@ emb_status create_adamw(const adamw_tensor* tensors, int32_t n, bool eight, emb_
   EMB_CUDA_TRY(cudaMemcpy((void*)h->grads_d, grads.data(), sizeof(void*) * n, cudaMemcpyHostToDevice));
   if (!units.empty())
     EMB_CUDA_TRY(cudaMemcpy(h->units_d, units.data(), sizeof(AdamUnit) * units.size(), cudaMemcpyHostToDevice));
-  return EMB_OK;
+  // a copy from pageable memory may return before it has arrived, and a step on
+  // a non-blocking stream does not wait for the stream that it runs on
+  return cuda_status(cudaStreamSynchronize(nullptr));
 }
 
 }  // namespace
