@@ -1283,10 +1283,12 @@ extern "C" emb_status scan_destroy(emb_scan h) {
 
 extern "C" emb_status scan_get_device_status(emb_scan h, void* stream) {
   if (!h) return EMB_ERR_INVALID_ARG;
+  // read and cleared in the stream's own order: a clear on another stream could
+  // come after the next call has latched an error
   uint32_t st = 0;
+  EMB_CUDA_TRY(cudaMemcpyAsync(&st, h->status_d, sizeof(uint32_t), cudaMemcpyDeviceToHost, (cudaStream_t)stream));
+  EMB_CUDA_TRY(cudaMemsetAsync(h->status_d, 0, sizeof(uint32_t), (cudaStream_t)stream));
   EMB_CUDA_TRY(cudaStreamSynchronize((cudaStream_t)stream));
-  EMB_CUDA_TRY(cudaMemcpy(&st, h->status_d, sizeof(uint32_t), cudaMemcpyDeviceToHost));
-  EMB_CUDA_TRY(cudaMemset(h->status_d, 0, sizeof(uint32_t)));
   return (emb_status)st;
 }
 

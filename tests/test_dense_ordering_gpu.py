@@ -2,6 +2,9 @@
 order, for the next call on any stream: torch's side streams do not wait for
 the default stream."""
 
+import threading
+import time
+
 import pytest
 
 import sparse_lookup_gb300 as sl
@@ -43,3 +46,26 @@ def test_a_first_step_on_another_stream_finds_the_handle_complete():
         assert all(torch.equal(x, y) for x, y in zip(q, want))
         torch.cuda.synchronize()
         opt.close()
+
+
+def test_reading_the_status_does_not_clear_a_later_error():
+    """The status is read on a side stream while the default stream is busy: the
+    clear belongs before the next call, whose error must stay."""
+    import torch
+    plan = sl.GatedScan(8, 2, 20)
+    x = torch.randn(2, 20, 8, device="cuda")
+    good, bad = (torch.tensor(o, dtype=torch.int32, device="cuda") for o in ([0, 20, 40], [0, 20, 5]))
+    side = torch.cuda.Stream()
+    y, last = plan.forward(x, x, good)
+    torch.cuda.synchronize()
+    ms = int(2e6)   # cycles, about a millisecond
+    for _ in range(3):
+        torch.cuda._sleep(60 * ms)                        # the default stream is busy ...
+        more = threading.Thread(target=lambda: (time.sleep(0.02), torch.cuda._sleep(60 * ms)))
+        more.start()                                      # ... and gets more while the status is read
+        assert plan.device_status(stream=side) == 0
+        plan.forward(x, x, bad, y=y, last=last, stream=side)
+        more.join()
+        torch.cuda.synchronize()
+        assert plan.device_status(stream=side) == 7
+    plan.close()
