@@ -61,9 +61,12 @@ def test_reading_the_status_does_not_clear_a_later_error():
     ms = int(2e6)   # cycles, about a millisecond
     for _ in range(3):
         torch.cuda._sleep(60 * ms)                        # the default stream is busy ...
+        busy = torch.cuda.Event()
+        busy.record()
         more = threading.Thread(target=lambda: (time.sleep(0.02), torch.cuda._sleep(60 * ms)))
         more.start()                                      # ... and gets more while the status is read
         assert plan.device_status(stream=side) == 0
+        assert not busy.query()                           # nothing of it went through the default stream
         plan.forward(x, x, bad, y=y, last=last, stream=side)
         more.join()
         torch.cuda.synchronize()
