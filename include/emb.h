@@ -561,7 +561,8 @@ emb_status adamw_create(const adamw_tensor* tensors, int32_t n, uint32_t flags, 
 
 /* adamw_bind_grads -- from the next step on the gradients are read from
  * grads[0..n) (host array of device pointers; same element types as before).
- * Stream-ordered; the host array may be reused when the call returns. */
+ * Stream-ordered; the host array may be reused when the call returns, also
+ * where the stream is being captured (each replay then binds these again). */
 emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream);
 
 /* adamw_step -- step number `step` >= 1 on every tensor:

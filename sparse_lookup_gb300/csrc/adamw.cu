@@ -342,6 +342,19 @@ __global__ void __launch_bounds__(kAdamThreads) k_adamw_export(const AdamTensor*
   }
 }
 
+// Gradient addresses, by value: a launch holds them itself, whenever it runs (a
+// copy from the host's array would read it later, and again in every replay of
+// a graph).  As many as the 4 KB of arguments that any launch takes.
+constexpr int kBindAtOnce = 480;
+struct AdamBind {
+  const void* grad[kBindAtOnce];
+};
+__global__ void __launch_bounds__(kBindAtOnce) k_adamw_bind(const __grid_constant__ AdamBind a, int n,
+                                                            const void** __restrict__ grads) {
+  const int i = threadIdx.x;
+  if (i < n) grads[i] = a.grad[i];
+}
+
 // A kind of tensors: element types and master decide the kernel.
 using AdamKernel = void (*)(const AdamTensor*, const void* const*, const AdamUnit*, int64_t, AdamScalars, const float*);
 
@@ -495,9 +508,14 @@ extern "C" emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, vo
   if (!h || !grads) return EMB_ERR_INVALID_ARG;
   for (int32_t i = 0; i < h->n; ++i)
     if (h->numel[i] > 0 && (!grads[i] || !aligned_to(grads[i], h->grad_size[i]))) return EMB_ERR_INVALID_ARG;
-  // pageable host memory: the copy has left the array when the call returns
-  return cuda_status(cudaMemcpyAsync((void*)h->grads_d, grads, sizeof(void*) * h->n, cudaMemcpyHostToDevice,
-                                     (cudaStream_t)stream));
+  for (int32_t first = 0; first < h->n; first += kBindAtOnce) {
+    const int32_t left = h->n - first, k = left < kBindAtOnce ? left : kBindAtOnce;
+    AdamBind a{};
+    for (int32_t i = 0; i < k; ++i) a.grad[i] = grads[first + i];
+    k_adamw_bind<<<1, kBindAtOnce, 0, (cudaStream_t)stream>>>(a, k, h->grads_d + first);
+    EMB_CUDA_TRY(cudaGetLastError());
+  }
+  return EMB_OK;
 }
 
 extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,

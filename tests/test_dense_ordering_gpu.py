@@ -72,3 +72,42 @@ def test_reading_the_status_does_not_clear_a_later_error():
         torch.cuda.synchronize()
         assert plan.device_status(stream=side) == 7
     plan.close()
+
+
+@pytest.mark.parametrize("n", [1, 3, 480, 481, 1500])
+def test_bound_gradients_are_those_of_the_call(n):
+    """The host's array of addresses is gone when the call returns; a captured
+    call binds the same gradients in every replay."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    p = [torch.randn(5 + i % 7, generator=gen, device="cuda") for i in range(n)]
+    sets = [[torch.randn(x.shape, generator=gen, device="cuda") for x in p] for _ in range(3)]
+    q = [x.clone() for x in p]
+    a, b = sl.AdamW(p, sets[0]), sl.AdamW(q, sets[0])
+
+    def follow(grads):
+        """b does what a did, with a handle's own first gradients."""
+        for x, y in zip(sets[0], grads):
+            x.copy_(y)
+        b.step(1e-2)
+        assert all(torch.equal(x, y) for x, y in zip(p + a.m + a.v, q + b.m + b.v))
+    first = [x.clone() for x in sets[0]]
+    a.bind_grads(sets[1])
+    a.step(1e-2)
+    follow(sets[1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        a.bind_grads(sets[2])
+    junk = [[k] * 2000 for k in range(200)]   # what was freed is used again
+    for _ in range(3):
+        a.bind_grads(sets[1])
+        graph.replay()
+        a.step(1e-2)
+        follow(sets[2])
+        a.bind_grads(sets[0])
+        for x, y in zip(sets[0], first):
+            x.copy_(y)
+        a.step(1e-2)
+        follow(first)
+    assert len(junk) == 200
