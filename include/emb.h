@@ -565,7 +565,7 @@ emb_status adamw_create(const adamw_tensor* tensors, int32_t n, uint32_t flags, 
  * where the stream is being captured (each replay then binds these again). */
 emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream);
 
-/* adamw_step -- step number `step` >= 1 on every tensor:
+/* adamw_step -- step number `step` on every tensor:
  *   g = grad * (grad_scale ? *grad_scale : 1)
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g g
  *   w = w - lr weight_decay w
@@ -574,9 +574,20 @@ emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream)
  * states are the same bits as the formulas' operations rounded one by one;
  * the weights use the hardware's approximate square root and division (a few
  * ulp of the step).  grad_scale: device fp32 or NULL.
- * Needs lr, eps >= 0 and 0 <= beta < 1, all finite. */
+ * Needs lr, eps >= 0 and 0 <= beta < 1, all finite.
+ * step 0: one more than the handle's last step, counted on the device when the
+ * step runs (one more small launch).  Only such a call may be captured: every
+ * replay is then a step of its own, with its own corrections and noise, and with
+ * the lr, betas, eps, seed and grad_scale address of the capture.  A call that
+ * names its step is refused in a stream that is being captured
+ * (EMB_ERR_UNSUPPORTED): its replays would repeat that step. */
 emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,
                       const float* grad_scale, uint32_t seed, void* stream);
+
+/* The number of the handle's last step (0 at first), read or set in the
+ * stream's order; both synchronize `stream`. */
+emb_status adamw_get_step(emb_adamw h, int64_t* step, void* stream);
+emb_status adamw_set_step(emb_adamw h, int64_t step, void* stream);
 
 /* adamw_export_states -- what 8-bit states stand for, exactly (every value has
  * three bits of fraction), as bf16: m_out, v_out [adamw_export_size] with

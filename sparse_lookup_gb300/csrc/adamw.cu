@@ -13,9 +13,10 @@ constexpr int kAdamThreads = 128;
 constexpr int kExportUnits = 2;
 // CTAs on an SM: as many as hold a block's values without spilling much.
 // Measured with 8-bit states on 128 M weights: bf16 262 us with 10, 267 with 9;
-// bf16 with fp32 masters 365 and 353; 100 M fp32 283 and 248.
-template <class P, bool MASTER>
-constexpr int adam_ctas() { return sizeof(P) == 4 || MASTER ? 9 : 10; }
+// bf16 with fp32 masters 365 and 353; 100 M fp32 283 and 248.  COUNTED calls hold
+// their scalars in registers: bf16 296 with 10, 276 with 9, 325 with 8.
+template <class P, bool MASTER, bool COUNTED>
+constexpr int adam_ctas() { return COUNTED || sizeof(P) == 4 || MASTER ? 9 : 10; }
 
 struct AdamTensor {
   void* param;
@@ -41,7 +42,49 @@ struct AdamScalars {
   float lr, lr_c1, b1, nb1, b2, nb2, c2, eps, one;
   bool flush;            // eps is large enough to drop roots below fp32's normal range
   uint64_t key;          // SplitMix64 output for seed and step
+  int64_t step;
 };
+struct AdamHyper {
+  double lr, beta1, beta2, eps;
+  uint32_t seed;
+};
+// The handle's count of steps, on the device, and the scalars of a step that is
+// counted there.
+struct AdamCount {
+  int64_t step;
+  AdamScalars s;
+};
+
+// b^n by squaring, n >= 0: products alone, the same bits on host and device.
+__host__ __device__ __noinline__ inline double power(double b, int64_t n) {
+  double r = 1.0;
+  for (; n; n >>= 1, b *= b)
+    if (n & 1) r *= b;
+  return r;
+}
+EMB_HD AdamScalars adam_scalars(const AdamHyper& h, int64_t step) {
+  AdamScalars s;
+  s.lr = (float)h.lr;
+  s.b1 = (float)h.beta1;
+  s.nb1 = (float)(1.0 - h.beta1);
+  s.b2 = (float)h.beta2;
+  s.nb2 = (float)(1.0 - h.beta2);
+  s.lr_c1 = (float)(h.lr / (1.0 - power(h.beta1, step)));
+  s.c2 = (float)(1.0 / (1.0 - power(h.beta2, step)));
+  s.eps = (float)h.eps;
+  s.one = 1.f;
+  s.flush = h.eps >= 1e-12;
+  s.key = splitmix64(((uint64_t)h.seed << 32) + (uint64_t)step);
+  s.step = step;
+  return s;
+}
+
+// The next step's number and scalars, counted on the device: where a call is
+// replayed, its host part does not run again.  step > 0 sets the count.
+__global__ void k_adamw_count(AdamHyper h, int64_t step, AdamCount* count) {
+  count->step = step > 0 ? step : count->step + 1;
+  count->s = adam_scalars(h, count->step);
+}
 
 // Places on the 8-bit grid, and back (emb.h).  Codes of eight elements are
 // handled as two words of four bytes.
@@ -289,14 +332,19 @@ __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64
 // blocks in flight for the registers that took, and were slower.  128 M
 // weights: fp32 506 us (7.1 TB/s), 8-bit states with bf16 258 us (4.95 TB/s),
 // with bf16 and masters 350 us (5.9 TB/s).
-template <class P, class G, bool MASTER, bool EIGHT>
-__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adamw(const AdamTensor* __restrict__ tensors,
+// COUNTED: the scalars are k_adamw_count's; otherwise they come as arguments, which
+// cost no registers, and the count follows them.
+template <class P, class G, bool MASTER, bool EIGHT, bool COUNTED>
+__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER, COUNTED>())) k_adamw(const AdamTensor* __restrict__ tensors,
                                                                    const void* const* __restrict__ grads,
                                                                    const AdamUnit* __restrict__ units, int64_t n_units,
-                                                                   const __grid_constant__ AdamScalars s,
+                                                                   const __grid_constant__ AdamScalars given,
+                                                                   AdamCount* __restrict__ count,
                                                                    const float* __restrict__ grad_scale) {
   const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
   if (i >= n_units) return;
+  const AdamScalars& s = COUNTED ? count->s : given;
+  if (!COUNTED && i == 0 && threadIdx.x == 0) count->step = given.step;
   const AdamUnit u = units[i];
   const AdamTensor& t = tensors[u.tensor];
   const G* gp = (const G*)grads[u.tensor];
@@ -356,25 +404,30 @@ __global__ void __launch_bounds__(kBindAtOnce) k_adamw_bind(const __grid_constan
 }
 
 // A kind of tensors: element types and master decide the kernel.
-using AdamKernel = void (*)(const AdamTensor*, const void* const*, const AdamUnit*, int64_t, AdamScalars, const float*);
+using AdamKernel = void (*)(const AdamTensor*, const void* const*, const AdamUnit*, int64_t, AdamScalars, AdamCount*,
+                            const float*);
+struct AdamKernels {
+  AdamKernel given, counted;
+};
 
 template <class P, class G, bool MASTER>
-AdamKernel adam_states(bool eight) {
-  return eight ? (AdamKernel)k_adamw<P, G, MASTER, true> : (AdamKernel)k_adamw<P, G, MASTER, false>;
+AdamKernels adam_states(bool eight) {
+  if (eight) return {k_adamw<P, G, MASTER, true, false>, k_adamw<P, G, MASTER, true, true>};
+  return {k_adamw<P, G, MASTER, false, false>, k_adamw<P, G, MASTER, false, true>};
 }
 template <class P>
-AdamKernel adam_half(bool f32_grad, bool master, bool eight) {
+AdamKernels adam_half(bool f32_grad, bool master, bool eight) {
   if (f32_grad) return master ? adam_states<P, float, true>(eight) : adam_states<P, float, false>(eight);
   return master ? adam_states<P, P, true>(eight) : adam_states<P, P, false>(eight);
 }
-AdamKernel adam_kernel(int32_t dtype, int32_t grad_dtype, bool master, bool eight) {
+AdamKernels adam_kernels(int32_t dtype, int32_t grad_dtype, bool master, bool eight) {
   if (dtype == EMB_DT_F32) return adam_states<float, float, false>(eight);
   if (dtype == EMB_DT_BF16) return adam_half<__nv_bfloat16>(grad_dtype == EMB_DT_F32, master, eight);
   return adam_half<__half>(grad_dtype == EMB_DT_F32, master, eight);
 }
 
 struct AdamKind {
-  AdamKernel kernel;
+  AdamKernels kernels;
   int64_t first, count;   // its units
 };
 
@@ -391,6 +444,7 @@ struct emb_adamw_s {
   emb::AdamTensor* tensors_d = nullptr;
   const void** grads_d = nullptr;
   emb::AdamUnit* units_d = nullptr;
+  emb::AdamCount* count_d = nullptr;
 };
 
 using namespace emb;
@@ -401,6 +455,7 @@ void free_adamw(emb_adamw_s* h) {
   dev_free(h->tensors_d);
   dev_free((void*)h->grads_d);
   dev_free(h->units_d);
+  dev_free(h->count_d);
   delete h;
 }
 
@@ -444,7 +499,7 @@ emb_status create_adamw(const adamw_tensor* tensors, int32_t n, bool eight, emb_
     if (k == kind_key.size()) {
       kind_key.push_back(key);
       of_kind.emplace_back();
-      h->kinds.push_back(AdamKind{adam_kernel(t.dtype, t.grad_dtype, t.master != nullptr, eight), 0, 0});
+      h->kinds.push_back(AdamKind{adam_kernels(t.dtype, t.grad_dtype, t.master != nullptr, eight), 0, 0});
     }
     of_kind[k].push_back(i);
   }
@@ -462,6 +517,8 @@ emb_status create_adamw(const adamw_tensor* tensors, int32_t n, bool eight, emb_
   EMB_CUDA_TRY(dev_alloc((void**)&h->tensors_d, sizeof(AdamTensor) * n));
   EMB_CUDA_TRY(dev_alloc((void**)&h->grads_d, sizeof(void*) * n));
   EMB_CUDA_TRY(dev_alloc((void**)&h->units_d, sizeof(AdamUnit) * (units.empty() ? 1 : units.size())));
+  EMB_CUDA_TRY(dev_alloc((void**)&h->count_d, sizeof(AdamCount)));
+  EMB_CUDA_TRY(cudaMemset(h->count_d, 0, sizeof(AdamCount)));
   EMB_CUDA_TRY(cudaMemcpy(h->tensors_d, meta.data(), sizeof(AdamTensor) * n, cudaMemcpyHostToDevice));
   EMB_CUDA_TRY(cudaMemcpy((void*)h->grads_d, grads.data(), sizeof(void*) * n, cudaMemcpyHostToDevice));
   if (!units.empty())
@@ -520,27 +577,40 @@ extern "C" emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, vo
 
 extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,
                                  const float* grad_scale, uint32_t seed, void* stream) {
-  if (!h || step < 1 || !(lr >= 0) || !(eps >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) ||
+  if (!h || step < 0 || !(lr >= 0) || !(eps >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) ||
       std::isinf(lr) || std::isinf(eps) || !aligned_to(grad_scale, 4))
     return EMB_ERR_INVALID_ARG;
-  AdamScalars s;
-  s.lr = (float)lr;
-  s.b1 = (float)beta1;
-  s.nb1 = (float)(1.0 - beta1);
-  s.b2 = (float)beta2;
-  s.nb2 = (float)(1.0 - beta2);
-  s.lr_c1 = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
-  s.c2 = (float)(1.0 / (1.0 - std::pow(beta2, (double)step)));
-  s.eps = (float)eps;
-  s.one = 1.f;
-  s.flush = eps >= 1e-12;
-  s.key = splitmix64(((uint64_t)seed << 32) + (uint64_t)step);
+  const cudaStream_t st = (cudaStream_t)stream;
+  if (step > 0) {   // a replay would take the same step again
+    cudaStreamCaptureStatus capture;
+    EMB_CUDA_TRY(cudaStreamIsCapturing(st, &capture));
+    if (capture != cudaStreamCaptureStatusNone) return EMB_ERR_UNSUPPORTED;
+  }
+  const AdamHyper hyper{lr, beta1, beta2, eps, seed};
+  AdamScalars s{};
+  if (step > 0) s = adam_scalars(hyper, step);
+  if (step == 0 || h->kinds.empty()) {
+    k_adamw_count<<<1, 1, 0, st>>>(hyper, step, h->count_d);
+    EMB_CUDA_TRY(cudaGetLastError());
+  }
   for (const AdamKind& k : h->kinds) {
-    k.kernel<<<unit_grid(k.count), kAdamThreads, 0, (cudaStream_t)stream>>>(
-        h->tensors_d, h->grads_d, h->units_d + k.first, k.count, s, grad_scale);
+    (step > 0 ? k.kernels.given : k.kernels.counted)<<<unit_grid(k.count), kAdamThreads, 0, st>>>(
+        h->tensors_d, h->grads_d, h->units_d + k.first, k.count, s, h->count_d, grad_scale);
     EMB_CUDA_TRY(cudaGetLastError());
   }
   return EMB_OK;
+}
+
+extern "C" emb_status adamw_get_step(emb_adamw h, int64_t* step, void* stream) {
+  if (!h || !step) return EMB_ERR_INVALID_ARG;
+  EMB_CUDA_TRY(cudaMemcpyAsync(step, &h->count_d->step, sizeof(int64_t), cudaMemcpyDeviceToHost, (cudaStream_t)stream));
+  return cuda_status(cudaStreamSynchronize((cudaStream_t)stream));
+}
+
+extern "C" emb_status adamw_set_step(emb_adamw h, int64_t step, void* stream) {
+  if (!h || step < 0) return EMB_ERR_INVALID_ARG;
+  EMB_CUDA_TRY(cudaMemcpyAsync(&h->count_d->step, &step, sizeof(int64_t), cudaMemcpyHostToDevice, (cudaStream_t)stream));
+  return cuda_status(cudaStreamSynchronize((cudaStream_t)stream));
 }
 
 extern "C" emb_status adamw_export_size(emb_adamw h, int64_t* elements) {

@@ -16,6 +16,7 @@ from ctypes import c_float, c_int32, c_int64, c_void_p
 from . import TABLE_DTYPE, _check, lib, ptr
 
 STATES_8BIT = 1
+UNSUPPORTED = 2      # EMB_ERR_UNSUPPORTED
 BLOCK = 256          # elements that share a top in an 8-bit state
 _ELEMENT = {k: v for k, v in TABLE_DTYPE.items() if k != "int8"}
 _dtype_codes = {}    # torch dtype -> emb_table_dtype
@@ -144,6 +145,16 @@ def adamw_bind_grads(h, grads, stream=None):
 
 def adamw_step(h, step, lr, beta1, beta2, eps, grad_scale, seed, stream=None):
     _check(lib().adamw_step(h, step, lr, beta1, beta2, eps, ptr(grad_scale), seed, _stream(stream)), "adamw_step")
+
+
+def adamw_get_step(h, stream=None):
+    n = c_int64()
+    _check(lib().adamw_get_step(h, ctypes.byref(n), _stream(stream)), "adamw_get_step")
+    return n.value
+
+
+def adamw_set_step(h, step, stream=None):
+    _check(lib().adamw_set_step(h, step, _stream(stream)), "adamw_set_step")
 
 
 def adamw_export_states(h, m_out, v_out, stream=None):
@@ -477,7 +488,12 @@ class AdamW(_Handle):
     weight_decay is a number or one per tensor.  state_bits 32: m and v are
     float32 tensors shaped like the params; 8: uint8 codes of that shape and
     int16 tops, one per 256 elements (``m``, ``v``, ``m_top``, ``v_top``; created
-    at zero, or given).  step: steps already taken."""
+    at zero, or given).  step: steps already taken.
+
+    A step may be captured in a graph: each replay is a step of its own, counted
+    on the device, with the lr and grad_scale tensor of the capture.  From then
+    on every step of the handle is counted there (a launch more), and reading
+    step_count waits for the current stream."""
 
     _destroy = staticmethod(adamw_destroy)
 
@@ -485,7 +501,7 @@ class AdamW(_Handle):
                  m=None, v=None, m_top=None, v_top=None, seed=0, step=0):
         super().__init__()
         torch = self._t
-        self.params, self.betas, self.eps, self.seed, self.step_count = list(params), betas, eps, seed, step
+        self.params, self.betas, self.eps, self.seed = list(params), betas, eps, seed
         self.grads = list(grads)
         self.masters = list(masters) if masters is not None else [None] * len(self.params)
         n = len(self.params)
@@ -525,6 +541,21 @@ class AdamW(_Handle):
         self.handle = adamw_create(_tensors(fields, n), STATES_8BIT if eight else 0)
         self._device = self.params[0].device.index
         self._step, self._size = lib().adamw_step, adamw_export_size(self.handle)
+        self._taken, self._counted = 0, False   # steps, where the host counts them
+        if step:
+            self.step_count = step
+
+    @property
+    def step_count(self):
+        """Steps taken; may be set."""
+        if self._counted:
+            return adamw_get_step(self.handle, _stream(None, self._device))
+        return self._taken
+
+    @step_count.setter
+    def step_count(self, step):
+        adamw_set_step(self.handle, step, _stream(None, self._device))
+        self._taken = step
 
     def bind_grads(self, grads, stream=None):
         """Read other gradient tensors (same shapes and types) from the next
@@ -543,12 +574,19 @@ class AdamW(_Handle):
         if grad_scale is not None:
             if grad_scale.numel() != 1 or not grad_scale.is_cuda or grad_scale.dtype != self._t.float32:
                 raise ValueError("grad_scale: one float32 on the GPU")
-        st = self._step(self.handle, self.step_count + 1, lr, self.betas[0], self.betas[1], self.eps,
-                        None if grad_scale is None else grad_scale.data_ptr(), self.seed,
-                        _stream(stream, self._device))
+        args = (lr, self.betas[0], self.betas[1], self.eps, None if grad_scale is None else grad_scale.data_ptr(),
+                self.seed, _stream(stream, self._device))
+        if not self._counted:
+            st = self._step(self.handle, self._taken + 1, *args)
+            if not st:
+                self._taken += 1
+                return
+            if st != UNSUPPORTED:
+                _check(st, "adamw_step")
+            self._counted = True   # the stream is being captured
+        st = self._step(self.handle, 0, *args)
         if st:
             _check(st, "adamw_step")
-        self.step_count += 1
 
     def states(self, stream=None):
         """What the 8-bit states stand for: (m, v), bfloat16 (exact), tensor
