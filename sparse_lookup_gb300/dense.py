@@ -26,6 +26,9 @@ class ScanView(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("time_stride", c_int64)]
 
 
+_Views = c_int64 * 18   # a call's scan_views, one after the other: each call has its own
+
+
 class AdamwTensor(ctypes.Structure):
     _fields_ = [("param", c_void_p), ("grad", c_void_p), ("master", c_void_p), ("m", c_void_p), ("v", c_void_p),
                 ("m_top", c_void_p), ("v_top", c_void_p), ("numel", c_int64), ("weight_decay", c_float),
@@ -248,10 +251,6 @@ class GatedScan(_Handle):
         self.handle = scan_create(dim, max_batch, max_len)
         L = lib()
         self._fwd, self._bwd, self._step = L.scan_forward, L.scan_backward, L.scan_step
-        # the views of a call, rewritten by each call and read before it returns
-        self._views = (c_int64 * 18)()
-        at = ctypes.addressof(self._views)
-        self._view_at = [at + 24 * i for i in range(6)]
 
     def _view(self, t, name, shape, dtype):
         """(pointer, batch stride, time stride) of a [batch, time, dim] tensor."""
@@ -283,9 +282,9 @@ class GatedScan(_Handle):
             y = self._empty(shape, dt, x, stream)
         if last is None:
             last = self._empty(ends, self._f32, x, stream)
-        self._views[0:9] = views + self._view(y, "y", shape, dt)
-        v = self._view_at
-        st = self._fwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2],
+        held = _Views(*views, *self._view(y, "y", shape, dt))
+        v = ctypes.addressof(held)
+        st = self._fwd(self.handle, shape[0], shape[1], code, v, v + 24, o, s, v + 48,
                        _want(last, "last", ends, self._f32), _stream(stream, dev.index))
         if st:
             _check(st, "scan_forward")
@@ -305,10 +304,10 @@ class GatedScan(_Handle):
             grad_gate = self._empty(shape, dt, x, stream)
         if grad_state is None:
             grad_state = self._empty(ends, f32, x, stream)
-        self._views[:] = (views + self._view(y, "y", shape, dt) + self._view(grad_y, "grad_y", shape, dt) +
-                          self._view(grad_x, "grad_x", shape, dt) + self._view(grad_gate, "grad_gate", shape, dt))
-        v = self._view_at
-        st = self._bwd(self.handle, shape[0], shape[1], code, v[0], v[1], o, s, v[2], v[3], gl, v[4], v[5],
+        held = _Views(*views, *self._view(y, "y", shape, dt), *self._view(grad_y, "grad_y", shape, dt),
+                      *self._view(grad_x, "grad_x", shape, dt), *self._view(grad_gate, "grad_gate", shape, dt))
+        v = ctypes.addressof(held)
+        st = self._bwd(self.handle, shape[0], shape[1], code, v, v + 24, o, s, v + 48, v + 72, gl, v + 96, v + 120,
                        _want(grad_state, "grad_state", ends, f32), _stream(stream, dev.index))
         if st:
             _check(st, "scan_backward")
