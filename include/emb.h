@@ -404,7 +404,9 @@ emb_status emb_noalloc_get_device_status(void* stream);
  * of 16 bits is rounded once, when it is stored.  Pointers need the alignment
  * of their element; rows whose pointers, strides and sizes are multiples of
  * 16 bytes move in 16-byte accesses.  Outputs must not overlap inputs or
- * each other. */
+ * each other.  A handle belongs to the device that was current when it was
+ * created: calls while another one is are refused, and every pointer of a call is
+ * that device's. */
 
 typedef struct emb_scan_s* emb_scan;
 

@@ -435,6 +435,7 @@ struct AdamKind {
 
 struct emb_adamw_s {
   int32_t n = 0;
+  int device = 0;
   bool eight = false;
   int64_t elements = 0;                 // of the padded order
   int64_t n_units = 0;
@@ -514,6 +515,7 @@ emb_status create_adamw(const adamw_tensor* tensors, int32_t n, bool eight, emb_
     h->kinds[k].count = (int64_t)units.size() - h->kinds[k].first;
   }
   h->n_units = (int64_t)units.size();
+  EMB_CUDA_TRY(cudaGetDevice(&h->device));
   EMB_CUDA_TRY(dev_alloc((void**)&h->tensors_d, sizeof(AdamTensor) * n));
   EMB_CUDA_TRY(dev_alloc((void**)&h->grads_d, sizeof(void*) * n));
   EMB_CUDA_TRY(dev_alloc((void**)&h->units_d, sizeof(AdamUnit) * (units.empty() ? 1 : units.size())));
@@ -562,7 +564,7 @@ extern "C" emb_status adamw_destroy(emb_adamw h) {
 }
 
 extern "C" emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream) {
-  if (!h || !grads) return EMB_ERR_INVALID_ARG;
+  if (!h || !grads || !on_device(h->device)) return EMB_ERR_INVALID_ARG;
   for (int32_t i = 0; i < h->n; ++i)
     if (h->numel[i] > 0 && (!grads[i] || !aligned_to(grads[i], h->grad_size[i]))) return EMB_ERR_INVALID_ARG;
   for (int32_t first = 0; first < h->n; first += kBindAtOnce) {
@@ -578,7 +580,7 @@ extern "C" emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, vo
 extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,
                                  const float* grad_scale, uint32_t seed, void* stream) {
   if (!h || step < 0 || !(lr >= 0) || !(eps >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) ||
-      std::isinf(lr) || std::isinf(eps) || !aligned_to(grad_scale, 4))
+      std::isinf(lr) || std::isinf(eps) || !aligned_to(grad_scale, 4) || !on_device(h->device))
     return EMB_ERR_INVALID_ARG;
   const cudaStream_t st = (cudaStream_t)stream;
   if (step > 0) {   // a replay would take the same step again
@@ -620,7 +622,7 @@ extern "C" emb_status adamw_export_size(emb_adamw h, int64_t* elements) {
 }
 
 extern "C" emb_status adamw_export_states(emb_adamw h, void* m_out, void* v_out, void* stream) {
-  if (!h) return EMB_ERR_INVALID_ARG;
+  if (!h || !on_device(h->device)) return EMB_ERR_INVALID_ARG;
   if (!h->eight) return EMB_ERR_UNSUPPORTED;
   if (h->n_units == 0) return EMB_OK;
   if (!m_out || !v_out || !aligned16(m_out) || !aligned16(v_out)) return EMB_ERR_INVALID_ARG;

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kRowThreads, kBwdCtas) k_combine_bwd(RowArgs a
 struct emb_moe_s {
   int32_t n_experts = 0, top_k = 0, align = 1;
   int64_t max_tokens = 0;
-  int sm_count = 0;
+  int sm_count = 0, device = 0;
   uint32_t* part = nullptr;
 };
 
@@ -376,7 +376,8 @@ int64_t rows_of(const emb_moe_s* h, int64_t n) {
 }
 
 bool rows_ok(emb_moe h, int64_t n, int32_t dim, int32_t dtype) {
-  return h && n >= 0 && n <= h->max_tokens && dim >= 1 && dim <= (1 << 20) && dtype_size(dtype) != 0;
+  return h && n >= 0 && n <= h->max_tokens && dim >= 1 && dim <= (1 << 20) && dtype_size(dtype) != 0 &&
+         on_device(h->device);
 }
 
 // Largest access, in elements, that divides the row, both strides and every
@@ -434,9 +435,8 @@ extern "C" emb_status moe_create(int32_t n_experts, int32_t top_k, int64_t max_t
   h->top_k = top_k;
   h->align = align;
   h->max_tokens = max_tokens;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) e = dev_alloc((void**)&h->part, sizeof(uint32_t) * h->sm_count * n_experts);
   for (auto k : {k_route_place<true>, k_route_place<false>})
     if (e == cudaSuccess)
@@ -461,7 +461,7 @@ extern "C" emb_status moe_destroy(emb_moe h) {
 
 extern "C" emb_status moe_route(emb_moe h, int64_t n, const int32_t* experts, int32_t* offsets, int32_t* counts,
                                 int32_t* pos, int32_t* src, void* stream) {
-  if (!h || n < 0 || n > h->max_tokens || !offsets || !counts || (n > 0 && (!experts || !pos)) ||
+  if (!h || n < 0 || n > h->max_tokens || !on_device(h->device) || !offsets || !counts || (n > 0 && (!experts || !pos)) ||
       (rows_of(h, n) > 0 && !src))
     return EMB_ERR_INVALID_ARG;
   for (const void* p : {(const void*)experts, (const void*)offsets, (const void*)counts, (const void*)pos, (const void*)src})

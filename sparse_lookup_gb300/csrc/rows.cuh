@@ -103,6 +103,12 @@ inline int dtype_size(int32_t dtype) {
   return dtype == EMB_DT_F32 ? 4 : dtype == EMB_DT_BF16 || dtype == EMB_DT_F16 ? 2 : 0;
 }
 
+// A handle's calls run on the device that it was created on.
+inline bool on_device(int device) {
+  int now = -1;
+  return cudaGetDevice(&now) == cudaSuccess && now == device;
+}
+
 inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 
 // Calls f with a null pointer of the element type `dtype` names.

@@ -1,5 +1,6 @@
 // scan.cu -- gated linear recurrence over padded sequences, forward, backward
 // and one position at a time (scan_* in emb.h).
+#include <atomic>
 #include <new>
 
 #include "rows.cuh"
@@ -19,7 +20,7 @@ struct ScanShared {
 
 struct emb_scan_s {
   int32_t dim = 0, max_batch = 0, max_len = 0;
-  int sm_count = 0;
+  int sm_count = 0, device = 0;
   int64_t max_records = 0;
   uint32_t* status_d = nullptr;
   emb::ScanShared* shared_d = nullptr;
@@ -1035,7 +1036,8 @@ View<T> as_view(const scan_view* v) {
 }
 
 bool call_ok(emb_scan h, int32_t batch, int32_t len, int32_t dtype) {
-  return h && batch >= 0 && batch <= h->max_batch && len >= 0 && len <= h->max_len && dtype_size(dtype) != 0;
+  return h && batch >= 0 && batch <= h->max_batch && len >= 0 && len <= h->max_len && dtype_size(dtype) != 0 &&
+         on_device(h->device);
 }
 
 // How a call is cut.  R: positions of a thread.
@@ -1044,6 +1046,7 @@ struct Cut {
   bool chain, fits;
   bool follows;   // launched as the dependant of the kernel ahead of it
   unsigned grid;
+  int device;
 };
 
 // Positions of a thread, as many as its registers hold, for V = 4, 2 and 1
@@ -1135,6 +1138,7 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   // the records were sized for this call when the handle was made; a cut that does not fit them is not launched
   c.fits = !c.chain || chain_records(TT, a.pitch, len) <= h->max_records;
   const int64_t all = groups * a.tiles;
+  c.device = h->device;
   c.grid = (unsigned)(c.chain && all >= slots ? slots : c.chain ? all : groups);
   return c;
 }
@@ -1168,11 +1172,16 @@ unsigned short_grid(const Cut& c) { return (unsigned)((c.args.vecs + 127) / 128)
 template <int V, auto kernel, class... A>
 cudaError_t launch(const Cut& c, size_t staged, int areas, cudaStream_t stream, A... a) {
   constexpr int kMostShared = 100 << 10;   // of each of the CTAs that share an SM
-  static const cudaError_t room =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+  // the limit is set once per kernel and device (one bit each), when it has been set
+  static std::atomic<uint64_t> set{0};
+  const uint64_t mine = c.device < 64 ? uint64_t(1) << c.device : 0;
+  if (!(set.load(std::memory_order_relaxed) & mine)) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostShared);
+    if (e != cudaSuccess) return e;
+    set.fetch_or(mine, std::memory_order_relaxed);
+  }
   const size_t smem = staged + (size_t)areas * (kScanThreads >> c.args.cx_log) * ((V << c.args.cx_log) + 1) *
                                    sizeof(float);
-  if (room != cudaSuccess) return room;
   if (!c.fits || smem > kMostShared) return cudaErrorNotSupported;
   if (c.follows) return launch_dependent(kernel, c.grid, kScanThreads, smem, stream, c.args, a...);
   kernel<<<c.grid, kScanThreads, smem, stream>>>(c.args, a...);
@@ -1243,9 +1252,8 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   h->dim = dim;
   h->max_batch = max_batch;
   h->max_len = max_len;
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, dev);
+  cudaError_t e = cudaGetDevice(&h->device);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) {
     // a call with more channels than this walks
     const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 * 2 + dim, all = (int64_t)max_batch * dim;
