@@ -2,7 +2,8 @@
 of include/emb.h): raw C names, then GatedScan, ExpertRouter and AdamW over
 PyTorch tensors.  Marshalling only, like the rest of the binding; arguments
 that the library cannot see (shapes, element types, devices) are checked here
-and raise ValueError.
+and raise ValueError: every tensor of a call, its stream and the current device
+are those of the handle, which is the device that was current when it was made.
 
 An output that a call allocates belongs to the stream the call runs on.
 Tensors that come from another stream are the caller's to order (an event, or
@@ -188,12 +189,12 @@ def _element(dtype):
     return code
 
 
-def _want(t, name, shape, dtype, dense=True):
-    """Checks one tensor argument -- on the GPU, of this shape and type, dense
+def _want(t, name, shape, dtype, device, dense=True):
+    """Checks one tensor argument -- on this GPU, of this shape and type, dense
     (or only its last axis contiguous) -- and returns its pointer."""
-    if t.dtype is not dtype or t.shape != shape or not t.is_cuda:
-        raise ValueError("%s: %s %s on the GPU expected, got %s %s on %s" % (
-            name, tuple(shape), dtype, tuple(t.shape), t.dtype, t.device))
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device:
+        raise ValueError("%s: %s %s on cuda:%d expected, got %s %s on %s" % (
+            name, tuple(shape), dtype, device, tuple(t.shape), t.dtype, t.device))
     if not t.is_contiguous():
         if dense:
             raise ValueError("%s: a contiguous tensor expected, got strides %s" % (name, t.stride()))
@@ -208,6 +209,25 @@ class _Handle:
     def __init__(self):
         import torch
         self._t, self._f32, self._i32, self._new = torch, torch.float32, torch.int32, torch.empty
+        self._current = torch._C._cuda_getDevice
+
+    def _made(self, handle):
+        """The handle belongs to the device that is current now."""
+        self.handle, self._device = handle, self._current()
+
+    def _want(self, t, name, shape, dtype, dense=True):
+        return _want(t, name, shape, dtype, self._device, dense)
+
+    def _at(self, stream):
+        """The raw stream of a call (None: the current one)."""
+        device = self._device
+        if self._current() != device:
+            raise ValueError("a handle of cuda:%d, but cuda:%d is the current device" % (device, self._current()))
+        if stream is None or isinstance(stream, int):
+            return _stream(stream, device)
+        if stream.device_index != device:
+            raise ValueError("a handle of cuda:%d, but a stream of cuda:%d" % (device, stream.device_index))
+        return stream.cuda_stream
 
     def close(self):
         if self.handle:
@@ -248,13 +268,13 @@ class GatedScan(_Handle):
     def __init__(self, dim, max_batch, max_len):
         super().__init__()
         self.dim = dim
-        self.handle = scan_create(dim, max_batch, max_len)
+        self._made(scan_create(dim, max_batch, max_len))
         L = lib()
         self._fwd, self._bwd, self._step = L.scan_forward, L.scan_backward, L.scan_step
 
     def _view(self, t, name, shape, dtype):
         """(pointer, batch stride, time stride) of a [batch, time, dim] tensor."""
-        p = _want(t, name, shape, dtype, False)
+        p = self._want(t, name, shape, dtype, False)
         if t.is_contiguous():
             return p, shape[1] * shape[2], shape[2]
         sb, st, _ = t.stride()
@@ -268,15 +288,16 @@ class GatedScan(_Handle):
         if code is None:
             code = _element(dt)
         B = shape[0]
-        return (code, dt, shape, x.device, None if offsets is None else _want(offsets, "offsets", (B + 1,), self._i32),
-                None if state is None else _want(state, "state", (B, self.dim), self._f32),
+        return (code, dt, shape,
+                None if offsets is None else self._want(offsets, "offsets", (B + 1,), self._i32),
+                None if state is None else self._want(state, "state", (B, self.dim), self._f32),
                 self._view(x, "x", shape, dt) + self._view(gate, "gate", shape, dt))
 
     def forward(self, x, gate, offsets=None, state=None, y=None, last=None, stream=None):
         """(y, last): h_t at every position, and the state [batch, dim]
         float32 after the last live one.  state: the one before the first
         (None = 0).  y and last may be given."""
-        code, dt, shape, dev, o, s, views = self._common(x, gate, offsets, state)
+        code, dt, shape, o, s, views = self._common(x, gate, offsets, state)
         ends = (shape[0], shape[2])
         if y is None:
             y = self._empty(shape, dt, x, stream)
@@ -285,7 +306,7 @@ class GatedScan(_Handle):
         held = _Views(*views, *self._view(y, "y", shape, dt))
         v = ctypes.addressof(held)
         st = self._fwd(self.handle, shape[0], shape[1], code, v, v + 24, o, s, v + 48,
-                       _want(last, "last", ends, self._f32), _stream(stream, dev.index))
+                       self._want(last, "last", ends, self._f32), self._at(stream))
         if st:
             _check(st, "scan_forward")
         return y, last
@@ -295,9 +316,9 @@ class GatedScan(_Handle):
         """(grad_x, grad_gate, grad_state) from the gradients of y and (None =
         0) of last; x, gate, offsets and state as in forward, y as it gave
         it.  The results may be given."""
-        code, dt, shape, dev, o, s, views = self._common(x, gate, offsets, state)
+        code, dt, shape, o, s, views = self._common(x, gate, offsets, state)
         f32, ends = self._f32, (shape[0], shape[2])
-        gl = None if grad_last is None else _want(grad_last, "grad_last", ends, f32)
+        gl = None if grad_last is None else self._want(grad_last, "grad_last", ends, f32)
         if grad_x is None:
             grad_x = self._empty(shape, dt, x, stream)
         if grad_gate is None:
@@ -308,7 +329,7 @@ class GatedScan(_Handle):
                       *self._view(grad_x, "grad_x", shape, dt), *self._view(grad_gate, "grad_gate", shape, dt))
         v = ctypes.addressof(held)
         st = self._bwd(self.handle, shape[0], shape[1], code, v, v + 24, o, s, v + 48, v + 72, gl, v + 96, v + 120,
-                       _want(grad_state, "grad_state", ends, f32), _stream(stream, dev.index))
+                       self._want(grad_state, "grad_state", ends, f32), self._at(stream))
         if st:
             _check(st, "scan_backward")
         return grad_x, grad_gate, grad_state
@@ -321,19 +342,20 @@ class GatedScan(_Handle):
         shape, dt, D = x.shape, x.dtype, self.dim
         if len(shape) != 2 or shape[1] != D or states.dim() != 2:
             raise ValueError("x: [n, %d] and states [num_rows, %d] expected" % (D, D))
-        n, pool, dev = shape[0], states.shape[0], x.device
+        n, pool = shape[0], states.shape[0]
         if y is None:
             y = self._empty(shape, dt, x, stream)
-        st = self._step(n, D, _element(dt), _want(x, "x", shape, dt, False), x.stride(0),
-                        _want(gate, "gate", shape, dt, False), gate.stride(0),
-                        _want(rows, "rows", (n,), self._t.int64), _want(states, "states", (pool, D), self._f32), pool,
-                        _want(y, "y", shape, dt, False), y.stride(0), _stream(stream, dev.index))
+        st = self._step(n, D, _element(dt), self._want(x, "x", shape, dt, False), x.stride(0),
+                        self._want(gate, "gate", shape, dt, False), gate.stride(0),
+                        self._want(rows, "rows", (n,), self._t.int64),
+                        self._want(states, "states", (pool, D), self._f32), pool,
+                        self._want(y, "y", shape, dt, False), y.stride(0), self._at(stream))
         if st:
             _check(st, "scan_step")
         return y
 
     def device_status(self, stream=None):
-        return scan_get_device_status(self.handle, stream)
+        return scan_get_device_status(self.handle, self._at(stream))
 
 
 class Routing:
@@ -347,10 +369,13 @@ class Routing:
 
     def __init__(self, offsets, counts, pos, src):
         import torch
+        if not offsets.is_cuda or pos.dim() != 2:
+            raise ValueError("a routing's arrays: on the GPU expected, and pos [tokens, top_k]")
+        device = offsets.get_device()
         for t, name in ((offsets, "offsets"), (counts, "counts"), (pos, "pos"), (src, "src")):
-            _want(t, name, t.shape, torch.int32)
+            _want(t, name, t.shape, torch.int32, device)
         self._arrays = (offsets, counts, pos, src)
-        self._at, self._shape = (pos.data_ptr(), src.data_ptr()), (*pos.shape, src.numel())
+        self._at, self._shape = (pos.data_ptr(), src.data_ptr()), (*pos.shape, src.numel(), device)
 
     def __iter__(self):
         return iter(self._arrays)
@@ -378,7 +403,7 @@ class ExpertRouter(_Handle):
     def __init__(self, n_experts, top_k, max_tokens, align=1):
         super().__init__()
         self.n_experts, self.top_k, self.align = n_experts, top_k, align
-        self.handle = moe_create(n_experts, top_k, max_tokens, align)
+        self._made(moe_create(n_experts, top_k, max_tokens, align))
         L = lib()
         self._route, self._dispatch, self._combine = L.moe_route, L.moe_dispatch, L.moe_combine
         self._combine_backward = L.moe_combine_backward
@@ -394,29 +419,30 @@ class ExpertRouter(_Handle):
         shape, i32, E = experts.shape, self._i32, self.n_experts
         if len(shape) != 2:
             raise ValueError("experts: [tokens, %d] expected, got %s" % (self.top_k, tuple(shape)))
-        n, dev = shape[0], experts.device
+        n = shape[0]
         pos = (n, self.top_k)
-        e = _want(experts, "experts", pos, i32)
+        e = self._want(experts, "experts", pos, i32)
         rows = self.rows(n)
         offsets, counts = self._empty((E + 1,), i32, experts, stream), self._empty((E,), i32, experts, stream)
         pos, src = self._empty(pos, i32, experts, stream), self._empty((rows,), i32, experts, stream)
         at = (pos.data_ptr(), src.data_ptr())
         st = self._route(self.handle, n, e, offsets.data_ptr(), counts.data_ptr(), at[0], at[1],
-                         _stream(stream, dev.index))
+                         self._at(stream))
         if st:
             _check(st, "moe_route")
-        return Routing._made(offsets, counts, pos, src, at, (n, self.top_k, rows))
+        return Routing._made(offsets, counts, pos, src, at, (n, self.top_k, rows, self._device))
 
     def _routed(self, n, r):
         """(pointer of pos, pointer of src, rows) of a routing of n tokens."""
-        m, k, rows = r._shape
-        if m != n or k != self.top_k or rows != self.rows(n):
-            raise ValueError("routing: of %d tokens by %d and %d rows, for %d tokens" % (m, k, rows, n))
+        m, k, rows, device = r._shape
+        if m != n or k != self.top_k or rows != self.rows(n) or device != self._device:
+            raise ValueError("routing: of %d tokens by %d and %d rows on cuda:%d, for %d tokens" % (
+                m, k, rows, device, n))
         return r._at[0], r._at[1], rows
 
     def dispatch(self, x, routing, xs=None, stream=None):
         """xs [rows, dim]: the token of each row; padding rows are 0."""
-        shape, dt, dev = x.shape, x.dtype, x.device
+        shape, dt = x.shape, x.dtype
         if len(shape) != 2:
             raise ValueError("x: [tokens, dim] expected, got %s" % (tuple(shape),))
         n, dim = shape
@@ -425,9 +451,9 @@ class ExpertRouter(_Handle):
             xs = self._empty((rows, dim), dt, x, stream)
             to = xs.data_ptr()
         else:
-            to = _want(xs, "xs", (rows, dim), dt)
-        st = self._dispatch(self.handle, n, dim, _element(dt), _want(x, "x", shape, dt, False), x.stride(0), pos, src,
-                            to, _stream(stream, dev.index))
+            to = self._want(xs, "xs", (rows, dim), dt)
+        st = self._dispatch(self.handle, n, dim, _element(dt), self._want(x, "x", shape, dt, False), x.stride(0),
+                            pos, src, to, self._at(stream))
         if st:
             _check(st, "moe_dispatch")
         return xs
@@ -435,19 +461,19 @@ class ExpertRouter(_Handle):
     def combine(self, ys, weights, routing, y=None, stream=None):
         """y [tokens, dim]: the sum of each token's rows of ys, each times its
         weight ([tokens, top_k] float32; None = 1)."""
-        shape, dt, dev = ys.shape, ys.dtype, ys.device
+        shape, dt = ys.shape, ys.dtype
         if len(shape) != 2:
             raise ValueError("ys: [rows, dim] expected, got %s" % (tuple(shape),))
         n, dim = routing._shape[0], shape[1]
         pos, _, rows = self._routed(n, routing)
-        w = None if weights is None else _want(weights, "weights", (n, self.top_k), self._f32)
+        w = None if weights is None else self._want(weights, "weights", (n, self.top_k), self._f32)
         if y is None:
             y = self._empty((n, dim), dt, ys, stream)
             to, stride = y.data_ptr(), dim
         else:
-            to, stride = _want(y, "y", (n, dim), dt, False), y.stride(0)
-        st = self._combine(self.handle, n, dim, _element(dt), _want(ys, "ys", (rows, dim), dt), w, pos, to, stride,
-                           _stream(stream, dev.index))
+            to, stride = self._want(y, "y", (n, dim), dt, False), y.stride(0)
+        st = self._combine(self.handle, n, dim, _element(dt), self._want(ys, "ys", (rows, dim), dt), w, pos, to, stride,
+                           self._at(stream))
         if st:
             _check(st, "moe_combine")
         return y
@@ -455,21 +481,21 @@ class ExpertRouter(_Handle):
     def combine_backward(self, grad_y, ys, weights, routing, grad_ys=None, grad_weights=None, stream=None):
         """(grad_ys, grad_weights) of combine; weights None gives grad_weights
         None."""
-        shape, dt, dev, f32 = grad_y.shape, grad_y.dtype, grad_y.device, self._f32
+        shape, dt, f32 = grad_y.shape, grad_y.dtype, self._f32
         if len(shape) != 2:
             raise ValueError("grad_y: [tokens, dim] expected, got %s" % (tuple(shape),))
         n, dim = shape
         pos, src, rows = self._routed(n, routing)
         wide, each = (rows, dim), (n, self.top_k)
-        w = None if weights is None else _want(weights, "weights", each, f32)
+        w = None if weights is None else self._want(weights, "weights", each, f32)
         if weights is not None and grad_weights is None:
             grad_weights = self._empty(each, f32, weights, stream)
-        gw = None if grad_weights is None else _want(grad_weights, "grad_weights", each, f32)
+        gw = None if grad_weights is None else self._want(grad_weights, "grad_weights", each, f32)
         if grad_ys is None:
             grad_ys = self._empty(wide, dt, grad_y, stream)
-        st = self._combine_backward(self.handle, n, dim, _element(dt), _want(grad_y, "grad_y", shape, dt, False),
-                                    grad_y.stride(0), _want(ys, "ys", wide, dt), w, pos, src,
-                                    _want(grad_ys, "grad_ys", wide, dt), gw, _stream(stream, dev.index))
+        st = self._combine_backward(self.handle, n, dim, _element(dt), self._want(grad_y, "grad_y", shape, dt, False),
+                                    grad_y.stride(0), self._want(ys, "ys", wide, dt), w, pos, src,
+                                    self._want(grad_ys, "grad_ys", wide, dt), gw, self._at(stream))
         if st:
             _check(st, "moe_combine_backward")
         return grad_ys, grad_weights
@@ -512,12 +538,13 @@ class AdamW(_Handle):
         self.state_bits = state_bits
         eight = state_bits == 8
         state = torch.uint8 if eight else torch.float32
+        self._device = self._current()
         shapes = [p.shape for p in self.params]
         blocks = [_blocks(p) for p in self.params] if eight else None
-        fields = {"param": [_want(p, "params", k, p.dtype) for p, k in zip(self.params, shapes)],
-                  "grad": [_want(g, "grads", k, p.dtype if g.dtype is p.dtype else torch.float32)
+        fields = {"param": [self._want(p, "params", k, p.dtype) for p, k in zip(self.params, shapes)],
+                  "grad": [self._want(g, "grads", k, p.dtype if g.dtype is p.dtype else torch.float32)
                            for g, p, k in zip(self.grads, self.params, shapes)],
-                  "master": [0 if w is None else _want(w, "masters", k, torch.float32)
+                  "master": [0 if w is None else self._want(w, "masters", k, torch.float32)
                              for w, k in zip(self.masters, shapes)]}
         for given, name, dtype, sizes in ((m, "m", state, shapes), (v, "v", state, shapes),
                                           (m_top, "m_top", torch.int16, blocks), (v_top, "v_top", torch.int16, blocks)):
@@ -530,15 +557,14 @@ class AdamW(_Handle):
                     if given is None else list(given))
             if len(held) != n:
                 raise ValueError("%s: one per parameter" % name)
-            fields[name] = [_want(t, name, k, dtype) for t, k in zip(held, sizes)]
+            fields[name] = [self._want(t, name, k, dtype) for t, k in zip(held, sizes)]
             setattr(self, name, held)
         fields["numel"] = [p.numel() for p in self.params]
         fields["weight_decay"] = decay
         fields["dtype"] = [_element(p.dtype) for p in self.params]
         fields["grad_dtype"] = [_element(g.dtype) for g in self.grads]
         self._grad_dtypes = [g.dtype for g in self.grads]
-        self.handle = adamw_create(_tensors(fields, n), STATES_8BIT if eight else 0)
-        self._device = self.params[0].device.index
+        self._made(adamw_create(_tensors(fields, n), STATES_8BIT if eight else 0))
         self._step, self._size = lib().adamw_step, adamw_export_size(self.handle)
         self._taken, self._counted = 0, False   # steps, where the host counts them
         if step:
@@ -548,12 +574,12 @@ class AdamW(_Handle):
     def step_count(self):
         """Steps taken; may be set."""
         if self._counted:
-            return adamw_get_step(self.handle, _stream(None, self._device))
+            return adamw_get_step(self.handle, self._at(None))
         return self._taken
 
     @step_count.setter
     def step_count(self, step):
-        adamw_set_step(self.handle, step, _stream(None, self._device))
+        adamw_set_step(self.handle, step, self._at(None))
         self._taken = step
 
     def bind_grads(self, grads, stream=None):
@@ -563,18 +589,19 @@ class AdamW(_Handle):
         if len(grads) != len(self.params):
             raise ValueError("one gradient per parameter")
         for i, g in enumerate(grads):
-            _want(g, "grads", self.params[i].shape, self._grad_dtypes[i])
-        adamw_bind_grads(self.handle, grads, stream)
+            self._want(g, "grads", self.params[i].shape, self._grad_dtypes[i])
+        adamw_bind_grads(self.handle, grads, self._at(stream))
         self.grads = grads
 
     def step(self, lr, grad_scale=None, stream=None):
         """One step on every parameter.  grad_scale: a float32 scalar tensor
         on the GPU that every gradient is multiplied by."""
         if grad_scale is not None:
-            if grad_scale.numel() != 1 or not grad_scale.is_cuda or grad_scale.dtype != self._t.float32:
-                raise ValueError("grad_scale: one float32 on the GPU")
+            if (grad_scale.numel() != 1 or grad_scale.get_device() != self._device or
+                    grad_scale.dtype != self._t.float32):
+                raise ValueError("grad_scale: one float32 on cuda:%d" % self._device)
         args = (lr, self.betas[0], self.betas[1], self.eps, None if grad_scale is None else grad_scale.data_ptr(),
-                self.seed, _stream(stream, self._device))
+                self.seed, self._at(stream))
         if not self._counted:
             st = self._step(self.handle, self._taken + 1, *args)
             if not st:
@@ -593,7 +620,7 @@ class AdamW(_Handle):
         between them."""
         like, bf16 = self.params[0], self._t.bfloat16
         m, v = self._empty((self._size,), bf16, like, stream), self._empty((self._size,), bf16, like, stream)
-        adamw_export_states(self.handle, m, v, _stream(stream, self._device))
+        adamw_export_states(self.handle, m, v, self._at(stream))
         return m, v
 
 
