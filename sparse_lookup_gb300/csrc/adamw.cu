@@ -13,10 +13,9 @@ constexpr int kAdamThreads = 128;
 constexpr int kExportUnits = 2;
 // CTAs on an SM: as many as hold a block's values without spilling much.
 // Measured with 8-bit states on 128 M weights: bf16 262 us with 10, 267 with 9;
-// bf16 with fp32 masters 365 and 353; 100 M fp32 283 and 248.  COUNTED calls hold
-// their scalars in registers: bf16 296 with 10, 276 with 9, 325 with 8.
-template <class P, bool MASTER, bool COUNTED>
-constexpr int adam_ctas() { return COUNTED || sizeof(P) == 4 || MASTER ? 9 : 10; }
+// bf16 with fp32 masters 365 and 353; 100 M fp32 283 and 248.
+template <class P, bool MASTER>
+constexpr int adam_ctas() { return sizeof(P) == 4 || MASTER ? 9 : 10; }
 
 struct AdamTensor {
   void* param;
@@ -37,22 +36,27 @@ struct AdamUnit {
   int32_t block;
 };
 
-// A step's scalars, each computed in 64 bits and rounded once.
-struct AdamScalars {
-  float lr, lr_c1, b1, nb1, b2, nb2, c2, eps, one;
-  bool flush;            // eps is large enough to drop roots below fp32's normal range
+// A step's scalars, each computed in 64 bits and rounded once: those of its
+// number, and the others.
+struct AdamNumber {
+  float lr_c1, c2;
   uint64_t key;          // SplitMix64 output for seed and step
+};
+struct AdamScalars {
+  float lr, b1, nb1, b2, nb2, eps, one;
+  bool flush;            // eps is large enough to drop roots below fp32's normal range
+  AdamNumber n;
   int64_t step;
 };
 struct AdamHyper {
   double lr, beta1, beta2, eps;
   uint32_t seed;
 };
-// The handle's count of steps, on the device, and the scalars of a step that is
-// counted there.
+// The handle's count of steps, on the device, and the scalars of the number of a
+// step that is counted there.
 struct AdamCount {
   int64_t step;
-  AdamScalars s;
+  AdamNumber n;
 };
 
 // b^n by squaring, n >= 0: products alone, the same bits on host and device.
@@ -62,28 +66,30 @@ __host__ __device__ __noinline__ inline double power(double b, int64_t n) {
     if (n & 1) r *= b;
   return r;
 }
-EMB_HD AdamScalars adam_scalars(const AdamHyper& h, int64_t step) {
+EMB_HD AdamNumber adam_number(const AdamHyper& h, int64_t step) {
+  return {(float)(h.lr / (1.0 - power(h.beta1, step))), (float)(1.0 / (1.0 - power(h.beta2, step))),
+          splitmix64(((uint64_t)h.seed << 32) + (uint64_t)step)};
+}
+inline AdamScalars adam_scalars(const AdamHyper& h, int64_t step) {
   AdamScalars s;
   s.lr = (float)h.lr;
   s.b1 = (float)h.beta1;
   s.nb1 = (float)(1.0 - h.beta1);
   s.b2 = (float)h.beta2;
   s.nb2 = (float)(1.0 - h.beta2);
-  s.lr_c1 = (float)(h.lr / (1.0 - power(h.beta1, step)));
-  s.c2 = (float)(1.0 / (1.0 - power(h.beta2, step)));
   s.eps = (float)h.eps;
   s.one = 1.f;
   s.flush = h.eps >= 1e-12;
-  s.key = splitmix64(((uint64_t)h.seed << 32) + (uint64_t)step);
+  s.n = step > 0 ? adam_number(h, step) : AdamNumber{};
   s.step = step;
   return s;
 }
 
-// The next step's number and scalars, counted on the device: where a call is
+// The next step's number and what follows from it, on the device: where a call is
 // replayed, its host part does not run again.  step > 0 sets the count.
 __global__ void k_adamw_count(AdamHyper h, int64_t step, AdamCount* count) {
   count->step = step > 0 ? step : count->step + 1;
-  count->s = adam_scalars(h, count->step);
+  count->n = adam_number(h, count->step);
 }
 
 // Places on the 8-bit grid, and back (emb.h).  Codes of eight elements are
@@ -239,7 +245,7 @@ __device__ __forceinline__ int lane_elements(const AdamTensor& t, int64_t i0) {
 // tensor's.  VEC: all of the block's are, and every access is wide.
 template <class P, class G, bool MASTER, bool EIGHT, bool VEC>
 __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int64_t block, const AdamScalars& s,
-                                           const float* grad_scale) {
+                                           const AdamNumber& step, const float* grad_scale) {
   const int64_t i0 = block * kBlock + (threadIdx.x & 31) * 8;
   const int n = VEC ? 8 : lane_elements(t, i0);
   Eight<G> gr;
@@ -283,7 +289,7 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int
     mi = __ffma2_rn(__fmul2_rn(mi, both(s.b1)), both(s.one), __fmul2_rn(gi, both(s.nb1)));
     vi = __ffma2_rn(__fmul2_rn(vi, both(s.b2)), both(s.one), __fmul2_rn(__fmul2_rn(gi, gi), both(s.nb2)));
     m[i] = mi.x, m[i + 1] = mi.y, v[i] = vi.x, v[i + 1] = vi.y;
-    float2 r = __fmul2_rn(vi, both(s.c2)), q;
+    float2 r = __fmul2_rn(vi, both(step.c2)), q;
     if (s.flush) {
       // the flushing forms are single instructions; what they drop (a root
       // below 1.1e-19) is under 2^-23 of eps
@@ -300,14 +306,14 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int
       q = make_float2(__fdividef(mi.x, r.x), __fdividef(mi.y, r.y));
     }
     const float2 w0 = make_float2(w[i], w[i + 1]);
-    const float2 wi = __fadd2_rn(w0, __ffma2_rn(q, both(-s.lr_c1), __fmul2_rn(w0, both(off))));
+    const float2 wi = __fadd2_rn(w0, __ffma2_rn(q, both(-step.lr_c1), __fmul2_rn(w0, both(off))));
     w[i] = wi.x, w[i + 1] = wi.y;
   }
   if constexpr (MASTER) store8(t.master + i0, w, n, VEC);
   store8((P*)t.param + i0, w, n, VEC);
   if constexpr (EIGHT) {
     const uint64_t group = (uint64_t)(t.start + i0) / 4;
-    const uint64_t z0 = splitmix64(s.key + group), z1 = splitmix64(s.key + group + 1);
+    const uint64_t z0 = splitmix64(step.key + group), z1 = splitmix64(step.key + group + 1);
     const uint32_t noise[4] = {(uint32_t)z0, (uint32_t)(z0 >> 32), (uint32_t)z1, (uint32_t)(z1 >> 32)};
     mt = encode8<127>(m, noise, mc);
     if (n) store_codes((uint8_t*)t.m + i0, mc, n, VEC);
@@ -324,8 +330,8 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int
 // would cost the others registers.
 template <class P, class G, bool MASTER, bool EIGHT>
 __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64_t block, const AdamScalars* s,
-                                         const float* grad_scale) {
-  adam_block<P, G, MASTER, EIGHT, false>(*t, gp, block, *s, grad_scale);
+                                         const AdamNumber* step, const float* grad_scale) {
+  adam_block<P, G, MASTER, EIGHT, false>(*t, gp, block, *s, *step, grad_scale);
 }
 
 // All bytes are read once and written once; a warp takes one block, and the
@@ -336,26 +342,27 @@ __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64
 // blocks in flight for the registers that took, and were slower.  128 M
 // weights: fp32 506 us (7.1 TB/s), 8-bit states with bf16 258 us (4.95 TB/s),
 // with bf16 and masters 350 us (5.9 TB/s).
-// COUNTED: the scalars are k_adamw_count's; otherwise they come as arguments, which
-// cost no registers, and the count follows them.
+// COUNTED: the step's number is k_adamw_count's; otherwise it comes as an argument,
+// like the other scalars, which costs no registers, and the count follows it
+// (128 M weights with 8-bit states, replayed: bf16 268 us, with masters 329).
 template <class P, class G, bool MASTER, bool EIGHT, bool COUNTED>
-__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER, COUNTED>())) k_adamw(const AdamTensor* __restrict__ tensors,
+__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adamw(const AdamTensor* __restrict__ tensors,
                                                                    const void* const* __restrict__ grads,
                                                                    const AdamUnit* __restrict__ units, int64_t n_units,
-                                                                   const __grid_constant__ AdamScalars given,
+                                                                   const __grid_constant__ AdamScalars s,
                                                                    AdamCount* __restrict__ count,
                                                                    const float* __restrict__ grad_scale) {
   const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
   if (i >= n_units) return;
-  const AdamScalars& s = COUNTED ? count->s : given;
-  if (!COUNTED && i == 0 && threadIdx.x == 0) count->step = given.step;
+  const AdamNumber& step = COUNTED ? count->n : s.n;
+  if (!COUNTED && i == 0 && threadIdx.x == 0) count->step = s.step;
   const AdamUnit u = units[i];
   const AdamTensor& t = tensors[u.tensor];
   const G* gp = (const G*)grads[u.tensor];
   if (t.aligned && ((uintptr_t)gp & 15) == 0 && ((int64_t)u.block + 1) * kBlock <= t.numel)
-    adam_block<P, G, MASTER, EIGHT, true>(t, gp, u.block, s, grad_scale);
+    adam_block<P, G, MASTER, EIGHT, true>(t, gp, u.block, s, step, grad_scale);
   else
-    adam_ragged<P, G, MASTER, EIGHT>(&t, gp, u.block, &s, grad_scale);
+    adam_ragged<P, G, MASTER, EIGHT>(&t, gp, u.block, &s, &step, grad_scale);
 }
 
 // What the codes stand for, in bf16 (exact: three bits of fraction).  Bound by
@@ -593,8 +600,7 @@ extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double be
     if (capture != cudaStreamCaptureStatusNone) return EMB_ERR_UNSUPPORTED;
   }
   const AdamHyper hyper{lr, beta1, beta2, eps, seed};
-  AdamScalars s{};
-  if (step > 0) s = adam_scalars(hyper, step);
+  const AdamScalars s = adam_scalars(hyper, step);
   if (step == 0 || h->kinds.empty()) {
     k_adamw_count<<<1, 1, 0, st>>>(hyper, step, h->count_d);
     EMB_CUDA_TRY(cudaGetLastError());
