@@ -558,6 +558,13 @@ typedef struct {
  * output per four elements), so runs repeat bit for bit.  An element whose new
  * state is not finite is left out of its block's top and its state restarts
  * at 0 (its parameter shows the fault, as with 32-bit states).
+ * Two moments of one element can leave their blocks' ranges at different
+ * times: where another element of the block has a large v and, its gradient
+ * changing sign, a small m, v falls to 0 while m does not, and the element
+ * moves by m / (what one gradient adds to v) or m / eps.  With beta 0.9 and
+ * 0.999, eps 1e-8, one gradient of +-1 in a block of 1e-5: 16 lr a step, and 940
+ * lr when the 1e-5 become 0, where 32-bit states move it by 1 lr and 0.9 lr;
+ * ratios up to 2e4 or so do not show it.  adamw_set_max_update bounds the steps.
  *  tensors (host) [n], copied; 1 <= n < 2^24, fewer than 2^40 elements */
 emb_status adamw_create(const adamw_tensor* tensors, int32_t n, uint32_t flags, emb_adamw* out);
 
@@ -572,6 +579,7 @@ emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream)
  *   m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g g
  *   w = w - lr weight_decay w
  *         - lr (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps)
+ *           (the quotient at most adamw_set_max_update's limit)
  * in fp32, from the new m and v before they are rounded to 8 bits.  The new
  * states are the same bits as the formulas' operations rounded one by one;
  * the weights use the hardware's approximate square root and division (a few
@@ -585,6 +593,15 @@ emb_status adamw_bind_grads(emb_adamw h, const void* const* grads, void* stream)
  * (EMB_ERR_UNSUPPORTED): its replays would repeat that step. */
 emb_status adamw_step(emb_adamw h, int64_t step, double lr, double beta1, double beta2, double eps,
                       const float* grad_scale, uint32_t seed, void* stream);
+
+/* adamw_set_max_update -- from the next step on no weight's update
+ * (m / (1 - beta1^step)) / (sqrt(v / (1 - beta2^step)) + eps) is larger than
+ * `limit` in magnitude: larger ones count as limit, NaN stays.  0 or infinity: no
+ * limit, as at first.  Updates from moments that no rounding has touched stay
+ * below (1 - beta1) / sqrt((1 - beta2)(1 - beta1^2 / beta2)) (beta1^2 < beta2): 7.3
+ * for 0.9 and 0.999, which as a limit therefore changes nothing but what 8-bit
+ * states have lost. */
+emb_status adamw_set_max_update(emb_adamw h, double limit);
 
 /* The number of the handle's last step (0 at first), read or set in the
  * stream's order; both synchronize `stream`. */

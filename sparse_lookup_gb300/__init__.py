@@ -115,6 +115,7 @@ _SIGS = {
     "adamw_bind_grads": (c_int32, [c_void_p, c_void_p, c_void_p]),
     "adamw_step": (c_int32, [c_void_p, c_int64, c_double, c_double, c_double, c_double, c_void_p, c_uint32,
                              c_void_p]),
+    "adamw_set_max_update": (c_int32, [c_void_p, c_double]),
     "adamw_get_step": (c_int32, [c_void_p, POINTER(c_int64), c_void_p]),
     "adamw_set_step": (c_int32, [c_void_p, c_int64, c_void_p]),
     "adamw_export_states": (c_int32, [c_void_p, c_void_p, c_void_p, c_void_p]),
@@ -513,6 +514,6 @@ def _device_view(ptr_value, shape):
 
 from .dense import (AdamW, AdamwTensor, ExpertRouter, GatedScan, Routing, ScanView, adamw_bind_grads,  # noqa: E402,F401
                     adamw_create, adamw_destroy, adamw_export_size, adamw_export_states, adamw_get_step,
-                    adamw_set_step, adamw_step, moe_combine,
+                    adamw_set_max_update, adamw_set_step, adamw_step, moe_combine,
                     moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_route, scan_backward,
                     scan_create, scan_destroy, scan_forward, scan_get_device_status, scan_selftest_timeout, scan_step)

@@ -40,6 +40,7 @@ struct AdamUnit {
 // number, and the others.
 struct AdamNumber {
   float lr_c1, c2;
+  float limit;           // of the quotient before its correction by beta1; 0: none
   uint64_t key;          // SplitMix64 output for seed and step
 };
 struct AdamScalars {
@@ -49,7 +50,7 @@ struct AdamScalars {
   int64_t step;
 };
 struct AdamHyper {
-  double lr, beta1, beta2, eps;
+  double lr, beta1, beta2, eps, limit;
   uint32_t seed;
 };
 // The handle's count of steps, on the device, and the scalars of the number of a
@@ -67,7 +68,8 @@ __host__ __device__ __noinline__ inline double power(double b, int64_t n) {
   return r;
 }
 EMB_HD AdamNumber adam_number(const AdamHyper& h, int64_t step) {
-  return {(float)(h.lr / (1.0 - power(h.beta1, step))), (float)(1.0 / (1.0 - power(h.beta2, step))),
+  const double c1 = 1.0 - power(h.beta1, step);
+  return {(float)(h.lr / c1), (float)(1.0 / (1.0 - power(h.beta2, step))), (float)(h.limit * c1),
           splitmix64(((uint64_t)h.seed << 32) + (uint64_t)step)};
 }
 inline AdamScalars adam_scalars(const AdamHyper& h, int64_t step) {
@@ -305,6 +307,10 @@ __device__ __forceinline__ void adam_block(const AdamTensor& t, const G* gp, int
       r = __fadd2_rn(r, both(s.eps));
       q = make_float2(__fdividef(mi.x, r.x), __fdividef(mi.y, r.y));
     }
+    if (step.limit > 0.f) {
+      asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(q.x) : "f"(step.limit));
+      asm("min.NaN.xorsign.abs.f32 %0, %0, %1;" : "+f"(q.y) : "f"(step.limit));
+    }
     const float2 w0 = make_float2(w[i], w[i + 1]);
     const float2 wi = __fadd2_rn(w0, __ffma2_rn(q, both(-step.lr_c1), __fmul2_rn(w0, both(off))));
     w[i] = wi.x, w[i + 1] = wi.y;
@@ -448,6 +454,7 @@ struct emb_adamw_s {
   int32_t n = 0;
   int device = 0;
   bool eight = false;
+  double limit = 0.0;                   // adamw_set_max_update
   int64_t elements = 0;                 // of the padded order
   int64_t n_units = 0;
   std::vector<emb::AdamKind> kinds;
@@ -599,7 +606,7 @@ extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double be
     EMB_CUDA_TRY(cudaStreamIsCapturing(st, &capture));
     if (capture != cudaStreamCaptureStatusNone) return EMB_ERR_UNSUPPORTED;
   }
-  const AdamHyper hyper{lr, beta1, beta2, eps, seed};
+  const AdamHyper hyper{lr, beta1, beta2, eps, h->limit, seed};
   const AdamScalars s = adam_scalars(hyper, step);
   if (step == 0 || h->kinds.empty()) {
     k_adamw_count<<<1, 1, 0, st>>>(hyper, step, h->count_d);
@@ -610,6 +617,12 @@ extern "C" emb_status adamw_step(emb_adamw h, int64_t step, double lr, double be
         h->tensors_d, h->grads_d, h->units_d + k.first, k.count, s, h->count_d, grad_scale);
     EMB_CUDA_TRY(cudaGetLastError());
   }
+  return EMB_OK;
+}
+
+extern "C" emb_status adamw_set_max_update(emb_adamw h, double limit) {
+  if (!h || !(limit >= 0)) return EMB_ERR_INVALID_ARG;
+  h->limit = std::isinf(limit) ? 0.0 : limit;
   return EMB_OK;
 }
 

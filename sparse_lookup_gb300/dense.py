@@ -151,6 +151,10 @@ def adamw_step(h, step, lr, beta1, beta2, eps, grad_scale, seed, stream=None):
     _check(lib().adamw_step(h, step, lr, beta1, beta2, eps, ptr(grad_scale), seed, _stream(stream)), "adamw_step")
 
 
+def adamw_set_max_update(h, limit):
+    _check(lib().adamw_set_max_update(h, limit), "adamw_set_max_update")
+
+
 def adamw_get_step(h, stream=None):
     n = c_int64()
     _check(lib().adamw_get_step(h, ctypes.byref(n), _stream(stream)), "adamw_get_step")
@@ -515,6 +519,12 @@ class AdamW(_Handle):
     int16 tops, one per 256 elements (``m``, ``v``, ``m_top``, ``v_top``; created
     at zero, or given).  step: steps already taken.
 
+    max_update: the largest magnitude of m / sqrt(v) that a step may use (None: no
+    limit).  8-bit states can lose a small second moment beside a large one in its
+    block and keep the first: such a weight would move by many lr (emb.h gives a
+    case of 16, and of 940 when its gradient stops).  7.3 bounds that for betas
+    (0.9, 0.999) and leaves every update of unrounded moments as it is.
+
     A step may be captured in a graph: each replay is a step of its own, counted
     on the device, with the lr and grad_scale tensor of the capture.  From then
     on every step of the handle is counted there (a launch more), and reading
@@ -523,7 +533,7 @@ class AdamW(_Handle):
     _destroy = staticmethod(adamw_destroy)
 
     def __init__(self, params, grads, masters=None, weight_decay=0.01, betas=(0.9, 0.999), eps=1e-8, state_bits=32,
-                 m=None, v=None, m_top=None, v_top=None, seed=0, step=0):
+                 m=None, v=None, m_top=None, v_top=None, seed=0, step=0, max_update=None):
         super().__init__()
         torch = self._t
         self.params, self.betas, self.eps, self.seed = list(params), betas, eps, seed
@@ -569,6 +579,8 @@ class AdamW(_Handle):
         self._taken, self._counted = 0, False   # steps, where the host counts them
         if step:
             self.step_count = step
+        if max_update is not None:
+            adamw_set_max_update(self.handle, max_update)
 
     @property
     def step_count(self):

@@ -156,3 +156,11 @@ def test_the_current_device_and_the_stream_are_the_handles(fakes):
     plan._current = lambda: 1
     with pytest.raises(ValueError):
         plan.forward(*t[:2], y=t[2], last=Fake((2, 8)), stream=7)
+
+
+def test_null_handles_of_the_count_and_the_limit():
+    slbuild.build()
+    L, n = sl.lib(), ctypes.c_int64()
+    assert L.adamw_get_step(None, ctypes.byref(n), None) == 1
+    assert L.adamw_set_step(None, 1, None) == 1
+    assert L.adamw_set_max_update(None, 1.0) == 1
