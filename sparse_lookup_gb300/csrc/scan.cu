@@ -1091,6 +1091,10 @@ int64_t chain_records(int TT, int64_t cols, int64_t len) {
 // and 107; 430 of 2400 positions fp32 69 and 79; 100 of 600, 1200 and 2400
 // positions bf16 8.4 and 10.4, 12.6 and 12.9, 22 and 19; 800 x 512 10.4 and 8.1.
 // chain_r, walk_r: positions of a thread in either case.
+bool idle_enough(int64_t wide, int64_t slots) { return wide * 5 < (wide + slots - 1) / slots * slots * 3; }
+// The tiles of 32 channels across the widest call that is chained: under 6/5 of
+// the places (under 3/5 of one round of them, of two, and never of three).
+int64_t most_chained(int64_t slots) { return (6 * slots - 1) / 5; }
 template <int V>
 Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* offsets, int chain_r, int walk_r) {
   Cut c{};
@@ -1109,7 +1113,7 @@ Cut cut_call(const emb_scan_s* h, int32_t batch, int32_t len, const int32_t* off
   const int64_t slots = (int64_t)h->sm_count * kCtasPerSm;
   const auto across = [&](int cx_log) { return (a.vecs + (1 << cx_log) - 1) >> cx_log; };
   const int64_t wide = across(kCx), places = (wide + slots - 1) / slots * slots;
-  c.chain = wide * 5 < places * 3 && len * places > (kScanThreads >> kCx) * chain_r * (2 * places + 10 * wide);
+  c.chain = idle_enough(wide, slots) && len * places > (kScanThreads >> kCx) * chain_r * (2 * places + 10 * wide);
   const int R = c.chain ? chain_r : walk_r;
   if (c.chain) {
     a.cx_log = kCx;
@@ -1255,8 +1259,8 @@ extern "C" emb_status scan_create(int32_t dim, int32_t max_batch, int32_t max_le
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) {
-    // a call with more channels than this walks
-    const int64_t most = (int64_t)h->sm_count * kCtasPerSm * 32 * 2 + dim, all = (int64_t)max_batch * dim;
+    const int64_t slots = (int64_t)h->sm_count * kCtasPerSm, most = most_chained(slots) * 32;
+    const int64_t all = (int64_t)max_batch * dim;
     const int V = channels_at_once(dim), TT = V == 4 ? least_tile<4>() : V == 2 ? least_tile<2>() : least_tile<1>();
     h->max_records = chain_records(TT, all < most ? all : most, max_len);
     e = dev_alloc((void**)&h->status_d, sizeof(uint32_t));
