@@ -596,9 +596,9 @@ __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_fwd(ScanArgs 
 // in the first rows of the tile's gradients, the upper half of an fp32 in one
 // and the lower in the other, which that tile's CTA reads and overwrites: no
 // workspace.  Only whole tiles with live positions behind them are looked at.
-// 131072 x 512 bf16: 45 us, the inputs read a second time at 5.9 TB/s, and 32 us,
-// the latency of few channels' strided rows; 128 x 1024 x 512 41 and 8 us.  As
-// a chain of tiles like the forward's they took 139 us and 68.
+// 131072 x 512 bf16: 45 us, the inputs read a second time at 5.9 TB/s, and 11 us,
+// the latency of strided rows (one CTA for 32 channels: 32); 128 x 1024 x 512 41
+// and 10 us.  As a chain of tiles like the forward's they took 139 us and 68.
 template <class T, int V>
 __device__ __forceinline__ void put_halves(const View<T>& up, const View<T>& low, int b, int t, int d,
                                            const Lanes<V>& x) {
@@ -665,19 +665,41 @@ __global__ void __launch_bounds__(kEffectWarps * 32) k_scan_effects(const __grid
   put_halves<T, V>(gx, gg, c.b, t0 + 1, c.d, b);
 }
 
-// A CTA takes 32 channels, its warps `each` neighbouring tiles.  A few warps per
-// channel walk the whole sequence, so loads go in batches.
-constexpr int kStateWarps = 32, kStateRows = 8;
+// A cluster takes 32 channels, the warps of its CTAs `each` neighbouring tiles:
+// up to 2048 tiles are then read once, all loads in flight.  Effects of the CTAs
+// ahead are read from their shared memory.
+constexpr int kStateWarps = 32, kStateRows = 8, kStateCtas = 8;
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_ctas() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire;" ::: "memory"); }
+__device__ __forceinline__ Affine of_cta(const Affine* p, uint32_t rank) {   // the same variable of another CTA
+  uint32_t a;
+  Affine f;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(f.a), "=f"(f.b) : "r"(a) : "memory");
+  return f;
+}
 template <class T>
 __global__ void __launch_bounds__(kStateWarps * 32) k_scan_states(const __grid_constant__ ScanArgs s, int each,
                                                                   View<T> gx, View<T> gg,
                                                                   const float* __restrict__ state_in) {
   __shared__ Affine part[kStateWarps][32];
+  __shared__ alignas(8) Affine cta[32];
   pdl_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, TT = (int)s.tile.d;
-  const Channel c = channel_of<1>(s, (int64_t)blockIdx.x * 32 + lane, 0);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5, TT = (int)s.tile.d;
+  const uint32_t rank = cluster_rank(), ctas = cluster_ctas();
+  const Channel c = channel_of<1>(s, (int64_t)(blockIdx.x / ctas) * 32 + lane, 0);
   const int whole = c.n > 0 ? (int)div_magic32((uint32_t)c.n - 1, s.tile) : 0;   // tiles with live positions behind them
-  const int lo = min(warp * each, whole), hi = min(lo + each, whole);
+  const int lo = min(((int)rank * warps + warp) * each, whole), hi = min(lo + each, whole);
   Affine f[kStateRows];
   const auto load = [&](int k0) {
 #pragma unroll
@@ -688,18 +710,29 @@ __global__ void __launch_bounds__(kStateWarps * 32) k_scan_states(const __grid_c
                 get_halves<1>(gx, gg, c.b, (k0 + i) * TT + 1, c.d).v[0]};
     }
   };
-  Affine all{1.f, 0.f};
-  for (int k0 = lo; k0 < hi; k0 += kStateRows) {
+  Affine all{1.f, 0.f}, before = all;
+  for (int k0 = lo; k0 == lo || k0 < hi; k0 += kStateRows) {
     load(k0);
 #pragma unroll
     for (int i = 0; i < kStateRows; ++i) all = after(f[i], all);
   }
   part[warp][lane] = all;
   __syncthreads();
+  for (int w = 0; w < warp; ++w) before = after(part[w][lane], before);
+  if (warp == warps - 1) cta[lane] = after(all, before);
   float h = state_in && c.ok ? state_in[c.col] : 0.f;
-  for (int w = 0; w < warp; ++w) h = fmaf(part[w][lane].a, h, part[w][lane].b);
+  if (ctas > 1) {
+    cluster_arrive();
+    cluster_wait();
+    for (uint32_t r = 0; r < rank; ++r) {
+      const Affine e = of_cta(&cta[lane], r);
+      h = fmaf(e.a, h, e.b);
+    }
+    cluster_arrive();   // no CTA leaves before the others have read its effects
+  }
+  h = fmaf(before.a, h, before.b);
   for (int k0 = lo; k0 < hi; k0 += kStateRows) {   // effects are read before states take their places
-    load(k0);
+    if (each > kStateRows) load(k0);
 #pragma unroll
     for (int i = 0; i < kStateRows; ++i) {
       if (k0 + i < hi && k0 + i > 0) put_halves<T, 1>(gx, gg, c.b, (k0 + i) * TT, c.d, all_of<1>(h));
@@ -707,6 +740,7 @@ __global__ void __launch_bounds__(kStateWarps * 32) k_scan_states(const __grid_c
     }
   }
   if (hi > lo && hi == whole) put_halves<T, 1>(gx, gg, c.b, whole * TT, c.d, all_of<1>(h));
+  if (ctas > 1) cluster_wait();
 }
 
 template <class T>
@@ -723,7 +757,7 @@ __device__ __forceinline__ float get_state(const View<T>& up, const View<T>& low
 // gate (k_scan_effects, k_scan_states) and y is not read.
 // Bound as the forward is: 16 x 8192 x 512 fp32 208 us, 6.4 TB/s; 128 x 1024 x
 // 512 bf16 156 us, 131072 x 512 bf16 206 us, with the states before the tiles
-// 215 and 293 (from y as it is rounded 154 and 202: every position's y read, and
+// 215 and 270 (from y as it is rounded 154 and 202: every position's y read, and
 // the gate's gradient as far off as h's rounding is beside h - x).
 template <class T, int V, int R, bool CHAIN, bool WIDE>
 __global__ void __launch_bounds__(kScanThreads, kCtasPerSm) k_scan_bwd(ScanArgs s, View<const T> x, View<const T> g,
@@ -1206,10 +1240,23 @@ cudaError_t find_states(const Cut& c, View<const T> x, View<const T> g, View<T> 
   if (e != cudaSuccess) return e;
   a.vecs = (int64_t)a.batch * a.dim;
   a.per = make_div_magic32((uint32_t)a.dim);
-  int warps = 1;   // about four tiles each
+  int warps = 1, ctas = 1;   // about four tiles each, and no more than are read at once if there are warps enough
   while (warps < kStateWarps && warps * 4 < most) warps *= 2;
-  return launch_dependent(k_scan_states<T>, (unsigned)((a.vecs + 31) / 32), warps * 32, 0, stream, a,
-                          (int)((most + warps - 1) / warps), gx, gg, state_in);
+  while (ctas < kStateCtas && ctas * kStateWarps * kStateRows < most) ctas *= 2;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.vecs + 31) / 32 * ctas));
+  cfg.blockDim = dim3(warps * 32);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  const int64_t parts = warps * ctas;
+  return cudaLaunchKernelEx(&cfg, k_scan_states<T>, a, (int)((most + parts - 1) / parts), gx, gg, state_in);
 }
 
 // All views wide, with the first one's strides: the kernels of this variant
