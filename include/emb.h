@@ -421,6 +421,8 @@ typedef struct {
 
 /* scan_create -- workspace of a gated linear recurrence over sequences:
  *   a_t = sigmoid(gate_t);  h_t = a_t * h_{t-1} + (1 - a_t) * x_t
+ * (the exponential and reciprocal are the hardware's approximate ones: a and 1 - a
+ * are off by at most (|gate| + 8) 2^-24 of themselves)
  * per batch entry and channel, over dim channels (1 .. 65536), at most
  * max_batch (1 .. 2^31-1) entries of at most max_len (1 .. 2^30) positions,
  * batch * dim < 2^32 in a call.

@@ -346,18 +346,18 @@ __device__ __noinline__ void adam_ragged(const AdamTensor* t, const G* gp, int64
 // latency in front of it: arithmetic goes in pairs, codes in words of four.
 // Warps that walked several blocks with the next one's loads ahead held fewer
 // blocks in flight for the registers that took, and were slower.  128 M
-// weights: fp32 506 us (7.1 TB/s), 8-bit states with bf16 258 us (4.95 TB/s),
-// with bf16 and masters 350 us (5.9 TB/s).
+// weights: fp32 506 us (7.1 TB/s), bf16 401 us and with masters 512 (7.0), 8-bit
+// states with bf16 264 us (4.85 TB/s), with bf16 and masters 351 us (5.8 TB/s).
+// Tensors off 16-byte boundaries go element by element (fp32 979 us, 8-bit states
+// with bf16 540).
 // COUNTED: the step's number is k_adamw_count's; otherwise it comes as an argument,
 // like the other scalars, which costs no registers, and the count follows it
 // (128 M weights with 8-bit states, replayed: bf16 268 us, with masters 329).
 template <class P, class G, bool MASTER, bool EIGHT, bool COUNTED>
-__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>())) k_adamw(const AdamTensor* __restrict__ tensors,
-                                                                   const void* const* __restrict__ grads,
-                                                                   const AdamUnit* __restrict__ units, int64_t n_units,
-                                                                   const __grid_constant__ AdamScalars s,
-                                                                   AdamCount* __restrict__ count,
-                                                                   const float* __restrict__ grad_scale) {
+__global__ void __launch_bounds__(kAdamThreads, (adam_ctas<P, MASTER>()))
+    k_adamw(const AdamTensor* __restrict__ tensors, const void* const* __restrict__ grads,
+            const AdamUnit* __restrict__ units, int64_t n_units, const __grid_constant__ AdamScalars s,
+            AdamCount* __restrict__ count, const float* __restrict__ grad_scale) {
   const int64_t i = (blockIdx.x * (int64_t)kAdamThreads + threadIdx.x) >> 5;
   if (i >= n_units) return;
   const AdamNumber& step = COUNTED ? count->n : s.n;

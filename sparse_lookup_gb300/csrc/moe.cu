@@ -12,7 +12,7 @@ constexpr int kRouteOne = 8192;       // choices that one CTA places alone
 constexpr int kRouteMinSpan = 2048;   // choices of a CTA at least, where there are more
 constexpr int kMaxExperts = 2048;
 constexpr int kRowThreads = 128;
-constexpr int kBwdCtas = 8;           // its CTAs on an SM: at 64 registers a lane none spill
+constexpr int kBwdCtas = 8;           // its CTAs on an SM: at 64 registers a lane only single fp32 columns spill (8 bytes)
 constexpr int kInFlight = 4;          // accesses of a lane that the combine's backward keeps in flight
 
 struct RouteArgs {
