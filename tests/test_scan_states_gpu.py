@@ -83,3 +83,62 @@ def test_what_dead_positions_and_the_outputs_held_changes_nothing():
             for p, q in zip(got, want):
                 assert torch.equal(p, q)
         plan.close()
+
+
+@pytest.mark.parametrize("B,T,D", [(1, 41000, 16), (1, 41120, 30), (1, 33000, 33), (2, 90000, 8), (1, 200000, 8),
+                                   (1, 330000, 4)])
+def test_more_tiles_than_one_cta_joins(B, T, D):
+    """From 257 tiles on, clusters of two, four and eight CTAs, and more tiles than
+    those read at once."""
+    run(B, T, D, "bfloat16")
+
+
+def test_a_walking_call_of_many_tiles():
+    """Enough sequences to walk, long enough for a cluster; three of them against
+    the formulas."""
+    import torch
+    B, T, D = 190, 33500, 32
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    x, g, gy = (torch.empty(B, T, D, device="cuda").normal_(m, s, generator=gen).to(torch.bfloat16)
+                for m, s in ((16.0, 1.0), (1.0, 1.5), (0.0, 1.0)))
+    h0, gl = (torch.randn(B, D, generator=gen, device="cuda") for _ in range(2))
+    lens = torch.randint(0, T + 1, (B,), generator=gen, device="cuda")
+    lens[0], lens[1] = T, 32769
+    off = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    plan = sl.GatedScan(D, B, T)
+    y, _ = plan.forward(x, g, off, h0)
+    grads = plan.backward(x, g, y, gy, off, h0, gl)
+    assert plan.device_status() == 0
+    for b in (slice(0, 2), slice(B - 1, B)):
+        rx, rg, rs, ex, eg, es = backward64(f64(x[b]), f64(g[b]), lens[b].cpu().numpy(), f64(h0[b]), f64(gy[b]),
+                                            f64(gl[b]), 0.0)
+        close(grads[0][b], rx, ex, "bfloat16", "grad_x")
+        close(grads[1][b], rg, eg, "bfloat16", "grad_gate")
+        close(grads[2][b], rs, es, "float32", "grad_state")
+    plan.close()
+
+
+def test_replayed_in_a_graph_and_on_another_stream():
+    import torch
+    B, T, D = 1, 41000, 32
+    x, g, gy, h0, gl, lens, off = make(B, T, D, "bfloat16", 3)
+    plan = sl.GatedScan(D, B, T)
+    y, _ = plan.forward(x, g, off, h0)
+    want = plan.backward(x, g, y, gy, off, h0, gl)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = plan.backward(x, g, y, gy, off, h0, gl, stream=side)
+    side.synchronize()
+    assert all(torch.equal(p, q) for p, q in zip(got, want))
+    out = [torch.empty_like(t) for t in want]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, capture_error_mode="relaxed"):
+        plan.backward(x, g, y, gy, off, h0, gl, grad_x=out[0], grad_gate=out[1], grad_state=out[2])
+    for _ in range(3):
+        for t in out:
+            t.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p, q) for p, q in zip(out, want))
+    assert plan.device_status() == 0
