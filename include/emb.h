@@ -522,6 +522,42 @@ emb_status moe_combine(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const v
 emb_status moe_combine_backward(emb_moe h, int64_t n, int32_t dim, int32_t dtype, const void* grad_y,
                                 int64_t grad_y_stride, const void* ys, const float* weights, const int32_t* pos,
                                 const int32_t* src, void* grad_ys, float* grad_weights, void* stream);
+
+/* moe_gate -- choices, weights, counts and losses of a batch from its logits
+ * [n, n_experts] of `dtype`, rows logits_stride elements apart:
+ *   p = softmax(logits) and lse = log(sum(exp(logits))) of a live token
+ *   choices  its top_k largest logits, equal ones in the order of the experts;
+ *            an expert whose logit is -infinity is never chosen
+ *   weights  normalize != 0: the softmax over the choices alone; 0: their p
+ *   balance  n_experts * sum over e of f_e P_e, with f_e = counts_e / (N top_k) and
+ *            P_e = sum of p_e / N over the N live tokens;  z = sum of lse^2 / N
+ *            (both 0 where N = 0).  f is a constant in the gradient.
+ *  live     NULL, or [n] bytes: a token with 0 reads no logits, has no choice and
+ *           no share in counts and losses.  So has one whose logits are all
+ *           -infinity.  A NaN or +infinity makes its token's weights NaN, and both
+ *           losses.
+ *  experts  [n, top_k] int32, -1 where there is no choice (as moe_route takes them)
+ *  weights  [n, top_k] fp32, 0 where there is no choice
+ *  counts   [n_experts] int32;  losses [2] fp32: balance, z
+ *  stats    [n][2] fp32, 8-byte aligned: a token's largest logit (-infinity where
+ *           it is not live) and its sum of exp(logit - largest); live_count [1]
+ *           int32 (N): both for the backward */
+emb_status moe_gate(emb_moe h, int64_t n, int32_t dtype, const void* logits, int64_t logits_stride,
+                    const uint8_t* live, int32_t normalize, int32_t* experts, float* weights, int32_t* counts,
+                    float* losses, float* stats, int32_t* live_count, void* stream);
+
+/* moe_gate_backward -- gradient of moe_gate's logits from its outputs (experts,
+ * weights, counts, stats, live_count, read-only) and the gradients of weights [n,
+ * top_k] and of losses [2], both fp32, NULL = 0.  With gb and gz those of losses
+ * and c_e = gb n_experts f_e / N:
+ *   p_e (c_e - sum p c + 2 gz lse / N), and for the weights: a chosen one
+ *   w (gw - sum w gw) more (normalize), or w gw more and every one p_e sum w gw less
+ * Tokens that are not live get 0.  grad_logits: rows grad_stride elements apart. */
+emb_status moe_gate_backward(emb_moe h, int64_t n, int32_t dtype, const void* logits, int64_t logits_stride,
+                             int32_t normalize, const int32_t* experts, const float* weights,
+                             const int32_t* counts, const float* stats, const int32_t* live_count,
+                             const float* grad_weights, const float* grad_losses, void* grad_logits,
+                             int64_t grad_stride, void* stream);
 emb_status moe_destroy(emb_moe h);
 
 typedef struct emb_adamw_s* emb_adamw;
@@ -621,6 +657,41 @@ emb_status adamw_set_step(emb_adamw h, int64_t step, void* stream);
 emb_status adamw_export_states(emb_adamw h, void* m_out, void* v_out, void* stream);
 emb_status adamw_export_size(emb_adamw h, int64_t* elements);
 emb_status adamw_destroy(emb_adamw h);
+
+typedef struct emb_norm_s* emb_norm;
+
+/* norm_create -- workspace of a layer norm over rows of dim (1 .. 16384)
+ * channels: 8 bytes a channel for each CTA that sums the weight's gradient (4 per
+ * SM; 5 MB for 1024 channels).  Calls on one handle must be ordered.  *out is
+ * NULL on error. */
+emb_status norm_create(int32_t dim, emb_norm* out);
+
+/* norm_forward -- y = (x - mean) * rstd * weight + bias over each row's channels,
+ *   mean = sum(x) / dim;  rstd = 1 / sqrt(sum((x - mean)^2) / dim + eps)
+ * in two passes over the row, which stays in registers.
+ *  x, y     (host structs) rows (b, t) of [batch, len, dim] arrays of `dtype`;
+ *           a plain matrix is batch 1
+ *  offsets  NULL, or [batch + 1] int32 as in scan_forward: positions past an
+ *           entry's end read nothing; their y is 0
+ *  weight, bias  [dim] of weight_dtype (dtype or EMB_DT_F32); NULL = 1 and 0
+ *  stats    NULL, or [batch * len][2] fp32, 8-byte aligned: mean and rstd of each
+ *           row for the backward; 0 past an entry's end */
+emb_status norm_forward(emb_norm h, int32_t batch, int64_t len, int32_t dtype, const scan_view* x,
+                        const int32_t* offsets, int32_t weight_dtype, const void* weight, const void* bias,
+                        double eps, const scan_view* y, float* stats, void* stream);
+
+/* norm_backward -- gradients of norm_forward from its x, weight and stats and
+ * the gradient of y: with xh = (x - mean) * rstd and g = grad_y * weight
+ *   grad_x = rstd * (g - sum(g) / dim - xh * sum(g * xh) / dim)
+ *   grad_weight = sum over the rows of grad_y * xh;  grad_bias = sum of grad_y
+ * Positions past an entry's end read nothing, get gradient 0 and add nothing.
+ * grad_weight and grad_bias: [dim] fp32, NULL = not wanted; sums in an order
+ * that the sizes fix. */
+emb_status norm_backward(emb_norm h, int32_t batch, int64_t len, int32_t dtype, const scan_view* x,
+                         const int32_t* offsets, int32_t weight_dtype, const void* weight, const scan_view* grad_y,
+                         const float* stats, const scan_view* grad_x, float* grad_weight, float* grad_bias,
+                         void* stream);
+emb_status norm_destroy(emb_norm h);
 
 /* ------------------------------------------------------------------------ */
 /* Self tests and fault injection (no counterpart on the pages)              */

@@ -110,7 +110,15 @@ _SIGS = {
                               c_void_p]),
     "moe_combine_backward": (c_int32, [c_void_p, c_int64, c_int32, c_int32, c_void_p, c_int64, c_void_p, c_void_p,
                                        c_void_p, c_void_p, c_void_p, c_void_p, c_void_p]),
+    "moe_gate": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_void_p, c_int32] + [c_void_p] * 7),
+    "moe_gate_backward": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32] + [c_void_p] * 8 +
+                          [c_int64, c_void_p]),
     "moe_destroy": (c_int32, [c_void_p]),
+    "norm_create": (c_int32, [c_int32, POINTER(c_void_p)]),
+    "norm_forward": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
+                               c_double, c_void_p, c_void_p, c_void_p]),
+    "norm_backward": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_int32] + [c_void_p] * 7),
+    "norm_destroy": (c_int32, [c_void_p]),
     "adamw_create": (c_int32, [c_void_p, c_int32, c_uint32, POINTER(c_void_p)]),
     "adamw_bind_grads": (c_int32, [c_void_p, c_void_p, c_void_p]),
     "adamw_step": (c_int32, [c_void_p, c_int64, c_double, c_double, c_double, c_double, c_void_p, c_uint32,
@@ -512,8 +520,9 @@ def _device_view(ptr_value, shape):
     return torch.as_tensor(h, device="cuda")
 
 
-from .dense import (AdamW, AdamwTensor, ExpertRouter, GatedScan, Routing, ScanView, adamw_bind_grads,  # noqa: E402,F401
-                    adamw_create, adamw_destroy, adamw_export_size, adamw_export_states, adamw_get_step,
-                    adamw_set_max_update, adamw_set_step, adamw_step, moe_combine,
-                    moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_route, scan_backward,
-                    scan_create, scan_destroy, scan_forward, scan_get_device_status, scan_selftest_timeout, scan_step)
+from .dense import (AdamW, AdamwTensor, ExpertRouter, Gate, GatedScan, LayerNorm, Routing, ScanView,  # noqa: E402,F401
+                    adamw_bind_grads, adamw_create, adamw_destroy, adamw_export_size, adamw_export_states,
+                    adamw_get_step, adamw_set_max_update, adamw_set_step, adamw_step, moe_combine,
+                    moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_gate, moe_gate_backward,
+                    moe_route, norm_backward, norm_create, norm_destroy, norm_forward, scan_backward, scan_create,
+                    scan_destroy, scan_forward, scan_get_device_status, scan_selftest_timeout, scan_step)

@@ -2,7 +2,7 @@
 // emb.h).
 #include <new>
 
-#include "rows.cuh"
+#include "moe.cuh"
 
 namespace emb {
 
@@ -10,7 +10,6 @@ constexpr int kRouteThreads = 512;
 constexpr int kRouteWarps = kRouteThreads / 32;
 constexpr int kRouteOne = 8192;       // choices that one CTA places alone
 constexpr int kRouteMinSpan = 2048;   // choices of a CTA at least, where there are more
-constexpr int kMaxExperts = 2048;
 constexpr int kRowThreads = 128;
 constexpr int kBwdCtas = 8;           // its CTAs on an SM: at 64 registers a lane only single fp32 columns spill (8 bytes)
 constexpr int kInFlight = 4;          // accesses of a lane that the combine's backward keeps in flight
@@ -359,13 +358,6 @@ __global__ void __launch_bounds__(kRowThreads, kBwdCtas) k_combine_bwd(RowArgs a
 
 }  // namespace emb
 
-struct emb_moe_s {
-  int32_t n_experts = 0, top_k = 0, align = 1;
-  int64_t max_tokens = 0;
-  int sm_count = 0, device = 0;
-  uint32_t* part = nullptr;
-};
-
 using namespace emb;
 
 namespace {
@@ -438,12 +430,15 @@ extern "C" emb_status moe_create(int32_t n_experts, int32_t top_k, int64_t max_t
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   if (e == cudaSuccess) e = dev_alloc((void**)&h->part, sizeof(uint32_t) * h->sm_count * n_experts);
+  if (e == cudaSuccess) e = dev_alloc(&h->gate, gate_bytes(h->sm_count, n_experts));
+  if (e == cudaSuccess) e = gate_clear(h->gate, h->sm_count, n_experts);
   for (auto k : {k_route_place<true>, k_route_place<false>})
     if (e == cudaSuccess)
       e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                (kRouteWarps + 2) * kMaxExperts * (int)sizeof(uint32_t));
   if (e != cudaSuccess) {
     dev_free(h->part);
+    dev_free(h->gate);
     delete h;
     return cuda_status(e);
   }
@@ -455,6 +450,7 @@ extern "C" emb_status moe_destroy(emb_moe h) {
   if (!h) return EMB_ERR_INVALID_ARG;
   const cudaError_t e = cudaDeviceSynchronize();
   dev_free(h->part);
+  dev_free(h->gate);
   delete h;
   return cuda_status(e);
 }

@@ -129,8 +129,43 @@ def moe_combine_backward(h, n, dim, dtype, grad_y, grad_y_stride, ys, weights, p
            "moe_combine_backward")
 
 
+def moe_gate(h, n, dtype, logits, logits_stride, live, normalize, experts, weights, counts, losses, stats, live_count,
+             stream=None):
+    _check(lib().moe_gate(h, n, dtype, ptr(logits), logits_stride, ptr(live), normalize, ptr(experts), ptr(weights),
+                          ptr(counts), ptr(losses), ptr(stats), ptr(live_count), _stream(stream)), "moe_gate")
+
+
+def moe_gate_backward(h, n, dtype, logits, logits_stride, normalize, experts, weights, counts, stats, live_count,
+                      grad_weights, grad_losses, grad_logits, grad_stride, stream=None):
+    _check(lib().moe_gate_backward(h, n, dtype, ptr(logits), logits_stride, normalize, ptr(experts), ptr(weights),
+                                   ptr(counts), ptr(stats), ptr(live_count), ptr(grad_weights), ptr(grad_losses),
+                                   ptr(grad_logits), grad_stride, _stream(stream)), "moe_gate_backward")
+
+
 def moe_destroy(h):
     _check(lib().moe_destroy(h), "moe_destroy")
+
+
+def norm_create(dim):
+    h = c_void_p()
+    _check(lib().norm_create(dim, ctypes.byref(h)), "norm_create")
+    return h.value
+
+
+def norm_forward(h, batch, length, dtype, x, offsets, weight_dtype, weight, bias, eps, y, stats, stream=None):
+    _check(lib().norm_forward(h, batch, length, dtype, _ref(x), ptr(offsets), weight_dtype, ptr(weight), ptr(bias),
+                              eps, _ref(y), ptr(stats), _stream(stream)), "norm_forward")
+
+
+def norm_backward(h, batch, length, dtype, x, offsets, weight_dtype, weight, grad_y, stats, grad_x, grad_weight,
+                  grad_bias, stream=None):
+    _check(lib().norm_backward(h, batch, length, dtype, _ref(x), ptr(offsets), weight_dtype, ptr(weight),
+                               _ref(grad_y), ptr(stats), _ref(grad_x), ptr(grad_weight), ptr(grad_bias),
+                               _stream(stream)), "norm_backward")
+
+
+def norm_destroy(h):
+    _check(lib().norm_destroy(h), "norm_destroy")
 
 
 def adamw_create(tensors, flags):
@@ -397,10 +432,34 @@ class Routing:
         return r
 
 
+class Gate:
+    """What a batch's logits gave (moe_gate of emb.h):
+    experts     [tokens, top_k] int32: choices, -1 where there is none
+    weights     [tokens, top_k] float32
+    counts      [experts] int32: choices of each expert
+    losses      [2] float32: balance and z
+    stats       [tokens, 2] float32: largest logit, -infinity for a token that is
+                not live, and sum of the exponentials beside it
+    live_count  [1] int32
+    normalize   whether the weights are a softmax over the choices alone"""
+
+    __slots__ = ("_arrays", "_shape", "normalize")
+
+    def __init__(self, arrays, shape, normalize):
+        self._arrays, self._shape, self.normalize = arrays, shape, normalize
+
+    experts = property(lambda self: self._arrays[0])
+    weights = property(lambda self: self._arrays[1])
+    counts = property(lambda self: self._arrays[2])
+    losses = property(lambda self: self._arrays[3])
+    stats = property(lambda self: self._arrays[4])
+    live_count = property(lambda self: self._arrays[5])
+
+
 class ExpertRouter(_Handle):
-    """Tokens sorted by expert and back.  Each of at most max_tokens tokens
-    chooses top_k experts; every expert's rows start at a multiple of
-    align."""
+    """Tokens sorted by expert and back, and the gate that chooses their experts.
+    Each of at most max_tokens tokens chooses top_k experts; every expert's rows
+    start at a multiple of align."""
 
     _destroy = staticmethod(moe_destroy)
 
@@ -411,11 +470,57 @@ class ExpertRouter(_Handle):
         L = lib()
         self._route, self._dispatch, self._combine = L.moe_route, L.moe_dispatch, L.moe_combine
         self._combine_backward = L.moe_combine_backward
+        self._gate, self._gate_backward = L.moe_gate, L.moe_gate_backward
 
     def rows(self, n_tokens):
         """Rows of the expert-ordered arrays for n_tokens tokens."""
         a = self.align
         return (n_tokens * self.top_k + self.n_experts * (a - 1) + a - 1) // a * a
+
+    def gate(self, logits, live=None, normalize=True, stream=None):
+        """Gate of logits [tokens, experts]: every live token's top_k choices
+        (equal logits in the experts' order), their weights (normalize: a softmax
+        over the choices, else over all), the experts' counts and the balance
+        and z losses.  live: [tokens] bool, None = all."""
+        shape, E, K, i32, f32 = logits.shape, self.n_experts, self.top_k, self._i32, self._f32
+        if len(shape) != 2 or shape[1] != E:
+            raise ValueError("logits: [tokens, %d] expected, got %s" % (E, tuple(shape)))
+        n, dt = shape[0], logits.dtype
+        at = self._want(logits, "logits", shape, dt, False)
+        on = None if live is None else self._want(live, "live", (n,), self._t.bool)
+        # one allocation each of the arrays that grow with the batch and of the others
+        each = self._empty((2 * n * (K + 1),), f32, logits, stream)
+        rest = self._empty((E + 3,), i32, logits, stream)
+        stats, experts = each[:2 * n].view(n, 2), each[2 * n:n * (K + 2)].view(i32).view(n, K)
+        weights = each[n * (K + 2):].view(n, K)
+        counts, losses, count = rest[:E], rest[E:E + 2].view(f32), rest[E + 2:]
+        p, q = each.data_ptr(), rest.data_ptr()
+        st = self._gate(self.handle, n, _element(dt), at, logits.stride(0), on, normalize, p + 8 * n,
+                        p + 4 * n * (K + 2), q, q + 4 * E, p, q + 4 * (E + 2), self._at(stream))
+        if st:
+            _check(st, "moe_gate")
+        return Gate((experts, weights, counts, losses, stats, count), (n, K, E, self._device), bool(normalize))
+
+    def gate_backward(self, logits, gate, grad_weights=None, grad_losses=None, grad_logits=None, stream=None):
+        """Gradient of gate()'s logits from those of its weights [tokens, top_k]
+        and losses [2] (float32, None = 0)."""
+        shape, dt, f32 = logits.shape, logits.dtype, self._f32
+        n, K, E, device = gate._shape
+        if K != self.top_k or E != self.n_experts or device != self._device:
+            raise ValueError("gate: %d of %d experts on cuda:%d" % (K, E, device))
+        at = self._want(logits, "logits", (n, E), dt, False)
+        gw = None if grad_weights is None else self._want(grad_weights, "grad_weights", (n, K), f32)
+        gl = None if grad_losses is None else self._want(grad_losses, "grad_losses", (2,), f32)
+        if grad_logits is None:
+            grad_logits = self._empty(shape, dt, logits, stream)
+        to = self._want(grad_logits, "grad_logits", shape, dt, False)
+        experts, weights, counts, _, stats, count = gate._arrays
+        st = self._gate_backward(self.handle, n, _element(dt), at, logits.stride(0), gate.normalize,
+                                 experts.data_ptr(), weights.data_ptr(), counts.data_ptr(), stats.data_ptr(),
+                                 count.data_ptr(), gw, gl, to, grad_logits.stride(0), self._at(stream))
+        if st:
+            _check(st, "moe_gate_backward")
+        return grad_logits
 
     def route(self, experts, stream=None):
         """Routing of experts [tokens, top_k] int32 (a choice outside [0,
@@ -507,6 +612,86 @@ class ExpertRouter(_Handle):
     def dispatch_backward(self, grad_xs, routing, grad_x=None, stream=None):
         """grad_x [tokens, dim] of dispatch: the sum of each token's rows."""
         return self.combine(grad_xs, None, routing, grad_x, stream)
+
+
+class LayerNorm(_Handle):
+    """Layer norm over the last axis of rows [rows, dim] or of padded sequences
+    [batch, time, dim] (float32, bfloat16 or float16, any strides with a contiguous
+    last axis), forward and backward with the gradients of weight and bias.  weight
+    and bias are float32 or of the rows' type; None = 1 and 0.  ``offsets`` as
+    GatedScan takes them: past an entry's end y and the gradient are 0, and nothing
+    is added to the weight's."""
+
+    _destroy = staticmethod(norm_destroy)
+
+    def __init__(self, dim, eps=1e-5):
+        super().__init__()
+        self.dim, self.eps = dim, eps
+        self._made(norm_create(dim))
+        L = lib()
+        self._fwd, self._bwd = L.norm_forward, L.norm_backward
+
+    def _view(self, t, name, shape, dtype):
+        """(pointer, batch stride, row stride) of rows or of padded sequences."""
+        p = self._want(t, name, shape, dtype, False)
+        s = t.stride()
+        return (p, 0, s[0]) if len(s) == 2 else (p, s[0], s[1])
+
+    def _common(self, x, weight, bias, offsets):
+        shape, dt = x.shape, x.dtype
+        if len(shape) not in (2, 3) or shape[-1] != self.dim:
+            raise ValueError("x: [rows, %d] or [batch, time, %d] expected, got %s" % (self.dim, self.dim, tuple(shape)))
+        B, n = (1, shape[0]) if len(shape) == 2 else (shape[0], shape[1])
+        if offsets is not None and len(shape) == 2:
+            raise ValueError("offsets: of [batch, time, dim] sequences only")
+        code, wdt = _element(dt), self._f32
+        given = weight if weight is not None else bias
+        if given is not None and given.dtype is dt:
+            wdt = dt
+        flat = (self.dim,)
+        return (B, n, code, dt, shape, None if offsets is None else self._want(offsets, "offsets", (B + 1,), self._i32),
+                _element(wdt), None if weight is None else self._want(weight, "weight", flat, wdt),
+                None if bias is None else self._want(bias, "bias", flat, wdt))
+
+    def forward(self, x, weight=None, bias=None, offsets=None, y=None, stats=None, stream=None):
+        """(y, stats): the normalised rows, and [..., 2] float32 with each row's
+        mean and 1 / deviation, which backward takes.  Both may be given."""
+        B, n, code, dt, shape, o, wc, w, b = self._common(x, weight, bias, offsets)
+        if y is None:
+            y = self._empty(shape, dt, x, stream)
+        two = (*shape[:-1], 2)
+        if stats is None:
+            stats = self._empty(two, self._f32, x, stream)
+        held = (c_int64 * 6)(*self._view(x, "x", shape, dt), *self._view(y, "y", shape, dt))
+        v = ctypes.addressof(held)
+        st = self._fwd(self.handle, B, n, code, v, o, wc, w, b, self.eps, v + 24,
+                       self._want(stats, "stats", two, self._f32), self._at(stream))
+        if st:
+            _check(st, "norm_forward")
+        return y, stats
+
+    def backward(self, x, grad_y, stats, weight=None, offsets=None, grad_x=None, grad_weight=None, grad_bias=None,
+                 stream=None):
+        """(grad_x, grad_weight, grad_bias) from the gradient of y; x, weight and
+        offsets as in forward, stats as it gave them.  The weight's and the bias'
+        are [dim] float32.  The results may be given."""
+        B, n, code, dt, shape, o, wc, w, _ = self._common(x, weight, None, offsets)
+        f32, flat = self._f32, (self.dim,)
+        if grad_x is None:
+            grad_x = self._empty(shape, dt, x, stream)
+        if grad_weight is None:
+            grad_weight = self._empty(flat, f32, x, stream)
+        if grad_bias is None:
+            grad_bias = self._empty(flat, f32, x, stream)
+        held = (c_int64 * 9)(*self._view(x, "x", shape, dt), *self._view(grad_y, "grad_y", shape, dt),
+                             *self._view(grad_x, "grad_x", shape, dt))
+        v = ctypes.addressof(held)
+        st = self._bwd(self.handle, B, n, code, v, o, wc, w, v + 24, self._want(stats, "stats", (*shape[:-1], 2), f32),
+                       v + 48, self._want(grad_weight, "grad_weight", flat, f32),
+                       self._want(grad_bias, "grad_bias", flat, f32), self._at(stream))
+        if st:
+            _check(st, "norm_backward")
+        return grad_x, grad_weight, grad_bias
 
 
 class AdamW(_Handle):
