@@ -693,6 +693,78 @@ emb_status norm_backward(emb_norm h, int32_t batch, int64_t len, int32_t dtype, 
                          void* stream);
 emb_status norm_destroy(emb_norm h);
 
+typedef struct emb_delta_s* emb_delta;
+
+/* A [batch, time, heads, dim] array: element (b, t, h, d) is data[b * batch_stride +
+ * t * time_stride + h * head_stride + d] (strides in elements, >= 0); of decays and
+ * betas [batch, time, heads] fp32, without d.  Outputs need heads within positions
+ * within entries, each behind the one before. */
+typedef struct {
+    void* data;
+    int64_t batch_stride;
+    int64_t time_stride;
+    int64_t head_stride;
+} delta_view;
+
+/* delta_create -- workspace of the gated delta rule over sequences, a recurrence whose
+ * state of a head is a matrix S [key_dim, value_dim]:
+ *   S' = exp(decay_t) S_{t-1};  e_t = v_t - S'^T k_t
+ *   S_t = S' + beta_t k_t e_t^T;  y_t = scale S_t^T q_t
+ * key_dim, value_dim 1 .. 128; heads of v, y, decay and beta, a multiple of key_heads,
+ * those of q and k (head h reads key head h / (heads / key_heads)); at most max_batch
+ * entries of at most max_len positions, max_batch * heads < 2^27.
+ * training != 0: the handle can run the backward, for which it holds, for each head of
+ * each entry and each 32 positions, the state before them (6 bytes a number, key_dim
+ * rounded up to 32, 64 or 128 and value_dim to a multiple of 16) and 136 bytes a value
+ * channel; where value heads share a key head, 8 bytes a position, head and key channel
+ * more.  Calls on one handle must be ordered.  *out is NULL on error. */
+emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t heads, int32_t key_heads, int32_t max_batch,
+                        int32_t max_len, int32_t training, emb_delta* out);
+
+/* delta_forward -- y at every position and the state after the last live one.
+ *  q, k       [batch, len, key_heads, key_dim] of `dtype`
+ *  v, y       [batch, len, heads, value_dim] of `dtype`
+ *  decay      [batch, len, heads] fp32, the logarithm of the factor (<= 0 in use; below
+ *             -512, -infinity among it, it counts as -512, whose factor is 0: the state
+ *             is forgotten)
+ *  beta       [batch, len, heads] fp32.  The recurrence stays bounded where
+ *             0 <= beta <= 2 / |k|^2: keys are usually of unit length
+ *  offsets    NULL, or [batch + 1] int32 as in scan_forward: positions past an
+ *             entry's end read nothing; their y is 0
+ *  state_in   NULL = 0, or [batch, heads, key_dim, value_dim] fp32
+ *  state_out  NULL, or the same shape
+ * Products run on the matrix units: fp32 operands in three bf16 terms (24 bits; two for
+ * a 16-bit y), sums in fp32.  An infinite input or state makes its head's later numbers
+ * infinite or NaN. */
+emb_status delta_forward(emb_delta h, int32_t batch, int32_t len, int32_t dtype, const delta_view* q,
+                         const delta_view* k, const delta_view* v, const delta_view* decay, const delta_view* beta,
+                         const int32_t* offsets, double scale, const float* state_in, const delta_view* y,
+                         float* state_out, void* stream);
+
+/* delta_backward -- gradients of delta_forward's q, k, v, decay, beta and state_in from
+ * its inputs and the gradients of y and state_out (NULL = 0).  q and k that several value
+ * heads share get the sum over them.  Positions past an entry's end read nothing and get
+ * gradient 0.  grad_state_in NULL = not wanted.  A training handle's;
+ * EMB_ERR_UNSUPPORTED on another.  fp32 operands are in three bf16 terms, of fp16 and
+ * fp32 calls with key_dim > 64 in two (each off by 2^-17 of itself at most); for the
+ * gradients of q and k of bf16 calls the states are rounded to bf16. */
+emb_status delta_backward(emb_delta h, int32_t batch, int32_t len, int32_t dtype, const delta_view* q,
+                          const delta_view* k, const delta_view* v, const delta_view* decay, const delta_view* beta,
+                          const int32_t* offsets, double scale, const float* state_in, const delta_view* grad_y,
+                          const float* grad_state_out, const delta_view* grad_q, const delta_view* grad_k,
+                          const delta_view* grad_v, const delta_view* grad_decay, const delta_view* grad_beta,
+                          float* grad_state_in, void* stream);
+
+/* delta_step -- one position for each of n sessions whose states are rows of a pool
+ * [num_rows, heads, key_dim, value_dim] fp32 (serving): row = rows[i].  A row outside
+ * [0, num_rows) (-1: no row yet) is dropped: y_i = 0.  Rows of one call must be
+ * distinct.  The views' time strides are not used; n * heads < 2^31. */
+emb_status delta_step(int64_t n, int32_t key_dim, int32_t value_dim, int32_t heads, int32_t key_heads, int32_t dtype,
+                      const delta_view* q, const delta_view* k, const delta_view* v, const delta_view* decay,
+                      const delta_view* beta, double scale, const int64_t* rows, float* states, int64_t num_rows,
+                      const delta_view* y, void* stream);
+emb_status delta_destroy(emb_delta h);
+
 /* ------------------------------------------------------------------------ */
 /* Self tests and fault injection (no counterpart on the pages)              */
 /* ------------------------------------------------------------------------ */

@@ -114,6 +114,13 @@ _SIGS = {
     "moe_gate_backward": (c_int32, [c_void_p, c_int64, c_int32, c_void_p, c_int64, c_int32] + [c_void_p] * 8 +
                           [c_int64, c_void_p]),
     "moe_destroy": (c_int32, [c_void_p]),
+    "delta_create": (c_int32, [c_int32] * 7 + [POINTER(c_void_p)]),
+    "delta_forward": (c_int32, [c_void_p, c_int32, c_int32, c_int32] + [c_void_p] * 6 + [c_double] + [c_void_p] * 4),
+    "delta_backward": (c_int32, [c_void_p, c_int32, c_int32, c_int32] + [c_void_p] * 6 + [c_double] +
+                       [c_void_p] * 10),
+    "delta_step": (c_int32, [c_int64] + [c_int32] * 5 + [c_void_p] * 5 + [c_double, c_void_p, c_void_p, c_int64] +
+                   [c_void_p] * 2),
+    "delta_destroy": (c_int32, [c_void_p]),
     "norm_create": (c_int32, [c_int32, POINTER(c_void_p)]),
     "norm_forward": (c_int32, [c_void_p, c_int32, c_int64, c_int32, c_void_p, c_void_p, c_int32, c_void_p, c_void_p,
                                c_double, c_void_p, c_void_p, c_void_p]),
@@ -520,9 +527,10 @@ def _device_view(ptr_value, shape):
     return torch.as_tensor(h, device="cuda")
 
 
-from .dense import (AdamW, AdamwTensor, ExpertRouter, Gate, GatedScan, LayerNorm, Routing, ScanView,  # noqa: E402,F401
-                    adamw_bind_grads, adamw_create, adamw_destroy, adamw_export_size, adamw_export_states,
-                    adamw_get_step, adamw_set_max_update, adamw_set_step, adamw_step, moe_combine,
+from .dense import (AdamW, AdamwTensor, DeltaScan, DeltaView, ExpertRouter, Gate, GatedScan, LayerNorm,  # noqa: E402,F401
+                    Routing, ScanView, adamw_bind_grads, adamw_create, adamw_destroy, adamw_export_size,
+                    adamw_export_states, adamw_get_step, adamw_set_max_update, adamw_set_step, adamw_step,
+                    delta_backward, delta_create, delta_destroy, delta_forward, delta_step, moe_combine,
                     moe_combine_backward, moe_create, moe_destroy, moe_dispatch, moe_gate, moe_gate_backward,
                     moe_route, norm_backward, norm_create, norm_destroy, norm_forward, scan_backward, scan_create,
                     scan_destroy, scan_forward, scan_get_device_status, scan_selftest_timeout, scan_step)

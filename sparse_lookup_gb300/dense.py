@@ -1,6 +1,6 @@
-"""Operators of the dense layers behind the lookups (scan_*, moe_* and adamw_*
-of include/emb.h): raw C names, then GatedScan, ExpertRouter and AdamW over
-PyTorch tensors.  Marshalling only, like the rest of the binding; arguments
+"""Operators of the dense layers behind the lookups (scan_*, delta_*, moe_*,
+norm_* and adamw_* of include/emb.h): raw C names, then GatedScan, DeltaScan,
+ExpertRouter, LayerNorm and AdamW over PyTorch tensors.  Marshalling only, like the rest of the binding; arguments
 that the library cannot see (shapes, element types, devices) are checked here
 and raise ValueError: every tensor of a call, its stream and the current device
 are those of the handle, which is the device that was current when it was made.
@@ -25,6 +25,10 @@ _dtype_codes = {}    # torch dtype -> emb_table_dtype
 
 class ScanView(ctypes.Structure):
     _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("time_stride", c_int64)]
+
+
+class DeltaView(ctypes.Structure):
+    _fields_ = [("data", c_void_p), ("batch_stride", c_int64), ("time_stride", c_int64), ("head_stride", c_int64)]
 
 
 _Views = c_int64 * 18   # a call's scan_views, one after the other: each call has its own
@@ -144,6 +148,38 @@ def moe_gate_backward(h, n, dtype, logits, logits_stride, normalize, experts, we
 
 def moe_destroy(h):
     _check(lib().moe_destroy(h), "moe_destroy")
+
+
+def delta_create(key_dim, value_dim, heads, key_heads, max_batch, max_len, training):
+    h = c_void_p()
+    _check(lib().delta_create(key_dim, value_dim, heads, key_heads, max_batch, max_len, training, ctypes.byref(h)),
+           "delta_create")
+    return h.value
+
+
+def delta_forward(h, batch, length, dtype, q, k, v, decay, beta, offsets, scale, state_in, y, state_out, stream=None):
+    _check(lib().delta_forward(h, batch, length, dtype, _ref(q), _ref(k), _ref(v), _ref(decay), _ref(beta),
+                               ptr(offsets), scale, ptr(state_in), _ref(y), ptr(state_out), _stream(stream)),
+           "delta_forward")
+
+
+def delta_backward(h, batch, length, dtype, q, k, v, decay, beta, offsets, scale, state_in, grad_y, grad_state_out,
+                   grad_q, grad_k, grad_v, grad_decay, grad_beta, grad_state_in, stream=None):
+    _check(lib().delta_backward(h, batch, length, dtype, _ref(q), _ref(k), _ref(v), _ref(decay), _ref(beta),
+                                ptr(offsets), scale, ptr(state_in), _ref(grad_y), ptr(grad_state_out), _ref(grad_q),
+                                _ref(grad_k), _ref(grad_v), _ref(grad_decay), _ref(grad_beta), ptr(grad_state_in),
+                                _stream(stream)), "delta_backward")
+
+
+def delta_step(n, key_dim, value_dim, heads, key_heads, dtype, q, k, v, decay, beta, scale, rows, states, num_rows, y,
+               stream=None):
+    _check(lib().delta_step(n, key_dim, value_dim, heads, key_heads, dtype, _ref(q), _ref(k), _ref(v), _ref(decay),
+                            _ref(beta), scale, ptr(rows), ptr(states), num_rows, _ref(y), _stream(stream)),
+           "delta_step")
+
+
+def delta_destroy(h):
+    _check(lib().delta_destroy(h), "delta_destroy")
 
 
 def norm_create(dim):
@@ -395,6 +431,137 @@ class GatedScan(_Handle):
 
     def device_status(self, stream=None):
         return scan_get_device_status(self.handle, self._at(stream))
+
+
+class DeltaScan(_Handle):
+    """The gated delta rule over [batch, time, heads, dim] sequences, a recurrence
+    whose state of a head is a matrix S [key_dim, value_dim]:
+
+        S' = exp(decay_t) S_{t-1};  S_t = S' + beta_t k_t (v_t - S'^T k_t)^T;  y_t = scale S_t^T q_t
+
+    forward and backward over whole sequences (float32, bfloat16 or float16, any
+    strides with a contiguous last axis; decay, beta and states in float32), and one
+    step for serving on state rows of a pool.  v, y, decay and beta have ``heads``
+    heads, q and k ``key_heads`` (None: as many), each for heads / key_heads
+    neighbouring ones.  decay is a logarithm (<= 0; -infinity forgets the state).
+    scale: key_dim ** -0.5 if None.  ``offsets`` as GatedScan takes them: past an
+    entry's end y and the gradients are 0.  training: room for backward."""
+
+    _destroy = staticmethod(delta_destroy)
+
+    def __init__(self, key_dim, value_dim, heads, max_batch, max_len, key_heads=None, scale=None, training=False):
+        super().__init__()
+        self.key_dim, self.value_dim, self.heads = key_dim, value_dim, heads
+        self.key_heads = heads if key_heads is None else key_heads
+        self.scale = (key_dim ** -0.5 if key_dim > 0 else 1.0) if scale is None else scale
+        self.training = bool(training)
+        self._made(delta_create(key_dim, value_dim, heads, self.key_heads, max_batch, max_len, self.training))
+        L = lib()
+        self._fwd, self._bwd, self._step = L.delta_forward, L.delta_backward, L.delta_step
+
+    def _view(self, t, name, shape, dtype):
+        """(pointer, batch, time and head stride) of a [batch, time, heads, dim] tensor."""
+        p = self._want(t, name, shape, dtype, False)
+        return (p, *t.stride()[:3])
+
+    def _each(self, t, name, shape):
+        """The same of a [batch, time, heads] float32 tensor of any strides."""
+        if t.dtype is not self._f32 or t.shape != shape or t.get_device() != self._device:
+            self._want(t, name, shape, self._f32)
+        return (t.data_ptr(), *t.stride())
+
+    def _common(self, q, k, v, decay, beta, offsets, state):
+        shape, dt = v.shape, v.dtype
+        if len(shape) != 4 or shape[2] != self.heads or shape[3] != self.value_dim:
+            raise ValueError("v: [batch, time, %d, %d] expected, got %s" % (self.heads, self.value_dim, tuple(shape)))
+        B, n = shape[0], shape[1]
+        keys, each, ends = (B, n, self.key_heads, self.key_dim), (B, n, self.heads), self._ends(B)
+        views = (*self._view(q, "q", keys, dt), *self._view(k, "k", keys, dt), *self._view(v, "v", shape, dt),
+                 *self._each(decay, "decay", each), *self._each(beta, "beta", each))
+        return (B, n, _element(dt), dt, shape, keys, each, ends,
+                None if offsets is None else self._want(offsets, "offsets", (B + 1,), self._i32),
+                None if state is None else self._want(state, "state", ends, self._f32), views)
+
+    def _ends(self, n):
+        return (n, self.heads, self.key_dim, self.value_dim)
+
+    def forward(self, q, k, v, decay, beta, offsets=None, state=None, y=None, last=None, stream=None):
+        """(y, last): [batch, time, heads, value_dim], and the state [batch, heads,
+        key_dim, value_dim] float32 after the last live position.  state: the one
+        before the first (None = 0).  y and last may be given."""
+        B, n, code, dt, shape, _, _, ends, o, s, views = self._common(q, k, v, decay, beta, offsets, state)
+        if y is None:
+            y = self._empty(shape, dt, v, stream)
+        if last is None:
+            last = self._empty(ends, self._f32, v, stream)
+        held = (c_int64 * 24)(*views, *self._view(y, "y", shape, dt))
+        a = ctypes.addressof(held)
+        st = self._fwd(self.handle, B, n, code, a, a + 32, a + 64, a + 96, a + 128, o, self.scale, s, a + 160,
+                       self._want(last, "last", ends, self._f32), self._at(stream))
+        if st:
+            _check(st, "delta_forward")
+        return y, last
+
+    def backward(self, q, k, v, decay, beta, grad_y, offsets=None, state=None, grad_last=None, grad_q=None,
+                 grad_k=None, grad_v=None, grad_decay=None, grad_beta=None, grad_state=None, stream=None):
+        """(grad_q, grad_k, grad_v, grad_decay, grad_beta, grad_state) from the
+        gradients of y and (None = 0) of last; the inputs as in forward.  The
+        results may be given."""
+        B, n, code, dt, shape, keys, each, ends, o, s, views = self._common(q, k, v, decay, beta, offsets, state)
+        f32 = self._f32
+        gl = None if grad_last is None else self._want(grad_last, "grad_last", ends, f32)
+        if grad_q is None:
+            grad_q = self._empty(keys, dt, v, stream)
+        if grad_k is None:
+            grad_k = self._empty(keys, dt, v, stream)
+        if grad_v is None:
+            grad_v = self._empty(shape, dt, v, stream)
+        if grad_decay is None:
+            grad_decay = self._empty(each, f32, v, stream)
+        if grad_beta is None:
+            grad_beta = self._empty(each, f32, v, stream)
+        if grad_state is None:
+            grad_state = self._empty(ends, f32, v, stream)
+        held = (c_int64 * 44)(*views, *self._view(grad_y, "grad_y", shape, dt), *self._view(grad_q, "grad_q", keys, dt),
+                              *self._view(grad_k, "grad_k", keys, dt), *self._view(grad_v, "grad_v", shape, dt),
+                              *self._each(grad_decay, "grad_decay", each), *self._each(grad_beta, "grad_beta", each))
+        a = ctypes.addressof(held)
+        st = self._bwd(self.handle, B, n, code, a, a + 32, a + 64, a + 96, a + 128, o, self.scale, s, a + 160, gl,
+                       a + 192, a + 224, a + 256, a + 288, a + 320, self._want(grad_state, "grad_state", ends, f32),
+                       self._at(stream))
+        if st:
+            _check(st, "delta_backward")
+        return grad_q, grad_k, grad_v, grad_decay, grad_beta, grad_state
+
+    def step(self, q, k, v, decay, beta, rows, states, y=None, stream=None):
+        """One position for each of n sessions: q, k [n, key_heads, key_dim], v [n,
+        heads, value_dim], decay, beta [n, heads]; rows [n] int64, the session's row of
+        states [num_rows, heads, key_dim, value_dim] float32 (outside: dropped, y = 0).
+        Updates states in place, returns y [n, heads, value_dim].  Rows of one call
+        must be distinct."""
+        shape, dt, H = v.shape, v.dtype, self.heads
+        if len(shape) != 3 or shape[1] != H or shape[2] != self.value_dim or states.dim() != 4:
+            raise ValueError("v: [n, %d, %d] and states [num_rows, %d, %d, %d] expected" % (
+                H, self.value_dim, H, self.key_dim, self.value_dim))
+        n, pool = shape[0], states.shape[0]
+        keys = (n, self.key_heads, self.key_dim)
+        if y is None:
+            y = self._empty(shape, dt, v, stream)
+        held = []
+        for t, name, want in ((q, "q", keys), (k, "k", keys), (v, "v", shape), (y, "y", shape)):
+            p = self._want(t, name, want, dt, False)
+            held += (p, t.stride(0), 0, t.stride(1))
+        for t, name in ((decay, "decay"), (beta, "beta")):
+            p = self._each(t, name, (n, H))
+            held += (p[0], p[1], 0, p[2])
+        held = (c_int64 * 24)(*held)
+        a = ctypes.addressof(held)
+        st = self._step(n, self.key_dim, self.value_dim, H, self.key_heads, _element(dt), a, a + 32, a + 64, a + 128,
+                        a + 160, self.scale, self._want(rows, "rows", (n,), self._t.int64),
+                        self._want(states, "states", self._ends(pool), self._f32), pool, a + 96, self._at(stream))
+        if st:
+            _check(st, "delta_step")
+        return y
 
 
 class Routing:
