@@ -430,9 +430,9 @@ __global__ void __launch_bounds__(384)
                 int producers) {
   using Stage = ForwardStage<T, DK, STATES>;
   constexpr int NT = Stage::NT, IT = Stage::IT, lp = Stage::lp, plane = Stage::plane;
-  // terms of what goes into y alone: 16 bits are stored of it, or its product with
-  // grad_y summed over the channels, so two carry enough; fp32 results get all
-  constexpr int NO = sizeof(T) == 2 ? 2 : NT;
+  // terms of what goes into y alone: 16 bits are stored of it, so two carry enough.  The
+  // decays' gradients are sums of <grad_y, y> over many positions: all terms
+  constexpr int NO = !STATES && sizeof(T) == 2 ? 2 : NT;
   extern __shared__ __align__(128) unsigned char held[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int consumers = (blockDim.x >> 5) - producers, meeting = 32 * (consumers + 1);
