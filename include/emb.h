@@ -713,11 +713,12 @@ typedef struct {
  * key_dim, value_dim 1 .. 128; heads of v, y, decay and beta, a multiple of key_heads,
  * those of q and k (head h reads key head h / (heads / key_heads)); at most max_batch
  * entries of at most max_len positions, max_batch * heads < 2^27.
- * training != 0: the handle can run the backward, for which it holds, for each head of
- * each entry and each 32 positions, the state before them (6 bytes a number, key_dim
- * rounded up to 32, 64 or 128 and value_dim to a multiple of 16) and 136 bytes a value
- * channel; where value heads share a key head, 8 bytes a position, head and key channel
- * more.  Calls on one handle must be ordered.  *out is NULL on error. */
+ * The handle holds 14464 bytes for each head of each entry and each 32 positions, of
+ * which there may be 2^36 (237 MB for 32 x 2048 positions of 8 heads).
+ * training != 0: it can run the backward, for which it holds as often the state before
+ * them (6 bytes a number, key_dim rounded up to 32, 64 or 128 and value_dim to a multiple
+ * of 16) and 136 bytes a value channel; where value heads share a key head, 8 bytes a
+ * position, head and key channel more.  Calls on one handle must be ordered.  *out is NULL on error. */
 emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t heads, int32_t key_heads, int32_t max_batch,
                         int32_t max_len, int32_t training, emb_delta* out);
 

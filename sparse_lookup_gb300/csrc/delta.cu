@@ -147,7 +147,7 @@ DeltaArgs delta_args(emb_delta h, int32_t batch, int32_t len, const int32_t* off
   a.scale = (float)scale;
   a.offsets = offsets;
   a.state_in = state_in;
-  a.work = {{h->s[0], h->s[1], h->s[2]}, h->e, h->dots, h->shared, (int64_t)batch * h->heads * a.chunks};
+  a.work = {h->record, {h->s[0], h->s[1], h->s[2]}, h->e, h->dots, h->shared, (int64_t)batch * h->heads * a.chunks};
   return a;
 }
 
@@ -158,6 +158,7 @@ cudaError_t run(emb_delta h, const DeltaArgs& a, const DeltaViews& w, int32_t dt
 }
 
 void delta_free(emb_delta h) {
+  dev_free(h->record);
   for (uint4* p : h->s) dev_free(p);
   dev_free(h->e);
   dev_free(h->dots);
@@ -178,7 +179,8 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
   if (key_dim < 1 || value_dim < 1 || heads < 1 || key_heads < 1 || heads % key_heads || max_batch < 1 || max_len < 1)
     return EMB_ERR_INVALID_ARG;
   if (key_dim > 128 || value_dim > 128 || heads > 65536 || max_len > (1 << 30) ||
-      (int64_t)max_batch * heads >= (int64_t(1) << 27))
+      (int64_t)max_batch * heads >= (int64_t(1) << 27) ||
+      (int64_t)max_batch * heads * (max_len / kChunk + 1) >= (int64_t(1) << 36))
     return EMB_ERR_UNSUPPORTED;
   emb_delta_s* h = new (std::nothrow) emb_delta_s();
   if (!h) return EMB_ERR_OOM;
@@ -186,11 +188,10 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
   h->max_batch = max_batch, h->max_len = max_len, h->training = training != 0;
   cudaError_t e = cudaGetDevice(&h->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
+  const int64_t all = (int64_t)max_batch * heads, chunks = ((int64_t)max_len + kChunk - 1) / kChunk;
+  if (e == cudaSuccess) e = dev_alloc((void**)&h->record, all * chunks * Record::bytes);
   if (training) {
-    const int64_t all = (int64_t)max_batch * heads, chunks = ((int64_t)max_len + kChunk - 1) / kChunk;
     const int64_t W = (value_dim + 15) / 16, dk = dk_of(key_dim);
-    // sizes that do not fit 64 bits are refused as the allocation would refuse them
-    if (e == cudaSuccess && (double)all * (chunks + 1) * kChunk * W * dk * 32 >= 9e18) e = cudaErrorMemoryAllocation;
     for (uint4*& p : h->s)
       if (e == cudaSuccess) e = dev_alloc((void**)&p, all * (chunks + 1) * W * (dk / 16) * 32 * sizeof(uint4));
     if (e == cudaSuccess) e = dev_alloc((void**)&h->e, all * chunks * W * 4 * 32 * sizeof(float4));

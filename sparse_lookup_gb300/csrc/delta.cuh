@@ -19,8 +19,11 @@
 // these are warp-wide products (m16n8k16) and not tcgen05 ones: a tensor-memory
 // accumulator would have to come back through registers and shared memory after each
 // of the chain's five products, and 16 x 32 results fill an eighth of its smallest
-// tile.  Producer warps, each with a stage of shared memory, load a chunk and find
-// its inverse and A, one chunk each, ahead of the consumers.
+// tile.  What follows from a chunk's keys, queries and decays alone (the inverse, A, M)
+// is found before, all chunks at once, a warp each (k_delta_prepare): a warp needs some
+// microseconds for it, and one that ran ahead of the consumers would hold them up.
+// Producer warps, each with a stage of shared memory, copy a chunk's inputs and that
+// record ahead of the consumers.
 //
 // Precision: sums are fp32.  An fp32 operand is split into bf16 terms (x = x0 + x1 +
 // x2, each the rounded rest of those before); the products of terms i and j with i +
@@ -34,7 +37,8 @@
 struct emb_delta_s {
   int32_t key_dim = 0, value_dim = 0, heads = 0, key_heads = 0, max_batch = 0, max_len = 0, training = 0;
   int sm_count = 0, device = 0;
-  // for the backward (see DeltaWork)
+  unsigned char* record = nullptr;   // see DeltaWork
+  // for the backward
   uint4* s[3] = {nullptr, nullptr, nullptr};
   float4* e = nullptr;
   float* dots = nullptr;
@@ -52,9 +56,10 @@ struct DView {
   int64_t batch, time, head;
 };
 
-// What the states' pass leaves for the reverse pass, chunk after chunk of each
-// (entry, head), in the order of the lanes' registers.
+// A chunk's record, and what the states' pass leaves for the reverse pass, chunk after
+// chunk of each (entry, head), the states in the order of the lanes' registers.
 struct DeltaWork {
+  unsigned char* record;   // [chunks][Record::bytes]
   uint4* s[3];     // [chunks + 1][warps][DK / 16][32]: the state before a chunk in bf16 terms (fp32: three, else two)
   float4* e;       // [chunks][warps][4][32]: E
   float* dots;     // [warps][chunks][32]: <grad_y, y> over a warp's channels
@@ -93,6 +98,12 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
+// The way back: a lane's pairs to rows of 8 elements.
+__device__ __forceinline__ void store_matrices(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+               "r"(d) : "memory");
+}
+
 __device__ __forceinline__ void multiply(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
                "{%0,%1,%2,%3};"
@@ -114,8 +125,8 @@ __device__ __forceinline__ void split(float x, float y, uint32_t (&t)[N]) {
   for (int i = 0; i < N; ++i) {
     t[i] = pack(x, y);
     if (i + 1 < N) {
-      const float2 h = unpack(t[i]);
-      x -= h.x, y -= h.y;
+      const float2 r = __ffma2_rn(unpack(t[i]), make_float2(-1.f, -1.f), make_float2(x, y));
+      x = r.x, y = r.y;
     }
   }
 }
@@ -208,11 +219,14 @@ __device__ __forceinline__ void arrive(int id, int n) { asm volatile("bar.arrive
 // a stage: one chunk's inputs and what follows from them alone
 // ---------------------------------------------------------------------------
 
-// Numbers of a position in its chunk.
-struct Spot {
-  float since, until;   // exp(G_i), exp(G_31 - G_i)
-  float beta;
-  float g_hi, g_lo;     // G_i, as a multiple of 1/64 and the rest: differences keep their digits beside a large G
+// What follows from a chunk's keys, queries, decays and betas.
+struct Record {
+  // [32] floats each: exp(G_i), exp(G_31 - G_i), beta, and G_i as a multiple of 1/64 and the
+  // rest (differences keep their digits beside a large G)
+  static constexpr int since = 0, until = 128, beta = 256, g_hi = 384, g_lo = 512;
+  // [3 terms] of lower triangular matrices
+  static constexpr int inverse = 640, a = inverse + 3 * kLower, m = a + 3 * kLower, bytes = m + 3 * kLower;
+  static constexpr int forward_bytes = m;   // M is the backward's
 };
 
 template <class T>
@@ -244,14 +258,31 @@ struct Eight {
   __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(u)[i]); }
 };
 
-// Rows 0 .. 31 (`live` of them) of `cols` columns, by one warp: as bf16 terms in tiles
-// `plane` bytes apart of 2^lp pieces a row, or as fp32 rows of `width` (a multiple of
-// 16) and four floats.  Columns and rows beyond the array's are 0.
+__device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool on) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+// Rows 0 .. 31 (`live` of them) of `cols` columns, by one warp, as bf16 terms in tiles
+// `plane` bytes apart of 2^lp pieces a row.  Columns and rows beyond the array's are 0.
+// Aligned bf16 is only copied; copies_done() has to follow.
 template <class T, int IT>
 __device__ __forceinline__ void load_terms(unsigned char* tile, int plane, int lp, const T* rows, int64_t stride, int live,
                                            int cols, bool wide, int lane) {
   constexpr int U = sizeof(T) == 2 ? 8 : 4;
   const int pieces = 1 << lp, units = kChunk << lp;
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    if (wide) {
+      const uint32_t to = smem_of(tile);
+#pragma unroll 4
+      for (int u = lane; u < units; u += 32) {
+        const int r = u >> lp, p = u & (pieces - 1);
+        const bool on = r < live && p * 8 < cols;
+        copy_async(to + piece(r, p, lp), on ? rows + r * stride + p * 8 : rows, on);
+      }
+      return;
+    }
+  }
   for (int u0 = lane; u0 < units; u0 += 32 * U) {
     Eight<T> x[U];
 #pragma unroll
@@ -279,121 +310,55 @@ __device__ __forceinline__ void load_terms(unsigned char* tile, int plane, int l
     }
   }
 }
-template <class T>
-__device__ __forceinline__ void load_floats(float* tile, int width, const T* rows, int64_t stride, int live, int cols,
-                                            bool wide, int lane) {
-  constexpr int U = sizeof(T) == 2 ? 8 : 4;
-  const int lp = 32 - __clz((width >> 3) - 1), pieces = 1 << lp, units = kChunk << lp;
-  for (int u0 = lane; u0 < units; u0 += 32 * U) {
-    Eight<T> x[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k, r = u >> lp, c = (u & (pieces - 1)) << 3;
-      if (u >= units || r >= live || c >= cols) x[k].clear();
-      else if (wide) x[k].load(rows + r * stride + c);
-      else x[k].gather(rows + r * stride + c, cols - c);
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k, c = (u & (pieces - 1)) << 3;
-      if (u >= units || c >= width) continue;
-      float* to = tile + (u >> lp) * (width + 4) + c;
-      *reinterpret_cast<float4*>(to) = make_float4(x[k].at(0), x[k].at(1), x[k].at(2), x[k].at(3));
-      *reinterpret_cast<float4*>(to + 4) = make_float4(x[k].at(4), x[k].at(5), x[k].at(6), x[k].at(7));
-    }
-  }
-}
 
-// The chunk's positions, by one warp: position i is lane i.  A decay below -512 counts
-// as -512 (exp is 0 long before), so that -infinity forgets and sums stay exact.
-__device__ __forceinline__ void find_spots(Spot* spots, float g, float beta, int lane) {
-  g = g < -512.f ? -512.f : g;
-  float hi = rintf(g * 64.f) * 0.015625f, lo = g - hi;
+// X^T of such a tile in the layout of accumulators: rows e0 .. e0 + 15 are the tile's
+// columns, columns its 32 rows.
+template <int IT>
+__device__ __forceinline__ void load_turned(float (&x)[4][4], uint32_t tile, int plane, int e0, int lp, int lane) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const float a = __shfl_up_sync(kFull, hi, o), b = __shfl_up_sync(kFull, lo, o);
-    if (lane >= o) hi += a, lo += b;
-  }
-  const float end_hi = __shfl_sync(kFull, hi, 31), end_lo = __shfl_sync(kFull, lo, 31);
-  Spot s;
-  s.since = expf(hi) * expf(lo);
-  s.until = expf((end_hi - hi) + (end_lo - lo));
-  s.beta = beta;
-  s.g_hi = hi, s.g_lo = lo;
-  spots[lane] = s;
-}
-
-// exp(G_i - G_j)
-__device__ __forceinline__ float between(const Spot& i, const Spot& j) {
-  return expf((i.g_hi - j.g_hi) + (i.g_lo - j.g_lo));
-}
-
-// Lower blocks of D o (X K^T) by one warp, X and K in tiles of IT terms; put(i, j, value)
-// gets every element of the three blocks.
-template <int DK, int IT, class F>
-__device__ __forceinline__ void find_lower(uint32_t x, uint32_t k, int plane, const Spot* spots, int lane, F put) {
-  constexpr int lp = DK == 128 ? 4 : DK == 64 ? 3 : 2;
-  const int g = lane >> 2, t = lane & 3;
+  for (int s = 0; s < 2; ++s) {
+    uint32_t y[IT][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float acc[4][4];
-    zero(acc);
-    const auto left = [&](int s, uint32_t (&a)[IT][4]) {
+    for (int i = 0; i < IT; ++i) load_matrices<true>(y[i], tile + i * plane + left_cols(lane, e0, 16 * s, lp));
 #pragma unroll
-      for (int i = 0; i < IT; ++i) load_matrices<false>(a[i], x + i * plane + left_rows(lane, 16 * m, 16 * s, lp));
-    };
-    const auto right = [&](int p, int s, int j) { return k + j * plane + right_rows(lane, 16 * p, 16 * s, lp); };
-    if (m == 0) {
-      float one[2][4];
-      zero(one);
-      product<DK / 16, 1, IT, IT, 3, false, 0>(one, left, right);
+    for (int i = 0; i < 4; ++i) {
+      float2 f = unpack(y[IT - 1][i]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][r] = one[i][r];
-    } else {
-      product<DK / 16, 2, IT, IT, 3, false, 0>(acc, left, right);
-    }
-#pragma unroll
-    for (int n = 0; n < 2 * (m + 1); ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 16 * m + g + (r >> 1) * 8, j = 8 * n + 2 * t + (r & 1);
-        put(i, j, i >= j ? acc[n][r] * between(spots[i], spots[j]) : 0.f);
+      for (int j = IT - 2; j >= 0; --j) {
+        const float2 l = unpack(y[j][i]);
+        f.x += l.x, f.y += l.y;
       }
-  }
-}
-
-template <int N>
-__device__ __forceinline__ void put_lower(unsigned char* tile, int i, int j, float x) {
-#pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const __nv_bfloat16 h = __float2bfloat16_rn(x);
-    *reinterpret_cast<__nv_bfloat16*>(tile + k * kLower + lower_at(i, j)) = h;
-    x -= __bfloat162float(h);
-  }
-}
-
-// (I + M diag(beta))^-1 by forward substitution, column j in lane j; row i of `m`
-// (32 x 36 floats) holds M_ij beta_j.  By substitution, not by powers of M, which
-// cancel where keys repeat.
-template <int N>
-__device__ __forceinline__ void invert(const float* m, unsigned char* tile, int lane) {
-  float x[kChunk];
-#pragma unroll
-  for (int i = 0; i < kChunk; ++i) {
-    float a = i == lane ? 1.f : 0.f, b = 0.f, c = 0.f, d = 0.f;
-#pragma unroll
-    for (int l = 0; l < i; l += 4) {
-      const float4 w = *reinterpret_cast<const float4*>(m + i * 36 + l);
-      a -= w.x * x[l];
-      if (l + 1 < i) b -= w.y * x[l + 1];
-      if (l + 2 < i) c -= w.z * x[l + 2];
-      if (l + 3 < i) d -= w.w * x[l + 3];
+      x[2 * s + (i >> 1)][2 * (i & 1)] = f.x, x[2 * s + (i >> 1)][2 * (i & 1) + 1] = f.y;
     }
-    x[i] = (a + b) + (c + d);
-    if (i >= 16 || lane < 16) put_lower<N>(tile, i, lane, x[i]);
   }
+}
+
+__device__ __forceinline__ void copy_record(unsigned char* to, const unsigned char* from, int bytes, int lane) {
+  const uint32_t at = smem_of(to);
+#pragma unroll 4
+  for (int u = lane * 16; u < bytes; u += 512) copy_async(at + u, from + u, true);
+}
+
+// A record's floats of a lane's columns 8 n + 2 t and the next.
+__device__ __forceinline__ float2 pair_at(const unsigned char* record, int array, int n, int t) {
+  return *reinterpret_cast<const float2*>(record + array + (8 * n + 2 * t) * 4);
+}
+__device__ __forceinline__ float float_at(const unsigned char* record, int array, int i) {
+  return *reinterpret_cast<const float*>(record + array + i * 4);
+}
+// exp(G_i - G_j)
+__device__ __forceinline__ float between(const unsigned char* record, int i, int j) {
+  return expf((float_at(record, Record::g_hi, i) - float_at(record, Record::g_hi, j)) +
+              (float_at(record, Record::g_lo, i) - float_at(record, Record::g_lo, j)));
+}
+
+// Neighbours of a row of a tile, as N terms `plane` bytes apart.
+template <int N>
+__device__ __forceinline__ void put_pair(unsigned char* at, int plane, float x, float y) {
+  uint32_t t[N];
+  split<N>(x, y, t);
+#pragma unroll
+  for (int i = 0; i < N; ++i) *reinterpret_cast<uint32_t*>(at + i * plane) = t[i];
 }
 
 __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
@@ -403,6 +368,176 @@ __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
 }
 
 constexpr int log_of(int n) { return n <= 1 ? 0 : 1 + log_of(n / 2); }
+constexpr int kMostShared = 227 << 10;
+
+// ---------------------------------------------------------------------------
+// records
+// ---------------------------------------------------------------------------
+
+// A warp's shared memory: K and Q, then in their place the record, M diag(beta) of the two
+// diagonal blocks in floats, and a block in terms.
+template <class T, int DK>
+struct PrepareShared {
+  static constexpr int IT = Terms<T>::of(3), lp = log_of(DK / 8), plane = kChunk * DK * 2;
+  static constexpr int tiles = 2 * IT * plane, m = Record::bytes, block = m + 2 * 16 * 20 * 4,
+                       rest = block + 3 * 512, bytes = tiles > rest ? tiles : rest;
+};
+
+// A warp a chunk.  The inverse of I + N, N = M diag(beta) = [N11 0; N21 N22]: both
+// diagonal blocks by forward substitution (column j of them in lane j and 16 + j; not by
+// powers of N, which cancel where keys repeat), the block below them as -X22 N21 X11 on
+// the matrix units.
+template <class T, int DK>
+__global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const T> q, DView<const T> k, int backward) {
+  using Shared = PrepareShared<T, DK>;
+  constexpr int IT = Shared::IT, lp = Shared::lp, plane = Shared::plane;
+  extern __shared__ __align__(128) unsigned char held[];
+  const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
+  const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  if (job >= a.work.chunks) return;
+  const int64_t bh = job / a.chunks;
+  const int c = (int)(job - bh * a.chunks), b = (int)(bh / a.heads), h = (int)(bh % a.heads), hk = h / a.share;
+  const int len = length_of(a, b), t0 = c * kChunk, live = min(kChunk, len - t0), t = t0 + lane;
+  if (live <= 0) return;
+  unsigned char* mine = held + (threadIdx.x >> 5) * Shared::bytes;
+  float g = lane < live ? a.decay.data[b * a.decay.batch + t * a.decay.time + h * a.decay.head] : 0.f;
+  const float beta = lane < live ? a.beta.data[b * a.beta.batch + t * a.beta.time + h * a.beta.head] : 0.f;
+  load_terms<T, IT>(mine, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live, a.key_dim,
+                    a.wide_qk, lane);
+  load_terms<T, IT>(mine + IT * plane, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
+                    a.key_dim, a.wide_qk, lane);
+  copies_done();
+  __syncwarp();
+  // lower blocks of K K^T and Q K^T: rows 0 .. 15 by columns 0 .. 15 (two accumulators),
+  // rows 16 .. 31 by all (four)
+  float kk[6][4], qk[6][4];
+  zero(kk), zero(qk);
+  const uint32_t kt = smem_of(mine), qt = kt + IT * plane;
+#pragma unroll
+  for (int s = 0; s < DK / 16; ++s) {
+    uint32_t bk[2][IT][4];
+#pragma unroll
+    for (int p = 0; p < 2; ++p)
+#pragma unroll
+      for (int j = 0; j < IT; ++j) load_matrices<false>(bk[p][j], kt + j * plane + right_rows(lane, 16 * p, 16 * s, lp));
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int i = 0; i < IT; ++i) {
+        uint32_t x[4], y[4];
+        load_matrices<false>(x, kt + i * plane + left_rows(lane, 16 * m, 16 * s, lp));
+        load_matrices<false>(y, qt + i * plane + left_rows(lane, 16 * m, 16 * s, lp));
+#pragma unroll
+        for (int p = 0; p <= m; ++p)
+#pragma unroll
+          for (int j = 0; j < IT && i + j < 3; ++j)
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+              multiply(kk[2 * (m + p) + n], x, bk[p][j][2 * n], bk[p][j][2 * n + 1]);
+              multiply(qk[2 * (m + p) + n], y, bk[p][j][2 * n], bk[p][j][2 * n + 1]);
+            }
+      }
+  }
+  __syncwarp();
+  // the positions: a decay below -512 counts as -512 (exp is 0 long before), so that
+  // -infinity forgets and sums stay exact
+  g = g < -512.f ? -512.f : g;
+  float hi = rintf(g * 64.f) * 0.015625f, lo = g - hi;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const float x = __shfl_up_sync(kFull, hi, o), y = __shfl_up_sync(kFull, lo, o);
+    if (lane >= o) hi += x, lo += y;
+  }
+  const float end_hi = __shfl_sync(kFull, hi, 31), end_lo = __shfl_sync(kFull, lo, 31);
+  float* numbers = reinterpret_cast<float*>(mine);
+  numbers[Record::since / 4 + lane] = expf(hi) * expf(lo);
+  numbers[Record::until / 4 + lane] = expf((end_hi - hi) + (end_lo - lo));
+  numbers[Record::beta / 4 + lane] = beta;
+  numbers[Record::g_hi / 4 + lane] = hi;
+  numbers[Record::g_lo / 4 + lane] = lo;
+  __syncwarp();
+  float below[2][4];   // N21
+#pragma unroll
+  for (int u = 0; u < 6; ++u) {
+    const int blk = u >> 1, row0 = 16 * ((blk + 1) >> 1), col = 16 * (blk >> 1) + 8 * (u & 1) + 2 * t4;
+    const float2 bj = *reinterpret_cast<const float2*>(mine + Record::beta + col * 4);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int i = row0 + g4 + 8 * r;
+      const float d0 = i >= col ? between(mine, i, col) : 0.f, d1 = i > col ? between(mine, i, col + 1) : 0.f;
+      const uint32_t to = lower_at(i, col);
+      put_pair<3>(mine + Record::a + to, kLower, qk[u][2 * r] * d0 * a.scale, qk[u][2 * r + 1] * d1 * a.scale);
+      const float m0 = i > col ? kk[u][2 * r] * d0 : 0.f, m1 = i > col + 1 ? kk[u][2 * r + 1] * d1 : 0.f;
+      if (backward) put_pair<3>(mine + Record::m + to, kLower, m0, m1);
+      if (blk == 1) {
+        below[u & 1][2 * r] = m0 * bj.x, below[u & 1][2 * r + 1] = m1 * bj.y;
+      } else {
+        float* at = reinterpret_cast<float*>(mine + Shared::m) + ((blk >> 1) * 16 + (i & 15)) * 20 + (col & 15);
+        at[0] = m0 * bj.x, at[1] = m1 * bj.y;
+      }
+    }
+  }
+  __syncwarp();
+  {
+    const float* n = reinterpret_cast<const float*>(mine + Shared::m) + (lane >> 4) * 320;
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      float s[4] = {i == (lane & 15) ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int l = 0; l < i; l += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(n + i * 20 + l);
+        s[0] -= w.x * x[l];
+        if (l + 1 < i) s[1] -= w.y * x[l + 1];
+        if (l + 2 < i) s[2] -= w.z * x[l + 2];
+        if (l + 3 < i) s[3] -= w.w * x[l + 3];
+      }
+      x[i] = (s[0] + s[1]) + (s[2] + s[3]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      unsigned char* to = mine + Record::inverse + (lane >> 4) * 1024 + element_at(i, lane & 15, 1);
+      float y = x[i];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        const __nv_bfloat16 e = __float2bfloat16_rn(y);
+        *reinterpret_cast<__nv_bfloat16*>(to + j * kLower) = e;
+        y -= __bfloat162float(e);
+      }
+    }
+  }
+  __syncwarp();
+  const uint32_t inverse = smem_of(mine + Record::inverse), block = smem_of(mine + Shared::block);
+  float x[2][4];
+  zero(x);
+  product<1, 1, 3, 3, 3, true, 0>(
+      x, [&](int s, uint32_t (&y)[3][4]) { left_of<3>(below, s, y); },
+      [&](int, int, int j) { return inverse + j * kLower + right_cols(lane, 0, 0, 1); });
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      put_pair<3>(mine + Shared::block + element_at(g4 + 8 * r, 8 * n + 2 * t4, 1), 512, x[n][2 * r], x[n][2 * r + 1]);
+  __syncwarp();
+  zero(x);
+  product<1, 1, 3, 3, 3, true, 0>(
+      x,
+      [&](int, uint32_t (&y)[3][4]) {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) load_matrices<false>(y[i], inverse + i * kLower + 1024 + left_rows(lane, 0, 0, 1));
+      },
+      [&](int, int, int j) { return block + j * 512 + right_cols(lane, 0, 0, 1); });
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      put_pair<3>(mine + Record::inverse + 512 + element_at(g4 + 8 * r, 8 * n + 2 * t4, 1), kLower, -x[n][2 * r],
+                  -x[n][2 * r + 1]);
+  __syncwarp();
+  uint4* out = reinterpret_cast<uint4*>(a.work.record + job * Record::bytes);
+  const uint4* in = reinterpret_cast<const uint4*>(mine);
+  for (int u = lane; u < (backward ? Record::bytes : Record::forward_bytes) / 16; u += 32) out[u] = in[u];
+}
 
 // ---------------------------------------------------------------------------
 // forward, and the states' pass before a backward
@@ -412,69 +547,64 @@ constexpr int kForwardTerms = 3;
 template <class T>
 constexpr int kKept = sizeof(T) == 2 ? 2 : 3;   // terms of the states that are kept for a backward
 
-// Bytes of a stage.  STATES: the states' pass, which has grad_y in it.
-template <class T, int DK, bool STATES>
+enum DeltaMode {
+  kForward,   // y and the last state
+  kStates,    // what the reverse pass needs (DeltaWork)
+};
+
+template <class T, int DK, DeltaMode MODE>
 struct ForwardStage {
   static constexpr int NT = kForwardTerms, IT = Terms<T>::of(NT), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr int k = 0, q = k + IT * plane, inverse = q + IT * plane, a = inverse + NT * kLower,
-                       spots = a + NT * kLower, scratch = spots + kChunk * (int)sizeof(Spot),
-                       v = scratch + kChunk * 36 * 4;
-  // V and grad_y are fp32 rows of `dv` columns and four more, which keep the banks of a read apart
-  static constexpr int bytes(int dv) { return v + (STATES ? 2 : 1) * kChunk * (dv + 4) * 4; }
+  static constexpr int record = 0, k = 9856, q = k + IT * plane, v = q + IT * plane;
+  static_assert(Record::forward_bytes == k && k % 128 == 0, "");
+  // V (and grad_y) in terms, rows of dvp channels
+  static constexpr int bytes(int dvp) { return v + (MODE == kStates ? 2 : 1) * IT * kChunk * dvp * 2; }
+  // a warp's results on their way to rows: 16 bits swizzled, fp32 rows of 17
+  static constexpr int own = MODE == kStates ? 128 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
 };
 
 // Consumer warps first (one for 16 value channels), then the producers.
-template <class T, int DK, bool STATES>
+template <class T, int DK, DeltaMode MODE>
 __global__ void __launch_bounds__(384)
     k_delta_fwd(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> y,
                 int producers) {
-  using Stage = ForwardStage<T, DK, STATES>;
+  using Stage = ForwardStage<T, DK, MODE>;
   constexpr int NT = Stage::NT, IT = Stage::IT, lp = Stage::lp, plane = Stage::plane;
   // terms of what goes into y alone: 16 bits are stored of it, so two carry enough.  The
   // decays' gradients are sums of <grad_y, y> over many positions: all terms
-  constexpr int NO = !STATES && sizeof(T) == 2 ? 2 : NT;
+  constexpr int NO = MODE == kForward && sizeof(T) == 2 ? 2 : NT;
   extern __shared__ __align__(128) unsigned char held[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int consumers = (blockDim.x >> 5) - producers, meeting = 32 * (consumers + 1);
-  const int dv = 16 * consumers, size = Stage::bytes(dv);
+  const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
+  const int size = Stage::bytes(8 << lv);
   const int part = blockIdx.x % a.parts, bh = blockIdx.x / a.parts, b = bh / a.heads, h = bh % a.heads;
-  const int hk = h / a.share, first_v = part * dv;
+  const int hk = h / a.share, first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
+  const int64_t head = (int64_t)b * a.heads + h;
   if (warp >= consumers) {
-    const int p = warp - consumers;
+    const int p = warp - consumers, cols_v = min(16 * consumers, a.value_dim - first_v);
     unsigned char* st = held + p * size;
-    Spot* spots = reinterpret_cast<Spot*>(st + Stage::spots);
-    float* scratch = reinterpret_cast<float*>(st + Stage::scratch);
-    const int cols_v = min(dv, a.value_dim - first_v);
     for (int c = p; c < chunks; c += producers) {
       if (c >= producers) meet(1 + producers + p, meeting);
-      const int t0 = c * kChunk, live = min(kChunk, len - t0), t = t0 + lane;
-      const float g = lane < live ? a.decay.data[b * a.decay.batch + t * a.decay.time + h * a.decay.head] : 0.f;
-      const float beta = lane < live ? a.beta.data[b * a.beta.batch + t * a.beta.time + h * a.beta.head] : 0.f;
+      const int t0 = c * kChunk, live = min(kChunk, len - t0);
+      copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::forward_bytes, lane);
       load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
                         a.key_dim, a.wide_qk, lane);
       load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
                         a.key_dim, a.wide_qk, lane);
-      float* tile = reinterpret_cast<float*>(st + Stage::v);
-      for (int w = 0; w < (STATES ? 2 : 1); ++w) {
-        const DView<const T>& x = w ? gy : v;
-        load_floats<T>(tile + w * kChunk * (dv + 4), dv, x.data + b * x.batch + t0 * x.time + h * x.head + first_v,
-                       x.time, live, cols_v, a.wide_v, lane);
-      }
-      find_spots(spots, g, beta, lane);
-      __syncwarp();
-      find_lower<DK, IT>(smem_of(st + Stage::k), smem_of(st + Stage::k), plane, spots, lane,
-                         [&](int i, int j, float x) { scratch[i * 36 + j] = i > j ? x * spots[j].beta : 0.f; });
-      find_lower<DK, IT>(smem_of(st + Stage::q), smem_of(st + Stage::k), plane, spots, lane,
-                         [&](int i, int j, float x) { put_lower<NO>(st + Stage::a, i, j, x * a.scale); });
-      __syncwarp();
-      invert<NT>(scratch, st + Stage::inverse, lane);
+      load_terms<T, IT>(st + Stage::v, plane_v, lv, v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time,
+                        live, cols_v, a.wide_v, lane);
+      if constexpr (MODE == kStates)
+        load_terms<T, IT>(st + Stage::v + IT * plane_v, plane_v, lv,
+                          gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v, gy.time, live, cols_v,
+                          a.wide_v, lane);
+      copies_done();
       arrive(1 + p, meeting);
     }
     return;
   }
   const int g = lane >> 2, t = lane & 3, e0 = first_v + 16 * warp;
-  const int64_t head = (int64_t)b * a.heads + h;
   float S[DK / 8][4];   // S^T: channel e0 + g (+ 8), key columns 8 n + 2 t (+ 1)
 #pragma unroll
   for (int n = 0; n < DK / 8; ++n)
@@ -484,9 +614,9 @@ __global__ void __launch_bounds__(384)
       S[n][r] = a.state_in && d < a.key_dim && e < a.value_dim
                     ? a.state_in[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
     }
-  const int64_t warps = (int64_t)consumers * a.parts;
+  const int64_t warps = (int64_t)consumers * a.parts, mine = part * consumers + warp;
   const auto keep = [&](int c) {   // the state before chunk c, for the reverse pass
-    const int64_t at = ((head * (a.chunks + 1) + c) * warps + part * consumers + warp) * (DK / 16) * 32 + lane;
+    const int64_t at = ((head * (a.chunks + 1) + c) * warps + mine) * (DK / 16) * 32 + lane;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
       uint32_t x[kKept<T>][4];
@@ -495,106 +625,143 @@ __global__ void __launch_bounds__(384)
       for (int j = 0; j < kKept<T>; ++j) a.work.s[j][at + s * 32] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
     }
   };
-  float* own = reinterpret_cast<float*>(held + producers * size) + warp * kChunk * 17;   // a warp's results, turned
+  unsigned char* own = held + producers * size + warp * Stage::own;
   int stage = 0;
   for (int c = 0; c < chunks; ++c) {
     unsigned char* st = held + stage * size;
     const uint32_t base = smem_of(st);
-    const Spot* spots = reinterpret_cast<const Spot*>(st + Stage::spots);
-    const float* vt = reinterpret_cast<const float*>(st + Stage::v) + 16 * warp;
-    if constexpr (STATES) keep(c);
+    if constexpr (MODE == kStates) keep(c);
     meet(1 + stage, meeting);
     const int t0 = c * kChunk, live = min(kChunk, len - t0);
+    // K S0 and Q S0
+    float Z[4][4], E[4][4], Y[4][4];
+    zero(Z), zero(Y);
+#pragma unroll
+    for (int s = 0; s < DK / 16; ++s) {
+      uint32_t x[NT][4];
+      left_of<NT>(S, s, x);
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int j = 0; j < IT; ++j) {
+          uint32_t u[4], w[4];
+          const uint32_t at = base + j * plane + right_rows(lane, 16 * p, 16 * s, lp);
+          load_matrices<false>(u, at + Stage::k);
+          load_matrices<false>(w, at + Stage::q);
+#pragma unroll
+          for (int i = 0; i < NT; ++i) {
+            if (i + j < NT) multiply(Z[2 * p], x[i], u[0], u[1]), multiply(Z[2 * p + 1], x[i], u[2], u[3]);
+            if (i + j < NO) multiply(Y[2 * p], x[i], w[0], w[1]), multiply(Y[2 * p + 1], x[i], w[2], w[3]);
+          }
+        }
+    }
     // Z = V - exp(G) K S0
-    float Z[4][4], E[4][4];
-    zero(Z);
-    product<DK / 16, 2, NT, IT, NT, false, 0>(
-        Z, [&](int s, uint32_t (&x)[NT][4]) { left_of<NT>(S, s, x); },
-        [&](int p, int s, int j) { return base + Stage::k + j * plane + right_rows(lane, 16 * p, 16 * s, lp); });
+    load_turned<IT>(E, base + Stage::v, plane_v, 16 * warp, lv, lane);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 8 * n + 2 * t + (r & 1);
-        Z[n][r] = vt[i * (dv + 4) + g + (r >> 1) * 8] - spots[i].since * Z[n][r];
-      }
+    for (int n = 0; n < 4; ++n) {
+      const float2 f = pair_at(st, Record::since, n, t);
+      Z[n][0] = E[n][0] - f.x * Z[n][0], Z[n][1] = E[n][1] - f.y * Z[n][1];
+      Z[n][2] = E[n][2] - f.x * Z[n][2], Z[n][3] = E[n][3] - f.y * Z[n][3];
+      Y[n][0] *= f.x * a.scale, Y[n][1] *= f.y * a.scale, Y[n][2] *= f.x * a.scale, Y[n][3] *= f.y * a.scale;
+    }
+    const auto lower = [&](int tile, int p, int s, int j) {
+      return base + tile + j * kLower + (p + s) * 512 + right_rows(lane, 0, 0, 1);
+    };
     zero(E);
     product<2, 2, NT, NT, NT, false, 1>(
         E, [&](int s, uint32_t (&x)[NT][4]) { left_of<NT>(Z, s, x); },
-        [&](int p, int s, int j) {
-          return base + Stage::inverse + j * kLower + (p + s) * 512 + right_rows(lane, 0, 0, 1);
-        });
-    {
-      float Y[4][4], U[4][4];
-      zero(Y);
-      product<DK / 16, 2, NO, IT, NO, false, 0>(
-          Y, [&](int s, uint32_t (&x)[NO][4]) { left_of<NO>(S, s, x); },
-          [&](int p, int s, int j) { return base + Stage::q + j * plane + right_rows(lane, 16 * p, 16 * s, lp); });
+        [&](int p, int s, int j) { return lower(Record::inverse, p, s, j); });
+    if constexpr (MODE == kStates) {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+        a.work.e[(((head * a.chunks + c) * warps + mine) * 4 + n) * 32 + lane] =
+            make_float4(E[n][0], E[n][1], E[n][2], E[n][3]);
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {   // U
+      const float2 f = pair_at(st, Record::beta, n, t);
+      E[n][0] *= f.x, E[n][1] *= f.y, E[n][2] *= f.x, E[n][3] *= f.y;
+    }
+    product<2, 2, NO, NO, NO, false, 1>(
+        Y, [&](int s, uint32_t (&x)[NO][4]) { left_of<NO>(E, s, x); },
+        [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
+    if constexpr (MODE == kStates) {
+      // <grad_y, y> over the warp's channels
+      float* sums = reinterpret_cast<float*>(own);
+      load_turned<IT>(Z, base + Stage::v + IT * plane_v, plane_v, 16 * warp, lv, lane);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const Spot& s = spots[8 * n + 2 * t + (r & 1)];
-          Y[n][r] *= a.scale * s.since;
-          U[n][r] = s.beta * E[n][r];
+        for (int r = 0; r < 2; ++r) {
+          float x = Y[n][r] * Z[n][r] + Y[n][2 + r] * Z[n][2 + r];
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
+          if (g == 0) sums[8 * n + 2 * t + r] = x;
         }
-      product<2, 2, NO, NO, NO, false, 1>(
-          Y, [&](int s, uint32_t (&x)[NO][4]) { left_of<NO>(U, s, x); },
-          [&](int p, int s, int j) { return base + Stage::a + j * kLower + (p + s) * 512 + right_rows(lane, 0, 0, 1); });
-      if constexpr (STATES) {
-        // <grad_y, y> over the warp's channels; E for the reverse pass
-        const float* gt = vt + kChunk * (dv + 4);
+      __syncwarp();
+      a.work.dots[(mine * a.work.chunks + head * a.chunks + c) * kChunk + lane] = sums[lane];
+      __syncwarp();
+    } else {
+      const bool there = t0 + lane < a.len, on = lane < live;   // dead positions of the chunk too: 0
+      T* to = y.data + b * y.batch + (int64_t)(t0 + lane) * y.time + h * y.head + e0;
+      if constexpr (sizeof(T) == 2) {
+        const auto both = [](float lo, float hi) {
+          Vec<T, 2> o;
+          narrow2(o.e, make_float2(lo, hi));
+          return *reinterpret_cast<const uint32_t*>(&o);
+        };
 #pragma unroll
-        for (int n = 0; n < 4; ++n) {
+        for (int s = 0; s < 2; ++s)
+          store_matrices(smem_of(own) + left_cols(lane, 0, 16 * s, 1), both(Y[2 * s][0], Y[2 * s][1]),
+                         both(Y[2 * s][2], Y[2 * s][3]), both(Y[2 * s + 1][0], Y[2 * s + 1][1]),
+                         both(Y[2 * s + 1][2], Y[2 * s + 1][3]));
+        __syncwarp();
+        if (there) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int i = 8 * n + 2 * t + r;
-            float x = Y[n][r] * gt[i * (dv + 4) + g] + Y[n][2 + r] * gt[i * (dv + 4) + g + 8];
+          for (int u = 0; u < 2; ++u) {
+            Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(own + piece(lane, u, 1)));
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
-            if (g == 0) own[i] = x;
+            for (int i = 0; i < 8; ++i) o.e[i] = on ? o.e[i] : from_f32<T>(0.f);
+            if (a.wide_y && e0 + 8 * u + 8 <= a.value_dim) {
+              store_vec(to + 8 * u, o);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (e0 + 8 * u + i < a.value_dim) to[8 * u + i] = o.e[i];
+            }
           }
-          a.work.e[(((head * a.chunks + c) * warps + part * consumers + warp) * 4 + n) * 32 + lane] =
-              make_float4(E[n][0], E[n][1], E[n][2], E[n][3]);
         }
-        __syncwarp();
-        a.work.dots[((part * consumers + warp) * a.work.chunks + head * a.chunks + c) * kChunk + lane] = own[lane];
-        __syncwarp();
       } else {
+        float* turned = reinterpret_cast<float*>(own);
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
-          for (int r = 0; r < 4; ++r) own[(8 * n + 2 * t + (r & 1)) * 17 + g + (r >> 1) * 8] = Y[n][r];
+          for (int r = 0; r < 4; ++r) turned[(8 * n + 2 * t + (r & 1)) * 17 + g + (r >> 1) * 8] = Y[n][r];
         __syncwarp();
-        if (t0 + lane < a.len) {   // dead positions of the chunk too: 0
-          T* to = y.data + b * y.batch + (int64_t)(t0 + lane) * y.time + h * y.head + e0;
-          const float* from = own + lane * 17;
-          const bool on = lane < live;
+        if (there) {
+          const float* from = turned + lane * 17;
           if (a.wide_y && e0 + 16 <= a.value_dim) {
-            constexpr int V = 16 / sizeof(T);
 #pragma unroll
-            for (int i = 0; i < 16; i += V) {
-              Vec<T, V> o;
+            for (int i = 0; i < 16; i += 4) {
+              Vec<T, 4> o;
 #pragma unroll
-              for (int u = 0; u < V; ++u) o.e[u] = from_f32<T>(on ? from[i + u] : 0.f);
+              for (int u = 0; u < 4; ++u) o.e[u] = on ? from[i + u] : 0.f;
               store_vec(to + i, o);
             }
           } else {
-            for (int i = 0; i < 16 && e0 + i < a.value_dim; ++i) to[i] = from_f32<T>(on ? from[i] : 0.f);
+            for (int i = 0; i < 16 && e0 + i < a.value_dim; ++i) to[i] = on ? from[i] : 0.f;
           }
         }
-        __syncwarp();
       }
+      __syncwarp();
     }
-    // S1 = exp(G_31) S0 + K^T (exp(G_31 - G) beta E)
-    const float whole = spots[kChunk - 1].since;
+    // S1 = exp(G_31) S0 + K^T (exp(G_31 - G) U)
+    const float whole = float_at(st, Record::since, kChunk - 1);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const Spot& s = spots[8 * n + 2 * t + (r & 1)];
-        E[n][r] *= s.until * s.beta;
-      }
+    for (int n = 0; n < 4; ++n) {
+      const float2 f = pair_at(st, Record::until, n, t);
+      E[n][0] *= f.x, E[n][1] *= f.y, E[n][2] *= f.x, E[n][3] *= f.y;
+    }
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
@@ -605,8 +772,8 @@ __global__ void __launch_bounds__(384)
     if (c + producers < chunks) arrive(1 + producers + stage, meeting);
     stage = stage + 1 == producers ? 0 : stage + 1;
   }
-  if constexpr (STATES) keep(chunks);
-  if constexpr (!STATES) {
+  if constexpr (MODE == kStates) keep(chunks);
+  if constexpr (MODE == kForward) {
     if (a.state_out)
 #pragma unroll
       for (int n = 0; n < DK / 8; ++n)
@@ -645,12 +812,11 @@ template <class T, int DK>
 struct ReverseStage {
   static constexpr int NR = ReverseTerms<T, DK>::R;
   static constexpr int IT = Terms<T>::of(NR), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr int k = 0, q = k + IT * plane, inverse = q + IT * plane, a = inverse + NR * kLower,
-                       m = a + NR * kLower, spots = m + NR * kLower, gy = spots + kChunk * (int)sizeof(Spot);
-  // before grad_y is there, its place holds the matrix that is inverted
-  static constexpr int bytes(int dvp) {
-    return gy + (IT * kChunk * dvp * 2 > kChunk * 36 * 4 ? IT * kChunk * dvp * 2 : kChunk * 36 * 4);
-  }
+  static constexpr bool v_too = std::is_same_v<T, __nv_bfloat16>;   // others leave no room for V
+  // of the record: numbers, then NR terms of each matrix
+  static constexpr int inverse = Record::inverse, a = inverse + NR * kLower, m = a + NR * kLower, k = m + NR * kLower,
+                       q = k + IT * plane, gy = q + IT * plane;
+  static constexpr int bytes(int dvp) { return gy + (v_too ? 2 : 1) * IT * kChunk * dvp * 2; }
 };
 // What the consumers share: dS and S [channels][DK], U and dZ [32][channels], dA and X +
 // X^T [32][32], sums.
@@ -700,41 +866,36 @@ __global__ void __launch_bounds__(320)
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
   const Shared at(W, dvp);
   unsigned char* shared = held + producers * size;
+  const int64_t head = (int64_t)b * a.heads + h;
   if (warp >= W) {
     const int p = warp - W;
     unsigned char* st = held + p * size;
-    Spot* spots = reinterpret_cast<Spot*>(st + Stage::spots);
-    float* scratch = reinterpret_cast<float*>(st + Stage::gy);
     for (int n = p; n < chunks; n += producers) {
       if (n >= producers) meet(1 + producers + p, meeting);
-      const int t0 = (chunks - 1 - n) * kChunk, live = min(kChunk, len - t0), t = t0 + lane;
-      const float g = lane < live ? a.decay.data[b * a.decay.batch + t * a.decay.time + h * a.decay.head] : 0.f;
-      const float beta = lane < live ? a.beta.data[b * a.beta.batch + t * a.beta.time + h * a.beta.head] : 0.f;
+      const int c = chunks - 1 - n, t0 = c * kChunk, live = min(kChunk, len - t0);
+      const unsigned char* record = a.work.record + (head * a.chunks + c) * Record::bytes;
+      if constexpr (NR == 3) {
+        copy_record(st, record, Record::bytes, lane);
+      } else {
+        copy_record(st, record, Record::inverse + NR * kLower, lane);
+        copy_record(st + Stage::a, record + Record::a, NR * kLower, lane);
+        copy_record(st + Stage::m, record + Record::m, NR * kLower, lane);
+      }
       load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
                         a.key_dim, a.wide_qk, lane);
       load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
                         a.key_dim, a.wide_qk, lane);
-      find_spots(spots, g, beta, lane);
-      __syncwarp();
-      find_lower<DK, IT>(smem_of(st + Stage::k), smem_of(st + Stage::k), plane, spots, lane,
-                         [&](int i, int j, float x) {
-                           x = i > j ? x : 0.f;
-                           scratch[i * 36 + j] = x * spots[j].beta;
-                           put_lower<NR>(st + Stage::m, i, j, x);
-                         });
-      find_lower<DK, IT>(smem_of(st + Stage::q), smem_of(st + Stage::k), plane, spots, lane,
-                         [&](int i, int j, float x) { put_lower<NR>(st + Stage::a, i, j, x * a.scale); });
-      __syncwarp();
-      invert<NR>(scratch, st + Stage::inverse, lane);
-      __syncwarp();
       load_terms<T, IT>(st + Stage::gy, plane_v, lv, gy.data + b * gy.batch + t0 * gy.time + h * gy.head, gy.time, live,
                         a.value_dim, a.wide_v, lane);
+      if constexpr (Stage::v_too)
+        load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
+                          v.data + b * v.batch + t0 * v.time + h * v.head, v.time, live, a.value_dim, a.wide_v, lane);
+      copies_done();
       arrive(1 + p, meeting);
     }
     return;
   }
   const int g = lane >> 2, t = lane & 3, e0 = 16 * warp;
-  const int64_t head = (int64_t)b * a.heads + h;
   float dS[DK / 8][4];
 #pragma unroll
   for (int n = 0; n < DK / 8; ++n)
@@ -779,7 +940,6 @@ __global__ void __launch_bounds__(320)
     const int c = chunks - 1 - n0, t0 = c * kChunk, live = min(kChunk, len - t0);
     unsigned char* st = held + stage * size;
     const uint32_t base = smem_of(st);
-    const Spot* spots = reinterpret_cast<const Spot*>(st + Stage::spots);
     // what the states' pass left, and V where this lane's dV will be
     uint4 s0[DK / 16];
     const int64_t from = state_at(c);
@@ -790,12 +950,13 @@ __global__ void __launch_bounds__(320)
     for (int n = 0; n < 4; ++n) {
       const float4 x = a.work.e[(((head * a.chunks + c) * W + warp) * 4 + n) * 32 + lane];
       E[n][0] = x.x, E[n][1] = x.y, E[n][2] = x.z, E[n][3] = x.w;
+      if constexpr (!Stage::v_too)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-        V[n][r] = i < live && e < a.value_dim
-                      ? to_f32(v.data[b * v.batch + (int64_t)(t0 + i) * v.time + h * v.head + e]) : 0.f;
-      }
+        for (int r = 0; r < 4; ++r) {
+          const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
+          V[n][r] = i < live && e < a.value_dim
+                        ? to_f32(v.data[b * v.batch + (int64_t)(t0 + i) * v.time + h * v.head + e]) : 0.f;
+        }
     }
     float dots = 0.f;
     if (warp == 0)
@@ -825,10 +986,14 @@ __global__ void __launch_bounds__(320)
     product<DK / 16, 2, NR, IT, NR, false, 0>(
         dU, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dS, s, x); },
         [&](int p, int s, int j) { return base + Stage::k + j * plane + right_rows(lane, 16 * p, 16 * s, lp); });
+    const auto columns = [&](float (&x)[4][4], const float (&y)[4][4], int array) {   // x = y times a number a column
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dU[n][r] *= spots[8 * n + 2 * t + (r & 1)].until;
+      for (int n = 0; n < 4; ++n) {
+        const float2 f = pair_at(st, array, n, t);
+        x[n][0] = y[n][0] * f.x, x[n][1] = y[n][1] * f.y, x[n][2] = y[n][2] * f.x, x[n][3] = y[n][3] * f.y;
+      }
+    };
+    columns(dU, dU, Record::until);
     const auto lower = [&](int tile, int p, int s, int j) {
       return base + tile + j * kLower + (p + s) * 512 + right_cols(lane, 0, 0, 1);
     };
@@ -843,16 +1008,14 @@ __global__ void __launch_bounds__(320)
     zero(dZ);
     {
       float dE[4][4];
-#pragma unroll
-      for (int n = 0; n < 4; ++n)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) dE[n][r] = spots[8 * n + 2 * t + (r & 1)].beta * dU[n][r];
+      columns(dE, dU, Record::beta);
       product<2, 2, NR, NR, NR, true, 2>(
           dZ, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dE, s, x); },
           [&](int p, int s, int j) { return lower(Stage::inverse, p, s, j); });
     }
     {
       float R[4][4];
+      if constexpr (Stage::v_too) load_turned<IT>(V, base + Stage::gy + IT * plane_v, plane_v, e0, lv, lane);
       zero(R);
       product<2, 2, NR, NR, NR, true, 2>(
           R, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
@@ -874,26 +1037,52 @@ __global__ void __launch_bounds__(320)
           }
         }
     }
-    // U and dZ for the other warps; dV
+    // U and dZ for the other warps
+    columns(E, E, Record::beta);
 #pragma unroll
-    for (int n = 0; n < 4; ++n)
+    for (int s = 0; s < 2; ++s) {
+      uint32_t u[NU][4], z[NU][4];
+      left_of<NU>(E, s, u);
+      left_of<NU>(dZ, s, z);
+      const uint32_t to = sh + left_cols(lane, e0, 16 * s, lv);
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-        const uint32_t to = element_at(i, e, lv);
-        float u = spots[i].beta * E[n][r], z = dZ[n][r];
-        if (t0 + i < a.len && e < a.value_dim)
-          gv.data[b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head + e] = from_f32<T>(i < live ? z : 0.f);
+      for (int j = 0; j < NU; ++j) {
+        store_matrices(to + at.u + j * plane_v, u[j][0], u[j][1], u[j][2], u[j][3]);
+        store_matrices(to + at.dz + j * plane_v, z[j][0], z[j][1], z[j][2], z[j][3]);
+      }
+    }
+    // dV: a bf16 one is the first term as it lies there
+    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+      __syncwarp();
+      if (t0 + lane < a.len) {
+        T* to = gv.data + b * gv.batch + (int64_t)(t0 + lane) * gv.time + h * gv.head + e0;
 #pragma unroll
-        for (int j = 0; j < NU; ++j) {
-          const __nv_bfloat16 uh = __float2bfloat16_rn(u), zh = __float2bfloat16_rn(z);
-          *reinterpret_cast<__nv_bfloat16*>(shared + at.u + j * plane_v + to) = uh;
-          *reinterpret_cast<__nv_bfloat16*>(shared + at.dz + j * plane_v + to) = zh;
-          u -= __bfloat162float(uh), z -= __bfloat162float(zh);
+        for (int u = 0; u < 2; ++u) {
+          Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(shared + at.dz + piece(lane, e0 / 8 + u, lv)));
+#pragma unroll
+          for (int i = 0; i < 8; ++i) o.e[i] = lane < live ? o.e[i] : from_f32<T>(0.f);
+          if (a.wide_y && e0 + 8 * u + 8 <= a.value_dim) {
+            store_vec(to + 8 * u, o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (e0 + 8 * u + i < a.value_dim) to[8 * u + i] = o.e[i];
+          }
         }
       }
+    } else {
+#pragma unroll
+      for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
+          if (t0 + i < a.len && e < a.value_dim)
+            gv.data[b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head + e] =
+                from_f32<T>(i < live ? dZ[n][r] : 0.f);
+        }
+    }
     // the gradient of the state before the chunk
-    const float whole = spots[kChunk - 1].since;
+    const float whole = float_at(st, Record::since, kChunk - 1);
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
@@ -907,7 +1096,7 @@ __global__ void __launch_bounds__(320)
             load_matrices<true>(y[i], base + Stage::gy + i * plane_v + left_cols(lane, e0, 16 * s, lv));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int at_i = 16 * s + 8 * (i >> 1) + 2 * t;
+            const float2 since = pair_at(st, Record::since, 2 * s + (i >> 1), t);
             float2 f = unpack(y[IT - 1][i]);
 #pragma unroll
             for (int j = IT - 2; j >= 0; --j) {
@@ -915,16 +1104,17 @@ __global__ void __launch_bounds__(320)
               f.x += l.x, f.y += l.y;
             }
             uint32_t w[NR];
-            split<NR>(f.x * (a.scale * spots[at_i].since), f.y * (a.scale * spots[at_i + 1].since), w);
+            split<NR>(f.x * (a.scale * since.x), f.y * (a.scale * since.y), w);
 #pragma unroll
             for (int j = 0; j < NR; ++j) x[j][i] = w[j];
           }
         },
         [&](int p, int s, int j) { return base + Stage::q + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
+    columns(dZ, dZ, Record::since);
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) dZ[n][r] *= -spots[8 * n + 2 * t + (r & 1)].since;
+      for (int r = 0; r < 4; ++r) dZ[n][r] = -dZ[n][r];
     product<2, DK / 16, NR, IT, NR, true, 0>(
         dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
         [&](int p, int s, int j) { return base + Stage::k + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
@@ -981,7 +1171,7 @@ __global__ void __launch_bounds__(320)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * mi + g + (r >> 1) * 8, j = 16 * pj + 8 * n + 2 * t + (r & 1);
-          float x = i >= j ? acc[n][r] * between(spots[i], spots[j]) : 0.f;
+          float x = i >= j ? acc[n][r] * between(st, i, j) : 0.f;
           x = is_x ? (i > j ? -x : 0.f) : a.scale * x;
           unsigned char* tile = shared + (is_x ? at.xs : at.da);
 #pragma unroll
@@ -1039,11 +1229,12 @@ __global__ void __launch_bounds__(320)
         for (int m = 0; m < 2; ++m)
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
-            const Spot& s = spots[16 * m + g + (r >> 1) * 8];
+            const int i = 16 * m + g + (r >> 1) * 8;
+            const float since = float_at(st, Record::since, i), until = float_at(st, Record::until, i);
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
-              aq[m][n][r] *= a.scale * s.since;
-              ak[m][n][r] = s.until * ak[m][n][r] - s.since * az[m][n][r];
+              aq[m][n][r] *= a.scale * since;
+              ak[m][n][r] = until * ak[m][n][r] - since * az[m][n][r];
             }
           }
       }
@@ -1174,25 +1365,39 @@ DView<T> dview(const delta_view* v) {
   return v ? DView<T>{(T*)v->data, v->batch_stride, v->time_stride, v->head_stride} : DView<T>{nullptr, 0, 0, 0};
 }
 
-constexpr int kMostShared = 227 << 10;
+template <class T, int DK>
+cudaError_t launch_delta_prepare(const DeltaArgs& a, const DeltaViews& w, bool backward, cudaStream_t stream) {
+  if (a.work.chunks == 0) return cudaSuccess;
+  const int most = kMostShared / PrepareShared<T, DK>::bytes, warps = most < 4 ? most : 4;
+  const int smem = warps * PrepareShared<T, DK>::bytes;
+  const auto kernel = k_delta_prepare<T, DK>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)((a.work.chunks + warps - 1) / warps), 32 * warps, smem, stream>>>(
+      a, dview<const T>(w.q), dview<const T>(w.k), backward);
+  return cudaGetLastError();
+}
 
-template <class T, bool STATES, int DK>
+template <class T, int DK, DeltaMode MODE>
 cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
-  using Stage = ForwardStage<T, DK, STATES>;
+  using Stage = ForwardStage<T, DK, MODE>;
+  cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
+  if (e != cudaSuccess) return e;
   const int W = (a.value_dim + 15) / 16;
   const int64_t heads = (int64_t)a.batch * a.heads;
-  // value channels over several CTAs where there are too few sequences for the SMs: each
-  // finds the chunks' inverses for itself
+  // value channels over several CTAs where there are too few sequences for the SMs
   a.parts = 1;
   for (int d = 2; d <= W && heads * a.parts < h->sm_count; ++d)
     if (W % d == 0) a.parts = d;
-  const int consumers = W / a.parts, own = consumers * kChunk * 17 * 4;
+  const int consumers = W / a.parts, own = consumers * Stage::own;
+  int dvp = 16;
+  while (dvp < 16 * consumers) dvp *= 2;
   const int64_t ctas = heads * a.parts;
   int producers = ctas > h->sm_count ? 2 : 4;
-  while (producers > 1 && producers * Stage::bytes(16 * consumers) + own > kMostShared) --producers;
-  const int smem = producers * Stage::bytes(16 * consumers) + own;
-  const auto kernel = k_delta_fwd<T, DK, STATES>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  while (producers > 1 && producers * Stage::bytes(dvp) + own > kMostShared) --producers;
+  const int smem = producers * Stage::bytes(dvp) + own;
+  const auto kernel = k_delta_fwd<T, DK, MODE>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   kernel<<<(unsigned)ctas, 32 * (consumers + producers), smem, stream>>>(
       a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.y), producers);
@@ -1201,7 +1406,7 @@ cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews
 
 template <class T, int DK>
 cudaError_t launch_delta_bwd(const emb_delta_s* h, const DeltaArgs& a, const DeltaViews& w, cudaStream_t stream) {
-  cudaError_t e = launch_delta_fwd<T, true, DK>(h, a, w, stream);
+  cudaError_t e = launch_delta_fwd<T, DK, kStates>(h, a, w, stream);
   if (e != cudaSuccess) return e;
   const int W = (a.value_dim + 15) / 16;
   int dvp = 16;
@@ -1228,7 +1433,7 @@ template <class T>
 cudaError_t launch_delta(const emb_delta_s* h, const DeltaArgs& a, const DeltaViews& w, bool backward, cudaStream_t s) {
   const auto of = [&](auto dk) {
     constexpr int DK = decltype(dk)::value;
-    return backward ? launch_delta_bwd<T, DK>(h, a, w, s) : launch_delta_fwd<T, false, DK>(h, a, w, s);
+    return backward ? launch_delta_bwd<T, DK>(h, a, w, s) : launch_delta_fwd<T, DK, kForward>(h, a, w, s);
   };
   if (a.key_dim <= 32) return of(std::integral_constant<int, 32>());
   if (a.key_dim <= 64) return of(std::integral_constant<int, 64>());
