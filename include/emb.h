@@ -714,11 +714,11 @@ typedef struct {
  * those of q and k (head h reads key head h / (heads / key_heads)); at most max_batch
  * entries of at most max_len positions, max_batch * heads < 2^27.
  * The handle holds 14464 bytes for each head of each entry and each 32 positions, of
- * which there may be 2^36 (237 MB for 32 x 2048 positions of 8 heads).
- * training != 0: it can run the backward, for which it holds as often the state before
- * them (6 bytes a number, key_dim rounded up to 32, 64 or 128 and value_dim to a multiple
- * of 16) and 136 bytes a value channel; where value heads share a key head, 8 bytes a
- * position, head and key channel more.  Calls on one handle must be ordered.  *out is NULL on error. */
+ * which there may be 2^30 (237 MB for 32 x 2048 positions of 8 heads).  training != 0: it
+ * can run the backward, for which it holds as often the state before them and its
+ * gradient after them (12 bytes a number, key_dim rounded up to 32, 64 or 128 and
+ * value_dim to a multiple of 16) and 280 bytes a value channel: 3.9 GB more for those of
+ * 128 x 128.  Calls on one handle must be ordered.  *out is NULL on error. */
 emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t heads, int32_t key_heads, int32_t max_batch,
                         int32_t max_len, int32_t training, emb_delta* out);
 
@@ -746,9 +746,8 @@ emb_status delta_forward(emb_delta h, int32_t batch, int32_t len, int32_t dtype,
  * its inputs and the gradients of y and state_out (NULL = 0).  q and k that several value
  * heads share get the sum over them.  Positions past an entry's end read nothing and get
  * gradient 0.  grad_state_in NULL = not wanted.  A training handle's;
- * EMB_ERR_UNSUPPORTED on another.  fp32 operands are in three bf16 terms, of fp16 and
- * fp32 calls with key_dim > 64 in two (each off by 2^-17 of itself at most); for the
- * gradients of q and k of bf16 calls the states are rounded to bf16. */
+ * EMB_ERR_UNSUPPORTED on another.  fp32 operands are in three bf16 terms; in the products
+ * that give 16-bit gradients of q and k in two, the states for bf16 in one. */
 emb_status delta_backward(emb_delta h, int32_t batch, int32_t len, int32_t dtype, const delta_view* q,
                           const delta_view* k, const delta_view* v, const delta_view* decay, const delta_view* beta,
                           const int32_t* offsets, double scale, const float* state_in, const delta_view* grad_y,

@@ -144,10 +144,12 @@ DeltaArgs delta_args(emb_delta h, int32_t batch, int32_t len, const int32_t* off
   a.key_dim = h->key_dim, a.value_dim = h->value_dim;
   a.chunks = (len + kChunk - 1) / kChunk;
   a.parts = 1;
+  a.warps = (h->value_dim + 15) / 16;
   a.scale = (float)scale;
   a.offsets = offsets;
   a.state_in = state_in;
-  a.work = {h->record, {h->s[0], h->s[1], h->s[2]}, h->e, h->dots, h->shared, (int64_t)batch * h->heads * a.chunks};
+  a.work = {h->record, {h->s[0], h->s[1], h->s[2]}, {h->ds[0], h->ds[1], h->ds[2]}, h->e, h->dz, h->sums, h->along,
+            (int64_t)batch * h->heads * a.chunks};
   return a;
 }
 
@@ -160,9 +162,11 @@ cudaError_t run(emb_delta h, const DeltaArgs& a, const DeltaViews& w, int32_t dt
 void delta_free(emb_delta h) {
   dev_free(h->record);
   for (uint4* p : h->s) dev_free(p);
+  for (uint4* p : h->ds) dev_free(p);
   dev_free(h->e);
-  dev_free(h->dots);
-  dev_free(h->shared);
+  dev_free(h->dz);
+  dev_free(h->sums);
+  dev_free(h->along);
   delete h;
 }
 
@@ -180,7 +184,7 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
     return EMB_ERR_INVALID_ARG;
   if (key_dim > 128 || value_dim > 128 || heads > 65536 || max_len > (1 << 30) ||
       (int64_t)max_batch * heads >= (int64_t(1) << 27) ||
-      (int64_t)max_batch * heads * (max_len / kChunk + 1) >= (int64_t(1) << 36))
+      (int64_t)max_batch * heads * (max_len / kChunk + 1) >= (int64_t(1) << 30))
     return EMB_ERR_UNSUPPORTED;
   emb_delta_s* h = new (std::nothrow) emb_delta_s();
   if (!h) return EMB_ERR_OOM;
@@ -192,12 +196,15 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
   if (e == cudaSuccess) e = dev_alloc((void**)&h->record, all * chunks * Record::bytes);
   if (training) {
     const int64_t W = (value_dim + 15) / 16, dk = dk_of(key_dim);
+    const int64_t state = W * (dk / 16) * 32 * sizeof(uint4), each = W * 4 * 32 * sizeof(float4);
     for (uint4*& p : h->s)
-      if (e == cudaSuccess) e = dev_alloc((void**)&p, all * (chunks + 1) * W * (dk / 16) * 32 * sizeof(uint4));
-    if (e == cudaSuccess) e = dev_alloc((void**)&h->e, all * chunks * W * 4 * 32 * sizeof(float4));
-    if (e == cudaSuccess) e = dev_alloc((void**)&h->dots, W * all * chunks * kChunk * sizeof(float));
-    if (e == cudaSuccess && heads > key_heads)
-      e = dev_alloc((void**)&h->shared, 2 * all * max_len * dk * sizeof(float));
+      if (e == cudaSuccess) e = dev_alloc((void**)&p, all * (chunks + 1) * state);
+    for (uint4*& p : h->ds)
+      if (e == cudaSuccess) e = dev_alloc((void**)&p, all * chunks * state);
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->e, all * chunks * each);
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->dz, all * chunks * each);
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->sums, 3 * W * all * chunks * kChunk * sizeof(float));
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->along, W * all * (chunks + 1) * sizeof(float));
   }
   if (e != cudaSuccess) {
     delta_free(h);

@@ -39,10 +39,9 @@ struct emb_delta_s {
   int sm_count = 0, device = 0;
   unsigned char* record = nullptr;   // see DeltaWork
   // for the backward
-  uint4* s[3] = {nullptr, nullptr, nullptr};
-  float4* e = nullptr;
-  float* dots = nullptr;
-  float* shared = nullptr;
+  uint4 *s[3] = {nullptr, nullptr, nullptr}, *ds[3] = {nullptr, nullptr, nullptr};
+  float4 *e = nullptr, *dz = nullptr;
+  float *sums = nullptr, *along = nullptr;
 };
 
 namespace emb {
@@ -56,22 +55,26 @@ struct DView {
   int64_t batch, time, head;
 };
 
-// A chunk's record, and what the states' pass leaves for the reverse pass, chunk after
-// chunk of each (entry, head), the states in the order of the lanes' registers.
+// What the passes leave for each other, chunk after chunk of each (entry, head): a
+// chunk's record, and for the backward states and intermediates in the order of the
+// lanes' registers.
 struct DeltaWork {
   unsigned char* record;   // [chunks][Record::bytes]
-  uint4* s[3];     // [chunks + 1][warps][DK / 16][32]: the state before a chunk in bf16 terms (fp32: three, else two)
-  float4* e;       // [chunks][warps][4][32]: E
-  float* dots;     // [warps][chunks][32]: <grad_y, y> over a warp's channels
-  float* shared;   // [2][positions][heads][DK]: gradients of q and k before value heads are joined
-  int64_t chunks;  // batch * heads * chunks of an entry
+  uint4* s[3];             // [chunks + 1][warps][DK / 16][32]: the state before a chunk in bf16 terms
+  uint4* ds[3];            // [chunks][warps][DK / 16][32]: the gradient of the state after it
+  float4 *e, *dz;          // [chunks][warps][4][32]: E and dZ
+  float* sums;             // [3][warps][chunks][32]: <grad_y, y>, <grad_v, v> and grad_beta over a warp's channels
+  float* along;            // [chunks + 1][warps]: <dS, S> before a chunk, of every fourth and the last
+  int64_t chunks;          // batch * heads * chunks of an entry
 };
+constexpr int kAgain = 4;
 
 struct DeltaArgs {
   int32_t batch, len, heads, share;   // share: value heads of a key head
   int32_t key_dim, value_dim;
   int32_t chunks;                     // of an entry: (len + 31) / 32
   int32_t parts;                      // CTAs that share an (entry, head)'s value channels
+  int32_t warps;                      // of 16 value channels, of all parts
   float scale;
   const int32_t* offsets;
   const float *state_in, *grad_last;
@@ -311,6 +314,24 @@ __device__ __forceinline__ void load_terms(unsigned char* tile, int plane, int l
   }
 }
 
+// One piece of such a tile: eight elements, `n` of them there.
+template <class T, int IT>
+__device__ __forceinline__ void put_eight(unsigned char* to, int plane, const T* from, int n, bool wide) {
+  Eight<T> x;
+  if (n <= 0) x.clear();
+  else if (wide) x.load(from);
+  else x.gather(from, n);
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    *reinterpret_cast<uint4*>(to) = x.u[0];
+  } else {
+    uint32_t w[4][IT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split<IT>(x.at(2 * i), x.at(2 * i + 1), w[i]);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) *reinterpret_cast<uint4*>(to + i * plane) = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+  }
+}
+
 // X^T of such a tile in the layout of accumulators: rows e0 .. e0 + 15 are the tile's
 // columns, columns its 32 rows.
 template <int IT>
@@ -544,8 +565,13 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
 // ---------------------------------------------------------------------------
 
 constexpr int kForwardTerms = 3;
+// Terms of the states (and of their gradients) in the products that give the gradients
+// of q and k: as many bits as those have.  A bf16 one rounds the states once, as its own
+// store rounds it.  The states are kept in one more, where <dS, S> is taken.
 template <class T>
-constexpr int kKept = sizeof(T) == 2 ? 2 : 3;   // terms of the states that are kept for a backward
+constexpr int kStateTerms = std::is_same_v<T, __nv_bfloat16> ? 1 : std::is_same_v<T, __half> ? 2 : 3;
+template <class T>
+constexpr int kKept = kStateTerms<T> < 3 ? kStateTerms<T> + 1 : 3;
 
 enum DeltaMode {
   kForward,   // y and the last state
@@ -614,15 +640,17 @@ __global__ void __launch_bounds__(384)
       S[n][r] = a.state_in && d < a.key_dim && e < a.value_dim
                     ? a.state_in[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
     }
-  const int64_t warps = (int64_t)consumers * a.parts, mine = part * consumers + warp;
+  const int64_t warps = a.warps, mine = part * consumers + warp;
   const auto keep = [&](int c) {   // the state before chunk c, for the reverse pass
     const int64_t at = ((head * (a.chunks + 1) + c) * warps + mine) * (DK / 16) * 32 + lane;
+    const bool all = kKept<T> == kStateTerms<T> || c % kAgain == 0 || c == chunks;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
       uint32_t x[kKept<T>][4];
       left_of<kKept<T>>(S, s, x);
 #pragma unroll
-      for (int j = 0; j < kKept<T>; ++j) a.work.s[j][at + s * 32] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
+      for (int j = 0; j < kKept<T>; ++j)
+        if (j < kStateTerms<T> || all) a.work.s[j][at + s * 32] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
     }
   };
   unsigned char* own = held + producers * size + warp * Stage::own;
@@ -699,7 +727,7 @@ __global__ void __launch_bounds__(384)
           if (g == 0) sums[8 * n + 2 * t + r] = x;
         }
       __syncwarp();
-      a.work.dots[(mine * a.work.chunks + head * a.chunks + c) * kChunk + lane] = sums[lane];
+      a.work.sums[(mine * a.work.chunks + head * a.chunks + c) * kChunk + lane] = sums[lane];
       __syncwarp();
     } else {
       const bool there = t0 + lane < a.len, on = lane < live;   // dead positions of the chunk too: 0
@@ -790,112 +818,69 @@ __global__ void __launch_bounds__(384)
 }
 
 // ---------------------------------------------------------------------------
-// reverse
+// backward
 // ---------------------------------------------------------------------------
-
-// Terms of the reverse pass' operands: of the recursion (R), of the states (S) and of
-// U, dZ, dA and X (U) in the products that give the gradients of q and k.  Those alone
-// are of 16 bits where q is: the states are rounded once for a bf16 result, as its own
-// store rounds it.  128 key channels of fp16 or fp32 leave shared memory for two terms
-// (2^-17 of an operand at most, 5e-6 of an fp32 gradient); <dS, S> is then taken anew
-// in every chunk.
-template <class T, int DK>
-struct ReverseTerms {
-  static constexpr bool tight = DK == 128 && !std::is_same_v<T, __nv_bfloat16>;
-  static constexpr int R = tight ? 2 : 3;
-  static constexpr int S = std::is_same_v<T, __nv_bfloat16> ? 1 : std::is_same_v<T, float> && !tight ? 3 : 2;
-  static constexpr int U = std::is_same_v<T, float> && !tight ? 3 : 2;
-  static constexpr int again = tight ? 1 : 4;   // chunks between the exact values of <dS, S>
-};
-
-template <class T, int DK>
-struct ReverseStage {
-  static constexpr int NR = ReverseTerms<T, DK>::R;
-  static constexpr int IT = Terms<T>::of(NR), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr bool v_too = std::is_same_v<T, __nv_bfloat16>;   // others leave no room for V
-  // of the record: numbers, then NR terms of each matrix
-  static constexpr int inverse = Record::inverse, a = inverse + NR * kLower, m = a + NR * kLower, k = m + NR * kLower,
-                       q = k + IT * plane, gy = q + IT * plane;
-  static constexpr int bytes(int dvp) { return gy + (v_too ? 2 : 1) * IT * kChunk * dvp * 2; }
-};
-// What the consumers share: dS and S [channels][DK], U and dZ [32][channels], dA and X +
-// X^T [32][32], sums.
-template <class T, int DK>
-struct ReverseShared {
-  static constexpr int NS = ReverseTerms<T, DK>::S, NU = ReverseTerms<T, DK>::U;
-  int ds, s, u, dz, da, xs, red, bytes;
-  __host__ __device__ ReverseShared(int warps, int dvp) {
-    ds = 0;
-    s = ds + NS * warps * 16 * DK * 2;
-    u = s + NS * warps * 16 * DK * 2;
-    dz = u + NU * kChunk * dvp * 2;
-    da = dz + NU * kChunk * dvp * 2;
-    xs = da + NU * kLower;
-    red = xs + NU * 2048;
-    bytes = red + (warps * 66 + 3) / 4 * 16;
-  }
-};
-
-// From the last chunk to the first, with dS (the gradient of the state after the
-// chunk) in the accumulators as S was:
+//
+// From the last chunk to the first, with dS the gradient of the state after the chunk,
+// A^T dY and so on as above:
 //   dU = A^T dY + diag(exp(G_31 - G)) K dS;  dE = diag(beta) dU;  dZ = (..)^-T dE = dV
 //   dbeta = E . (dU - M^T dZ)                        (sums over the channels)
 //   dS0 = exp(G_31) dS + Q^T (scale exp(G) dY) - K^T (exp(G) dZ)
-// and, with the channels of all warps in shared memory, dA = scale D o (dY U^T) and X =
-// -D o (dZ U^T) below the diagonal,
+// Value channels do not meet here either (k_delta_reverse, warps as in the forward).
+// Then, all chunks at once (k_delta_gradients): dA = scale D o (dY U^T) and X = -D o (dZ
+// U^T) below the diagonal,
 //   dQ = scale exp(G) dY S0^T + dA K
 //   dK = exp(G_31 - G) U dS^T - exp(G) dZ S0^T + dA^T Q + (X + X^T) K
-// Decays: y and S1 are homogeneous in (S0, V), so dG_i = dY_i . Y_i - dV_i . V_i, and
-// the gradient of g_t is their sum from t to the chunk's end and <dS, S1> there.  That
-// number is carried from chunk to chunk by the same sums, and taken anew from the
-// states every few chunks, before roundings add up.
+// Decays: y and S1 are homogeneous in (S0, V), so dG_i = dY_i . Y_i - dV_i . V_i, and the
+// gradient of g_t is their sum from t to the chunk's end and <dS, S1> there.  That number
+// is the same sum over the chunks up to the next one where it is taken from the states:
+// every fourth, before roundings add up.
+
 template <class T, int DK>
-__global__ void __launch_bounds__(320)
-    k_delta_bwd(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> gq,
-                DView<T> gk, DView<T> gv, int producers) {
+struct ReverseStage {
+  static constexpr int NR = 3, IT = Terms<T>::of(NR), lp = log_of(DK / 8), plane = kChunk * DK * 2;
+  static constexpr int record = 0, k = (Record::bytes + 127) / 128 * 128, q = k + IT * plane, gy = q + IT * plane;
+  static constexpr int bytes(int dvp) { return gy + 2 * IT * kChunk * dvp * 2; }   // grad_y and V
+  static constexpr int own = sizeof(T) == 2 ? 1024 : 256;   // dV on its way to rows; sums
+};
+
+template <class T, int DK>
+__global__ void __launch_bounds__(384)
+    k_delta_reverse(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> gv,
+                    int producers) {
   using Stage = ReverseStage<T, DK>;
-  using Shared = ReverseShared<T, DK>;
-  constexpr int IT = Stage::IT, lp = Stage::lp, plane = Stage::plane, NR = Stage::NR, NS = Shared::NS, NU = Shared::NU,
-                kAgain = ReverseTerms<T, DK>::again;
+  constexpr int IT = Stage::IT, lp = Stage::lp, plane = Stage::plane, NR = Stage::NR, NS = kStateTerms<T>;
   extern __shared__ __align__(128) unsigned char held[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = (blockDim.x >> 5) - producers, meeting = 32 * (W + 1);
-  const int lv = W == 1 ? 1 : 32 - __clz(2 * W - 1), dvp = 8 << lv, plane_v = kChunk * dvp * 2;
-  const int size = Stage::bytes(dvp);
-  const int bh = blockIdx.x, b = bh / a.heads, h = bh % a.heads, hk = h / a.share;
+  const int consumers = (blockDim.x >> 5) - producers, meeting = 32 * (consumers + 1);
+  const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
+  const int size = Stage::bytes(8 << lv);
+  const int part = blockIdx.x % a.parts, bh = blockIdx.x / a.parts, b = bh / a.heads, h = bh % a.heads;
+  const int hk = h / a.share, first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
-  const Shared at(W, dvp);
-  unsigned char* shared = held + producers * size;
   const int64_t head = (int64_t)b * a.heads + h;
-  if (warp >= W) {
-    const int p = warp - W;
+  if (warp >= consumers) {
+    const int p = warp - consumers, cols_v = min(16 * consumers, a.value_dim - first_v);
     unsigned char* st = held + p * size;
     for (int n = p; n < chunks; n += producers) {
       if (n >= producers) meet(1 + producers + p, meeting);
       const int c = chunks - 1 - n, t0 = c * kChunk, live = min(kChunk, len - t0);
-      const unsigned char* record = a.work.record + (head * a.chunks + c) * Record::bytes;
-      if constexpr (NR == 3) {
-        copy_record(st, record, Record::bytes, lane);
-      } else {
-        copy_record(st, record, Record::inverse + NR * kLower, lane);
-        copy_record(st + Stage::a, record + Record::a, NR * kLower, lane);
-        copy_record(st + Stage::m, record + Record::m, NR * kLower, lane);
-      }
+      copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::bytes, lane);
       load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
                         a.key_dim, a.wide_qk, lane);
       load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
                         a.key_dim, a.wide_qk, lane);
-      load_terms<T, IT>(st + Stage::gy, plane_v, lv, gy.data + b * gy.batch + t0 * gy.time + h * gy.head, gy.time, live,
-                        a.value_dim, a.wide_v, lane);
-      if constexpr (Stage::v_too)
-        load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
-                          v.data + b * v.batch + t0 * v.time + h * v.head, v.time, live, a.value_dim, a.wide_v, lane);
+      load_terms<T, IT>(st + Stage::gy, plane_v, lv, gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v,
+                        gy.time, live, cols_v, a.wide_v, lane);
+      load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
+                        v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time, live, cols_v, a.wide_v, lane);
       copies_done();
       arrive(1 + p, meeting);
     }
     return;
   }
-  const int g = lane >> 2, t = lane & 3, e0 = 16 * warp;
+  const int g = lane >> 2, t = lane & 3, e0 = first_v + 16 * warp;
+  const int64_t warps = a.warps, mine = part * consumers + warp;
   float dS[DK / 8][4];
 #pragma unroll
   for (int n = 0; n < DK / 8; ++n)
@@ -905,14 +890,10 @@ __global__ void __launch_bounds__(320)
       dS[n][r] = a.grad_last && d < a.key_dim && e < a.value_dim
                      ? a.grad_last[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
     }
-  float* red = reinterpret_cast<float*>(shared + at.red);   // [warps][2][32]: dbeta, <dV, V>
-  float* along = red + W * 64;                              // [2][warps]: <dS, S>, of chunks in turn
-  const uint32_t sh = smem_of(shared);
-  const auto state_at = [&](int c) { return ((head * (a.chunks + 1) + c) * W + warp) * (DK / 16) * 32 + lane; };
   const auto word = [](const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; };
-  // <dS, S> over the warp's channels
+  // <dS, S> before chunk c over the warp's channels
   const auto find_along = [&](int c) {
-    const int64_t from = state_at(c);
+    const int64_t at = (head * (a.chunks + 1) + c) * warps + mine, from = at * (DK / 16) * 32 + lane;
     float x = 0.f;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
@@ -931,61 +912,39 @@ __global__ void __launch_bounds__(320)
       }
     }
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-    if (lane == 0) along[(c & 1) * W + warp] = x;
+    if (lane == 0) a.work.along[at] = x;
   };
   find_along(chunks);
-  float carry = 0.f;
+  unsigned char* own = held + producers * size + warp * Stage::own;
   int stage = 0;
   for (int n0 = 0; n0 < chunks; ++n0) {
     const int c = chunks - 1 - n0, t0 = c * kChunk, live = min(kChunk, len - t0);
     unsigned char* st = held + stage * size;
     const uint32_t base = smem_of(st);
-    // what the states' pass left, and V where this lane's dV will be
-    uint4 s0[DK / 16];
-    const int64_t from = state_at(c);
+    const int64_t chunk = head * a.chunks + c, at_c = chunk * warps + mine;
+    float4 e[4];   // E, from the states' pass
 #pragma unroll
-    for (int s = 0; s < DK / 16; ++s) s0[s] = a.work.s[0][from + s * 32];
-    float E[4][4], V[4][4];
-#pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float4 x = a.work.e[(((head * a.chunks + c) * W + warp) * 4 + n) * 32 + lane];
-      E[n][0] = x.x, E[n][1] = x.y, E[n][2] = x.z, E[n][3] = x.w;
-      if constexpr (!Stage::v_too)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-          V[n][r] = i < live && e < a.value_dim
-                        ? to_f32(v.data[b * v.batch + (int64_t)(t0 + i) * v.time + h * v.head + e]) : 0.f;
-        }
-    }
-    float dots = 0.f;
-    if (warp == 0)
-      for (int w = 0; w < W; ++w) dots += a.work.dots[(w * a.work.chunks + head * a.chunks + c) * kChunk + lane];
-    meet(1 + stage, meeting);   // the stage is there, and every warp is through with the chunk before
+    for (int n = 0; n < 4; ++n) e[n] = a.work.e[(at_c * 4 + n) * 32 + lane];
+    meet(1 + stage, meeting);
+    float dU[4][4], dZ[4][4], X[4][4];
+    zero(dU);
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
-      uint32_t x[NS][4];
-      left_of<NS>(dS, s, x);
-      uint4 u[NS];
-      u[0] = s0[s];
+      uint32_t x[NR][4];
+      left_of<NR>(dS, s, x);
 #pragma unroll
-      for (int j = 1; j < NS; ++j) u[j] = a.work.s[j][from + s * 32];
+      for (int j = 0; j < NS; ++j)
+        a.work.ds[j][at_c * (DK / 16) * 32 + s * 32 + lane] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t to = element_at(e0 + g + 8 * (i & 1), 16 * s + 8 * (i >> 1) + 2 * t, lp);
+      for (int p = 0; p < 2; ++p)
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          const int tile = j * W * 16 * DK * 2;
-          *reinterpret_cast<uint32_t*>(shared + at.ds + tile + to) = x[j][i];
-          *reinterpret_cast<uint32_t*>(shared + at.s + tile + to) = word(u[j], i);
+        for (int j = 0; j < IT; ++j) {
+          uint32_t u[4];
+          load_matrices<false>(u, base + Stage::k + j * plane + right_rows(lane, 16 * p, 16 * s, lp));
+#pragma unroll
+          for (int i = 0; i + j < NR; ++i) multiply(dU[2 * p], x[i], u[0], u[1]), multiply(dU[2 * p + 1], x[i], u[2], u[3]);
         }
-      }
     }
-    float dU[4][4], dZ[4][4];
-    zero(dU);
-    product<DK / 16, 2, NR, IT, NR, false, 0>(
-        dU, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dS, s, x); },
-        [&](int p, int s, int j) { return base + Stage::k + j * plane + right_rows(lane, 16 * p, 16 * s, lp); });
     const auto columns = [&](float (&x)[4][4], const float (&y)[4][4], int array) {   // x = y times a number a column
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -993,72 +952,72 @@ __global__ void __launch_bounds__(320)
         x[n][0] = y[n][0] * f.x, x[n][1] = y[n][1] * f.y, x[n][2] = y[n][2] * f.x, x[n][3] = y[n][3] * f.y;
       }
     };
-    columns(dU, dU, Record::until);
     const auto lower = [&](int tile, int p, int s, int j) {
       return base + tile + j * kLower + (p + s) * 512 + right_cols(lane, 0, 0, 1);
     };
+    columns(dU, dU, Record::until);
     product<2, 2, IT, NR, NR, true, 2>(
         dU,
         [&](int s, uint32_t (&x)[IT][4]) {
 #pragma unroll
           for (int i = 0; i < IT; ++i)
-            load_matrices<true>(x[i], base + Stage::gy + i * plane_v + left_cols(lane, e0, 16 * s, lv));
+            load_matrices<true>(x[i], base + Stage::gy + i * plane_v + left_cols(lane, 16 * warp, 16 * s, lv));
         },
-        [&](int p, int s, int j) { return lower(Stage::a, p, s, j); });
+        [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
+    columns(X, dU, Record::beta);
     zero(dZ);
-    {
-      float dE[4][4];
-      columns(dE, dU, Record::beta);
-      product<2, 2, NR, NR, NR, true, 2>(
-          dZ, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dE, s, x); },
-          [&](int p, int s, int j) { return lower(Stage::inverse, p, s, j); });
-    }
-    {
-      float R[4][4];
-      if constexpr (Stage::v_too) load_turned<IT>(V, base + Stage::gy + IT * plane_v, plane_v, e0, lv, lane);
-      zero(R);
-      product<2, 2, NR, NR, NR, true, 2>(
-          R, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
-          [&](int p, int s, int j) { return lower(Stage::m, p, s, j); });
+    product<2, 2, NR, NR, NR, true, 2>(
+        dZ, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(X, s, x); },
+        [&](int p, int s, int j) { return lower(Record::inverse, p, s, j); });
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+    for (int n = 0; n < 4; ++n)
+      a.work.dz[(at_c * 4 + n) * 32 + lane] = make_float4(dZ[n][0], dZ[n][1], dZ[n][2], dZ[n][3]);
+    zero(X);
+    product<2, 2, NR, NR, NR, true, 2>(
+        X, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
+        [&](int p, int s, int j) { return lower(Record::m, p, s, j); });
+    {
+      float V[4][4];
+      load_turned<IT>(V, base + Stage::gy + IT * plane_v, plane_v, 16 * warp, lv, lane);
+      float* sums = reinterpret_cast<float*>(own);
+#pragma unroll
+      for (int n = 0; n < 4; ++n) {
+        const float E[4] = {e[n].x, e[n].y, e[n].z, e[n].w};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x = E[n][r] * (dU[n][r] - R[n][r]) + E[n][2 + r] * (dU[n][2 + r] - R[n][2 + r]);
+          float x = E[r] * (dU[n][r] - X[n][r]) + E[2 + r] * (dU[n][2 + r] - X[n][2 + r]);
           float y = dZ[n][r] * V[n][r] + dZ[n][2 + r] * V[n][2 + r];
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) {
             x += __shfl_xor_sync(kFull, x, o);
             y += __shfl_xor_sync(kFull, y, o);
           }
-          if (g == 0) {
-            red[warp * 64 + 8 * n + 2 * t + r] = x;
-            red[warp * 64 + 32 + 8 * n + 2 * t + r] = y;
-          }
+          if (g == 0) sums[8 * n + 2 * t + r] = y, sums[32 + 8 * n + 2 * t + r] = x;
         }
-    }
-    // U and dZ for the other warps
-    columns(E, E, Record::beta);
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      uint32_t u[NU][4], z[NU][4];
-      left_of<NU>(E, s, u);
-      left_of<NU>(dZ, s, z);
-      const uint32_t to = sh + left_cols(lane, e0, 16 * s, lv);
-#pragma unroll
-      for (int j = 0; j < NU; ++j) {
-        store_matrices(to + at.u + j * plane_v, u[j][0], u[j][1], u[j][2], u[j][3]);
-        store_matrices(to + at.dz + j * plane_v, z[j][0], z[j][1], z[j][2], z[j][3]);
       }
+      __syncwarp();
+      a.work.sums[((warps + mine) * a.work.chunks + chunk) * kChunk + lane] = sums[lane];
+      a.work.sums[((2 * warps + mine) * a.work.chunks + chunk) * kChunk + lane] = sums[32 + lane];
+      __syncwarp();
     }
-    // dV: a bf16 one is the first term as it lies there
-    if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    // dV
+    if constexpr (sizeof(T) == 2) {
+      const auto both = [](float lo, float hi) {
+        Vec<T, 2> o;
+        narrow2(o.e, make_float2(lo, hi));
+        return *reinterpret_cast<const uint32_t*>(&o);
+      };
+#pragma unroll
+      for (int s = 0; s < 2; ++s)
+        store_matrices(smem_of(own) + left_cols(lane, 0, 16 * s, 1), both(dZ[2 * s][0], dZ[2 * s][1]),
+                       both(dZ[2 * s][2], dZ[2 * s][3]), both(dZ[2 * s + 1][0], dZ[2 * s + 1][1]),
+                       both(dZ[2 * s + 1][2], dZ[2 * s + 1][3]));
       __syncwarp();
       if (t0 + lane < a.len) {
         T* to = gv.data + b * gv.batch + (int64_t)(t0 + lane) * gv.time + h * gv.head + e0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(shared + at.dz + piece(lane, e0 / 8 + u, lv)));
+          Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(own + piece(lane, u, 1)));
 #pragma unroll
           for (int i = 0; i < 8; ++i) o.e[i] = lane < live ? o.e[i] : from_f32<T>(0.f);
           if (a.wide_y && e0 + 8 * u + 8 <= a.value_dim) {
@@ -1070,6 +1029,7 @@ __global__ void __launch_bounds__(320)
           }
         }
       }
+      __syncwarp();
     } else {
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -1077,8 +1037,7 @@ __global__ void __launch_bounds__(320)
         for (int r = 0; r < 4; ++r) {
           const int i = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
           if (t0 + i < a.len && e < a.value_dim)
-            gv.data[b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head + e] =
-                from_f32<T>(i < live ? dZ[n][r] : 0.f);
+            gv.data[b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head + e] = i < live ? dZ[n][r] : 0.f;
         }
     }
     // the gradient of the state before the chunk
@@ -1087,53 +1046,185 @@ __global__ void __launch_bounds__(320)
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
       for (int r = 0; r < 4; ++r) dS[n][r] *= whole;
+    load_turned<IT>(X, base + Stage::gy, plane_v, 16 * warp, lv, lane);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) {
+      const float2 f = pair_at(st, Record::since, n, t);
+      const float2 w = make_float2(f.x * a.scale, f.y * a.scale);
+      X[n][0] *= w.x, X[n][1] *= w.y, X[n][2] *= w.x, X[n][3] *= w.y;
+      dZ[n][0] *= -f.x, dZ[n][1] *= -f.y, dZ[n][2] *= -f.x, dZ[n][3] *= -f.y;
+    }
     product<2, DK / 16, NR, IT, NR, true, 0>(
-        dS,
-        [&](int s, uint32_t (&x)[NR][4]) {
-          uint32_t y[IT][4];
-#pragma unroll
-          for (int i = 0; i < IT; ++i)
-            load_matrices<true>(y[i], base + Stage::gy + i * plane_v + left_cols(lane, e0, 16 * s, lv));
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 since = pair_at(st, Record::since, 2 * s + (i >> 1), t);
-            float2 f = unpack(y[IT - 1][i]);
-#pragma unroll
-            for (int j = IT - 2; j >= 0; --j) {
-              const float2 l = unpack(y[j][i]);
-              f.x += l.x, f.y += l.y;
-            }
-            uint32_t w[NR];
-            split<NR>(f.x * (a.scale * since.x), f.y * (a.scale * since.y), w);
-#pragma unroll
-            for (int j = 0; j < NR; ++j) x[j][i] = w[j];
-          }
-        },
+        dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(X, s, x); },
         [&](int p, int s, int j) { return base + Stage::q + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
-    columns(dZ, dZ, Record::since);
-#pragma unroll
-    for (int n = 0; n < 4; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dZ[n][r] = -dZ[n][r];
     product<2, DK / 16, NR, IT, NR, true, 0>(
         dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
         [&](int p, int s, int j) { return base + Stage::k + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
-    meet(1 + 2 * producers, 32 * W);
-    if (warp == 0) {
-      float gb = 0.f, dv = 0.f;
-      for (int w = 0; w < W; ++w) gb += red[w * 64 + lane], dv += red[w * 64 + 32 + lane];
-      if (n0 == 0 || (c + 1) % kAgain == 0) {
-        carry = 0.f;
-        for (int w = 0; w < W; ++w) carry += along[((c + 1) & 1) * W + w];
+    if (n0 + producers < chunks) arrive(1 + producers + stage, meeting);
+    stage = stage + 1 == producers ? 0 : stage + 1;
+    if (c % kAgain == 0 && c > 0) find_along(c);
+  }
+  if (a.grad_state)
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
+        if (d < a.key_dim && e < a.value_dim) a.grad_state[(head * a.key_dim + d) * a.value_dim + e] = dS[n][r];
       }
-      float x = dots - dv;
+}
+
+// A CTA has a chunk of a key head and COLS of its channels.  In shared memory: S0 and dS
+// [value channels][COLS], U and dZ [value channels][32], grad_y, K and Q, dA and X + X^T.
+template <class T, int DK>
+struct GradientShared {
+  static constexpr int COLS = DK == 128 ? 64 : DK, lc = log_of(COLS / 8);
+  static constexpr int IT = Terms<T>::of(3), NS = kStateTerms<T>, NU = std::is_same_v<T, float> ? 3 : 2;
+  static constexpr int warps = COLS / 8;   // 16 channels by 16 positions each
+  static constexpr int plane = kChunk * COLS * 2;
+  int s, ds, u, dz, gy, k, q, da, xs, bytes;
+  __host__ __device__ GradientShared(int W, int dvp) {
+    s = 640;   // the record's numbers first
+    ds = s + NS * W * 16 * COLS * 2;
+    u = ds + NS * W * 16 * COLS * 2;
+    dz = u + NU * W * 1024;
+    gy = dz + NU * W * 1024;
+    k = gy + IT * kChunk * dvp * 2;
+    q = k + IT * plane;
+    da = q + IT * plane;
+    xs = da + NU * kLower;
+    bytes = xs + NU * 2048;
+  }
+};
+
+template <class T, int DK>
+__global__ void __launch_bounds__(256)
+    k_delta_gradients(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> gy, DView<T> gq, DView<T> gk,
+                      DView<T> gv) {
+  using Shared = GradientShared<T, DK>;
+  constexpr int IT = Shared::IT, NS = Shared::NS, NU = Shared::NU, COLS = Shared::COLS, lc = Shared::lc,
+                plane = Shared::plane, kWarps = Shared::warps, kThreads = 32 * kWarps;
+  extern __shared__ __align__(128) unsigned char held[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int W = a.warps, lv = W == 1 ? 1 : 32 - __clz(2 * W - 1), plane_v = (kChunk * 16) << lv;
+  const Shared at(W, 8 << lv);
+  const int J = a.heads / a.share;
+  const int64_t job = blockIdx.x / (DK / COLS);
+  const int col0 = (int)(blockIdx.x % (DK / COLS)) * COLS;
+  const int c = (int)(job % a.chunks), b = (int)(job / a.chunks / J), hk = (int)(job / a.chunks % J);
+  const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk, t0 = c * kChunk;
+  const int live = min(kChunk, len - t0), there = min(kChunk, a.len - t0);
+  if (live <= 0) {   // past the entry's end
+    for (int i = warp; i < there; i += kWarps) {
+      T* tq = gq.data + b * gq.batch + (int64_t)(t0 + i) * gq.time + hk * gq.head;
+      T* tk = gk.data + b * gk.batch + (int64_t)(t0 + i) * gk.time + hk * gk.head;
+      for (int d = col0 + lane; d < min(a.key_dim, col0 + COLS); d += 32) tq[d] = tk[d] = from_f32<T>(0.f);
+      if (col0) continue;
+      for (int h = hk * a.share; h < (hk + 1) * a.share; ++h) {
+        T* to = gv.data + b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head;
+        for (int e = lane; e < a.value_dim; e += 32) to[e] = from_f32<T>(0.f);
+        if (lane == 0) {
+          a.grad_decay.data[b * a.grad_decay.batch + (t0 + i) * a.grad_decay.time + h * a.grad_decay.head] = 0.f;
+          a.grad_beta.data[b * a.grad_beta.batch + (t0 + i) * a.grad_beta.time + h * a.grad_beta.head] = 0.f;
+        }
+      }
+    }
+    return;
+  }
+  const uint32_t sh = smem_of(held);
+  // this warp's part of dQ and dK: positions 16 m .., channels col0 + 16 p ..
+  const int m = warp & 1, p = warp >> 1;
+  float sq[2][4], sk[2][4];
+  zero(sq), zero(sk);
+  const int cols = min(COLS, max(0, a.key_dim - col0));
+  // K and Q: a stripe of the rows for each warp
+  for (int w = 0; w < 2; ++w) {
+    const DView<const T>& x = w ? q : k;
+    const T* rows = x.data + b * x.batch + t0 * x.time + hk * x.head + col0;
+    unsigned char* tile = held + (w ? at.q : at.k);
+    for (int u = threadIdx.x; u < kChunk << lc; u += kThreads) {
+      const int r = u >> lc, n = u & ((1 << lc) - 1);
+      const bool on = r < live && n * 8 < cols;
+      if constexpr (std::is_same_v<T, __nv_bfloat16>)
+        if (a.wide_qk) {
+          copy_async(smem_of(tile) + piece(r, n, lc), on ? rows + r * x.time + n * 8 : rows, on);
+          continue;
+        }
+      put_eight<T, IT>(tile + piece(r, n, lc), plane, rows + r * x.time + n * 8, on ? cols - n * 8 : 0, a.wide_qk);
+    }
+  }
+  for (int hs = 0; hs < a.share; ++hs) {
+    const int h = hk * a.share + hs;
+    const int64_t head = (int64_t)b * a.heads + h, chunk = head * a.chunks + c;
+    if (hs) __syncthreads();   // every warp is through with the head before
+    const unsigned char* record = a.work.record + chunk * Record::bytes;
+    if (threadIdx.x < 40) copy_async(sh + threadIdx.x * 16, record + threadIdx.x * 16, true);
+    for (int u = threadIdx.x; u < kChunk << lv; u += kThreads) {
+      const int r = u >> lv, n = u & ((1 << lv) - 1);
+      const bool on = r < live && n * 8 < a.value_dim;
+      const T* rows = gy.data + b * gy.batch + t0 * gy.time + h * gy.head;
+      if constexpr (std::is_same_v<T, __nv_bfloat16>)
+        if (a.wide_v) {
+          copy_async(sh + at.gy + piece(r, n, lv), on ? rows + r * gy.time + n * 8 : rows, on);
+          continue;
+        }
+      put_eight<T, IT>(held + at.gy + piece(r, n, lv), plane_v, rows + r * gy.time + n * 8, on ? a.value_dim - n * 8 : 0,
+                       a.wide_v);
+    }
+    // states: a lane's four words of 16 channels by 16 key channels
+    const auto put_states = [&](uint4* const (&from)[3], int64_t first, int tile) {
+      for (int u = threadIdx.x; u < W * (COLS / 16) * 32; u += kThreads) {
+        const int l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
+        const int row = 16 * w + (l >> 2), col = 16 * s + 2 * (l & 3);
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          const uint4 x = from[j][((first + w) * (DK / 16) + col0 / 16 + s) * 32 + l];
+          unsigned char* to = held + tile + j * W * 16 * COLS * 2;
+          *reinterpret_cast<uint32_t*>(to + element_at(row, col, lc)) = x.x;
+          *reinterpret_cast<uint32_t*>(to + element_at(row + 8, col, lc)) = x.y;
+          *reinterpret_cast<uint32_t*>(to + element_at(row, col + 8, lc)) = x.z;
+          *reinterpret_cast<uint32_t*>(to + element_at(row + 8, col + 8, lc)) = x.w;
+        }
+      }
+    };
+    put_states(a.work.s, (head * (a.chunks + 1) + c) * W, at.s);
+    put_states(a.work.ds, chunk * W, at.ds);
+    for (int u = threadIdx.x; u < W * 128; u += kThreads) {
+      const int l = u & 31, n = (u >> 5) & 3, w = u >> 7;
+      const float4 e = a.work.e[chunk * W * 128 + u], z = a.work.dz[chunk * W * 128 + u];
+      const float2 f = *reinterpret_cast<const float2*>(record + Record::beta + (8 * n + 2 * (l & 3)) * 4);
+      const uint32_t r0 = element_at(16 * w + (l >> 2), 8 * n + 2 * (l & 3), 2);
+      const uint32_t r1 = element_at(16 * w + (l >> 2) + 8, 8 * n + 2 * (l & 3), 2);
+      put_pair<NU>(held + at.u + r0, W * 1024, e.x * f.x, e.y * f.y);
+      put_pair<NU>(held + at.u + r1, W * 1024, e.z * f.x, e.w * f.y);
+      put_pair<NU>(held + at.dz + r0, W * 1024, z.x, z.y);
+      put_pair<NU>(held + at.dz + r1, W * 1024, z.z, z.w);
+    }
+    copies_done();
+    __syncthreads();
+    if (col0 == 0 && warp == kWarps - 1) {
+      // decays and betas: the chunk's sums, and those of the chunks up to where <dS, S> is known
+      float x = 0.f, gb = 0.f;
+      for (int w = 0; w < W; ++w) {
+        x += a.work.sums[(w * a.work.chunks + chunk) * kChunk + lane] -
+             a.work.sums[((W + w) * a.work.chunks + chunk) * kChunk + lane];
+        gb += a.work.sums[((2 * W + w) * a.work.chunks + chunk) * kChunk + lane];
+      }
+      const int known = min(chunks, (c / kAgain + 1) * kAgain);
+      float carry = 0.f;
+      for (int n = c + 1; n < known; ++n)
+        for (int w = 0; w < W; ++w)
+          carry += a.work.sums[(w * a.work.chunks + head * a.chunks + n) * kChunk + lane] -
+                   a.work.sums[((W + w) * a.work.chunks + head * a.chunks + n) * kChunk + lane];
+      if (lane < W) carry += a.work.along[(head * (a.chunks + 1) + known) * W + lane];
+      for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const float y = __shfl_down_sync(kFull, x, o);
         if (lane + o < 32) x += y;
       }
-      const int i = t0 + lane;
-      if (i < a.len) {
+      const int64_t i = t0 + lane;
+      if (lane < there) {
         const bool on = lane < live;
         // where exp(g) is 0 so is its gradient, which the sums give to their rounding
         const float g_i = on ? a.decay.data[b * a.decay.batch + i * a.decay.time + h * a.decay.head] : 0.f;
@@ -1141,39 +1232,37 @@ __global__ void __launch_bounds__(320)
             on && expf(g_i) != 0.f ? x + carry : 0.f;
         a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = on ? gb : 0.f;
       }
-      carry += __shfl_sync(kFull, x, 0);
     }
     // dA and X, a 16 x 16 block at a time
-    for (int u = warp; u < 6; u += W) {
+    for (int u = warp; u < 6; u += kWarps) {
       const bool is_x = u >= 3;
       const int blk = is_x ? u - 3 : u, mi = (blk + 1) >> 1, pj = blk >> 1;
       float acc[2][4];
       zero(acc);
+#pragma unroll 2
       for (int s = 0; s < W; ++s) {
-        uint32_t x[NU][4], y[NU][4];
+        uint32_t y[NU][4];
+#pragma unroll
+        for (int j = 0; j < NU; ++j)
+          load_matrices<true>(y[j], sh + at.u + j * W * 1024 + right_cols(lane, 16 * pj, 16 * s, 2));
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
-          load_matrices<false>(y[i], sh + at.u + i * plane_v + right_rows(lane, 16 * pj, 16 * s, lv));
-          if (is_x) load_matrices<false>(x[i], sh + at.dz + i * plane_v + left_rows(lane, 16 * mi, 16 * s, lv));
-          else if (i < IT) load_matrices<false>(x[i], base + Stage::gy + i * plane_v + left_rows(lane, 16 * mi, 16 * s, lv));
-          else x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0u;
+          uint32_t x[4];
+          if (is_x) load_matrices<true>(x, sh + at.dz + i * W * 1024 + left_cols(lane, 16 * mi, 16 * s, 2));
+          else if (i < IT) load_matrices<false>(x, sh + at.gy + i * plane_v + left_rows(lane, 16 * mi, 16 * s, lv));
+          if (!is_x && i >= IT) continue;
+#pragma unroll
+          for (int j = 0; j + i < NU; ++j) multiply(acc[0], x, y[j][0], y[j][1]), multiply(acc[1], x, y[j][2], y[j][3]);
         }
-#pragma unroll
-        for (int i = 0; i < NU; ++i)
-#pragma unroll
-          for (int j = 0; j + i < NU; ++j) {
-            multiply(acc[0], x[i], y[j][0], y[j][1]);
-            multiply(acc[1], x[i], y[j][2], y[j][3]);
-          }
       }
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const int i = 16 * mi + g + (r >> 1) * 8, j = 16 * pj + 8 * n + 2 * t + (r & 1);
-          float x = i >= j ? acc[n][r] * between(st, i, j) : 0.f;
+          float x = i >= j ? acc[n][r] * between(held, i, j) : 0.f;
           x = is_x ? (i > j ? -x : 0.f) : a.scale * x;
-          unsigned char* tile = shared + (is_x ? at.xs : at.da);
+          unsigned char* tile = held + (is_x ? at.xs : at.da);
 #pragma unroll
           for (int w = 0; w < NU; ++w) {
             const __nv_bfloat16 y = __float2bfloat16_rn(x);
@@ -1184,170 +1273,103 @@ __global__ void __launch_bounds__(320)
           }
         }
     }
-    meet(1 + 2 * producers, 32 * W);
-    // dQ and dK, 16 of their columns at a time
-    for (int p = warp; p < DK / 16; p += W) {
-      float aq[2][2][4], ak[2][2][4];
+    {
+      float aq[2][4], ak[2][4], az[2][4];
+      zero(aq), zero(ak), zero(az);
+#pragma unroll 2
+      for (int s = 0; s < W; ++s) {
+        uint32_t bs[NS][4], bd[NS][4];
 #pragma unroll
-      for (int m = 0; m < 2; ++m) zero(aq[m]), zero(ak[m]);
-      {
-        float az[2][2][4];
-#pragma unroll
-        for (int m = 0; m < 2; ++m) zero(az[m]);
-        for (int s = 0; s < W; ++s) {
-          uint32_t bs[NS][4], bd[NS][4];
-#pragma unroll
-          for (int j = 0; j < NS; ++j) {
-            const uint32_t to = j * W * 16 * DK * 2 + right_cols(lane, 16 * p, 16 * s, lp);
-            load_matrices<true>(bs[j], sh + at.s + to);
-            load_matrices<true>(bd[j], sh + at.ds + to);
-          }
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            const uint32_t to = left_rows(lane, 16 * m, 16 * s, lv);
-#pragma unroll
-            for (int i = 0; i < NU; ++i) {
-              uint32_t x[4];
-              if (i < IT) {
-                load_matrices<false>(x, base + Stage::gy + i * plane_v + to);
-#pragma unroll
-                for (int j = 0; j < NS && i + j < NU; ++j)
-                  multiply(aq[m][0], x, bs[j][0], bs[j][1]), multiply(aq[m][1], x, bs[j][2], bs[j][3]);
-              }
-              load_matrices<false>(x, sh + at.dz + i * plane_v + to);
-#pragma unroll
-              for (int j = 0; j < NS && i + j < NU; ++j)
-                multiply(az[m][0], x, bs[j][0], bs[j][1]), multiply(az[m][1], x, bs[j][2], bs[j][3]);
-              load_matrices<false>(x, sh + at.u + i * plane_v + to);
-#pragma unroll
-              for (int j = 0; j < NS && i + j < NU; ++j)
-                multiply(ak[m][0], x, bd[j][0], bd[j][1]), multiply(ak[m][1], x, bd[j][2], bd[j][3]);
-            }
-          }
+        for (int j = 0; j < NS; ++j) {
+          const uint32_t to = sh + j * W * 16 * COLS * 2 + right_cols(lane, 16 * p, 16 * s, lc);
+          load_matrices<true>(bs[j], to + at.s);
+          load_matrices<true>(bd[j], to + at.ds);
         }
+        const uint32_t to = left_cols(lane, 16 * m, 16 * s, 2);
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
+        for (int i = 0; i < NU; ++i) {
+          uint32_t x[4];
+          if (i < IT) {
+            load_matrices<false>(x, sh + at.gy + i * plane_v + left_rows(lane, 16 * m, 16 * s, lv));
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int i = 16 * m + g + (r >> 1) * 8;
-            const float since = float_at(st, Record::since, i), until = float_at(st, Record::until, i);
-#pragma unroll
-            for (int n = 0; n < 2; ++n) {
-              aq[m][n][r] *= a.scale * since;
-              ak[m][n][r] = until * ak[m][n][r] - since * az[m][n][r];
-            }
+            for (int j = 0; j < NS && i + j < NU; ++j)
+              multiply(aq[0], x, bs[j][0], bs[j][1]), multiply(aq[1], x, bs[j][2], bs[j][3]);
           }
+          load_matrices<true>(x, sh + at.dz + i * W * 1024 + to);
+#pragma unroll
+          for (int j = 0; j < NS && i + j < NU; ++j)
+            multiply(az[0], x, bs[j][0], bs[j][1]), multiply(az[1], x, bs[j][2], bs[j][3]);
+          load_matrices<true>(x, sh + at.u + i * W * 1024 + to);
+#pragma unroll
+          for (int j = 0; j < NS && i + j < NU; ++j)
+            multiply(ak[0], x, bd[j][0], bd[j][1]), multiply(ak[1], x, bd[j][2], bd[j][3]);
+        }
       }
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        uint32_t bk[IT][4], bq[IT][4];
-#pragma unroll
-        for (int j = 0; j < IT; ++j) {
-          const uint32_t to = j * plane + right_cols(lane, 16 * p, 16 * s, lp);
-          load_matrices<true>(bk[j], base + Stage::k + to);
-          load_matrices<true>(bq[j], base + Stage::q + to);
-        }
-        const auto add = [&](float (&acc)[2][4], const uint32_t (&x)[4], const uint32_t (&y)[IT][4], int i) {
-#pragma unroll
-          for (int j = 0; j < IT; ++j)
-            if (i + j < NU) multiply(acc[0], x, y[j][0], y[j][1]), multiply(acc[1], x, y[j][2], y[j][3]);
-        };
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int i = 0; i < NU; ++i) {
-            uint32_t x[4];
-            if (s <= m) {
-              load_matrices<false>(x, sh + at.da + i * kLower + (m + s) * 512 + left_rows(lane, 0, 0, 1));
-              add(aq[m], x, bk, i);
-            }
-            if (s >= m) {
-              load_matrices<true>(x, sh + at.da + i * kLower + (m + s) * 512 + left_cols(lane, 0, 0, 1));
-              add(ak[m], x, bq, i);
-            }
-            load_matrices<false>(x, sh + at.xs + i * 2048 + left_rows(lane, 16 * m, 16 * s, 2));
-            add(ak[m], x, bk, i);
-          }
-      }
-#pragma unroll
-      for (int m = 0; m < 2; ++m)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int i = 16 * m + g + 8 * r;
-          if (t0 + i >= a.len) continue;
-          const bool on = i < live;
-#pragma unroll
-          for (int n = 0; n < 2; ++n) {
-            const int d = 16 * p + 8 * n + 2 * t;
-            const float2 x = on ? make_float2(aq[m][n][2 * r], aq[m][n][2 * r + 1]) : make_float2(0.f, 0.f);
-            const float2 y = on ? make_float2(ak[m][n][2 * r], ak[m][n][2 * r + 1]) : make_float2(0.f, 0.f);
-            if (a.share > 1) {
-              const int64_t pos = ((int64_t)b * a.len + t0 + i) * a.heads + h;
-              const int64_t all = (int64_t)a.batch * a.len * a.heads;
-              *reinterpret_cast<float2*>(a.work.shared + pos * DK + d) = x;
-              *reinterpret_cast<float2*>(a.work.shared + (all + pos) * DK + d) = y;
-              continue;
-            }
-            T* tq = gq.data + b * gq.batch + (int64_t)(t0 + i) * gq.time + h * gq.head + d;
-            T* tk = gk.data + b * gk.batch + (int64_t)(t0 + i) * gk.time + h * gk.head + d;
-            if (a.wide_gy && d < a.key_dim) {
-              Vec<T, 2> o;
-              narrow2(o.e, x);
-              store_vec(tq, o);
-              narrow2(o.e, y);
-              store_vec(tk, o);
-            } else {
-              if (d < a.key_dim) tq[0] = from_f32<T>(x.x), tk[0] = from_f32<T>(y.x);
-              if (d + 1 < a.key_dim) tq[1] = from_f32<T>(x.y), tk[1] = from_f32<T>(y.y);
-            }
-          }
-        }
-    }
-    if (c % kAgain == 0 && c > 0) find_along(c);
-    if (n0 + producers < chunks) arrive(1 + producers + stage, meeting);
-    stage = stage + 1 == producers ? 0 : stage + 1;
-  }
-  if (a.grad_state)
-#pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
-        const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-        if (d < a.key_dim && e < a.value_dim) a.grad_state[(head * a.key_dim + d) * a.value_dim + e] = dS[n][r];
+        const int i = 16 * m + g + (r >> 1) * 8;
+        const float since = float_at(held, Record::since, i), until = float_at(held, Record::until, i);
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+          sq[n][r] += a.scale * since * aq[n][r];
+          sk[n][r] += until * ak[n][r] - since * az[n][r];
+        }
       }
-  // positions past the last chunk
-  for (int64_t i = (int64_t)chunks * kChunk + warp; i < a.len; i += W) {
-    T* to = gv.data + b * gv.batch + i * gv.time + h * gv.head;
-    for (int e = lane; e < a.value_dim; e += 32) to[e] = from_f32<T>(0.f);
-    if (a.share == 1) {
-      T* tq = gq.data + b * gq.batch + i * gq.time + h * gq.head;
-      T* tk = gk.data + b * gk.batch + i * gk.time + h * gk.head;
-      for (int d = lane; d < a.key_dim; d += 32) tq[d] = tk[d] = from_f32<T>(0.f);
     }
-    if (lane == 0) {
-      a.grad_decay.data[b * a.grad_decay.batch + i * a.grad_decay.time + h * a.grad_decay.head] = 0.f;
-      a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = 0.f;
+    __syncthreads();   // dA and X are there
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      uint32_t bk[IT][4], bq[IT][4];
+#pragma unroll
+      for (int j = 0; j < IT; ++j) {
+        const uint32_t to = sh + j * plane + right_cols(lane, 16 * p, 16 * s, lc);
+        load_matrices<true>(bk[j], to + at.k);
+        load_matrices<true>(bq[j], to + at.q);
+      }
+      const auto add = [&](float (&acc)[2][4], const uint32_t (&x)[4], const uint32_t (&y)[IT][4], int i) {
+#pragma unroll
+        for (int j = 0; j < IT; ++j)
+          if (i + j < NU) multiply(acc[0], x, y[j][0], y[j][1]), multiply(acc[1], x, y[j][2], y[j][3]);
+      };
+#pragma unroll
+      for (int i = 0; i < NU; ++i) {
+        uint32_t x[4];
+        if (s <= m) {
+          load_matrices<false>(x, sh + at.da + i * kLower + (m + s) * 512 + left_rows(lane, 0, 0, 1));
+          add(sq, x, bk, i);
+        }
+        if (s >= m) {
+          load_matrices<true>(x, sh + at.da + i * kLower + (m + s) * 512 + left_cols(lane, 0, 0, 1));
+          add(sk, x, bq, i);
+        }
+        load_matrices<false>(x, sh + at.xs + i * 2048 + left_rows(lane, 16 * m, 16 * s, 2));
+        add(sk, x, bk, i);
+      }
     }
   }
-}
-
-// A key head's gradients of q and k: the sum over its value heads, in their order.
-template <class T>
-__global__ void __launch_bounds__(256) k_delta_join(DeltaArgs a, int dk, DView<T> gq, DView<T> gk) {
-  const int64_t rows = (int64_t)a.batch * a.len * a.heads, n = rows / a.share * a.key_dim;
-  const int kh = a.heads / a.share;
-  for (int64_t u = blockIdx.x * 256ll + threadIdx.x; u < n; u += gridDim.x * 256ll) {
-    const int64_t r = u / a.key_dim, pos = r / kh, b = pos / a.len, i = pos - b * a.len;
-    const int d = (int)(u - r * a.key_dim), j = (int)(r - pos * kh);
-    float x = 0.f, y = 0.f;
-    if (i < length_of(a, (int)b))
-      for (int s = 0; s < a.share; ++s) {
-        const int64_t from = (pos * a.heads + j * a.share + s) * dk + d;
-        x += a.work.shared[from];
-        y += a.work.shared[rows * dk + from];
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const int i = 16 * m + g + 8 * r;
+    if (i >= there) continue;
+    const bool on = i < live;
+#pragma unroll
+    for (int n = 0; n < 2; ++n) {
+      const int d = col0 + 16 * p + 8 * n + 2 * t;
+      const float2 x = on ? make_float2(sq[n][2 * r], sq[n][2 * r + 1]) : make_float2(0.f, 0.f);
+      const float2 y = on ? make_float2(sk[n][2 * r], sk[n][2 * r + 1]) : make_float2(0.f, 0.f);
+      T* tq = gq.data + b * gq.batch + (int64_t)(t0 + i) * gq.time + hk * gq.head + d;
+      T* tk = gk.data + b * gk.batch + (int64_t)(t0 + i) * gk.time + hk * gk.head + d;
+      if (a.wide_gy && d < a.key_dim) {
+        Vec<T, 2> o;
+        narrow2(o.e, x);
+        store_vec(tq, o);
+        narrow2(o.e, y);
+        store_vec(tk, o);
+      } else {
+        if (d < a.key_dim) tq[0] = from_f32<T>(x.x), tk[0] = from_f32<T>(y.x);
+        if (d + 1 < a.key_dim) tq[1] = from_f32<T>(x.y), tk[1] = from_f32<T>(y.y);
       }
-    gq.data[b * gq.batch + i * gq.time + j * gq.head + d] = from_f32<T>(x);
-    gk.data[b * gk.batch + i * gk.time + j * gk.head + d] = from_f32<T>(y);
+    }
   }
 }
 
@@ -1378,54 +1400,68 @@ cudaError_t launch_delta_prepare(const DeltaArgs& a, const DeltaViews& w, bool b
   return cudaGetLastError();
 }
 
-template <class T, int DK, DeltaMode MODE>
-cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
-  using Stage = ForwardStage<T, DK, MODE>;
-  cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
-  if (e != cudaSuccess) return e;
-  const int W = (a.value_dim + 15) / 16;
+// CTAs, warps and stages of the kernels that walk along time.
+struct DeltaShape {
+  int consumers, producers, smem;
+  unsigned ctas;
+};
+template <class Stage>
+DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a) {
+  const int W = a.warps;
   const int64_t heads = (int64_t)a.batch * a.heads;
   // value channels over several CTAs where there are too few sequences for the SMs
   a.parts = 1;
   for (int d = 2; d <= W && heads * a.parts < h->sm_count; ++d)
     if (W % d == 0) a.parts = d;
-  const int consumers = W / a.parts, own = consumers * Stage::own;
+  DeltaShape s;
+  s.consumers = W / a.parts;
+  s.ctas = (unsigned)(heads * a.parts);
   int dvp = 16;
-  while (dvp < 16 * consumers) dvp *= 2;
-  const int64_t ctas = heads * a.parts;
-  int producers = ctas > h->sm_count ? 2 : 4;
-  while (producers > 1 && producers * Stage::bytes(dvp) + own > kMostShared) --producers;
-  const int smem = producers * Stage::bytes(dvp) + own;
-  const auto kernel = k_delta_fwd<T, DK, MODE>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  while (dvp < 16 * s.consumers) dvp *= 2;
+  const int own = s.consumers * Stage::own;
+  s.producers = s.ctas > (unsigned)h->sm_count ? 2 : 4;
+  while (s.producers > 1 && s.producers * Stage::bytes(dvp) + own > kMostShared) --s.producers;
+  s.smem = s.producers * Stage::bytes(dvp) + own;
+  return s;
+}
+
+template <class T, int DK, DeltaMode MODE>
+cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
+  cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)ctas, 32 * (consumers + producers), smem, stream>>>(
-      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.y), producers);
+  const DeltaShape s = walk_shape<ForwardStage<T, DK, MODE>>(h, a);
+  const auto kernel = k_delta_fwd<T, DK, MODE>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<s.ctas, 32 * (s.consumers + s.producers), s.smem, stream>>>(
+      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.y),
+      s.producers);
   return cudaGetLastError();
 }
 
 template <class T, int DK>
-cudaError_t launch_delta_bwd(const emb_delta_s* h, const DeltaArgs& a, const DeltaViews& w, cudaStream_t stream) {
+cudaError_t launch_delta_bwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
   cudaError_t e = launch_delta_fwd<T, DK, kStates>(h, a, w, stream);
   if (e != cudaSuccess) return e;
-  const int W = (a.value_dim + 15) / 16;
-  int dvp = 16;
-  while (dvp < 16 * W) dvp *= 2;
-  const ReverseShared<T, DK> at(W, dvp);
-  int producers = 2;
-  while (producers > 1 && producers * ReverseStage<T, DK>::bytes(dvp) + at.bytes > kMostShared) --producers;
-  const int smem = producers * ReverseStage<T, DK>::bytes(dvp) + at.bytes;
-  const auto kernel = k_delta_bwd<T, DK>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const DeltaShape s = walk_shape<ReverseStage<T, DK>>(h, a);
+  const auto reverse = k_delta_reverse<T, DK>;
+  e = cudaFuncSetAttribute(reverse, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(a.batch * a.heads), 32 * (W + producers), smem, stream>>>(
-      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.gq),
-      dview<T>(w.gk), dview<T>(w.gv), producers);
+  reverse<<<s.ctas, 32 * (s.consumers + s.producers), s.smem, stream>>>(
+      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.gv),
+      s.producers);
   e = cudaGetLastError();
-  if (e != cudaSuccess || a.share == 1 || a.len == 0) return e;
-  const int64_t n = (int64_t)a.batch * a.len * (a.heads / a.share) * a.key_dim, need = (n + 255) / 256;
-  const int64_t most = (int64_t)h->sm_count * 32;
-  k_delta_join<T><<<(unsigned)(need < most ? need : most), 256, 0, stream>>>(a, DK, dview<T>(w.gq), dview<T>(w.gk));
+  if (e != cudaSuccess || a.chunks == 0) return e;
+  using Shared = GradientShared<T, DK>;
+  int dvp = 16;
+  while (dvp < 16 * a.warps) dvp *= 2;
+  const int smem = Shared(a.warps, dvp).bytes;
+  const auto gradients = k_delta_gradients<T, DK>;
+  e = cudaFuncSetAttribute(gradients, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  gradients<<<(unsigned)(a.work.chunks / a.share * (DK / Shared::COLS)), 32 * Shared::warps, smem, stream>>>(
+      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.gy), dview<T>(w.gq), dview<T>(w.gk),
+      dview<T>(w.gv));
   return cudaGetLastError();
 }
 
