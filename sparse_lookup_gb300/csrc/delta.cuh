@@ -101,7 +101,11 @@ __device__ __forceinline__ void load_matrices(uint32_t (&r)[4], uint32_t at) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(at) : "memory");
 }
 
-// The way back: a lane's pairs to rows of 8 elements.
+// The way back, transposed: a lane's pairs to columns of rows of 8 elements; and as they are.
+__device__ __forceinline__ void store_rows(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
+               "r"(d) : "memory");
+}
 __device__ __forceinline__ void store_matrices(uint32_t at, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(a), "r"(b), "r"(c),
                "r"(d) : "memory");
@@ -151,25 +155,27 @@ __device__ __forceinline__ uint32_t lower_at(int row, int col) {
   return (uint32_t)(((row >> 4) + (col >> 4)) * 512) + element_at(row & 15, col & 15, 1);
 }
 
-// Addresses of the matrix loads for a lane.  X [n][k] as right operand: rows n0..+15,
-// columns k0..+15 (not transposed); X [k][n]: rows k0, columns n0 (transposed).  As left
-// operand: X [m][k] (not transposed), X [k][m] (transposed).
-__device__ __forceinline__ uint32_t right_rows(int lane, int n0, int k0, int lp) {
-  return piece(n0 + (lane & 7) + ((lane >> 4) << 3), (k0 >> 3) + ((lane >> 3) & 1), lp);
+// Addresses of the matrix loads of a lane in a tile that starts at a multiple of 256
+// bytes: the first 16 x 16 elements' here, the others' by next().  X [n][k] as right
+// operand (not transposed), X [k][n] (transposed); as left operand X [m][k] (not
+// transposed), X [k][m] (transposed).
+__device__ __forceinline__ uint32_t right_rows(int lane, int lp) {
+  return piece((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1, lp);
 }
-__device__ __forceinline__ uint32_t right_cols(int lane, int n0, int k0, int lp) {
-  return piece(k0 + (lane & 15), (n0 >> 3) + (lane >> 4), lp);
+__device__ __forceinline__ uint32_t right_cols(int lane, int lp) { return piece(lane & 15, lane >> 4, lp); }
+__device__ __forceinline__ uint32_t left_rows(int lane, int lp) { return piece(lane & 15, lane >> 4, lp); }
+__device__ __forceinline__ uint32_t left_cols(int lane, int lp) {
+  return piece((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1, lp);
 }
-__device__ __forceinline__ uint32_t left_rows(int lane, int m0, int k0, int lp) {
-  return piece(m0 + (lane & 15), (k0 >> 3) + (lane >> 4), lp);
-}
-__device__ __forceinline__ uint32_t left_cols(int lane, int m0, int k0, int lp) {
-  return piece(k0 + (lane & 7) + ((lane >> 4) << 3), (m0 >> 3) + ((lane >> 3) & 1), lp);
+// 16 `rows` rows and 16 `cols` columns on: pieces are exchanged by their bits, so theirs are too.
+__device__ __forceinline__ uint32_t next(uint32_t at, int rows, int cols, int lp) {
+  return (at ^ (cols << 5)) + (rows << (lp + 8));
 }
 
 // acc += X Y over KS steps of 16.  left(s, a): the step's TA terms of X;
 // right(p, s, j): address of term j of Y for the p-th 16 columns.  Products of
-// terms i + j < N.  TRI 1: Y's steps s > p are zero, 2: s < p are.
+// terms i + j < N.  TRI 1: Y's steps s > p are zero, 2: s < p are.  Four accumulators
+// in turn, as a matrix instruction's result takes that long.
 template <int KS, int NP, int TA, int TB, int N, bool TRANS, int TRI, class L, class R>
 __device__ __forceinline__ void product(float (&acc)[2 * NP][4], L left, R right) {
 #pragma unroll
@@ -177,18 +183,22 @@ __device__ __forceinline__ void product(float (&acc)[2 * NP][4], L left, R right
     uint32_t a[TA][4];
     left(s, a);
 #pragma unroll
-    for (int p = 0; p < NP; ++p) {
-      if ((TRI == 1 && s > p) || (TRI == 2 && s < p)) continue;
+    for (int p0 = 0; p0 < NP; p0 += 2) {
+      const auto there = [&](int p) { return p < NP && !(TRI == 1 && s > p) && !(TRI == 2 && s < p); };
 #pragma unroll
       for (int j = 0; j < TB; ++j) {
-        uint32_t b[4];
-        load_matrices<TRANS>(b, right(p, s, j));
+        uint32_t b[2][4];
+#pragma unroll
+        for (int p = 0; p < 2; ++p)
+          if (there(p0 + p)) load_matrices<TRANS>(b[p], right(p0 + p, s, j));
 #pragma unroll
         for (int i = 0; i < TA; ++i)
-          if (i + j < N) {
-            multiply(acc[2 * p], a[i], b[0], b[1]);
-            multiply(acc[2 * p + 1], a[i], b[2], b[3]);
-          }
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            if (i + j < N && there(p0 + p)) {
+              multiply(acc[(2 * (p0 + p)) % (2 * NP)], a[i], b[p][0], b[p][1]);
+              multiply(acc[(2 * (p0 + p) + 1) % (2 * NP)], a[i], b[p][2], b[p][3]);
+            }
       }
     }
   }
@@ -206,6 +216,12 @@ __device__ __forceinline__ void left_of(const float (&x)[W][4], int s, uint32_t 
 #pragma unroll
       for (int i = 0; i < N; ++i) a[i][2 * h + r] = t[i];
     }
+}
+
+// x = y times a pair of numbers a row pair (accumulators' columns).
+__device__ __forceinline__ void times(float (&x)[4], const float (&y)[4], float2 f) {
+  const float2 a = __fmul2_rn(make_float2(y[0], y[1]), f), b = __fmul2_rn(make_float2(y[2], y[3]), f);
+  x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
 template <int W>
@@ -332,15 +348,15 @@ __device__ __forceinline__ void put_eight(unsigned char* to, int plane, const T*
   }
 }
 
-// X^T of such a tile in the layout of accumulators: rows e0 .. e0 + 15 are the tile's
-// columns, columns its 32 rows.
+// X^T of such a tile in the layout of accumulators: rows are 16 of the tile's columns
+// (`at` is left_cols' address of the first), columns its 32 rows.
 template <int IT>
-__device__ __forceinline__ void load_turned(float (&x)[4][4], uint32_t tile, int plane, int e0, int lp, int lane) {
+__device__ __forceinline__ void load_turned(float (&x)[4][4], uint32_t at, int plane, int lp) {
 #pragma unroll
   for (int s = 0; s < 2; ++s) {
     uint32_t y[IT][4];
 #pragma unroll
-    for (int i = 0; i < IT; ++i) load_matrices<true>(y[i], tile + i * plane + left_cols(lane, e0, 16 * s, lp));
+    for (int i = 0; i < IT; ++i) load_matrices<true>(y[i], next(at, s, 0, lp) + i * plane);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float2 f = unpack(y[IT - 1][i]);
@@ -395,13 +411,13 @@ constexpr int kMostShared = 227 << 10;
 // records
 // ---------------------------------------------------------------------------
 
-// A warp's shared memory: K and Q, then in their place the record, M diag(beta) of the two
-// diagonal blocks in floats, and a block in terms.
+// A warp's shared memory: K and Q, then in their place the record's numbers and inverse,
+// M diag(beta) of the two diagonal blocks in floats, and a block in terms.
 template <class T, int DK>
 struct PrepareShared {
   static constexpr int IT = Terms<T>::of(3), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr int tiles = 2 * IT * plane, m = Record::bytes, block = m + 2 * 16 * 20 * 4,
-                       rest = block + 3 * 512, bytes = tiles > rest ? tiles : rest;
+  static constexpr int tiles = 2 * IT * plane, m = Record::a, block = m + 2 * 16 * 20 * 4, rest = block + 3 * 512,
+                       bytes = ((tiles > rest ? tiles : rest) + 255) / 256 * 256;
 };
 
 // A warp a chunk.  The inverse of I + N, N = M diag(beta) = [N11 0; N21 N22]: both
@@ -433,21 +449,21 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   // rows 16 .. 31 by all (four)
   float kk[6][4], qk[6][4];
   zero(kk), zero(qk);
-  const uint32_t kt = smem_of(mine), qt = kt + IT * plane;
+  const uint32_t kr = smem_of(mine) + right_rows(lane, lp), kl = smem_of(mine) + left_rows(lane, lp);
 #pragma unroll
   for (int s = 0; s < DK / 16; ++s) {
     uint32_t bk[2][IT][4];
 #pragma unroll
     for (int p = 0; p < 2; ++p)
 #pragma unroll
-      for (int j = 0; j < IT; ++j) load_matrices<false>(bk[p][j], kt + j * plane + right_rows(lane, 16 * p, 16 * s, lp));
+      for (int j = 0; j < IT; ++j) load_matrices<false>(bk[p][j], next(kr, p, s, lp) + j * plane);
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int i = 0; i < IT; ++i) {
         uint32_t x[4], y[4];
-        load_matrices<false>(x, kt + i * plane + left_rows(lane, 16 * m, 16 * s, lp));
-        load_matrices<false>(y, qt + i * plane + left_rows(lane, 16 * m, 16 * s, lp));
+        load_matrices<false>(x, next(kl, m, s, lp) + i * plane);
+        load_matrices<false>(y, next(kl, m, s, lp) + (IT + i) * plane);
 #pragma unroll
         for (int p = 0; p <= m; ++p)
 #pragma unroll
@@ -478,24 +494,45 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   numbers[Record::g_lo / 4 + lane] = lo;
   __syncwarp();
   float below[2][4];   // N21
+  uint4* out = reinterpret_cast<uint4*>(a.work.record + job * Record::bytes);
+  // a block that lies in terms at Shared::block to its place in the record
+  const auto put_block = [&](int matrix, int blk) {
+    __syncwarp();
+    const uint4* in = reinterpret_cast<const uint4*>(mine + Shared::block);
 #pragma unroll
-  for (int u = 0; u < 6; ++u) {
-    const int blk = u >> 1, row0 = 16 * ((blk + 1) >> 1), col = 16 * (blk >> 1) + 8 * (u & 1) + 2 * t4;
-    const float2 bj = *reinterpret_cast<const float2*>(mine + Record::beta + col * 4);
+    for (int j = 0; j < 3; ++j) out[(matrix + j * kLower + blk * 512) / 16 + lane] = in[j * 32 + lane];
+    __syncwarp();
+  };
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const int i = row0 + g4 + 8 * r;
-      const float d0 = i >= col ? between(mine, i, col) : 0.f, d1 = i > col ? between(mine, i, col + 1) : 0.f;
-      const uint32_t to = lower_at(i, col);
-      put_pair<3>(mine + Record::a + to, kLower, qk[u][2 * r] * d0 * a.scale, qk[u][2 * r + 1] * d1 * a.scale);
-      const float m0 = i > col ? kk[u][2 * r] * d0 : 0.f, m1 = i > col + 1 ? kk[u][2 * r + 1] * d1 : 0.f;
-      if (backward) put_pair<3>(mine + Record::m + to, kLower, m0, m1);
-      if (blk == 1) {
-        below[u & 1][2 * r] = m0 * bj.x, below[u & 1][2 * r + 1] = m1 * bj.y;
-      } else {
-        float* at = reinterpret_cast<float*>(mine + Shared::m) + ((blk >> 1) * 16 + (i & 15)) * 20 + (col & 15);
-        at[0] = m0 * bj.x, at[1] = m1 * bj.y;
+  for (int blk = 0; blk < 3; ++blk) {
+    float keys[2][4];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int u = 2 * blk + n, col = 16 * (blk >> 1) + 8 * n + 2 * t4, i = 16 * ((blk + 1) >> 1) + g4 + 8 * r;
+        const float2 bj = *reinterpret_cast<const float2*>(mine + Record::beta + col * 4);
+        const float d0 = i >= col ? between(mine, i, col) : 0.f, d1 = i > col ? between(mine, i, col + 1) : 0.f;
+        put_pair<3>(mine + Shared::block + element_at(i & 15, col & 15, 1), 512, qk[u][2 * r] * d0 * a.scale,
+                    qk[u][2 * r + 1] * d1 * a.scale);
+        const float m0 = i > col ? kk[u][2 * r] * d0 : 0.f, m1 = i > col + 1 ? kk[u][2 * r + 1] * d1 : 0.f;
+        keys[n][2 * r] = m0, keys[n][2 * r + 1] = m1;
+        if (blk == 1) {
+          below[n][2 * r] = m0 * bj.x, below[n][2 * r + 1] = m1 * bj.y;
+        } else {
+          float* at = reinterpret_cast<float*>(mine + Shared::m) + ((blk >> 1) * 16 + (i & 15)) * 20 + (col & 15);
+          at[0] = m0 * bj.x, at[1] = m1 * bj.y;
+        }
       }
+    put_block(Record::a, blk);
+    if (backward) {
+#pragma unroll
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          put_pair<3>(mine + Shared::block + element_at(g4 + 8 * r, 8 * n + 2 * t4, 1), 512, keys[n][2 * r],
+                      keys[n][2 * r + 1]);
+      put_block(Record::m, blk);
     }
   }
   __syncwarp();
@@ -533,7 +570,7 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   zero(x);
   product<1, 1, 3, 3, 3, true, 0>(
       x, [&](int s, uint32_t (&y)[3][4]) { left_of<3>(below, s, y); },
-      [&](int, int, int j) { return inverse + j * kLower + right_cols(lane, 0, 0, 1); });
+      [&](int, int, int j) { return inverse + j * kLower + right_cols(lane, 1); });
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -545,9 +582,9 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
       x,
       [&](int, uint32_t (&y)[3][4]) {
 #pragma unroll
-        for (int i = 0; i < 3; ++i) load_matrices<false>(y[i], inverse + i * kLower + 1024 + left_rows(lane, 0, 0, 1));
+        for (int i = 0; i < 3; ++i) load_matrices<false>(y[i], inverse + i * kLower + 1024 + left_rows(lane, 1));
       },
-      [&](int, int, int j) { return block + j * 512 + right_cols(lane, 0, 0, 1); });
+      [&](int, int, int j) { return block + j * 512 + right_cols(lane, 1); });
 #pragma unroll
   for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -555,9 +592,8 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
       put_pair<3>(mine + Record::inverse + 512 + element_at(g4 + 8 * r, 8 * n + 2 * t4, 1), kLower, -x[n][2 * r],
                   -x[n][2 * r + 1]);
   __syncwarp();
-  uint4* out = reinterpret_cast<uint4*>(a.work.record + job * Record::bytes);
   const uint4* in = reinterpret_cast<const uint4*>(mine);
-  for (int u = lane; u < (backward ? Record::bytes : Record::forward_bytes) / 16; u += 32) out[u] = in[u];
+  for (int u = lane; u < Record::a / 16; u += 32) out[u] = in[u];
 }
 
 // ---------------------------------------------------------------------------
@@ -581,8 +617,7 @@ enum DeltaMode {
 template <class T, int DK, DeltaMode MODE>
 struct ForwardStage {
   static constexpr int NT = kForwardTerms, IT = Terms<T>::of(NT), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr int record = 0, k = 9856, q = k + IT * plane, v = q + IT * plane;
-  static_assert(Record::forward_bytes == k && k % 128 == 0, "");
+  static constexpr int record = 0, k = (Record::forward_bytes + 255) / 256 * 256, q = k + IT * plane, v = q + IT * plane;
   // V (and grad_y) in terms, rows of dvp channels
   static constexpr int bytes(int dvp) { return v + (MODE == kStates ? 2 : 1) * IT * kChunk * dvp * 2; }
   // a warp's results on their way to rows: 16 bits swizzled, fp32 rows of 17
@@ -654,6 +689,8 @@ __global__ void __launch_bounds__(384)
     }
   };
   unsigned char* own = held + producers * size + warp * Stage::own;
+  const uint32_t rows = right_rows(lane, lp), cols = right_cols(lane, lp);
+  const uint32_t turned_v = next(left_cols(lane, lv), 0, warp, lv), low = right_rows(lane, 1);
   int stage = 0;
   for (int c = 0; c < chunks; ++c) {
     unsigned char* st = held + stage * size;
@@ -673,9 +710,9 @@ __global__ void __launch_bounds__(384)
 #pragma unroll
         for (int j = 0; j < IT; ++j) {
           uint32_t u[4], w[4];
-          const uint32_t at = base + j * plane + right_rows(lane, 16 * p, 16 * s, lp);
-          load_matrices<false>(u, at + Stage::k);
-          load_matrices<false>(w, at + Stage::q);
+          const uint32_t at = next(base + Stage::k + rows, p, s, lp) + j * plane;
+          load_matrices<false>(u, at);
+          load_matrices<false>(w, at + IT * plane);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             if (i + j < NT) multiply(Z[2 * p], x[i], u[0], u[1]), multiply(Z[2 * p + 1], x[i], u[2], u[3]);
@@ -684,16 +721,16 @@ __global__ void __launch_bounds__(384)
         }
     }
     // Z = V - exp(G) K S0
-    load_turned<IT>(E, base + Stage::v, plane_v, 16 * warp, lv, lane);
+    load_turned<IT>(E, base + Stage::v + turned_v, plane_v, lv);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float2 f = pair_at(st, Record::since, n, t);
       Z[n][0] = E[n][0] - f.x * Z[n][0], Z[n][1] = E[n][1] - f.y * Z[n][1];
       Z[n][2] = E[n][2] - f.x * Z[n][2], Z[n][3] = E[n][3] - f.y * Z[n][3];
-      Y[n][0] *= f.x * a.scale, Y[n][1] *= f.y * a.scale, Y[n][2] *= f.x * a.scale, Y[n][3] *= f.y * a.scale;
+      times(Y[n], Y[n], make_float2(f.x * a.scale, f.y * a.scale));
     }
     const auto lower = [&](int tile, int p, int s, int j) {
-      return base + tile + j * kLower + (p + s) * 512 + right_rows(lane, 0, 0, 1);
+      return base + low + tile + j * kLower + (p + s) * 512;
     };
     zero(E);
     product<2, 2, NT, NT, NT, false, 1>(
@@ -706,17 +743,14 @@ __global__ void __launch_bounds__(384)
             make_float4(E[n][0], E[n][1], E[n][2], E[n][3]);
     }
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {   // U
-      const float2 f = pair_at(st, Record::beta, n, t);
-      E[n][0] *= f.x, E[n][1] *= f.y, E[n][2] *= f.x, E[n][3] *= f.y;
-    }
+    for (int n = 0; n < 4; ++n) times(E[n], E[n], pair_at(st, Record::beta, n, t));   // U
     product<2, 2, NO, NO, NO, false, 1>(
         Y, [&](int s, uint32_t (&x)[NO][4]) { left_of<NO>(E, s, x); },
         [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
     if constexpr (MODE == kStates) {
       // <grad_y, y> over the warp's channels
       float* sums = reinterpret_cast<float*>(own);
-      load_turned<IT>(Z, base + Stage::v + IT * plane_v, plane_v, 16 * warp, lv, lane);
+      load_turned<IT>(Z, base + Stage::v + IT * plane_v + turned_v, plane_v, lv);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -740,7 +774,7 @@ __global__ void __launch_bounds__(384)
         };
 #pragma unroll
         for (int s = 0; s < 2; ++s)
-          store_matrices(smem_of(own) + left_cols(lane, 0, 16 * s, 1), both(Y[2 * s][0], Y[2 * s][1]),
+          store_matrices(next(smem_of(own) + left_cols(lane, 1), s, 0, 1), both(Y[2 * s][0], Y[2 * s][1]),
                          both(Y[2 * s][2], Y[2 * s][3]), both(Y[2 * s + 1][0], Y[2 * s + 1][1]),
                          both(Y[2 * s + 1][2], Y[2 * s + 1][3]));
         __syncwarp();
@@ -786,17 +820,12 @@ __global__ void __launch_bounds__(384)
     // S1 = exp(G_31) S0 + K^T (exp(G_31 - G) U)
     const float whole = float_at(st, Record::since, kChunk - 1);
 #pragma unroll
-    for (int n = 0; n < 4; ++n) {
-      const float2 f = pair_at(st, Record::until, n, t);
-      E[n][0] *= f.x, E[n][1] *= f.y, E[n][2] *= f.x, E[n][3] *= f.y;
-    }
+    for (int n = 0; n < 4; ++n) times(E[n], E[n], pair_at(st, Record::until, n, t));
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) S[n][r] *= whole;
+    for (int n = 0; n < DK / 8; ++n) times(S[n], S[n], make_float2(whole, whole));
     product<2, DK / 16, NT, IT, NT, true, 0>(
         S, [&](int s, uint32_t (&x)[NT][4]) { left_of<NT>(E, s, x); },
-        [&](int p, int s, int j) { return base + Stage::k + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
+        [&](int p, int s, int j) { return next(base + Stage::k + cols, s, p, lp) + j * plane; });
     if (c + producers < chunks) arrive(1 + producers + stage, meeting);
     stage = stage + 1 == producers ? 0 : stage + 1;
   }
@@ -839,7 +868,7 @@ __global__ void __launch_bounds__(384)
 template <class T, int DK>
 struct ReverseStage {
   static constexpr int NR = 3, IT = Terms<T>::of(NR), lp = log_of(DK / 8), plane = kChunk * DK * 2;
-  static constexpr int record = 0, k = (Record::bytes + 127) / 128 * 128, q = k + IT * plane, gy = q + IT * plane;
+  static constexpr int record = 0, k = (Record::bytes + 255) / 256 * 256, q = k + IT * plane, gy = q + IT * plane;
   static constexpr int bytes(int dvp) { return gy + 2 * IT * kChunk * dvp * 2; }   // grad_y and V
   static constexpr int own = sizeof(T) == 2 ? 1024 : 256;   // dV on its way to rows; sums
 };
@@ -916,6 +945,8 @@ __global__ void __launch_bounds__(384)
   };
   find_along(chunks);
   unsigned char* own = held + producers * size + warp * Stage::own;
+  const uint32_t rows = right_rows(lane, lp), cols = right_cols(lane, lp);
+  const uint32_t turned_v = next(left_cols(lane, lv), 0, warp, lv), low = right_cols(lane, 1);
   int stage = 0;
   for (int n0 = 0; n0 < chunks; ++n0) {
     const int c = chunks - 1 - n0, t0 = c * kChunk, live = min(kChunk, len - t0);
@@ -936,24 +967,24 @@ __global__ void __launch_bounds__(384)
       for (int j = 0; j < NS; ++j)
         a.work.ds[j][at_c * (DK / 16) * 32 + s * 32 + lane] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int j = 0; j < IT; ++j) {
+        uint32_t u[2][4];
 #pragma unroll
-        for (int j = 0; j < IT; ++j) {
-          uint32_t u[4];
-          load_matrices<false>(u, base + Stage::k + j * plane + right_rows(lane, 16 * p, 16 * s, lp));
+        for (int p = 0; p < 2; ++p)
+          load_matrices<false>(u[p], next(base + Stage::k + rows, p, s, lp) + j * plane);
 #pragma unroll
-          for (int i = 0; i + j < NR; ++i) multiply(dU[2 * p], x[i], u[0], u[1]), multiply(dU[2 * p + 1], x[i], u[2], u[3]);
-        }
+        for (int i = 0; i + j < NR; ++i)
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+            multiply(dU[2 * p], x[i], u[p][0], u[p][1]), multiply(dU[2 * p + 1], x[i], u[p][2], u[p][3]);
+      }
     }
     const auto columns = [&](float (&x)[4][4], const float (&y)[4][4], int array) {   // x = y times a number a column
 #pragma unroll
-      for (int n = 0; n < 4; ++n) {
-        const float2 f = pair_at(st, array, n, t);
-        x[n][0] = y[n][0] * f.x, x[n][1] = y[n][1] * f.y, x[n][2] = y[n][2] * f.x, x[n][3] = y[n][3] * f.y;
-      }
+      for (int n = 0; n < 4; ++n) times(x[n], y[n], pair_at(st, array, n, t));
     };
     const auto lower = [&](int tile, int p, int s, int j) {
-      return base + tile + j * kLower + (p + s) * 512 + right_cols(lane, 0, 0, 1);
+      return base + low + tile + j * kLower + (p + s) * 512;
     };
     columns(dU, dU, Record::until);
     product<2, 2, IT, NR, NR, true, 2>(
@@ -961,7 +992,7 @@ __global__ void __launch_bounds__(384)
         [&](int s, uint32_t (&x)[IT][4]) {
 #pragma unroll
           for (int i = 0; i < IT; ++i)
-            load_matrices<true>(x[i], base + Stage::gy + i * plane_v + left_cols(lane, 16 * warp, 16 * s, lv));
+            load_matrices<true>(x[i], next(base + Stage::gy + turned_v, s, 0, lv) + i * plane_v);
         },
         [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
     columns(X, dU, Record::beta);
@@ -978,7 +1009,7 @@ __global__ void __launch_bounds__(384)
         [&](int p, int s, int j) { return lower(Record::m, p, s, j); });
     {
       float V[4][4];
-      load_turned<IT>(V, base + Stage::gy + IT * plane_v, plane_v, 16 * warp, lv, lane);
+      load_turned<IT>(V, base + Stage::gy + IT * plane_v + turned_v, plane_v, lv);
       float* sums = reinterpret_cast<float*>(own);
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
@@ -1009,7 +1040,7 @@ __global__ void __launch_bounds__(384)
       };
 #pragma unroll
       for (int s = 0; s < 2; ++s)
-        store_matrices(smem_of(own) + left_cols(lane, 0, 16 * s, 1), both(dZ[2 * s][0], dZ[2 * s][1]),
+        store_matrices(next(smem_of(own) + left_cols(lane, 1), s, 0, 1), both(dZ[2 * s][0], dZ[2 * s][1]),
                        both(dZ[2 * s][2], dZ[2 * s][3]), both(dZ[2 * s + 1][0], dZ[2 * s + 1][1]),
                        both(dZ[2 * s + 1][2], dZ[2 * s + 1][3]));
       __syncwarp();
@@ -1043,23 +1074,20 @@ __global__ void __launch_bounds__(384)
     // the gradient of the state before the chunk
     const float whole = float_at(st, Record::since, kChunk - 1);
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) dS[n][r] *= whole;
-    load_turned<IT>(X, base + Stage::gy, plane_v, 16 * warp, lv, lane);
+    for (int n = 0; n < DK / 8; ++n) times(dS[n], dS[n], make_float2(whole, whole));
+    load_turned<IT>(X, base + Stage::gy + turned_v, plane_v, lv);
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float2 f = pair_at(st, Record::since, n, t);
-      const float2 w = make_float2(f.x * a.scale, f.y * a.scale);
-      X[n][0] *= w.x, X[n][1] *= w.y, X[n][2] *= w.x, X[n][3] *= w.y;
-      dZ[n][0] *= -f.x, dZ[n][1] *= -f.y, dZ[n][2] *= -f.x, dZ[n][3] *= -f.y;
+      times(X[n], X[n], make_float2(f.x * a.scale, f.y * a.scale));
+      times(dZ[n], dZ[n], make_float2(-f.x, -f.y));
     }
     product<2, DK / 16, NR, IT, NR, true, 0>(
         dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(X, s, x); },
-        [&](int p, int s, int j) { return base + Stage::q + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
+        [&](int p, int s, int j) { return next(base + Stage::q + cols, s, p, lp) + j * plane; });
     product<2, DK / 16, NR, IT, NR, true, 0>(
         dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
-        [&](int p, int s, int j) { return base + Stage::k + j * plane + right_cols(lane, 16 * p, 16 * s, lp); });
+        [&](int p, int s, int j) { return next(base + Stage::k + cols, s, p, lp) + j * plane; });
     if (n0 + producers < chunks) arrive(1 + producers + stage, meeting);
     stage = stage + 1 == producers ? 0 : stage + 1;
     if (c % kAgain == 0 && c > 0) find_along(c);
@@ -1075,16 +1103,17 @@ __global__ void __launch_bounds__(384)
 }
 
 // A CTA has a chunk of a key head and COLS of its channels.  In shared memory: S0 and dS
-// [value channels][COLS], U and dZ [value channels][32], grad_y, K and Q, dA and X + X^T.
+// [value channels][COLS], U and dZ [value channels][32], grad_y, K and Q, dA and X.  16-bit
+// calls leave room for all channels; each CTA of a key head finds dA and X for itself.
 template <class T, int DK>
 struct GradientShared {
-  static constexpr int COLS = DK == 128 ? 64 : DK, lc = log_of(COLS / 8);
+  static constexpr int COLS = DK == 128 && sizeof(T) == 4 ? 64 : DK, lc = log_of(COLS / 8);
   static constexpr int IT = Terms<T>::of(3), NS = kStateTerms<T>, NU = std::is_same_v<T, float> ? 3 : 2;
   static constexpr int warps = COLS / 8;   // 16 channels by 16 positions each
   static constexpr int plane = kChunk * COLS * 2;
-  int s, ds, u, dz, gy, k, q, da, xs, bytes;
+  int s, ds, u, dz, gy, k, q, da, x, bytes;
   __host__ __device__ GradientShared(int W, int dvp) {
-    s = 640;   // the record's numbers first
+    s = 768;   // the record's numbers first
     ds = s + NS * W * 16 * COLS * 2;
     u = ds + NS * W * 16 * COLS * 2;
     dz = u + NU * W * 1024;
@@ -1092,13 +1121,13 @@ struct GradientShared {
     k = gy + IT * kChunk * dvp * 2;
     q = k + IT * plane;
     da = q + IT * plane;
-    xs = da + NU * kLower;
-    bytes = xs + NU * 2048;
+    x = da + NU * kLower;
+    bytes = x + NU * kLower;
   }
 };
 
 template <class T, int DK>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / GradientShared<T, DK>::warps)
     k_delta_gradients(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> gy, DView<T> gq, DView<T> gk,
                       DView<T> gv) {
   using Shared = GradientShared<T, DK>;
@@ -1171,34 +1200,58 @@ __global__ void __launch_bounds__(256)
       put_eight<T, IT>(held + at.gy + piece(r, n, lv), plane_v, rows + r * gy.time + n * 8, on ? a.value_dim - n * 8 : 0,
                        a.wide_v);
     }
-    // states: a lane's four words of 16 channels by 16 key channels
-    const auto put_states = [&](uint4* const (&from)[3], int64_t first, int tile) {
-      for (int u = threadIdx.x; u < W * (COLS / 16) * 32; u += kThreads) {
-        const int l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
-        const int row = 16 * w + (l >> 2), col = 16 * s + 2 * (l & 3);
+    // states: a lane's four words of 16 channels by 16 key channels; several of a thread's
+    // loads are in flight before the first is stored
+    constexpr int U = 4;
+    for (int j = 0; j < NS; ++j)
+      for (int u0 = threadIdx.x; u0 < W * (COLS / 16) * 32; u0 += U * kThreads) {
+        uint4 x[2][U];
 #pragma unroll
-        for (int j = 0; j < NS; ++j) {
-          const uint4 x = from[j][((first + w) * (DK / 16) + col0 / 16 + s) * 32 + l];
-          unsigned char* to = held + tile + j * W * 16 * COLS * 2;
-          *reinterpret_cast<uint32_t*>(to + element_at(row, col, lc)) = x.x;
-          *reinterpret_cast<uint32_t*>(to + element_at(row + 8, col, lc)) = x.y;
-          *reinterpret_cast<uint32_t*>(to + element_at(row, col + 8, lc)) = x.z;
-          *reinterpret_cast<uint32_t*>(to + element_at(row + 8, col + 8, lc)) = x.w;
+        for (int n = 0; n < U; ++n) {
+          const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
+          if (u >= W * (COLS / 16) * 32) continue;
+          const int64_t of = (int64_t)(w * (DK / 16) + col0 / 16 + s) * 32 + l;
+          x[0][n] = a.work.s[j][(head * (a.chunks + 1) + c) * W * (DK / 16) * 32 + of];
+          x[1][n] = a.work.ds[j][chunk * W * (DK / 16) * 32 + of];
+        }
+#pragma unroll
+        for (int n = 0; n < U; ++n) {
+          const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
+          if (u >= W * (COLS / 16) * 32) continue;
+          // words of rows 8 apart and of neighbouring pieces
+          unsigned char* to = held + at.s + j * W * 16 * COLS * 2;
+          const uint32_t first = element_at(16 * w + (l >> 2), 16 * s + 2 * (l & 3), lc), second = first ^ 16u;
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            if (k) to += at.ds - at.s;
+            *reinterpret_cast<uint32_t*>(to + first) = x[k][n].x;
+            *reinterpret_cast<uint32_t*>(to + first + 16 * COLS) = x[k][n].y;
+            *reinterpret_cast<uint32_t*>(to + second) = x[k][n].z;
+            *reinterpret_cast<uint32_t*>(to + second + 16 * COLS) = x[k][n].w;
+          }
         }
       }
-    };
-    put_states(a.work.s, (head * (a.chunks + 1) + c) * W, at.s);
-    put_states(a.work.ds, chunk * W, at.ds);
-    for (int u = threadIdx.x; u < W * 128; u += kThreads) {
-      const int l = u & 31, n = (u >> 5) & 3, w = u >> 7;
-      const float4 e = a.work.e[chunk * W * 128 + u], z = a.work.dz[chunk * W * 128 + u];
-      const float2 f = *reinterpret_cast<const float2*>(record + Record::beta + (8 * n + 2 * (l & 3)) * 4);
-      const uint32_t r0 = element_at(16 * w + (l >> 2), 8 * n + 2 * (l & 3), 2);
-      const uint32_t r1 = element_at(16 * w + (l >> 2) + 8, 8 * n + 2 * (l & 3), 2);
-      put_pair<NU>(held + at.u + r0, W * 1024, e.x * f.x, e.y * f.y);
-      put_pair<NU>(held + at.u + r1, W * 1024, e.z * f.x, e.w * f.y);
-      put_pair<NU>(held + at.dz + r0, W * 1024, z.x, z.y);
-      put_pair<NU>(held + at.dz + r1, W * 1024, z.z, z.w);
+    for (int u0 = threadIdx.x; u0 < W * 128; u0 += U * kThreads) {
+      float4 e[U], z[U];
+      float2 f[U];
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int u = u0 + n * kThreads;
+        if (u >= W * 128) continue;
+        e[n] = a.work.e[chunk * W * 128 + u];
+        z[n] = a.work.dz[chunk * W * 128 + u];
+        f[n] = *reinterpret_cast<const float2*>(record + Record::beta + (8 * ((u >> 5) & 3) + 2 * (u & 3)) * 4);
+      }
+#pragma unroll
+      for (int n = 0; n < U; ++n) {
+        const int u = u0 + n * kThreads, l = u & 31, col = 8 * ((u >> 5) & 3) + 2 * (l & 3), row = 16 * (u >> 7) + (l >> 2);
+        if (u >= W * 128) continue;
+        const uint32_t r0 = element_at(row, col, 2), r1 = r0 + 512;
+        put_pair<NU>(held + at.u + r0, W * 1024, e[n].x * f[n].x, e[n].y * f[n].y);
+        put_pair<NU>(held + at.u + r1, W * 1024, e[n].z * f[n].x, e[n].w * f[n].y);
+        put_pair<NU>(held + at.dz + r0, W * 1024, z[n].x, z[n].y);
+        put_pair<NU>(held + at.dz + r1, W * 1024, z[n].z, z[n].w);
+      }
     }
     copies_done();
     __syncthreads();
@@ -1239,67 +1292,68 @@ __global__ void __launch_bounds__(256)
       const int blk = is_x ? u - 3 : u, mi = (blk + 1) >> 1, pj = blk >> 1;
       float acc[2][4];
       zero(acc);
-#pragma unroll 2
+      const uint32_t right = next(sh + at.u + right_cols(lane, 2), 0, pj, 2);
+      const uint32_t left = is_x ? next(sh + at.dz + left_cols(lane, 2), 0, mi, 2) : next(sh + at.gy + left_rows(lane, lv), mi, 0, lv);
       for (int s = 0; s < W; ++s) {
         uint32_t y[NU][4];
 #pragma unroll
-        for (int j = 0; j < NU; ++j)
-          load_matrices<true>(y[j], sh + at.u + j * W * 1024 + right_cols(lane, 16 * pj, 16 * s, 2));
+        for (int j = 0; j < NU; ++j) load_matrices<true>(y[j], next(right, s, 0, 2) + j * W * 1024);
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
           uint32_t x[4];
-          if (is_x) load_matrices<true>(x, sh + at.dz + i * W * 1024 + left_cols(lane, 16 * mi, 16 * s, 2));
-          else if (i < IT) load_matrices<false>(x, sh + at.gy + i * plane_v + left_rows(lane, 16 * mi, 16 * s, lv));
-          if (!is_x && i >= IT) continue;
+          if (is_x) load_matrices<true>(x, next(left, s, 0, 2) + i * W * 1024);
+          else if (i < IT) load_matrices<false>(x, next(left, 0, s, lv) + i * plane_v);
+          else continue;
 #pragma unroll
           for (int j = 0; j + i < NU; ++j) multiply(acc[0], x, y[j][0], y[j][1]), multiply(acc[1], x, y[j][2], y[j][3]);
         }
       }
+      uint32_t out[4][NU];   // pairs of rows g and g + 8, of columns 2 t and 8 + 2 t
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const int i = 16 * mi + g + (r >> 1) * 8, j = 16 * pj + 8 * n + 2 * t + (r & 1);
-          float x = i >= j ? acc[n][r] * between(held, i, j) : 0.f;
-          x = is_x ? (i > j ? -x : 0.f) : a.scale * x;
-          unsigned char* tile = held + (is_x ? at.xs : at.da);
-#pragma unroll
-          for (int w = 0; w < NU; ++w) {
-            const __nv_bfloat16 y = __float2bfloat16_rn(x);
-            if (!is_x) *reinterpret_cast<__nv_bfloat16*>(tile + w * kLower + lower_at(i, j)) = y;
-            if (is_x && i >= j) *reinterpret_cast<__nv_bfloat16*>(tile + w * 2048 + element_at(i, j, 2)) = y;
-            if (is_x && i > j) *reinterpret_cast<__nv_bfloat16*>(tile + w * 2048 + element_at(j, i, 2)) = y;
-            x -= __bfloat162float(y);
-          }
+        for (int r = 0; r < 2; ++r) {
+          const int i = 16 * mi + g + 8 * r, j = 16 * pj + 8 * n + 2 * t;
+          float x = i >= j ? acc[n][2 * r] * between(held, i, j) : 0.f;
+          float y = i > j ? acc[n][2 * r + 1] * between(held, i, j + 1) : 0.f;
+          if (is_x) x = i > j ? -x : 0.f, y = i > j + 1 ? -y : 0.f;
+          else x *= a.scale, y *= a.scale;
+          split<NU>(x, y, out[2 * n + r]);
         }
+#pragma unroll
+      for (int w = 0; w < NU; ++w)
+        store_rows(sh + (is_x ? at.x : at.da) + w * kLower + blk * 512 + left_rows(lane, 1), out[0][w], out[1][w],
+                   out[2][w], out[3][w]);
     }
     {
       float aq[2][4], ak[2][4], az[2][4];
       zero(aq), zero(ak), zero(az);
-#pragma unroll 2
+      const uint32_t states = next(sh + at.s + right_cols(lane, lc), 0, p, lc);
+      const uint32_t us = next(sh + at.u + left_cols(lane, 2), 0, m, 2);
+      const uint32_t ys = next(sh + at.gy + left_rows(lane, lv), m, 0, lv);
       for (int s = 0; s < W; ++s) {
         uint32_t bs[NS][4], bd[NS][4];
 #pragma unroll
         for (int j = 0; j < NS; ++j) {
-          const uint32_t to = sh + j * W * 16 * COLS * 2 + right_cols(lane, 16 * p, 16 * s, lc);
-          load_matrices<true>(bs[j], to + at.s);
-          load_matrices<true>(bd[j], to + at.ds);
+          const uint32_t to = next(states, s, 0, lc) + j * W * 16 * COLS * 2;
+          load_matrices<true>(bs[j], to);
+          load_matrices<true>(bd[j], to + at.ds - at.s);
         }
-        const uint32_t to = left_cols(lane, 16 * m, 16 * s, 2);
+        const uint32_t to = next(us, s, 0, 2);
 #pragma unroll
         for (int i = 0; i < NU; ++i) {
           uint32_t x[4];
           if (i < IT) {
-            load_matrices<false>(x, sh + at.gy + i * plane_v + left_rows(lane, 16 * m, 16 * s, lv));
+            load_matrices<false>(x, next(ys, 0, s, lv) + i * plane_v);
 #pragma unroll
             for (int j = 0; j < NS && i + j < NU; ++j)
               multiply(aq[0], x, bs[j][0], bs[j][1]), multiply(aq[1], x, bs[j][2], bs[j][3]);
           }
-          load_matrices<true>(x, sh + at.dz + i * W * 1024 + to);
+          load_matrices<true>(x, to + i * W * 1024 + at.dz - at.u);
 #pragma unroll
           for (int j = 0; j < NS && i + j < NU; ++j)
             multiply(az[0], x, bs[j][0], bs[j][1]), multiply(az[1], x, bs[j][2], bs[j][3]);
-          load_matrices<true>(x, sh + at.u + i * W * 1024 + to);
+          load_matrices<true>(x, to + i * W * 1024);
 #pragma unroll
           for (int j = 0; j < NS && i + j < NU; ++j)
             multiply(ak[0], x, bd[j][0], bd[j][1]), multiply(ak[1], x, bd[j][2], bd[j][3]);
@@ -1322,9 +1376,9 @@ __global__ void __launch_bounds__(256)
       uint32_t bk[IT][4], bq[IT][4];
 #pragma unroll
       for (int j = 0; j < IT; ++j) {
-        const uint32_t to = sh + j * plane + right_cols(lane, 16 * p, 16 * s, lc);
-        load_matrices<true>(bk[j], to + at.k);
-        load_matrices<true>(bq[j], to + at.q);
+        const uint32_t to = next(sh + at.k + right_cols(lane, lc), s, p, lc) + j * plane;
+        load_matrices<true>(bk[j], to);
+        load_matrices<true>(bq[j], to + IT * plane);
       }
       const auto add = [&](float (&acc)[2][4], const uint32_t (&x)[4], const uint32_t (&y)[IT][4], int i) {
 #pragma unroll
@@ -1334,16 +1388,19 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
       for (int i = 0; i < NU; ++i) {
         uint32_t x[4];
+        const uint32_t to = sh + at.da + i * kLower + (m + s) * 512;
         if (s <= m) {
-          load_matrices<false>(x, sh + at.da + i * kLower + (m + s) * 512 + left_rows(lane, 0, 0, 1));
+          load_matrices<false>(x, to + left_rows(lane, 1));
           add(sq, x, bk, i);
+          load_matrices<false>(x, to + at.x - at.da + left_rows(lane, 1));
+          add(sk, x, bk, i);
         }
         if (s >= m) {
-          load_matrices<true>(x, sh + at.da + i * kLower + (m + s) * 512 + left_cols(lane, 0, 0, 1));
+          load_matrices<true>(x, to + left_cols(lane, 1));
           add(sk, x, bq, i);
+          load_matrices<true>(x, to + at.x - at.da + left_cols(lane, 1));
+          add(sk, x, bk, i);
         }
-        load_matrices<false>(x, sh + at.xs + i * 2048 + left_rows(lane, 16 * m, 16 * s, 2));
-        add(sk, x, bk, i);
       }
     }
   }
