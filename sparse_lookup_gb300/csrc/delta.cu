@@ -149,7 +149,7 @@ DeltaArgs delta_args(emb_delta h, int32_t batch, int32_t len, const int32_t* off
   a.offsets = offsets;
   a.state_in = state_in;
   a.work = {h->record, {h->s[0], h->s[1], h->s[2]}, {h->ds[0], h->ds[1], h->ds[2]}, h->e, h->dz, h->sums, h->along,
-            (int64_t)batch * h->heads * a.chunks};
+            h->totals, (int64_t)batch * h->heads * a.chunks};
   return a;
 }
 
@@ -167,6 +167,7 @@ void delta_free(emb_delta h) {
   dev_free(h->dz);
   dev_free(h->sums);
   dev_free(h->along);
+  dev_free(h->totals);
   delete h;
 }
 
@@ -205,6 +206,7 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
     if (e == cudaSuccess) e = dev_alloc((void**)&h->dz, all * chunks * each);
     if (e == cudaSuccess) e = dev_alloc((void**)&h->sums, 3 * W * all * chunks * kChunk * sizeof(float));
     if (e == cudaSuccess) e = dev_alloc((void**)&h->along, W * all * (chunks + 1) * sizeof(float));
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->totals, W * all * chunks * sizeof(float));
   }
   if (e != cudaSuccess) {
     delta_free(h);

@@ -41,7 +41,7 @@ struct emb_delta_s {
   // for the backward
   uint4 *s[3] = {nullptr, nullptr, nullptr}, *ds[3] = {nullptr, nullptr, nullptr};
   float4 *e = nullptr, *dz = nullptr;
-  float *sums = nullptr, *along = nullptr;
+  float *sums = nullptr, *along = nullptr, *totals = nullptr;
 };
 
 namespace emb {
@@ -64,10 +64,11 @@ struct DeltaWork {
   uint4* ds[3];            // [chunks][warps][DK / 16][32]: the gradient of the state after it
   float4 *e, *dz;          // [chunks][warps][4][32]: E and dZ
   float* sums;             // [3][warps][chunks][32]: <grad_y, y>, <grad_v, v> and grad_beta over a warp's channels
-  float* along;            // [chunks + 1][warps]: <dS, S> before a chunk, of every fourth and the last
+  float* along;            // [chunks + 1][warps]: <dS, S> before a chunk, of every kAgain-th and the last
+  float* totals;           // [chunks][warps]: the sum of <grad_y, y> - <grad_v, v> over a chunk
   int64_t chunks;          // batch * heads * chunks of an entry
 };
-constexpr int kAgain = 4;
+constexpr int kAgain = 16;   // chunks between the states whose <dS, S> is taken
 
 struct DeltaArgs {
   int32_t batch, len, heads, share;   // share: value heads of a key head
@@ -222,6 +223,25 @@ __device__ __forceinline__ void left_of(const float (&x)[W][4], int s, uint32_t 
 __device__ __forceinline__ void times(float (&x)[4], const float (&y)[4], float2 f) {
   const float2 a = __fmul2_rn(make_float2(y[0], y[1]), f), b = __fmul2_rn(make_float2(y[2], y[3]), f);
   x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
+}
+
+// Sums over the eight lanes of equal lane % 4 of N values; lane keeps N / 8 of them: of
+// N = 8 value 4 [lane & 16] + 2 [lane & 8] + [lane & 4], of N = 16 twice that and the next.
+template <int N>
+__device__ __forceinline__ void fold(float (&x)[N], int lane) {
+#pragma unroll
+  for (int o = 16, h = N / 2; o >= 4; o >>= 1, h >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float keep = up ? x[i + h] : x[i], give = up ? x[i] : x[i + h];
+      x[i] = keep + __shfl_xor_sync(kFull, give, o);
+    }
+  }
+}
+// The column of accumulators whose sums are value 2 n + r of 8 in that: 8 n + 2 t + r.
+__device__ __forceinline__ int folded_column(int lane) {
+  return ((lane & 16) ? 16 : 0) + ((lane & 8) ? 8 : 0) + 2 * (lane & 3) + ((lane & 4) ? 1 : 0);
 }
 
 template <int W>
@@ -430,10 +450,11 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   constexpr int IT = Shared::IT, lp = Shared::lp, plane = Shared::plane;
   extern __shared__ __align__(128) unsigned char held[];
   const int lane = threadIdx.x & 31, g4 = lane >> 2, t4 = lane & 3;
-  const int64_t job = (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
+  const uint32_t job = blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5);
   if (job >= a.work.chunks) return;
-  const int64_t bh = job / a.chunks;
-  const int c = (int)(job - bh * a.chunks), b = (int)(bh / a.heads), h = (int)(bh % a.heads), hk = h / a.share;
+  const uint32_t bh = job / (uint32_t)a.chunks;
+  const int c = (int)(job - bh * a.chunks), b = (int)(bh / (uint32_t)a.heads), h = (int)(bh - b * (uint32_t)a.heads);
+  const int hk = h / a.share;
   const int len = length_of(a, b), t0 = c * kChunk, live = min(kChunk, len - t0), t = t0 + lane;
   if (live <= 0) return;
   unsigned char* mine = held + (threadIdx.x >> 5) * Shared::bytes;
@@ -494,7 +515,7 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   numbers[Record::g_lo / 4 + lane] = lo;
   __syncwarp();
   float below[2][4];   // N21
-  uint4* out = reinterpret_cast<uint4*>(a.work.record + job * Record::bytes);
+  uint4* out = reinterpret_cast<uint4*>(a.work.record + (int64_t)job * Record::bytes);
   // a block that lies in terms at Shared::block to its place in the record
   const auto put_block = [&](int matrix, int blk) {
     __syncwarp();
@@ -603,11 +624,9 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
 constexpr int kForwardTerms = 3;
 // Terms of the states (and of their gradients) in the products that give the gradients
 // of q and k: as many bits as those have.  A bf16 one rounds the states once, as its own
-// store rounds it.  The states are kept in one more, where <dS, S> is taken.
+// store rounds it.  Where <dS, S> is taken the states are kept in three.
 template <class T>
 constexpr int kStateTerms = std::is_same_v<T, __nv_bfloat16> ? 1 : std::is_same_v<T, __half> ? 2 : 3;
-template <class T>
-constexpr int kKept = kStateTerms<T> < 3 ? kStateTerms<T> + 1 : 3;
 
 enum DeltaMode {
   kForward,   // y and the last state
@@ -621,7 +640,7 @@ struct ForwardStage {
   // V (and grad_y) in terms, rows of dvp channels
   static constexpr int bytes(int dvp) { return v + (MODE == kStates ? 2 : 1) * IT * kChunk * dvp * 2; }
   // a warp's results on their way to rows: 16 bits swizzled, fp32 rows of 17
-  static constexpr int own = MODE == kStates ? 128 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
+  static constexpr int own = MODE == kStates ? 0 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
 };
 
 // Consumer warps first (one for 16 value channels), then the producers.
@@ -678,13 +697,13 @@ __global__ void __launch_bounds__(384)
   const int64_t warps = a.warps, mine = part * consumers + warp;
   const auto keep = [&](int c) {   // the state before chunk c, for the reverse pass
     const int64_t at = ((head * (a.chunks + 1) + c) * warps + mine) * (DK / 16) * 32 + lane;
-    const bool all = kKept<T> == kStateTerms<T> || c % kAgain == 0 || c == chunks;
+    const bool all = c % kAgain == 0 || c == chunks;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
-      uint32_t x[kKept<T>][4];
-      left_of<kKept<T>>(S, s, x);
+      uint32_t x[3][4];
+      left_of<3>(S, s, x);
 #pragma unroll
-      for (int j = 0; j < kKept<T>; ++j)
+      for (int j = 0; j < 3; ++j)
         if (j < kStateTerms<T> || all) a.work.s[j][at + s * 32] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
     }
   };
@@ -749,20 +768,14 @@ __global__ void __launch_bounds__(384)
         [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
     if constexpr (MODE == kStates) {
       // <grad_y, y> over the warp's channels
-      float* sums = reinterpret_cast<float*>(own);
+      float x[8];
       load_turned<IT>(Z, base + Stage::v + IT * plane_v + turned_v, plane_v, lv);
 #pragma unroll
       for (int n = 0; n < 4; ++n)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float x = Y[n][r] * Z[n][r] + Y[n][2 + r] * Z[n][2 + r];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) x += __shfl_xor_sync(kFull, x, o);
-          if (g == 0) sums[8 * n + 2 * t + r] = x;
-        }
-      __syncwarp();
-      a.work.sums[(mine * a.work.chunks + head * a.chunks + c) * kChunk + lane] = sums[lane];
-      __syncwarp();
+        for (int r = 0; r < 2; ++r) x[2 * n + r] = Y[n][r] * Z[n][r] + Y[n][2 + r] * Z[n][2 + r];
+      fold<8>(x, lane);
+      a.work.sums[(mine * a.work.chunks + head * a.chunks + c) * kChunk + folded_column(lane)] = x[0];
     } else {
       const bool there = t0 + lane < a.len, on = lane < live;   // dead positions of the chunk too: 0
       T* to = y.data + b * y.batch + (int64_t)(t0 + lane) * y.time + h * y.head + e0;
@@ -863,14 +876,14 @@ __global__ void __launch_bounds__(384)
 // Decays: y and S1 are homogeneous in (S0, V), so dG_i = dY_i . Y_i - dV_i . V_i, and the
 // gradient of g_t is their sum from t to the chunk's end and <dS, S1> there.  That number
 // is the same sum over the chunks up to the next one where it is taken from the states:
-// every fourth, before roundings add up.
+// every sixteenth, before roundings add up.
 
 template <class T, int DK>
 struct ReverseStage {
   static constexpr int NR = 3, IT = Terms<T>::of(NR), lp = log_of(DK / 8), plane = kChunk * DK * 2;
   static constexpr int record = 0, k = (Record::bytes + 255) / 256 * 256, q = k + IT * plane, gy = q + IT * plane;
   static constexpr int bytes(int dvp) { return gy + 2 * IT * kChunk * dvp * 2; }   // grad_y and V
-  static constexpr int own = sizeof(T) == 2 ? 1024 : 256;   // dV on its way to rows; sums
+  static constexpr int own = sizeof(T) == 2 ? 1024 : 0;   // dV on its way to rows
 };
 
 template <class T, int DK>
@@ -926,14 +939,14 @@ __global__ void __launch_bounds__(384)
     float x = 0.f;
 #pragma unroll
     for (int s = 0; s < DK / 16; ++s) {
-      uint4 u[kKept<T>];
+      uint4 u[3];
 #pragma unroll
-      for (int j = 0; j < kKept<T>; ++j) u[j] = a.work.s[j][from + s * 32];
+      for (int j = 0; j < 3; ++j) u[j] = a.work.s[j][from + s * 32];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        float2 f = unpack(word(u[kKept<T> - 1], i));
+        float2 f = unpack(word(u[2], i));
 #pragma unroll
-        for (int j = kKept<T> - 2; j >= 0; --j) {
+        for (int j = 1; j >= 0; --j) {
           const float2 w = unpack(word(u[j], i));
           f.x += w.x, f.y += w.y;
         }
@@ -956,6 +969,7 @@ __global__ void __launch_bounds__(384)
     float4 e[4];   // E, from the states' pass
 #pragma unroll
     for (int n = 0; n < 4; ++n) e[n] = a.work.e[(at_c * 4 + n) * 32 + lane];
+    const float dots = a.work.sums[(mine * a.work.chunks + chunk) * kChunk + folded_column(lane)];
     meet(1 + stage, meeting);
     float dU[4][4], dZ[4][4], X[4][4];
     zero(dU);
@@ -1010,26 +1024,24 @@ __global__ void __launch_bounds__(384)
     {
       float V[4][4];
       load_turned<IT>(V, base + Stage::gy + IT * plane_v + turned_v, plane_v, lv);
-      float* sums = reinterpret_cast<float*>(own);
+      float x[16];   // of a column: <grad_v, v>, grad_beta
 #pragma unroll
       for (int n = 0; n < 4; ++n) {
         const float E[4] = {e[n].x, e[n].y, e[n].z, e[n].w};
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float x = E[r] * (dU[n][r] - X[n][r]) + E[2 + r] * (dU[n][2 + r] - X[n][2 + r]);
-          float y = dZ[n][r] * V[n][r] + dZ[n][2 + r] * V[n][2 + r];
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            x += __shfl_xor_sync(kFull, x, o);
-            y += __shfl_xor_sync(kFull, y, o);
-          }
-          if (g == 0) sums[8 * n + 2 * t + r] = y, sums[32 + 8 * n + 2 * t + r] = x;
+          x[4 * n + 2 * r] = dZ[n][r] * V[n][r] + dZ[n][2 + r] * V[n][2 + r];
+          x[4 * n + 2 * r + 1] = E[r] * (dU[n][r] - X[n][r]) + E[2 + r] * (dU[n][2 + r] - X[n][2 + r]);
         }
       }
-      __syncwarp();
-      a.work.sums[((warps + mine) * a.work.chunks + chunk) * kChunk + lane] = sums[lane];
-      a.work.sums[((2 * warps + mine) * a.work.chunks + chunk) * kChunk + lane] = sums[32 + lane];
-      __syncwarp();
+      fold<16>(x, lane);
+      const int i = folded_column(lane);
+      a.work.sums[((warps + mine) * a.work.chunks + chunk) * kChunk + i] = x[0];
+      a.work.sums[((2 * warps + mine) * a.work.chunks + chunk) * kChunk + i] = x[1];
+      float total = dots - x[0];   // a column each
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kFull, total, o);
+      if (lane == 0) a.work.totals[at_c] = total;
     }
     // dV
     if constexpr (sizeof(T) == 2) {
@@ -1138,9 +1150,9 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
   const int W = a.warps, lv = W == 1 ? 1 : 32 - __clz(2 * W - 1), plane_v = (kChunk * 16) << lv;
   const Shared at(W, 8 << lv);
   const int J = a.heads / a.share;
-  const int64_t job = blockIdx.x / (DK / COLS);
+  const uint32_t job = blockIdx.x / (DK / COLS), bj = job / (uint32_t)a.chunks;
   const int col0 = (int)(blockIdx.x % (DK / COLS)) * COLS;
-  const int c = (int)(job % a.chunks), b = (int)(job / a.chunks / J), hk = (int)(job / a.chunks % J);
+  const int c = (int)(job - bj * a.chunks), b = (int)(bj / (uint32_t)J), hk = (int)(bj - b * (uint32_t)J);
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk, t0 = c * kChunk;
   const int live = min(kChunk, len - t0), there = min(kChunk, a.len - t0);
   if (live <= 0) {   // past the entry's end
@@ -1265,10 +1277,7 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
       }
       const int known = min(chunks, (c / kAgain + 1) * kAgain);
       float carry = 0.f;
-      for (int n = c + 1; n < known; ++n)
-        for (int w = 0; w < W; ++w)
-          carry += a.work.sums[(w * a.work.chunks + head * a.chunks + n) * kChunk + lane] -
-                   a.work.sums[((W + w) * a.work.chunks + head * a.chunks + n) * kChunk + lane];
+      for (int n = (c + 1) * W + lane; n < known * W; n += 32) carry += a.work.totals[head * a.chunks * W + n];
       if (lane < W) carry += a.work.along[(head * (a.chunks + 1) + known) * W + lane];
       for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
 #pragma unroll
