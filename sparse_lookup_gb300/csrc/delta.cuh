@@ -390,6 +390,30 @@ __device__ __forceinline__ void load_turned(float (&x)[4][4], uint32_t at, int p
   }
 }
 
+// 16 channels, e0 on, of 32 rows (`there` of them in the array, the live ones not 0) from a
+// swizzled tile of 16-bit elements: two lanes a row, so that its 32 bytes leave together.
+template <class T>
+__device__ __forceinline__ void store_turned(const unsigned char* tile, T* rows, int64_t stride, int e0, int dim,
+                                             int there, int live, bool wide, int lane) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int r = 16 * u + (lane >> 1), e = e0 + 8 * (lane & 1);
+    if (r >= there) continue;
+    Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(tile + piece(r, lane & 1, 1)));
+    if (r >= live)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.e[i] = from_f32<T>(0.f);
+    T* to = rows + r * stride + e;
+    if (wide && e + 8 <= dim) {
+      store_vec(to, o);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (e + i < dim) to[i] = o.e[i];
+    }
+  }
+}
+
 __device__ __forceinline__ void copy_record(unsigned char* to, const unsigned char* from, int bytes, int lane) {
   const uint32_t at = smem_of(to);
 #pragma unroll 4
@@ -777,8 +801,7 @@ __global__ void __launch_bounds__(384)
       fold<8>(x, lane);
       a.work.sums[(mine * a.work.chunks + head * a.chunks + c) * kChunk + folded_column(lane)] = x[0];
     } else {
-      const bool there = t0 + lane < a.len, on = lane < live;   // dead positions of the chunk too: 0
-      T* to = y.data + b * y.batch + (int64_t)(t0 + lane) * y.time + h * y.head + e0;
+      // dead positions of the chunk too: 0
       if constexpr (sizeof(T) == 2) {
         const auto both = [](float lo, float hi) {
           Vec<T, 2> o;
@@ -791,21 +814,8 @@ __global__ void __launch_bounds__(384)
                          both(Y[2 * s][2], Y[2 * s][3]), both(Y[2 * s + 1][0], Y[2 * s + 1][1]),
                          both(Y[2 * s + 1][2], Y[2 * s + 1][3]));
         __syncwarp();
-        if (there) {
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(own + piece(lane, u, 1)));
-#pragma unroll
-            for (int i = 0; i < 8; ++i) o.e[i] = on ? o.e[i] : from_f32<T>(0.f);
-            if (a.wide_y && e0 + 8 * u + 8 <= a.value_dim) {
-              store_vec(to + 8 * u, o);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (e0 + 8 * u + i < a.value_dim) to[8 * u + i] = o.e[i];
-            }
-          }
-        }
+        store_turned(own, y.data + b * y.batch + (int64_t)t0 * y.time + h * y.head, y.time, e0, a.value_dim,
+                     min(kChunk, a.len - t0), live, a.wide_y, lane);
       } else {
         float* turned = reinterpret_cast<float*>(own);
 #pragma unroll
@@ -813,7 +823,9 @@ __global__ void __launch_bounds__(384)
 #pragma unroll
           for (int r = 0; r < 4; ++r) turned[(8 * n + 2 * t + (r & 1)) * 17 + g + (r >> 1) * 8] = Y[n][r];
         __syncwarp();
-        if (there) {
+        if (t0 + lane < a.len) {
+          const bool on = lane < live;
+          T* to = y.data + b * y.batch + (int64_t)(t0 + lane) * y.time + h * y.head + e0;
           const float* from = turned + lane * 17;
           if (a.wide_y && e0 + 16 <= a.value_dim) {
 #pragma unroll
@@ -1056,22 +1068,8 @@ __global__ void __launch_bounds__(384)
                        both(dZ[2 * s][2], dZ[2 * s][3]), both(dZ[2 * s + 1][0], dZ[2 * s + 1][1]),
                        both(dZ[2 * s + 1][2], dZ[2 * s + 1][3]));
       __syncwarp();
-      if (t0 + lane < a.len) {
-        T* to = gv.data + b * gv.batch + (int64_t)(t0 + lane) * gv.time + h * gv.head + e0;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          Vec<T, 8> o = load_vec<T, 8>(reinterpret_cast<const T*>(own + piece(lane, u, 1)));
-#pragma unroll
-          for (int i = 0; i < 8; ++i) o.e[i] = lane < live ? o.e[i] : from_f32<T>(0.f);
-          if (a.wide_y && e0 + 8 * u + 8 <= a.value_dim) {
-            store_vec(to + 8 * u, o);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              if (e0 + 8 * u + i < a.value_dim) to[8 * u + i] = o.e[i];
-          }
-        }
-      }
+      store_turned(own, gv.data + b * gv.batch + (int64_t)t0 * gv.time + h * gv.head, gv.time, e0, a.value_dim,
+                   min(kChunk, a.len - t0), live, a.wide_y, lane);
       __syncwarp();
     } else {
 #pragma unroll

@@ -7,7 +7,8 @@ namespace emb {
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateCtas = 4;      // CTAs on an SM that sum columns
-constexpr int kSumRows = 16;      // CTAs' rows that the last reduction takes side by side
+constexpr int kSumCols = 8;       // experts of a CTA of the last reduction
+constexpr int kSumRows = 64;      // CTAs' rows that it takes side by side
 
 // What the CTAs of one call leave for the reduction.
 struct GateSums {
@@ -15,7 +16,7 @@ struct GateSums {
   uint32_t* chosen;  // [CTAs][E]
   double* z;         // [CTAs] sums of lse^2
   uint32_t* live;    // [CTAs]
-  double* share;     // [E / 32] sums of counts * p of 32 experts
+  double* share;     // [E / kSumCols] sums of counts * p of so many experts
   uint32_t* done;    // reducing CTAs that are through: 0 between calls
 };
 
@@ -82,7 +83,7 @@ __device__ __forceinline__ void write_losses(const GateArgs& a, double share, do
 // every token pays.  Column sums of the probabilities stay in registers too, and
 // leave as one row a CTA.  ONE: a single CTA, which writes the losses itself.
 template <class T, int V, int M, bool ONE>
-__global__ void __launch_bounds__(kGateThreads) k_gate(GateArgs a, const T* __restrict__ logits, int glog) {
+__global__ void __launch_bounds__(kGateThreads, M <= 16 ? 3 : 1) k_gate(GateArgs a, const T* __restrict__ logits, int glog) {
   extern __shared__ float held[];   // [warps][E] probabilities; [E] choices
   __shared__ double zs[kGateWarps];
   __shared__ uint32_t ns[kGateWarps];
@@ -214,14 +215,15 @@ __global__ void __launch_bounds__(kGateThreads) k_gate(GateArgs a, const T* __re
   }
 }
 
-// The CTAs' sums, 32 experts a CTA; the last one through adds up the parts, in
+// The CTAs' sums, kSumCols experts a CTA; the last one through adds up the parts, in
 // their order.
-__global__ void __launch_bounds__(32 * kSumRows) k_gate_sum(GateArgs a, int ctas) {
-  __shared__ float ps[kSumRows][33];
-  __shared__ uint32_t cs[kSumRows][33];
+__global__ void __launch_bounds__(kSumCols* kSumRows) k_gate_sum(GateArgs a, int ctas) {
+  __shared__ float ps[kSumRows][kSumCols + 1];
+  __shared__ uint32_t cs[kSumRows][kSumCols + 1];
   __shared__ uint32_t last;
   pdl_wait();
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5, e = blockIdx.x * 32 + lane, E = a.n_experts;
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols, e = blockIdx.x * kSumCols + col;
+  const int E = a.n_experts, lane = threadIdx.x & 31;
   float p = 0.f;
   uint32_t c = 0;
   if (e < E)
@@ -230,13 +232,19 @@ __global__ void __launch_bounds__(32 * kSumRows) k_gate_sum(GateArgs a, int ctas
       p += a.sums.p[(int64_t)i * E + e];
       c += a.sums.chosen[(int64_t)i * E + e];
     }
-  ps[row][lane] = p, cs[row][lane] = c;
+  ps[row][col] = p, cs[row][col] = c;
   __syncthreads();
-  if (row) return;
-  for (int i = 1; i < kSumRows; ++i) p += ps[i][lane], c += cs[i][lane];
-  if (e < E) a.counts[e] = (int32_t)c;
+  if (threadIdx.x >= 32) return;
+  // four lanes an expert
+  p = 0.f, c = 0;
+  for (int i = lane / kSumCols; i < kSumRows; i += 32 / kSumCols) p += ps[i][col], c += cs[i][col];
+  for (int o = kSumCols; o < 32; o <<= 1) {
+    p += __shfl_xor_sync(kFull, p, o);
+    c += __shfl_xor_sync(kFull, c, o);
+  }
+  if (e < E && lane < kSumCols) a.counts[e] = (int32_t)c;
   double share = (double)c * p;
-  for (int o = 16; o > 0; o >>= 1) share += __shfl_xor_sync(kFull, share, o);
+  for (int o = kSumCols / 2; o > 0; o >>= 1) share += __shfl_xor_sync(kFull, share, o);
   if (lane == 0) {
     a.sums.share[blockIdx.x] = share;
     __threadfence();
@@ -342,7 +350,7 @@ GateSums sums_at(void* gate, int sm_count, int n_experts) {
   GateSums s;
   s.z = (double*)gate;
   s.share = s.z + ctas;
-  s.p = (float*)(s.share + (E + 31) / 32);
+  s.p = (float*)(s.share + (E + kSumCols - 1) / kSumCols);
   s.chosen = (uint32_t*)(s.p + ctas * E);
   s.live = s.chosen + ctas * E;
   s.done = s.live + ctas;
@@ -425,7 +433,8 @@ extern "C" emb_status moe_gate(emb_moe h, int64_t n, int32_t dtype, const void* 
     kernel<<<ctas, kGateThreads, smem, s>>>(a, (const T*)logits, glog);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || ctas == 1) return e;
-    return launch_dependent(k_gate_sum, (unsigned)((E + 31) / 32), 32 * kSumRows, 0, s, a, (int)ctas);
+    return launch_dependent(k_gate_sum, (unsigned)((E + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, s, a,
+                            (int)ctas);
   }));
 }
 

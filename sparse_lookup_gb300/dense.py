@@ -610,17 +610,18 @@ class Gate:
     live_count  [1] int32
     normalize   whether the weights are a softmax over the choices alone"""
 
-    __slots__ = ("_arrays", "_shape", "normalize")
+    __slots__ = ("_arrays", "_at", "_shape", "normalize")
 
-    def __init__(self, arrays, shape, normalize):
-        self._arrays, self._shape, self.normalize = arrays, shape, normalize
+    def __init__(self, arrays, at, shape, normalize):
+        self._arrays, self._at, self._shape, self.normalize = arrays, at, shape, normalize
 
+    # not to be replaced: the calls use the addresses found when it was made
     experts = property(lambda self: self._arrays[0])
     weights = property(lambda self: self._arrays[1])
     counts = property(lambda self: self._arrays[2])
     losses = property(lambda self: self._arrays[3])
-    stats = property(lambda self: self._arrays[4])
-    live_count = property(lambda self: self._arrays[5])
+    stats = property(lambda self: self._arrays[4][:2 * self._shape[0]].view(-1, 2))
+    live_count = property(lambda self: self._arrays[4][2 * self._shape[0]:].view(self._arrays[0].dtype))
 
 
 class ExpertRouter(_Handle):
@@ -653,20 +654,19 @@ class ExpertRouter(_Handle):
         if len(shape) != 2 or shape[1] != E:
             raise ValueError("logits: [tokens, %d] expected, got %s" % (E, tuple(shape)))
         n, dt = shape[0], logits.dtype
-        at = self._want(logits, "logits", shape, dt, False)
+        x = self._want(logits, "logits", shape, dt, False)
         on = None if live is None else self._want(live, "live", (n,), self._t.bool)
-        # one allocation each of the arrays that grow with the batch and of the others
-        each = self._empty((2 * n * (K + 1),), f32, logits, stream)
-        rest = self._empty((E + 3,), i32, logits, stream)
-        stats, experts = each[:2 * n].view(n, 2), each[2 * n:n * (K + 2)].view(i32).view(n, K)
-        weights = each[n * (K + 2):].view(n, K)
-        counts, losses, count = rest[:E], rest[E:E + 2].view(f32), rest[E + 2:]
-        p, q = each.data_ptr(), rest.data_ptr()
-        st = self._gate(self.handle, n, _element(dt), at, logits.stride(0), on, normalize, p + 8 * n,
-                        p + 4 * n * (K + 2), q, q + 4 * E, p, q + 4 * (E + 2), self._at(stream))
+        s = self._at(stream)
+        experts, weights = self._empty((n, K), i32, logits, stream), self._empty((n, K), f32, logits, stream)
+        counts, losses = self._empty((E,), i32, logits, stream), self._empty((2,), f32, logits, stream)
+        stats = self._empty((2 * n + 1,), f32, logits, stream)      # and the live count
+        p = stats.data_ptr()
+        at = (experts.data_ptr(), weights.data_ptr(), counts.data_ptr(), p, p + 8 * n)
+        st = self._gate(self.handle, n, _element(dt), x, logits.stride(0), on, normalize, at[0], at[1], at[2],
+                        losses.data_ptr(), p, at[4], s)
         if st:
             _check(st, "moe_gate")
-        return Gate((experts, weights, counts, losses, stats, count), (n, K, E, self._device), bool(normalize))
+        return Gate((experts, weights, counts, losses, stats), at, (n, K, E, self._device), bool(normalize))
 
     def gate_backward(self, logits, gate, grad_weights=None, grad_losses=None, grad_logits=None, stream=None):
         """Gradient of gate()'s logits from those of its weights [tokens, top_k]
@@ -681,10 +681,8 @@ class ExpertRouter(_Handle):
         if grad_logits is None:
             grad_logits = self._empty(shape, dt, logits, stream)
         to = self._want(grad_logits, "grad_logits", shape, dt, False)
-        experts, weights, counts, _, stats, count = gate._arrays
-        st = self._gate_backward(self.handle, n, _element(dt), at, logits.stride(0), gate.normalize,
-                                 experts.data_ptr(), weights.data_ptr(), counts.data_ptr(), stats.data_ptr(),
-                                 count.data_ptr(), gw, gl, to, grad_logits.stride(0), self._at(stream))
+        st = self._gate_backward(self.handle, n, _element(dt), at, logits.stride(0), gate.normalize, *gate._at, gw, gl,
+                                 to, grad_logits.stride(0), self._at(stream))
         if st:
             _check(st, "moe_gate_backward")
         return grad_logits

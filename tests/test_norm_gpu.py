@@ -156,14 +156,14 @@ def test_strided_views_and_given_outputs():
         v = wide[:, 1:9, first:first + 64]
         out = torch.full((6, 8, 130), 7.0, device="cuda", dtype=torch.bfloat16)
         plan = sl.LayerNorm(64)
-        want, stats = plan.forward(v.contiguous(), w, b)
-        got, _ = plan.forward(v, w, b, y=out[..., 1:65])
-        assert torch.equal(got, want) and (out[..., 65:] == 7).all() and (out[..., 0] == 7).all()
-        g1 = plan.backward(v, dy[:, :8], stats, w)
-        g2 = plan.backward(v.contiguous(), dy[:, :8].contiguous(), stats, w)
-        assert torch.equal(g1[0], g2[0])
-        for p, q in zip(g1[1:], g2[1:]):
-            assert (p - q).abs().max() <= 1e-4
+        # the accesses' width decides the order of a row's sums: against the formulas, not against each other
+        got, stats = plan.forward(v, w, b, y=out[..., 1:65])
+        want, tol = reference(v, dy[:, :8], w, b, plan.eps)
+        grads = plan.backward(v, dy[:, :8], stats, w)
+        for name, p, q, t, kind in zip(("y", "grad_x", "grad_weight", "grad_bias"), (got, *grads), want, tol,
+                                       ("bfloat16", "bfloat16", "float32", "float32")):
+            check(p, q, t, kind, name)
+        assert (out[..., 65:] == 7).all() and (out[..., 0] == 7).all()
     rows = x[:, 4]                      # rows with a stride of their own
     want, _ = sl.LayerNorm(64).forward(rows.contiguous(), w, b)
     assert torch.equal(sl.LayerNorm(64).forward(rows, w, b)[0], want)
