@@ -149,7 +149,7 @@ DeltaArgs delta_args(emb_delta h, int32_t batch, int32_t len, const int32_t* off
   a.offsets = offsets;
   a.state_in = state_in;
   a.work = {h->record, {h->s[0], h->s[1], h->s[2]}, {h->ds[0], h->ds[1], h->ds[2]}, h->e, h->dz, h->sums, h->along,
-            h->totals, (int64_t)batch * h->heads * a.chunks};
+            h->totals, (int64_t)batch * h->heads * a.chunks, h->effect, h->between};
   return a;
 }
 
@@ -168,6 +168,8 @@ void delta_free(emb_delta h) {
   dev_free(h->sums);
   dev_free(h->along);
   dev_free(h->totals);
+  dev_free(h->effect);
+  dev_free(h->between);
   delete h;
 }
 
@@ -195,8 +197,14 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   const int64_t all = (int64_t)max_batch * heads, chunks = ((int64_t)max_len + kChunk - 1) / kChunk;
   if (e == cudaSuccess) e = dev_alloc((void**)&h->record, all * chunks * Record::bytes);
+  const int64_t W = (value_dim + 15) / 16, dk = dk_of(key_dim);
+  if (chunks >= kLeastChunks && e == cudaSuccess) {
+    // calls of a few heads are cut into segments, one an SM: an effect forward and one backward
+    h->max_pairs = h->sm_count;
+    e = dev_alloc((void**)&h->effect, h->max_pairs * (2 * W * 16 + dk) * dk * sizeof(float));
+    if (e == cudaSuccess) e = dev_alloc((void**)&h->between, h->max_pairs * W * 16 * dk * sizeof(float));
+  }
   if (training) {
-    const int64_t W = (value_dim + 15) / 16, dk = dk_of(key_dim);
     const int64_t state = W * (dk / 16) * 32 * sizeof(uint4), each = W * 4 * 32 * sizeof(float4);
     for (uint4*& p : h->s)
       if (e == cudaSuccess) e = dev_alloc((void**)&p, all * (chunks + 1) * state);

@@ -42,11 +42,15 @@ struct emb_delta_s {
   uint4 *s[3] = {nullptr, nullptr, nullptr}, *ds[3] = {nullptr, nullptr, nullptr};
   float4 *e = nullptr, *dz = nullptr;
   float *sums = nullptr, *along = nullptr, *totals = nullptr;
+  // for sequences in segments
+  float *effect = nullptr, *between = nullptr;
+  int64_t max_pairs = 0;
 };
 
 namespace emb {
 
 constexpr int kChunk = 32;
+constexpr int kLeastChunks = 64;   // of a sequence that is cut into segments
 
 // A [batch, time, heads, dim] array (or [batch, time, heads]).
 template <class T>
@@ -67,6 +71,9 @@ struct DeltaWork {
   float* along;            // [chunks + 1][warps]: <dS, S> before a chunk, of every kAgain-th and the last
   float* totals;           // [chunks][warps]: the sum of <grad_y, y> - <grad_v, v> over a chunk
   int64_t chunks;          // batch * heads * chunks of an entry
+  // [batch * heads * segments][channels][DK] floats: what a segment makes of a zero state and of
+  // the identity; the state before a segment (its gradient after it)
+  float *effect, *between;
 };
 constexpr int kAgain = 16;   // chunks between the states whose <dS, S> is taken
 
@@ -76,6 +83,7 @@ struct DeltaArgs {
   int32_t chunks;                     // of an entry: (len + 31) / 32
   int32_t parts;                      // CTAs that share an (entry, head)'s value channels
   int32_t warps;                      // of 16 value channels, of all parts
+  int32_t segments, span;             // of a sequence, and chunks of one
   float scale;
   const int32_t* offsets;
   const float *state_in, *grad_last;
@@ -655,6 +663,7 @@ constexpr int kStateTerms = std::is_same_v<T, __nv_bfloat16> ? 1 : std::is_same_
 enum DeltaMode {
   kForward,   // y and the last state
   kStates,    // what the reverse pass needs (DeltaWork)
+  kEffect,    // what a segment makes of a zero state (value channels) and of the identity (key_dim channels more)
 };
 
 template <class T, int DK, DeltaMode MODE>
@@ -664,7 +673,7 @@ struct ForwardStage {
   // V (and grad_y) in terms, rows of dvp channels
   static constexpr int bytes(int dvp) { return v + (MODE == kStates ? 2 : 1) * IT * kChunk * dvp * 2; }
   // a warp's results on their way to rows: 16 bits swizzled, fp32 rows of 17
-  static constexpr int own = MODE == kStates ? 0 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
+  static constexpr int own = MODE != kForward ? 0 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
 };
 
 // Consumer warps first (one for 16 value channels), then the producers.
@@ -682,20 +691,24 @@ __global__ void __launch_bounds__(384)
   const int consumers = (blockDim.x >> 5) - producers, meeting = 32 * (consumers + 1);
   const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
   const int size = Stage::bytes(8 << lv);
-  const int part = blockIdx.x % a.parts, bh = blockIdx.x / a.parts, b = bh / a.heads, h = bh % a.heads;
-  const int hk = h / a.share, first_v = part * 16 * consumers;
+  const int part = blockIdx.x % a.parts, pair = blockIdx.x / a.parts, seg = pair % a.segments, bh = pair / a.segments;
+  const int b = bh / a.heads, h = bh % a.heads, hk = h / a.share, first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
+  // this segment's chunks; the last one that has any ends the sequence
+  const int first = min(chunks, seg * a.span), end = min(chunks, first + a.span);
+  const bool ends = seg == (chunks ? (chunks - 1) / a.span : 0);
   const int64_t head = (int64_t)b * a.heads + h;
   if (warp >= consumers) {
-    const int p = warp - consumers, cols_v = min(16 * consumers, a.value_dim - first_v);
+    const int p = warp - consumers, cols_v = max(0, min(16 * consumers, a.value_dim - first_v));
     unsigned char* st = held + p * size;
-    for (int c = p; c < chunks; c += producers) {
-      if (c >= producers) meet(1 + producers + p, meeting);
+    for (int c = first + p; c < end; c += producers) {
+      if (c >= first + producers) meet(1 + producers + p, meeting);
       const int t0 = c * kChunk, live = min(kChunk, len - t0);
       copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::forward_bytes, lane);
       load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
                         a.key_dim, a.wide_qk, lane);
-      load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
+      if constexpr (MODE != kEffect)
+        load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
                         a.key_dim, a.wide_qk, lane);
       load_terms<T, IT>(st + Stage::v, plane_v, lv, v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time,
                         live, cols_v, a.wide_v, lane);
@@ -715,8 +728,13 @@ __global__ void __launch_bounds__(384)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-      S[n][r] = a.state_in && d < a.key_dim && e < a.value_dim
-                    ? a.state_in[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
+      if constexpr (MODE == kEffect)
+        S[n][r] = e - 16 * a.warps == d ? 1.f : 0.f;
+      else if (seg)
+        S[n][r] = first < end ? a.work.between[((int64_t)pair * a.warps * 16 + e) * DK + d] : 0.f;
+      else
+        S[n][r] = a.state_in && d < a.key_dim && e < a.value_dim
+                      ? a.state_in[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
     }
   const int64_t warps = a.warps, mine = part * consumers + warp;
   const auto keep = [&](int c) {   // the state before chunk c, for the reverse pass
@@ -735,7 +753,7 @@ __global__ void __launch_bounds__(384)
   const uint32_t rows = right_rows(lane, lp), cols = right_cols(lane, lp);
   const uint32_t turned_v = next(left_cols(lane, lv), 0, warp, lv), low = right_rows(lane, 1);
   int stage = 0;
-  for (int c = 0; c < chunks; ++c) {
+  for (int c = first; c < end; ++c) {
     unsigned char* st = held + stage * size;
     const uint32_t base = smem_of(st);
     if constexpr (MODE == kStates) keep(c);
@@ -755,11 +773,11 @@ __global__ void __launch_bounds__(384)
           uint32_t u[4], w[4];
           const uint32_t at = next(base + Stage::k + rows, p, s, lp) + j * plane;
           load_matrices<false>(u, at);
-          load_matrices<false>(w, at + IT * plane);
+          if constexpr (MODE != kEffect) load_matrices<false>(w, at + IT * plane);
 #pragma unroll
           for (int i = 0; i < NT; ++i) {
             if (i + j < NT) multiply(Z[2 * p], x[i], u[0], u[1]), multiply(Z[2 * p + 1], x[i], u[2], u[3]);
-            if (i + j < NO) multiply(Y[2 * p], x[i], w[0], w[1]), multiply(Y[2 * p + 1], x[i], w[2], w[3]);
+            if (MODE != kEffect && i + j < NO) multiply(Y[2 * p], x[i], w[0], w[1]), multiply(Y[2 * p + 1], x[i], w[2], w[3]);
           }
         }
     }
@@ -787,7 +805,7 @@ __global__ void __launch_bounds__(384)
     }
 #pragma unroll
     for (int n = 0; n < 4; ++n) times(E[n], E[n], pair_at(st, Record::beta, n, t));   // U
-    product<2, 2, NO, NO, NO, false, 1>(
+    if constexpr (MODE != kEffect) product<2, 2, NO, NO, NO, false, 1>(
         Y, [&](int s, uint32_t (&x)[NO][4]) { left_of<NO>(E, s, x); },
         [&](int p, int s, int j) { return lower(Record::a, p, s, j); });
     if constexpr (MODE == kStates) {
@@ -800,7 +818,7 @@ __global__ void __launch_bounds__(384)
         for (int r = 0; r < 2; ++r) x[2 * n + r] = Y[n][r] * Z[n][r] + Y[n][2 + r] * Z[n][2 + r];
       fold<8>(x, lane);
       a.work.sums[(mine * a.work.chunks + head * a.chunks + c) * kChunk + folded_column(lane)] = x[0];
-    } else {
+    } else if constexpr (MODE == kForward) {
       // dead positions of the chunk too: 0
       if constexpr (sizeof(T) == 2) {
         const auto both = [](float lo, float hi) {
@@ -851,12 +869,21 @@ __global__ void __launch_bounds__(384)
     product<2, DK / 16, NT, IT, NT, true, 0>(
         S, [&](int s, uint32_t (&x)[NT][4]) { left_of<NT>(E, s, x); },
         [&](int p, int s, int j) { return next(base + Stage::k + cols, s, p, lp) + j * plane; });
-    if (c + producers < chunks) arrive(1 + producers + stage, meeting);
+    if (c + producers < end) arrive(1 + producers + stage, meeting);
     stage = stage + 1 == producers ? 0 : stage + 1;
   }
-  if constexpr (MODE == kStates) keep(chunks);
+  if constexpr (MODE == kEffect) {
+    float* out = a.work.effect + ((int64_t)pair * (a.warps * 16 + DK) + e0 + g) * DK + 2 * t;
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n) {
+      *reinterpret_cast<float2*>(out + 8 * n) = make_float2(S[n][0], S[n][1]);
+      *reinterpret_cast<float2*>(out + 8 * DK + 8 * n) = make_float2(S[n][2], S[n][3]);
+    }
+  }
+  if constexpr (MODE == kStates)
+    if (ends) keep(chunks);
   if constexpr (MODE == kForward) {
-    if (a.state_out)
+    if (ends && a.state_out)
 #pragma unroll
       for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
@@ -864,10 +891,83 @@ __global__ void __launch_bounds__(384)
           const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
           if (d < a.key_dim && e < a.value_dim) a.state_out[(head * a.key_dim + d) * a.value_dim + e] = S[n][r];
         }
-    // positions past the last chunk
-    for (int64_t i = (int64_t)chunks * kChunk + (lane >> 4); i < a.len; i += 2)
+    // positions past the last chunk, of this segment
+    const int64_t from = (int64_t)kChunk * max(chunks, seg * a.span);
+    const int64_t to = min((int64_t)a.len, (int64_t)kChunk * a.span * (seg + 1));
+    for (int64_t i = from + (lane >> 4); i < to; i += 2)
       if (e0 + (lane & 15) < a.value_dim)
         y.data[b * y.batch + i * y.time + h * y.head + e0 + (lane & 15)] = from_f32<T>(0.f);
+  }
+}
+
+// From segment to segment: S^T (rows are value channels) before each from what the one
+// before makes of a state, S^T_p+1 = S^T_p M_p^T + N_p^T, with M^T and N^T as k_delta_fwd left them; or
+// the gradients after each, dS^T_p-1 = dS^T_p M_p + N'_p^T.  A CTA has kChainRows rows; the
+// next segment's M^T comes while this one's is used.
+constexpr int kChainRows = 8;
+template <int DK, bool REVERSE>
+__global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs a) {
+  constexpr int G = 256 / DK, R = kChainRows / G > 0 ? kChainRows / G : 1, V = DK * DK / 1024;
+  static_assert(G * R == kChainRows, "");
+  extern __shared__ float chain[];
+  float* m = chain;                      // [DK][DK + 1] M^T
+  float* x = chain + DK * (DK + 1);      // [kChainRows][DK + 4]
+  const int blocks = a.warps * 16 / kChainRows, rows0 = blockIdx.x % blocks * kChainRows, bh = blockIdx.x / blocks;
+  const int b = bh / a.heads, len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
+  const int last = chunks ? (chunks - 1) / a.span : 0, d = threadIdx.x % DK, r0 = threadIdx.x / DK * R;
+  const float* given = REVERSE ? a.grad_last : a.state_in;
+  // M^T follows N^T in a segment's effect of the forward; N'^T lies in another array of N^T's size
+  const int64_t all = (int64_t)(a.warps * 16 + DK) * DK, some = (int64_t)a.warps * 16 * DK;
+  const float* reversed = a.work.effect + (int64_t)a.batch * a.heads * a.segments * all;
+  const auto matrix = [&](int p) {
+    return reinterpret_cast<const float4*>(a.work.effect + ((int64_t)bh * a.segments + p) * all + some);
+  };
+  float4 next_m[V];
+  const int p0 = REVERSE ? last : 0, steps = last;
+  if (steps == 0) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) next_m[i] = matrix(p0)[threadIdx.x + i * 256];
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const int e = rows0 + r0 + r;
+    x[(r0 + r) * (DK + 4) + d] = given && d < a.key_dim && e < a.value_dim
+                                     ? given[((int64_t)bh * a.key_dim + d) * a.value_dim + e] : 0.f;
+  }
+  for (int n = 0; n < steps; ++n) {
+    const int p = REVERSE ? last - n : n, to = REVERSE ? p - 1 : p + 1;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int u = (threadIdx.x + i * 256) * 4;
+      float* at = m + u / DK * (DK + 1) + u % DK;
+      at[0] = next_m[i].x, at[1] = next_m[i].y, at[2] = next_m[i].z, at[3] = next_m[i].w;
+    }
+    __syncthreads();
+    if (n + 1 < steps)
+#pragma unroll
+      for (int i = 0; i < V; ++i) next_m[i] = matrix(to)[threadIdx.x + i * 256];
+    float acc[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const int64_t row = rows0 + r0 + r, pair = (int64_t)bh * a.segments + p;
+      acc[r] = REVERSE ? reversed[pair * some + row * DK + d] : a.work.effect[pair * all + row * DK + d];
+    }
+#pragma unroll 8
+    for (int j = 0; j < DK; j += 4) {
+      float w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = REVERSE ? m[d * (DK + 1) + j + i] : m[(j + i) * (DK + 1) + d];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float4 y = *reinterpret_cast<const float4*>(x + (r0 + r) * (DK + 4) + j);
+        acc[r] += y.x * w[0] + y.y * w[1] + y.z * w[2] + y.w * w[3];
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      x[(r0 + r) * (DK + 4) + d] = acc[r];
+      a.work.between[(((int64_t)bh * a.segments + to) * a.warps * 16 + rows0 + r0 + r) * DK + d] = acc[r];
+    }
   }
 }
 
@@ -898,7 +998,8 @@ struct ReverseStage {
   static constexpr int own = sizeof(T) == 2 ? 1024 : 0;   // dV on its way to rows
 };
 
-template <class T, int DK>
+// EFFECT: only the gradient before a segment of a zero one after it.
+template <class T, int DK, bool EFFECT>
 __global__ void __launch_bounds__(384)
     k_delta_reverse(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> gv,
                     int producers) {
@@ -909,16 +1010,18 @@ __global__ void __launch_bounds__(384)
   const int consumers = (blockDim.x >> 5) - producers, meeting = 32 * (consumers + 1);
   const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
   const int size = Stage::bytes(8 << lv);
-  const int part = blockIdx.x % a.parts, bh = blockIdx.x / a.parts, b = bh / a.heads, h = bh % a.heads;
-  const int hk = h / a.share, first_v = part * 16 * consumers;
+  const int part = blockIdx.x % a.parts, pair = blockIdx.x / a.parts, seg = pair % a.segments, bh = pair / a.segments;
+  const int b = bh / a.heads, h = bh % a.heads, hk = h / a.share, first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
+  const int first = min(chunks, seg * a.span), end = min(chunks, first + a.span);
+  const bool ends = seg == (chunks ? (chunks - 1) / a.span : 0);
   const int64_t head = (int64_t)b * a.heads + h;
   if (warp >= consumers) {
     const int p = warp - consumers, cols_v = min(16 * consumers, a.value_dim - first_v);
     unsigned char* st = held + p * size;
-    for (int n = p; n < chunks; n += producers) {
+    for (int n = p; n < end - first; n += producers) {
       if (n >= producers) meet(1 + producers + p, meeting);
-      const int c = chunks - 1 - n, t0 = c * kChunk, live = min(kChunk, len - t0);
+      const int c = end - 1 - n, t0 = c * kChunk, live = min(kChunk, len - t0);
       copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::bytes, lane);
       load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
                         a.key_dim, a.wide_qk, lane);
@@ -926,8 +1029,10 @@ __global__ void __launch_bounds__(384)
                         a.key_dim, a.wide_qk, lane);
       load_terms<T, IT>(st + Stage::gy, plane_v, lv, gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v,
                         gy.time, live, cols_v, a.wide_v, lane);
-      load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
-                        v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time, live, cols_v, a.wide_v, lane);
+      if constexpr (!EFFECT)
+        load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
+                          v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time, live, cols_v, a.wide_v,
+                          lane);
       copies_done();
       arrive(1 + p, meeting);
     }
@@ -941,8 +1046,13 @@ __global__ void __launch_bounds__(384)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
-      dS[n][r] = a.grad_last && d < a.key_dim && e < a.value_dim
-                     ? a.grad_last[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
+      if constexpr (EFFECT)
+        dS[n][r] = 0.f;
+      else if (!ends)
+        dS[n][r] = first < end ? a.work.between[((int64_t)pair * a.warps * 16 + e) * DK + d] : 0.f;
+      else
+        dS[n][r] = a.grad_last && d < a.key_dim && e < a.value_dim
+                       ? a.grad_last[(head * a.key_dim + d) * a.value_dim + e] : 0.f;
     }
   const auto word = [](const uint4& u, int i) { return i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w; };
   // <dS, S> before chunk c over the warp's channels
@@ -968,20 +1078,23 @@ __global__ void __launch_bounds__(384)
     for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
     if (lane == 0) a.work.along[at] = x;
   };
-  find_along(chunks);
+  if (!EFFECT && ends) find_along(chunks);
   unsigned char* own = held + producers * size + warp * Stage::own;
   const uint32_t rows = right_rows(lane, lp), cols = right_cols(lane, lp);
   const uint32_t turned_v = next(left_cols(lane, lv), 0, warp, lv), low = right_cols(lane, 1);
   int stage = 0;
-  for (int n0 = 0; n0 < chunks; ++n0) {
-    const int c = chunks - 1 - n0, t0 = c * kChunk, live = min(kChunk, len - t0);
+  for (int n0 = 0; n0 < end - first; ++n0) {
+    const int c = end - 1 - n0, t0 = c * kChunk, live = min(kChunk, len - t0);
     unsigned char* st = held + stage * size;
     const uint32_t base = smem_of(st);
     const int64_t chunk = head * a.chunks + c, at_c = chunk * warps + mine;
     float4 e[4];   // E, from the states' pass
+    float dots = 0.f;
+    if constexpr (!EFFECT) {
 #pragma unroll
-    for (int n = 0; n < 4; ++n) e[n] = a.work.e[(at_c * 4 + n) * 32 + lane];
-    const float dots = a.work.sums[(mine * a.work.chunks + chunk) * kChunk + folded_column(lane)];
+      for (int n = 0; n < 4; ++n) e[n] = a.work.e[(at_c * 4 + n) * 32 + lane];
+      dots = a.work.sums[(mine * a.work.chunks + chunk) * kChunk + folded_column(lane)];
+    }
     meet(1 + stage, meeting);
     float dU[4][4], dZ[4][4], X[4][4];
     zero(dU);
@@ -990,7 +1103,7 @@ __global__ void __launch_bounds__(384)
       uint32_t x[NR][4];
       left_of<NR>(dS, s, x);
 #pragma unroll
-      for (int j = 0; j < NS; ++j)
+      for (int j = 0; j < (EFFECT ? 0 : NS); ++j)
         a.work.ds[j][at_c * (DK / 16) * 32 + s * 32 + lane] = make_uint4(x[j][0], x[j][1], x[j][2], x[j][3]);
 #pragma unroll
       for (int j = 0; j < IT; ++j) {
@@ -1026,6 +1139,7 @@ __global__ void __launch_bounds__(384)
     product<2, 2, NR, NR, NR, true, 2>(
         dZ, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(X, s, x); },
         [&](int p, int s, int j) { return lower(Record::inverse, p, s, j); });
+    if constexpr (!EFFECT) {
 #pragma unroll
     for (int n = 0; n < 4; ++n)
       a.work.dz[(at_c * 4 + n) * 32 + lane] = make_float4(dZ[n][0], dZ[n][1], dZ[n][2], dZ[n][3]);
@@ -1081,6 +1195,7 @@ __global__ void __launch_bounds__(384)
             gv.data[b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head + e] = i < live ? dZ[n][r] : 0.f;
         }
     }
+    }
     // the gradient of the state before the chunk
     const float whole = float_at(st, Record::since, kChunk - 1);
 #pragma unroll
@@ -1098,11 +1213,19 @@ __global__ void __launch_bounds__(384)
     product<2, DK / 16, NR, IT, NR, true, 0>(
         dS, [&](int s, uint32_t (&x)[NR][4]) { left_of<NR>(dZ, s, x); },
         [&](int p, int s, int j) { return next(base + Stage::k + cols, s, p, lp) + j * plane; });
-    if (n0 + producers < chunks) arrive(1 + producers + stage, meeting);
+    if (n0 + producers < end - first) arrive(1 + producers + stage, meeting);
     stage = stage + 1 == producers ? 0 : stage + 1;
-    if (c % kAgain == 0 && c > 0) find_along(c);
+    if (!EFFECT && c % kAgain == 0 && c > 0) find_along(c);
   }
-  if (a.grad_state)
+  if constexpr (EFFECT) {
+    float* out = a.work.effect + (int64_t)a.batch * a.heads * a.segments * (a.warps * 16 + DK) * DK +
+                 ((int64_t)pair * a.warps * 16 + e0 + g) * DK + 2 * t;
+#pragma unroll
+    for (int n = 0; n < DK / 8; ++n) {
+      *reinterpret_cast<float2*>(out + 8 * n) = make_float2(dS[n][0], dS[n][1]);
+      *reinterpret_cast<float2*>(out + 8 * DK + 8 * n) = make_float2(dS[n][2], dS[n][3]);
+    }
+  } else if (seg == 0 && a.grad_state) {
 #pragma unroll
     for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
@@ -1110,6 +1233,7 @@ __global__ void __launch_bounds__(384)
         const int d = 8 * n + 2 * t + (r & 1), e = e0 + g + (r >> 1) * 8;
         if (d < a.key_dim && e < a.value_dim) a.grad_state[(head * a.key_dim + d) * a.value_dim + e] = dS[n][r];
       }
+  }
 }
 
 // A CTA has a chunk of a key head and COLS of its channels.  In shared memory: S0 and dS
@@ -1464,22 +1588,22 @@ cudaError_t launch_delta_prepare(const DeltaArgs& a, const DeltaViews& w, bool b
   return cudaGetLastError();
 }
 
-// CTAs, warps and stages of the kernels that walk along time.
+// CTAs, warps and stages of the kernels that walk along time, over `blocks` of 16 channels.
 struct DeltaShape {
   int consumers, producers, smem;
   unsigned ctas;
 };
 template <class Stage>
-DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a) {
-  const int W = a.warps;
-  const int64_t heads = (int64_t)a.batch * a.heads;
-  // value channels over several CTAs where there are too few sequences for the SMs
+DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a, int blocks) {
+  const int64_t pairs = (int64_t)a.batch * a.heads * a.segments;
+  // channels over several CTAs where there are too few sequences for the SMs, and where there
+  // are more than eight warps' of them
   a.parts = 1;
-  for (int d = 2; d <= W && heads * a.parts < h->sm_count; ++d)
-    if (W % d == 0) a.parts = d;
+  for (int d = 2; d <= blocks && (pairs * a.parts < h->sm_count || blocks / a.parts > 8); ++d)
+    if (blocks % d == 0) a.parts = d;
   DeltaShape s;
-  s.consumers = W / a.parts;
-  s.ctas = (unsigned)(heads * a.parts);
+  s.consumers = blocks / a.parts;
+  s.ctas = (unsigned)(pairs * a.parts);
   int dvp = 16;
   while (dvp < 16 * s.consumers) dvp *= 2;
   const int own = s.consumers * Stage::own;
@@ -1489,13 +1613,27 @@ DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a) {
   return s;
 }
 
+// Long sequences of few heads go in segments, all at once: first what each makes of any
+// state (twice a walk's work), then from one to the next, then the walk itself.
+template <int DK>
+void cut_segments(const emb_delta_s* h, DeltaArgs& a) {
+  a.segments = 1, a.span = a.chunks > 0 ? a.chunks : 1;
+  const int64_t heads = (int64_t)a.batch * a.heads;
+  if (heads * 4 > h->sm_count || a.chunks < kLeastChunks || !h->effect) return;
+  int64_t n = h->sm_count / heads;
+  if (n > a.chunks / 8) n = a.chunks / 8;
+  if (n * heads > h->max_pairs) n = h->max_pairs / heads;
+  if (n < 2) return;
+  a.span = (int)((a.chunks + n - 1) / n);
+  a.segments = (a.chunks + a.span - 1) / a.span;
+}
+
 template <class T, int DK, DeltaMode MODE>
-cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
-  cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
-  if (e != cudaSuccess) return e;
-  const DeltaShape s = walk_shape<ForwardStage<T, DK, MODE>>(h, a);
+cudaError_t launch_walk(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
+  const int blocks = a.warps + (MODE == kEffect ? DK / 16 : 0);
+  const DeltaShape s = walk_shape<ForwardStage<T, DK, MODE>>(h, a, blocks);
   const auto kernel = k_delta_fwd<T, DK, MODE>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
   if (e != cudaSuccess) return e;
   kernel<<<s.ctas, 32 * (s.consumers + s.producers), s.smem, stream>>>(
       a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.y),
@@ -1503,18 +1641,43 @@ cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews
   return cudaGetLastError();
 }
 
+template <int DK, bool REVERSE>
+cudaError_t launch_chain(const DeltaArgs& a, cudaStream_t stream) {
+  constexpr int smem = (DK * (DK + 1) + kChainRows * (DK + 4)) * 4;
+  const auto kernel = k_delta_chain<DK, REVERSE>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<(unsigned)(a.batch * a.heads * (a.warps * 16 / kChainRows)), 256, smem, stream>>>(a);
+  return cudaGetLastError();
+}
+
+template <class T, int DK, DeltaMode MODE>
+cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs& a, const DeltaViews& w, cudaStream_t stream) {
+  cut_segments<DK>(h, a);
+  cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
+  if (e == cudaSuccess && a.segments > 1) e = launch_walk<T, DK, kEffect>(h, a, w, stream);
+  if (e == cudaSuccess && a.segments > 1) e = launch_chain<DK, false>(a, stream);
+  return e == cudaSuccess ? launch_walk<T, DK, MODE>(h, a, w, stream) : e;
+}
+
+template <class T, int DK, bool EFFECT>
+cudaError_t launch_reverse(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
+  const DeltaShape s = walk_shape<ReverseStage<T, DK>>(h, a, a.warps);
+  const auto kernel = k_delta_reverse<T, DK, EFFECT>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
+  if (e != cudaSuccess) return e;
+  kernel<<<s.ctas, 32 * (s.consumers + s.producers), s.smem, stream>>>(
+      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.gv),
+      s.producers);
+  return cudaGetLastError();
+}
+
 template <class T, int DK>
 cudaError_t launch_delta_bwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, cudaStream_t stream) {
   cudaError_t e = launch_delta_fwd<T, DK, kStates>(h, a, w, stream);
-  if (e != cudaSuccess) return e;
-  const DeltaShape s = walk_shape<ReverseStage<T, DK>>(h, a);
-  const auto reverse = k_delta_reverse<T, DK>;
-  e = cudaFuncSetAttribute(reverse, cudaFuncAttributeMaxDynamicSharedMemorySize, s.smem);
-  if (e != cudaSuccess) return e;
-  reverse<<<s.ctas, 32 * (s.consumers + s.producers), s.smem, stream>>>(
-      a, dview<const T>(w.q), dview<const T>(w.k), dview<const T>(w.v), dview<const T>(w.gy), dview<T>(w.gv),
-      s.producers);
-  e = cudaGetLastError();
+  if (e == cudaSuccess && a.segments > 1) e = launch_reverse<T, DK, true>(h, a, w, stream);
+  if (e == cudaSuccess && a.segments > 1) e = launch_chain<DK, true>(a, stream);
+  if (e == cudaSuccess) e = launch_reverse<T, DK, false>(h, a, w, stream);
   if (e != cudaSuccess || a.chunks == 0) return e;
   using Shared = GradientShared<T, DK>;
   int dvp = 16;
@@ -1530,13 +1693,14 @@ cudaError_t launch_delta_bwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews
 }
 
 template <class T>
-cudaError_t launch_delta(const emb_delta_s* h, const DeltaArgs& a, const DeltaViews& w, bool backward, cudaStream_t s) {
+cudaError_t launch_delta(const emb_delta_s* h, const DeltaArgs& call, const DeltaViews& w, bool backward, cudaStream_t s) {
   const auto of = [&](auto dk) {
     constexpr int DK = decltype(dk)::value;
+    DeltaArgs a = call;
     return backward ? launch_delta_bwd<T, DK>(h, a, w, s) : launch_delta_fwd<T, DK, kForward>(h, a, w, s);
   };
-  if (a.key_dim <= 32) return of(std::integral_constant<int, 32>());
-  if (a.key_dim <= 64) return of(std::integral_constant<int, 64>());
+  if (call.key_dim <= 32) return of(std::integral_constant<int, 32>());
+  if (call.key_dim <= 64) return of(std::integral_constant<int, 64>());
   return of(std::integral_constant<int, 128>());
 }
 

@@ -177,6 +177,27 @@ def test_many_sequences_and_long_memory(dtype):
     check(make(2, 400, 1, 1, 128, 128, dtype, 3, slow=True))
 
 
+# sequences that are cut into segments: of lengths on and off theirs, entries that end in each, and none
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("T,H,J,N,V,slow", [(2048, 2, 1, 32, 32, True), (2100, 1, 1, 128, 128, False),
+                                            (2305, 3, 3, 64, 40, True), (3000, 1, 1, 100, 120, True),
+                                            (2500, 2, 2, 16, 128, False)])
+def test_long_sequences(T, H, J, N, V, slow, dtype):
+    check(make(1, T, H, J, N, V, dtype, T, slow=slow))
+
+
+def test_long_sequences_of_many_lengths():
+    import torch
+    B, T = 6, 2200
+    case = make(B, T, 1, 1, 32, 48, "bfloat16", 21, slow=True)
+    lens = torch.tensor([0, 5, 256, 700, 2177, 2200], device="cuda")
+    offsets = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    _, y, end, got = check(case, offsets=offsets, lens=lens)
+    dead = torch.arange(T, device="cuda")[None] >= lens[:, None]
+    assert not y[dead].any() and torch.equal(end[0], case[5][0])
+    assert not any(g[dead].any() for g in got[:5]) and torch.equal(got[5][0], case[7][0])
+
+
 @pytest.mark.parametrize("dtype", ["float32", "float16"])
 def test_lengths(dtype):
     """Entries of no position, of some, of all and (by their offsets) of more than the time axis; NaN and infinities
