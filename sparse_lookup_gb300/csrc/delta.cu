@@ -279,7 +279,8 @@ extern "C" emb_status delta_backward(emb_delta h, int32_t batch, int32_t len, in
   a.grad_decay = dview<float>(grad_decay), a.grad_beta = dview<float>(grad_beta);
   a.wide_qk = whole_pieces(size, N, {q, k}, 16 / size, 8);
   a.wide_v = whole_pieces(size, D, {v, grad_y}, 16 / size, 8);
-  a.wide_gy = whole_pieces(size, N, {grad_q, grad_k}, 2, 2);
+  a.wide_y = whole_pieces(size, D, {grad_v}, 16 / size, 8);
+  a.wide_gy = whole_pieces(size, N, {grad_q, grad_k}, 16 / size, 8);
   DeltaViews w = {};
   w.q = q, w.k = k, w.v = v, w.gy = grad_y, w.gq = grad_q, w.gk = grad_k, w.gv = grad_v;
   return cuda_status(run(h, a, w, dtype, true, stream));

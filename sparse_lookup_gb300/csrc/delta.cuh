@@ -90,7 +90,7 @@ struct DeltaArgs {
   float *state_out, *grad_state;
   DView<const float> decay, beta;
   DView<float> grad_decay, grad_beta;
-  bool wide_qk, wide_v, wide_y, wide_gy;   // accesses of 16 bytes (of grad_q and grad_k: of two elements)
+  bool wide_qk, wide_v, wide_y, wide_gy;   // accesses of 16 bytes
   DeltaWork work;
 };
 
@@ -909,9 +909,9 @@ template <int DK, bool REVERSE>
 __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs a) {
   constexpr int G = 256 / DK, R = kChainRows / G > 0 ? kChainRows / G : 1, V = DK * DK / 1024;
   static_assert(G * R == kChainRows, "");
-  extern __shared__ float chain[];
-  float* m = chain;                      // [DK][DK + 1] M^T
-  float* x = chain + DK * (DK + 1);      // [kChainRows][DK + 4]
+  extern __shared__ __align__(128) float chain[];
+  float* m = chain;                // [DK][DK] M^T, groups of four exchanged by their row so that rows and columns are read alike
+  float* x = chain + DK * DK;      // [kChainRows][DK]
   const int blocks = a.warps * 16 / kChainRows, rows0 = blockIdx.x % blocks * kChainRows, bh = blockIdx.x / blocks;
   const int b = bh / a.heads, len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
   const int last = chunks ? (chunks - 1) / a.span : 0, d = threadIdx.x % DK, r0 = threadIdx.x / DK * R;
@@ -919,53 +919,57 @@ __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs a) {
   // M^T follows N^T in a segment's effect of the forward; N'^T lies in another array of N^T's size
   const int64_t all = (int64_t)(a.warps * 16 + DK) * DK, some = (int64_t)a.warps * 16 * DK;
   const float* reversed = a.work.effect + (int64_t)a.batch * a.heads * a.segments * all;
-  const auto matrix = [&](int p) {
-    return reinterpret_cast<const float4*>(a.work.effect + ((int64_t)bh * a.segments + p) * all + some);
-  };
   float4 next_m[V];
-  const int p0 = REVERSE ? last : 0, steps = last;
-  if (steps == 0) return;
+  float next_n[R];
+  const auto fetch = [&](int p) {
+    const int64_t pair = (int64_t)bh * a.segments + p;
+    const float4* from = reinterpret_cast<const float4*>(a.work.effect + pair * all + some);
 #pragma unroll
-  for (int i = 0; i < V; ++i) next_m[i] = matrix(p0)[threadIdx.x + i * 256];
+    for (int i = 0; i < V; ++i) next_m[i] = from[threadIdx.x + i * 256];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+      next_n[r] = (REVERSE ? reversed + pair * some : a.work.effect + pair * all)[(int64_t)(rows0 + r0 + r) * DK + d];
+  };
+  if (last == 0) return;
+  fetch(REVERSE ? last : 0);
 #pragma unroll
   for (int r = 0; r < R; ++r) {
     const int e = rows0 + r0 + r;
-    x[(r0 + r) * (DK + 4) + d] = given && d < a.key_dim && e < a.value_dim
-                                     ? given[((int64_t)bh * a.key_dim + d) * a.value_dim + e] : 0.f;
+    x[(r0 + r) * DK + d] = given && d < a.key_dim && e < a.value_dim
+                               ? given[((int64_t)bh * a.key_dim + d) * a.value_dim + e] : 0.f;
   }
-  for (int n = 0; n < steps; ++n) {
+  for (int n = 0; n < last; ++n) {
     const int p = REVERSE ? last - n : n, to = REVERSE ? p - 1 : p + 1;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int u = (threadIdx.x + i * 256) * 4;
-      float* at = m + u / DK * (DK + 1) + u % DK;
-      at[0] = next_m[i].x, at[1] = next_m[i].y, at[2] = next_m[i].z, at[3] = next_m[i].w;
-    }
-    __syncthreads();
-    if (n + 1 < steps)
-#pragma unroll
-      for (int i = 0; i < V; ++i) next_m[i] = matrix(to)[threadIdx.x + i * 256];
     float acc[R];
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-      const int64_t row = rows0 + r0 + r, pair = (int64_t)bh * a.segments + p;
-      acc[r] = REVERSE ? reversed[pair * some + row * DK + d] : a.work.effect[pair * all + row * DK + d];
+    for (int i = 0; i < V; ++i) {
+      const int u = threadIdx.x + i * 256, row = u / (DK / 4), col = u % (DK / 4);
+      *reinterpret_cast<float4*>(m + row * DK + ((col ^ (row & 7)) << 2)) = next_m[i];
     }
-#pragma unroll 8
+#pragma unroll
+    for (int r = 0; r < R; ++r) acc[r] = next_n[r];
+    __syncthreads();
+    if (n + 1 < last) fetch(to);
+#pragma unroll 4
     for (int j = 0; j < DK; j += 4) {
       float w[4];
+      if constexpr (REVERSE) {
+        const float4 y = *reinterpret_cast<const float4*>(m + d * DK + (((j >> 2) ^ (d & 7)) << 2));
+        w[0] = y.x, w[1] = y.y, w[2] = y.z, w[3] = y.w;
+      } else {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = REVERSE ? m[d * (DK + 1) + j + i] : m[(j + i) * (DK + 1) + d];
+        for (int i = 0; i < 4; ++i) w[i] = m[(j + i) * DK + ((((d >> 2) ^ ((j + i) & 7)) << 2) | (d & 3))];
+      }
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const float4 y = *reinterpret_cast<const float4*>(x + (r0 + r) * (DK + 4) + j);
+        const float4 y = *reinterpret_cast<const float4*>(x + (r0 + r) * DK + j);
         acc[r] += y.x * w[0] + y.y * w[1] + y.z * w[2] + y.w * w[3];
       }
     }
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      x[(r0 + r) * (DK + 4) + d] = acc[r];
+      x[(r0 + r) * DK + d] = acc[r];
       a.work.between[(((int64_t)bh * a.segments + to) * a.warps * 16 + rows0 + r0 + r) * DK + d] = acc[r];
     }
   }
@@ -1320,6 +1324,34 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
     const int h = hk * a.share + hs;
     const int64_t head = (int64_t)b * a.heads + h, chunk = head * a.chunks + c;
     if (hs) __syncthreads();   // every warp is through with the head before
+    if (col0 == 0 && warp == kWarps - 1) {
+      // decays and betas: the chunk's sums, and those of the chunks up to where <dS, S> is known
+      float x = 0.f, gb = 0.f;
+      for (int w = 0; w < W; ++w) {
+        x += a.work.sums[(w * a.work.chunks + chunk) * kChunk + lane] -
+             a.work.sums[((W + w) * a.work.chunks + chunk) * kChunk + lane];
+        gb += a.work.sums[((2 * W + w) * a.work.chunks + chunk) * kChunk + lane];
+      }
+      const int known = min(chunks, (c / kAgain + 1) * kAgain);
+      float carry = 0.f;
+      for (int n = (c + 1) * W + lane; n < known * W; n += 32) carry += a.work.totals[head * a.chunks * W + n];
+      if (lane < W) carry += a.work.along[(head * (a.chunks + 1) + known) * W + lane];
+      for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_down_sync(kFull, x, o);
+        if (lane + o < 32) x += y;
+      }
+      const int64_t i = t0 + lane;
+      if (lane < there) {
+        const bool on = lane < live;
+        // where exp(g) is 0 so is its gradient, which the sums give to their rounding
+        const float g_i = on ? a.decay.data[b * a.decay.batch + i * a.decay.time + h * a.decay.head] : 0.f;
+        a.grad_decay.data[b * a.grad_decay.batch + i * a.grad_decay.time + h * a.grad_decay.head] =
+            on && expf(g_i) != 0.f ? x + carry : 0.f;
+        a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = on ? gb : 0.f;
+      }
+    }
     const unsigned char* record = a.work.record + chunk * Record::bytes;
     if (threadIdx.x < 40) copy_async(sh + threadIdx.x * 16, record + threadIdx.x * 16, true);
     for (int u = threadIdx.x; u < kChunk << lv; u += kThreads) {
@@ -1389,34 +1421,6 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
     }
     copies_done();
     __syncthreads();
-    if (col0 == 0 && warp == kWarps - 1) {
-      // decays and betas: the chunk's sums, and those of the chunks up to where <dS, S> is known
-      float x = 0.f, gb = 0.f;
-      for (int w = 0; w < W; ++w) {
-        x += a.work.sums[(w * a.work.chunks + chunk) * kChunk + lane] -
-             a.work.sums[((W + w) * a.work.chunks + chunk) * kChunk + lane];
-        gb += a.work.sums[((2 * W + w) * a.work.chunks + chunk) * kChunk + lane];
-      }
-      const int known = min(chunks, (c / kAgain + 1) * kAgain);
-      float carry = 0.f;
-      for (int n = (c + 1) * W + lane; n < known * W; n += 32) carry += a.work.totals[head * a.chunks * W + n];
-      if (lane < W) carry += a.work.along[(head * (a.chunks + 1) + known) * W + lane];
-      for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(kFull, x, o);
-        if (lane + o < 32) x += y;
-      }
-      const int64_t i = t0 + lane;
-      if (lane < there) {
-        const bool on = lane < live;
-        // where exp(g) is 0 so is its gradient, which the sums give to their rounding
-        const float g_i = on ? a.decay.data[b * a.decay.batch + i * a.decay.time + h * a.decay.head] : 0.f;
-        a.grad_decay.data[b * a.grad_decay.batch + i * a.grad_decay.time + h * a.grad_decay.head] =
-            on && expf(g_i) != 0.f ? x + carry : 0.f;
-        a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = on ? gb : 0.f;
-      }
-    }
     // dA and X, a 16 x 16 block at a time
     for (int u = warp; u < 6; u += kWarps) {
       const bool is_x = u >= 3;
@@ -1535,28 +1539,37 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
       }
     }
   }
+  // to rows by way of shared memory, so that whole sectors leave
+  __syncthreads();
+  constexpr int V = 16 / sizeof(T), pieces = COLS / V;
+  const auto place = [](int row, int p) { return (row * pieces + (p ^ (row & (pieces < 8 ? pieces - 1 : 7)))) * 16; };
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int i = 16 * m + g + 8 * r;
-    if (i >= there) continue;
-    const bool on = i < live;
+  for (int w = 0; w < 2; ++w)
 #pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const int d = col0 + 16 * p + 8 * n + 2 * t;
-      const float2 x = on ? make_float2(sq[n][2 * r], sq[n][2 * r + 1]) : make_float2(0.f, 0.f);
-      const float2 y = on ? make_float2(sk[n][2 * r], sk[n][2 * r + 1]) : make_float2(0.f, 0.f);
-      T* tq = gq.data + b * gq.batch + (int64_t)(t0 + i) * gq.time + hk * gq.head + d;
-      T* tk = gk.data + b * gk.batch + (int64_t)(t0 + i) * gk.time + hk * gk.head + d;
-      if (a.wide_gy && d < a.key_dim) {
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int col = 16 * p + 8 * n + 2 * t;
         Vec<T, 2> o;
-        narrow2(o.e, x);
-        store_vec(tq, o);
-        narrow2(o.e, y);
-        store_vec(tk, o);
-      } else {
-        if (d < a.key_dim) tq[0] = from_f32<T>(x.x), tk[0] = from_f32<T>(y.x);
-        if (d + 1 < a.key_dim) tq[1] = from_f32<T>(x.y), tk[1] = from_f32<T>(y.y);
+        narrow2(o.e, w ? make_float2(sk[n][2 * r], sk[n][2 * r + 1]) : make_float2(sq[n][2 * r], sq[n][2 * r + 1]));
+        store_vec(reinterpret_cast<T*>(held + w * kChunk * COLS * sizeof(T) + place(16 * m + g + 8 * r, col / V)) + col % V, o);
       }
+  __syncthreads();
+  for (int u = threadIdx.x; u < 2 * kChunk * pieces; u += kThreads) {
+    const int w = u / (kChunk * pieces), i = u / pieces % kChunk, n = u % pieces, d = col0 + n * V;
+    if (i >= there || d >= a.key_dim) continue;
+    Vec<T, V> o = load_vec<T, V>(reinterpret_cast<const T*>(held + w * kChunk * COLS * sizeof(T) + place(i, n)));
+    if (i >= live)
+#pragma unroll
+      for (int e = 0; e < V; ++e) o.e[e] = from_f32<T>(0.f);
+    const DView<T>& to = w ? gk : gq;
+    T* at = to.data + b * to.batch + (int64_t)(t0 + i) * to.time + hk * to.head + d;
+    if (a.wide_gy) {
+      store_vec(at, o);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (d + e < a.key_dim) at[e] = o.e[e];
     }
   }
 }
@@ -1643,7 +1656,7 @@ cudaError_t launch_walk(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, 
 
 template <int DK, bool REVERSE>
 cudaError_t launch_chain(const DeltaArgs& a, cudaStream_t stream) {
-  constexpr int smem = (DK * (DK + 1) + kChainRows * (DK + 4)) * 4;
+  constexpr int smem = (DK + kChainRows) * DK * 4;
   const auto kernel = k_delta_chain<DK, REVERSE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
