@@ -1240,6 +1240,42 @@ __global__ void __launch_bounds__(384)
   }
 }
 
+// The gradients of decays and betas: a warp a chunk, a lane a position.  The chunk's sums,
+// and those of the chunks up to where <dS, S> is known.
+static __global__ void __launch_bounds__(128) k_delta_numbers(DeltaArgs a) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t chunk = blockIdx.x * 4 + (threadIdx.x >> 5);
+  if (chunk >= a.work.chunks) return;
+  const uint32_t head = chunk / (uint32_t)a.chunks;
+  const int c = (int)(chunk - head * a.chunks), b = (int)(head / (uint32_t)a.heads), h = (int)(head - b * (uint32_t)a.heads);
+  const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk, W = a.warps;
+  const int64_t i = (int64_t)c * kChunk + lane, stride = (int64_t)W * a.work.chunks * kChunk;
+  float x = 0.f, gb = 0.f, g = 0.f;
+  const bool on = i < len;
+  if (c < chunks) {
+    const float* sums = a.work.sums + (int64_t)chunk * kChunk + lane;
+#pragma unroll 4
+    for (int w = 0; w < W; ++w, sums += a.work.chunks * kChunk) x += sums[0] - sums[stride], gb += sums[2 * stride];
+    if (on) g = a.decay.data[b * a.decay.batch + i * a.decay.time + h * a.decay.head];
+    const int known = min(chunks, (c / kAgain + 1) * kAgain);
+    float carry = 0.f;
+    for (int n = (c + 1) * W + lane; n < known * W; n += 32) carry += a.work.totals[(int64_t)head * a.chunks * W + n];
+    if (lane < W) carry += a.work.along[((int64_t)head * (a.chunks + 1) + known) * W + lane];
+    for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const float y = __shfl_down_sync(kFull, x, o);
+      if (lane + o < 32) x += y;
+    }
+    x += carry;
+  }
+  if (i >= a.len) return;
+  // where exp(g) is 0 so is its gradient, which the sums give to their rounding
+  a.grad_decay.data[b * a.grad_decay.batch + i * a.grad_decay.time + h * a.grad_decay.head] =
+      on && expf(g) != 0.f ? x : 0.f;
+  a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = on ? gb : 0.f;
+}
+
 // A CTA has a chunk of a key head and COLS of its channels.  In shared memory: S0 and dS
 // [value channels][COLS], U and dZ [value channels][32], grad_y, K and Q, dA and X.  16-bit
 // calls leave room for all channels; each CTA of a key head finds dA and X for itself.
@@ -1290,10 +1326,6 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
       for (int h = hk * a.share; h < (hk + 1) * a.share; ++h) {
         T* to = gv.data + b * gv.batch + (int64_t)(t0 + i) * gv.time + h * gv.head;
         for (int e = lane; e < a.value_dim; e += 32) to[e] = from_f32<T>(0.f);
-        if (lane == 0) {
-          a.grad_decay.data[b * a.grad_decay.batch + (t0 + i) * a.grad_decay.time + h * a.grad_decay.head] = 0.f;
-          a.grad_beta.data[b * a.grad_beta.batch + (t0 + i) * a.grad_beta.time + h * a.grad_beta.head] = 0.f;
-        }
       }
     }
     return;
@@ -1324,34 +1356,6 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
     const int h = hk * a.share + hs;
     const int64_t head = (int64_t)b * a.heads + h, chunk = head * a.chunks + c;
     if (hs) __syncthreads();   // every warp is through with the head before
-    if (col0 == 0 && warp == kWarps - 1) {
-      // decays and betas: the chunk's sums, and those of the chunks up to where <dS, S> is known
-      float x = 0.f, gb = 0.f;
-      for (int w = 0; w < W; ++w) {
-        x += a.work.sums[(w * a.work.chunks + chunk) * kChunk + lane] -
-             a.work.sums[((W + w) * a.work.chunks + chunk) * kChunk + lane];
-        gb += a.work.sums[((2 * W + w) * a.work.chunks + chunk) * kChunk + lane];
-      }
-      const int known = min(chunks, (c / kAgain + 1) * kAgain);
-      float carry = 0.f;
-      for (int n = (c + 1) * W + lane; n < known * W; n += 32) carry += a.work.totals[head * a.chunks * W + n];
-      if (lane < W) carry += a.work.along[(head * (a.chunks + 1) + known) * W + lane];
-      for (int o = 16; o > 0; o >>= 1) carry += __shfl_xor_sync(kFull, carry, o);
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const float y = __shfl_down_sync(kFull, x, o);
-        if (lane + o < 32) x += y;
-      }
-      const int64_t i = t0 + lane;
-      if (lane < there) {
-        const bool on = lane < live;
-        // where exp(g) is 0 so is its gradient, which the sums give to their rounding
-        const float g_i = on ? a.decay.data[b * a.decay.batch + i * a.decay.time + h * a.decay.head] : 0.f;
-        a.grad_decay.data[b * a.grad_decay.batch + i * a.grad_decay.time + h * a.grad_decay.head] =
-            on && expf(g_i) != 0.f ? x + carry : 0.f;
-        a.grad_beta.data[b * a.grad_beta.batch + i * a.grad_beta.time + h * a.grad_beta.head] = on ? gb : 0.f;
-      }
-    }
     const unsigned char* record = a.work.record + chunk * Record::bytes;
     if (threadIdx.x < 40) copy_async(sh + threadIdx.x * 16, record + threadIdx.x * 16, true);
     for (int u = threadIdx.x; u < kChunk << lv; u += kThreads) {
@@ -1366,50 +1370,57 @@ __global__ void __launch_bounds__(32 * GradientShared<T, DK>::warps, 16 / Gradie
       put_eight<T, IT>(held + at.gy + piece(r, n, lv), plane_v, rows + r * gy.time + n * 8, on ? a.value_dim - n * 8 : 0,
                        a.wide_v);
     }
-    // states: a lane's four words of 16 channels by 16 key channels; several of a thread's
-    // loads are in flight before the first is stored
-    constexpr int U = 4;
-    for (int j = 0; j < NS; ++j)
-      for (int u0 = threadIdx.x; u0 < W * (COLS / 16) * 32; u0 += U * kThreads) {
-        uint4 x[2][U];
+    // E and dZ, and the states, a lane's four words of 16 channels by 16 key channels: as many of
+    // a thread's loads as registers hold are in flight before the first is stored
+    constexpr int UE = 2, US = NS == 1 ? 4 : NS == 2 ? 2 : 1;
+    float4 e[UE], z[UE];
+    float2 f[UE];
+    const auto load_e = [&](int u0) {
 #pragma unroll
-        for (int n = 0; n < U; ++n) {
-          const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
-          if (u >= W * (COLS / 16) * 32) continue;
-          const int64_t of = (int64_t)(w * (DK / 16) + col0 / 16 + s) * 32 + l;
-          x[0][n] = a.work.s[j][(head * (a.chunks + 1) + c) * W * (DK / 16) * 32 + of];
-          x[1][n] = a.work.ds[j][chunk * W * (DK / 16) * 32 + of];
-        }
-#pragma unroll
-        for (int n = 0; n < U; ++n) {
-          const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
-          if (u >= W * (COLS / 16) * 32) continue;
-          // words of rows 8 apart and of neighbouring pieces
-          unsigned char* to = held + at.s + j * W * 16 * COLS * 2;
-          const uint32_t first = element_at(16 * w + (l >> 2), 16 * s + 2 * (l & 3), lc), second = first ^ 16u;
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            if (k) to += at.ds - at.s;
-            *reinterpret_cast<uint32_t*>(to + first) = x[k][n].x;
-            *reinterpret_cast<uint32_t*>(to + first + 16 * COLS) = x[k][n].y;
-            *reinterpret_cast<uint32_t*>(to + second) = x[k][n].z;
-            *reinterpret_cast<uint32_t*>(to + second + 16 * COLS) = x[k][n].w;
-          }
-        }
-      }
-    for (int u0 = threadIdx.x; u0 < W * 128; u0 += U * kThreads) {
-      float4 e[U], z[U];
-      float2 f[U];
-#pragma unroll
-      for (int n = 0; n < U; ++n) {
+      for (int n = 0; n < UE; ++n) {
         const int u = u0 + n * kThreads;
         if (u >= W * 128) continue;
         e[n] = a.work.e[chunk * W * 128 + u];
         z[n] = a.work.dz[chunk * W * 128 + u];
         f[n] = *reinterpret_cast<const float2*>(record + Record::beta + (8 * ((u >> 5) & 3) + 2 * (u & 3)) * 4);
       }
+    };
+    load_e(threadIdx.x);
+    for (int u0 = threadIdx.x; u0 < W * (COLS / 16) * 32; u0 += US * kThreads) {
+      uint4 x[2][US][NS];
 #pragma unroll
-      for (int n = 0; n < U; ++n) {
+      for (int n = 0; n < US; ++n) {
+        const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
+        if (u >= W * (COLS / 16) * 32) continue;
+        const int64_t of = (int64_t)(w * (DK / 16) + col0 / 16 + s) * 32 + l;
+#pragma unroll
+        for (int j = 0; j < NS; ++j) {
+          x[0][n][j] = a.work.s[j][(head * (a.chunks + 1) + c) * W * (DK / 16) * 32 + of];
+          x[1][n][j] = a.work.ds[j][chunk * W * (DK / 16) * 32 + of];
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < US; ++n) {
+        const int u = u0 + n * kThreads, l = u & 31, s = (u >> 5) % (COLS / 16), w = (u >> 5) / (COLS / 16);
+        if (u >= W * (COLS / 16) * 32) continue;
+        // words of rows 8 apart and of neighbouring pieces
+        const uint32_t first = element_at(16 * w + (l >> 2), 16 * s + 2 * (l & 3), lc), second = first ^ 16u;
+#pragma unroll
+        for (int j = 0; j < NS; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            unsigned char* to = held + (k ? at.ds : at.s) + j * W * 16 * COLS * 2;
+            *reinterpret_cast<uint32_t*>(to + first) = x[k][n][j].x;
+            *reinterpret_cast<uint32_t*>(to + first + 16 * COLS) = x[k][n][j].y;
+            *reinterpret_cast<uint32_t*>(to + second) = x[k][n][j].z;
+            *reinterpret_cast<uint32_t*>(to + second + 16 * COLS) = x[k][n][j].w;
+          }
+      }
+    }
+    for (int u0 = threadIdx.x; u0 < W * 128; u0 += UE * kThreads) {
+      if (u0 != threadIdx.x) load_e(u0);
+#pragma unroll
+      for (int n = 0; n < UE; ++n) {
         const int u = u0 + n * kThreads, l = u & 31, col = 8 * ((u >> 5) & 3) + 2 * (l & 3), row = 16 * (u >> 7) + (l >> 2);
         if (u >= W * 128) continue;
         const uint32_t r0 = element_at(row, col, 2), r1 = r0 + 512;
@@ -1692,6 +1703,9 @@ cudaError_t launch_delta_bwd(const emb_delta_s* h, DeltaArgs a, const DeltaViews
   if (e == cudaSuccess && a.segments > 1) e = launch_chain<DK, true>(a, stream);
   if (e == cudaSuccess) e = launch_reverse<T, DK, false>(h, a, w, stream);
   if (e != cudaSuccess || a.chunks == 0) return e;
+  k_delta_numbers<<<(unsigned)((a.work.chunks + 3) / 4), 128, 0, stream>>>(a);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   using Shared = GradientShared<T, DK>;
   int dvp = 16;
   while (dvp < 16 * a.warps) dvp *= 2;
