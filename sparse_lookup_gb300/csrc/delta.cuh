@@ -305,56 +305,84 @@ struct Eight {
   __device__ __forceinline__ float at(int i) const { return to_f32(reinterpret_cast<const T*>(u)[i]); }
 };
 
+// A piece's terms to tiles `plane` bytes apart.
+template <class T, int IT>
+__device__ __forceinline__ void put_terms(unsigned char* to, int plane, const Eight<T>& x) {
+  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    *reinterpret_cast<uint4*>(to) = x.u[0];
+  } else {
+    uint32_t w[4][IT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) split<IT>(x.at(2 * i), x.at(2 * i + 1), w[i]);
+#pragma unroll
+    for (int i = 0; i < IT; ++i) *reinterpret_cast<uint4*>(to + i * plane) = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+  }
+}
+
 __device__ __forceinline__ void copy_async(uint32_t to, const void* from, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(on ? 16 : 0) : "memory");
 }
 __device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-// Rows 0 .. 31 (`live` of them) of `cols` columns, by one warp, as bf16 terms in tiles
-// `plane` bytes apart of 2^lp pieces a row.  Columns and rows beyond the array's are 0.
-// Aligned bf16 is only copied; copies_done() has to follow.
-template <class T, int IT>
-__device__ __forceinline__ void load_terms(unsigned char* tile, int plane, int lp, const T* rows, int64_t stride, int live,
-                                           int cols, bool wide, int lane) {
-  constexpr int U = sizeof(T) == 2 ? 8 : 4;
-  const int pieces = 1 << lp, units = kChunk << lp;
+// Rows 0 .. 31 (`live` of them) of `cols` columns as bf16 terms in tiles `plane` bytes
+// apart of 2^lp pieces a row.  Columns and rows beyond the array's are 0.
+template <class T>
+struct TileSource {
+  unsigned char* tile;
+  int plane, lp;
+  const T* rows;
+  int64_t stride;
+  int cols;
+  bool wide;
+};
+
+// N such tiles by one warp, all tiles' loads in flight together.  Aligned bf16 is only
+// copied; copies_done() has to follow.
+template <int IT, int N, class T>
+__device__ __forceinline__ void load_tiles(const TileSource<T> (&x)[N], int live, int lane) {
   if constexpr (std::is_same_v<T, __nv_bfloat16>) {
+    bool wide = true;
+#pragma unroll
+    for (int w = 0; w < N; ++w) wide = wide && x[w].wide;
     if (wide) {
-      const uint32_t to = smem_of(tile);
+#pragma unroll
+      for (int w = 0; w < N; ++w) {
+        const uint32_t to = smem_of(x[w].tile);
+        const int lp = x[w].lp;
 #pragma unroll 4
-      for (int u = lane; u < units; u += 32) {
-        const int r = u >> lp, p = u & (pieces - 1);
-        const bool on = r < live && p * 8 < cols;
-        copy_async(to + piece(r, p, lp), on ? rows + r * stride + p * 8 : rows, on);
+        for (int u = lane; u < kChunk << lp; u += 32) {
+          const int r = u >> lp, p = u & ((1 << lp) - 1);
+          const bool on = r < live && p * 8 < x[w].cols;
+          copy_async(to + piece(r, p, lp), on ? x[w].rows + r * x[w].stride + p * 8 : x[w].rows, on);
+        }
       }
       return;
     }
   }
-  for (int u0 = lane; u0 < units; u0 += 32 * U) {
-    Eight<T> x[U];
+  constexpr int U = sizeof(T) == 2 || N <= 3 ? 4 : 2;
+  int most = 0;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k, r = u >> lp, c = (u & (pieces - 1)) << 3;
-      if (u >= units || r >= live || c >= cols) x[k].clear();
-      else if (wide) x[k].load(rows + r * stride + c);
-      else x[k].gather(rows + r * stride + c, cols - c);
-    }
+  for (int w = 0; w < N; ++w) most = max(most, kChunk << x[w].lp);
+  for (int u0 = lane; u0 < most; u0 += 32 * U) {
+    Eight<T> e[N][U];
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const int u = u0 + 32 * k;
-      if (u >= units) continue;
-      const uint32_t at = piece(u >> lp, u & (pieces - 1), lp);
-      if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-        *reinterpret_cast<uint4*>(tile + at) = x[k].u[0];
-      } else {
-        uint32_t w[4][IT];
+    for (int w = 0; w < N; ++w)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) split<IT>(x[k].at(2 * i), x[k].at(2 * i + 1), w[i]);
-#pragma unroll
-        for (int i = 0; i < IT; ++i)
-          *reinterpret_cast<uint4*>(tile + i * plane + at) = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
+      for (int k = 0; k < U; ++k) {
+        const int u = u0 + 32 * k, r = u >> x[w].lp, c = (u & ((1 << x[w].lp) - 1)) << 3;
+        const T* from = x[w].rows + r * x[w].stride + c;
+        if (r >= live || c >= x[w].cols) e[w][k].clear();
+        else if (x[w].wide) e[w][k].load(from);
+        else e[w][k].gather(from, x[w].cols - c);
       }
-    }
+#pragma unroll
+    for (int w = 0; w < N; ++w)
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int u = u0 + 32 * k, lp = x[w].lp;
+        if (u >= kChunk << lp) continue;
+        put_terms<T, IT>(x[w].tile + piece(u >> lp, u & ((1 << lp) - 1), lp), x[w].plane, e[w][k]);
+      }
   }
 }
 
@@ -365,15 +393,7 @@ __device__ __forceinline__ void put_eight(unsigned char* to, int plane, const T*
   if (n <= 0) x.clear();
   else if (wide) x.load(from);
   else x.gather(from, n);
-  if constexpr (std::is_same_v<T, __nv_bfloat16>) {
-    *reinterpret_cast<uint4*>(to) = x.u[0];
-  } else {
-    uint32_t w[4][IT];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) split<IT>(x.at(2 * i), x.at(2 * i + 1), w[i]);
-#pragma unroll
-    for (int i = 0; i < IT; ++i) *reinterpret_cast<uint4*>(to + i * plane) = make_uint4(w[0][i], w[1][i], w[2][i], w[3][i]);
-  }
+  put_terms<T, IT>(to, plane, x);
 }
 
 // X^T of such a tile in the layout of accumulators: rows are 16 of the tile's columns
@@ -492,10 +512,10 @@ __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const 
   unsigned char* mine = held + (threadIdx.x >> 5) * Shared::bytes;
   float g = lane < live ? a.decay.data[b * a.decay.batch + t * a.decay.time + h * a.decay.head] : 0.f;
   const float beta = lane < live ? a.beta.data[b * a.beta.batch + t * a.beta.time + h * a.beta.head] : 0.f;
-  load_terms<T, IT>(mine, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live, a.key_dim,
-                    a.wide_qk, lane);
-  load_terms<T, IT>(mine + IT * plane, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
-                    a.key_dim, a.wide_qk, lane);
+  const TileSource<T> tiles[2] = {
+      {mine, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, a.key_dim, a.wide_qk},
+      {mine + IT * plane, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, a.key_dim, a.wide_qk}};
+  load_tiles<IT>(tiles, live, lane);
   copies_done();
   __syncwarp();
   // lower blocks of K K^T and Q K^T: rows 0 .. 15 by columns 0 .. 15 (two accumulators),
@@ -705,17 +725,17 @@ __global__ void __launch_bounds__(384)
       if (c >= first + producers) meet(1 + producers + p, meeting);
       const int t0 = c * kChunk, live = min(kChunk, len - t0);
       copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::forward_bytes, lane);
-      load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
-                        a.key_dim, a.wide_qk, lane);
-      if constexpr (MODE != kEffect)
-        load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
-                        a.key_dim, a.wide_qk, lane);
-      load_terms<T, IT>(st + Stage::v, plane_v, lv, v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time,
-                        live, cols_v, a.wide_v, lane);
-      if constexpr (MODE == kStates)
-        load_terms<T, IT>(st + Stage::v + IT * plane_v, plane_v, lv,
-                          gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v, gy.time, live, cols_v,
-                          a.wide_v, lane);
+      const TileSource<T> kt{st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time,
+                             a.key_dim, a.wide_qk};
+      const TileSource<T> qt{st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time,
+                             a.key_dim, a.wide_qk};
+      const TileSource<T> vt{st + Stage::v, plane_v, lv, v.data + b * v.batch + t0 * v.time + h * v.head + first_v,
+                             v.time, cols_v, a.wide_v};
+      const TileSource<T> yt{st + Stage::v + IT * plane_v, plane_v, lv,
+                             gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v, gy.time, cols_v, a.wide_v};
+      if constexpr (MODE == kStates) load_tiles<IT, 4, T>({kt, qt, vt, yt}, live, lane);
+      else if constexpr (MODE == kForward) load_tiles<IT, 3, T>({kt, qt, vt}, live, lane);
+      else load_tiles<IT, 2, T>({kt, vt}, live, lane);
       copies_done();
       arrive(1 + p, meeting);
     }
@@ -1027,16 +1047,16 @@ __global__ void __launch_bounds__(384)
       if (n >= producers) meet(1 + producers + p, meeting);
       const int c = end - 1 - n, t0 = c * kChunk, live = min(kChunk, len - t0);
       copy_record(st, a.work.record + (head * a.chunks + c) * Record::bytes, Record::bytes, lane);
-      load_terms<T, IT>(st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time, live,
-                        a.key_dim, a.wide_qk, lane);
-      load_terms<T, IT>(st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time, live,
-                        a.key_dim, a.wide_qk, lane);
-      load_terms<T, IT>(st + Stage::gy, plane_v, lv, gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v,
-                        gy.time, live, cols_v, a.wide_v, lane);
-      if constexpr (!EFFECT)
-        load_terms<T, IT>(st + Stage::gy + IT * plane_v, plane_v, lv,
-                          v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time, live, cols_v, a.wide_v,
-                          lane);
+      const TileSource<T> kt{st + Stage::k, plane, lp, k.data + b * k.batch + t0 * k.time + hk * k.head, k.time,
+                             a.key_dim, a.wide_qk};
+      const TileSource<T> qt{st + Stage::q, plane, lp, q.data + b * q.batch + t0 * q.time + hk * q.head, q.time,
+                             a.key_dim, a.wide_qk};
+      const TileSource<T> yt{st + Stage::gy, plane_v, lv,
+                             gy.data + b * gy.batch + t0 * gy.time + h * gy.head + first_v, gy.time, cols_v, a.wide_v};
+      const TileSource<T> vt{st + Stage::gy + IT * plane_v, plane_v, lv,
+                             v.data + b * v.batch + t0 * v.time + h * v.head + first_v, v.time, cols_v, a.wide_v};
+      if constexpr (EFFECT) load_tiles<IT, 3, T>({kt, qt, yt}, live, lane);
+      else load_tiles<IT, 4, T>({kt, qt, yt, vt}, live, lane);
       copies_done();
       arrive(1 + p, meeting);
     }
