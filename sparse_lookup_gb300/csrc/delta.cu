@@ -161,6 +161,7 @@ cudaError_t run(emb_delta h, const DeltaArgs& a, const DeltaViews& w, int32_t dt
 
 void delta_free(emb_delta h) {
   dev_free(h->record);
+  dev_free(h->order);
   for (uint4* p : h->s) dev_free(p);
   for (uint4* p : h->ds) dev_free(p);
   dev_free(h->e);
@@ -197,6 +198,7 @@ extern "C" emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t h
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device);
   const int64_t all = (int64_t)max_batch * heads, chunks = ((int64_t)max_len + kChunk - 1) / kChunk;
   if (e == cudaSuccess) e = dev_alloc((void**)&h->record, all * chunks * Record::bytes);
+  if (e == cudaSuccess) e = dev_alloc((void**)&h->order, sizeof(int32_t) * kMostOrdered);
   const int64_t W = (value_dim + 15) / 16, dk = dk_of(key_dim);
   if (chunks >= kLeastChunks && e == cudaSuccess) {
     // calls of a few heads are cut into segments, one an SM: an effect forward and one backward

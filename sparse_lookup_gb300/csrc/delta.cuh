@@ -38,6 +38,7 @@ struct emb_delta_s {
   int32_t key_dim = 0, value_dim = 0, heads = 0, key_heads = 0, max_batch = 0, max_len = 0, training = 0;
   int sm_count = 0, device = 0;
   unsigned char* record = nullptr;   // see DeltaWork
+  int32_t* order = nullptr;          // [kMostOrdered]
   // for the backward
   uint4 *s[3] = {nullptr, nullptr, nullptr}, *ds[3] = {nullptr, nullptr, nullptr};
   float4 *e = nullptr, *dz = nullptr;
@@ -50,6 +51,7 @@ struct emb_delta_s {
 namespace emb {
 
 constexpr int kChunk = 32;
+constexpr int kMostOrdered = 4096;   // entries that are ordered by their length
 constexpr int kLeastChunks = 64;   // of a sequence that is cut into segments
 
 // A [batch, time, heads, dim] array (or [batch, time, heads]).
@@ -86,6 +88,7 @@ struct DeltaArgs {
   int32_t segments, span;             // of a sequence, and chunks of one
   float scale;
   const int32_t* offsets;
+  const int32_t* order;               // NULL, or entries from the longest
   const float *state_in, *grad_last;
   float *state_out, *grad_state;
   DView<const float> decay, beta;
@@ -476,6 +479,22 @@ __device__ __forceinline__ int length_of(const DeltaArgs& a, int b) {
   return n < 0 ? 0 : n < a.len ? (int)n : a.len;
 }
 
+// Entries from the longest, equal ones in their order: with more sequences than run at
+// once, the last to start are then the short ones.
+static __global__ void __launch_bounds__(256) k_delta_order(DeltaArgs a, int32_t* order) {
+  __shared__ int32_t lens[256];
+  const int b = blockIdx.x * 256 + threadIdx.x, mine = b < a.batch ? length_of(a, b) : 0;
+  int rank = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 256) {
+    __syncthreads();
+    lens[threadIdx.x] = b0 + threadIdx.x < a.batch ? length_of(a, b0 + threadIdx.x) : -1;
+    __syncthreads();
+#pragma unroll 8
+    for (int i = 0; i < 256; ++i) rank += lens[i] > mine || (lens[i] == mine && b0 + i < b);
+  }
+  if (b < a.batch) order[rank] = b;
+}
+
 constexpr int log_of(int n) { return n <= 1 ? 0 : 1 + log_of(n / 2); }
 constexpr int kMostShared = 227 << 10;
 
@@ -712,7 +731,8 @@ __global__ void __launch_bounds__(384)
   const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
   const int size = Stage::bytes(8 << lv);
   const int part = blockIdx.x % a.parts, pair = blockIdx.x / a.parts, seg = pair % a.segments, bh = pair / a.segments;
-  const int b = bh / a.heads, h = bh % a.heads, hk = h / a.share, first_v = part * 16 * consumers;
+  const int nth = bh / a.heads, b = a.order ? a.order[nth] : nth, h = bh % a.heads, hk = h / a.share;
+  const int first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
   // this segment's chunks; the last one that has any ends the sequence
   const int first = min(chunks, seg * a.span), end = min(chunks, first + a.span);
@@ -1035,7 +1055,8 @@ __global__ void __launch_bounds__(384)
   const int lv = consumers == 1 ? 1 : 32 - __clz(2 * consumers - 1), plane_v = (kChunk * 16) << lv;
   const int size = Stage::bytes(8 << lv);
   const int part = blockIdx.x % a.parts, pair = blockIdx.x / a.parts, seg = pair % a.segments, bh = pair / a.segments;
-  const int b = bh / a.heads, h = bh % a.heads, hk = h / a.share, first_v = part * 16 * consumers;
+  const int nth = bh / a.heads, b = a.order ? a.order[nth] : nth, h = bh % a.heads, hk = h / a.share;
+  const int first_v = part * 16 * consumers;
   const int len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
   const int first = min(chunks, seg * a.span), end = min(chunks, first + a.span);
   const bool ends = seg == (chunks ? (chunks - 1) / a.span : 0);
@@ -1640,10 +1661,12 @@ struct DeltaShape {
 template <class Stage>
 DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a, int blocks) {
   const int64_t pairs = (int64_t)a.batch * a.heads * a.segments;
-  // channels over several CTAs where there are too few sequences for the SMs, and where there
-  // are more than eight warps' of them
+  // channels over several CTAs where there are fewer than two sequences for an SM (a CTA's
+  // warps are faster alone, so the last ones do not last: 256 heads of 128 x 128 forward 431
+  // us in one CTA each, 385 in two, 450 in four, which copy keys and queries as often), and
+  // where there are more than eight warps' of them
   a.parts = 1;
-  for (int d = 2; d <= blocks && (pairs * a.parts < h->sm_count || blocks / a.parts > 8); ++d)
+  for (int d = 2; d <= blocks && (pairs * a.parts < 2 * h->sm_count || blocks / a.parts > 8); ++d)
     if (blocks % d == 0) a.parts = d;
   DeltaShape s;
   s.consumers = blocks / a.parts;
@@ -1698,6 +1721,12 @@ cudaError_t launch_chain(const DeltaArgs& a, cudaStream_t stream) {
 template <class T, int DK, DeltaMode MODE>
 cudaError_t launch_delta_fwd(const emb_delta_s* h, DeltaArgs& a, const DeltaViews& w, cudaStream_t stream) {
   cut_segments<DK>(h, a);
+  if (a.offsets && a.len > kChunk && a.batch <= kMostOrdered && (int64_t)a.batch * a.heads > h->sm_count) {
+    k_delta_order<<<(a.batch + 255) / 256, 256, 0, stream>>>(a, h->order);
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    a.order = h->order;
+  }
   cudaError_t e = launch_delta_prepare<T, DK>(a, w, MODE == kStates, stream);
   if (e == cudaSuccess && a.segments > 1) e = launch_walk<T, DK, kEffect>(h, a, w, stream);
   if (e == cudaSuccess && a.segments > 1) e = launch_chain<DK, false>(a, stream);

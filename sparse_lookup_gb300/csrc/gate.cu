@@ -6,7 +6,8 @@ namespace emb {
 
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
-constexpr int kGateCtas = 4;      // CTAs on an SM that sum columns
+constexpr int kGateCtas = 3;      // CTAs on an SM: as many as a token's 16 experts a lane leave registers for
+constexpr int kGradCtas = 6;      // of the backward
 constexpr int kSumCols = 8;       // experts of a CTA of the last reduction
 constexpr int kSumRows = 64;      // CTAs' rows that it takes side by side
 
@@ -83,7 +84,7 @@ __device__ __forceinline__ void write_losses(const GateArgs& a, double share, do
 // every token pays.  Column sums of the probabilities stay in registers too, and
 // leave as one row a CTA.  ONE: a single CTA, which writes the losses itself.
 template <class T, int V, int M, bool ONE>
-__global__ void __launch_bounds__(kGateThreads, M <= 16 ? 3 : 1) k_gate(GateArgs a, const T* __restrict__ logits, int glog) {
+__global__ void __launch_bounds__(kGateThreads, M <= 16 ? kGateCtas : 1) k_gate(GateArgs a, const T* __restrict__ logits, int glog) {
   extern __shared__ float held[];   // [warps][E] probabilities; [E] choices
   __shared__ double zs[kGateWarps];
   __shared__ uint32_t ns[kGateWarps];
@@ -285,7 +286,7 @@ struct GateGrad {
 // and a chosen one w gw more (normalised: w (gw - sum w gw)).  One pass; the
 // chosen are written over the row once it is there, by a lane each.
 template <class T, int V, int M>
-__global__ void __launch_bounds__(kGateThreads) k_gate_bwd(GateGrad a, const T* __restrict__ logits,
+__global__ void __launch_bounds__(kGateThreads, M <= 16 ? 3 : 1) k_gate_bwd(GateGrad a, const T* __restrict__ logits,
                                                            T* __restrict__ grad, int glog) {
   extern __shared__ float held[];   // [E] c
   const int E = a.n_experts, K = a.top_k, L = 1 << glog, sub = threadIdx.x & (L - 1);
@@ -385,9 +386,9 @@ bool gate_wide(int32_t dtype, int32_t E, int64_t stride, const void* p, int64_t 
   return E % v == 0 && stride % v == 0 && stride2 % v == 0 && aligned16(p) && aligned16(p2);
 }
 
-unsigned gate_grid(const emb_moe_s* h, int64_t n, int glog) {
+unsigned gate_grid(const emb_moe_s* h, int64_t n, int glog, int ctas) {
   const int per = kGateThreads >> glog;
-  const int64_t need = (n + per - 1) / per, most = (int64_t)h->sm_count * kGateCtas;
+  const int64_t need = (n + per - 1) / per, most = (int64_t)h->sm_count * ctas;
   return (unsigned)(need < most ? need : most);
 }
 
@@ -423,7 +424,7 @@ extern "C" emb_status moe_gate(emb_moe h, int64_t n, int32_t dtype, const void* 
                                [&](auto* t, auto width, auto count, int glog) {
     using T = std::remove_pointer_t<decltype(t)>;
     constexpr int V = decltype(width)::value, M = decltype(count)::value;
-    const unsigned ctas = n ? gate_grid(h, n, glog) : 1;
+    const unsigned ctas = n ? gate_grid(h, n, glog, kGateCtas) : 1;
     const size_t smem = sizeof(float) * (kGateWarps + 1) * E;
     const auto kernel = ctas == 1 ? k_gate<T, V, M, true> : k_gate<T, V, M, false>;
     if (smem > 48 << 10) {
@@ -460,7 +461,7 @@ extern "C" emb_status moe_gate_backward(emb_moe h, int64_t n, int32_t dtype, con
                                [&](auto* t, auto width, auto count, int glog) {
     using T = std::remove_pointer_t<decltype(t)>;
     const auto kernel = k_gate_bwd<T, decltype(width)::value, decltype(count)::value>;
-    kernel<<<gate_grid(h, n, glog), kGateThreads, sizeof(float) * E, (cudaStream_t)stream>>>(
+    kernel<<<gate_grid(h, n, glog, kGradCtas), kGateThreads, sizeof(float) * E, (cudaStream_t)stream>>>(
         a, (const T*)logits, (T*)grad_logits, glog);
     return cudaGetLastError();
   }));

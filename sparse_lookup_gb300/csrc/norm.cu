@@ -14,9 +14,9 @@ namespace emb {
 
 constexpr int kNormThreads = 128;      // of a CTA whose groups are within a warp
 constexpr int kNormWide = 512;         // threads of a row at most
-constexpr int kNormCtas = 4;           // CTAs of kNormThreads on an SM
+constexpr int kNormCtas = 4;           // CTAs of kNormThreads on an SM at most
 constexpr int kNormMaxDim = 16384;
-constexpr int kSumRows = 16;           // partial rows that the last reduction's CTA takes side by side
+constexpr int kSumCols = 16, kSumRows = 32;   // columns of the last reduction's CTA, and partial rows side by side
 
 // Rows are (b, t) of a [batch, len] array; a plain matrix is one batch entry.
 struct NormRows {
@@ -78,10 +78,18 @@ struct RowSum {
   }
 };
 
-// Whether a row's accesses are started a round early: not where a thread of a
-// wide CTA holds 32 elements, which leave no registers for it.
+// Whether a row's accesses are started a round early: not where a thread of a wide
+// CTA, or of the backward, holds 32 elements, which leave no registers for it.
 template <int V, int N, bool WIDE>
 constexpr bool kAhead = !(WIDE && V * N >= 32);
+template <int V, int N>
+constexpr bool kBwdAhead = V * N < 32;
+
+// CTAs on an SM: a backward's lane with 64 bytes of each operand in flight leaves
+// registers for three.  A grid of as many: a fourth would run after them, alone (1024 x
+// 1000 x 64 fp32 backward 141 us with four, 102 with three).
+template <class T, int V, int N>
+constexpr int kBwdCtas = V * N * sizeof(T) >= 64 && kBwdAhead<V, N> ? 3 : kNormCtas;
 
 // One row in a lane: N accesses of V elements, `lanes` accesses apart.
 template <class T, int V, int N>
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
 // over a CTA's rows in registers, lane by lane, joined at the end in a fixed
 // order.
 template <class T, class W, int V, int N, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
+__global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kBwdCtas<T, V, N>)
     k_norm_bwd(NormRows a, NormView<const T> x, NormView<const T> dy, const float2* __restrict__ stats,
                const W* __restrict__ w, NormView<T> dx, float* __restrict__ part, int glog) {
   extern __shared__ float held[];   // [dim] weight; at the end [2][dim] sums
@@ -236,16 +244,16 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
     nx.load(row_of(x, p), sub, L, a.vecs, p.live);
     ng.load(row_of(dy, p), sub, L, a.vecs, p.live);
   };
-  if constexpr (kAhead<V, N, WIDE>) load();
+  if constexpr (kBwdAhead<V, N>) load();
   for (int64_t k = 0; k < rounds; ++k, r += step) {
-    if constexpr (!kAhead<V, N, WIDE>) load();
+    if constexpr (!kBwdAhead<V, N>) load();
     const RowPart<T, V, N> xv = nx, gv = ng;
     const Place q = p;
     const float2 st = ns;
     const int64_t s = r + step;
     p = s < a.n ? place_of(a, s) : Place{0, 0, false};
     ns = p.live ? stats[s] : make_float2(0.f, 0.f);
-    if constexpr (kAhead<V, N, WIDE>) load();
+    if constexpr (kBwdAhead<V, N>) load();
     float2 m = make_float2(0.f, 0.f);   // sums of g and of g xh
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -327,22 +335,21 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
   }
 }
 
-// The CTAs' sums, column by column: 32 columns a CTA, kSumRows of its warps'
-// rows side by side, joined in a fixed order.
-__global__ void __launch_bounds__(32 * kSumRows) k_norm_sum(const float* __restrict__ part, int ctas, int dim,
-                                                           float* __restrict__ gw, float* __restrict__ gb) {
-  __shared__ float s[kSumRows][33];
+// The CTAs' sums, column by column, in a fixed order.
+__global__ void __launch_bounds__(kSumCols* kSumRows) k_norm_sum(const float* __restrict__ part, int ctas, int dim,
+                                                                float* __restrict__ gw, float* __restrict__ gb) {
+  __shared__ float s[kSumRows][kSumCols + 1];
   pdl_wait();
-  const int lane = threadIdx.x & 31, row = threadIdx.x >> 5;
-  const int c = blockIdx.x * 32 + lane;
+  const int col = threadIdx.x % kSumCols, row = threadIdx.x / kSumCols, c = blockIdx.x * kSumCols + col;
   float x = 0.f;
   if (c < 2 * dim)
 #pragma unroll 8
     for (int i = row; i < ctas; i += kSumRows) x += part[(int64_t)i * 2 * dim + c];
-  s[row][lane] = x;
+  s[row][col] = x;
   __syncthreads();
   if (row || c >= 2 * dim) return;
-  for (int i = 1; i < kSumRows; ++i) x += s[i][lane];
+#pragma unroll
+  for (int i = 1; i < kSumRows; ++i) x += s[i][col];
   if (c < dim && gw) gw[c] = x;
   if (c >= dim && gb) gb[c - dim] = x;
 }
@@ -414,10 +421,10 @@ cudaError_t with_norm(int32_t dtype, bool wide_weight, int v, int vecs, F f) {
   });
 }
 
-unsigned norm_grid(const emb_norm_s* h, int64_t rows, bool wide, int lanes) {
+unsigned norm_grid(const emb_norm_s* h, int64_t rows, bool wide, int lanes, int ctas) {
   const int per = wide ? 1 : kNormThreads >> lanes;
   const int64_t need = (rows + per - 1) / per;
-  const int64_t most = (int64_t)h->sm_count * (wide ? (lanes <= kNormThreads ? kNormCtas : lanes <= 256 ? 2 : 1) : kNormCtas);
+  const int64_t most = (int64_t)h->sm_count * (wide ? (lanes <= kNormThreads ? kNormCtas : lanes <= 256 ? 2 : 1) : ctas);
   return (unsigned)(need < most ? need : most);
 }
 
@@ -485,7 +492,7 @@ extern "C" emb_status norm_forward(emb_norm h, int32_t batch, int64_t len, int32
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
     }
-    kernel<<<norm_grid(h, a.n, WIDE, lanes), WIDE ? lanes : kNormThreads, smem, (cudaStream_t)stream>>>(
+    kernel<<<norm_grid(h, a.n, WIDE, lanes, kNormCtas), WIDE ? lanes : kNormThreads, smem, (cudaStream_t)stream>>>(
         a, norm_view<const T>(x), (const W*)weight, (const W*)bias, norm_view<T>(y), (float2*)stats, lanes);
     return cudaGetLastError();
   }));
@@ -522,13 +529,13 @@ extern "C" emb_status norm_backward(emb_norm h, int32_t batch, int64_t len, int3
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
     }
-    ctas = norm_grid(h, a.n, WIDE, lanes);
+    ctas = norm_grid(h, a.n, WIDE, lanes, kBwdCtas<T, decltype(width)::value, decltype(count)::value>);
     kernel<<<ctas, WIDE ? lanes : kNormThreads, smem, s>>>(a, norm_view<const T>(x), norm_view<const T>(grad_y),
                                                           (const float2*)stats, (const W*)weight,
                                                           norm_view<T>(grad_x), part, lanes);
     return cudaGetLastError();
   }));
   if (!part) return EMB_OK;
-  return cuda_status(launch_dependent(k_norm_sum, (unsigned)((2 * h->dim + 31) / 32), 32 * kSumRows, 0, s,
+  return cuda_status(launch_dependent(k_norm_sum, (unsigned)((2 * h->dim + kSumCols - 1) / kSumCols), kSumCols * kSumRows, 0, s,
                                       (const float*)part, (int)ctas, (int)h->dim, grad_weight, grad_bias));
 }
