@@ -85,11 +85,9 @@ constexpr bool kAhead = !(WIDE && V * N >= 32);
 template <int V, int N>
 constexpr bool kBwdAhead = V * N < 32;
 
-// CTAs on an SM: a backward's lane with 64 bytes of each operand in flight leaves
-// registers for three.  A grid of as many: a fourth would run after them, alone (1024 x
-// 1000 x 64 fp32 backward 141 us with four, 102 with three).
-template <class T, int V, int N>
-constexpr int kBwdCtas = V * N * sizeof(T) >= 64 && kBwdAhead<V, N> ? 3 : kNormCtas;
+// CTAs of a backward on an SM, as many as its registers allow: a fourth would run after
+// them, alone (1024 x 1000 x 64 fp32 141 us with four, 101 with three).
+constexpr int kBwdCtas = 3;
 
 // One row in a lane: N accesses of V elements, `lanes` accesses apart.
 template <class T, int V, int N>
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
     for (int i = 0; i < N; ++i) {
       const Pairs<V> f = pairs_of(now.v[i]);
 #pragma unroll
-      for (int e = 0; e < (V + 1) / 2; ++e) m.x += f.p[e].x, m.y += f.p[e].y;
+      for (int e = 0; e < (V + 1) / 2; ++e) m = __fadd2_rn(m, f.p[e]);
     }
     m = sum(m);
     const float mean = (m.x + m.y) * inv;
@@ -187,9 +185,8 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
       const Pairs<V> f = pairs_of(now.v[i]);
 #pragma unroll
       for (int e = 0; e < (V + 1) / 2; ++e) {
-        const float u = f.p[e].x - mean, v = f.p[e].y - mean;
-        d.x += u * u;
-        if (V > 1) d.y += v * v;
+        const float2 u = __fadd2_rn(f.p[e], make_float2(-mean, V > 1 ? -mean : 0.f));
+        d = __ffma2_rn(u, u, d);
       }
     }
     d = sum(d);
@@ -205,8 +202,9 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
       const Pairs<V> wj = weights_of<V>(ws, j, a.vecs), bj = weights_of<V>(bs, j, a.vecs);
 #pragma unroll
       for (int e = 0; e < (V + 1) / 2; ++e) {
-        f.p[e].x = q.live ? (f.p[e].x - mean) * rstd * wj.p[e].x + bj.p[e].x : 0.f;
-        if (V > 1) f.p[e].y = q.live ? (f.p[e].y - mean) * rstd * wj.p[e].y + bj.p[e].y : 0.f;
+        const float2 h = __fmul2_rn(__fadd2_rn(f.p[e], make_float2(-mean, -mean)), make_float2(rstd, rstd));
+        const float2 o = __ffma2_rn(h, wj.p[e], bj.p[e]);
+        f.p[e] = q.live ? o : make_float2(0.f, 0.f);
       }
       store_vec(to + (int64_t)j * V, vec_of<T, V>(f));
     }
@@ -217,7 +215,7 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
 // over a CTA's rows in registers, lane by lane, joined at the end in a fixed
 // order.
 template <class T, class W, int V, int N, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kBwdCtas<T, V, N>)
+__global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kBwdCtas)
     k_norm_bwd(NormRows a, NormView<const T> x, NormView<const T> dy, const float2* __restrict__ stats,
                const W* __restrict__ w, NormView<T> dx, float* __restrict__ part, int glog) {
   extern __shared__ float held[];   // [dim] weight; at the end [2][dim] sums
@@ -254,7 +252,9 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kB
     p = s < a.n ? place_of(a, s) : Place{0, 0, false};
     ns = p.live ? stats[s] : make_float2(0.f, 0.f);
     if constexpr (kBwdAhead<V, N>) load();
-    float2 m = make_float2(0.f, 0.f);   // sums of g and of g xh
+    // sums of g and of g xh, in pairs: the row is bound by the instructions it takes
+    float2 m1 = make_float2(0.f, 0.f), m2 = m1;
+    const float2 minus_mean = make_float2(-st.x, -st.x), rstd = make_float2(st.y, st.y);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int j = sub + i * L;
@@ -262,20 +262,17 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kB
       const Pairs<V> f = pairs_of(xv.v[i]), g = pairs_of(gv.v[i]), wj = weights_of<V>(held, j, a.vecs);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        const float h = (f.p[e].x - st.x) * st.y, o = g.p[e].x * wj.p[e].x;
-        m.x += o, m.y += o * h;
-        gw[i][e].x += g.p[e].x * h, gb[i][e].x += g.p[e].x;
-        if (V > 1) {
-          const float h1 = (f.p[e].y - st.x) * st.y, o1 = g.p[e].y * wj.p[e].y;
-          m.x += o1, m.y += o1 * h1;
-          gw[i][e].y += g.p[e].y * h1, gb[i][e].y += g.p[e].y;
-        }
+        const float2 h = __fmul2_rn(__fadd2_rn(f.p[e], minus_mean), rstd), o = __fmul2_rn(g.p[e], wj.p[e]);
+        m1 = __fadd2_rn(m1, o), m2 = __ffma2_rn(o, h, m2);
+        gw[i][e] = __ffma2_rn(g.p[e], h, gw[i][e]), gb[i][e] = __fadd2_rn(gb[i][e], g.p[e]);
       }
     }
+    float2 m = make_float2(m1.x + m1.y, m2.x + m2.y);
     m = sum(m);
     m.x *= inv, m.y *= inv;
     if (r >= a.n) continue;
     T* to = row_of(dx, q);
+    const float2 scale1 = make_float2(-m.x * st.y, -m.x * st.y), scale2 = make_float2(-m.y * st.y, -m.y * st.y);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int j = sub + i * L;
@@ -283,9 +280,9 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kB
       Pairs<V> f = pairs_of(xv.v[i]), g = pairs_of(gv.v[i]), wj = weights_of<V>(held, j, a.vecs);
 #pragma unroll
       for (int e = 0; e < P; ++e) {
-        f.p[e].x = q.live ? st.y * (g.p[e].x * wj.p[e].x - m.x - (f.p[e].x - st.x) * st.y * m.y) : 0.f;
-        if (V > 1)
-          f.p[e].y = q.live ? st.y * (g.p[e].y * wj.p[e].y - m.x - (f.p[e].y - st.x) * st.y * m.y) : 0.f;
+        const float2 h = __fmul2_rn(__fadd2_rn(f.p[e], minus_mean), rstd), o = __fmul2_rn(g.p[e], wj.p[e]);
+        const float2 x = __ffma2_rn(h, scale2, __ffma2_rn(o, rstd, scale1));
+        f.p[e] = q.live ? x : make_float2(0.f, 0.f);
       }
       store_vec(to + (int64_t)j * V, vec_of<T, V>(f));
     }
@@ -529,7 +526,7 @@ extern "C" emb_status norm_backward(emb_norm h, int32_t batch, int64_t len, int3
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       if (e != cudaSuccess) return e;
     }
-    ctas = norm_grid(h, a.n, WIDE, lanes, kBwdCtas<T, decltype(width)::value, decltype(count)::value>);
+    ctas = norm_grid(h, a.n, WIDE, lanes, kBwdCtas);
     kernel<<<ctas, WIDE ? lanes : kNormThreads, smem, s>>>(a, norm_view<const T>(x), norm_view<const T>(grad_y),
                                                           (const float2*)stats, (const W*)weight,
                                                           norm_view<T>(grad_x), part, lanes);
