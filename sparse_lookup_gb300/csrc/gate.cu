@@ -7,7 +7,7 @@ namespace emb {
 constexpr int kGateThreads = 256;
 constexpr int kGateWarps = kGateThreads / 32;
 constexpr int kGateCtas = 3;      // CTAs on an SM: as many as a token's 16 experts a lane leave registers for
-constexpr int kGradCtas = 6;      // of the backward
+constexpr int kGradCtas = 4;      // of the backward
 constexpr int kSumCols = 8;       // experts of a CTA of the last reduction
 constexpr int kSumRows = 64;      // CTAs' rows that it takes side by side
 
@@ -114,14 +114,17 @@ __global__ void __launch_bounds__(kGateThreads, M <= 16 ? kGateCtas : 1) k_gate(
     const bool some = top > -INFINITY;
     // the row's exponentials; an all -inf row has none
     const float base = some ? top : 0.f;
-    float total = 0.f;
+    float total = 0.f, e[M];
 #pragma unroll
-    for (int m = 0; m < M; ++m) total += expf(v[m] - base);
+    for (int m = 0; m < M; ++m) {
+      e[m] = expf(v[m] - base);
+      total += e[m];
+    }
     total = group_sum(total, L);
     const float lse = some ? base + logf(total) : total > 0.f || total != total ? total : -INFINITY;
     const float inv = some ? 1.f / total : total;
 #pragma unroll
-    for (int m = 0; m < M; ++m) psum[m] += expf(v[m] - base) * inv;
+    for (int m = 0; m < M; ++m) psum[m] += e[m] * inv;
     if (sub == 0 && in) {
       a.stats[t] = make_float2(top, total);
       if (lse != -INFINITY) {
@@ -141,22 +144,22 @@ __global__ void __launch_bounds__(kGateThreads, M <= 16 ? kGateCtas : 1) k_gate(
         for (int m = 1; m < M; ++m) best = fmaxf(best, v[m]);
         best = group_max(best, L);
       }
-      int at = 1 << 30;
+      int own = -1;   // the lane's first of the largest
 #pragma unroll
       for (int m = M - 1; m >= 0; --m)
-        if (v[m] == best) at = expert_of<V>(m, sub, L);
+        if (v[m] == best) own = m;
       const bool any = best > -INFINITY;
-      const int mine = at;
-      at = group_min(at, L);
+      const int mine = own >= 0 ? expert_of<V>(own, sub, L) : 1 << 30, at = group_min(mine, L);
+      if (mine != at) own = -1;
 #pragma unroll
       for (int m = 0; m < M; ++m)
-        if (mine == at && expert_of<V>(m, sub, L) == at) v[m] = -INFINITY;
-      const float e = any ? expf(best - base) : 0.f;
-      kept += e;
+        if (m == own) v[m] = -INFINITY;
+      const float each = any ? expf(best - base) : 0.f;
+      kept += each;
       if (in && sub == (k & (L - 1))) {
         a.experts[t * K + k] = any ? at : -1;
-        mine_e = e;
-        if (K > L) a.weights[t * K + k] = e;
+        mine_e = each;
+        if (K > L) a.weights[t * K + k] = each;
         if (any) atomicAdd(&chosen[at], 1u);
       }
     }
@@ -286,7 +289,7 @@ struct GateGrad {
 // and a chosen one w gw more (normalised: w (gw - sum w gw)).  One pass; the
 // chosen are written over the row once it is there, by a lane each.
 template <class T, int V, int M>
-__global__ void __launch_bounds__(kGateThreads, M <= 16 ? 3 : 1) k_gate_bwd(GateGrad a, const T* __restrict__ logits,
+__global__ void __launch_bounds__(kGateThreads) k_gate_bwd(GateGrad a, const T* __restrict__ logits,
                                                            T* __restrict__ grad, int glog) {
   extern __shared__ float held[];   // [E] c
   const int E = a.n_experts, K = a.top_k, L = 1 << glog, sub = threadIdx.x & (L - 1);
