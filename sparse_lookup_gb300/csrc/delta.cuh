@@ -942,17 +942,17 @@ __global__ void __launch_bounds__(384)
 
 // From segment to segment: S^T (rows are value channels) before each from what the one
 // before makes of a state, S^T_p+1 = S^T_p M_p^T + N_p^T, with M^T and N^T as k_delta_fwd left them; or
-// the gradients after each, dS^T_p-1 = dS^T_p M_p + N'_p^T.  A CTA has kChainRows rows; the
+// the gradients after each, dS^T_p-1 = dS^T_p M_p + N'_p^T.  A CTA has some rows; the
 // next segment's M^T comes while this one's is used.
-constexpr int kChainRows = 8;
+constexpr int chain_rows(int dk) { return dk == 128 ? 4 : 8; }
 template <int DK, bool REVERSE>
 __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs a) {
-  constexpr int G = 256 / DK, R = kChainRows / G > 0 ? kChainRows / G : 1, V = DK * DK / 1024;
-  static_assert(G * R == kChainRows, "");
+  constexpr int kRows = chain_rows(DK), G = 256 / DK, R = kRows / G, V = DK * DK / 1024;
+  static_assert(R > 0 && G * R == kRows, "");
   extern __shared__ __align__(128) float chain[];
   float* m = chain;                // [DK][DK] M^T, groups of four exchanged by their row so that rows and columns are read alike
-  float* x = chain + DK * DK;      // [kChainRows][DK]
-  const int blocks = a.warps * 16 / kChainRows, rows0 = blockIdx.x % blocks * kChainRows, bh = blockIdx.x / blocks;
+  float* x = chain + DK * DK;      // [kRows][DK]
+  const int blocks = a.warps * 16 / kRows, rows0 = blockIdx.x % blocks * kRows, bh = blockIdx.x / blocks;
   const int b = bh / a.heads, len = length_of(a, b), chunks = (len + kChunk - 1) / kChunk;
   const int last = chunks ? (chunks - 1) / a.span : 0, d = threadIdx.x % DK, r0 = threadIdx.x / DK * R;
   const float* given = REVERSE ? a.grad_last : a.state_in;
@@ -1713,11 +1713,11 @@ cudaError_t launch_walk(const emb_delta_s* h, DeltaArgs a, const DeltaViews& w, 
 
 template <int DK, bool REVERSE>
 cudaError_t launch_chain(const DeltaArgs& a, cudaStream_t stream) {
-  constexpr int smem = (DK + kChainRows) * DK * 4;
+  constexpr int smem = (DK + chain_rows(DK)) * DK * 4;
   const auto kernel = k_delta_chain<DK, REVERSE>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kernel<<<(unsigned)(a.batch * a.heads * (a.warps * 16 / kChainRows)), 256, smem, stream>>>(a);
+  kernel<<<(unsigned)(a.batch * a.heads * (a.warps * 16 / chain_rows(DK))), 256, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
