@@ -397,11 +397,13 @@ emb_status emb_noalloc_get_device_status(void* stream);
 
 /* ------------------------------------------------------------------------ */
 /* Dense operators behind the lookups (no counterpart on the pages): a gated */
-/* recurrence over padded sequences, tokens sorted by expert and back, AdamW  */
+/* recurrence and the gated delta rule over padded sequences, layer norm,     */
+/* tokens' experts chosen, sorted by expert and back, AdamW                   */
 /* ------------------------------------------------------------------------ */
 /* Element types are EMB_DT_F32, EMB_DT_BF16 and EMB_DT_F16 of
- * emb_table_dtype (called dtype below).  All arithmetic is fp32; a result
- * of 16 bits is rounded once, when it is stored.  Pointers need the alignment
+ * emb_table_dtype (called dtype below).  All arithmetic is fp32 (the delta
+ * rule's products: see there); a result of 16 bits is rounded once, when it is
+ * stored.  Pointers need the alignment
  * of their element; rows whose pointers, strides and sizes are multiples of
  * 16 bytes move in 16-byte accesses.  Outputs must not overlap inputs or
  * each other.  A handle belongs to the device that was current when it was
@@ -717,8 +719,9 @@ typedef struct {
  * which there may be 2^30 (237 MB for 32 x 2048 positions of 8 heads).  training != 0: it
  * can run the backward, for which it holds as often the state before them and its
  * gradient after them (12 bytes a number, key_dim rounded up to 32, 64 or 128 and
- * value_dim to a multiple of 16) and 280 bytes a value channel: 3.9 GB more for those of
- * 128 x 128.  Calls on one handle must be ordered.  *out is NULL on error. */
+ * value_dim to a multiple of 16) and 280 bytes a value channel: 3.8 GB more for those of
+ * 128 x 128.  max_len >= 2048: 40 MB more for 128 x 128, for sequences of few heads that are
+ * cut into segments.  Calls on one handle must be ordered.  *out is NULL on error. */
 emb_status delta_create(int32_t key_dim, int32_t value_dim, int32_t heads, int32_t key_heads, int32_t max_batch,
                         int32_t max_len, int32_t training, emb_delta* out);
 

@@ -21,7 +21,8 @@ struct StepArgs {
 //   y = scale (S'^T q + beta <k, q> e),  S = S' + beta k e^T,  e = v - S'^T k
 // so both products with the state are ready after one pass over it, which stays in
 // registers until it is written back.  A thread holds V neighbouring channels of R
-// rows; the rows' partial sums meet in shared memory.
+// rows; the rows' partial sums meet in shared memory.  Bound by memory where there are
+// many sessions, by the launch where few (192 x 4 heads of 64 x 64 bf16).
 template <class T, int V, int R>
 __global__ void __launch_bounds__(kStepThreads) k_delta_step(StepArgs a, DView<const T> q, DView<const T> k,
                                                              DView<const T> v, DView<T> y, int log_cols) {

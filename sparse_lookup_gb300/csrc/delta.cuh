@@ -514,7 +514,8 @@ struct PrepareShared {
 // A warp a chunk.  The inverse of I + N, N = M diag(beta) = [N11 0; N21 N22]: both
 // diagonal blocks by forward substitution (column j of them in lane j and 16 + j; not by
 // powers of N, which cancel where keys repeat), the block below them as -X22 N21 X11 on
-// the matrix units.
+// the matrix units.  32 sequences of 1024 .. 2048 positions, 8 heads of 128, bf16 (12.3
+// thousand chunks, the workload of the figures below): 62 us, 2000 instructions a chunk.
 template <class T, int DK>
 __global__ void __launch_bounds__(384) k_delta_prepare(DeltaArgs a, DView<const T> q, DView<const T> k, int backward) {
   using Shared = PrepareShared<T, DK>;
@@ -715,7 +716,11 @@ struct ForwardStage {
   static constexpr int own = MODE != kForward ? 0 : sizeof(T) == 2 ? 1024 : kChunk * 17 * 4;
 };
 
-// Consumer warps first (one for 16 value channels), then the producers.
+// Consumer warps first (one for 16 value channels), then the producers.  A chunk's 310
+// matrix instructions a warp (128 x 128, bf16) take 8.5 cycles each of a quarter of an SM,
+// which bounds the workload above by 220 us; it takes 385 (states' pass 480): a warp's
+// products follow from one another, and registers hold no more than two warps for each
+// quarter.
 template <class T, int DK, DeltaMode MODE>
 __global__ void __launch_bounds__(384)
     k_delta_fwd(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> y,
@@ -943,7 +948,8 @@ __global__ void __launch_bounds__(384)
 // From segment to segment: S^T (rows are value channels) before each from what the one
 // before makes of a state, S^T_p+1 = S^T_p M_p^T + N_p^T, with M^T and N^T as k_delta_fwd left them; or
 // the gradients after each, dS^T_p-1 = dS^T_p M_p + N'_p^T.  A CTA has some rows; the
-// next segment's M^T comes while this one's is used.
+// next segment's M^T comes while this one's is used.  38 segments of 4 heads of 128 x 128:
+// 76 us.
 constexpr int chain_rows(int dk) { return dk == 128 ? 4 : 8; }
 template <int DK, bool REVERSE>
 __global__ void __launch_bounds__(256) k_delta_chain(DeltaArgs a) {
@@ -1042,7 +1048,9 @@ struct ReverseStage {
   static constexpr int own = sizeof(T) == 2 ? 1024 : 0;   // dV on its way to rows
 };
 
-// EFFECT: only the gradient before a segment of a zero one after it.
+// 378 matrix instructions a warp and chunk (128 x 128, bf16): 550 us of the workload above,
+// where those alone would take 270.  EFFECT: only the gradient before a segment of a zero
+// one after it.
 template <class T, int DK, bool EFFECT>
 __global__ void __launch_bounds__(384)
     k_delta_reverse(DeltaArgs a, DView<const T> q, DView<const T> k, DView<const T> v, DView<const T> gy, DView<T> gv,
@@ -1319,7 +1327,9 @@ static __global__ void __launch_bounds__(128) k_delta_numbers(DeltaArgs a) {
 
 // A CTA has a chunk of a key head and COLS of its channels.  In shared memory: S0 and dS
 // [value channels][COLS], U and dZ [value channels][32], grad_y, K and Q, dA and X.  16-bit
-// calls leave room for all channels; each CTA of a key head finds dA and X for itself.
+// calls leave room for all channels; each CTA of a key head finds dA and X for itself.  630
+// us of the workload above (reading 1.3 GB of states and intermediates, 190 us): loads,
+// and the barriers around two short rounds of products, one CTA an SM.
 template <class T, int DK>
 struct GradientShared {
   static constexpr int COLS = DK == 128 && sizeof(T) == 4 ? 64 : DK, lc = log_of(COLS / 8);

@@ -79,7 +79,8 @@ struct RowSum {
 };
 
 // Whether a row's accesses are started a round early: not where a thread of a wide
-// CTA, or of the backward, holds 32 elements, which leave no registers for it.
+// CTA, or of the backward, holds 32 elements: the registers are worth more warps
+// (131072 x 1024 bf16 backward 200 us without, 290 with).
 template <int V, int N, bool WIDE>
 constexpr bool kAhead = !(WIDE && V * N >= 32);
 template <int V, int N>
@@ -114,7 +115,7 @@ __device__ __forceinline__ float weight_at(const W* w, int32_t c, float none) {
 
 // A weight in shared memory: of accesses of four and more in groups of four, the groups
 // of neighbouring accesses side by side, so that lanes read 16 bytes each without
-// conflicts (read one by one, 1024 bf16 channels took 240 us where they take 100).
+// conflicts (read one by one, 131072 x 1024 bf16 took 240 us where it takes 104).
 template <int V>
 __device__ __forceinline__ int place_in(int c, int vecs) {
   if constexpr (V < 4) return c;
@@ -138,7 +139,8 @@ __device__ __forceinline__ Pairs<V> weights_of(const float* w, int j, int vecs) 
 
 // y = (x - mean) rstd w + b.  A row stays in its lanes' registers, so x is
 // read once although mean and deviations need a pass each; the next row's
-// accesses are in flight meanwhile.
+// accesses are in flight meanwhile.  131072 x 1024 bf16 104 us (5.2 TB/s), 1024 x
+// 1000 x 64 fp32 with lengths 200 .. 1000 70 us (6.0 TB/s).
 template <class T, class W, int V, int N, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
     k_norm_fwd(NormRows a, NormView<const T> x, const W* __restrict__ w, const W* __restrict__ b, NormView<T> y,
@@ -213,7 +215,9 @@ __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads)
 
 // dx = rstd (g - mean(g) - xh mean(g xh)), g = dy w; the sums of dy xh and dy
 // over a CTA's rows in registers, lane by lane, joined at the end in a fixed
-// order.
+// order.  131072 x 1024 bf16 190 us (4.2 TB/s): 900 instructions a row on half of the
+// issue slots, with the 12 warps an SM that 32 channels' sums in a lane leave room for.
+// 1024 x 1000 x 64 fp32 98 us.
 template <class T, class W, int V, int N, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? kNormWide : kNormThreads, WIDE ? 1 : kBwdCtas)
     k_norm_bwd(NormRows a, NormView<const T> x, NormView<const T> dy, const float2* __restrict__ stats,
