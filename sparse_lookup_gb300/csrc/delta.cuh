@@ -1679,14 +1679,28 @@ DeltaShape walk_shape(const emb_delta_s* h, DeltaArgs& a, int blocks) {
   for (int d = 2; d <= blocks && (pairs * a.parts < 2 * h->sm_count || blocks / a.parts > 8); ++d)
     if (blocks % d == 0) a.parts = d;
   DeltaShape s;
-  s.consumers = blocks / a.parts;
-  s.ctas = (unsigned)(pairs * a.parts);
-  int dvp = 16;
-  while (dvp < 16 * s.consumers) dvp *= 2;
-  const int own = s.consumers * Stage::own;
-  s.producers = s.ctas > (unsigned)h->sm_count ? 2 : 4;
-  while (s.producers > 1 && s.producers * Stage::bytes(dvp) + own > kMostShared) --s.producers;
-  s.smem = s.producers * Stage::bytes(dvp) + own;
+  const auto shape = [&](int most_producers) {
+    s.consumers = blocks / a.parts;
+    s.ctas = (unsigned)(pairs * a.parts);
+    int dvp = 16;
+    while (dvp < 16 * s.consumers) dvp *= 2;
+    const int own = s.consumers * Stage::own;
+    // a producer without a chunk would hold shared memory that another CTA can have (886 x 3
+    // positions of 8 heads of 123 x 16 fp32, forward 459 us with two, 215 with one)
+    s.producers = most_producers < a.span ? most_producers : a.span;
+    while (s.producers > 1 && s.producers * Stage::bytes(dvp) + own > kMostShared) --s.producers;
+    s.smem = s.producers * Stage::bytes(dvp) + own;
+  };
+  // six or eight warps' channels over two CTAs also where there are many sequences, if an SM
+  // has shared memory for both: one's start and end then lie beside the other's chunks
+  // (1024 heads of 64 x 128 fp16, 300 positions, forward + backward 2184 us in one, 1882 in
+  // two; fp32 of 128 x 128, where only one fits, 4578 and 5503)
+  if (a.parts == 1 && blocks >= 6 && blocks % 2 == 0) {
+    a.parts = 2;
+    shape(2);
+    if (2 * s.smem > kMostShared) a.parts = 1;
+  }
+  shape(pairs * a.parts > h->sm_count ? 2 : 4);
   return s;
 }
 
