@@ -177,6 +177,21 @@ def test_many_sequences_and_long_memory(dtype):
     check(make(2, 400, 1, 1, 128, 128, dtype, 3, slow=True))
 
 
+# more heads than an SM takes two of, values of six to eight tiles of 16: in one CTA and in two, with fewer chunks than
+# a CTA may have producers
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("B,T,H,J,N,V", [(100, 3, 4, 2, 16, 83), (90, 40, 4, 4, 64, 128), (80, 33, 4, 1, 128, 112),
+                                         (85, 70, 4, 2, 100, 96), (400, 1, 1, 1, 128, 128)])
+def test_many_wide_heads(B, T, H, J, N, V, dtype):
+    import torch
+    case = make(B, T, H, J, N, V, dtype, B + T)
+    lens = torch.arange(B, device="cuda") * 7 % (T + 1)
+    offsets = torch.cat([lens.new_zeros(1), lens.cumsum(0)]).int()
+    _, y, end, got = check(case, offsets=offsets, lens=lens)
+    dead = torch.arange(T, device="cuda")[None] >= lens[:, None]
+    assert not y[dead].any() and not any(g[dead].any() for g in got[:5])
+
+
 # sequences that are cut into segments: of lengths on and off theirs, entries that end in each, and none
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("T,H,J,N,V,slow", [(2048, 2, 1, 32, 32, True), (2100, 1, 1, 128, 128, False),

@@ -91,6 +91,16 @@ def test_rows(rows, dim, dtype):
     run(*make((rows, dim), dtype, rows + dim))
 
 
+# rows at the ends of what a warp holds, of each access, and rows enough that a CTA has several
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("rows,dim", [(3000, 56), (3000, 64), (900, 127), (3000, 258), (3000, 499), (20, 511), (3000, 513),
+                                      (3000, 514), (3000, 516), (3000, 618), (20, 767), (3000, 768), (3000, 1020),
+                                      (3000, 1022), (3000, 1023), (3000, 1025), (3000, 1028), (3000, 1536),
+                                      (3000, 2046), (2000, 4553), (700, 8190), (700, 8193), (300, 16382)])
+def test_widths(rows, dim, dtype):
+    run(*make((rows, dim), dtype, rows + dim))
+
+
 @pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
 @pytest.mark.parametrize("dim", [64, 99, 1024, 2048])
 def test_many_rows(dim, dtype):
