@@ -17,17 +17,23 @@ struct StepArgs {
   DView<const float> decay, beta;
 };
 
+// CTAs of it on an SM, as many as the registers leave room for: 4096 sessions of 8 heads of
+// 128 x 128 take 880 us with one and 733 with two, 4 heads of 64 x 64 145 with three, 102 with four.
+constexpr int step_ctas(int v, int r) { return v * r <= 8 ? 6 : v * r <= 16 ? 4 : v * r <= 32 ? 3 : v > 1 ? 2 : 1; }
+
 // One position of a session's head: with S' = exp(g) S,
 //   y = scale (S'^T q + beta <k, q> e),  S = S' + beta k e^T,  e = v - S'^T k
 // so both products with the state are ready after one pass over it, which stays in
 // registers until it is written back.  A thread holds V neighbouring channels of R
 // rows; the rows' partial sums meet in shared memory.  Bound by memory where there are
-// many sessions, by the launch where few (192 x 4 heads of 64 x 64 bf16).
+// many sessions (4096 of 8 heads of 128 x 128 bf16 5.9 TB/s, of 4 heads of 64 x 64 5.4), by a
+// CTA's two barriers where heads are small (20000 of 2 heads of 32 x 32 2.1), by the launch
+// where sessions are few (192 of 4 heads of 64 x 64: 6 us).
 template <class T, int V, int R>
-__global__ void __launch_bounds__(kStepThreads) k_delta_step(StepArgs a, DView<const T> q, DView<const T> k,
+__global__ void __launch_bounds__(kStepThreads, step_ctas(V, R)) k_delta_step(StepArgs a, DView<const T> q, DView<const T> k,
                                                              DView<const T> v, DView<T> y, int log_cols) {
   __shared__ float ks[128], qs[128], kq[kStepThreads / 32];
-  __shared__ float part[2][kStepThreads * V];
+  __shared__ alignas(16) float part[2][kStepThreads * V];
   const int i = blockIdx.x / a.heads, h = blockIdx.x % a.heads, hk = h / a.share;
   const int64_t row = a.rows[i];
   const bool on = row >= 0 && row < a.num_rows;
@@ -80,12 +86,19 @@ __global__ void __launch_bounds__(kStepThreads) k_delta_step(StepArgs a, DView<c
       sk[u] += s[r].e[u] * kx, sq[u] += s[r].e[u] * qx;
     }
   }
+  // a warp's rows first
+  for (int o = cols; o < 32; o <<= 1)
 #pragma unroll
-  for (int u = 0; u < V; ++u) part[0][threadIdx.x * V + u] = sk[u], part[1][threadIdx.x * V + u] = sq[u];
+    for (int u = 0; u < V; ++u)
+      sk[u] += __shfl_xor_sync(kFull, sk[u], o), sq[u] += __shfl_xor_sync(kFull, sq[u], o);
+  const int sums = cols < 32 ? kStepThreads / 32 : groups, mine = cols < 32 ? threadIdx.x >> 5 : group;
+  if (cols >= 32 || (int)(threadIdx.x & 31) < cols)
+#pragma unroll
+    for (int u = 0; u < V; ++u) part[0][mine * cols * V + c + u] = sk[u], part[1][mine * cols * V + c + u] = sq[u];
   __syncthreads();
 #pragma unroll
   for (int u = 0; u < V; ++u) sk[u] = sq[u] = 0.f;
-  for (int w = 0; w < groups; ++w)
+  for (int w = 0; w < sums; ++w)
 #pragma unroll
     for (int u = 0; u < V; ++u) sk[u] += part[0][w * cols * V + c + u], sq[u] += part[1][w * cols * V + c + u];
   both = 0.f;
@@ -308,19 +321,23 @@ extern "C" emb_status delta_step(int64_t n, int32_t key_dim, int32_t value_dim, 
   if (n == 0) return EMB_OK;
   const StepArgs a{heads, heads / key_heads, key_dim, value_dim, (float)scale, rows, num_rows, states,
                    dview<const float>(decay), dview<const float>(beta)};
-  const bool wide = value_dim % 4 == 0 && aligned16(states);
+  const int width = value_dim % 4 == 0 && aligned16(states) ? 4 : value_dim % 2 == 0 && aligned_to(states, 8) ? 2 : 1;
   int log_cols = 0;
-  while (((wide ? 4 : 1) << log_cols) < value_dim) ++log_cols;
+  while ((width << log_cols) < value_dim) ++log_cols;
   const int groups = kStepThreads >> log_cols, need = (key_dim + groups - 1) / groups;
   return cuda_status(with_element(dtype, [&](auto* t) {
     using T = std::remove_pointer_t<decltype(t)>;
-    const auto kernel = wide ? (need <= 2    ? k_delta_step<T, 4, 2>
-                                : need <= 4  ? k_delta_step<T, 4, 4>
-                                : need <= 8  ? k_delta_step<T, 4, 8>
-                                             : k_delta_step<T, 4, 16>)
-                             : (need <= 8    ? k_delta_step<T, 1, 8>
-                                : need <= 16 ? k_delta_step<T, 1, 16>
-                                             : k_delta_step<T, 1, 64>);
+    const auto kernel = width == 4   ? (need <= 2    ? k_delta_step<T, 4, 2>
+                                        : need <= 4  ? k_delta_step<T, 4, 4>
+                                        : need <= 8  ? k_delta_step<T, 4, 8>
+                                                     : k_delta_step<T, 4, 16>)
+                        : width == 2 ? (need <= 8    ? k_delta_step<T, 2, 8>
+                                        : need <= 16 ? k_delta_step<T, 2, 16>
+                                                     : k_delta_step<T, 2, 32>)
+                                     : (need <= 8    ? k_delta_step<T, 1, 8>
+                                        : need <= 16 ? k_delta_step<T, 1, 16>
+                                        : need <= 32 ? k_delta_step<T, 1, 32>
+                                                     : k_delta_step<T, 1, 64>);
     kernel<<<(unsigned)(n * heads), kStepThreads, 0, (cudaStream_t)stream>>>(
         a, dview<const T>(q), dview<const T>(k), dview<const T>(v), dview<T>(y), log_cols);
     return cudaGetLastError();

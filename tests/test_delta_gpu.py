@@ -394,6 +394,14 @@ def test_step(n, H, J, N, V, dtype):
     assert torch.equal(pool[others], before[others]) and not y[~on].any()
 
 
+# accesses of two channels and of one, with few and many rows of the state to a thread
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("n,H,J,N,V", [(6, 2, 2, 100, 50), (6, 2, 1, 128, 126), (5, 1, 1, 60, 127), (50, 2, 2, 16, 6),
+                                       (4, 1, 1, 128, 65), (4, 3, 3, 64, 62)])
+def test_step_widths(n, H, J, N, V, dtype):
+    test_step(n, H, J, N, V, dtype)
+
+
 def test_gradients_are_differences():
     """A step of 1e-3 along a direction through the recurrence in 64 bits against the gradient: third order terms are
     below 1e-4 of the gradient's magnitudes."""
