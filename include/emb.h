@@ -664,8 +664,8 @@ typedef struct emb_norm_s* emb_norm;
 
 /* norm_create -- workspace of a layer norm over rows of dim (1 .. 16384)
  * channels: 8 bytes a channel for each CTA that sums the weight's gradient (4 per
- * SM up to 512 channels, else 8 or fewer; 10 MB for 1024, 40 MB for 16384).  Calls on one handle must be ordered.  *out is
- * NULL on error. */
+ * SM up to 512 channels, else 8 or fewer; 10 MB for 1024, 40 MB for 16384).  Calls
+ * on one handle must be ordered.  *out is NULL on error. */
 emb_status norm_create(int32_t dim, emb_norm* out);
 
 /* norm_forward -- y = (x - mean) * rstd * weight + bias over each row's channels,
